@@ -443,6 +443,139 @@ MA_API ma_status muon_adamw_grad_norm_noalloc(const void* const* grads, const in
                                               const int32_t* dtypes, int n_tensors, double max_norm,
                                               double clip_eps, float* out_total_coef, void* cuda_stream);
 
+/* ---- Operators of the training step ----
+ * The article's optimizer takes gradients that a model's training step has
+ * produced; it has no counterpart to these calls. They are three operators of
+ * that step, each with its gradient: the embedding lookup, the norm and
+ * rotation of queries and keys, and causal attention with a sliding window
+ * and sink tokens. Their gradients come out in the layouts and types that
+ * muon_adamw_register_param takes.
+ *
+ * Conventions: no handle; work is queued on cuda_stream (a cudaStream_t of the
+ * current device, NULL = legacy default stream) and the call does not wait for
+ * it, allocates nothing and keeps nothing. Scratch memory is the caller's:
+ * the `_workspace` call says how many bytes a call needs, and the workspace
+ * (256-byte aligned) must stay allocated until the work has run. Strides count
+ * elements; a row's own elements are consecutive. Every sum, norm and softmax
+ * statistic is held in fp32 and results are rounded once when stored. Results
+ * do not depend on the order in which the GPU runs blocks: equal inputs give
+ * equal bits on a GPU of the same kind. Inputs and outputs may not overlap. */
+
+/* out[t] = scale * weight[ids[t]] for t < n_tokens; a row of zeros where
+ * ids[t] is outside [0, vocab) (e.g. -1 for a position that holds no token).
+ *   weight  vocab rows of `width` elements, weight_stride >= width apart;
+ *   ids     n_tokens int32 (id_bytes 4) or int64 (id_bytes 8) values;
+ *   out     n_tokens rows, out_stride >= width apart.
+ * Types MA_DT_F32 or MA_DT_BF16 each. Whole 16-byte accesses are used where
+ * width is a multiple of 8 and all rows start on 16-byte boundaries, single
+ * elements otherwise. Errors: MA_ERR_ARG, MA_ERR_SHAPE (width outside
+ * [1, 2^20], vocab outside [1, 2^30], n_tokens outside [0, 2^30], a stride
+ * below the width), MA_ERR_DTYPE, MA_ERR_ALIGN, MA_ERR_CUDA. */
+MA_API ma_status muon_adamw_embedding(const void* weight, int weight_dtype, int64_t weight_stride, int64_t vocab,
+                                      int64_t width, const void* ids, int id_bytes, int64_t n_tokens, double scale,
+                                      void* out, int out_dtype, int64_t out_stride, void* cuda_stream);
+
+/* The lookup's gradient, dense: grad[v] = scale * (sum of dout[t] over the
+ * tokens with ids[t] = v), zero for the rows that do not occur; with
+ * accumulate = 1 the sums are added to what grad holds and other rows stay
+ * untouched. Tokens outside [0, vocab) give nothing. The rows of one id are
+ * added in the order of their positions within fixed groups, so the result
+ * does not change from run to run. Errors as above. */
+MA_API ma_status muon_adamw_embedding_backward_workspace(int64_t n_tokens, int64_t vocab, int64_t width,
+                                                         int64_t* bytes);
+MA_API ma_status muon_adamw_embedding_backward(const void* dout, int dout_dtype, int64_t dout_stride, const void* ids,
+                                               int id_bytes, int64_t n_tokens, double scale, void* grad,
+                                               int grad_dtype, int64_t grad_stride, int64_t vocab, int64_t width,
+                                               int accumulate, void* workspace, int64_t workspace_bytes,
+                                               void* cuda_stream);
+
+/* Queries and keys, their norm and their rotation. For each head x of
+ * head_dim elements: y = x * w / sqrt(mean(x^2) + eps), then the pairs (a, b)
+ * among its first rot_dim elements become (a cos - b sin, b cos + a sin) with
+ * the cosine and sine of the token's position. Pair i is elements i and
+ * i + rot_dim / 2, or 2 i and 2 i + 1 with neighbours = 1.
+ *   dtype         of q, k, their outputs and gradients (weights and tables are fp32);
+ *   head_dim      a multiple of 8, at most 256; rot_dim a multiple of 16, 0 for none;
+ *   q, k          [token][head][head_dim] with strides; each row start 16-byte aligned;
+ *   q_weight      head_dim values (NULL allowed with no heads), k_weight likewise;
+ *   cos_table     [table_rows][rot_dim / 2], sin_table likewise, contiguous;
+ *   positions     n_tokens int32 or int64 (position_bytes 4 or 8); one outside
+ *                 the tables is read as their nearest row. */
+typedef struct {
+  int64_t n_tokens;
+  int32_t n_heads, n_kv_heads, head_dim, rot_dim;
+  int32_t dtype, neighbours, position_bytes, reserved;
+  double eps;
+  const void* q;
+  const void* k;
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+  const float* q_weight;
+  const float* k_weight;
+  const float* cos_table;
+  const float* sin_table;
+  int64_t table_rows;
+  const void* positions;
+} ma_qk_norm_rope;
+
+/* q_out and k_out: contiguous [token][head][head_dim]. Errors: MA_ERR_ARG,
+ * MA_ERR_SHAPE, MA_ERR_DTYPE, MA_ERR_ALIGN, MA_ERR_CUDA. */
+MA_API ma_status muon_adamw_qk_norm_rope(const ma_qk_norm_rope* d, void* q_out, void* k_out, void* cuda_stream);
+
+/* Its gradient: dq and dk (contiguous) from dq_out and dk_out (with strides),
+ * and the gradients of the two weights, summed over tokens and heads. q and k
+ * are the forward call's inputs; the norms are computed again from them. */
+MA_API ma_status muon_adamw_qk_norm_rope_backward_workspace(const ma_qk_norm_rope* d, int64_t* bytes);
+MA_API ma_status muon_adamw_qk_norm_rope_backward(const ma_qk_norm_rope* d, const void* dq_out,
+                                                  int64_t dq_token_stride, int64_t dq_head_stride, const void* dk_out,
+                                                  int64_t dk_token_stride, int64_t dk_head_stride, void* dq, void* dk,
+                                                  float* dq_weight, float* dk_weight, void* workspace,
+                                                  int64_t workspace_bytes, void* cuda_stream);
+
+/* Causal attention with a sliding window and sink tokens over packed samples.
+ * Query i of a sample sees key j of the same sample where j <= i and either
+ * i - j < window or j < sinks (both counted from the sample's first token):
+ *   s_ij = scale * q_i . k_j,  out_i = sum_j exp(s_ij - lse_i) v_j,
+ *   lse_i = log(sum_j exp(s_ij)) over the keys it sees.
+ * A query that sees no key (window 0 without sinks, or a token behind the last
+ * sample) has out 0, lse -infinity and no gradient.
+ *   n_heads       a multiple of n_kv_heads; query head h reads key head
+ *                 h / (n_heads / n_kv_heads);
+ *   head_dim      a multiple of 8, at most 128; all tensors are bf16, lse fp32;
+ *   window        >= 0 (values past n_tokens mean every earlier token);
+ *   sinks         0 .. 128;
+ *   cu_seqlens    device, n_seqs + 1 int32 values: sample b holds tokens
+ *                 cu_seqlens[b] to cu_seqlens[b + 1] - 1; ascending from 0 and
+ *                 at most n_tokens (values beyond are read as n_tokens).
+ *                 NULL: one sample of all n_tokens;
+ *   q, k, v       [token][head][head_dim] with strides, every row start
+ *                 16-byte aligned. */
+typedef struct {
+  int64_t n_tokens;
+  int32_t n_heads, n_kv_heads, head_dim, sinks;
+  int64_t window;
+  double scale;
+  const int32_t* cu_seqlens;
+  int32_t n_seqs, reserved;
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+} ma_window_attention;
+
+/* out: contiguous [token][head][head_dim] bf16; lse: contiguous
+ * [head][token] fp32. Errors: MA_ERR_ARG, MA_ERR_SHAPE, MA_ERR_ALIGN,
+ * MA_ERR_CUDA. */
+MA_API ma_status muon_adamw_window_attention(const ma_window_attention* d, void* out, float* lse, void* cuda_stream);
+
+/* Its gradient. dout: [token][head][head_dim] bf16 with strides; out, lse: as
+ * the forward call left them; dq, dk, dv: contiguous [token][head][head_dim]
+ * bf16 (dk and dv summed over the query heads that share a key head). */
+MA_API ma_status muon_adamw_window_attention_backward_workspace(const ma_window_attention* d, int64_t* bytes);
+MA_API ma_status muon_adamw_window_attention_backward(const ma_window_attention* d, const void* dout,
+                                                      int64_t dout_token_stride, int64_t dout_head_stride,
+                                                      const void* out, const float* lse, void* dq, void* dk, void* dv,
+                                                      void* workspace, int64_t workspace_bytes, void* cuda_stream);
+
 /* Message of the last error on this thread ("" if none). Never NULL. */
 MA_API const char* muon_adamw_last_error(void);
 

@@ -4,7 +4,9 @@ Argument marshalling only: every step of the optimizer runs in the CUDA
 kernels of ``lib/libmuon_adamw_gb300.so`` behind the C ABI declared in
 ``include/muon_adamw.h``. The functions below carry the C names; the
 ``MuonAdamW`` class is a convenience wrapper that takes torch tensors and
-passes their device pointers and the current CUDA stream.
+passes their device pointers and the current CUDA stream. The operators of
+the training step (embedding, query/key norm and rotation, sliding-window
+attention) have their wrappers over torch tensors in the module ``ops``.
 
 There is no fallback: if the shared library has not been built, every call
 raises ``LibraryNotBuilt`` (run ``muon_adamw_hybrid_grad_gb300.build.build()``).
@@ -111,6 +113,59 @@ class PlanInfo(ctypes.Structure):
     ]
 
 
+class QkNormRope(ctypes.Structure):
+    """ma_qk_norm_rope: the norm and rotation of queries and keys."""
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64),
+        ("n_heads", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("neighbours", ctypes.c_int32),
+        ("position_bytes", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("eps", ctypes.c_double),
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("k_token_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
+        ("cos_table", ctypes.c_void_p),
+        ("sin_table", ctypes.c_void_p),
+        ("table_rows", ctypes.c_int64),
+        ("positions", ctypes.c_void_p),
+    ]
+
+
+class WindowAttention(ctypes.Structure):
+    """ma_window_attention: causal attention with a window and sinks."""
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64),
+        ("n_heads", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("sinks", ctypes.c_int32),
+        ("window", ctypes.c_int64),
+        ("scale", ctypes.c_double),
+        ("cu_seqlens", ctypes.c_void_p),
+        ("n_seqs", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q_token_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("k_token_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_token_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+    ]
+
+
 class LibraryNotBuilt(RuntimeError):
     pass
 
@@ -165,6 +220,27 @@ _SIGNATURES = {
     "muon_adamw_grad_norm_noalloc": (ctypes.c_int, [ctypes.POINTER(_P), ctypes.POINTER(ctypes.c_int64),
                                                     ctypes.POINTER(ctypes.c_int32), ctypes.c_int, ctypes.c_double,
                                                     ctypes.c_double, _P, _P]),
+    "muon_adamw_embedding": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P,
+                                            ctypes.c_int, ctypes.c_int64, ctypes.c_double, _P, ctypes.c_int,
+                                            ctypes.c_int64, _P]),
+    "muon_adamw_embedding_backward_workspace": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                                               ctypes.POINTER(ctypes.c_int64)]),
+    "muon_adamw_embedding_backward": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int64, _P, ctypes.c_int,
+                                                     ctypes.c_int64, ctypes.c_double, _P, ctypes.c_int,
+                                                     ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, _P,
+                                                     ctypes.c_int64, _P]),
+    "muon_adamw_qk_norm_rope": (ctypes.c_int, [ctypes.POINTER(QkNormRope), _P, _P, _P]),
+    "muon_adamw_qk_norm_rope_backward_workspace": (ctypes.c_int, [ctypes.POINTER(QkNormRope),
+                                                                  ctypes.POINTER(ctypes.c_int64)]),
+    "muon_adamw_qk_norm_rope_backward": (ctypes.c_int, [ctypes.POINTER(QkNormRope), _P, ctypes.c_int64,
+                                                        ctypes.c_int64, _P, ctypes.c_int64, ctypes.c_int64, _P, _P,
+                                                        _P, _P, _P, ctypes.c_int64, _P]),
+    "muon_adamw_window_attention": (ctypes.c_int, [ctypes.POINTER(WindowAttention), _P, _P, _P]),
+    "muon_adamw_window_attention_backward_workspace": (ctypes.c_int, [ctypes.POINTER(WindowAttention),
+                                                                      ctypes.POINTER(ctypes.c_int64)]),
+    "muon_adamw_window_attention_backward": (ctypes.c_int, [ctypes.POINTER(WindowAttention), _P, ctypes.c_int64,
+                                                            ctypes.c_int64, _P, _P, _P, _P, _P, _P, ctypes.c_int64,
+                                                            _P]),
     "muon_adamw_last_error": (ctypes.c_char_p, []),
     "muon_adamw_version": (ctypes.c_char_p, []),
 }

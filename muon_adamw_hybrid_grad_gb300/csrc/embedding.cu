@@ -1,0 +1,540 @@
+// Embedding lookup with scaling, and its dense gradient from sorted tokens.
+//
+//   out[t]  = scale * weight[ids[t]]                    (zero where ids[t] is no row)
+//   grad[v] = scale * sum over {t : ids[t] = v} dout[t]  (+ grad[v] when accumulating)
+//
+// The gradient is deterministic: tokens are brought into the order (id,
+// position) by a stable radix sort and each id's rows are added in that order
+// in fp32, whatever the launch shape of other work on the GPU.
+#include <limits.h>
+
+#include "op_common.cuh"
+
+namespace ma {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ids as written by the caller: int32 or int64. Anything outside [0, vocab) is
+// no token and maps to `vocab`.
+__device__ __forceinline__ uint32_t read_id(const void* ids, bool wide, int64_t t, uint32_t vocab) {
+  const int64_t v = wide ? static_cast<const int64_t*>(ids)[t] : (int64_t)static_cast<const int32_t*>(ids)[t];
+  return (v < 0 || v >= (int64_t)vocab) ? vocab : (uint32_t)v;
+}
+
+// ---- lookup ----
+// blockDim.x threads take VEC columns each, blockDim.y token groups of ROWS
+// tokens whose rows are loaded before any is stored.
+template <typename W, typename O, int VEC>
+__global__ void __launch_bounds__(kThreads) embedding_kernel(const W* __restrict__ weight, int64_t wstride,
+                                                             uint32_t vocab, int width, const void* __restrict__ ids,
+                                                             int wide, int64_t n, float scale, O* __restrict__ out,
+                                                             int64_t ostride) {
+  constexpr int ROWS = 4;
+  pdl_launch();
+  pdl_wait();
+  const int64_t t0 = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * ROWS;
+  uint32_t id[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) id[r] = t0 + r < n ? read_id(ids, wide != 0, t0 + r, vocab) : vocab;
+  for (int c = (int)(threadIdx.x + blockDim.x * blockIdx.y) * VEC; c < width; c += (int)(blockDim.x * gridDim.y) * VEC) {
+    float x[ROWS][VEC];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) x[r][i] = 0.f;
+      if (id[r] < vocab) load_vec<VEC>(weight + (int64_t)id[r] * wstride + c, x[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      if (t0 + r >= n) break;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) x[r][i] = id[r] < vocab ? x[r][i] * scale : 0.f;
+      store_vec<VEC>(out + (t0 + r) * ostride + c, x[r]);
+    }
+  }
+}
+
+// ---- gradient: sort, then sum ----
+// The first cluster sorts the tokens by id (stable least-significant-digit
+// radix sort over the cluster's CTAs, digit totals exchanged through
+// distributed shared memory); every other CTA meanwhile fills the gradient
+// with zeros, which hides the sort behind the writes of a large vocabulary.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortCluster = 8;
+constexpr int kDigitBits = 9;  // two passes cover ids below 2^18
+constexpr int kDigits = 1 << kDigitBits;
+constexpr size_t kSortSmem = (size_t)kSortWarps * kDigits * 4 + 2 * kDigits * 4 + 64 * 4;
+
+struct SortArgs {
+  const void* ids;
+  int wide;
+  int64_t n;
+  uint32_t vocab;
+  int passes, bits;            // digits of `bits` bits
+  uint32_t *key0, *pos0, *key1, *pos1;  // ping-pong buffers; the last pass writes key0/pos0
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t ld_dsmem(const uint32_t* p, uint32_t rank) {
+  uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(r) : "memory");
+  return v;
+}
+
+__device__ void sort_tokens(const SortArgs& a, uint32_t* sm) {
+  uint32_t* hist = sm;                             // [warp][digit]
+  uint32_t* total = sm + kSortWarps * kDigits;     // this CTA's count of each digit
+  uint32_t* wsum = total + 2 * kDigits;            // block scan
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  // contiguous runs of whole 32-token groups: CTA, then warp
+  const int64_t groups = (a.n + 31) / 32;
+  const int64_t per_cta = (groups + kSortCluster - 1) / kSortCluster;
+  const int64_t per_warp = (per_cta + kSortWarps - 1) / kSortWarps;
+  int64_t g0 = (int64_t)rank * per_cta + warp * per_warp;
+  int64_t g1 = min(min(g0 + per_warp, (int64_t)(rank + 1) * per_cta), groups);
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const bool first = pass == 0;
+    // the last pass writes buffer 0, so the one before it writes buffer 1
+    const bool to0 = ((a.passes - 1 - pass) & 1) == 0;
+    const uint32_t* skey = to0 ? a.key1 : a.key0;
+    const uint32_t* spos = to0 ? a.pos1 : a.pos0;
+    uint32_t* dkey = to0 ? a.key0 : a.key1;
+    uint32_t* dpos = to0 ? a.pos0 : a.pos1;
+    const int shift = pass * a.bits;
+    const uint32_t mask = (1u << a.bits) - 1;
+    for (int i = tid; i < kSortWarps * kDigits; i += kSortThreads) hist[i] = 0;
+    __syncthreads();
+    uint32_t* mine = hist + warp * kDigits;
+    for (int64_t g = g0; g < g1; ++g) {
+      const int64_t t = g * 32 + lane;
+      if (t < a.n) {
+        const uint32_t key = first ? read_id(a.ids, a.wide != 0, t, a.vocab) : __ldcg(skey + t);
+        atomicAdd(mine + ((key >> shift) & mask), 1u);
+      }
+    }
+    __syncthreads();
+    // per digit: exclusive scan over this CTA's warps, and the CTA's total
+    if (tid < kDigits) {
+      uint32_t s = 0;
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t c = hist[w * kDigits + tid];
+        hist[w * kDigits + tid] = s;
+        s += c;
+      }
+      total[tid] = s;
+    }
+    cluster_barrier();
+    // digits below this one over the whole cluster, plus this digit in lower CTAs
+    uint32_t all = 0, lower = 0;
+    if (tid < kDigits) {
+      for (int r = 0; r < kSortCluster; ++r) {
+        const uint32_t c = ld_dsmem(total + tid, r);
+        if (r < (int)rank) lower += c;
+        all += c;
+      }
+    }
+    uint32_t incl = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+      uint32_t w = wsum[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+      }
+      wsum[32 + lane] = w;
+    }
+    __syncthreads();
+    if (tid < kDigits) {
+      const uint32_t base = incl - all + (warp > 0 ? wsum[32 + warp - 1] : 0) + lower;
+      for (int w = 0; w < kSortWarps; ++w) hist[w * kDigits + tid] += base;
+    }
+    __syncthreads();
+    for (int64_t g = g0; g < g1; ++g) {
+      const int64_t t = g * 32 + lane;
+      const bool on = t < a.n;
+      uint32_t key = 0, pos = 0;
+      if (on) {
+        key = first ? read_id(a.ids, a.wide != 0, t, a.vocab) : __ldcg(skey + t);
+        pos = first ? (uint32_t)t : __ldcg(spos + t);
+      }
+      const uint32_t d = (key >> shift) & mask;
+      const uint32_t peers = __match_any_sync(0xffffffffu, on ? d : 0xffffffffu);
+      const uint32_t before = __popc(peers & ((1u << lane) - 1));
+      uint32_t at = 0;
+      if (on) at = mine[d] + before;
+      __syncwarp();
+      if (on) {
+        if (before == 0) mine[d] += __popc(peers);
+        dkey[at] = key;
+        dpos[at] = pos;
+      }
+      __syncwarp();
+    }
+    // the cluster's writes are visible to the cluster after its barrier
+    __threadfence();
+    cluster_barrier();
+  }
+}
+
+__global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __grid_constant__ SortArgs a,
+                                                                      uint8_t* __restrict__ grad, int64_t row_bytes,
+                                                                      int64_t stride_bytes, int64_t rows, int vec) {
+  extern __shared__ __align__(16) uint32_t sort_sm[];
+  pdl_launch();
+  pdl_wait();
+  if (blockIdx.x < kSortCluster) {
+    sort_tokens(a, sort_sm);
+  } else {
+    const int64_t nth = (int64_t)(gridDim.x - kSortCluster) * kSortThreads;
+    const int64_t me = (int64_t)(blockIdx.x - kSortCluster) * kSortThreads + threadIdx.x;
+    if (stride_bytes == row_bytes) row_bytes *= rows, stride_bytes = row_bytes, rows = 1;
+    const int unit = vec ? 16 : 2;
+    const int64_t per_row = row_bytes / unit;
+    if (rows == 1) {
+      for (int64_t i = me; i < per_row; i += nth) {
+        if (vec)
+          reinterpret_cast<uint4*>(grad)[i] = make_uint4(0, 0, 0, 0);
+        else
+          reinterpret_cast<uint16_t*>(grad)[i] = 0;
+      }
+    } else {
+      // a CTA to a row, so that no index is divided
+      for (int64_t r = blockIdx.x - kSortCluster; r < rows; r += gridDim.x - kSortCluster) {
+        uint8_t* row = grad + r * stride_bytes;
+        for (int64_t i = threadIdx.x; i < per_row; i += kSortThreads) {
+          if (vec)
+            reinterpret_cast<uint4*>(row)[i] = make_uint4(0, 0, 0, 0);
+          else
+            reinterpret_cast<uint16_t*>(row)[i] = 0;
+        }
+      }
+    }
+  }
+}
+
+// Sums of dout over runs of equal ids. A chunk of `per` sorted tokens belongs
+// to one row of threads; a run inside it is written to the gradient at once,
+// a run that reaches over a border leaves fp32 partial sums: slot 0 of a chunk
+// holds the run that came in from the chunk before, slot 1 the run that starts
+// here and goes on.
+struct SumArgs {
+  const uint32_t *key, *pos;
+  int64_t n;
+  uint32_t vocab;
+  int width, per;
+  float scale;
+  int accumulate;
+  int64_t dstride, gstride;
+  float* partial;  // [chunk][2][width]
+};
+
+template <int VEC, typename G>
+__device__ __forceinline__ void write_grad(G* grad, const SumArgs& a, uint32_t key, int c, const float (&s)[VEC]) {
+  float y[VEC];
+  G* p = grad + (int64_t)key * a.gstride + c;
+  if (a.accumulate) {
+    load_vec<VEC>(p, y);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) y[i] = fmaf(s[i], a.scale, y[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) y[i] = s[i] * a.scale;
+  }
+  store_vec<VEC>(p, y);
+}
+
+template <typename D, typename G, int VEC>
+__global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_constant__ SumArgs a,
+                                                                 const D* __restrict__ dout, G* __restrict__ grad) {
+  constexpr int AHEAD = 4;
+  pdl_launch();
+  pdl_wait();
+  const int64_t chunk = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t t0 = chunk * a.per, t1 = min(t0 + a.per, a.n);
+  const int c = (int)(threadIdx.x + blockDim.x * blockIdx.y) * VEC;
+  if (t0 < a.n && c < a.width) {
+    const uint32_t before = t0 > 0 ? a.key[t0 - 1] : UINT_MAX;
+    const uint32_t after = t1 < a.n ? a.key[t1] : UINT_MAX;
+    float* part = a.partial + chunk * 2 * a.width + c;
+    float s[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s[i] = 0.f;
+    uint32_t cur = a.key[t0];
+    bool came_in = cur == before;
+    for (int64_t t = t0; t < t1 && cur < a.vocab; t += AHEAD) {
+      float x[AHEAD][VEC];
+      uint32_t key[AHEAD];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        key[u] = t + u < t1 ? a.key[t + u] : a.vocab;
+        if (key[u] < a.vocab) load_vec<VEC>(dout + (int64_t)a.pos[t + u] * a.dstride + c, x[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        if (t + u >= t1) break;
+        if (key[u] != cur) {
+          if (came_in)
+            store_vec<VEC>(part, s);
+          else
+            write_grad<VEC>(grad, a, cur, c, s);
+          came_in = false;
+          cur = key[u];
+          if (cur >= a.vocab) break;  // ids of no token are last
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) s[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s[i] += x[u][i];
+      }
+    }
+    if (cur < a.vocab) {
+      if (came_in)
+        store_vec<VEC>(part, s);
+      else if (cur == after)
+        store_vec<VEC>(part + a.width, s);
+      else
+        write_grad<VEC>(grad, a, cur, c, s);
+    }
+  }
+}
+
+// Joins the runs that reach over a border, at the chunk where they start.
+template <typename G, int VEC>
+__global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_constant__ SumArgs a,
+                                                                  G* __restrict__ grad) {
+  pdl_launch();
+  pdl_wait();
+  const int64_t chunk = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t t0 = chunk * a.per, t1 = t0 + a.per;
+  const int c = (int)(threadIdx.x + blockDim.x * blockIdx.y) * VEC;
+  if (t1 < a.n && c < a.width) {
+    const uint32_t cur = a.key[t1 - 1];
+    const bool starts_here = t0 == 0 || a.key[t0 - 1] != cur || a.key[t0] != cur;
+    if (cur < a.vocab && a.key[t1] == cur && starts_here) {
+      float s[VEC];
+      load_vec<VEC>(a.partial + (chunk * 2 + 1) * a.width + c, s);
+      for (int64_t k = chunk + 1; k * a.per < a.n && a.key[k * a.per] == cur; ++k) {
+        float y[VEC];
+        load_vec<VEC>(a.partial + k * 2 * a.width + c, y);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s[i] += y[i];
+      }
+      write_grad<VEC>(grad, a, cur, c, s);
+    }
+  }
+}
+
+// ---- host ----
+struct Plan {
+  int per;          // sorted tokens of a chunk
+  int64_t chunks;
+  int64_t key_bytes, bytes;
+};
+
+Plan plan_backward(int64_t n, int64_t width) {
+  Plan p;
+  p.per = 16;
+  p.chunks = (n + p.per - 1) / p.per;
+  p.key_bytes = (n * 4 + 255) / 256 * 256;
+  p.bytes = 4 * p.key_bytes + p.chunks * 2 * ((width + 7) / 8 * 8) * 4 + 256;
+  return p;
+}
+
+// Threads of a block: x over the columns, y over rows.
+dim3 block_of(int64_t width, int vec) {
+  int64_t cols = (width + vec - 1) / vec;
+  int x = 32;
+  while (x < kThreads && x < cols) x *= 2;
+  return dim3((unsigned)x, (unsigned)(kThreads / x));
+}
+
+ma_status check_rows(const char* what, const void* p, int dt, int64_t stride, int64_t width, int64_t rows) {
+  if (!op_dtype_ok(dt)) return op_fail(MA_ERR_DTYPE, "%s: dtype %d is neither MA_DT_F32 nor MA_DT_BF16", what, dt);
+  if (rows > 0 && !p) return op_fail(MA_ERR_ARG, "%s must not be NULL", what);
+  if (!op_aligned(p, op_dtype_size(dt))) return op_fail(MA_ERR_ALIGN, "%s is not aligned to its element size", what);
+  if (stride < width) return op_fail(MA_ERR_SHAPE, "%s: row stride %lld below the width", what, (long long)stride);
+  return MA_OK;
+}
+
+ma_status check_common(int64_t vocab, int64_t width, const void* ids, int id_bytes, int64_t n, double scale) {
+  if (vocab < 1 || vocab > ((int64_t)1 << 30)) return op_fail(MA_ERR_SHAPE, "vocab outside [1, 2^30]");
+  if (width < 1 || width > ((int64_t)1 << 20)) return op_fail(MA_ERR_SHAPE, "width outside [1, 2^20]");
+  if (n < 0 || n > ((int64_t)1 << 30)) return op_fail(MA_ERR_SHAPE, "n_tokens outside [0, 2^30]");
+  if (id_bytes != 4 && id_bytes != 8) return op_fail(MA_ERR_ARG, "id_bytes must be 4 or 8");
+  if (n > 0 && !ids) return op_fail(MA_ERR_ARG, "ids must not be NULL");
+  if (!op_aligned(ids, id_bytes)) return op_fail(MA_ERR_ALIGN, "ids are not aligned to their size");
+  if (!(scale - scale == 0.0)) return op_fail(MA_ERR_ARG, "scale must be finite");
+  return MA_OK;
+}
+
+// 8-element accesses: whole vectors, and rows on 16-byte boundaries.
+bool rows_vec(const void* p, int dt, int64_t stride, int64_t width) {
+  return width % 8 == 0 && op_aligned(p, 16) && stride * op_dtype_size(dt) % 16 == 0;
+}
+
+template <typename W, typename O>
+cudaError_t run_lookup(bool vec, const void* weight, int64_t wstride, int64_t vocab, int64_t width, const void* ids,
+                       int wide, int64_t n, float scale, void* out, int64_t ostride, cudaStream_t st) {
+  const dim3 b = block_of(width, vec ? 8 : 1);
+  const dim3 g((unsigned)((n + 4 * b.y - 1) / (4 * b.y)), 1);
+  if (vec)
+    return op_launch(embedding_kernel<W, O, 8>, g, b, 0, st, 1, static_cast<const W*>(weight), wstride,
+                     (uint32_t)vocab, (int)width, ids, wide, n, scale, static_cast<O*>(out), ostride);
+  return op_launch(embedding_kernel<W, O, 1>, g, b, 0, st, 1, static_cast<const W*>(weight), wstride, (uint32_t)vocab,
+                   (int)width, ids, wide, n, scale, static_cast<O*>(out), ostride);
+}
+
+template <typename D, typename G, int VEC>
+cudaError_t run_sums(const SumArgs& a, int64_t chunks, const void* dout, void* grad, cudaStream_t st) {
+  const dim3 b = block_of(a.width, VEC);
+  const dim3 g((unsigned)((chunks + b.y - 1) / b.y), (unsigned)((a.width + b.x * VEC - 1) / (b.x * VEC)));
+  cudaError_t e = op_launch(embedding_sum_kernel<D, G, VEC>, g, b, 0, st, 1, a, static_cast<const D*>(dout),
+                            static_cast<G*>(grad));
+  if (e != cudaSuccess || chunks < 2) return e;
+  return op_launch(embedding_join_kernel<G, VEC>, g, b, 0, st, 1, a, static_cast<G*>(grad));
+}
+
+}  // namespace
+}  // namespace ma
+
+using namespace ma;
+
+extern "C" {
+
+ma_status muon_adamw_embedding(const void* weight, int weight_dtype, int64_t weight_stride, int64_t vocab,
+                               int64_t width, const void* ids, int id_bytes, int64_t n_tokens, double scale,
+                               void* out, int out_dtype, int64_t out_stride, void* cuda_stream) {
+  ma_status st = check_common(vocab, width, ids, id_bytes, n_tokens, scale);
+  if (st == MA_OK) st = check_rows("weight", weight, weight_dtype, weight_stride, width, vocab);
+  if (st == MA_OK) st = check_rows("out", out, out_dtype, out_stride, width, n_tokens);
+  if (st != MA_OK) return st;
+  if (n_tokens > 0) {
+    const bool vec = rows_vec(weight, weight_dtype, weight_stride, width) && rows_vec(out, out_dtype, out_stride, width);
+    cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    const int wide = id_bytes == 8;
+    const float sc = (float)scale;
+    cudaError_t e;
+    if (weight_dtype == MA_DT_BF16)
+      e = out_dtype == MA_DT_BF16
+              ? run_lookup<__nv_bfloat16, __nv_bfloat16>(vec, weight, weight_stride, vocab, width, ids, wide, n_tokens,
+                                                         sc, out, out_stride, s)
+              : run_lookup<__nv_bfloat16, float>(vec, weight, weight_stride, vocab, width, ids, wide, n_tokens, sc,
+                                                 out, out_stride, s);
+    else
+      e = out_dtype == MA_DT_BF16 ? run_lookup<float, __nv_bfloat16>(vec, weight, weight_stride, vocab, width, ids,
+                                                                     wide, n_tokens, sc, out, out_stride, s)
+                                  : run_lookup<float, float>(vec, weight, weight_stride, vocab, width, ids, wide,
+                                                             n_tokens, sc, out, out_stride, s);
+    if (e != cudaSuccess) return op_cuda(e, "embedding launch");
+  }
+  clear_last_error();
+  return MA_OK;
+}
+
+ma_status muon_adamw_embedding_backward_workspace(int64_t n_tokens, int64_t vocab, int64_t width, int64_t* bytes) {
+  if (!bytes) return op_fail(MA_ERR_ARG, "bytes must not be NULL");
+  ma_status st = check_common(vocab, width, bytes, 8, n_tokens, 1.0);
+  if (st != MA_OK) return st;
+  *bytes = plan_backward(n_tokens, width).bytes;
+  clear_last_error();
+  return MA_OK;
+}
+
+ma_status muon_adamw_embedding_backward(const void* dout, int dout_dtype, int64_t dout_stride, const void* ids,
+                                        int id_bytes, int64_t n_tokens, double scale, void* grad, int grad_dtype,
+                                        int64_t grad_stride, int64_t vocab, int64_t width, int accumulate,
+                                        void* workspace, int64_t workspace_bytes, void* cuda_stream) {
+  ma_status st = check_common(vocab, width, ids, id_bytes, n_tokens, scale);
+  if (st == MA_OK) st = check_rows("dout", dout, dout_dtype, dout_stride, width, n_tokens);
+  if (st == MA_OK) st = check_rows("grad", grad, grad_dtype, grad_stride, width, vocab);
+  if (st != MA_OK) return st;
+  if (accumulate != 0 && accumulate != 1) return op_fail(MA_ERR_ARG, "accumulate must be 0 or 1");
+  const Plan p = plan_backward(n_tokens, width);
+  if (!workspace) return op_fail(MA_ERR_ARG, "workspace must not be NULL");
+  if (!op_aligned(workspace, 256)) return op_fail(MA_ERR_ALIGN, "workspace is not 256-byte aligned");
+  if (workspace_bytes < p.bytes)
+    return op_fail(MA_ERR_ARG, "workspace of %lld bytes, %lld are needed", (long long)workspace_bytes,
+                   (long long)p.bytes);
+  if (n_tokens == 0 && accumulate) {
+    clear_last_error();
+    return MA_OK;
+  }
+  int sms = 0;
+  cudaError_t e = op_num_sms(&sms);
+  if (e != cudaSuccess) return op_cuda(e, "device query");
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  SortArgs a{};
+  a.ids = ids;
+  a.wide = id_bytes == 8;
+  a.n = n_tokens;
+  a.vocab = (uint32_t)vocab;
+  int bits = 1;
+  while (((int64_t)1 << bits) <= vocab) ++bits;  // keys 0 .. vocab
+  a.passes = n_tokens > 0 ? (bits + kDigitBits - 1) / kDigitBits : 0;
+  a.bits = a.passes > 0 ? (bits + a.passes - 1) / a.passes : 0;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.key0 = reinterpret_cast<uint32_t*>(ws);
+  a.pos0 = reinterpret_cast<uint32_t*>(ws + p.key_bytes);
+  a.key1 = reinterpret_cast<uint32_t*>(ws + 2 * p.key_bytes);
+  a.pos1 = reinterpret_cast<uint32_t*>(ws + 3 * p.key_bytes);
+  const int64_t gsize = op_dtype_size(grad_dtype);
+  const int64_t fill = accumulate ? 0 : vocab * width * gsize;
+  int64_t fill_ctas = (fill + 64 * kSortThreads - 1) / (64 * kSortThreads);  // four 16-byte stores a thread at least
+  if (fill_ctas > 2 * sms) fill_ctas = 2 * sms;
+  const unsigned grid = (unsigned)(kSortCluster + (fill_ctas + kSortCluster - 1) / kSortCluster * kSortCluster);
+  e = cudaFuncSetAttribute(embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortSmem);
+  if (e != cudaSuccess) return op_cuda(e, "embedding sort attributes");
+  e = op_launch(embedding_sort_kernel, dim3(grid), dim3(kSortThreads), kSortSmem, s, kSortCluster, a,
+                static_cast<uint8_t*>(grad), width * gsize, grad_stride * gsize, accumulate ? (int64_t)0 : vocab,
+                (int)(op_aligned(grad, 16) && width * gsize % 16 == 0 && grad_stride * gsize % 16 == 0));
+  if (e != cudaSuccess) return op_cuda(e, "embedding sort launch");
+  if (n_tokens > 0) {
+    SumArgs u{};
+    u.key = a.key0;
+    u.pos = a.pos0;
+    u.n = n_tokens;
+    u.vocab = (uint32_t)vocab;
+    u.width = (int)width;
+    u.per = p.per;
+    u.scale = (float)scale;
+    u.accumulate = accumulate;
+    u.dstride = dout_stride;
+    u.gstride = grad_stride;
+    u.partial = reinterpret_cast<float*>(ws + 4 * p.key_bytes);
+    const bool vec = rows_vec(dout, dout_dtype, dout_stride, width) && rows_vec(grad, grad_dtype, grad_stride, width);
+    const bool db = dout_dtype == MA_DT_BF16, gb = grad_dtype == MA_DT_BF16;
+    typedef __nv_bfloat16 B;
+    if (vec)
+      e = db ? (gb ? run_sums<B, B, 8>(u, p.chunks, dout, grad, s) : run_sums<B, float, 8>(u, p.chunks, dout, grad, s))
+             : (gb ? run_sums<float, B, 8>(u, p.chunks, dout, grad, s)
+                   : run_sums<float, float, 8>(u, p.chunks, dout, grad, s));
+    else
+      e = db ? (gb ? run_sums<B, B, 1>(u, p.chunks, dout, grad, s) : run_sums<B, float, 1>(u, p.chunks, dout, grad, s))
+             : (gb ? run_sums<float, B, 1>(u, p.chunks, dout, grad, s)
+                   : run_sums<float, float, 1>(u, p.chunks, dout, grad, s));
+    if (e != cudaSuccess) return op_cuda(e, "embedding sum launch");
+  }
+  clear_last_error();
+  return MA_OK;
+}
+
+}  // extern "C"
