@@ -538,8 +538,8 @@ MA_API ma_status muon_adamw_qk_norm_rope_backward(const ma_qk_norm_rope* d, cons
  *   lse_i = log(sum_j exp(s_ij)) over the keys it sees.
  * A query that sees no key (window 0 without sinks, or a token behind the last
  * sample) has out 0, lse -infinity and no gradient.
- *   n_heads       a multiple of n_kv_heads; query head h reads key head
- *                 h / (n_heads / n_kv_heads);
+ *   n_heads       a multiple of n_kv_heads, at most 1024; query head h reads key
+ *                 head h / (n_heads / n_kv_heads);
  *   head_dim      a multiple of 8, at most 128; all tensors are bf16, lse fp32;
  *   window        >= 0 (values past n_tokens mean every earlier token);
  *   sinks         0 .. 128;
@@ -547,8 +547,14 @@ MA_API ma_status muon_adamw_qk_norm_rope_backward(const ma_qk_norm_rope* d, cons
  *                 cu_seqlens[b] to cu_seqlens[b + 1] - 1; ascending from 0 and
  *                 at most n_tokens (values beyond are read as n_tokens).
  *                 NULL: one sample of all n_tokens;
+ *   scale         positive;
  *   q, k, v       [token][head][head_dim] with strides, every row start
- *                 16-byte aligned. */
+ *                 16-byte aligned, strides at least head_dim.
+ * Softmax weights, and in the gradient those of the scores, are rounded to
+ * bf16 before they enter a product. Values that are not finite stay within
+ * their sample: a sample's results do not depend on any other token. Within a
+ * sample they can also reach queries that do not see their key, in products
+ * with weights that are zero. */
 typedef struct {
   int64_t n_tokens;
   int32_t n_heads, n_kv_heads, head_dim, sinks;
@@ -575,6 +581,11 @@ MA_API ma_status muon_adamw_window_attention_backward(const ma_window_attention*
                                                       int64_t dout_token_stride, int64_t dout_head_stride,
                                                       const void* out, const float* lse, void* dq, void* dk, void* dv,
                                                       void* workspace, int64_t workspace_bytes, void* cuda_stream);
+
+/* Wait for cuda_stream and read the attention kernels' error word.
+ * MA_ERR_DEVICE_CHECK if a bounded in-kernel wait of an earlier call on this
+ * device ran out (the word is then cleared); MA_ERR_CUDA. */
+MA_API ma_status muon_adamw_window_attention_check(void* cuda_stream);
 
 /* Message of the last error on this thread ("" if none). Never NULL. */
 MA_API const char* muon_adamw_last_error(void);

@@ -1,184 +1,406 @@
-// Causal attention with a sliding window and sink tokens, and its gradient.
+// Causal attention with a sliding window and sink tokens, forward pass, and
+// the C entry points of the operator.
 //
-// One warp to a query (forward, dq) or to a key (dk, dv), a head's elements
-// spread over its lanes; scores, softmax statistics and sums in fp32.
-#include <math.h>
-
-#include "op_common.cuh"
+// One pass over the keys with the running maximum m and sum l of the softmax:
+//   S = Q K^T,  P = exp2(c S - m),  l += rowsum(P),  O += P V,  c = scale log2(e)
+// and out = O / l, lse = (m + log2 l) ln 2.
+//
+// window_forward_kernel (one persistent CTA per SM, 320 threads) works on two
+// tiles of 128 queries that share their keys and values: the same queries of
+// two heads that read one key head, or, where heads do not pair, two
+// neighbouring tiles of one head.
+//   warps 0-3, 4-7  softmax of the first and of the second tile, a thread to a
+//                   query: S from TMEM, P (bf16) back to TMEM over S;
+//   warp 8          TMA: the two query tiles, then key and value tiles into a
+//                   ring;
+//   warp 9          tcgen05.mma: S = Q K^T from shared memory, O += P V with P
+//                   from TMEM. The two tiles alternate, so that one tile's
+//                   products run while the other's softmax does.
+// TMEM: S0 | S1 | O0 | O1, 128 columns each.
+//
+// O is rescaled only when a row's maximum has grown by more than 2^8 since it
+// was last taken as m: P then stays below 2^8 and sums in fp32 lose nothing.
+#include "window_attention.cuh"
 
 namespace ma {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kMaxDim = 128, kPer = kMaxDim / 32;
+constexpr int kThreads = 320;
+constexpr int kErrForward = 0x201, kErrAlign = 0x204;
 
-struct AttnArgs {
-  int n, heads, kv_heads, dim, sinks, window, n_seqs;
-  float scale;
-  const int32_t* cu;
-  const __nv_bfloat16 *q, *k, *v;
-  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;
+template <int DP>
+struct FwdSmem {
+  static constexpr uint32_t TILE = kAttnTile * DP * 2;
+  static constexpr int SLOTS = DP == 128 ? 5 : 8;
+  static constexpr uint32_t RING = 2 * TILE;
+  static constexpr uint32_t BARS = RING + SLOTS * TILE;
+  // full[SLOTS], empty[SLOTS], q full, q empty, s full[2], p full[2], o full[2], drain
+  static constexpr int NBARS = 2 * SLOTS + 9;
+  static constexpr uint32_t BYTES = BARS + NBARS * 8 + 16;
+  static_assert(BYTES <= 232448, "shared memory per CTA");
 };
 
-// The sample [b, e) of token t; empty where t lies behind the last one.
-__device__ __forceinline__ int2 sample_of(const AttnArgs& a, int t) {
-  if (!a.cu) return make_int2(0, a.n);
-  int b = 0;
-  for (int i = 1; i <= a.n_seqs; ++i) {
-    const int e = min(max(a.cu[i], b), a.n);
-    if (t < e) return make_int2(b, e);
-    b = e;
+// The key tiles two query tiles meet, as one list: tile 0 for the sinks where
+// no window reaches it, then lo .. hi.
+struct PairTiles {
+  KeyTiles r[2];
+  int lo, steps, sink;
+  __device__ __forceinline__ int tile(int n) const { return sink && n == 0 ? 0 : lo + n - sink; }
+  __device__ __forceinline__ bool use(int s, int kt) const {
+    return (kt >= r[s].lo && kt <= r[s].hi) || (kt == 0 && r[s].sink);
   }
-  return make_int2(t, t);
+};
+__device__ __forceinline__ PairTiles pair_tiles(const AttnArgs& a, const SampleTile& t, int step) {
+  PairTiles p;
+  p.r[0] = key_tiles(a, t.live, t.len, t.p0);
+  p.r[1] = key_tiles(a, t.live, t.len, t.p0 + step);
+  p.sink = p.r[0].sink ? 1 : 0;
+  p.lo = p.r[0].lo;
+  p.steps = p.sink + max(0, max(p.r[0].hi, p.r[1].hi) - p.lo + 1);
+  return p;
 }
 
-__device__ __forceinline__ void load_row(const __nv_bfloat16* p, int dim, int lane, float (&x)[kPer]) {
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) x[i] = lane + 32 * i < dim ? __bfloat162float(p[lane + 32 * i]) : 0.f;
-}
-__device__ __forceinline__ void store_row(__nv_bfloat16* p, int dim, int lane, const float (&x)[kPer]) {
-#pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (lane + 32 * i < dim) p[lane + 32 * i] = __float2bfloat16_rn(x[i]);
-}
-__device__ __forceinline__ float dot(const float (&x)[kPer], const float (&y)[kPer]) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) s = fmaf(x[i], y[i], s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
-// f(j) for every key that query t of the sample [b, e) sees.
-template <typename F>
-__device__ __forceinline__ void each_key(const AttnArgs& a, int t, int2 smp, F f) {
-  if (smp.x >= smp.y) return;
-  const int lo = max(smp.x, t - a.window + 1), sink = min(min(smp.x + a.sinks, lo), t + 1);
-  for (int j = smp.x; j < sink; ++j) f(j);
-  for (int j = lo; j <= t; ++j) f(j);
-}
-
-__global__ void __launch_bounds__(kWarps * 32) window_forward_kernel(const __grid_constant__ AttnArgs a,
-                                                                     __nv_bfloat16* __restrict__ out,
-                                                                     float* __restrict__ lse) {
-  pdl_launch();
-  pdl_wait();
-  const int lane = threadIdx.x & 31, t = blockIdx.x * kWarps + (threadIdx.x >> 5), h = blockIdx.y;
-  if (t >= a.n) return;
-  const int g = h / (a.heads / a.kv_heads);
-  float q[kPer], o[kPer] = {}, m = -INFINITY, l = 0.f;
-  load_row(a.q + t * a.q_ts + h * a.q_hs, a.dim, lane, q);
-  each_key(a, t, sample_of(a, t), [&](int j) {
-    float k[kPer], v[kPer];
-    load_row(a.k + j * a.k_ts + g * a.k_hs, a.dim, lane, k);
-    load_row(a.v + j * a.v_ts + g * a.v_hs, a.dim, lane, v);
-    const float s = dot(q, k) * a.scale, mn = fmaxf(m, s);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float f = expf(m - base), p = expf(s - base);
-    l = l * f + p;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) o[i] = fmaf(p, v[i], o[i] * f);
-    m = mn;
-  });
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) o[i] *= inv;
-  store_row(out + ((int64_t)t * a.heads + h) * a.dim, a.dim, lane, o);
-  if (lane == 0) lse[(int64_t)h * a.n + t] = l == 0.f ? -INFINITY : m + logf(l);
-}
-
-struct GradArgs {
-  const __nv_bfloat16 *dout, *out;
-  int64_t do_ts, do_hs;
-  const float* lse;
-  float* delta;  // [head][token]: sum of dout * out
-  __nv_bfloat16 *dq, *dk, *dv;
+struct FwdItem {
+  SampleTile t;
+  PairTiles k;
+  int head[2], kv;
 };
 
-__global__ void __launch_bounds__(kWarps * 32) window_dq_kernel(const __grid_constant__ AttnArgs a,
-                                                                const __grid_constant__ GradArgs r) {
-  pdl_launch();
-  pdl_wait();
-  const int lane = threadIdx.x & 31, t = blockIdx.x * kWarps + (threadIdx.x >> 5), h = blockIdx.y;
-  if (t >= a.n) return;
-  const int g = h / (a.heads / a.kv_heads);
-  float q[kPer], d[kPer], o[kPer], dq[kPer] = {};
-  load_row(a.q + t * a.q_ts + h * a.q_hs, a.dim, lane, q);
-  load_row(r.dout + t * r.do_ts + h * r.do_hs, a.dim, lane, d);
-  load_row(r.out + ((int64_t)t * a.heads + h) * a.dim, a.dim, lane, o);
-  const float delta = dot(d, o), lse = r.lse[(int64_t)h * a.n + t];
-  if (lane == 0) r.delta[(int64_t)h * a.n + t] = delta;
-  each_key(a, t, sample_of(a, t), [&](int j) {
-    float k[kPer], v[kPer];
-    load_row(a.k + j * a.k_ts + g * a.k_hs, a.dim, lane, k);
-    load_row(a.v + j * a.v_ts + g * a.v_hs, a.dim, lane, v);
-    const float p = expf(dot(q, k) * a.scale - lse), ds = p * (dot(d, v) - delta);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) dq[i] = fmaf(ds, k[i], dq[i]);
-  });
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) dq[i] *= a.scale;
-  store_row(r.dq + ((int64_t)t * a.heads + h) * a.dim, a.dim, lane, dq);
+// Work item: a pair of query tiles. by_head: of two heads, else of one head.
+__device__ __forceinline__ FwdItem fwd_item(const AttnArgs& a, int item, int units, int lane) {
+  const bool by_head = units * 2 == a.heads;
+  const int rows = by_head ? kAttnTile : 2 * kAttnTile;
+  const int tile = item / units, u = item - tile * units;
+  FwdItem w;
+  w.t = find_unit(a, tile, lane, [rows](int len, bool) { return (len + rows - 1) / rows; });
+  w.t.p0 = w.t.index * rows;
+  w.k = pair_tiles(a, w.t, by_head ? 0 : kAttnTile);
+  w.head[0] = by_head ? 2 * u : u;
+  w.head[1] = by_head ? 2 * u + 1 : u;
+  w.kv = w.head[0] / (a.heads / a.kv_heads);
+  return w;
 }
 
-__global__ void __launch_bounds__(kWarps * 32) window_dkv_kernel(const __grid_constant__ AttnArgs a,
-                                                                 const __grid_constant__ GradArgs r) {
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_forward_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tmQ,
+                          const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                          __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int* __restrict__ err, int units) {
+  using SM = FwdSmem<DP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  // two words after the barriers: the TMEM base and the abort flag
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::BARS + SM::NBARS * 8);
+  volatile int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = smem_u32(smem), bars = base + SM::BARS;
+  Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, SM::TILE};
+  const uint32_t q_full = bars + 2 * SM::SLOTS * 8, q_empty = q_full + 8, s_full = q_full + 16, p_full = q_full + 32,
+                 o_full = q_full + 48, drain = q_full + 64;
+  if (base & 1023u) {  // the swizzle's phase is that of the address
+    if (threadIdx.x == 0) atomicCAS(err, 0, kErrAlign);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < SM::SLOTS; ++i) mbar_init(ring.full + 8 * i, 1), mbar_init(ring.empty + 8 * i, 1);
+    mbar_init(q_full, 1), mbar_init(q_empty, 1), mbar_init(drain, 1);
+    for (int s = 0; s < 2; ++s) mbar_init(s_full + 8 * s, 1), mbar_init(p_full + 8 * s, 128), mbar_init(o_full + 8 * s, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 9) tmem_alloc<1>(smem_u32(tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   pdl_launch();
   pdl_wait();
-  const int lane = threadIdx.x & 31, j = blockIdx.x * kWarps + (threadIdx.x >> 5), g = blockIdx.y;
-  if (j >= a.n) return;
-  const int2 smp = sample_of(a, j);
-  float k[kPer], v[kPer], dk[kPer] = {}, dv[kPer] = {};
-  load_row(a.k + j * a.k_ts + g * a.k_hs, a.dim, lane, k);
-  load_row(a.v + j * a.v_ts + g * a.v_hs, a.dim, lane, v);
-  const int last = j - smp.x < a.sinks ? smp.y : (int)min((int64_t)smp.y, (int64_t)j + a.window);
-  const int per = a.heads / a.kv_heads;
-  for (int h = g * per; h < (g + 1) * per; ++h) {
-    for (int t = j; t < last; ++t) {
-      float q[kPer], d[kPer];
-      load_row(a.q + t * a.q_ts + h * a.q_hs, a.dim, lane, q);
-      load_row(r.dout + t * r.do_ts + h * r.do_hs, a.dim, lane, d);
-      const float p = expf(dot(q, k) * a.scale - r.lse[(int64_t)h * a.n + t]);
-      const float ds = p * (dot(d, v) - r.delta[(int64_t)h * a.n + t]);
+  const int rows = units * 2 == a.heads ? kAttnTile : 2 * kAttnTile;
+  const int items = units * count_units(a, lane, [rows](int len, bool) { return (len + rows - 1) / rows; });
+  bool ok = true;
+
+  if (warp < 8) {
+    // ---- softmax ----
+    const int s = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + 128u * s + lanes, to = tmem + 256u + 128u * s + lanes;
+    uint32_t s_ph = 0, o_ph = 0;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const FwdItem w = fwd_item(a, item, units, lane);
+      const int p0 = w.t.p0 + (w.head[0] == w.head[1] ? s * kAttnTile : 0), i = p0 + row;
+      float m = -INFINITY, l = 0.f;
+      bool any = false;
+      for (int n = 0; n < w.k.steps && ok; ++n) {
+        const int kt = w.k.tile(n);
+        if (!w.k.use(s, kt)) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait(s_full + 8 * s, s_ph, abort_flag, err, kErrForward));
+        if (!ok) break;
+        s_ph ^= 1;
+        tc_fence_after();
+        uint32_t v[4][32];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        dk[i] = fmaf(ds, q[i], dk[i]);
-        dv[i] = fmaf(p, d[i], dv[i]);
+        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + 32 * c, v[c]);
+        tmem_ld_wait();
+        const int k0 = kt * kAttnTile;
+        if (!tile_full(a, p0, k0)) {
+          // key k0 + col is visible for col <= last and (col >= first or col < sink)
+          const int last = i - k0, first = i - a.window + 1 - k0, sink = a.sinks - k0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int col = 32 * c + j;
+              if (col > last || (col < first && col >= sink)) v[c][j] = 0xff800000u;
+            }
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(v[c][j]));
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+        const bool grow = mt > m + 8.f;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow ? ex2(m - mt) : 1.f;
+          if (grow) m = mt;
+          l *= f;
+          if (any) {
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 32) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(to + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st_32x32b_x32(to + c, o);
+            }
+          }
+        }
+        any = true;
+        const float shift = m == -INFINITY ? 0.f : -m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float x = ex2(fmaf(__uint_as_float(v[c][2 * j]), a.scale_log2, shift));
+            const float y = ex2(fmaf(__uint_as_float(v[c][2 * j + 1]), a.scale_log2, shift));
+            sum[j & 1] += x;
+            sum[2 + (j & 1)] += y;
+            p[j] = op_pack_bf16(x, y);
+          }
+          tmem_st_32x32b_x16(ts + 16 * c, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(p_full + 8 * s);
+      }
+      if (!ok) break;
+      if (any) {
+        ok = __all_sync(0xffffffffu, mbar_wait(o_full + 8 * s, o_ph, abort_flag, err, kErrForward));
+        if (!ok) break;
+        o_ph ^= 1;
+        tc_fence_after();
+      }
+      // a query that saw no key: zeros and -infinity
+      const float inv = any ? 1.f / l : 0.f;
+      const int64_t t = (int64_t)w.t.b + i;
+      __nv_bfloat16* po = out + (t * a.heads + w.head[s]) * a.dim;
+#pragma unroll 1
+      for (int c = 0; c < DP; c += 32) {
+        uint32_t o[32];
+        if (any) {
+          tmem_ld_32x32b_x32(to + c, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0u;
+        }
+        if (i < w.t.len) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            if (c + j < a.dim) {
+              uint32_t r[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                r[e] = op_pack_bf16(__uint_as_float(o[j + 2 * e]) * inv, __uint_as_float(o[j + 2 * e + 1]) * inv);
+              *reinterpret_cast<uint4*>(po + c + j) = make_uint4(r[0], r[1], r[2], r[3]);
+            }
+          }
+        }
+      }
+      if (i < w.t.len)
+        lse[(int64_t)w.head[s] * a.n + t] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      tc_fence_before();
+    }
+  } else if (warp == 8) {
+    // ---- TMA ----
+    uint32_t pos = 0, q_ph = 1, q_loads = 0;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const FwdItem w = fwd_item(a, item, units, lane);
+      const bool two = w.head[0] == w.head[1];
+      for (int n = 0; n < w.k.steps && ok; ++n) {
+        const int token = w.t.b + w.k.tile(n) * kAttnTile;
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          ok = mbar_wait(ring.empty_bar(pos), ring.empty_parity(pos), abort_flag, err, kErrForward);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_expect_tx(ring.full_bar(pos), SM::TILE);
+            load_tile<DP>(ring.slot(pos), kv ? &tmV : &tmK, token, w.kv, ring.full_bar(pos));
+          }
+          ++pos;
+          if (n == 0 && kv == 0) {
+            // the queries after the first keys: their buffer is free once the item before has issued its last S
+            ok = mbar_wait(q_empty, q_ph, abort_flag, err, kErrForward);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            q_ph ^= 1;
+            ++q_loads;
+            if (lane == 0) {
+              mbar_expect_tx(q_full, 2 * SM::TILE);
+              load_tile<DP>(base, &tmQ, w.t.b + w.t.p0, w.head[0], q_full);
+              load_tile<DP>(base + SM::TILE, &tmQ, w.t.b + w.t.p0 + (two ? kAttnTile : 0), w.head[1], q_full);
+            }
+          }
+        }
       }
     }
+    // every copy has landed before the CTA leaves
+    for (uint32_t k = pos > SM::SLOTS ? pos - SM::SLOTS : 0; k < pos; ++k)
+      drain_wait(ring.full_bar(k), ring.full_parity(k));
+    if (q_loads) drain_wait(q_full, (q_loads - 1) & 1);
+  } else {
+    // ---- MMA ----
+    uint32_t pos = 0, q_ph = 0, p_ph[2] = {0, 0};
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const FwdItem w = fwd_item(a, item, units, lane);
+      if (w.k.steps == 0) continue;
+      ok = __all_sync(0xffffffffu, mbar_wait(q_full, q_ph, abort_flag, err, kErrForward));
+      if (!ok) break;
+      q_ph ^= 1;
+      bool pend[2] = {false, false}, begun[2] = {false, false};
+      // step n issues S of tile n and O += P V of tile n - 1
+      for (int n = 0; n <= w.k.steps && ok; ++n) {
+        const uint32_t kpos = pos + 2 * n, vpos = pos + 2 * n - 1;
+        const int kt = n < w.k.steps ? w.k.tile(n) : 0;
+        bool k_in = false, v_in = false;
+        for (int s = 0; s < 2 && ok; ++s) {
+          if (pend[s]) {
+            if (!v_in) {
+              ok = mbar_wait(ring.full_bar(vpos), ring.full_parity(vpos), abort_flag, err, kErrForward);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              v_in = true;
+              const int valid = w.t.len - w.k.tile(n - 1) * kAttnTile;
+              if (valid < kAttnTile) clear_rows<DP>(ring.slot(vpos), valid, lane);
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(p_full + 8 * s, p_ph[s], abort_flag, err, kErrForward));
+            if (!ok) break;
+            p_ph[s] ^= 1;
+            tc_fence_after();
+            // the tile's last step for this half?
+            bool last = true;
+            for (int x = n; x < w.k.steps; ++x) last = last && !w.k.use(s, w.k.tile(x));
+            if (lane == 0) {
+              mma_ab<DP>(tmem + 256u + 128u * s, tmem + 128u * s, 32, ring.slot(vpos), begun[s]);
+              if (last) umma_commit<1>(o_full + 8 * s);
+            }
+            begun[s] = true;
+            pend[s] = false;
+          }
+          if (n < w.k.steps && w.k.use(s, kt)) {
+            if (!k_in) {
+              ok = mbar_wait(ring.full_bar(kpos), ring.full_parity(kpos), abort_flag, err, kErrForward);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              k_in = true;
+              tc_fence_after();
+            }
+            if (lane == 0) {
+              mma_abt<DP>(tmem + 128u * s, base + s * SM::TILE, ring.slot(kpos));
+              umma_commit<1>(s_full + 8 * s);
+            }
+            pend[s] = true;
+          }
+        }
+        if (ok && lane == 0) {
+          if (n > 0) umma_commit<1>(ring.empty_bar(vpos));
+          if (n < w.k.steps) umma_commit<1>(ring.empty_bar(kpos));
+          if (n == w.k.steps - 1) umma_commit<1>(q_empty);
+        }
+        __syncwarp();
+      }
+      pos += 2 * w.k.steps;
+    }
+    if (lane == 0) {
+      umma_commit<1>(drain);
+      drain_wait(drain, 0);
+    }
+    __syncwarp();
   }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) dk[i] *= a.scale;
-  store_row(r.dk + ((int64_t)j * a.kv_heads + g) * a.dim, a.dim, lane, dk);
-  store_row(r.dv + ((int64_t)j * a.kv_heads + g) * a.dim, a.dim, lane, dv);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc<1>(tmem, 512);
+}
+
+template <int DP>
+cudaError_t run_forward(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                        __nv_bfloat16* out, float* lse, int* err, int sms, cudaStream_t st) {
+  const int group = a.heads / a.kv_heads;
+  const int units = group % 2 == 0 ? a.heads / 2 : a.heads;
+  const int rows = group % 2 == 0 ? kAttnTile : 2 * kAttnTile;
+  const int64_t most = attn_max_tiles(a.n, a.cu ? a.n_seqs : 1, rows) * units;
+  cudaError_t e = cudaFuncSetAttribute(window_forward_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)FwdSmem<DP>::BYTES);
+  if (e != cudaSuccess) return e;
+  return op_launch(window_forward_kernel<DP>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads),
+                   FwdSmem<DP>::BYTES, st, 1, a, q, k, v, out, lse, err, units);
 }
 
 // ---- host ----
-ma_status check_rows(const char* what, const void* p, int64_t ts, int64_t hs) {
+__device__ int g_attn_error;  // first error code of a bounded wait that ran out
+
+cudaError_t error_word(int** p) {
+  void* v = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&v, g_attn_error);
+  *p = static_cast<int*>(v);
+  return e;
+}
+
+ma_status check_rows(const char* what, const void* p, int64_t dim, int64_t tokens, int64_t heads, int64_t ts,
+                     int64_t hs) {
   if (!p) return op_fail(MA_ERR_ARG, "%s must not be NULL", what);
   if (!op_aligned(p, 16) || ts % 8 != 0 || hs % 8 != 0)
     return op_fail(MA_ERR_ALIGN, "%s: the pointer and the token and head strides must keep 16-byte alignment", what);
+  if ((tokens > 1 && ts < dim) || (heads > 1 && hs < dim))
+    return op_fail(MA_ERR_SHAPE, "%s: a token or head stride below head_dim", what);
   return MA_OK;
 }
 
 ma_status check_attn(const ma_window_attention* d) {
   if (!d) return op_fail(MA_ERR_ARG, "the description must not be NULL");
   if (d->n_tokens < 0 || d->n_tokens > (int64_t)1 << 30) return op_fail(MA_ERR_SHAPE, "n_tokens outside [0, 2^30]");
-  if (d->n_heads < 1 || d->n_kv_heads < 1 || d->n_heads > 32768 || d->n_heads % d->n_kv_heads)
-    return op_fail(MA_ERR_SHAPE, "%d query heads over %d key heads: no whole number of queries for each", d->n_heads,
-                   d->n_kv_heads);
-  if (d->head_dim < 8 || d->head_dim > kMaxDim || d->head_dim % 8)
-    return op_fail(MA_ERR_SHAPE, "head_dim %d is no multiple of 8 in [8, %d]", d->head_dim, kMaxDim);
+  if (d->n_heads < 1 || d->n_kv_heads < 1 || d->n_heads > 1024 || d->n_heads % d->n_kv_heads)
+    return op_fail(MA_ERR_SHAPE, "%d query heads over %d key heads: no whole number of queries for each, or over 1024",
+                   d->n_heads, d->n_kv_heads);
+  if (d->head_dim < 8 || d->head_dim > 128 || d->head_dim % 8)
+    return op_fail(MA_ERR_SHAPE, "head_dim %d is no multiple of 8 in [8, 128]", d->head_dim);
   if (d->window < 0) return op_fail(MA_ERR_ARG, "window must not be negative");
-  if (d->sinks < 0 || d->sinks > 128) return op_fail(MA_ERR_ARG, "sinks outside [0, 128]");
-  if (!(d->scale - d->scale == 0.0)) return op_fail(MA_ERR_ARG, "scale must be finite");
+  if (d->sinks < 0 || d->sinks > kAttnTile) return op_fail(MA_ERR_ARG, "sinks outside [0, %d]", kAttnTile);
+  if (!(d->scale > 0.0) || !(d->scale - d->scale == 0.0)) return op_fail(MA_ERR_ARG, "scale must be finite and positive");
   if (d->n_seqs < 0 || (d->cu_seqlens && d->n_seqs < 1)) return op_fail(MA_ERR_ARG, "cu_seqlens needs n_seqs >= 1");
   if (!op_aligned(d->cu_seqlens, 4)) return op_fail(MA_ERR_ALIGN, "cu_seqlens is not aligned to 4 bytes");
+  if (((d->cu_seqlens ? d->n_seqs : 0) + d->n_tokens / kAttnTile + 2) * d->n_heads >= (int64_t)1 << 31)
+    return op_fail(MA_ERR_SHAPE, "too many tokens, samples and heads");
   if (d->n_tokens == 0) return MA_OK;
-  ma_status st = check_rows("q", d->q, d->q_token_stride, d->q_head_stride);
-  if (st == MA_OK) st = check_rows("k", d->k, d->k_token_stride, d->k_head_stride);
-  if (st == MA_OK) st = check_rows("v", d->v, d->v_token_stride, d->v_head_stride);
+  ma_status st = check_rows("q", d->q, d->head_dim, d->n_tokens, d->n_heads, d->q_token_stride, d->q_head_stride);
+  if (st == MA_OK)
+    st = check_rows("k", d->k, d->head_dim, d->n_tokens, d->n_kv_heads, d->k_token_stride, d->k_head_stride);
+  if (st == MA_OK)
+    st = check_rows("v", d->v, d->head_dim, d->n_tokens, d->n_kv_heads, d->v_token_stride, d->v_head_stride);
   return st;
 }
 
@@ -190,26 +412,72 @@ AttnArgs args_of(const ma_window_attention* d) {
   a.dim = d->head_dim;
   a.sinks = d->sinks;
   a.window = (int)(d->window < d->n_tokens ? d->window : d->n_tokens);
-  a.n_seqs = d->n_seqs;
+  a.n_seqs = d->cu_seqlens ? d->n_seqs : 1;
   a.scale = (float)d->scale;
+  a.scale_log2 = (float)(d->scale * 1.4426950408889634);
   a.cu = d->cu_seqlens;
-  a.q = static_cast<const __nv_bfloat16*>(d->q);
-  a.k = static_cast<const __nv_bfloat16*>(d->k);
-  a.v = static_cast<const __nv_bfloat16*>(d->v);
-  a.q_ts = d->q_token_stride;
-  a.q_hs = d->q_head_stride;
-  a.k_ts = d->k_token_stride;
-  a.k_hs = d->k_head_stride;
-  a.v_ts = d->v_token_stride;
-  a.v_hs = d->v_head_stride;
   return a;
 }
 
-int64_t workspace_bytes_of(const ma_window_attention* d) {
-  return ((int64_t)d->n_heads * d->n_tokens * 4 + 255) / 256 * 256 + 256;
+struct Maps {
+  CUtensorMap q, k, v, dout;
+};
+
+bool maps_of(const ma_window_attention* d, Maps* m) {
+  return attn_map(&m->q, d->q, d->head_dim, d->n_tokens, d->n_heads, d->q_token_stride, d->q_head_stride) &&
+         attn_map(&m->k, d->k, d->head_dim, d->n_tokens, d->n_kv_heads, d->k_token_stride, d->k_head_stride) &&
+         attn_map(&m->v, d->v, d->head_dim, d->n_tokens, d->n_kv_heads, d->v_token_stride, d->v_head_stride);
+}
+
+// Workspace of the gradient: lse2 and delta [head][token], then the partial
+// sums of the sink keys, one slot for each sample and each chunk.
+struct GradSpace {
+  int64_t stats, slots, slot_bytes, bytes;
+};
+GradSpace grad_space(const ma_window_attention* d) {
+  GradSpace g;
+  const int64_t seqs = d->cu_seqlens ? d->n_seqs : 1;
+  g.stats = ((int64_t)d->n_heads * d->n_tokens * 4 + 255) / 256 * 256;
+  g.slots = d->sinks > 0 ? 2 * seqs + attn_max_tiles(d->n_tokens, seqs, kAttnTile) / kSinkChunk + 1 : 0;
+  g.slot_bytes = (int64_t)d->n_kv_heads * 2 * d->sinks * d->head_dim * 4;
+  g.bytes = 2 * g.stats + g.slots * g.slot_bytes + 256;
+  return g;
 }
 
 }  // namespace
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+bool attn_map(CUtensorMap* tm, const void* base, int dim, int64_t tokens, int64_t heads, int64_t token_stride,
+              int64_t head_stride) {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  if (!fn) return false;
+  // the stride of a single token or head is never used, but has to be a legal one
+  if (tokens <= 1) token_stride = dim;
+  if (heads <= 1) head_stride = dim;
+  const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)tokens, (cuuint64_t)heads};
+  const cuuint64_t strides[2] = {(cuuint64_t)token_stride * 2, (cuuint64_t)head_stride * 2};
+  const cuuint32_t box[3] = {64, kAttnTile, 1}, estr[3] = {1, 1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t attn_forward(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                         __nv_bfloat16* out, float* lse, int* err, int sms, cudaStream_t st) {
+  return a.dim > 64 ? run_forward<128>(a, q, k, v, out, lse, err, sms, st)
+                    : run_forward<64>(a, q, k, v, out, lse, err, sms, st);
+}
+
 }  // namespace ma
 
 using namespace ma;
@@ -220,13 +488,18 @@ ma_status muon_adamw_window_attention(const ma_window_attention* d, void* out, f
   ma_status st = check_attn(d);
   if (st != MA_OK) return st;
   if (d->n_tokens > 0) {
-    st = check_rows("out", out, 0, 0);
+    st = check_rows("out", out, 0, 1, 1, 0, 0);
     if (st != MA_OK) return st;
     if (!lse) return op_fail(MA_ERR_ARG, "lse must not be NULL");
     if (!op_aligned(lse, 4)) return op_fail(MA_ERR_ALIGN, "lse is not aligned to 4 bytes");
-    AttnArgs a = args_of(d);
-    cudaError_t e = op_launch(window_forward_kernel, dim3((a.n + kWarps - 1) / kWarps, a.heads), dim3(kWarps * 32), 0,
-                              static_cast<cudaStream_t>(cuda_stream), 1, a, static_cast<__nv_bfloat16*>(out), lse);
+    int sms = 0, *err = nullptr;
+    cudaError_t e = op_num_sms(&sms);
+    if (e == cudaSuccess) e = error_word(&err);
+    if (e != cudaSuccess) return op_cuda(e, "device query");
+    Maps m;
+    if (!maps_of(d, &m)) return op_fail(MA_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor");
+    e = attn_forward(args_of(d), m.q, m.k, m.v, static_cast<__nv_bfloat16*>(out), lse, err, sms,
+                     static_cast<cudaStream_t>(cuda_stream));
     if (e != cudaSuccess) return op_cuda(e, "attention launch");
   }
   clear_last_error();
@@ -237,7 +510,7 @@ ma_status muon_adamw_window_attention_backward_workspace(const ma_window_attenti
   if (!bytes) return op_fail(MA_ERR_ARG, "bytes must not be NULL");
   ma_status st = check_attn(d);
   if (st != MA_OK) return st;
-  *bytes = workspace_bytes_of(d);
+  *bytes = grad_space(d).bytes;
   clear_last_error();
   return MA_OK;
 }
@@ -249,35 +522,59 @@ ma_status muon_adamw_window_attention_backward(const ma_window_attention* d, con
   ma_status st = check_attn(d);
   if (st != MA_OK) return st;
   if (d->n_tokens > 0) {
-    st = check_rows("dout", dout, dout_token_stride, dout_head_stride);
-    if (st == MA_OK) st = check_rows("out", out, 0, 0);
-    if (st == MA_OK) st = check_rows("dq", dq, 0, 0);
-    if (st == MA_OK) st = check_rows("dk", dk, 0, 0);
-    if (st == MA_OK) st = check_rows("dv", dv, 0, 0);
+    st = check_rows("dout", dout, d->head_dim, d->n_tokens, d->n_heads, dout_token_stride, dout_head_stride);
+    if (st == MA_OK) st = check_rows("out", out, 0, 1, 1, 0, 0);
+    if (st == MA_OK) st = check_rows("dq", dq, 0, 1, 1, 0, 0);
+    if (st == MA_OK) st = check_rows("dk", dk, 0, 1, 1, 0, 0);
+    if (st == MA_OK) st = check_rows("dv", dv, 0, 1, 1, 0, 0);
     if (st != MA_OK) return st;
     if (!lse || !op_aligned(lse, 4)) return op_fail(lse ? MA_ERR_ALIGN : MA_ERR_ARG, "lse is NULL or not aligned to 4 bytes");
     if (!workspace || !op_aligned(workspace, 256))
       return op_fail(workspace ? MA_ERR_ALIGN : MA_ERR_ARG, "workspace is NULL or not 256-byte aligned");
-    const int64_t need = workspace_bytes_of(d);
-    if (workspace_bytes < need)
-      return op_fail(MA_ERR_ARG, "workspace of %lld bytes, %lld are needed", (long long)workspace_bytes, (long long)need);
-    AttnArgs a = args_of(d);
-    GradArgs r{};
-    r.dout = static_cast<const __nv_bfloat16*>(dout);
-    r.out = static_cast<const __nv_bfloat16*>(out);
-    r.do_ts = dout_token_stride;
-    r.do_hs = dout_head_stride;
-    r.lse = lse;
-    r.delta = static_cast<float*>(workspace);
-    r.dq = static_cast<__nv_bfloat16*>(dq);
-    r.dk = static_cast<__nv_bfloat16*>(dk);
-    r.dv = static_cast<__nv_bfloat16*>(dv);
-    cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-    const unsigned blocks = (a.n + kWarps - 1) / kWarps;
-    cudaError_t e = op_launch(window_dq_kernel, dim3(blocks, a.heads), dim3(kWarps * 32), 0, s, 1, a, r);
-    if (e == cudaSuccess) e = op_launch(window_dkv_kernel, dim3(blocks, a.kv_heads), dim3(kWarps * 32), 0, s, 1, a, r);
+    const GradSpace sp = grad_space(d);
+    if (workspace_bytes < sp.bytes)
+      return op_fail(MA_ERR_ARG, "workspace of %lld bytes, %lld are needed", (long long)workspace_bytes,
+                     (long long)sp.bytes);
+    int sms = 0, *err = nullptr;
+    cudaError_t e = op_num_sms(&sms);
+    if (e == cudaSuccess) e = error_word(&err);
+    if (e != cudaSuccess) return op_cuda(e, "device query");
+    Maps m;
+    if (!maps_of(d, &m) || !attn_map(&m.dout, dout, d->head_dim, d->n_tokens, d->n_heads, dout_token_stride, dout_head_stride))
+      return op_fail(MA_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor");
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    AttnGrad g{};
+    g.dout = static_cast<const __nv_bfloat16*>(dout);
+    g.out = static_cast<const __nv_bfloat16*>(out);
+    g.do_ts = dout_token_stride;
+    g.do_hs = dout_head_stride;
+    g.lse = lse;
+    g.lse2 = reinterpret_cast<float*>(ws);
+    g.delta = reinterpret_cast<float*>(ws + sp.stats);
+    g.partial = reinterpret_cast<float*>(ws + 2 * sp.stats);
+    g.partial_slots = sp.slots;
+    g.dq = static_cast<__nv_bfloat16*>(dq);
+    g.dk = static_cast<__nv_bfloat16*>(dk);
+    g.dv = static_cast<__nv_bfloat16*>(dv);
+    e = attn_backward(args_of(d), m.q, m.k, m.v, m.dout, g, err, sms, static_cast<cudaStream_t>(cuda_stream));
     if (e != cudaSuccess) return op_cuda(e, "attention gradient launch");
   }
+  clear_last_error();
+  return MA_OK;
+}
+
+ma_status muon_adamw_window_attention_check(void* cuda_stream) {
+  int *p = nullptr, code = 0;
+  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  cudaError_t e = error_word(&p);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&code, p, sizeof code, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && code != 0) {
+    e = cudaMemsetAsync(p, 0, sizeof code, s);
+    if (e == cudaSuccess)
+      return op_fail(MA_ERR_DEVICE_CHECK, "a kernel's bounded wait ran out (code 0x%x); its results are not valid", code);
+  }
+  if (e != cudaSuccess) return op_cuda(e, "attention check");
   clear_last_error();
   return MA_OK;
 }

@@ -189,11 +189,17 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, cos, sin, po
 
 # ---- attention ----
 
+def _apart(name: str, t, dim: Optional[int] = None):
+    """``_heads``, with no two heads on the same elements (as in an expanded tensor)."""
+    t = _heads(name, t, dim)
+    return t.contiguous() if any(t.shape[i] > 1 and t.stride(i) < t.shape[2] for i in (0, 1)) else t
+
+
 def _attention(q, k, v, window, sinks, scale, cu_seqlens):
     dev = _on_gpu(q, k=k, v=v, cu_seqlens=cu_seqlens)
-    q = _heads("q", q)
+    q = _apart("q", q)
     n, h, dim = q.shape
-    k, v = _heads("k", k, dim), _heads("v", v, dim)
+    k, v = _apart("k", k, dim), _apart("v", v, dim)
     if k.shape[0] != n or v.shape != k.shape:
         raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit together")
     if q.dtype != torch.bfloat16 or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
@@ -235,7 +241,7 @@ def window_attention_backward(dout, q, k, v, out, lse, *, window: Optional[int],
         raise ValueError("dout and out must have the shape and the type of q")
     if lse.shape != (q.shape[1], q.shape[0]) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 [head, token]")
-    dout = _heads("dout", dout)
+    dout = _apart("dout", dout)
     out = out if out.is_contiguous() else out.contiguous()
     lib = load_library()
     ws, n = _scratch(dev, lib.muon_adamw_window_attention_backward_workspace, d)
@@ -245,6 +251,12 @@ def window_attention_backward(dout, q, k, v, out, lse, *, window: Optional[int],
     _call(dev, lib.muon_adamw_window_attention_backward, d, dout.data_ptr(), *_strides(dout),
           out.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), n)
     return dq, dk, dv
+
+
+def check() -> None:
+    """Wait for the current stream; raises if a bounded wait of an attention
+    kernel has run out (a fault of the machine or of the library)."""
+    _check(load_library().muon_adamw_window_attention_check(torch.cuda.current_stream().cuda_stream))
 
 
 # ---- forms for autograd ----
