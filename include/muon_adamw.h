@@ -582,10 +582,10 @@ MA_API ma_status muon_adamw_window_attention_backward(const ma_window_attention*
                                                       const void* out, const float* lse, void* dq, void* dk, void* dv,
                                                       void* workspace, int64_t workspace_bytes, void* cuda_stream);
 
-/* Wait for cuda_stream and read the attention kernels' error word.
+/* Wait for cuda_stream and read the operators' error word.
  * MA_ERR_DEVICE_CHECK if a bounded in-kernel wait of an earlier call on this
  * device ran out (the word is then cleared); MA_ERR_CUDA. */
-MA_API ma_status muon_adamw_window_attention_check(void* cuda_stream);
+MA_API ma_status muon_adamw_operators_check(void* cuda_stream);
 
 /* Message of the last error on this thread ("" if none). Never NULL. */
 MA_API const char* muon_adamw_last_error(void);

@@ -241,7 +241,7 @@ _SIGNATURES = {
     "muon_adamw_window_attention_backward": (ctypes.c_int, [ctypes.POINTER(WindowAttention), _P, ctypes.c_int64,
                                                             ctypes.c_int64, _P, _P, _P, _P, _P, _P, ctypes.c_int64,
                                                             _P]),
-    "muon_adamw_window_attention_check": (ctypes.c_int, [_P]),
+    "muon_adamw_operators_check": (ctypes.c_int, [_P]),
     "muon_adamw_last_error": (ctypes.c_char_p, []),
     "muon_adamw_version": (ctypes.c_char_p, []),
 }

@@ -478,8 +478,8 @@ ma_status muon_adamw_embedding_backward(const void* dout, int dout_dtype, int64_
     clear_last_error();
     return MA_OK;
   }
-  int sms = 0;
-  cudaError_t e = op_num_sms(&sms);
+  int sms = 0, *err = nullptr;
+  cudaError_t e = op_device(&sms, &err);
   if (e != cudaSuccess) return op_cuda(e, "device query");
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   SortArgs a{};
@@ -501,7 +501,7 @@ ma_status muon_adamw_embedding_backward(const void* dout, int dout_dtype, int64_
   int64_t fill_ctas = (fill + 64 * kSortThreads - 1) / (64 * kSortThreads);  // four 16-byte stores a thread at least
   if (fill_ctas > 2 * sms) fill_ctas = 2 * sms;
   const unsigned grid = (unsigned)(kSortCluster + (fill_ctas + kSortCluster - 1) / kSortCluster * kSortCluster);
-  e = cudaFuncSetAttribute(embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSortSmem);
+  e = op_smem_limit<embedding_sort_kernel>((int)kSortSmem);
   if (e != cudaSuccess) return op_cuda(e, "embedding sort attributes");
   e = op_launch(embedding_sort_kernel, dim3(grid), dim3(kSortThreads), kSortSmem, s, kSortCluster, a,
                 static_cast<uint8_t*>(grad), width * gsize, grad_stride * gsize, accumulate ? (int64_t)0 : vocab,

@@ -9,6 +9,8 @@
 #include <stdint.h>
 #include <stdio.h>
 
+#include <atomic>
+
 #include "internal.h"
 #include "muon_adamw.h"
 
@@ -32,11 +34,23 @@ inline bool op_dtype_ok(int dt) { return dt == MA_DT_F32 || dt == MA_DT_BF16; }
 inline int64_t op_dtype_size(int dt) { return dt == MA_DT_BF16 ? 2 : 4; }
 inline bool op_aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
 
-// SM count of the current device.
-inline cudaError_t op_num_sms(int* sms) {
+// SM count of the current device, and the address on it of the word that takes
+// the first error code of a bounded wait that ran out (operators.cu; looked up
+// once per device).
+cudaError_t op_device(int* sms, int** err);
+
+// Raise a kernel's dynamic shared memory limit, once per device.
+constexpr int kOpMaxDevices = 64;
+template <auto KERNEL>
+inline cudaError_t op_smem_limit(int bytes) {
+  static std::atomic<bool> done[kOpMaxDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < kOpMaxDevices;
+  if (known && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_release);
   return e;
 }
 

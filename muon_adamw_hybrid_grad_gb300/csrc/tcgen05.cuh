@@ -286,5 +286,13 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Bounded wait that does not give up when the CTA aborts: for copies and
+// products that must have ended before the CTA leaves.
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = global_timer();
+  while (!mbar_try_wait(bar, parity) && global_timer() - t0 < kWaitLimitNs) {
+  }
+}
+
 }  // namespace
 }  // namespace ma

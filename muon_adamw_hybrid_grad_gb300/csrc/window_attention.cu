@@ -353,23 +353,13 @@ cudaError_t run_forward(const AttnArgs& a, const CUtensorMap& q, const CUtensorM
   const int units = group % 2 == 0 ? a.heads / 2 : a.heads;
   const int rows = group % 2 == 0 ? kAttnTile : 2 * kAttnTile;
   const int64_t most = attn_max_tiles(a.n, a.cu ? a.n_seqs : 1, rows) * units;
-  cudaError_t e = cudaFuncSetAttribute(window_forward_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)FwdSmem<DP>::BYTES);
+  const cudaError_t e = op_smem_limit<window_forward_kernel<DP>>((int)FwdSmem<DP>::BYTES);
   if (e != cudaSuccess) return e;
   return op_launch(window_forward_kernel<DP>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads),
                    FwdSmem<DP>::BYTES, st, 1, a, q, k, v, out, lse, err, units);
 }
 
 // ---- host ----
-__device__ int g_attn_error;  // first error code of a bounded wait that ran out
-
-cudaError_t error_word(int** p) {
-  void* v = nullptr;
-  const cudaError_t e = cudaGetSymbolAddress(&v, g_attn_error);
-  *p = static_cast<int*>(v);
-  return e;
-}
-
 ma_status check_rows(const char* what, const void* p, int64_t dim, int64_t tokens, int64_t heads, int64_t ts,
                      int64_t hs) {
   if (!p) return op_fail(MA_ERR_ARG, "%s must not be NULL", what);
@@ -493,8 +483,7 @@ ma_status muon_adamw_window_attention(const ma_window_attention* d, void* out, f
     if (!lse) return op_fail(MA_ERR_ARG, "lse must not be NULL");
     if (!op_aligned(lse, 4)) return op_fail(MA_ERR_ALIGN, "lse is not aligned to 4 bytes");
     int sms = 0, *err = nullptr;
-    cudaError_t e = op_num_sms(&sms);
-    if (e == cudaSuccess) e = error_word(&err);
+    cudaError_t e = op_device(&sms, &err);
     if (e != cudaSuccess) return op_cuda(e, "device query");
     Maps m;
     if (!maps_of(d, &m)) return op_fail(MA_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor");
@@ -536,8 +525,7 @@ ma_status muon_adamw_window_attention_backward(const ma_window_attention* d, con
       return op_fail(MA_ERR_ARG, "workspace of %lld bytes, %lld are needed", (long long)workspace_bytes,
                      (long long)sp.bytes);
     int sms = 0, *err = nullptr;
-    cudaError_t e = op_num_sms(&sms);
-    if (e == cudaSuccess) e = error_word(&err);
+    cudaError_t e = op_device(&sms, &err);
     if (e != cudaSuccess) return op_cuda(e, "device query");
     Maps m;
     if (!maps_of(d, &m) || !attn_map(&m.dout, dout, d->head_dim, d->n_tokens, d->n_heads, dout_token_stride, dout_head_stride))
@@ -559,22 +547,6 @@ ma_status muon_adamw_window_attention_backward(const ma_window_attention* d, con
     e = attn_backward(args_of(d), m.q, m.k, m.v, m.dout, g, err, sms, static_cast<cudaStream_t>(cuda_stream));
     if (e != cudaSuccess) return op_cuda(e, "attention gradient launch");
   }
-  clear_last_error();
-  return MA_OK;
-}
-
-ma_status muon_adamw_window_attention_check(void* cuda_stream) {
-  int *p = nullptr, code = 0;
-  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  cudaError_t e = error_word(&p);
-  if (e == cudaSuccess) e = cudaMemcpyAsync(&code, p, sizeof code, cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e == cudaSuccess && code != 0) {
-    e = cudaMemsetAsync(p, 0, sizeof code, s);
-    if (e == cudaSuccess)
-      return op_fail(MA_ERR_DEVICE_CHECK, "a kernel's bounded wait ran out (code 0x%x); its results are not valid", code);
-  }
-  if (e != cudaSuccess) return op_cuda(e, "attention check");
   clear_last_error();
   return MA_OK;
 }

@@ -216,14 +216,6 @@ __device__ __forceinline__ void clear_rows(uint32_t tile, int rows, int lane) {
   __syncwarp();
 }
 
-// Bounded wait that does not give up when the CTA aborts: for copies and
-// products that must have ended before the CTA leaves.
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = global_timer();
-  while (!mbar_try_wait(bar, parity) && global_timer() - t0 < kWaitLimitNs) {
-  }
-}
-
 }  // namespace
 #endif
 

@@ -729,11 +729,8 @@ template <int DP>
 cudaError_t run_backward(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                          const CUtensorMap& dout, const AttnGrad& g, int* err, int sms, cudaStream_t st) {
   const int64_t tiles = attn_max_tiles(a.n, a.n_seqs, kAttnTile);
-  cudaError_t e = cudaFuncSetAttribute(window_dq_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)DqSmem<DP>::BYTES);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(window_dkv_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)DkvSmem<DP>::BYTES);
+  cudaError_t e = op_smem_limit<window_dq_kernel<DP>>((int)DqSmem<DP>::BYTES);
+  if (e == cudaSuccess) e = op_smem_limit<window_dkv_kernel<DP>>((int)DkvSmem<DP>::BYTES);
   if (e != cudaSuccess) return e;
   int64_t grid = tiles * a.heads;
   e = op_launch(window_dq_kernel<DP>, dim3((unsigned)(grid < sms ? grid : sms)), dim3(kThreads), DqSmem<DP>::BYTES, st,
