@@ -460,3 +460,41 @@ def test_autograd_forms(ops):
     dw = ops.embedding_backward(dx.view(n, h * d), ids, torch.empty_like(w), scale=2.0)
     for got, want in ((w.grad, dw), (k.grad, dk), (qw.grad, dqw), (kw.grad, dkw), (v.grad, dv)):
         assert torch.equal(got, want)
+
+
+def test_wrappers_refuse(ops):
+    """Wrong types, shapes and devices raise before anything is queued."""
+    import torch
+
+    from muon_adamw_hybrid_grad_gb300 import MuonAdamWError
+
+    w, ids = torch.zeros(4, 16, device="cuda"), torch.zeros(3, dtype=torch.int64, device="cuda")
+    x = torch.zeros(3, 2, 16, dtype=torch.bfloat16, device="cuda")
+    ones, table = torch.ones(16, device="cuda"), torch.ones(5, 8, device="cuda")
+    for error, call in (
+            (TypeError, lambda: ops.embedding(w, ids.float())), (TypeError, lambda: ops.embedding(w.half(), ids)),
+            (TypeError, lambda: ops.embedding(w, ids, dtype=torch.float16)), (TypeError, lambda: ops.embedding(w, 3)),
+            (ValueError, lambda: ops.embedding(w, ids.cpu())), (ValueError, lambda: ops.embedding(w.T, ids)),
+            (ValueError, lambda: ops.embedding(ones, ids)), (TypeError, lambda: ops.embedding(w, ids, scale="a")),
+            (MuonAdamWError, lambda: ops.embedding(w, ids, scale=float("nan"))),
+            (ValueError, lambda: ops.embedding_backward(torch.zeros(2, 16, device="cuda"), ids, w)),
+            (ValueError, lambda: ops.embedding_backward(torch.zeros(3, 8, device="cuda"), ids, w)),
+            (TypeError, lambda: ops.qk_norm_rope(x, x.float(), ones, ones, table, table, ids)),
+            (ValueError, lambda: ops.qk_norm_rope(x, x[:2], ones, ones, table, table, ids)),
+            (ValueError, lambda: ops.qk_norm_rope(x, x, ones[:8], ones, table, table, ids)),
+            (ValueError, lambda: ops.qk_norm_rope(x, x, ones, ones, table, table[:4], ids)),
+            (ValueError, lambda: ops.qk_norm_rope(x, x, ones, ones, table, table, ids[:2])),
+            (ValueError, lambda: ops.qk_norm_rope(x[0], x, ones, ones, table, table, ids)),
+            (MuonAdamWError, lambda: ops.qk_norm_rope(x, x, ones, ones, torch.ones(5, 7, device="cuda"),
+                                                      torch.ones(5, 7, device="cuda"), ids)),
+            (ValueError, lambda: ops.qk_norm_rope_backward(x, x.float(), x, x, ones, ones, table, table, ids)),
+            (TypeError, lambda: ops.window_attention(x.float(), x, x, window=1)),
+            (ValueError, lambda: ops.window_attention(x, x, x[:2], window=1)),
+            (ValueError, lambda: ops.window_attention(x, x, x, window=1, cu_seqlens=ids)),
+            (MuonAdamWError, lambda: ops.window_attention(x, x, x, window=-1)),
+            (MuonAdamWError, lambda: ops.window_attention(x, x, x, window=1, sinks=200)),
+            (MuonAdamWError, lambda: ops.window_attention(x, x, x, window=1, scale=-1.0)),
+            (ValueError, lambda: ops.window_attention_backward(x, x, x, x, x, w, window=1))):
+        with pytest.raises(error):
+            call()
+    ops.check()
