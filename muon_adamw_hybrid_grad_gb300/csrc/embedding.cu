@@ -3,9 +3,12 @@
 //   out[t]  = scale * weight[ids[t]]                    (zero where ids[t] is no row)
 //   grad[v] = scale * sum over {t : ids[t] = v} dout[t]  (+ grad[v] when accumulating)
 //
-// The gradient is deterministic: tokens are brought into the order (id,
-// position) by a stable radix sort and each id's rows are added in that order
-// in fp32, whatever the launch shape of other work on the GPU.
+// The gradient is deterministic: each id's rows are added in the order of their
+// positions (within groups of fixed size) in fp32. Two ways lead there:
+//   - up to kDirectTokens tokens, one launch: every block owns some rows of the
+//     gradient, picks their tokens out of all ids and writes each row once;
+//   - more tokens: a stable radix sort brings the tokens into the order
+//     (id, position), then runs of equal ids are added up.
 #include <limits.h>
 
 #include "op_common.cuh"
@@ -38,19 +41,140 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const W* __restrict
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) id[r] = t0 + r < n ? read_id(ids, wide != 0, t0 + r, vocab) : vocab;
   for (int c = (int)(threadIdx.x + blockDim.x * blockIdx.y) * VEC; c < width; c += (int)(blockDim.x * gridDim.y) * VEC) {
-    float x[ROWS][VEC];
+    RawVec<W, VEC> raw[ROWS];
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) x[r][i] = 0.f;
-      if (id[r] < vocab) load_vec<VEC>(weight + (int64_t)id[r] * wstride + c, x[r]);
-    }
+    for (int r = 0; r < ROWS; ++r)
+      if (id[r] < vocab) raw[r].load(weight + (int64_t)id[r] * wstride + c);
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       if (t0 + r >= n) break;
+      float x[VEC];
+      raw[r].get(x);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) x[r][i] = id[r] < vocab ? x[r][i] * scale : 0.f;
-      store_vec<VEC>(out + (t0 + r) * ostride + c, x[r]);
+      for (int i = 0; i < VEC; ++i) x[i] = id[r] < vocab ? x[i] * scale : 0.f;
+      store_vec<VEC>(out + (t0 + r) * ostride + c, x);
+    }
+  }
+}
+
+// ---- gradient of few tokens: one launch ----
+// Block b owns rows b, b + B, b + 2 B, ... (neighbouring ids are of like
+// frequency in most vocabularies, so consecutive rows would load the first
+// blocks with all the frequent ones). Its warps read all ids, each a contiguous
+// part, and keep the tokens of the block's rows in order; then every row is
+// written once: zeros, or the sum over its tokens by the warps, a warp to 32 VEC
+// columns, eight rows of dout in flight.
+constexpr int kDirectTokens = 4096;
+constexpr int kDirectRows = 4096;  // rows of a block, at most: bits of its presence map
+constexpr int kDirectWarps = kThreads / 32;
+
+struct DirectArgs {
+  const void* ids;
+  int wide, n;
+  uint32_t vocab;
+  int width;
+  float scale;
+  int accumulate;
+  int64_t dstride, gstride;
+};
+
+template <typename D, typename G, int VEC>
+__global__ void __launch_bounds__(kThreads) embedding_direct_kernel(const __grid_constant__ DirectArgs a,
+                                                                    const D* __restrict__ dout, G* __restrict__ grad) {
+  extern __shared__ uint32_t list[];  // [warp][per]: row of the block << 12 | position
+  __shared__ uint32_t present[kDirectRows / 32];
+  __shared__ int count[kDirectWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t B = gridDim.x, b = blockIdx.x;
+  const int rows = (int)((a.vocab - b + B - 1) / B);
+  const int per = ((a.n + kDirectWarps - 1) / kDirectWarps + 31) / 32 * 32;
+  for (int i = threadIdx.x; i < (rows + 31) / 32; i += kThreads) present[i] = 0;
+  __syncthreads();
+  pdl_launch();
+  pdl_wait();
+  {
+    uint32_t* mine = list + warp * per;
+    int found = 0;
+    const int t1 = min((warp + 1) * per, a.n);
+    for (int t0 = warp * per; t0 < t1; t0 += 32) {
+      const int t = t0 + lane;
+      const uint32_t id = t < t1 ? read_id(a.ids, a.wide != 0, t, a.vocab) : a.vocab;
+      const uint32_t r = id / B;
+      const bool hit = id < a.vocab && id - r * B == b;
+      const uint32_t hits = __ballot_sync(0xffffffffu, hit);
+      if (hit) {
+        mine[found + __popc(hits & ((1u << lane) - 1))] = r << 12 | (uint32_t)t;
+        atomicOr(present + (r >> 5), 1u << (r & 31));
+      }
+      found += __popc(hits);
+    }
+    if (lane == 0) count[warp] = found;
+  }
+  __syncthreads();
+  constexpr int COLS = 32 * VEC;
+  if (!a.accumulate) {
+    float zero[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) zero[i] = 0.f;
+    for (int r = warp; r < rows; r += kDirectWarps) {
+      if (present[r >> 5] >> (r & 31) & 1) continue;
+      G* p = grad + (int64_t)(b + (uint32_t)r * B) * a.gstride;
+      for (int c = lane * VEC; c < a.width; c += COLS) store_vec<VEC>(p + c, zero);
+    }
+  }
+  const int passes = (a.width + COLS - 1) / COLS;
+  int task = 0;
+  for (int w = 0; w < (rows + 31) / 32; ++w) {
+    for (uint32_t left = present[w]; left; left &= left - 1) {
+      const uint32_t r = w * 32 + __ffs(left) - 1;
+      for (int pass = 0; pass < passes; ++pass, ++task) {
+        if (task % kDirectWarps != warp) continue;
+        const int c = pass * COLS + lane * VEC;
+        const bool on = c < a.width;
+        float s[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s[i] = 0.f;
+        for (int q = 0; q < kDirectWarps; ++q) {
+          for (int e0 = 0; e0 < count[q]; e0 += 32) {
+            const uint32_t entry = e0 + lane < count[q] ? list[q * per + e0 + lane] : UINT_MAX;
+            uint32_t hits = __ballot_sync(0xffffffffu, (entry >> 12) == r && e0 + lane < count[q]);
+            while (hits) {
+              RawVec<D, VEC> raw[8];
+              int m = 0;
+#pragma unroll
+              for (int u = 0; u < 8; ++u) {
+                if (hits) {
+                  const int t = (int)(__shfl_sync(0xffffffffu, entry, __ffs(hits) - 1) & 4095u);
+                  hits &= hits - 1;
+                  if (on) raw[u].load(dout + (int64_t)t * a.dstride + c);
+                  ++m;
+                }
+              }
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                if (u < m) {
+                  float x[VEC];
+                  raw[u].get(x);
+#pragma unroll
+                  for (int i = 0; i < VEC; ++i) s[i] += x[i];
+                }
+            }
+          }
+        }
+        if (on) {
+          G* p = grad + (int64_t)(b + r * B) * a.gstride + c;
+          float y[VEC];
+          if (a.accumulate) {
+            load_vec<VEC>(p, y);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) y[i] = fmaf(s[i], a.scale, y[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) y[i] = s[i] * a.scale;
+          }
+          store_vec<VEC>(p, y);
+        }
+      }
     }
   }
 }
@@ -265,7 +389,7 @@ __device__ __forceinline__ void write_grad(G* grad, const SumArgs& a, uint32_t k
 template <typename D, typename G, int VEC>
 __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_constant__ SumArgs a,
                                                                  const D* __restrict__ dout, G* __restrict__ grad) {
-  constexpr int AHEAD = 4;
+  constexpr int AHEAD = 8;
   pdl_launch();
   pdl_wait();
   const int64_t chunk = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -281,12 +405,12 @@ __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_co
     uint32_t cur = a.key[t0];
     bool came_in = cur == before;
     for (int64_t t = t0; t < t1 && cur < a.vocab; t += AHEAD) {
-      float x[AHEAD][VEC];
+      RawVec<D, VEC> raw[AHEAD];
       uint32_t key[AHEAD];
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u) {
         key[u] = t + u < t1 ? a.key[t + u] : a.vocab;
-        if (key[u] < a.vocab) load_vec<VEC>(dout + (int64_t)a.pos[t + u] * a.dstride + c, x[u]);
+        if (key[u] < a.vocab) raw[u].load(dout + (int64_t)a.pos[t + u] * a.dstride + c);
       }
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u) {
@@ -302,8 +426,10 @@ __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_co
 #pragma unroll
           for (int i = 0; i < VEC; ++i) s[i] = 0.f;
         }
+        float x[VEC];
+        raw[u].get(x);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) s[i] += x[u][i];
+        for (int i = 0; i < VEC; ++i) s[i] += x[i];
       }
     }
     if (cur < a.vocab) {
@@ -317,29 +443,57 @@ __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_co
   }
 }
 
-// Joins the runs that reach over a border, at the chunk where they start.
+// Joins the runs that reach over a border, at the chunk where they start: 32
+// threads to 32 VEC columns, eight walkers that take every eighth partial sum of
+// the run, four of them in flight, and are added in their order.
 template <typename G, int VEC>
 __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_constant__ SumArgs a,
                                                                   G* __restrict__ grad) {
+  constexpr int WALKERS = kThreads / 32;
+  __shared__ float sums[WALKERS][32][VEC + 1];
   pdl_launch();
   pdl_wait();
-  const int64_t chunk = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t chunk = blockIdx.x;
   const int64_t t0 = chunk * a.per, t1 = t0 + a.per;
-  const int c = (int)(threadIdx.x + blockDim.x * blockIdx.y) * VEC;
-  if (t1 < a.n && c < a.width) {
-    const uint32_t cur = a.key[t1 - 1];
-    const bool starts_here = t0 == 0 || a.key[t0 - 1] != cur || a.key[t0] != cur;
-    if (cur < a.vocab && a.key[t1] == cur && starts_here) {
-      float s[VEC];
-      load_vec<VEC>(a.partial + (chunk * 2 + 1) * a.width + c, s);
-      for (int64_t k = chunk + 1; k * a.per < a.n && a.key[k * a.per] == cur; ++k) {
-        float y[VEC];
-        load_vec<VEC>(a.partial + k * 2 * a.width + c, y);
+  const int lane = threadIdx.x & 31, walker = threadIdx.x >> 5;
+  const int c = (int)(lane + 32 * blockIdx.y) * VEC;
+  if (t1 >= a.n) return;
+  const uint32_t cur = a.key[t1 - 1];
+  // the run has to go on, and to start in this chunk
+  if (cur >= a.vocab || a.key[t1] != cur || (t0 > 0 && a.key[t0 - 1] == cur && a.key[t0] == cur)) return;
+  float s[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) s[i] += y[i];
+  for (int i = 0; i < VEC; ++i) s[i] = 0.f;
+  if (c < a.width) {
+    if (walker == 0) load_vec<VEC>(a.partial + (chunk * 2 + 1) * a.width + c, s);
+    bool more = true;
+    for (int64_t k = chunk + 1 + walker; more; k += 4 * WALKERS) {
+      float y[4][VEC];
+      bool on[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t ku = k + u * WALKERS;
+        on[u] = ku * a.per < a.n && a.key[ku * a.per] == cur;
+        if (on[u]) load_vec<VEC>(a.partial + ku * 2 * a.width + c, y[u]);
       }
-      write_grad<VEC>(grad, a, cur, c, s);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (on[u]) {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) s[i] += y[u][i];
+        }
+      more = on[3];
     }
+  }
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) sums[walker][lane][i] = s[i];
+  __syncthreads();
+  if (walker == 0 && c < a.width) {
+#pragma unroll
+    for (int w = 1; w < WALKERS; ++w)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) s[i] += sums[w][lane][i];
+    write_grad<VEC>(grad, a, cur, c, s);
   }
 }
 
@@ -410,7 +564,30 @@ cudaError_t run_sums(const SumArgs& a, int64_t chunks, const void* dout, void* g
   cudaError_t e = op_launch(embedding_sum_kernel<D, G, VEC>, g, b, 0, st, 1, a, static_cast<const D*>(dout),
                             static_cast<G*>(grad));
   if (e != cudaSuccess || chunks < 2) return e;
-  return op_launch(embedding_join_kernel<G, VEC>, g, b, 0, st, 1, a, static_cast<G*>(grad));
+  return op_launch(embedding_join_kernel<G, VEC>,
+                   dim3((unsigned)(chunks - 1), (unsigned)((a.width + 32 * VEC - 1) / (32 * VEC))), dim3(kThreads), 0,
+                   st, 1, a, static_cast<G*>(grad));
+}
+
+// Blocks of the one-launch gradient: up to eight an SM.
+int64_t direct_blocks(int64_t vocab, int sms) { return vocab < 8 * sms ? vocab : 8 * (int64_t)sms; }
+
+template <typename D, typename G, int VEC>
+cudaError_t run_direct(const DirectArgs& a, int64_t blocks, const void* dout, void* grad, cudaStream_t st) {
+  const int per = ((a.n + kDirectWarps - 1) / kDirectWarps + 31) / 32 * 32;
+  return op_launch(embedding_direct_kernel<D, G, VEC>, dim3((unsigned)blocks), dim3(kThreads),
+                   (size_t)kDirectWarps * per * 4, st, 1, a, static_cast<const D*>(dout), static_cast<G*>(grad));
+}
+
+// f(dout type, gradient type, vector width) for the call's own.
+template <typename F>
+cudaError_t by_types(bool vec, int dout_dtype, int grad_dtype, F f) {
+  typedef __nv_bfloat16 B;
+  const bool db = dout_dtype == MA_DT_BF16, gb = grad_dtype == MA_DT_BF16;
+  const std::integral_constant<int, 8> v;
+  const std::integral_constant<int, 1> o;
+  if (vec) return db ? (gb ? f(B(), B(), v) : f(B(), 0.f, v)) : (gb ? f(0.f, B(), v) : f(0.f, 0.f, v));
+  return db ? (gb ? f(B(), B(), o) : f(B(), 0.f, o)) : (gb ? f(0.f, B(), o) : f(0.f, 0.f, o));
 }
 
 }  // namespace
@@ -482,6 +659,26 @@ ma_status muon_adamw_embedding_backward(const void* dout, int dout_dtype, int64_
   cudaError_t e = op_device(&sms, &err);
   if (e != cudaSuccess) return op_cuda(e, "device query");
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  const bool vec = rows_vec(dout, dout_dtype, dout_stride, width) && rows_vec(grad, grad_dtype, grad_stride, width);
+  const int64_t blocks = direct_blocks(vocab, sms);
+  if (n_tokens <= kDirectTokens && (vocab + blocks - 1) / blocks <= kDirectRows) {
+    DirectArgs d{};
+    d.ids = ids;
+    d.wide = id_bytes == 8;
+    d.n = (int)n_tokens;
+    d.vocab = (uint32_t)vocab;
+    d.width = (int)width;
+    d.scale = (float)scale;
+    d.accumulate = accumulate;
+    d.dstride = dout_stride;
+    d.gstride = grad_stride;
+    e = by_types(vec, dout_dtype, grad_dtype, [&](auto x, auto y, auto v) {
+      return run_direct<decltype(x), decltype(y), v.value>(d, blocks, dout, grad, s);
+    });
+    if (e != cudaSuccess) return op_cuda(e, "embedding gradient launch");
+    clear_last_error();
+    return MA_OK;
+  }
   SortArgs a{};
   a.ids = ids;
   a.wide = id_bytes == 8;
@@ -520,17 +717,9 @@ ma_status muon_adamw_embedding_backward(const void* dout, int dout_dtype, int64_
     u.dstride = dout_stride;
     u.gstride = grad_stride;
     u.partial = reinterpret_cast<float*>(ws + 4 * p.key_bytes);
-    const bool vec = rows_vec(dout, dout_dtype, dout_stride, width) && rows_vec(grad, grad_dtype, grad_stride, width);
-    const bool db = dout_dtype == MA_DT_BF16, gb = grad_dtype == MA_DT_BF16;
-    typedef __nv_bfloat16 B;
-    if (vec)
-      e = db ? (gb ? run_sums<B, B, 8>(u, p.chunks, dout, grad, s) : run_sums<B, float, 8>(u, p.chunks, dout, grad, s))
-             : (gb ? run_sums<float, B, 8>(u, p.chunks, dout, grad, s)
-                   : run_sums<float, float, 8>(u, p.chunks, dout, grad, s));
-    else
-      e = db ? (gb ? run_sums<B, B, 1>(u, p.chunks, dout, grad, s) : run_sums<B, float, 1>(u, p.chunks, dout, grad, s))
-             : (gb ? run_sums<float, B, 1>(u, p.chunks, dout, grad, s)
-                   : run_sums<float, float, 1>(u, p.chunks, dout, grad, s));
+    e = by_types(vec, dout_dtype, grad_dtype, [&](auto x, auto y, auto v) {
+      return run_sums<decltype(x), decltype(y), v.value>(u, p.chunks, dout, grad, s);
+    });
     if (e != cudaSuccess) return op_cuda(e, "embedding sum launch");
   }
   clear_last_error();

@@ -98,14 +98,22 @@ def test_embedding_backward(ops, tokens, vocab, width, dt, gt, accumulate):
     within(got, want, (count + 4) * O.U32 * mag, gt)
 
 
+@pytest.mark.parametrize("tokens,vocab,width", [(4500, 40, 264), (4099, 6000, 77), (9000, 3, 16), (4321, 30000, 2056)])
+@pytest.mark.parametrize("dt,gt", [("bf16", "bf16"), ("fp32", "bf16"), ("bf16", "fp32")])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embedding_backward_of_many_tokens(ops, tokens, vocab, width, dt, gt, accumulate):
+    """Past the one-launch form: sorted tokens, runs within and over the groups."""
+    test_embedding_backward(ops, tokens, vocab, width, dt, gt, accumulate)
+
+
+@pytest.mark.parametrize("n", [777, 4096, 4097])
 @pytest.mark.parametrize("ids", ["one", "two", "none", "runs", "sorted", "reversed"])
 @pytest.mark.parametrize("vocab", [3, 513, 262145])
-def test_embedding_backward_orders(ops, ids, vocab):
+def test_embedding_backward_orders(ops, ids, vocab, n):
     """Heavy tokens, runs over many groups, and vocabularies of one to three digits."""
     import torch
 
     rng = np.random.default_rng(vocab)
-    n = 4097
     v = {"one": np.full(n, vocab - 1), "two": np.where(np.arange(n) % 2, 0, vocab - 1), "none": np.full(n, -1),
          "runs": np.repeat(rng.integers(0, vocab, n // 100 + 1), 100)[:n],
          "sorted": np.sort(rng.integers(0, vocab, n)), "reversed": np.sort(rng.integers(0, vocab, n))[::-1].copy()}[ids]
