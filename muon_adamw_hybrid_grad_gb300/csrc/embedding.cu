@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(kThreads) embedding_direct_kernel(const __grid
   extern __shared__ uint32_t list[];  // [warp][per]: row of the block << 12 | position
   __shared__ uint32_t present[kDirectRows / 32];
   __shared__ int count[kDirectWarps];
+  __shared__ float sums[kDirectWarps][32][VEC + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t B = gridDim.x, b = blockIdx.x;
   const int rows = (int)((a.vocab - b + B - 1) / B);
@@ -93,20 +94,28 @@ __global__ void __launch_bounds__(kThreads) embedding_direct_kernel(const __grid
   pdl_launch();
   pdl_wait();
   {
+    constexpr int AHEAD = 4;
     uint32_t* mine = list + warp * per;
     int found = 0;
     const int t1 = min((warp + 1) * per, a.n);
-    for (int t0 = warp * per; t0 < t1; t0 += 32) {
-      const int t = t0 + lane;
-      const uint32_t id = t < t1 ? read_id(a.ids, a.wide != 0, t, a.vocab) : a.vocab;
-      const uint32_t r = id / B;
-      const bool hit = id < a.vocab && id - r * B == b;
-      const uint32_t hits = __ballot_sync(0xffffffffu, hit);
-      if (hit) {
-        mine[found + __popc(hits & ((1u << lane) - 1))] = r << 12 | (uint32_t)t;
-        atomicOr(present + (r >> 5), 1u << (r & 31));
+    for (int t0 = warp * per; t0 < t1; t0 += 32 * AHEAD) {
+      uint32_t id[AHEAD];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int t = t0 + 32 * u + lane;
+        id[u] = t < t1 ? read_id(a.ids, a.wide != 0, t, a.vocab) : a.vocab;
       }
-      found += __popc(hits);
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const uint32_t r = id[u] / B;
+        const bool hit = id[u] < a.vocab && id[u] - r * B == b;
+        const uint32_t hits = __ballot_sync(0xffffffffu, hit);
+        if (hit) {
+          mine[found + __popc(hits & ((1u << lane) - 1))] = r << 12 | (uint32_t)(t0 + 32 * u + lane);
+          atomicOr(present + (r >> 5), 1u << (r & 31));
+        }
+        found += __popc(hits);
+      }
     }
     if (lane == 0) count[warp] = found;
   }
@@ -122,57 +131,80 @@ __global__ void __launch_bounds__(kThreads) embedding_direct_kernel(const __grid
       for (int c = lane * VEC; c < a.width; c += COLS) store_vec<VEC>(p + c, zero);
     }
   }
+  // s += the rows of the tokens of the block's row r in list q, in order
+  auto add_list = [&](float (&s)[VEC], uint32_t r, int q, int c) {
+    for (int e0 = 0; e0 < count[q]; e0 += 32) {
+      const uint32_t entry = e0 + lane < count[q] ? list[q * per + e0 + lane] : UINT_MAX;
+      uint32_t hits = __ballot_sync(0xffffffffu, (entry >> 12) == r && e0 + lane < count[q]);
+      while (hits) {
+        RawVec<D, VEC> raw[8];
+        int m = 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (hits) {
+            const int t = (int)(__shfl_sync(0xffffffffu, entry, __ffs(hits) - 1) & 4095u);
+            hits &= hits - 1;
+            if (c < a.width) raw[u].load(dout + (int64_t)t * a.dstride + c);
+            ++m;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (u < m) {
+            float x[VEC];
+            raw[u].get(x);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) s[i] += x[i];
+          }
+      }
+    }
+  };
+  auto write = [&](uint32_t r, int c, const float (&s)[VEC]) {
+    if (c >= a.width) return;
+    G* p = grad + (int64_t)(b + r * B) * a.gstride + c;
+    float y[VEC];
+    if (a.accumulate) {
+      load_vec<VEC>(p, y);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) y[i] = fmaf(s[i], a.scale, y[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) y[i] = s[i] * a.scale;
+    }
+    store_vec<VEC>(p, y);
+  };
+  // A task is 32 VEC columns of a row. With as many tasks as warps each warp
+  // takes its own; with fewer all warps share each, a list to a warp.
   const int passes = (a.width + COLS - 1) / COLS;
+  int tasks = 0;
+  for (int w = 0; w < (rows + 31) / 32; ++w) tasks += __popc(present[w]);
+  tasks *= passes;
+  const bool share = tasks < kDirectWarps;
   int task = 0;
   for (int w = 0; w < (rows + 31) / 32; ++w) {
     for (uint32_t left = present[w]; left; left &= left - 1) {
       const uint32_t r = w * 32 + __ffs(left) - 1;
       for (int pass = 0; pass < passes; ++pass, ++task) {
-        if (task % kDirectWarps != warp) continue;
         const int c = pass * COLS + lane * VEC;
-        const bool on = c < a.width;
         float s[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) s[i] = 0.f;
-        for (int q = 0; q < kDirectWarps; ++q) {
-          for (int e0 = 0; e0 < count[q]; e0 += 32) {
-            const uint32_t entry = e0 + lane < count[q] ? list[q * per + e0 + lane] : UINT_MAX;
-            uint32_t hits = __ballot_sync(0xffffffffu, (entry >> 12) == r && e0 + lane < count[q]);
-            while (hits) {
-              RawVec<D, VEC> raw[8];
-              int m = 0;
+        if (share) {
+          add_list(s, r, warp, c);
 #pragma unroll
-              for (int u = 0; u < 8; ++u) {
-                if (hits) {
-                  const int t = (int)(__shfl_sync(0xffffffffu, entry, __ffs(hits) - 1) & 4095u);
-                  hits &= hits - 1;
-                  if (on) raw[u].load(dout + (int64_t)t * a.dstride + c);
-                  ++m;
-                }
-              }
+          for (int i = 0; i < VEC; ++i) sums[warp][lane][i] = s[i];
+          __syncthreads();
+          if (warp == 0) {
 #pragma unroll
-              for (int u = 0; u < 8; ++u)
-                if (u < m) {
-                  float x[VEC];
-                  raw[u].get(x);
+            for (int q = 1; q < kDirectWarps; ++q)
 #pragma unroll
-                  for (int i = 0; i < VEC; ++i) s[i] += x[i];
-                }
-            }
+              for (int i = 0; i < VEC; ++i) s[i] += sums[q][lane][i];
+            write(r, c, s);
           }
-        }
-        if (on) {
-          G* p = grad + (int64_t)(b + r * B) * a.gstride + c;
-          float y[VEC];
-          if (a.accumulate) {
-            load_vec<VEC>(p, y);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) y[i] = fmaf(s[i], a.scale, y[i]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) y[i] = s[i] * a.scale;
-          }
-          store_vec<VEC>(p, y);
+          __syncthreads();
+        } else if (task % kDirectWarps == warp) {
+          for (int q = 0; q < kDirectWarps; ++q) add_list(s, r, q, c);
+          write(r, c, s);
         }
       }
     }
@@ -355,16 +387,18 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
   }
 }
 
-// Sums of dout over runs of equal ids. A chunk of `per` sorted tokens belongs
+// Sums of dout over runs of equal ids. A chunk of kChunkTokens sorted tokens belongs
 // to one row of threads; a run inside it is written to the gradient at once,
 // a run that reaches over a border leaves fp32 partial sums: slot 0 of a chunk
 // holds the run that came in from the chunk before, slot 1 the run that starts
 // here and goes on.
+constexpr int kChunkTokens = 16;
+
 struct SumArgs {
   const uint32_t *key, *pos;
   int64_t n;
   uint32_t vocab;
-  int width, per;
+  int width;
   float scale;
   int accumulate;
   int64_t dstride, gstride;
@@ -392,122 +426,140 @@ __global__ void __launch_bounds__(kThreads) embedding_sum_kernel(const __grid_co
   constexpr int AHEAD = 8;
   pdl_launch();
   pdl_wait();
+  const int lane = threadIdx.x & 31;
   const int64_t chunk = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const int64_t t0 = chunk * a.per, t1 = min(t0 + a.per, a.n);
+  const int64_t t0 = chunk * kChunkTokens;
+  if (t0 >= a.n) return;  // the same for a whole warp
+  const int m = (int)min((int64_t)kChunkTokens, a.n - t0);
+  // the chunk's ids and positions, a lane to a token, and the ids beside it
+  const uint32_t my_key = lane < m ? a.key[t0 + lane] : a.vocab, my_pos = lane < m ? a.pos[t0 + lane] : 0;
+  const uint32_t before = t0 > 0 ? a.key[t0 - 1] : UINT_MAX;
+  const uint32_t after = t0 + m < a.n ? a.key[t0 + m] : UINT_MAX;
   const int c = (int)(threadIdx.x + blockDim.x * blockIdx.y) * VEC;
-  if (t0 < a.n && c < a.width) {
-    const uint32_t before = t0 > 0 ? a.key[t0 - 1] : UINT_MAX;
-    const uint32_t after = t1 < a.n ? a.key[t1] : UINT_MAX;
-    float* part = a.partial + chunk * 2 * a.width + c;
-    float s[VEC];
+  float* part = a.partial + chunk * 2 * a.width + c;
+  float s[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) s[i] = 0.f;
-    uint32_t cur = a.key[t0];
-    bool came_in = cur == before;
-    for (int64_t t = t0; t < t1 && cur < a.vocab; t += AHEAD) {
-      RawVec<D, VEC> raw[AHEAD];
-      uint32_t key[AHEAD];
+  for (int i = 0; i < VEC; ++i) s[i] = 0.f;
+  uint32_t cur = __shfl_sync(0xffffffffu, my_key, 0);
+  bool came_in = cur == before;
+  for (int t = 0; t < m && cur < a.vocab; t += AHEAD) {
+    RawVec<D, VEC> raw[AHEAD];
+    uint32_t key[AHEAD];
 #pragma unroll
-      for (int u = 0; u < AHEAD; ++u) {
-        key[u] = t + u < t1 ? a.key[t + u] : a.vocab;
-        if (key[u] < a.vocab) raw[u].load(dout + (int64_t)a.pos[t + u] * a.dstride + c);
-      }
+    for (int u = 0; u < AHEAD; ++u) {
+      key[u] = __shfl_sync(0xffffffffu, my_key, t + u);
+      const uint32_t pos = __shfl_sync(0xffffffffu, my_pos, t + u);
+      if (key[u] < a.vocab && c < a.width) raw[u].load(dout + (int64_t)pos * a.dstride + c);
+    }
 #pragma unroll
-      for (int u = 0; u < AHEAD; ++u) {
-        if (t + u >= t1) break;
-        if (key[u] != cur) {
+    for (int u = 0; u < AHEAD; ++u) {
+      if (t + u >= m) break;
+      if (key[u] != cur) {
+        if (c < a.width) {
           if (came_in)
             store_vec<VEC>(part, s);
           else
             write_grad<VEC>(grad, a, cur, c, s);
-          came_in = false;
-          cur = key[u];
-          if (cur >= a.vocab) break;  // ids of no token are last
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) s[i] = 0.f;
         }
-        float x[VEC];
-        raw[u].get(x);
+        came_in = false;
+        cur = key[u];
+        if (cur >= a.vocab) break;  // ids of no token are last
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) s[i] += x[i];
+        for (int i = 0; i < VEC; ++i) s[i] = 0.f;
       }
+      float x[VEC];
+      raw[u].get(x);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) s[i] += x[i];
     }
-    if (cur < a.vocab) {
-      if (came_in)
-        store_vec<VEC>(part, s);
-      else if (cur == after)
-        store_vec<VEC>(part + a.width, s);
-      else
-        write_grad<VEC>(grad, a, cur, c, s);
-    }
+  }
+  if (cur < a.vocab && c < a.width) {
+    if (came_in)
+      store_vec<VEC>(part, s);
+    else if (cur == after)
+      store_vec<VEC>(part + a.width, s);
+    else
+      write_grad<VEC>(grad, a, cur, c, s);
   }
 }
 
-// Joins the runs that reach over a border, at the chunk where they start: 32
-// threads to 32 VEC columns, eight walkers that take every eighth partial sum of
-// the run, four of them in flight, and are added in their order.
+constexpr int kJoinChunks = 8;  // chunks of a block
+
+// Joins the runs that reach over a border, at the chunk where they start. A warp
+// takes 32 VEC columns of one or two such slabs, and the block's other warps walk
+// along with it: each takes every WALKERS-th partial sum of the run,
+// four of them in flight, and the walkers' sums are added in their order.
 template <typename G, int VEC>
 __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const __grid_constant__ SumArgs a,
-                                                                  G* __restrict__ grad) {
-  constexpr int WALKERS = kThreads / 32;
-  __shared__ float sums[WALKERS][32][VEC + 1];
+                                                                  G* __restrict__ grad, int slabs) {
+  constexpr int WARPS = kThreads / 32, AHEAD = 4;
+  __shared__ float sums[WARPS][32][VEC + 1];
   pdl_launch();
   pdl_wait();
-  const int64_t chunk = blockIdx.x;
-  const int64_t t0 = chunk * a.per, t1 = t0 + a.per;
-  const int lane = threadIdx.x & 31, walker = threadIdx.x >> 5;
-  const int c = (int)(lane + 32 * blockIdx.y) * VEC;
-  if (t1 >= a.n) return;
-  const uint32_t cur = a.key[t1 - 1];
-  // the run has to go on, and to start in this chunk
-  if (cur >= a.vocab || a.key[t1] != cur || (t0 > 0 && a.key[t0 - 1] == cur && a.key[t0] == cur)) return;
-  float s[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) s[i] = 0.f;
-  if (c < a.width) {
-    if (walker == 0) load_vec<VEC>(a.partial + (chunk * 2 + 1) * a.width + c, s);
-    bool more = true;
-    for (int64_t k = chunk + 1 + walker; more; k += 4 * WALKERS) {
-      float y[4][VEC];
-      bool on[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int64_t ku = k + u * WALKERS;
-        on[u] = ku * a.per < a.n && a.key[ku * a.per] == cur;
-        if (on[u]) load_vec<VEC>(a.partial + ku * 2 * a.width + c, y[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (on[u]) {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) s[i] += y[u][i];
-        }
-      more = on[3];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slab = warp % slabs, walker = warp / slabs;
+  const int walkers = WARPS / slabs;
+  const int c = (lane + 32 * (slab + slabs * (int)blockIdx.y)) * VEC;
+  // which of this block's chunks start a run that goes on
+  bool starts = false;
+  {
+    const int64_t t0 = ((int64_t)blockIdx.x * kJoinChunks + lane) * kChunkTokens, t1 = t0 + kChunkTokens;
+    if (lane < kJoinChunks && t1 < a.n) {
+      const uint32_t first = a.key[t0], cur = a.key[t1 - 1], next = a.key[t1];
+      const uint32_t before = t0 > 0 ? a.key[t0 - 1] : UINT_MAX;
+      starts = cur < a.vocab && next == cur && !(before == cur && first == cur);
     }
   }
+  for (uint32_t left = __ballot_sync(0xffffffffu, starts); left; left &= left - 1) {
+    const int64_t chunk = (int64_t)blockIdx.x * kJoinChunks + __ffs(left) - 1;
+    const uint32_t cur = a.key[(chunk + 1) * kChunkTokens];
+    // the first chunk behind the run, looked for 32 chunks at a time
+    int64_t end = chunk + 1;
+    for (uint32_t same = 0xffffffffu; same == 0xffffffffu;) {
+      const int64_t at = (end + lane) * kChunkTokens;
+      same = __ballot_sync(0xffffffffu, at < a.n && a.key[at] == cur);
+      end += __ffs(~same) ? __ffs(~same) - 1 : 32;
+    }
+    float s[VEC];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) sums[walker][lane][i] = s[i];
-  __syncthreads();
-  if (walker == 0 && c < a.width) {
+    for (int i = 0; i < VEC; ++i) s[i] = 0.f;
+    if (c < a.width) {
+      if (walker == 0) load_vec<VEC>(a.partial + (chunk * 2 + 1) * a.width + c, s);
+      for (int64_t k = chunk + 1 + walker; k < end; k += AHEAD * walkers) {
+        float y[AHEAD][VEC];
 #pragma unroll
-    for (int w = 1; w < WALKERS; ++w)
+        for (int u = 0; u < AHEAD; ++u)
+          if (k + u * walkers < end) load_vec<VEC>(a.partial + (k + u * walkers) * 2 * a.width + c, y[u]);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) s[i] += sums[w][lane][i];
-    write_grad<VEC>(grad, a, cur, c, s);
+        for (int u = 0; u < AHEAD; ++u)
+          if (k + u * walkers < end) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) s[i] += y[u][i];
+          }
+      }
+    }
+    if (walkers > 1) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) sums[warp][lane][i] = s[i];
+      __syncthreads();
+      if (walker == 0)
+        for (int w = 1; w < walkers; ++w)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) s[i] += sums[w * slabs + slab][lane][i];
+      __syncthreads();
+    }
+    if (walker == 0 && c < a.width) write_grad<VEC>(grad, a, cur, c, s);
   }
 }
 
 // ---- host ----
 struct Plan {
-  int per;          // sorted tokens of a chunk
   int64_t chunks;
   int64_t key_bytes, bytes;
 };
 
 Plan plan_backward(int64_t n, int64_t width) {
   Plan p;
-  p.per = 16;
-  p.chunks = (n + p.per - 1) / p.per;
+  p.chunks = (n + kChunkTokens - 1) / kChunkTokens;
   p.key_bytes = (n * 4 + 255) / 256 * 256;
   p.bytes = 4 * p.key_bytes + p.chunks * 2 * ((width + 7) / 8 * 8) * 4 + 256;
   return p;
@@ -564,9 +616,11 @@ cudaError_t run_sums(const SumArgs& a, int64_t chunks, const void* dout, void* g
   cudaError_t e = op_launch(embedding_sum_kernel<D, G, VEC>, g, b, 0, st, 1, a, static_cast<const D*>(dout),
                             static_cast<G*>(grad));
   if (e != cudaSuccess || chunks < 2) return e;
-  return op_launch(embedding_join_kernel<G, VEC>,
-                   dim3((unsigned)(chunks - 1), (unsigned)((a.width + 32 * VEC - 1) / (32 * VEC))), dim3(kThreads), 0,
-                   st, 1, a, static_cast<G*>(grad));
+  const int all = (a.width + 32 * VEC - 1) / (32 * VEC);
+  int slabs = 1;
+  while (slabs < all && slabs < 2) slabs *= 2;
+  return op_launch(embedding_join_kernel<G, VEC>, 
+                   dim3((unsigned)((chunks + kJoinChunks - 2) / kJoinChunks), (unsigned)((all + slabs - 1) / slabs)), dim3(kThreads), 0, st, 1, a, static_cast<G*>(grad), slabs);
 }
 
 // Blocks of the one-launch gradient: up to eight an SM.
@@ -711,7 +765,6 @@ ma_status muon_adamw_embedding_backward(const void* dout, int dout_dtype, int64_
     u.n = n_tokens;
     u.vocab = (uint32_t)vocab;
     u.width = (int)width;
-    u.per = p.per;
     u.scale = (float)scale;
     u.accumulate = accumulate;
     u.dstride = dout_stride;
