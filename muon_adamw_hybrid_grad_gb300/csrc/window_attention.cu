@@ -5,7 +5,7 @@
 //   S = Q K^T,  P = exp2(c S - m),  l += rowsum(P),  O += P V,  c = scale log2(e)
 // and out = O / l, lse = (m + log2 l) ln 2.
 //
-// window_forward_kernel (one persistent CTA per SM, 320 threads) works on two
+// window_forward_kernel (one persistent CTA per SM, 384 threads) works on two
 // tiles of 128 queries that share their keys and values: the same queries of
 // two heads that read one key head, or, where heads do not pair, two
 // neighbouring tiles of one head.
@@ -15,7 +15,12 @@
 //                   ring;
 //   warp 9          tcgen05.mma: S = Q K^T from shared memory, O += P V with P
 //                   from TMEM. The two tiles alternate, so that one tile's
-//                   products run while the other's softmax does.
+//                   products run while the other's softmax does. The tensor
+//                   core queues little, so whatever this warp does between
+//                   products leaves it idle: the next item is worked out while
+//                   the softmax of the first tiles runs;
+//   warp 10         (11 idles) clears the rows of a sample's last value tile that belong to
+//                   other samples.
 // TMEM: S0 | S1 | O0 | O1, 128 columns each.
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since it
@@ -25,45 +30,60 @@
 namespace ma {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+// of the 168 registers a thread is launched with: 8 softmax warps and 4 others, 8 * 208 + 4 * 80 <= 12 * 168
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
 constexpr int kErrForward = 0x201, kErrAlign = 0x204;
 
 template <int DP>
 struct FwdSmem {
   static constexpr uint32_t TILE = kAttnTile * DP * 2;
-  static constexpr int SLOTS = DP == 128 ? 5 : 8;
+  static constexpr int SLOTS = DP == 128 ? 4 : 8;
   static constexpr uint32_t RING = 2 * TILE;
-  static constexpr uint32_t BARS = RING + SLOTS * TILE;
-  // full[SLOTS], empty[SLOTS], q full, q empty, s full[2], p full[2], o full[2], drain
-  static constexpr int NBARS = 2 * SLOTS + 9;
+  static constexpr uint32_t STAGE = RING + SLOTS * TILE;  // 4 KB a softmax warp, for the results on their way out
+  static constexpr uint32_t BARS = STAGE + 8 * 4096;
+  // full[SLOTS], empty[SLOTS], raw[SLOTS], q full, q empty, s full[2], p full[2], o full[2], drain
+  static constexpr int NBARS = 3 * SLOTS + 9;
   static constexpr uint32_t BYTES = BARS + NBARS * 8 + 16;
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
 
 // The key tiles two query tiles meet, as one list: tile 0 for the sinks where
-// no window reaches it, then lo .. hi.
+// no window reaches it, then lo .. hi. Query tile s uses the steps a[s] .. b[s]
+// of it in full, and step 0 for the sinks where z[s] (written out, a0 to z1, so
+// that they stay in registers).
 struct PairTiles {
-  KeyTiles r[2];
   int lo, steps, sink;
+  int a0, b0, a1, b1;
+  bool z0, z1;
   __device__ __forceinline__ int tile(int n) const { return sink && n == 0 ? 0 : lo + n - sink; }
-  __device__ __forceinline__ bool use(int s, int kt) const {
-    return (kt >= r[s].lo && kt <= r[s].hi) || (kt == 0 && r[s].sink);
+  __device__ __forceinline__ bool whole(int s, int n) const { return n >= (s ? a1 : a0) && n <= (s ? b1 : b0); }
+  __device__ __forceinline__ bool use(int s, int n) const { return whole(s, n) || (n == 0 && (s ? z1 : z0)); }
+  __device__ __forceinline__ int last(int s) const {
+    const int a = s ? a1 : a0, b = s ? b1 : b0;
+    return b >= a ? b : (s ? z1 : z0) ? 0 : -1;
   }
 };
 __device__ __forceinline__ PairTiles pair_tiles(const AttnArgs& a, const SampleTile& t, int step) {
   PairTiles p;
-  p.r[0] = key_tiles(a, t.live, t.len, t.p0);
-  p.r[1] = key_tiles(a, t.live, t.len, t.p0 + step);
-  p.sink = p.r[0].sink ? 1 : 0;
-  p.lo = p.r[0].lo;
-  p.steps = p.sink + max(0, max(p.r[0].hi, p.r[1].hi) - p.lo + 1);
+  const KeyTiles r0 = key_tiles(a, t.live, t.len, t.p0), r1 = key_tiles(a, t.live, t.len, t.p0 + step);
+  p.sink = r0.sink ? 1 : 0;
+  p.lo = r0.lo;
+  p.steps = p.sink + max(0, max(r0.hi, r1.hi) - p.lo + 1);
+  const bool w0 = r0.hi >= r0.lo, w1 = r1.hi >= r1.lo;
+  p.a0 = w0 ? p.sink : 1;
+  p.b0 = w0 ? p.sink + r0.hi - p.lo : 0;
+  p.a1 = w1 ? p.sink + r1.lo - p.lo : 1;
+  p.b1 = w1 ? p.sink + r1.hi - p.lo : 0;
+  p.z0 = r0.sink;
+  p.z1 = r1.sink;
   return p;
 }
 
 struct FwdItem {
   SampleTile t;
   PairTiles k;
-  int head[2], kv;
+  int head0, head1, kv;
 };
 
 // Work item: a pair of query tiles. by_head: of two heads, else of one head.
@@ -75,9 +95,9 @@ __device__ __forceinline__ FwdItem fwd_item(const AttnArgs& a, int item, int uni
   w.t = find_unit(a, tile, lane, [rows](int len, bool) { return (len + rows - 1) / rows; });
   w.t.p0 = w.t.index * rows;
   w.k = pair_tiles(a, w.t, by_head ? 0 : kAttnTile);
-  w.head[0] = by_head ? 2 * u : u;
-  w.head[1] = by_head ? 2 * u + 1 : u;
-  w.kv = w.head[0] / (a.heads / a.kv_heads);
+  w.head0 = by_head ? 2 * u : u;
+  w.head1 = by_head ? 2 * u + 1 : u;
+  w.kv = w.head0 / (a.heads / a.kv_heads);
   return w;
 }
 
@@ -93,8 +113,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem), bars = base + SM::BARS;
-  Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, SM::TILE};
-  const uint32_t q_full = bars + 2 * SM::SLOTS * 8, q_empty = q_full + 8, s_full = q_full + 16, p_full = q_full + 32,
+  Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, bars + SM::SLOTS * 16, SM::TILE};
+  const uint32_t q_full = bars + 3 * SM::SLOTS * 8, q_empty = q_full + 8, s_full = q_full + 16, p_full = q_full + 32,
                  o_full = q_full + 48, drain = q_full + 64;
   if (base & 1023u) {  // the swizzle's phase is that of the address
     if (threadIdx.x == 0) atomicCAS(err, 0, kErrAlign);
@@ -102,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < SM::SLOTS; ++i) mbar_init(ring.full + 8 * i, 1), mbar_init(ring.empty + 8 * i, 1);
+    ring.init();
     mbar_init(q_full, 1), mbar_init(q_empty, 1), mbar_init(drain, 1);
     for (int s = 0; s < 2; ++s) mbar_init(s_full + 8 * s, 1), mbar_init(p_full + 8 * s, 128), mbar_init(o_full + 8 * s, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -117,6 +137,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rows = units * 2 == a.heads ? kAttnTile : 2 * kAttnTile;
   const int items = units * count_units(a, lane, [rows](int len, bool) { return (len + rows - 1) / rows; });
   bool ok = true;
+  // (one instruction for all four warps of a group)
+  if (warp < 8)
+    regs_up<kSoftmaxRegs>();
+  else
+    regs_down<kOtherRegs>();
 
   if (warp < 8) {
     // ---- softmax ----
@@ -124,34 +149,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + 128u * s + lanes, to = tmem + 256u + 128u * s + lanes;
     uint32_t s_ph = 0, o_ph = 0;
+    FwdItem next = fwd_item(a, blockIdx.x, units, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const FwdItem w = fwd_item(a, item, units, lane);
-      const int p0 = w.t.p0 + (w.head[0] == w.head[1] ? s * kAttnTile : 0), i = p0 + row;
+      const FwdItem w = next;
+      const int p0 = w.t.p0 + (w.head0 == w.head1 ? s * kAttnTile : 0), i = p0 + row, row0 = p0 + (row & ~31);
       float m = -INFINITY, l = 0.f;
       bool any = false;
       for (int n = 0; n < w.k.steps && ok; ++n) {
-        const int kt = w.k.tile(n);
-        if (!w.k.use(s, kt)) continue;
-        ok = __all_sync(0xffffffffu, mbar_wait(s_full + 8 * s, s_ph, abort_flag, err, kErrForward));
+        if (!w.k.use(s, n)) continue;
+        const int k0 = w.k.tile(n) * kAttnTile;
+        ok = mbar_wait_warp(s_full + 8 * s, s_ph, abort_flag, err, kErrForward);
         if (!ok) break;
         s_ph ^= 1;
         tc_fence_after();
+        if (!tile_full(a, p0, k0)) {
+          // key k0 + col is visible for col <= last and (col >= first or col < sink); past the sinks' columns
+          // of a tile that is there for them alone no score has been formed
+          const int last = w.k.whole(s, n) ? i - k0 : min(i - k0, sink_columns(a) - 1);
+          const int first = i - a.window + 1 - k0, sink = a.sinks - k0;
+          mask_tile(ts, 4, [&](int c) { return block_full(a, row0, k0 + 32 * c); },
+                    [&](int col) { return col > last || (col < first && col >= sink); });
+        }
         uint32_t v[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + 32 * c, v[c]);
         tmem_ld_wait();
-        const int k0 = kt * kAttnTile;
-        if (!tile_full(a, p0, k0)) {
-          // key k0 + col is visible for col <= last and (col >= first or col < sink)
-          const int last = i - k0, first = i - a.window + 1 - k0, sink = a.sinks - k0;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int col = 32 * c + j;
-              if (col > last || (col < first && col >= sink)) v[c][j] = 0xff800000u;
-            }
-        }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -197,148 +219,146 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(p_full + 8 * s);
       }
       if (!ok) break;
+      if (item + (int)gridDim.x < items) next = fwd_item(a, item + gridDim.x, units, lane);
       if (any) {
-        ok = __all_sync(0xffffffffu, mbar_wait(o_full + 8 * s, o_ph, abort_flag, err, kErrForward));
+        ok = mbar_wait_warp(o_full + 8 * s, o_ph, abort_flag, err, kErrForward);
         if (!ok) break;
         o_ph ^= 1;
         tc_fence_after();
       }
       // a query that saw no key: zeros and -infinity
       const float inv = any ? 1.f / l : 0.f;
-      const int64_t t = (int64_t)w.t.b + i;
-      __nv_bfloat16* po = out + (t * a.heads + w.head[s]) * a.dim;
-#pragma unroll 1
-      for (int c = 0; c < DP; c += 32) {
-        uint32_t o[32];
-        if (any) {
-          tmem_ld_32x32b_x32(to + c, o);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0u;
-        }
-        if (i < w.t.len) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            if (c + j < a.dim) {
-              uint32_t r[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                r[e] = op_pack_bf16(__uint_as_float(o[j + 2 * e]) * inv, __uint_as_float(o[j + 2 * e + 1]) * inv);
-              *reinterpret_cast<uint4*>(po + c + j) = make_uint4(r[0], r[1], r[2], r[3]);
-            }
-          }
-        }
-      }
+      const int head = s ? w.head1 : w.head0;
+      store_rows<DP>(to, inv, !any, out + (((int64_t)w.t.b + row0) * a.heads + head) * a.dim, (int64_t)a.heads * a.dim,
+                     w.t.len - row0, a.dim, base + SM::STAGE + warp * 4096, lane);
       if (i < w.t.len)
-        lse[(int64_t)w.head[s] * a.n + t] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        lse[(int64_t)head * a.n + w.t.b + i] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
       tc_fence_before();
     }
   } else if (warp == 8) {
     // ---- TMA ----
-    uint32_t pos = 0, q_ph = 1, q_loads = 0;
+    Cursor<SM::SLOTS> cur;
+    uint32_t loads = 0, raw_phase = 0;
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       const FwdItem w = fwd_item(a, item, units, lane);
-      const bool two = w.head[0] == w.head[1];
-      for (int n = 0; n < w.k.steps && ok; ++n) {
-        const int token = w.t.b + w.k.tile(n) * kAttnTile;
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          ok = mbar_wait(ring.empty_bar(pos), ring.empty_parity(pos), abort_flag, err, kErrForward);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (lane == 0) {
-            mbar_expect_tx(ring.full_bar(pos), SM::TILE);
-            load_tile<DP>(ring.slot(pos), kv ? &tmV : &tmK, token, w.kv, ring.full_bar(pos));
-          }
-          ++pos;
-          if (n == 0 && kv == 0) {
-            // the queries after the first keys: their buffer is free once the item before has issued its last S
-            ok = mbar_wait(q_empty, q_ph, abort_flag, err, kErrForward);
-            ok = __all_sync(0xffffffffu, ok);
+      if (lane == 0) {
+        for (int n = 0; n < w.k.steps && ok; ++n) {
+          const int at = w.k.tile(n) * kAttnTile;
+          for (int kv = 0; kv < 2 && ok; ++kv) {
+            ok = mbar_wait_in(cur.empty(ring), cur.phase ^ 1, abort_flag, err, kErrForward);
             if (!ok) break;
-            q_ph ^= 1;
-            ++q_loads;
-            if (lane == 0) {
+            // value rows of another sample are cleared; keys of another are masked in S
+            fill_slot<DP>(ring, cur, kv ? &tmV : &tmK, w.t.b + at, w.kv, kv ? w.t.len - at : kAttnTile, raw_phase);
+            cur.advance();
+            if (n == 0 && kv == 0) {
+              // the queries after the first keys: their buffer is free once the item before has formed its last S
+              ok = mbar_wait_in(q_empty, (loads & 1) ^ 1, abort_flag, err, kErrForward);
+              if (!ok) break;
+              ++loads;
               mbar_expect_tx(q_full, 2 * SM::TILE);
-              load_tile<DP>(base, &tmQ, w.t.b + w.t.p0, w.head[0], q_full);
-              load_tile<DP>(base + SM::TILE, &tmQ, w.t.b + w.t.p0 + (two ? kAttnTile : 0), w.head[1], q_full);
+              load_tile<DP>(base, &tmQ, w.t.b + w.t.p0, w.head0, q_full);
+              load_tile<DP>(base + SM::TILE, &tmQ, w.t.b + w.t.p0 + (w.head0 == w.head1 ? kAttnTile : 0), w.head1, q_full);
             }
           }
         }
       }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
     }
-    // every copy has landed before the CTA leaves
-    for (uint32_t k = pos > SM::SLOTS ? pos - SM::SLOTS : 0; k < pos; ++k)
-      drain_wait(ring.full_bar(k), ring.full_parity(k));
-    if (q_loads) drain_wait(q_full, (q_loads - 1) & 1);
-  } else {
+    if (lane == 0) {
+      // every copy has landed before the CTA leaves
+      drain_ring(ring, cur, raw_phase);
+      if (loads) drain_wait(q_full, (loads - 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
     // ---- MMA ----
-    uint32_t pos = 0, q_ph = 0, p_ph[2] = {0, 0};
+    Cursor<SM::SLOTS> cur;
+    uint32_t q_ph = 0, p_ph0 = 0, p_ph1 = 0;
+    const uint32_t tm = warp_uniform(tmem);
+    const int few = sink_columns(a);
+    FwdItem next = fwd_item(a, blockIdx.x, units, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const FwdItem w = fwd_item(a, item, units, lane);
-      if (w.k.steps == 0) continue;
-      ok = __all_sync(0xffffffffu, mbar_wait(q_full, q_ph, abort_flag, err, kErrForward));
-      if (!ok) break;
-      q_ph ^= 1;
-      bool pend[2] = {false, false}, begun[2] = {false, false};
-      // step n issues S of tile n and O += P V of tile n - 1
-      for (int n = 0; n <= w.k.steps && ok; ++n) {
-        const uint32_t kpos = pos + 2 * n, vpos = pos + 2 * n - 1;
-        const int kt = n < w.k.steps ? w.k.tile(n) : 0;
-        bool k_in = false, v_in = false;
-        for (int s = 0; s < 2 && ok; ++s) {
-          if (pend[s]) {
-            if (!v_in) {
-              ok = mbar_wait(ring.full_bar(vpos), ring.full_parity(vpos), abort_flag, err, kErrForward);
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
-              v_in = true;
-              const int valid = w.t.len - w.k.tile(n - 1) * kAttnTile;
-              if (valid < kAttnTile) clear_rows<DP>(ring.slot(vpos), valid, lane);
-            }
-            ok = __all_sync(0xffffffffu, mbar_wait(p_full + 8 * s, p_ph[s], abort_flag, err, kErrForward));
-            if (!ok) break;
-            p_ph[s] ^= 1;
-            tc_fence_after();
-            // the tile's last step for this half?
-            bool last = true;
-            for (int x = n; x < w.k.steps; ++x) last = last && !w.k.use(s, w.k.tile(x));
-            if (lane == 0) {
-              mma_ab<DP>(tmem + 256u + 128u * s, tmem + 128u * s, 32, ring.slot(vpos), begun[s]);
-              if (last) umma_commit<1>(o_full + 8 * s);
-            }
-            begun[s] = true;
-            pend[s] = false;
-          }
-          if (n < w.k.steps && w.k.use(s, kt)) {
-            if (!k_in) {
-              ok = mbar_wait(ring.full_bar(kpos), ring.full_parity(kpos), abort_flag, err, kErrForward);
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
-              k_in = true;
-              tc_fence_after();
-            }
-            if (lane == 0) {
-              mma_abt<DP>(tmem + 128u * s, base + s * SM::TILE, ring.slot(kpos));
-              umma_commit<1>(s_full + 8 * s);
-            }
-            pend[s] = true;
-          }
-        }
-        if (ok && lane == 0) {
-          if (n > 0) umma_commit<1>(ring.empty_bar(vpos));
-          if (n < w.k.steps) umma_commit<1>(ring.empty_bar(kpos));
-          if (n == w.k.steps - 1) umma_commit<1>(q_empty);
-        }
-        __syncwarp();
+      const FwdItem w = next;
+      const int steps = warp_uniform(w.k.steps), a0 = warp_uniform(w.k.a0), a1 = warp_uniform(w.k.a1),
+                b0 = warp_uniform(w.k.b0), b1 = warp_uniform(w.k.b1), z0 = warp_uniform((int)w.k.z0),
+                z1 = warp_uniform((int)w.k.z1);
+      const int last0 = b0 >= a0 ? b0 : z0 - 1, last1 = b1 >= a1 ? b1 : z1 - 1;
+      if (steps == 0 || !(ok = mbar_wait_warp(q_full, q_ph, abort_flag, err, kErrForward))) {
+        if (item + (int)gridDim.x < items) next = fwd_item(a, item + gridDim.x, units, lane);
+        continue;
       }
-      pos += 2 * w.k.steps;
+      q_ph ^= 1;
+      bool pend0 = false, pend1 = false, begun0 = false, begun1 = false;
+      Cursor<SM::SLOTS> vc;  // the value tile of the step before
+      // step n issues O += P V of tile n - 1 and S of tile n, for the one query tile and then for the other
+      for (int n = 0; n <= steps; ++n) {
+        const bool more = n < steps;
+        const bool whole0 = n >= a0 && n <= b0, whole1 = n >= a1 && n <= b1;
+        const bool use0 = more && (whole0 || (n == 0 && z0)), use1 = more && (whole1 || (n == 0 && z1));
+        const bool was0 = n - 1 >= a0 && n - 1 <= b0, was1 = n - 1 >= a1 && n - 1 <= b1;
+        if (n > 0 && !(ok = mbar_wait_warp(vc.full(ring), vc.phase, abort_flag, err, kErrForward))) break;
+        if (pend0) {
+          if (!(ok = mbar_wait_warp(p_full, p_ph0, abort_flag, err, kErrForward))) break;
+          p_ph0 ^= 1;
+          tc_fence_after();
+          if (was0)
+            mma_ab<DP>(tm + 256u, tm, 32, vc.data(ring), begun0);
+          else
+            mma_ab_few<DP>(tm + 256u, tm, 32, vc.data(ring), begun0, few);
+          if (n - 1 == last0) umma_commit_warp(o_full);
+          begun0 = true;
+        }
+        if (more && !(ok = mbar_wait_warp(cur.full(ring), cur.phase, abort_flag, err, kErrForward))) break;
+        tc_fence_after();
+        if (use0) {
+          mma_abt<DP>(tm, base, cur.data(ring), whole0 ? kAttnTile : few);
+          umma_commit_warp(s_full);
+        }
+        pend0 = use0;
+        if (pend1) {
+          if (!(ok = mbar_wait_warp(p_full + 8, p_ph1, abort_flag, err, kErrForward))) break;
+          p_ph1 ^= 1;
+          tc_fence_after();
+          if (was1)
+            mma_ab<DP>(tm + 384u, tm + 128u, 32, vc.data(ring), begun1);
+          else
+            mma_ab_few<DP>(tm + 384u, tm + 128u, 32, vc.data(ring), begun1, few);
+          if (n - 1 == last1) umma_commit_warp(o_full + 8);
+          begun1 = true;
+        }
+        if (n > 0) umma_commit_warp(vc.empty(ring));
+        if (use1) {
+          mma_abt<DP>(tm + 128u, base + SM::TILE, cur.data(ring), whole1 ? kAttnTile : few);
+          umma_commit_warp(s_full + 8);
+        }
+        pend1 = use1;
+        if (more) {
+          umma_commit_warp(cur.empty(ring));
+          if (n == steps - 1) umma_commit_warp(q_empty);
+          cur.advance();
+          vc = cur;
+          cur.advance();
+        }
+        if (n == 0 && item + (int)gridDim.x < items) next = fwd_item(a, item + gridDim.x, units, lane);
+      }
     }
     if (lane == 0) {
       umma_commit<1>(drain);
       drain_wait(drain, 0);
     }
     __syncwarp();
+  } else if (warp == 10) {
+    // ---- rows of other samples ----
+    Cursor<SM::SLOTS> cur;
+    uint32_t raw_phase = 0;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const FwdItem w = fwd_item(a, item, units, lane);
+      if (w.k.steps == 0) continue;
+      cur.skip(2 * w.k.steps - 1);
+      const int valid = w.t.len - w.k.tile(w.k.steps - 1) * kAttnTile;  // only the last tile can be ragged
+      if (valid < kAttnTile) ok = clear_slot<DP>(ring, cur, valid, raw_phase, lane, abort_flag, err, kErrForward);
+      cur.advance();
+    }
   }
   tc_fence_before();
   __syncthreads();

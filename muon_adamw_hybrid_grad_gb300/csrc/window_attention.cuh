@@ -150,6 +150,35 @@ __device__ __forceinline__ bool tile_full(const AttnArgs& a, int q0, int k0) {
   return k0 + kAttnTile - 1 <= q0 && (q0 + kAttnTile - 1 - k0 < a.window || k0 + kAttnTile - 1 < a.sinks);
 }
 
+// The same of 32 queries from q0 and 32 keys from k0: all of the pairs.
+__device__ __forceinline__ bool block_full(const AttnArgs& a, int q0, int k0) {
+  return k0 + 31 <= q0 && (q0 + 31 - k0 < a.window || k0 + 31 < a.sinks);
+}
+
+// Masks a tile of scores in TMEM: -infinity where `hidden(col)` in the 32-column
+// blocks for which `full(block)` does not hold; blocks first .. last - 1, whose
+// columns count from `taddr` on. A loop of its own over the few tiles at a
+// sample's and a window's edges: masks woven into the unrolled arithmetic made
+// it so long that fetching its instructions cost 4000 cycles a tile.
+template <typename F, typename H>
+__device__ __forceinline__ void mask_tile(uint32_t taddr, int blocks, F full, H hidden) {
+#pragma unroll 1
+  for (int c = 0; c < blocks; ++c) {
+    if (full(c)) continue;
+    uint32_t v[32];
+    tmem_ld_32x32b_x32(taddr + 32 * c, v);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (hidden(32 * c + j)) v[j] = 0xff800000u;
+    tmem_st_32x32b_x32(taddr + 32 * c, v);
+  }
+  tmem_st_wait();
+}
+
+// Columns that the products of a tile cover which only the sinks make visible.
+__device__ __forceinline__ int sink_columns(const AttnArgs& a) { return (a.sinks + 31) / 32 * 32; }
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -159,15 +188,41 @@ __device__ __forceinline__ float ex2(float x) {
 // A ring of equal slots that one thread fills by TMA in a fixed order of tiles
 // and the MMA warp empties in the same order. Position k of that order uses
 // slot k % SLOTS.
+//
+// A tile whose last rows belong to another sample takes a way round: its copy
+// signals the slot's `raw` barrier, a warp clears those rows and then signals
+// `full`. raw_phase (a bit per slot) is kept by each of the two.
 template <int SLOTS>
 struct Ring {
-  uint32_t data, full, empty, slot_bytes;
-  __device__ __forceinline__ uint32_t slot(uint32_t k) const { return data + (k % SLOTS) * slot_bytes; }
-  __device__ __forceinline__ uint32_t full_bar(uint32_t k) const { return full + (k % SLOTS) * 8; }
-  __device__ __forceinline__ uint32_t empty_bar(uint32_t k) const { return empty + (k % SLOTS) * 8; }
-  __device__ __forceinline__ uint32_t full_parity(uint32_t k) const { return (k / SLOTS) & 1; }
-  // of the wait before position k is filled (its slot's last user has finished)
-  __device__ __forceinline__ uint32_t empty_parity(uint32_t k) const { return ((k / SLOTS) & 1) ^ 1; }
+  uint32_t data, full, empty, raw, slot_bytes;
+  static constexpr int BARS = 3 * SLOTS;
+  __device__ __forceinline__ void init() const {
+    for (int i = 0; i < SLOTS; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1), mbar_init(raw + 8 * i, 1);
+  }
+};
+
+// A position of the ring's order: its slot, and the parity of its barriers'
+// phases there.
+template <int SLOTS>
+struct Cursor {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void advance() {
+    if (++slot == SLOTS) slot = 0, phase ^= 1;
+  }
+  __device__ __forceinline__ Cursor next() const {
+    Cursor c = *this;
+    c.advance();
+    return c;
+  }
+  __device__ __forceinline__ void skip(uint32_t n) {
+    slot += n;
+    phase ^= slot / SLOTS & 1;
+    slot %= SLOTS;
+  }
+  __device__ __forceinline__ uint32_t data(const Ring<SLOTS>& r) const { return r.data + slot * r.slot_bytes; }
+  __device__ __forceinline__ uint32_t full(const Ring<SLOTS>& r) const { return r.full + slot * 8; }
+  __device__ __forceinline__ uint32_t empty(const Ring<SLOTS>& r) const { return r.empty + slot * 8; }
+  __device__ __forceinline__ uint32_t raw(const Ring<SLOTS>& r) const { return r.raw + slot * 8; }
 };
 
 // One tile of 128 tokens from `token` of head `head`: DP / 64 panels.
@@ -177,20 +232,23 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* tm, i
   for (int p = 0; p < DP / 64; ++p) tma_load_3d(dst + p * (kAttnTile * 128), tm, p * 64, token, head, bar);
 }
 
-// D[128 x 128] = A B^T over DP elements, both operands K-major tiles.
+// D[128 x cols] = A B^T over DP elements, both operands K-major tiles; cols: the
+// first rows of B, a multiple of 32.
+// Issued by a whole warp, as all products here.
 template <int DP>
-__device__ __forceinline__ void mma_abt(uint32_t d_tmem, uint32_t a, uint32_t b) {
-  const uint32_t id = idesc_bf16(128, 128, false);
+__device__ __forceinline__ void mma_abt(uint32_t d_tmem, uint32_t a, uint32_t b, int cols = kAttnTile) {
+  const uint32_t id = idesc_bf16(128, cols, false);
+  const uint64_t da = sdesc(a, 16, 1024), db = sdesc(b, 16, 1024);
 #pragma unroll
-  for (int p = 0; p < DP / 64; ++p) {
-    const uint64_t da = sdesc(a + p * (kAttnTile * 128), 16, 1024), db = sdesc(b + p * (kAttnTile * 128), 16, 1024);
+  for (int p = 0; p < DP / 64; ++p)
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) umma_bf16<1>(d_tmem, da + 2u * kk, db + 2u * kk, id, (p | kk) != 0 ? 1u : 0u);
-  }
+    for (int kk = 0; kk < 4; ++kk)
+      umma_bf16_warp(d_tmem, da + (p * (kAttnTile * 128 / 16) + 2 * kk), db + (p * (kAttnTile * 128 / 16) + 2 * kk), id,
+                     (p | kk) != 0 ? 1u : 0u);
 }
 
-// D[128 x DP] (+)= A B with A bf16 in TMEM (128 x 128: 64 columns, the second
-// half of them `half_step` columns after the first) and B a tile whose 128
+// D[128 x DP] (+)= A B with A bf16 in TMEM (128 x 128: the columns of its second
+// half of 64 `half_step` TMEM columns after the first's) and B a tile whose 128
 // rows are the inner dimension.
 template <int DP>
 __device__ __forceinline__ void mma_ab(uint32_t d_tmem, uint32_t a_tmem, uint32_t half_step, uint32_t b, bool add) {
@@ -198,12 +256,77 @@ __device__ __forceinline__ void mma_ab(uint32_t d_tmem, uint32_t a_tmem, uint32_
   const uint64_t db = sdesc(b, kAttnTile * 128, 1024);
 #pragma unroll
   for (int ks = 0; ks < 8; ++ks)
-    umma_bf16_ts(d_tmem, a_tmem + (ks >> 2) * half_step + (ks & 3) * 8, db + 128u * ks, id, (add || ks != 0) ? 1u : 0u);
+    umma_bf16_ts_warp(d_tmem, a_tmem + (ks >> 2) * half_step + (ks & 3) * 8, db + 128u * ks, id,
+                      ks != 0 ? 1u : (uint32_t)add);
+}
+// The same with an inner dimension of `cols`, a multiple of 32.
+template <int DP>
+__device__ __forceinline__ void mma_ab_few(uint32_t d_tmem, uint32_t a_tmem, uint32_t half_step, uint32_t b, bool add,
+                                           int cols) {
+  const uint32_t id = idesc_bf16(128, DP, true);
+  const uint64_t db = sdesc(b, kAttnTile * 128, 1024);
+#pragma unroll 1
+  for (int ks = 0; ks * 16 < cols; ++ks)
+    umma_bf16_ts_warp(d_tmem, a_tmem + (ks >> 2) * half_step + (ks & 3) * 8, db + 128u * ks, id, add || ks != 0);
+}
+
+// Rows of a 128-row fp32 accumulator in TMEM, scaled and rounded to bf16, to
+// rows of the output that are `row_stride` elements apart; a warp handles its
+// own 32 lanes, its lane's row being valid where `rows` exceeds the lane. The
+// rows leave through 4 KB of the warp's shared memory, 64 columns at a time, so
+// that a store instruction covers four rows' whole 128-byte lines instead of 16
+// bytes of 32 rows. zero: store zeros and touch neither TMEM nor shared memory.
+template <int DP>
+__device__ __forceinline__ void store_rows(uint32_t taddr, float f, bool zero, __nv_bfloat16* out, int64_t row_stride,
+                                           int rows, int dim, uint32_t stage, int lane, int col0 = 0, int col1 = DP) {
+  const int q = lane & 7, r0 = lane >> 3;
+#pragma unroll 1
+  for (int c0 = col0; c0 < col1; c0 += 64) {
+    const int half = min(col1 - c0, 64);
+    const bool on = 8 * q < half && c0 + 8 * q < dim;
+    __nv_bfloat16* po = out + r0 * row_stride + c0 + 8 * q;
+    if (zero) {
+      for (int i = 0; i < 8; ++i)
+        if (on && 4 * i + r0 < rows) *reinterpret_cast<uint4*>(po + 4 * i * row_stride) = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h * 32 >= half) break;
+      uint32_t o[32];
+      tmem_ld_32x32b_x32(taddr + c0 + 32 * h, o);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t r[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          r[e] = op_pack_bf16(__uint_as_float(o[8 * j + 2 * e]) * f, __uint_as_float(o[8 * j + 2 * e + 1]) * f);
+        // 16-byte chunk 4 h + j of this lane's 128-byte row, swizzled by the row
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4)),
+                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                     : "memory");
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = 4 * i + r0;
+      uint4 v;
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "r"(stage + row * 128 + ((q ^ (row & 7)) << 4))
+                   : "memory");
+      if (on && row < rows) *reinterpret_cast<uint4*>(po + 4 * i * row_stride) = v;
+    }
+    __syncwarp();
+  }
 }
 
 // Zeros in the rows of a tile from `rows` on, by a whole warp: tokens there
 // belong to another sample, and a product with a zero weight must not take a
-// NaN or an infinity from them.
+// NaN or an infinity from them. A warp of its own does this, for a sample's
+// last tile only; the products wait for it there.
 template <int DP>
 __device__ __forceinline__ void clear_rows(uint32_t tile, int rows, int lane) {
   for (int i = rows * 8 + lane; i < kAttnTile * 8; i += 32) {
@@ -214,6 +337,43 @@ __device__ __forceinline__ void clear_rows(uint32_t tile, int rows, int lane) {
   }
   fence_proxy_async_smem();
   __syncwarp();
+}
+
+// Fills a position of the ring (one lane issues; the slot is free): `valid` rows
+// of the tile belong to the sample.
+template <int DP, int SLOTS>
+__device__ __forceinline__ void fill_slot(const Ring<SLOTS>& ring, const Cursor<SLOTS>& k, const CUtensorMap* tm,
+                                          int token, int head, int valid, uint32_t& raw_phase) {
+  const bool ragged = valid < kAttnTile;
+  const uint32_t bar = ragged ? k.raw(ring) : k.full(ring);
+  mbar_expect_tx(bar, ring.slot_bytes);
+  load_tile<DP>(k.data(ring), tm, token, head, bar);
+  if (ragged) raw_phase ^= 1u << k.slot;
+}
+
+// The clearing warp's part for a ragged tile.
+template <int DP, int SLOTS>
+__device__ __forceinline__ bool clear_slot(const Ring<SLOTS>& ring, const Cursor<SLOTS>& k, int valid,
+                                           uint32_t& raw_phase, int lane, volatile int* abort_flag, int* err,
+                                           int code) {
+  if (!mbar_wait_warp(k.raw(ring), raw_phase >> k.slot & 1, abort_flag, err, code)) return false;
+  raw_phase ^= 1u << k.slot;
+  clear_rows<DP>(k.data(ring), valid, lane);
+  if (lane == 0) mbar_arrive(k.full(ring));
+  return true;
+}
+
+// Every copy of the ring has landed, `cur` being the first position not filled:
+// the last of each slot, to either barrier. (A slot never filled waits for
+// nothing. Where the CTA gave up, a cleared tile's `full` may never come; the
+// wait for it is bounded like any other.)
+template <int SLOTS>
+__device__ __forceinline__ void drain_ring(const Ring<SLOTS>& ring, const Cursor<SLOTS>& cur, uint32_t raw_phase) {
+  for (uint32_t s = 0; s < SLOTS; ++s) {
+    drain_wait(ring.raw + 8 * s, (raw_phase >> s & 1) ^ 1);
+    // slots before the cursor were filled in its own round, the others in the round before
+    drain_wait(ring.full + 8 * s, s < cur.slot ? cur.phase : cur.phase ^ 1);
+  }
 }
 
 }  // namespace

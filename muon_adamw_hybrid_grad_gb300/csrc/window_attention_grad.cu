@@ -22,7 +22,9 @@
 namespace ma {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+// of the 168 registers a thread is launched with: 8 * 208 + 4 * 80 <= 12 * 168
+constexpr int kMathRegs = 208, kOtherRegs = 80;
 constexpr int kErrDq = 0x202, kErrDkv = 0x203, kErrAlign = 0x204;
 
 // ---- lse2 and delta ----
@@ -65,19 +67,27 @@ __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant
 
 // ---- dQ ----
 // Warps 0-7: a thread to a query and half of a tile's keys (warps 0-3 the
-// first 64, 4-7 the others); warp 8: TMA; warp 9: tcgen05.mma.
+// first 64, 4-7 the others); warp 8: TMA; warp 9: tcgen05.mma (one thread);
+// warp 10: clears the key and value rows of other samples.
 // TMEM: S of even steps | S of odd steps | dP | dQ. dS (bf16) overwrites the S
 // it came from, each half in the first 32 of its own 64 columns. S of the next
 // tile is formed while the threads work on this one's, and dP of the next as
 // soon as this one's has been read.
+//
+// Results leave through the shared memory of dO, whose next tile is therefore
+// loaded after the epilogue; the next Q comes in as soon as the last S has been
+// formed.
 template <int DP>
-struct DqSmem {
+struct GradSmem {
   static constexpr uint32_t TILE = kAttnTile * DP * 2;
   static constexpr int SLOTS = DP == 128 ? 5 : 8;
-  static constexpr uint32_t RING = 2 * TILE;  // after Q and dO
-  static constexpr uint32_t BARS = RING + SLOTS * TILE;
-  // full[SLOTS], empty[SLOTS], q full, q empty, s full[2], dp full, dp empty, ds full, dq full, drain
-  static constexpr int NBARS = 2 * SLOTS + 9;
+  static constexpr uint32_t RING = 2 * TILE;                   // after Q and dO, or K and V
+  static constexpr uint32_t STATS = RING + SLOTS * TILE;       // dkv: [2][lse2, delta][128] of the query tiles
+  static constexpr uint32_t OWN = STATS + 2 * 2 * kAttnTile * 4;
+  static constexpr uint32_t STAGE = DP == 128 ? TILE : OWN;    // 4 KB to each of 8 warps
+  static constexpr uint32_t BARS = DP == 128 ? OWN : OWN + 8 * 4096;
+  // full[SLOTS], empty[SLOTS], raw[SLOTS], then each kernel's own
+  static constexpr int NBARS = 3 * SLOTS + 12;
   static constexpr uint32_t BYTES = BARS + NBARS * 8 + 16;
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
@@ -100,47 +110,32 @@ __device__ __forceinline__ DqItem dq_item(const AttnArgs& a, int item, int lane)
   return w;
 }
 
-// The tile of S (64 columns of it) as softmax weights: v <- exp2(c v - lse2).
-// Key k0 + col is visible to query i for col <= last and (col >= first or col < sink).
-__device__ __forceinline__ void weights(uint32_t (&v)[2][32], float c, float shift, bool masked, int col0, int last,
-                                        int first, int sink) {
-#pragma unroll
-  for (int x = 0; x < 2; ++x)
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      float p = ex2(fmaf(__uint_as_float(v[x][j]), c, shift));
-      if (masked) {
-        const int col = col0 + 32 * x + j;
-        if (col > last || (col < first && col >= sink)) p = 0.f;
-      }
-      v[x][j] = __float_as_uint(p);
-    }
-}
-
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     window_dq_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ CUtensorMap tmDO, __nv_bfloat16* __restrict__ dq, int* __restrict__ err) {
-  using SM = DqSmem<DP>;
+  using SM = GradSmem<DP>;
   extern __shared__ __align__(1024) uint8_t smem[];
   // two words after the barriers: the TMEM base and the abort flag
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::BARS + SM::NBARS * 8);
   volatile int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem), bars = base + SM::BARS;
-  Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, SM::TILE};
-  const uint32_t q_full = bars + 2 * SM::SLOTS * 8, q_empty = q_full + 8, s_full = q_full + 16, dp_full = q_full + 32,
-                 dp_empty = q_full + 40, ds_full = q_full + 48, dq_full = q_full + 56, drain = q_full + 64;
+  Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, bars + SM::SLOTS * 16, SM::TILE};
+  const uint32_t own = bars + 3 * SM::SLOTS * 8, q_full = own, q_empty = own + 8, do_full = own + 16,
+                 do_empty = own + 24, s_full = own + 32, dp_full = own + 48, dp_empty = own + 56, ds_full = own + 64,
+                 dq_full = own + 72, drain = own + 80;
   if (base & 1023u) {  // the swizzle's phase is that of the address
     if (threadIdx.x == 0) atomicCAS(err, 0, kErrAlign);
     return;
   }
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < SM::SLOTS; ++i) mbar_init(ring.full + 8 * i, 1), mbar_init(ring.empty + 8 * i, 1);
-    mbar_init(q_full, 1), mbar_init(q_empty, 1), mbar_init(s_full, 1), mbar_init(s_full + 8, 1), mbar_init(dp_full, 1);
-    mbar_init(dp_empty, 256), mbar_init(ds_full, 256), mbar_init(dq_full, 1), mbar_init(drain, 1);
+    ring.init();
+    mbar_init(q_full, 1), mbar_init(q_empty, 1), mbar_init(do_full, 1), mbar_init(do_empty, 8);
+    mbar_init(s_full, 1), mbar_init(s_full + 8, 1), mbar_init(dp_full, 1), mbar_init(dp_empty, 256);
+    mbar_init(ds_full, 256), mbar_init(dq_full, 1), mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 9) tmem_alloc<1>(smem_u32(tmem_slot), 512);
@@ -151,38 +146,51 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch();
   pdl_wait();
   const int items = a.heads * count_units(a, lane, [](int len, bool) { return (len + kAttnTile - 1) / kAttnTile; });
+  const int few = sink_columns(a);
   bool ok = true;
+  // (one instruction for all four warps of a group)
+  if (warp < 8)
+    regs_up<kMathRegs>();
+  else
+    regs_down<kOtherRegs>();
 
   if (warp < 8) {
     const int half = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    uint32_t step = 0, dq_ph = 0;  // step: over all items; the S slot starts at 0 for each
-    uint32_t s_ph[2] = {0, 0};
+    uint32_t step = 0, s_ph = 0, dq_ph = 0;  // step: over all items; s_ph: a bit per S slot
+    DqItem next = dq_item(a, blockIdx.x, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const DqItem w = dq_item(a, item, lane);
-      const int i = w.t.p0 + row;
+      const DqItem w = next;
+      const int row0 = w.t.p0 + (row & ~31), i = w.t.p0 + row;
       const int64_t t = (int64_t)w.t.b + i;
       const bool mine = i < w.t.len;
       const float lse2 = mine ? a.lse2[(int64_t)w.head * a.n + t] : INFINITY;
       const float delta = mine ? a.delta[(int64_t)w.head * a.n + t] : 0.f;
       for (int n = 0; n < w.steps && ok; ++n, ++step) {
-        const uint32_t slot = n & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(s_full + 8 * slot, s_ph[slot], abort_flag, err, kErrDq));
+        const uint32_t slot = n & 1, ts = tmem + lanes + 128u * slot + 64u * half;
+        const int k0 = w.tile(n) * kAttnTile + 64 * half;  // of this half
+        ok = mbar_wait_warp(s_full + 8 * slot, s_ph >> slot & 1, abort_flag, err, kErrDq);
         if (!ok) break;
-        s_ph[slot] ^= 1;
+        s_ph ^= 1u << slot;
         tc_fence_after();
-        const uint32_t ts = tmem + lanes + 128u * slot + 64u * half;
-        uint32_t p[2][32], g[2][32];
+        if (!tile_full(a, w.t.p0, k0 - 64 * half)) {
+          // key k0 + col is visible for col <= last and (col >= first or col < sink); past the sinks' columns of
+          // a tile that is there for them alone no score has been formed
+          const int last = w.k.sink && n == 0 ? min(i - k0, few - 64 * half - 1) : i - k0;
+          const int first = i - k0 - a.window + 1, sink = a.sinks - k0;
+          mask_tile(ts, 2, [&](int c) { return block_full(a, row0, k0 + 32 * c); },
+                    [&](int col) { return col > last || (col < first && col >= sink); });
+        }
+        uint32_t p[2][32], g[2][32], ds[32];
         tmem_ld_32x32b_x32(ts, p[0]);
         tmem_ld_32x32b_x32(ts + 32, p[1]);
         tmem_ld_wait();
-        const int k0 = w.tile(n) * kAttnTile;
-        const bool masked = !tile_full(a, w.t.p0, k0);
-        if (masked)
-          weights(p, a.scale_log2, -lse2, true, 64 * half, i - k0, i - a.window + 1 - k0, a.sinks - k0);
-        else
-          weights(p, a.scale_log2, -lse2, false, 0, 0, 0, 0);
-        ok = __all_sync(0xffffffffu, mbar_wait(dp_full, step & 1, abort_flag, err, kErrDq));
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            p[x][j] = __float_as_uint(ex2(fmaf(__uint_as_float(p[x][j]), a.scale_log2, -lse2)));
+        ok = mbar_wait_warp(dp_full, step & 1, abort_flag, err, kErrDq);
         if (!ok) break;
         tc_fence_after();
         tmem_ld_32x32b_x32(tmem + lanes + 256u + 64u * half, g[0]);
@@ -190,162 +198,142 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive(dp_empty);
-        uint32_t ds[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const int x = j >> 4, e = (2 * j) & 31;
-          float d0 = __uint_as_float(p[x][e]) * (__uint_as_float(g[x][e]) - delta);
-          float d1 = __uint_as_float(p[x][e + 1]) * (__uint_as_float(g[x][e + 1]) - delta);
-          if (masked) {
-            // a value row of another sample may hold anything
-            if (p[x][e] == 0u) d0 = 0.f;
-            if (p[x][e + 1] == 0u) d1 = 0.f;
-          }
-          ds[j] = op_pack_bf16(d0, d1);
-        }
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            ds[16 * x + j] =
+                op_pack_bf16(__uint_as_float(p[x][2 * j]) * (__uint_as_float(g[x][2 * j]) - delta),
+                             __uint_as_float(p[x][2 * j + 1]) * (__uint_as_float(g[x][2 * j + 1]) - delta));
         tmem_st_32x32b_x32(ts, ds);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(ds_full);
       }
       if (!ok) break;
+      if (item + (int)gridDim.x < items) next = dq_item(a, item + gridDim.x, lane);
       if (w.steps) {
-        ok = __all_sync(0xffffffffu, mbar_wait(dq_full, dq_ph, abort_flag, err, kErrDq));
+        ok = mbar_wait_warp(dq_full, dq_ph, abort_flag, err, kErrDq);
         if (!ok) break;
         dq_ph ^= 1;
         tc_fence_after();
       }
-      __nv_bfloat16* po = dq + (t * a.heads + w.head) * a.dim;
-#pragma unroll 1
-      for (int c = half * (DP / 2); c < (half + 1) * (DP / 2); c += 32) {
-        uint32_t o[32];
-        if (w.steps) {
-          tmem_ld_32x32b_x32(tmem + lanes + 384u + c, o);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0u;
-        }
-        if (mine) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            if (c + j < a.dim) {
-              uint32_t r[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                r[e] = op_pack_bf16(__uint_as_float(o[j + 2 * e]) * a.scale, __uint_as_float(o[j + 2 * e + 1]) * a.scale);
-              *reinterpret_cast<uint4*>(po + c + j) = make_uint4(r[0], r[1], r[2], r[3]);
-            }
-          }
-        }
+      store_rows<DP>(tmem + lanes + 384u, a.scale, w.steps == 0,
+                     dq + (((int64_t)w.t.b + row0) * a.heads + w.head) * a.dim, (int64_t)a.heads * a.dim,
+                     w.t.len - row0, a.dim, base + SM::STAGE + warp * 4096, lane, half * (DP / 2), (half + 1) * (DP / 2));
+      if (w.steps) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(do_empty);
       }
       tc_fence_before();
     }
   } else if (warp == 8) {
-    uint32_t pos = 0, q_ph = 1, q_loads = 0;
+    Cursor<SM::SLOTS> cur;
+    uint32_t loads = 0, raw_phase = 0;
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       const DqItem w = dq_item(a, item, lane);
-      for (int n = 0; n < w.steps && ok; ++n) {
-        const int token = w.t.b + w.tile(n) * kAttnTile;
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          ok = mbar_wait(ring.empty_bar(pos), ring.empty_parity(pos), abort_flag, err, kErrDq);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (lane == 0) {
-            mbar_expect_tx(ring.full_bar(pos), SM::TILE);
-            load_tile<DP>(ring.slot(pos), kv ? &tmV : &tmK, token, w.kv, ring.full_bar(pos));
-          }
-          ++pos;
-          if (n == 0 && kv == 0) {
-            ok = mbar_wait(q_empty, q_ph, abort_flag, err, kErrDq);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            q_ph ^= 1;
-            ++q_loads;
-            if (lane == 0) {
-              mbar_expect_tx(q_full, 2 * SM::TILE);
-              load_tile<DP>(base, &tmQ, w.t.b + w.t.p0, w.head, q_full);
-              load_tile<DP>(base + SM::TILE, &tmDO, w.t.b + w.t.p0, w.head, q_full);
+      if (lane == 0) {
+        for (int n = 0; n < w.steps && ok; ++n) {
+          const int at = w.tile(n) * kAttnTile;
+          for (int kv = 0; kv < 2 && ok; ++kv) {
+            if (n == 0) {
+              // Q before the first keys, dO before the first values
+              ok = mbar_wait_in(kv ? do_empty : q_empty, (loads & 1) ^ 1, abort_flag, err, kErrDq);
+              if (!ok) break;
+              mbar_expect_tx(kv ? do_full : q_full, SM::TILE);
+              load_tile<DP>(base + kv * SM::TILE, kv ? &tmDO : &tmQ, w.t.b + w.t.p0, w.head, kv ? do_full : q_full);
             }
+            ok = mbar_wait_in(cur.empty(ring), cur.phase ^ 1, abort_flag, err, kErrDq);
+            if (!ok) break;
+            fill_slot<DP>(ring, cur, kv ? &tmV : &tmK, w.t.b + at, w.kv, w.t.len - at, raw_phase);
+            cur.advance();
           }
         }
+        if (w.steps) ++loads;
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+    }
+    if (lane == 0) {
+      drain_ring(ring, cur, raw_phase);
+      if (loads) {
+        // (after a wait that ran out dO's last copy may not have been asked for: this wait is bounded too)
+        drain_wait(q_full, (loads - 1) & 1);
+        drain_wait(do_full, (loads - 1) & 1);
       }
     }
-    for (uint32_t k = pos > SM::SLOTS ? pos - SM::SLOTS : 0; k < pos; ++k)
-      drain_wait(ring.full_bar(k), ring.full_parity(k));
-    if (q_loads) drain_wait(q_full, (q_loads - 1) & 1);
-  } else {
-    uint32_t pos = 0, q_ph = 0, step = 0;
+    __syncwarp();
+  } else if (warp == 9) {
+    Cursor<SM::SLOTS> sc;  // the next S's key tile
+    uint32_t q_ph = 0, step = 0;
+    const uint32_t tm = warp_uniform(tmem);
+    DqItem next = dq_item(a, blockIdx.x, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const DqItem w = dq_item(a, item, lane);
-      if (w.steps == 0) continue;
-      ok = __all_sync(0xffffffffu, mbar_wait(q_full, q_ph, abort_flag, err, kErrDq));
-      if (!ok) break;
-      q_ph ^= 1;
-      // S of step n into its slot, dP of step n
-      auto wait_tile = [&](uint32_t k) {
-        ok = mbar_wait(ring.full_bar(k), ring.full_parity(k), abort_flag, err, kErrDq);
-        ok = __all_sync(0xffffffffu, ok);
-        return ok;
-      };
+      const DqItem w = next;
+      const int steps = warp_uniform(w.steps), sink = warp_uniform((int)w.k.sink);
+      if (steps == 0) {
+        if (item + (int)gridDim.x < items) next = dq_item(a, item + gridDim.x, lane);
+        continue;
+      }
+      const int cols0 = sink ? few : kAttnTile;
+      Cursor<SM::SLOTS> pc = sc.next(), qc = sc;  // the next dP's value tile, the next dQ's key tile
       auto issue_s = [&](int n) {
-        const uint32_t k = pos + 2 * n;
-        if (!wait_tile(k)) return false;
-        const int valid = w.t.len - w.tile(n) * kAttnTile;
-        if (valid < kAttnTile) clear_rows<DP>(ring.slot(k), valid, lane);
+        if (!mbar_wait_warp(sc.full(ring), sc.phase, abort_flag, err, kErrDq)) return false;
         tc_fence_after();
-        if (lane == 0) {
-          mma_abt<DP>(tmem + 128u * (n & 1), base, ring.slot(k));
-          umma_commit<1>(s_full + 8 * (n & 1));
-        }
-        __syncwarp();
+        mma_abt<DP>(tm + 128u * (n & 1), base, sc.data(ring), n ? kAttnTile : cols0);
+        umma_commit_warp(s_full + 8 * (n & 1));
+        if (n == steps - 1) umma_commit_warp(q_empty);
+        sc.skip(2);
         return true;
       };
       auto issue_dp = [&](int n) {
-        const uint32_t k = pos + 2 * n + 1;
-        if (!wait_tile(k)) return false;
+        if (!mbar_wait_warp(pc.full(ring), pc.phase, abort_flag, err, kErrDq)) return false;
         tc_fence_after();
-        if (lane == 0) {
-          mma_abt<DP>(tmem + 256u, base + SM::TILE, ring.slot(k));
-          umma_commit<1>(dp_full);
-          umma_commit<1>(ring.empty_bar(k));
-        }
-        __syncwarp();
+        mma_abt<DP>(tm + 256u, base + SM::TILE, pc.data(ring), n ? kAttnTile : cols0);
+        umma_commit_warp(dp_full);
+        umma_commit_warp(pc.empty(ring));
+        pc.skip(2);
         return true;
       };
-      if (!issue_s(0) || !issue_dp(0)) break;
-      if (w.steps > 1 && !issue_s(1)) break;
-      for (int n = 0; n < w.steps && ok; ++n, ++step) {
-        if (n + 1 < w.steps) {
-          ok = __all_sync(0xffffffffu, mbar_wait(dp_empty, step & 1, abort_flag, err, kErrDq));
-          if (!ok || !issue_dp(n + 1)) break;
-        } else {
-          ok = __all_sync(0xffffffffu, mbar_wait(dp_empty, step & 1, abort_flag, err, kErrDq));
-          if (!ok) break;
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(ds_full, step & 1, abort_flag, err, kErrDq));
+      ok = mbar_wait_warp(q_full, q_ph, abort_flag, err, kErrDq) && issue_s(0) &&
+           mbar_wait_warp(do_full, q_ph, abort_flag, err, kErrDq) && issue_dp(0) && (steps == 1 || issue_s(1));
+      q_ph ^= 1;
+      if (item + (int)gridDim.x < items) next = dq_item(a, item + gridDim.x, lane);
+      for (int n = 0; n < steps && ok; ++n, ++step) {
+        // dP of the next step once this one's has been read
+        ok = mbar_wait_warp(dp_empty, step & 1, abort_flag, err, kErrDq) && (n + 1 == steps || issue_dp(n + 1)) &&
+             mbar_wait_warp(ds_full, step & 1, abort_flag, err, kErrDq);
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
-          mma_ab<DP>(tmem + 384u, tmem + 128u * (n & 1), 64, ring.slot(pos + 2 * n), n > 0);
-          umma_commit<1>(ring.empty_bar(pos + 2 * n));
-        }
-        __syncwarp();
-        if (n + 2 < w.steps && !issue_s(n + 2)) break;
+        if (n > 0 || !sink)
+          mma_ab<DP>(tm + 384u, tm + 128u * (n & 1), 64, qc.data(ring), n > 0);
+        else
+          mma_ab_few<DP>(tm + 384u, tm, 64, qc.data(ring), false, few);
+        umma_commit_warp(qc.empty(ring));
+        qc.skip(2);
+        if (n + 2 < steps) ok = issue_s(n + 2);
       }
-      if (!ok) break;
-      if (lane == 0) {
-        umma_commit<1>(dq_full);
-        umma_commit<1>(q_empty);
-      }
-      __syncwarp();
-      pos += 2 * w.steps;
+      if (ok) umma_commit_warp(dq_full);
     }
     if (lane == 0) {
       umma_commit<1>(drain);
       drain_wait(drain, 0);
     }
     __syncwarp();
+  } else if (warp == 10) {
+    Cursor<SM::SLOTS> cur;
+    uint32_t raw_phase = 0;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const DqItem w = dq_item(a, item, lane);
+      if (w.steps == 0) continue;
+      cur.skip(2 * w.steps - 2);
+      const int valid = w.t.len - w.tile(w.steps - 1) * kAttnTile;  // only the last tile can be ragged
+      for (int kv = 0; kv < 2; ++kv) {
+        if (valid < kAttnTile && ok)
+          ok = clear_slot<DP>(ring, cur, valid, raw_phase, lane, abort_flag, err, kErrDq);
+        cur.advance();
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -357,23 +345,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Scores are formed transposed, S^T = K Q^T and dP^T = V dO^T, so that P^T and
 // dS^T stand in TMEM as the left operands of dV += P^T dO and dK += dS^T Q.
 // Warps 0-7: a thread to a key and half of a tile's queries; warp 8: TMA;
-// warp 9: tcgen05.mma. TMEM: S^T | dP^T | dV | dK; P^T overwrites S^T and dS^T
+// warp 9: tcgen05.mma (one thread); warp 10: clears rows of Q and dO that belong
+// to other samples. TMEM: S^T | dP^T | dV | dK; P^T overwrites S^T and dS^T
 // dP^T, each half in the first 32 of its own 64 columns. While the threads form
 // P^T of a step the tensor core runs the step before's dK and this one's dP^T;
-// while they form dS^T it runs dV and the next step's S^T.
-template <int DP>
-struct DkvSmem {
-  static constexpr uint32_t TILE = kAttnTile * DP * 2;
-  static constexpr int SLOTS = DP == 128 ? 5 : 8;
-  static constexpr uint32_t RING = 2 * TILE;  // after K and V
-  static constexpr uint32_t STATS = RING + SLOTS * TILE;  // [2][lse2, delta][128] of the query tiles
-  static constexpr uint32_t BARS = STATS + 2 * 2 * kAttnTile * 4;
-  // full[SLOTS], empty[SLOTS], kv full, done, s full, dp full, p full, ds full, stats full, drain
-  static constexpr int NBARS = 2 * SLOTS + 8;
-  static constexpr uint32_t BYTES = BARS + NBARS * 8 + 16;
-  static_assert(BYTES <= 232448, "shared memory per CTA");
-};
-
+// while they form dS^T it runs dV and the next step's S^T. Results leave through
+// the shared memory of V, whose next tile is therefore loaded after the epilogue;
+// the next K comes in as soon as the last S^T has been formed.
 // First query tile that only the sinks reach in tile 0.
 __device__ __forceinline__ int first_sink_tile(const AttnArgs& a) {
   return a.window == 0 ? 0 : (kAttnTile - 1 + a.window - 1) / kAttnTile + 1;
@@ -424,16 +402,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tmDO, __nv_bfloat16* __restrict__ dk,
                       __nv_bfloat16* __restrict__ dv, float* __restrict__ partial, int64_t partial_slots,
                       int* __restrict__ err) {
-  using SM = DkvSmem<DP>;
+  using SM = GradSmem<DP>;
   extern __shared__ __align__(1024) uint8_t smem[];
   // two words after the barriers: the TMEM base and the abort flag
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::BARS + SM::NBARS * 8);
   volatile int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem), bars = base + SM::BARS;
-  Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, SM::TILE};
-  const uint32_t kv_full = bars + 2 * SM::SLOTS * 8, done = kv_full + 8, s_full = kv_full + 16, dp_full = kv_full + 24,
-                 p_full = kv_full + 32, ds_full = kv_full + 40, stat_full = kv_full + 48, drain = kv_full + 56;
+  Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, bars + SM::SLOTS * 16, SM::TILE};
+  const uint32_t own = bars + 3 * SM::SLOTS * 8, k_full = own, k_empty = own + 8, v_full = own + 16,
+                 v_empty = own + 24, s_full = own + 32, dp_full = own + 40, p_full = own + 48, ds_full = own + 56,
+                 stat_full = own + 64, done = own + 72, drain = own + 80;
   float* stats = reinterpret_cast<float*>(smem + SM::STATS);
   if (base & 1023u) {  // the swizzle's phase is that of the address
     if (threadIdx.x == 0) atomicCAS(err, 0, kErrAlign);
@@ -441,9 +420,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < SM::SLOTS; ++i) mbar_init(ring.full + 8 * i, 1), mbar_init(ring.empty + 8 * i, 1);
-    mbar_init(kv_full, 1), mbar_init(done, 1), mbar_init(s_full, 1), mbar_init(dp_full, 1), mbar_init(p_full, 256);
-    mbar_init(ds_full, 256), mbar_init(stat_full, 256), mbar_init(drain, 1);
+    ring.init();
+    mbar_init(k_full, 1), mbar_init(k_empty, 1), mbar_init(v_full, 1), mbar_init(v_empty, 8);
+    mbar_init(s_full, 1), mbar_init(dp_full, 1), mbar_init(p_full, 256), mbar_init(ds_full, 256);
+    mbar_init(stat_full, 256), mbar_init(done, 1), mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 9) tmem_alloc<1>(smem_u32(tmem_slot), 512);
@@ -459,57 +439,61 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int items = sink_items +
                     a.kv_heads * count_units(a, lane, [](int len, bool) { return (len + kAttnTile - 1) / kAttnTile; });
   bool ok = true;
+  // (one instruction for all four warps of a group)
+  if (warp < 8)
+    regs_up<kMathRegs>();
+  else
+    regs_down<kOtherRegs>();
 
   if (warp < 8) {
     const int half = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + 64u * half, tg = ts + 128u;
     uint32_t step = 0, done_ph = 0;
+    DkvItem upcoming = dkv_item(a, blockIdx.x, sink_items, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const DkvItem w = dkv_item(a, item, sink_items, lane);
-      const int steps = group * w.nq;
+      const DkvItem w = upcoming;
+      const int steps = group * w.nq, row0 = w.t.p0 + (row & ~31), j = w.t.p0 + row;
       // threads 0-127 bring lse2 of a query tile, threads 128-255 delta
-      auto stat = [&](int n) {
-        const int h = w.kv * group + n / w.nq, i = (w.q_lo + n % w.nq) * kAttnTile + row;
+      auto stat = [&](int head, int tile) {
+        const int i = tile * kAttnTile + row;
         if (i >= w.t.len) return half ? 0.f : INFINITY;
-        return (half ? a.delta : a.lse2)[(int64_t)h * a.n + w.t.b + i];
+        return (half ? a.delta : a.lse2)[(int64_t)head * a.n + w.t.b + i];
       };
+      int head = w.kv * group, tile = w.q_lo;  // of the step
       if (steps) {
-        stats[(step & 1) * 256 + threadIdx.x] = stat(0);
+        stats[(step & 1) * 256 + threadIdx.x] = stat(head, tile);
         mbar_arrive(stat_full);
       }
       for (int n = 0; n < steps && ok; ++n, ++step) {
-        const float next = n + 1 < steps ? stat(n + 1) : 0.f;
+        const int q0 = tile * kAttnTile;
+        if (++tile == w.q_lo + w.nq) tile = w.q_lo, ++head;
+        const float next = n + 1 < steps ? stat(head, tile) : 0.f;
         const float* st = stats + (step & 1) * 256 + 64 * half;
-        ok = __all_sync(0xffffffffu, mbar_wait(stat_full, step & 1, abort_flag, err, kErrDkv));
-        if (!ok) break;
-        ok = __all_sync(0xffffffffu, mbar_wait(s_full, step & 1, abort_flag, err, kErrDkv));
+        ok = mbar_wait_warp(stat_full, step & 1, abort_flag, err, kErrDkv) &&
+             mbar_wait_warp(s_full, step & 1, abort_flag, err, kErrDkv);
         if (!ok) break;
         tc_fence_after();
+        if (!tile_full(a, q0, w.t.p0)) {
+          // query q0 + 64 half + col sees key j for col >= from and col <= to
+          const int qh = q0 + 64 * half, from = j - qh;
+          const int to = j < a.sinks ? kAttnTile : (int)min((int64_t)from + a.window - 1, (int64_t)kAttnTile);
+          mask_tile(ts, 2, [&](int c) { return block_full(a, qh + 32 * c, row0); },
+                    [&](int col) { return col < from || col > to; });
+        }
         uint32_t p[2][32], g[2][32], r[32];
         tmem_ld_32x32b_x32(ts, p[0]);
         tmem_ld_32x32b_x32(ts + 32, p[1]);
         tmem_ld_wait();
-        const int q0 = (w.q_lo + n % w.nq) * kAttnTile;
-        // query q0 + col sees key j for col >= from and (col <= to or j < sinks)
-        const int j = w.t.p0 + row, from = j - q0;
-        const int to = j < a.sinks ? kAttnTile : (int)min((int64_t)j + a.window - 1 - q0, (int64_t)kAttnTile);
-        const bool masked = !tile_full(a, q0, w.t.p0);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(st + 32 * x + e);
-            const float l[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              float q = ex2(fmaf(__uint_as_float(p[x][e + y]), a.scale_log2, -l[y]));
-              if (masked) {
-                const int col = 64 * half + 32 * x + e + y;
-                if (col < from || col > to) q = 0.f;
-              }
-              p[x][e + y] = __float_as_uint(q);
-            }
+            const float4 l = *reinterpret_cast<const float4*>(st + 32 * x + e);
+            p[x][e] = __float_as_uint(ex2(fmaf(__uint_as_float(p[x][e]), a.scale_log2, -l.x)));
+            p[x][e + 1] = __float_as_uint(ex2(fmaf(__uint_as_float(p[x][e + 1]), a.scale_log2, -l.y)));
+            p[x][e + 2] = __float_as_uint(ex2(fmaf(__uint_as_float(p[x][e + 2]), a.scale_log2, -l.z)));
+            p[x][e + 3] = __float_as_uint(ex2(fmaf(__uint_as_float(p[x][e + 3]), a.scale_log2, -l.w)));
           }
 #pragma unroll
         for (int e = 0; e < 32; ++e)
@@ -518,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(p_full);
-        ok = __all_sync(0xffffffffu, mbar_wait(dp_full, step & 1, abort_flag, err, kErrDkv));
+        ok = mbar_wait_warp(dp_full, step & 1, abort_flag, err, kErrDkv);
         if (!ok) break;
         tc_fence_after();
         tmem_ld_32x32b_x32(tg, g[0]);
@@ -528,13 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const float4 d4 = *reinterpret_cast<const float4*>(st + 128 + 32 * x + e);
-            const float d[4] = {d4.x, d4.y, d4.z, d4.w};
-#pragma unroll
-            for (int y = 0; y < 4; y += 2)
-              r[16 * x + (e + y) / 2] =
-                  op_pack_bf16(__uint_as_float(p[x][e + y]) * (__uint_as_float(g[x][e + y]) - d[y]),
-                               __uint_as_float(p[x][e + y + 1]) * (__uint_as_float(g[x][e + y + 1]) - d[y + 1]));
+            const float4 d = *reinterpret_cast<const float4*>(st + 128 + 32 * x + e);
+            r[16 * x + e / 2] = op_pack_bf16(__uint_as_float(p[x][e]) * (__uint_as_float(g[x][e]) - d.x),
+                                             __uint_as_float(p[x][e + 1]) * (__uint_as_float(g[x][e + 1]) - d.y));
+            r[16 * x + e / 2 + 1] = op_pack_bf16(__uint_as_float(p[x][e + 2]) * (__uint_as_float(g[x][e + 2]) - d.z),
+                                                 __uint_as_float(p[x][e + 3]) * (__uint_as_float(g[x][e + 3]) - d.w));
           }
         tmem_st_32x32b_x32(tg, r);
         tmem_st_wait();
@@ -547,137 +529,162 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
+      if (item + (int)gridDim.x < items) upcoming = dkv_item(a, item + gridDim.x, sink_items, lane);
       if (steps) {
-        ok = __all_sync(0xffffffffu, mbar_wait(done, done_ph, abort_flag, err, kErrDkv));
+        ok = mbar_wait_warp(done, done_ph, abort_flag, err, kErrDkv);
         if (!ok) break;
         done_ph ^= 1;
         tc_fence_after();
       }
-      // warps 0-3 store dV, warps 4-7 dK
-      const int j = w.t.p0 + row;
+      // warps 0-3 store dV, warps 4-7 dK; the sink keys' rows go to their partial slot in fp32
       const float f = half ? a.scale : 1.f;
-      const bool part = w.slot >= 0 && j < a.sinks;
-      float* pp = partial + ((w.slot * a.kv_heads + w.kv) * 2 + half) * (int64_t)a.sinks * a.dim + (int64_t)j * a.dim;
-      __nv_bfloat16* po = (half ? dk : dv) + (((int64_t)w.t.b + j) * a.kv_heads + w.kv) * a.dim;
-      const bool mine = j < w.t.len && (part ? w.slot < partial_slots : !w.sink_only);
+      const uint32_t acc = tmem + lanes + 256u + 128u * half;
+      const int sinks = w.slot >= 0 ? a.sinks : 0;
+      if (row0 < sinks) {
+        float* pp = partial + ((w.slot * a.kv_heads + w.kv) * 2 + half) * (int64_t)a.sinks * a.dim + (int64_t)j * a.dim;
+        const bool mine = j < sinks && j < w.t.len && w.slot < partial_slots;
 #pragma unroll 1
-      for (int c = 0; c < DP; c += 32) {
-        uint32_t o[32];
-        if (steps) {
-          tmem_ld_32x32b_x32(tmem + lanes + 256u + 128u * half + c, o);
-          tmem_ld_wait();
-        } else {
+        for (int c = 0; c < DP; c += 32) {
+          uint32_t o[32];
+          if (steps) {
+            tmem_ld_32x32b_x32(acc + c, o);
+            tmem_ld_wait();
+          } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
-        }
-        if (mine) {
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          if (mine) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            if (c + e < a.dim) {
-              float x[8];
+            for (int e = 0; e < 32; e += 8) {
+              if (c + e < a.dim) {
+                float x[8];
 #pragma unroll
-              for (int y = 0; y < 8; ++y) x[y] = __uint_as_float(o[e + y]) * f;
-              if (part)
+                for (int y = 0; y < 8; ++y) x[y] = __uint_as_float(o[e + y]) * f;
                 store8(pp + c + e, x);
-              else
-                store8(po + c + e, x);
+              }
             }
           }
         }
+      }
+      if (!w.sink_only) {
+        // (rows of sink keys among these are written again, in full, by window_sink_kernel)
+        store_rows<DP>(acc, f, steps == 0, (half ? dk : dv) + (((int64_t)w.t.b + row0) * a.kv_heads + w.kv) * a.dim,
+                       (int64_t)a.kv_heads * a.dim, w.t.len - row0, a.dim, base + SM::STAGE + warp * 4096, lane);
+      }
+      if (steps) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_empty);
       }
       tc_fence_before();
     }
   } else if (warp == 8) {
-    uint32_t pos = 0, kv_ph = 1, kv_loads = 0;
+    Cursor<SM::SLOTS> cur;
+    uint32_t loads = 0, raw_phase = 0;
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       const DkvItem w = dkv_item(a, item, sink_items, lane);
-      const int steps = group * w.nq;
-      for (int n = 0; n < steps && ok; ++n) {
-        const int h = w.kv * group + n / w.nq, token = w.t.b + (w.q_lo + n % w.nq) * kAttnTile;
-        for (int x = 0; x < 2 && ok; ++x) {
-          ok = mbar_wait(ring.empty_bar(pos), ring.empty_parity(pos), abort_flag, err, kErrDkv);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (lane == 0) {
-            mbar_expect_tx(ring.full_bar(pos), SM::TILE);
-            load_tile<DP>(ring.slot(pos), x ? &tmDO : &tmQ, token, h, ring.full_bar(pos));
-          }
-          ++pos;
-          if (n == 0 && x == 0) {
-            // keys and values once the item before has done with its own
-            ok = mbar_wait(done, kv_ph, abort_flag, err, kErrDkv);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            kv_ph ^= 1;
-            ++kv_loads;
-            if (lane == 0) {
-              mbar_expect_tx(kv_full, 2 * SM::TILE);
-              load_tile<DP>(base, &tmK, w.t.b + w.t.p0, w.kv, kv_full);
-              load_tile<DP>(base + SM::TILE, &tmV, w.t.b + w.t.p0, w.kv, kv_full);
+      if (lane == 0) {
+        const int steps = group * w.nq;
+        int head = w.kv * group, tile = w.q_lo;
+        for (int n = 0; n < steps && ok; ++n) {
+          const int at = tile * kAttnTile;
+          for (int x = 0; x < 2 && ok; ++x) {
+            if (n == 0) {
+              // K before the first queries, V before the first output gradients
+              ok = mbar_wait_in(x ? v_empty : k_empty, (loads & 1) ^ 1, abort_flag, err, kErrDkv);
+              if (!ok) break;
+              mbar_expect_tx(x ? v_full : k_full, SM::TILE);
+              load_tile<DP>(base + x * SM::TILE, x ? &tmV : &tmK, w.t.b + w.t.p0, w.kv, x ? v_full : k_full);
             }
+            ok = mbar_wait_in(cur.empty(ring), cur.phase ^ 1, abort_flag, err, kErrDkv);
+            if (!ok) break;
+            fill_slot<DP>(ring, cur, x ? &tmDO : &tmQ, w.t.b + at, head, w.t.len - at, raw_phase);
+            cur.advance();
           }
+          if (++tile == w.q_lo + w.nq) tile = w.q_lo, ++head;
         }
+        if (steps) ++loads;
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+    }
+    if (lane == 0) {
+      drain_ring(ring, cur, raw_phase);
+      if (loads) {
+        drain_wait(k_full, (loads - 1) & 1);
+        drain_wait(v_full, (loads - 1) & 1);
       }
     }
-    for (uint32_t k = pos > SM::SLOTS ? pos - SM::SLOTS : 0; k < pos; ++k)
-      drain_wait(ring.full_bar(k), ring.full_parity(k));
-    if (kv_loads) drain_wait(kv_full, (kv_loads - 1) & 1);
-  } else {
-    uint32_t pos = 0, kv_ph = 0, step = 0;
+    __syncwarp();
+  } else if (warp == 9) {
+    Cursor<SM::SLOTS> sc;  // the next S^T's query tile; its output gradients follow it
+    uint32_t kv_ph = 0, step = 0;
+    const uint32_t tm = warp_uniform(tmem);
+    DkvItem upcoming = dkv_item(a, blockIdx.x, sink_items, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const DkvItem w = dkv_item(a, item, sink_items, lane);
-      const int steps = group * w.nq;
-      if (steps == 0) continue;
-      ok = __all_sync(0xffffffffu, mbar_wait(kv_full, kv_ph, abort_flag, err, kErrDkv));
-      if (!ok) break;
-      kv_ph ^= 1;
-      // x = 0: S^T of step n from its queries; 1: dP^T from its output gradients
-      auto issue = [&](int n, int x) {
-        const uint32_t k = pos + 2 * n + x;
-        ok = mbar_wait(ring.full_bar(k), ring.full_parity(k), abort_flag, err, kErrDkv);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return false;
-        const int valid = w.t.len - (w.q_lo + n % w.nq) * kAttnTile;
-        if (valid < kAttnTile) clear_rows<DP>(ring.slot(k), valid, lane);
+      const int steps = warp_uniform(group * upcoming.nq);
+      if (steps == 0) {
+        if (item + (int)gridDim.x < items) upcoming = dkv_item(a, item + gridDim.x, sink_items, lane);
+        continue;
+      }
+      Cursor<SM::SLOTS> pc = sc.next(), vc = pc, kc = sc;  // the next dP^T's, dV's and dK's tile
+      auto issue_s = [&](int n) {
+        if (!mbar_wait_warp(sc.full(ring), sc.phase, abort_flag, err, kErrDkv)) return false;
         tc_fence_after();
-        if (lane == 0) {
-          mma_abt<DP>(tmem + 128u * x, base + x * SM::TILE, ring.slot(k));
-          umma_commit<1>(x ? dp_full : s_full);
-        }
-        __syncwarp();
+        mma_abt<DP>(tm, base, sc.data(ring));
+        umma_commit_warp(s_full);
+        if (n == steps - 1) umma_commit_warp(k_empty);
+        sc.skip(2);
         return true;
       };
-      if (!issue(0, 0) || !issue(0, 1)) break;
+      auto issue_dp = [&]() {
+        if (!mbar_wait_warp(pc.full(ring), pc.phase, abort_flag, err, kErrDkv)) return false;
+        tc_fence_after();
+        mma_abt<DP>(tm + 128u, base + SM::TILE, pc.data(ring));
+        umma_commit_warp(dp_full);
+        pc.skip(2);
+        return true;
+      };
+      ok = mbar_wait_warp(k_full, kv_ph, abort_flag, err, kErrDkv) && issue_s(0) &&
+           mbar_wait_warp(v_full, kv_ph, abort_flag, err, kErrDkv) && issue_dp();
+      kv_ph ^= 1;
+      if (item + (int)gridDim.x < items) upcoming = dkv_item(a, item + gridDim.x, sink_items, lane);
       for (int n = 0; n < steps && ok; ++n, ++step) {
-        ok = __all_sync(0xffffffffu, mbar_wait(p_full, step & 1, abort_flag, err, kErrDkv));
-        if (!ok) break;
+        if (!(ok = mbar_wait_warp(p_full, step & 1, abort_flag, err, kErrDkv))) break;
         tc_fence_after();
-        if (lane == 0) {
-          mma_ab<DP>(tmem + 256u, tmem, 64, ring.slot(pos + 2 * n + 1), n > 0);
-          umma_commit<1>(ring.empty_bar(pos + 2 * n + 1));
-        }
-        __syncwarp();
-        if (n + 1 < steps && !issue(n + 1, 0)) break;
-        ok = __all_sync(0xffffffffu, mbar_wait(ds_full, step & 1, abort_flag, err, kErrDkv));
-        if (!ok) break;
+        mma_ab<DP>(tm + 256u, tm, 64, vc.data(ring), n > 0);
+        umma_commit_warp(vc.empty(ring));
+        vc.skip(2);
+        if (n + 1 < steps && !(ok = issue_s(n + 1))) break;
+        if (!(ok = mbar_wait_warp(ds_full, step & 1, abort_flag, err, kErrDkv))) break;
         tc_fence_after();
-        if (lane == 0) {
-          mma_ab<DP>(tmem + 384u, tmem + 128u, 64, ring.slot(pos + 2 * n), n > 0);
-          umma_commit<1>(ring.empty_bar(pos + 2 * n));
-        }
-        __syncwarp();
-        if (n + 1 < steps && !issue(n + 1, 1)) break;
+        mma_ab<DP>(tm + 384u, tm + 128u, 64, kc.data(ring), n > 0);
+        umma_commit_warp(kc.empty(ring));
+        kc.skip(2);
+        if (n + 1 < steps) ok = issue_dp();
       }
-      if (!ok) break;
-      if (lane == 0) umma_commit<1>(done);
-      __syncwarp();
-      pos += 2 * steps;
+      if (ok) umma_commit_warp(done);
     }
     if (lane == 0) {
       umma_commit<1>(drain);
       drain_wait(drain, 0);
     }
     __syncwarp();
+  } else if (warp == 10) {
+    Cursor<SM::SLOTS> cur;
+    uint32_t raw_phase = 0;
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const DkvItem w = dkv_item(a, item, sink_items, lane);
+      const int valid = w.t.len - (w.q_lo + w.nq - 1) * kAttnTile;  // of a head's last query tile
+      if (w.nq > 0)
+        for (int h = 0; h < group; ++h) {
+          cur.skip(2 * w.nq - 2);
+          for (int x = 0; x < 2; ++x) {
+            if (valid < kAttnTile && ok)
+              ok = clear_slot<DP>(ring, cur, valid, raw_phase, lane, abort_flag, err, kErrDkv);
+            cur.advance();
+          }
+        }
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -729,16 +736,16 @@ template <int DP>
 cudaError_t run_backward(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                          const CUtensorMap& dout, const AttnGrad& g, int* err, int sms, cudaStream_t st) {
   const int64_t tiles = attn_max_tiles(a.n, a.n_seqs, kAttnTile);
-  cudaError_t e = op_smem_limit<window_dq_kernel<DP>>((int)DqSmem<DP>::BYTES);
-  if (e == cudaSuccess) e = op_smem_limit<window_dkv_kernel<DP>>((int)DkvSmem<DP>::BYTES);
+  cudaError_t e = op_smem_limit<window_dq_kernel<DP>>((int)GradSmem<DP>::BYTES);
+  if (e == cudaSuccess) e = op_smem_limit<window_dkv_kernel<DP>>((int)GradSmem<DP>::BYTES);
   if (e != cudaSuccess) return e;
   int64_t grid = tiles * a.heads;
-  e = op_launch(window_dq_kernel<DP>, dim3((unsigned)(grid < sms ? grid : sms)), dim3(kThreads), DqSmem<DP>::BYTES, st,
+  e = op_launch(window_dq_kernel<DP>, dim3((unsigned)(grid < sms ? grid : sms)), dim3(kThreads), GradSmem<DP>::BYTES, st,
                 1, a, q, k, v, dout, g.dq, err);
   if (e != cudaSuccess) return e;
   grid = (tiles + g.partial_slots) * a.kv_heads;
   return op_launch(window_dkv_kernel<DP>, dim3((unsigned)(grid < sms ? grid : sms)), dim3(kThreads),
-                   DkvSmem<DP>::BYTES, st, 1, a, q, k, v, dout, g.dk, g.dv, g.partial, g.partial_slots, err);
+                   GradSmem<DP>::BYTES, st, 1, a, q, k, v, dout, g.dk, g.dv, g.partial, g.partial_slots, err);
 }
 
 }  // namespace
