@@ -13,13 +13,14 @@
 //                   query: S from TMEM, P (bf16) back to TMEM over S;
 //   warp 8          TMA: the two query tiles, then key and value tiles into a
 //                   ring;
-//   warp 9          tcgen05.mma: S = Q K^T from shared memory, O += P V with P
-//                   from TMEM. The two tiles alternate, so that one tile's
-//                   products run while the other's softmax does. The tensor
-//                   core queues little, so whatever this warp does between
-//                   products leaves it idle: the next item is worked out while
-//                   the softmax of the first tiles runs;
-//   warp 10         (11 idles) clears the rows of a sample's last value tile that belong to
+//   warps 9, 10     tcgen05.mma of the first and of the second tile: S = Q K^T
+//                   from shared memory, O += P V with P from TMEM. One tile's
+//                   products run while the other's softmax does. A warp issues
+//                   a product in 400 cycles and spends as much on the barriers
+//                   around it, a product runs for 520: one warp for both tiles
+//                   left the tensor core idle half the time (174 us for 16360
+//                   tokens of 16 heads of 128, window 1024);
+//   warp 11         clears the rows of a sample's last value tile that belong to
 //                   other samples.
 // TMEM: S0 | S1 | O0 | O1, 128 columns each.
 //
@@ -42,8 +43,8 @@ struct FwdSmem {
   static constexpr uint32_t RING = 2 * TILE;
   static constexpr uint32_t STAGE = RING + SLOTS * TILE;  // 4 KB a softmax warp, for the results on their way out
   static constexpr uint32_t BARS = STAGE + 8 * 4096;
-  // full[SLOTS], empty[SLOTS], raw[SLOTS], q full, q empty, s full[2], p full[2], o full[2], drain
-  static constexpr int NBARS = 3 * SLOTS + 9;
+  // full[SLOTS], empty[SLOTS], raw[SLOTS], q full, q empty, s full[2], p full[2], o full[2], drain[2]
+  static constexpr int NBARS = 3 * SLOTS + 10;
   static constexpr uint32_t BYTES = BARS + NBARS * 8 + 16;
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
@@ -122,8 +123,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    ring.init();
-    mbar_init(q_full, 1), mbar_init(q_empty, 1), mbar_init(drain, 1);
+    ring.init(2);
+    mbar_init(q_full, 1), mbar_init(q_empty, 2), mbar_init(drain, 1), mbar_init(drain + 8, 1);
     for (int s = 0; s < 2; ++s) mbar_init(s_full + 8 * s, 1), mbar_init(p_full + 8 * s, 128), mbar_init(o_full + 8 * s, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -165,10 +166,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!tile_full(a, p0, k0)) {
           // key k0 + col is visible for col <= last and (col >= first or col < sink); past the sinks' columns
           // of a tile that is there for them alone no score has been formed
-          const int last = w.k.whole(s, n) ? i - k0 : min(i - k0, sink_columns(a) - 1);
-          const int first = i - a.window + 1 - k0, sink = a.sinks - k0;
-          mask_tile(ts, 4, [&](int c) { return block_full(a, row0, k0 + 32 * c); },
-                    [&](int col) { return col > last || (col < first && col >= sink); });
+          const int end = (w.k.whole(s, n) ? i - k0 : min(i - k0, sink_columns(a) - 1)) + 1;
+          const int first = i - a.window + 1 - k0, sink = min(a.sinks - k0, end);
+          mask_tile(ts, 4, [&](int c) { return bit_range(first - 32 * c, end - 32 * c) | bit_range(0, sink - 32 * c); });
         }
         uint32_t v[4][32];
 #pragma unroll
@@ -270,84 +270,64 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (loads) drain_wait(q_full, (loads - 1) & 1);
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp < 11) {
     // ---- MMA ----
     Cursor<SM::SLOTS> cur;
-    uint32_t q_ph = 0, p_ph0 = 0, p_ph1 = 0;
-    const uint32_t tm = warp_uniform(tmem);
-    const int few = sink_columns(a);
+    uint32_t q_ph = 0, p_ph = 0;
+    const int s = warp_uniform(warp - 9), few = sink_columns(a);
+    const uint32_t ts = warp_uniform(tmem) + 128u * s, to = ts + 256u, qt = base + s * SM::TILE;
+    const uint32_t sf = s_full + 8 * s, pf = p_full + 8 * s, of = o_full + 8 * s;
     FwdItem next = fwd_item(a, blockIdx.x, units, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const FwdItem w = next;
-      const int steps = warp_uniform(w.k.steps), a0 = warp_uniform(w.k.a0), a1 = warp_uniform(w.k.a1),
-                b0 = warp_uniform(w.k.b0), b1 = warp_uniform(w.k.b1), z0 = warp_uniform((int)w.k.z0),
-                z1 = warp_uniform((int)w.k.z1);
-      const int last0 = b0 >= a0 ? b0 : z0 - 1, last1 = b1 >= a1 ? b1 : z1 - 1;
+      const int steps = warp_uniform(next.k.steps), first = warp_uniform(s ? next.k.a1 : next.k.a0),
+                last = warp_uniform(s ? next.k.b1 : next.k.b0), sink = warp_uniform((int)(s ? next.k.z1 : next.k.z0));
       if (steps == 0 || !(ok = mbar_wait_warp(q_full, q_ph, abort_flag, err, kErrForward))) {
         if (item + (int)gridDim.x < items) next = fwd_item(a, item + gridDim.x, units, lane);
         continue;
       }
       q_ph ^= 1;
-      bool pend0 = false, pend1 = false, begun0 = false, begun1 = false;
+      const int end = last >= first ? last : sink - 1;  // the last step that this tile uses
+      bool pend = false, whole = false, begun = false;
       Cursor<SM::SLOTS> vc;  // the value tile of the step before
-      // step n issues O += P V of tile n - 1 and S of tile n, for the one query tile and then for the other
+      // step n issues O += P V of tile n - 1 and S of tile n. Tiles that only the other warp uses are waited for
+      // and released all the same: a slot's release counts both warps once for each of its fills.
       for (int n = 0; n <= steps; ++n) {
-        const bool more = n < steps;
-        const bool whole0 = n >= a0 && n <= b0, whole1 = n >= a1 && n <= b1;
-        const bool use0 = more && (whole0 || (n == 0 && z0)), use1 = more && (whole1 || (n == 0 && z1));
-        const bool was0 = n - 1 >= a0 && n - 1 <= b0, was1 = n - 1 >= a1 && n - 1 <= b1;
-        if (n > 0 && !(ok = mbar_wait_warp(vc.full(ring), vc.phase, abort_flag, err, kErrForward))) break;
-        if (pend0) {
-          if (!(ok = mbar_wait_warp(p_full, p_ph0, abort_flag, err, kErrForward))) break;
-          p_ph0 ^= 1;
+        if (n > 0) {
+          if (!(ok = mbar_wait_warp(vc.full(ring), vc.phase, abort_flag, err, kErrForward))) break;
+          if (pend) {
+            if (!(ok = mbar_wait_warp(pf, p_ph, abort_flag, err, kErrForward))) break;
+            p_ph ^= 1;
+            tc_fence_after();
+            if (whole)
+              mma_ab<DP>(to, ts, 32, vc.data(ring), begun);
+            else
+              mma_ab_few<DP>(to, ts, 32, vc.data(ring), begun, few);
+            if (n - 1 == end) umma_commit_warp(of);
+            begun = true;
+          }
+          umma_commit_warp(vc.empty(ring));
+        }
+        if (n == steps) break;
+        if (!(ok = mbar_wait_warp(cur.full(ring), cur.phase, abort_flag, err, kErrForward))) break;
+        whole = n >= first && n <= last;
+        pend = whole || (n == 0 && sink);
+        if (pend) {
           tc_fence_after();
-          if (was0)
-            mma_ab<DP>(tm + 256u, tm, 32, vc.data(ring), begun0);
-          else
-            mma_ab_few<DP>(tm + 256u, tm, 32, vc.data(ring), begun0, few);
-          if (n - 1 == last0) umma_commit_warp(o_full);
-          begun0 = true;
+          mma_abt<DP>(ts, qt, cur.data(ring), whole ? kAttnTile : few);
+          umma_commit_warp(sf);
         }
-        if (more && !(ok = mbar_wait_warp(cur.full(ring), cur.phase, abort_flag, err, kErrForward))) break;
-        tc_fence_after();
-        if (use0) {
-          mma_abt<DP>(tm, base, cur.data(ring), whole0 ? kAttnTile : few);
-          umma_commit_warp(s_full);
-        }
-        pend0 = use0;
-        if (pend1) {
-          if (!(ok = mbar_wait_warp(p_full + 8, p_ph1, abort_flag, err, kErrForward))) break;
-          p_ph1 ^= 1;
-          tc_fence_after();
-          if (was1)
-            mma_ab<DP>(tm + 384u, tm + 128u, 32, vc.data(ring), begun1);
-          else
-            mma_ab_few<DP>(tm + 384u, tm + 128u, 32, vc.data(ring), begun1, few);
-          if (n - 1 == last1) umma_commit_warp(o_full + 8);
-          begun1 = true;
-        }
-        if (n > 0) umma_commit_warp(vc.empty(ring));
-        if (use1) {
-          mma_abt<DP>(tm + 128u, base + SM::TILE, cur.data(ring), whole1 ? kAttnTile : few);
-          umma_commit_warp(s_full + 8);
-        }
-        pend1 = use1;
-        if (more) {
-          umma_commit_warp(cur.empty(ring));
-          if (n == steps - 1) umma_commit_warp(q_empty);
-          cur.advance();
-          vc = cur;
-          cur.advance();
-        }
+        umma_commit_warp(cur.empty(ring));
+        if (n == steps - 1) umma_commit_warp(q_empty);
+        cur.advance();
+        vc = cur;
+        cur.advance();
         if (n == 0 && item + (int)gridDim.x < items) next = fwd_item(a, item + gridDim.x, units, lane);
       }
     }
-    if (lane == 0) {
-      umma_commit<1>(drain);
-      drain_wait(drain, 0);
-    }
+    umma_commit_warp(drain + 8 * s);
+    if (lane == 0) drain_wait(drain + 8 * s, 0);
     __syncwarp();
-  } else if (warp == 10) {
+  } else {
     // ---- rows of other samples ----
     Cursor<SM::SLOTS> cur;
     uint32_t raw_phase = 0;

@@ -150,27 +150,34 @@ __device__ __forceinline__ bool tile_full(const AttnArgs& a, int q0, int k0) {
   return k0 + kAttnTile - 1 <= q0 && (q0 + kAttnTile - 1 - k0 < a.window || k0 + kAttnTile - 1 < a.sinks);
 }
 
-// The same of 32 queries from q0 and 32 keys from k0: all of the pairs.
-__device__ __forceinline__ bool block_full(const AttnArgs& a, int q0, int k0) {
-  return k0 + 31 <= q0 && (q0 + 31 - k0 < a.window || k0 + 31 < a.sinks);
+// Bits [lo, hi) of a word, the bounds clamped to [0, 32].
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  lo = max(lo, 0);
+  hi = min(hi, 32);
+  return hi <= lo ? 0u : (0xffffffffu >> (32 - (hi - lo))) << lo;
 }
 
-// Masks a tile of scores in TMEM: -infinity where `hidden(col)` in the 32-column
-// blocks for which `full(block)` does not hold; blocks first .. last - 1, whose
-// columns count from `taddr` on. A loop of its own over the few tiles at a
-// sample's and a window's edges: masks woven into the unrolled arithmetic made
-// it so long that fetching its instructions cost 4000 cycles a tile.
-template <typename F, typename H>
-__device__ __forceinline__ void mask_tile(uint32_t taddr, int blocks, F full, H hidden) {
+// Masks a tile of scores in TMEM: -infinity in column 32 c + j of block c where
+// bit j of seen(c) is 0. A loop of its own over the few tiles at a sample's and
+// a window's edges: masks woven into the unrolled arithmetic made it so long
+// that fetching its instructions cost 4000 cycles a tile.
+template <typename F>
+__device__ __forceinline__ void mask_tile(uint32_t taddr, int blocks, F seen) {
 #pragma unroll 1
   for (int c = 0; c < blocks; ++c) {
-    if (full(c)) continue;
+    const uint32_t m = seen(c);
+    if (__all_sync(0xffffffffu, m == 0xffffffffu)) continue;
     uint32_t v[32];
-    tmem_ld_32x32b_x32(taddr + 32 * c, v);
-    tmem_ld_wait();
+    if (__any_sync(0xffffffffu, m != 0u)) {
+      tmem_ld_32x32b_x32(taddr + 32 * c, v);
+      tmem_ld_wait();
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = 0xff800000u;
+    }
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      if (hidden(32 * c + j)) v[j] = 0xff800000u;
+      if (!(m >> j & 1u)) v[j] = 0xff800000u;
     tmem_st_32x32b_x32(taddr + 32 * c, v);
   }
   tmem_st_wait();
@@ -196,8 +203,8 @@ template <int SLOTS>
 struct Ring {
   uint32_t data, full, empty, raw, slot_bytes;
   static constexpr int BARS = 3 * SLOTS;
-  __device__ __forceinline__ void init() const {
-    for (int i = 0; i < SLOTS; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1), mbar_init(raw + 8 * i, 1);
+  __device__ __forceinline__ void init(int users) const {  // MMA warps that release a slot
+    for (int i = 0; i < SLOTS; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, users), mbar_init(raw + 8 * i, 1);
   }
 };
 

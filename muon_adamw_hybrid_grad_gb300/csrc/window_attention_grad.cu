@@ -67,8 +67,8 @@ __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant
 
 // ---- dQ ----
 // Warps 0-7: a thread to a query and half of a tile's keys (warps 0-3 the
-// first 64, 4-7 the others); warp 8: TMA; warp 9: tcgen05.mma (one thread);
-// warp 10: clears the key and value rows of other samples.
+// first 64, 4-7 the others); warp 8: TMA; warps 9 and 10: tcgen05.mma, the one S
+// and dQ, the other dP; warp 11: clears the key and value rows of other samples.
 // TMEM: S of even steps | S of odd steps | dP | dQ. dS (bf16) overwrites the S
 // it came from, each half in the first 32 of its own 64 columns. S of the next
 // tile is formed while the threads work on this one's, and dP of the next as
@@ -87,7 +87,7 @@ struct GradSmem {
   static constexpr uint32_t STAGE = DP == 128 ? TILE : OWN;    // 4 KB to each of 8 warps
   static constexpr uint32_t BARS = DP == 128 ? OWN : OWN + 8 * 4096;
   // full[SLOTS], empty[SLOTS], raw[SLOTS], then each kernel's own
-  static constexpr int NBARS = 3 * SLOTS + 12;
+  static constexpr int NBARS = 3 * SLOTS + 13;
   static constexpr uint32_t BYTES = BARS + NBARS * 8 + 16;
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
@@ -125,17 +125,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, bars + SM::SLOTS * 16, SM::TILE};
   const uint32_t own = bars + 3 * SM::SLOTS * 8, q_full = own, q_empty = own + 8, do_full = own + 16,
                  do_empty = own + 24, s_full = own + 32, dp_full = own + 48, dp_empty = own + 56, ds_full = own + 64,
-                 dq_full = own + 72, drain = own + 80;
+                 dq_full = own + 80, drain = own + 88;
   if (base & 1023u) {  // the swizzle's phase is that of the address
     if (threadIdx.x == 0) atomicCAS(err, 0, kErrAlign);
     return;
   }
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    ring.init();
+    ring.init(1);
     mbar_init(q_full, 1), mbar_init(q_empty, 1), mbar_init(do_full, 1), mbar_init(do_empty, 8);
     mbar_init(s_full, 1), mbar_init(s_full + 8, 1), mbar_init(dp_full, 1), mbar_init(dp_empty, 256);
-    mbar_init(ds_full, 256), mbar_init(dq_full, 1), mbar_init(drain, 1);
+    mbar_init(ds_full, 256), mbar_init(ds_full + 8, 256), mbar_init(dq_full, 1), mbar_init(drain, 1), mbar_init(drain + 8, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 9) tmem_alloc<1>(smem_u32(tmem_slot), 512);
@@ -174,12 +174,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_ph ^= 1u << slot;
         tc_fence_after();
         if (!tile_full(a, w.t.p0, k0 - 64 * half)) {
-          // key k0 + col is visible for col <= last and (col >= first or col < sink); past the sinks' columns of
+          // key k0 + col is visible for col < end and (col >= first or col < sink); past the sinks' columns of
           // a tile that is there for them alone no score has been formed
-          const int last = w.k.sink && n == 0 ? min(i - k0, few - 64 * half - 1) : i - k0;
-          const int first = i - k0 - a.window + 1, sink = a.sinks - k0;
-          mask_tile(ts, 2, [&](int c) { return block_full(a, row0, k0 + 32 * c); },
-                    [&](int col) { return col > last || (col < first && col >= sink); });
+          const int end = w.k.sink && n == 0 ? min(i - k0 + 1, few - 64 * half) : i - k0 + 1;
+          const int first = i - k0 - a.window + 1, sink = min(a.sinks - k0, end);
+          mask_tile(ts, 2, [&](int c) { return bit_range(first - 32 * c, end - 32 * c) | bit_range(0, sink - 32 * c); });
         }
         uint32_t p[2][32], g[2][32], ds[32];
         tmem_ld_32x32b_x32(ts, p[0]);
@@ -208,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_32x32b_x32(ts, ds);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(ds_full);
+        mbar_arrive(ds_full + 8 * slot);
       }
       if (!ok) break;
       if (item + (int)gridDim.x < items) next = dq_item(a, item + gridDim.x, lane);
@@ -264,46 +263,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 9) {
+    // S of the next steps, dQ
     Cursor<SM::SLOTS> sc;  // the next S's key tile
-    uint32_t q_ph = 0, step = 0;
+    uint32_t q_ph = 0, ds_ph = 0;  // ds_ph: a bit per S slot
     const uint32_t tm = warp_uniform(tmem);
     DqItem next = dq_item(a, blockIdx.x, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const DqItem w = next;
-      const int steps = warp_uniform(w.steps), sink = warp_uniform((int)w.k.sink);
+      const int steps = warp_uniform(next.steps), sink = warp_uniform((int)next.k.sink);
       if (steps == 0) {
         if (item + (int)gridDim.x < items) next = dq_item(a, item + gridDim.x, lane);
         continue;
       }
-      const int cols0 = sink ? few : kAttnTile;
-      Cursor<SM::SLOTS> pc = sc.next(), qc = sc;  // the next dP's value tile, the next dQ's key tile
+      Cursor<SM::SLOTS> qc = sc;  // the next dQ's key tile
       auto issue_s = [&](int n) {
         if (!mbar_wait_warp(sc.full(ring), sc.phase, abort_flag, err, kErrDq)) return false;
         tc_fence_after();
-        mma_abt<DP>(tm + 128u * (n & 1), base, sc.data(ring), n ? kAttnTile : cols0);
+        mma_abt<DP>(tm + 128u * (n & 1), base, sc.data(ring), n == 0 && sink ? few : kAttnTile);
         umma_commit_warp(s_full + 8 * (n & 1));
         if (n == steps - 1) umma_commit_warp(q_empty);
         sc.skip(2);
         return true;
       };
-      auto issue_dp = [&](int n) {
-        if (!mbar_wait_warp(pc.full(ring), pc.phase, abort_flag, err, kErrDq)) return false;
-        tc_fence_after();
-        mma_abt<DP>(tm + 256u, base + SM::TILE, pc.data(ring), n ? kAttnTile : cols0);
-        umma_commit_warp(dp_full);
-        umma_commit_warp(pc.empty(ring));
-        pc.skip(2);
-        return true;
-      };
-      ok = mbar_wait_warp(q_full, q_ph, abort_flag, err, kErrDq) && issue_s(0) &&
-           mbar_wait_warp(do_full, q_ph, abort_flag, err, kErrDq) && issue_dp(0) && (steps == 1 || issue_s(1));
+      ok = mbar_wait_warp(q_full, q_ph, abort_flag, err, kErrDq) && issue_s(0) && (steps == 1 || issue_s(1));
       q_ph ^= 1;
       if (item + (int)gridDim.x < items) next = dq_item(a, item + gridDim.x, lane);
-      for (int n = 0; n < steps && ok; ++n, ++step) {
-        // dP of the next step once this one's has been read
-        ok = mbar_wait_warp(dp_empty, step & 1, abort_flag, err, kErrDq) && (n + 1 == steps || issue_dp(n + 1)) &&
-             mbar_wait_warp(ds_full, step & 1, abort_flag, err, kErrDq);
-        if (!ok) break;
+      for (int n = 0; n < steps && ok; ++n) {
+        // (a barrier to each slot of S: the threads need nothing of this warp for the step after, so that they
+        // may be through with it before this wait, and one barrier's phases would have passed twice)
+        const uint32_t slot = n & 1;
+        if (!(ok = mbar_wait_warp(ds_full + 8 * slot, ds_ph >> slot & 1, abort_flag, err, kErrDq))) break;
+        ds_ph ^= 1u << slot;
         tc_fence_after();
         if (n > 0 || !sink)
           mma_ab<DP>(tm + 384u, tm + 128u * (n & 1), 64, qc.data(ring), n > 0);
@@ -315,12 +304,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok) umma_commit_warp(dq_full);
     }
-    if (lane == 0) {
-      umma_commit<1>(drain);
-      drain_wait(drain, 0);
-    }
+    umma_commit_warp(drain);
+    if (lane == 0) drain_wait(drain, 0);
     __syncwarp();
   } else if (warp == 10) {
+    // dP, once the threads have read the one before
+    Cursor<SM::SLOTS> pc;  // a key tile, then its value tile
+    uint32_t q_ph = 0, step = 0;
+    const uint32_t tm = warp_uniform(tmem);
+    DqItem next = dq_item(a, blockIdx.x, lane);
+    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+      const int steps = warp_uniform(next.steps), sink = warp_uniform((int)next.k.sink);
+      if (item + (int)gridDim.x < items) next = dq_item(a, item + gridDim.x, lane);
+      if (steps == 0) continue;
+      ok = mbar_wait_warp(do_full, q_ph, abort_flag, err, kErrDq);
+      q_ph ^= 1;
+      for (int n = 0; n < steps && ok; ++n, ++step) {
+        pc.advance();
+        // (parity of the step before; the very first passes)
+        ok = mbar_wait_warp(dp_empty, (step & 1) ^ 1, abort_flag, err, kErrDq) &&
+             mbar_wait_warp(pc.full(ring), pc.phase, abort_flag, err, kErrDq);
+        if (!ok) break;
+        tc_fence_after();
+        mma_abt<DP>(tm + 256u, base + SM::TILE, pc.data(ring), n == 0 && sink ? few : kAttnTile);
+        umma_commit_warp(dp_full);
+        umma_commit_warp(pc.empty(ring));
+        pc.advance();
+      }
+    }
+    umma_commit_warp(drain + 8);
+    if (lane == 0) drain_wait(drain + 8, 0);
+    __syncwarp();
+  } else {
     Cursor<SM::SLOTS> cur;
     uint32_t raw_phase = 0;
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
@@ -345,8 +360,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Scores are formed transposed, S^T = K Q^T and dP^T = V dO^T, so that P^T and
 // dS^T stand in TMEM as the left operands of dV += P^T dO and dK += dS^T Q.
 // Warps 0-7: a thread to a key and half of a tile's queries; warp 8: TMA;
-// warp 9: tcgen05.mma (one thread); warp 10: clears rows of Q and dO that belong
-// to other samples. TMEM: S^T | dP^T | dV | dK; P^T overwrites S^T and dS^T
+// warps 9 and 10: tcgen05.mma, the one dV and then the next step's S^T, the other
+// dK and the next dP^T; warp 11: clears rows of Q and dO that belong to other
+// samples. TMEM: S^T | dP^T | dV | dK; P^T overwrites S^T and dS^T
 // dP^T, each half in the first 32 of its own 64 columns. While the threads form
 // P^T of a step the tensor core runs the step before's dK and this one's dP^T;
 // while they form dS^T it runs dV and the next step's S^T. Results leave through
@@ -420,10 +436,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    ring.init();
+    ring.init(2);
     mbar_init(k_full, 1), mbar_init(k_empty, 1), mbar_init(v_full, 1), mbar_init(v_empty, 8);
     mbar_init(s_full, 1), mbar_init(dp_full, 1), mbar_init(p_full, 256), mbar_init(ds_full, 256);
-    mbar_init(stat_full, 256), mbar_init(done, 1), mbar_init(drain, 1);
+    mbar_init(stat_full, 256), mbar_init(done, 2), mbar_init(drain, 1), mbar_init(drain + 8, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 9) tmem_alloc<1>(smem_u32(tmem_slot), 512);
@@ -475,11 +491,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (!tile_full(a, q0, w.t.p0)) {
-          // query q0 + 64 half + col sees key j for col >= from and col <= to
-          const int qh = q0 + 64 * half, from = j - qh;
-          const int to = j < a.sinks ? kAttnTile : (int)min((int64_t)from + a.window - 1, (int64_t)kAttnTile);
-          mask_tile(ts, 2, [&](int c) { return block_full(a, qh + 32 * c, row0); },
-                    [&](int col) { return col < from || col > to; });
+          // query q0 + 64 half + col sees key j for col >= from and col < to
+          const int from = j - q0 - 64 * half;
+          const int to = j < a.sinks ? kAttnTile : (int)min((int64_t)from + a.window, (int64_t)kAttnTile);
+          mask_tile(ts, 2, [&](int c) { return bit_range(from - 32 * c, to - 32 * c); });
         }
         uint32_t p[2][32], g[2][32], r[32];
         tmem_ld_32x32b_x32(ts, p[0]);
@@ -615,61 +630,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
-    Cursor<SM::SLOTS> sc;  // the next S^T's query tile; its output gradients follow it
+  } else if (warp < 11) {
+    // x = 0: S^T of Q, then dV += P^T dO; x = 1: dP^T of dO, then dK += dS^T Q
+    const int x = warp_uniform(warp - 9);
+    Cursor<SM::SLOTS> cur;  // a step's query tile; its output gradients follow it
     uint32_t kv_ph = 0, step = 0;
-    const uint32_t tm = warp_uniform(tmem);
+    const uint32_t ts = warp_uniform(tmem) + 128u * x, to = ts + 256u, kt = base + x * SM::TILE;
+    const uint32_t formed = x ? dp_full : s_full, ready = x ? ds_full : p_full;
     DkvItem upcoming = dkv_item(a, blockIdx.x, sink_items, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       const int steps = warp_uniform(group * upcoming.nq);
-      if (steps == 0) {
-        if (item + (int)gridDim.x < items) upcoming = dkv_item(a, item + gridDim.x, sink_items, lane);
-        continue;
-      }
-      Cursor<SM::SLOTS> pc = sc.next(), vc = pc, kc = sc;  // the next dP^T's, dV's and dK's tile
-      auto issue_s = [&](int n) {
-        if (!mbar_wait_warp(sc.full(ring), sc.phase, abort_flag, err, kErrDkv)) return false;
-        tc_fence_after();
-        mma_abt<DP>(tm, base, sc.data(ring));
-        umma_commit_warp(s_full);
-        if (n == steps - 1) umma_commit_warp(k_empty);
-        sc.skip(2);
-        return true;
-      };
-      auto issue_dp = [&]() {
-        if (!mbar_wait_warp(pc.full(ring), pc.phase, abort_flag, err, kErrDkv)) return false;
-        tc_fence_after();
-        mma_abt<DP>(tm + 128u, base + SM::TILE, pc.data(ring));
-        umma_commit_warp(dp_full);
-        pc.skip(2);
-        return true;
-      };
-      ok = mbar_wait_warp(k_full, kv_ph, abort_flag, err, kErrDkv) && issue_s(0) &&
-           mbar_wait_warp(v_full, kv_ph, abort_flag, err, kErrDkv) && issue_dp();
-      kv_ph ^= 1;
       if (item + (int)gridDim.x < items) upcoming = dkv_item(a, item + gridDim.x, sink_items, lane);
-      for (int n = 0; n < steps && ok; ++n, ++step) {
-        if (!(ok = mbar_wait_warp(p_full, step & 1, abort_flag, err, kErrDkv))) break;
+      if (steps == 0) continue;
+      ok = mbar_wait_warp(x ? v_full : k_full, kv_ph, abort_flag, err, kErrDkv);
+      kv_ph ^= 1;
+      Cursor<SM::SLOTS> other;  // the second product's right-hand tile, of the step before
+      // step n issues the second product of step n - 1 and the first of step n
+      for (int n = 0; n <= steps && ok; ++n) {
+        const Cursor<SM::SLOTS> qc = cur, oc = cur.next();
+        if (n > 0) {
+          if (!(ok = mbar_wait_warp(other.full(ring), other.phase, abort_flag, err, kErrDkv) &&
+                     mbar_wait_warp(ready, step & 1, abort_flag, err, kErrDkv)))
+            break;
+          ++step;
+          tc_fence_after();
+          mma_ab<DP>(to, ts, 64, other.data(ring), n > 1);
+          umma_commit_warp(other.empty(ring));
+        }
+        if (n == steps) break;
+        const Cursor<SM::SLOTS> c = x ? oc : qc;
+        if (!(ok = mbar_wait_warp(c.full(ring), c.phase, abort_flag, err, kErrDkv))) break;
         tc_fence_after();
-        mma_ab<DP>(tm + 256u, tm, 64, vc.data(ring), n > 0);
-        umma_commit_warp(vc.empty(ring));
-        vc.skip(2);
-        if (n + 1 < steps && !(ok = issue_s(n + 1))) break;
-        if (!(ok = mbar_wait_warp(ds_full, step & 1, abort_flag, err, kErrDkv))) break;
-        tc_fence_after();
-        mma_ab<DP>(tm + 384u, tm + 128u, 64, kc.data(ring), n > 0);
-        umma_commit_warp(kc.empty(ring));
-        kc.skip(2);
-        if (n + 1 < steps) ok = issue_dp();
+        mma_abt<DP>(ts, kt, c.data(ring));
+        umma_commit_warp(formed);
+        umma_commit_warp(c.empty(ring));
+        if (n == steps - 1 && x == 0) umma_commit_warp(k_empty);
+        other = x ? qc : oc;
+        cur.skip(2);
       }
       if (ok) umma_commit_warp(done);
     }
-    if (lane == 0) {
-      umma_commit<1>(drain);
-      drain_wait(drain, 0);
-    }
+    umma_commit_warp(drain + 8 * x);
+    if (lane == 0) drain_wait(drain + 8 * x, 0);
     __syncwarp();
-  } else if (warp == 10) {
+  } else {
     Cursor<SM::SLOTS> cur;
     uint32_t raw_phase = 0;
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {

@@ -506,3 +506,23 @@ def test_wrappers_refuse(ops):
         with pytest.raises(error):
             call()
     ops.check()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_window_attention_many_calls(ops, dim):
+    """A packed batch again and again: no bounded wait runs out, and every call gives the same bits."""
+    import torch
+
+    rng = np.random.default_rng(18)
+    q, k, v, do, cu = attn_case(rng, [513, 250, 1021, 64, 7, 700], 0, 16, 16, dim)
+    how = {"window": 256, "sinks": 8, "cu_seqlens": cu}
+    first = ops.window_attention(q, k, v, **how)
+    grads = ops.window_attention_backward(do, q, k, v, *first, **how)
+    same = torch.ones((), dtype=torch.bool, device="cuda")
+    for _ in range(500):
+        out = ops.window_attention(q, k, v, **how)
+        again = ops.window_attention_backward(do, q, k, v, *out, **how)
+        for a, b in zip((*out, *again), (*first, *grads)):
+            same &= (a == b).all()
+    assert bool(same)
+    ops.check()
