@@ -43,8 +43,8 @@ struct FwdSmem {
   static constexpr uint32_t RING = 2 * TILE;
   static constexpr uint32_t STAGE = RING + SLOTS * TILE;  // 4 KB a softmax warp, for the results on their way out
   static constexpr uint32_t BARS = STAGE + 8 * 4096;
-  // full[SLOTS], empty[SLOTS], raw[SLOTS], q full, q empty, s full[2], p full[2], o full[2], drain[2]
-  static constexpr int NBARS = 3 * SLOTS + 10;
+  // full[SLOTS], empty[SLOTS], raw[SLOTS], q full, q empty, s full[2], p full[2], o full[2], drain[2], turn[SLOTS / 2]
+  static constexpr int NBARS = 3 * SLOTS + 10 + SLOTS / 2;
   static constexpr uint32_t BYTES = BARS + NBARS * 8 + 16;
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = smem_u32(smem), bars = base + SM::BARS;
   Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, bars + SM::SLOTS * 16, SM::TILE};
   const uint32_t q_full = bars + 3 * SM::SLOTS * 8, q_empty = q_full + 8, s_full = q_full + 16, p_full = q_full + 32,
-                 o_full = q_full + 48, drain = q_full + 64;
+                 o_full = q_full + 48, drain = q_full + 64, turn = q_full + 80;
   if (base & 1023u) {  // the swizzle's phase is that of the address
     if (threadIdx.x == 0) atomicCAS(err, 0, kErrAlign);
     return;
@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     ring.init(2);
     mbar_init(q_full, 1), mbar_init(q_empty, 2), mbar_init(drain, 1), mbar_init(drain + 8, 1);
+    for (int i = 0; i < SM::SLOTS / 2; ++i) mbar_init(turn + 8 * i, 1);
     for (int s = 0; s < 2; ++s) mbar_init(s_full + 8 * s, 1), mbar_init(p_full + 8 * s, 128), mbar_init(o_full + 8 * s, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -163,12 +164,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         s_ph ^= 1;
         tc_fence_after();
+        Blocks seen = kAllBlocks;
         if (!tile_full(a, p0, k0)) {
-          // key k0 + col is visible for col <= last and (col >= first or col < sink); past the sinks' columns
-          // of a tile that is there for them alone no score has been formed
-          const int end = (w.k.whole(s, n) ? i - k0 : min(i - k0, sink_columns(a) - 1)) + 1;
-          const int first = i - a.window + 1 - k0, sink = min(a.sinks - k0, end);
-          mask_tile(ts, 4, [&](int c) { return bit_range(first - 32 * c, end - 32 * c) | bit_range(0, sink - 32 * c); });
+          // key k0 + col is visible for col < end and (col >= first or col < sink); past the sinks' columns of
+          // a tile that is there for them alone no score has been formed
+          const int cols = w.k.whole(s, n) ? kAttnTile : sink_columns(a);
+          const int end = min(i - k0 + 1, cols), first = i - a.window + 1 - k0, sink = min(a.sinks - k0, end);
+          seen = key_blocks(a, row0, k0, cols, 4);
+          mask_tile(ts, seen,
+                    [&](int c) { return bit_range(first - 32 * c, end - 32 * c) | bit_range(0, sink - 32 * c); });
         }
         uint32_t v[4][32];
 #pragma unroll
@@ -177,8 +181,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < 4; ++c)
+          if (c >= seen.lo && c < seen.hi) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(v[c][j]));
+            for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(v[c][j]));
+          }
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
         const bool grow = mt > m + 8.f;
         if (__any_sync(0xffffffffu, grow)) {
@@ -199,21 +205,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         any = true;
         const float shift = m == -INFINITY ? 0.f : -m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t shift2 = pack2(shift, shift), scale2 = pack2(a.scale_log2, a.scale_log2);
+        uint64_t sum0 = 0, sum1 = 0;  // two sums each
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t p[16];
+          if (c >= seen.lo && c < seen.hi) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float x = ex2(fmaf(__uint_as_float(v[c][2 * j]), a.scale_log2, shift));
-            const float y = ex2(fmaf(__uint_as_float(v[c][2 * j + 1]), a.scale_log2, shift));
-            sum[j & 1] += x;
-            sum[2 + (j & 1)] += y;
-            p[j] = op_pack_bf16(x, y);
+            for (int j = 0; j < 16; ++j) {
+              float x, y;
+              unpack2(fma2(pack2(v[c][2 * j], v[c][2 * j + 1]), scale2, shift2), x, y);
+              x = ex2(x);
+              y = ex2(y);
+              if (j & 1)
+                sum1 = add2(sum1, pack2(x, y));
+              else
+                sum0 = add2(sum0, pack2(x, y));
+              p[j] = op_pack_bf16(x, y);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) p[j] = 0u;
           }
           tmem_st_32x32b_x16(ts + 16 * c, p);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float l0, l1;
+        unpack2(add2(sum0, sum1), l0, l1);
+        l += l0 + l1;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(p_full + 8 * s);
@@ -291,7 +309,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       Cursor<SM::SLOTS> vc;  // the value tile of the step before
       // step n issues O += P V of tile n - 1 and S of tile n. Tiles that only the other warp uses are waited for
       // and released all the same: a slot's release counts both warps once for each of its fills.
+      //
+      // The second tile's products of a step are issued behind the first's. Issued freely they would run in turns,
+      // both softmaxes would start when both S are there, and products and softmaxes would alternate instead of
+      // overlapping (4000 cycles a step of both tiles instead of 2700).
       for (int n = 0; n <= steps; ++n) {
+        if (n < steps && s == 1 && !(ok = mbar_wait_warp(turn + 4 * cur.slot, cur.phase, abort_flag, err, kErrForward)))
+          break;
         if (n > 0) {
           if (!(ok = mbar_wait_warp(vc.full(ring), vc.phase, abort_flag, err, kErrForward))) break;
           if (pend) {
@@ -316,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_abt<DP>(ts, qt, cur.data(ring), whole ? kAttnTile : few);
           umma_commit_warp(sf);
         }
+        if (s == 0 && lane == 0) mbar_arrive(turn + 4 * cur.slot);  // (keys lie in even slots)
         umma_commit_warp(cur.empty(ring));
         if (n == steps - 1) umma_commit_warp(q_empty);
         cur.advance();
@@ -537,8 +562,8 @@ ma_status muon_adamw_window_attention_backward(const ma_window_attention* d, con
     g.do_ts = dout_token_stride;
     g.do_hs = dout_head_stride;
     g.lse = lse;
-    g.lse2 = reinterpret_cast<float*>(ws);
-    g.delta = reinterpret_cast<float*>(ws + sp.stats);
+    g.nlse2 = reinterpret_cast<float*>(ws);
+    g.ndelta = reinterpret_cast<float*>(ws + sp.stats);
     g.partial = reinterpret_cast<float*>(ws + 2 * sp.stats);
     g.partial_slots = sp.slots;
     g.dq = static_cast<__nv_bfloat16*>(dq);

@@ -16,8 +16,8 @@ struct AttnArgs {
   int n, heads, kv_heads, dim, sinks, window, n_seqs;
   float scale, scale_log2;  // scale, and scale * log2(e): scores enter exp2
   const int32_t* cu;
-  const float* lse2;        // gradient: lse * log2(e), +infinity for a query that sees nothing [head][token]
-  const float* delta;       // gradient: dout . out [head][token]
+  const float* nlse2;       // gradient: -lse * log2(e), -infinity for a query that sees nothing [head][token]
+  const float* ndelta;      // gradient: -dout . out [head][token]
 };
 
 // A 3-D map (element, token, head) of a bf16 tensor with 64 x 128 x 1 boxes in
@@ -33,7 +33,7 @@ struct AttnGrad {
   const __nv_bfloat16 *dout, *out;
   int64_t do_ts, do_hs;
   const float* lse;
-  float *lse2, *delta, *partial;
+  float *nlse2, *ndelta, *partial;
   int64_t partial_slots;
   __nv_bfloat16 *dq, *dk, *dv;
 };
@@ -157,30 +157,79 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
   return hi <= lo ? 0u : (0xffffffffu >> (32 - (hi - lo))) << lo;
 }
 
-// Masks a tile of scores in TMEM: -infinity in column 32 c + j of block c where
-// bit j of seen(c) is 0. A loop of its own over the few tiles at a sample's and
-// a window's edges: masks woven into the unrolled arithmetic made it so long
-// that fetching its instructions cost 4000 cycles a tile.
+// What 32 rows of a tile of scores see of its blocks of 32 columns: nothing
+// outside blocks lo .. hi - 1, all of block c where bit c of `all` is set.
+struct Blocks {
+  int lo, hi;
+  uint32_t all;
+};
+constexpr Blocks kAllBlocks{0, 4, 15u};
+
+// Masks the blocks of a tile of scores in TMEM that are neither all seen nor
+// unseen: -infinity in column 32 c + j of block c where bit j of seen(c) is 0. A
+// loop of its own over the few tiles at a sample's and a window's edges: masks
+// woven into the unrolled arithmetic made it so long that fetching its
+// instructions cost 4000 cycles a tile.
 template <typename F>
-__device__ __forceinline__ void mask_tile(uint32_t taddr, int blocks, F seen) {
+__device__ __forceinline__ void mask_tile(uint32_t taddr, const Blocks& b, F seen) {
 #pragma unroll 1
-  for (int c = 0; c < blocks; ++c) {
+  for (int c = b.lo; c < b.hi; ++c) {
+    if (b.all >> c & 1u) continue;
     const uint32_t m = seen(c);
-    if (__all_sync(0xffffffffu, m == 0xffffffffu)) continue;
     uint32_t v[32];
-    if (__any_sync(0xffffffffu, m != 0u)) {
-      tmem_ld_32x32b_x32(taddr + 32 * c, v);
-      tmem_ld_wait();
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = 0xff800000u;
-    }
+    tmem_ld_32x32b_x32(taddr + 32 * c, v);
+    tmem_ld_wait();
 #pragma unroll
     for (int j = 0; j < 32; ++j)
       if (!(m >> j & 1u)) v[j] = 0xff800000u;
     tmem_st_32x32b_x32(taddr + 32 * c, v);
   }
   tmem_st_wait();
+}
+
+// Blocks lo .. of a tile of keys from k0 (of `blocks` blocks) that 32 queries
+// from q0 see; cols: score columns that have been formed.
+__device__ __forceinline__ Blocks key_blocks(const AttnArgs& a, int q0, int k0, int cols, int blocks) {
+  Blocks b;
+  b.hi = max(0, min(min(blocks, (cols + 31) / 32), (q0 + 31 - k0) / 32 + 1));
+  if (q0 + 31 < k0) b.hi = 0;
+  const int first = q0 - a.window + 1 - k0;  // first column that the first query's window reaches
+  b.lo = k0 < a.sinks ? 0 : min(max(first, 0) / 32, b.hi);
+  b.all = 0;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (32 * c + 31 < cols && 32 * c + 31 <= q0 - k0 && (32 * c >= first + 31 || k0 + 32 * c + 31 < a.sinks)) b.all |= 1u << c;
+  return b;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t x, uint32_t y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // Columns that the products of a tile cover which only the sinks make visible.

@@ -1,7 +1,7 @@
 // Gradient of the sliding-window attention.
 //
-// With P = exp2(c S - lse2) (the forward pass's softmax weights, from its
-// saved lse), dP = dO V^T, delta_i = dO_i . O_i:
+// With P = exp2(c S - lse2) (the forward pass's softmax weights, lse2 = log2(e)
+// times its saved lse), dP = dO V^T, delta_i = dO_i . O_i:
 //   dS = P (dP - delta),  dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K.
 //
 // window_stats_kernel  lse2 and delta of every query and head.
@@ -32,8 +32,8 @@ constexpr int kErrDq = 0x202, kErrDkv = 0x203, kErrAlign = 0x204;
 __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant__ AttnArgs a,
                                                            const __nv_bfloat16* __restrict__ dout, int64_t do_ts,
                                                            int64_t do_hs, const __nv_bfloat16* __restrict__ out,
-                                                           const float* __restrict__ lse, float* __restrict__ lse2,
-                                                           float* __restrict__ delta) {
+                                                           const float* __restrict__ lse, float* __restrict__ nlse2,
+                                                           float* __restrict__ ndelta) {
   pdl_launch();
   pdl_wait();
   const int gl = threadIdx.x & 15;
@@ -59,8 +59,8 @@ __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant
     for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (u < total && gl == 0) {
       const float l = lse[(int64_t)h * a.n + t];
-      lse2[(int64_t)h * a.n + t] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
-      delta[(int64_t)h * a.n + t] = s;
+      nlse2[(int64_t)h * a.n + t] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
+      ndelta[(int64_t)h * a.n + t] = -s;
     }
   }
 }
@@ -82,7 +82,7 @@ struct GradSmem {
   static constexpr uint32_t TILE = kAttnTile * DP * 2;
   static constexpr int SLOTS = DP == 128 ? 5 : 8;
   static constexpr uint32_t RING = 2 * TILE;                   // after Q and dO, or K and V
-  static constexpr uint32_t STATS = RING + SLOTS * TILE;       // dkv: [2][lse2, delta][128] of the query tiles
+  static constexpr uint32_t STATS = RING + SLOTS * TILE;       // dkv: [2][nlse2, ndelta][128] of the query tiles
   static constexpr uint32_t OWN = STATS + 2 * 2 * kAttnTile * 4;
   static constexpr uint32_t STAGE = DP == 128 ? TILE : OWN;    // 4 KB to each of 8 warps
   static constexpr uint32_t BARS = DP == 128 ? OWN : OWN + 8 * 4096;
@@ -158,14 +158,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t step = 0, s_ph = 0, dq_ph = 0;  // step: over all items; s_ph: a bit per S slot
+    const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     DqItem next = dq_item(a, blockIdx.x, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       const DqItem w = next;
       const int row0 = w.t.p0 + (row & ~31), i = w.t.p0 + row;
       const int64_t t = (int64_t)w.t.b + i;
       const bool mine = i < w.t.len;
-      const float lse2 = mine ? a.lse2[(int64_t)w.head * a.n + t] : INFINITY;
-      const float delta = mine ? a.delta[(int64_t)w.head * a.n + t] : 0.f;
+      const float nlse2 = mine ? a.nlse2[(int64_t)w.head * a.n + t] : -INFINITY;
+      const float ndelta = mine ? a.ndelta[(int64_t)w.head * a.n + t] : 0.f;
+      const uint64_t shift2 = pack2(nlse2, nlse2), delta2 = pack2(ndelta, ndelta);
       for (int n = 0; n < w.steps && ok; ++n, ++step) {
         const uint32_t slot = n & 1, ts = tmem + lanes + 128u * slot + 64u * half;
         const int k0 = w.tile(n) * kAttnTile + 64 * half;  // of this half
@@ -173,12 +175,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         s_ph ^= 1u << slot;
         tc_fence_after();
+        Blocks seen{0, 2, 3u};
         if (!tile_full(a, w.t.p0, k0 - 64 * half)) {
           // key k0 + col is visible for col < end and (col >= first or col < sink); past the sinks' columns of
           // a tile that is there for them alone no score has been formed
-          const int end = w.k.sink && n == 0 ? min(i - k0 + 1, few - 64 * half) : i - k0 + 1;
-          const int first = i - k0 - a.window + 1, sink = min(a.sinks - k0, end);
-          mask_tile(ts, 2, [&](int c) { return bit_range(first - 32 * c, end - 32 * c) | bit_range(0, sink - 32 * c); });
+          const int cols = w.k.sink && n == 0 ? few - 64 * half : 64;
+          const int end = min(i - k0 + 1, cols), first = i - k0 - a.window + 1, sink = min(a.sinks - k0, end);
+          seen = key_blocks(a, row0, k0, cols, 2);
+          mask_tile(ts, seen,
+                    [&](int c) { return bit_range(first - 32 * c, end - 32 * c) | bit_range(0, sink - 32 * c); });
         }
         uint32_t p[2][32], g[2][32], ds[32];
         tmem_ld_32x32b_x32(ts, p[0]);
@@ -186,9 +191,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
 #pragma unroll
         for (int x = 0; x < 2; ++x)
+          if (x >= seen.lo && x < seen.hi) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            p[x][j] = __float_as_uint(ex2(fmaf(__uint_as_float(p[x][j]), a.scale_log2, -lse2)));
+            for (int j = 0; j < 32; j += 2) {
+              float u, v;
+              unpack2(fma2(pack2(p[x][j], p[x][j + 1]), scale2, shift2), u, v);
+              p[x][j] = __float_as_uint(ex2(u));
+              p[x][j + 1] = __float_as_uint(ex2(v));
+            }
+          }
         ok = mbar_wait_warp(dp_full, step & 1, abort_flag, err, kErrDq);
         if (!ok) break;
         tc_fence_after();
@@ -198,12 +209,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(dp_empty);
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < 2; ++x) {
+          if (x >= seen.lo && x < seen.hi) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            ds[16 * x + j] =
-                op_pack_bf16(__uint_as_float(p[x][2 * j]) * (__uint_as_float(g[x][2 * j]) - delta),
-                             __uint_as_float(p[x][2 * j + 1]) * (__uint_as_float(g[x][2 * j + 1]) - delta));
+            for (int j = 0; j < 32; j += 2) {
+              float u, v;
+              unpack2(mul2(pack2(p[x][j], p[x][j + 1]), add2(pack2(g[x][j], g[x][j + 1]), delta2)), u, v);
+              ds[16 * x + j / 2] = op_pack_bf16(u, v);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) ds[16 * x + j] = 0u;
+          }
+        }
         tmem_st_32x32b_x32(ts, ds);
         tmem_st_wait();
         tc_fence_before();
@@ -466,15 +484,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + 64u * half, tg = ts + 128u;
     uint32_t step = 0, done_ph = 0;
+    const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     DkvItem upcoming = dkv_item(a, blockIdx.x, sink_items, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       const DkvItem w = upcoming;
       const int steps = group * w.nq, row0 = w.t.p0 + (row & ~31), j = w.t.p0 + row;
-      // threads 0-127 bring lse2 of a query tile, threads 128-255 delta
+      // threads 0-127 bring nlse2 of a query tile, threads 128-255 ndelta
       auto stat = [&](int head, int tile) {
         const int i = tile * kAttnTile + row;
-        if (i >= w.t.len) return half ? 0.f : INFINITY;
-        return (half ? a.delta : a.lse2)[(int64_t)head * a.n + w.t.b + i];
+        if (i >= w.t.len) return half ? 0.f : -INFINITY;
+        return (half ? a.ndelta : a.nlse2)[(int64_t)head * a.n + w.t.b + i];
       };
       int head = w.kv * group, tile = w.q_lo;  // of the step
       if (steps) {
@@ -490,26 +509,43 @@ __global__ void __launch_bounds__(kThreads, 1)
              mbar_wait_warp(s_full, step & 1, abort_flag, err, kErrDkv);
         if (!ok) break;
         tc_fence_after();
+        Blocks seen{0, 2, 3u};
         if (!tile_full(a, q0, w.t.p0)) {
-          // query q0 + 64 half + col sees key j for col >= from and col < to
-          const int from = j - q0 - 64 * half;
+          // query qh + col sees key j for col >= from and col < to
+          const int qh = q0 + 64 * half, from = j - qh;
           const int to = j < a.sinks ? kAttnTile : (int)min((int64_t)from + a.window, (int64_t)kAttnTile);
-          mask_tile(ts, 2, [&](int c) { return bit_range(from - 32 * c, to - 32 * c); });
+          // this warp's keys row0 .. row0 + 31: the first is seen by the earliest queries and the last by the latest
+          seen.lo = min(max(row0 - qh, 0) / 32, 2);
+          seen.hi = row0 < a.sinks ? 2 : (int)min((int64_t)2, max((int64_t)0, ((int64_t)row0 + 31 + a.window - 1 - qh + 32) / 32));
+          seen.all = 0;
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (row0 + 31 <= qh + 32 * c && (qh + 32 * c + 31 - row0 < a.window || row0 + 31 < a.sinks)) seen.all |= 1u << c;
+          mask_tile(ts, seen, [&](int c) { return bit_range(from - 32 * c, to - 32 * c); });
         }
         uint32_t p[2][32], g[2][32], r[32];
         tmem_ld_32x32b_x32(ts, p[0]);
         tmem_ld_32x32b_x32(ts + 32, p[1]);
         tmem_ld_wait();
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < 2; ++x) {
+          if (x >= seen.lo && x < seen.hi) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(st + 32 * x + e);
-            p[x][e] = __float_as_uint(ex2(fmaf(__uint_as_float(p[x][e]), a.scale_log2, -l.x)));
-            p[x][e + 1] = __float_as_uint(ex2(fmaf(__uint_as_float(p[x][e + 1]), a.scale_log2, -l.y)));
-            p[x][e + 2] = __float_as_uint(ex2(fmaf(__uint_as_float(p[x][e + 2]), a.scale_log2, -l.z)));
-            p[x][e + 3] = __float_as_uint(ex2(fmaf(__uint_as_float(p[x][e + 3]), a.scale_log2, -l.w)));
+            for (int e = 0; e < 32; e += 4) {
+              const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(st + 32 * x + e);
+              float u, v;
+              unpack2(fma2(pack2(p[x][e], p[x][e + 1]), scale2, l.x), u, v);
+              p[x][e] = __float_as_uint(ex2(u));
+              p[x][e + 1] = __float_as_uint(ex2(v));
+              unpack2(fma2(pack2(p[x][e + 2], p[x][e + 3]), scale2, l.y), u, v);
+              p[x][e + 2] = __float_as_uint(ex2(u));
+              p[x][e + 3] = __float_as_uint(ex2(v));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) p[x][e] = 0u;
           }
+        }
 #pragma unroll
         for (int e = 0; e < 32; ++e)
           r[e] = op_pack_bf16(__uint_as_float(p[e >> 4][(2 * e) & 31]), __uint_as_float(p[e >> 4][((2 * e) & 31) + 1]));
@@ -527,11 +563,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const float4 d = *reinterpret_cast<const float4*>(st + 128 + 32 * x + e);
-            r[16 * x + e / 2] = op_pack_bf16(__uint_as_float(p[x][e]) * (__uint_as_float(g[x][e]) - d.x),
-                                             __uint_as_float(p[x][e + 1]) * (__uint_as_float(g[x][e + 1]) - d.y));
-            r[16 * x + e / 2 + 1] = op_pack_bf16(__uint_as_float(p[x][e + 2]) * (__uint_as_float(g[x][e + 2]) - d.z),
-                                                 __uint_as_float(p[x][e + 3]) * (__uint_as_float(g[x][e + 3]) - d.w));
+            const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(st + 128 + 32 * x + e);
+            float u, v;
+            unpack2(mul2(pack2(p[x][e], p[x][e + 1]), add2(pack2(g[x][e], g[x][e + 1]), d.x)), u, v);
+            r[16 * x + e / 2] = op_pack_bf16(u, v);
+            unpack2(mul2(pack2(p[x][e + 2], p[x][e + 3]), add2(pack2(g[x][e + 2], g[x][e + 3]), d.y)), u, v);
+            r[16 * x + e / 2 + 1] = op_pack_bf16(u, v);
           }
         tmem_st_32x32b_x32(tg, r);
         tmem_st_wait();
@@ -758,10 +795,10 @@ cudaError_t attn_backward(AttnArgs a, const CUtensorMap& q, const CUtensorMap& k
                           const CUtensorMap& dout, const AttnGrad& g, int* err, int sms, cudaStream_t st) {
   const int64_t rows = ((int64_t)a.n * a.heads + 15) / 16, most = (int64_t)sms * 8;
   cudaError_t e = op_launch(window_stats_kernel, dim3((unsigned)(rows < most ? rows : most)), dim3(256), 0, st, 1, a,
-                            g.dout, g.do_ts, g.do_hs, g.out, g.lse, g.lse2, g.delta);
+                            g.dout, g.do_ts, g.do_hs, g.out, g.lse, g.nlse2, g.ndelta);
   if (e != cudaSuccess) return e;
-  a.lse2 = g.lse2;
-  a.delta = g.delta;
+  a.nlse2 = g.nlse2;
+  a.ndelta = g.ndelta;
   e = a.dim > 64 ? run_backward<128>(a, q, k, v, dout, g, err, sms, st)
                  : run_backward<64>(a, q, k, v, dout, g, err, sms, st);
   if (e != cudaSuccess || a.sinks == 0) return e;
