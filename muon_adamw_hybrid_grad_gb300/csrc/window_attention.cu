@@ -323,9 +323,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             p_ph ^= 1;
             tc_fence_after();
             if (whole)
-              mma_ab<DP>(to, ts, 32, vc.data(ring), begun);
+              mma_ab<DP, 16>(to, ts, vc.data(ring), begun);
             else
-              mma_ab_few<DP>(to, ts, 32, vc.data(ring), begun, few);
+              mma_ab_few<DP, 16>(to, ts, vc.data(ring), begun, few);
             if (n - 1 == end) umma_commit_warp(of);
             begun = true;
           }

@@ -187,6 +187,13 @@ __device__ __forceinline__ void mask_tile(uint32_t taddr, const Blocks& b, F see
   tmem_st_wait();
 }
 
+// Masks one block of scores the same way, by the bits of m.
+__device__ __forceinline__ void mask_block(uint32_t (&v)[32], uint32_t m) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (!(m >> j & 1u)) v[j] = 0xff800000u;
+}
+
 // Blocks lo .. of a tile of keys from k0 (of `blocks` blocks) that 32 queries
 // from q0 see; cols: score columns that have been formed.
 __device__ __forceinline__ Blocks key_blocks(const AttnArgs& a, int q0, int k0, int cols, int blocks) {
@@ -303,27 +310,26 @@ __device__ __forceinline__ void mma_abt(uint32_t d_tmem, uint32_t a, uint32_t b,
                      (p | kk) != 0 ? 1u : 0u);
 }
 
-// D[128 x DP] (+)= A B with A bf16 in TMEM (128 x 128: the columns of its second
-// half of 64 `half_step` TMEM columns after the first's) and B a tile whose 128
-// rows are the inner dimension.
-template <int DP>
-__device__ __forceinline__ void mma_ab(uint32_t d_tmem, uint32_t a_tmem, uint32_t half_step, uint32_t b, bool add) {
+// D[128 x DP] (+)= A B with A bf16 in TMEM (128 x 128, each 32 columns of it in 16
+// TMEM columns, STEP after the 32 before) and B a tile whose 128 rows are the
+// inner dimension.
+template <int DP, int STEP>
+__device__ __forceinline__ void mma_ab(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool add) {
   const uint32_t id = idesc_bf16(128, DP, true);
   const uint64_t db = sdesc(b, kAttnTile * 128, 1024);
 #pragma unroll
   for (int ks = 0; ks < 8; ++ks)
-    umma_bf16_ts_warp(d_tmem, a_tmem + (ks >> 2) * half_step + (ks & 3) * 8, db + 128u * ks, id,
+    umma_bf16_ts_warp(d_tmem, a_tmem + (ks >> 1) * STEP + (ks & 1) * 8, db + 128u * ks, id,
                       ks != 0 ? 1u : (uint32_t)add);
 }
 // The same with an inner dimension of `cols`, a multiple of 32.
-template <int DP>
-__device__ __forceinline__ void mma_ab_few(uint32_t d_tmem, uint32_t a_tmem, uint32_t half_step, uint32_t b, bool add,
-                                           int cols) {
+template <int DP, int STEP>
+__device__ __forceinline__ void mma_ab_few(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool add, int cols) {
   const uint32_t id = idesc_bf16(128, DP, true);
   const uint64_t db = sdesc(b, kAttnTile * 128, 1024);
 #pragma unroll 1
   for (int ks = 0; ks * 16 < cols; ++ks)
-    umma_bf16_ts_warp(d_tmem, a_tmem + (ks >> 2) * half_step + (ks & 3) * 8, db + 128u * ks, id, add || ks != 0);
+    umma_bf16_ts_warp(d_tmem, a_tmem + (ks >> 1) * STEP + (ks & 1) * 8, db + 128u * ks, id, add || ks != 0);
 }
 
 // Rows of a 128-row fp32 accumulator in TMEM, scaled and rounded to bf16, to

@@ -22,9 +22,11 @@
 namespace ma {
 namespace {
 
-constexpr int kThreads = 384;
-// of the 168 registers a thread is launched with: 8 * 208 + 4 * 80 <= 12 * 168
-constexpr int kMathRegs = 208, kOtherRegs = 80;
+constexpr int kMathWarps = 16;
+constexpr int kThreads = (kMathWarps + 4) * 32;
+constexpr int kTma = kMathWarps, kMmaA = kMathWarps + 1, kMmaB = kMathWarps + 2;  // and the clearing warp
+// of the 96 registers a thread is launched with: 16 * 104 + 4 * 64 = 20 * 96
+constexpr int kMathRegs = 104, kOtherRegs = 64;
 constexpr int kErrDq = 0x202, kErrDkv = 0x203, kErrAlign = 0x204;
 
 // ---- lse2 and delta ----
@@ -66,11 +68,13 @@ __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant
 }
 
 // ---- dQ ----
-// Warps 0-7: a thread to a query and half of a tile's keys (warps 0-3 the
-// first 64, 4-7 the others); warp 8: TMA; warps 9 and 10: tcgen05.mma, the one S
-// and dQ, the other dP; warp 11: clears the key and value rows of other samples.
+// Warps 0-15: a thread to a query and a block of 32 of a tile's keys (warps 0-3
+// the first block, and so on); warp 16: TMA; warps 17 and 18: tcgen05.mma, the
+// one S and dQ, the other dP; warp 19: clears the key and value rows of other
+// samples. Sixteen warps rather than eight with twice the keys: a step's chain of
+// waits, TMEM reads and exponentials is what bounds this kernel.
 // TMEM: S of even steps | S of odd steps | dP | dQ. dS (bf16) overwrites the S
-// it came from, each half in the first 32 of its own 64 columns. S of the next
+// it came from, each block in the first 16 of its own 32 columns. S of the next
 // tile is formed while the threads work on this one's, and dP of the next as
 // soon as this one's has been read.
 //
@@ -87,7 +91,7 @@ struct GradSmem {
   static constexpr uint32_t STAGE = DP == 128 ? TILE : OWN;    // 4 KB to each of 8 warps
   static constexpr uint32_t BARS = DP == 128 ? OWN : OWN + 8 * 4096;
   // full[SLOTS], empty[SLOTS], raw[SLOTS], then each kernel's own
-  static constexpr int NBARS = 3 * SLOTS + 13;
+  static constexpr int NBARS = 3 * SLOTS + 16;
   static constexpr uint32_t BYTES = BARS + NBARS * 8 + 16;
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
@@ -134,11 +138,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     ring.init(1);
     mbar_init(q_full, 1), mbar_init(q_empty, 1), mbar_init(do_full, 1), mbar_init(do_empty, 8);
-    mbar_init(s_full, 1), mbar_init(s_full + 8, 1), mbar_init(dp_full, 1), mbar_init(dp_empty, 256);
-    mbar_init(ds_full, 256), mbar_init(ds_full + 8, 256), mbar_init(dq_full, 1), mbar_init(drain, 1), mbar_init(drain + 8, 1);
+    mbar_init(s_full, 1), mbar_init(s_full + 8, 1), mbar_init(dp_full, 1), mbar_init(dp_empty, kMathWarps);
+    mbar_init(ds_full, kMathWarps), mbar_init(ds_full + 8, kMathWarps), mbar_init(dq_full, 1), mbar_init(drain, 1), mbar_init(drain + 8, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 9) tmem_alloc<1>(smem_u32(tmem_slot), 512);
+  if (warp == kMmaA) tmem_alloc<1>(smem_u32(tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -149,13 +153,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int few = sink_columns(a);
   bool ok = true;
   // (one instruction for all four warps of a group)
-  if (warp < 8)
+  if (warp < kMathWarps)
     regs_up<kMathRegs>();
   else
     regs_down<kOtherRegs>();
 
-  if (warp < 8) {
-    const int half = warp >> 2, row = threadIdx.x & 127;
+  if (warp < kMathWarps) {
+    const int blk = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t step = 0, s_ph = 0, dq_ph = 0;  // step: over all items; s_ph: a bit per S slot
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
@@ -169,63 +173,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float ndelta = mine ? a.ndelta[(int64_t)w.head * a.n + t] : 0.f;
       const uint64_t shift2 = pack2(nlse2, nlse2), delta2 = pack2(ndelta, ndelta);
       for (int n = 0; n < w.steps && ok; ++n, ++step) {
-        const uint32_t slot = n & 1, ts = tmem + lanes + 128u * slot + 64u * half;
-        const int k0 = w.tile(n) * kAttnTile + 64 * half;  // of this half
+        const uint32_t slot = n & 1, ts = tmem + lanes + 128u * slot + 32u * blk;
+        const int k0 = w.tile(n) * kAttnTile + 32 * blk;  // of this block
         ok = mbar_wait_warp(s_full + 8 * slot, s_ph >> slot & 1, abort_flag, err, kErrDq);
         if (!ok) break;
         s_ph ^= 1u << slot;
         tc_fence_after();
-        Blocks seen{0, 2, 3u};
-        if (!tile_full(a, w.t.p0, k0 - 64 * half)) {
+        uint32_t p[32], g[32], ds[16];
+        tmem_ld_32x32b_x32(ts, p);
+        tmem_ld_wait();
+        bool seen = true;
+        if (!tile_full(a, w.t.p0, w.tile(n) * kAttnTile)) {
           // key k0 + col is visible for col < end and (col >= first or col < sink); past the sinks' columns of
           // a tile that is there for them alone no score has been formed
-          const int cols = w.k.sink && n == 0 ? few - 64 * half : 64;
+          const int cols = w.k.sink && n == 0 ? few - 32 * blk : 32;
           const int end = min(i - k0 + 1, cols), first = i - k0 - a.window + 1, sink = min(a.sinks - k0, end);
-          seen = key_blocks(a, row0, k0, cols, 2);
-          mask_tile(ts, seen,
-                    [&](int c) { return bit_range(first - 32 * c, end - 32 * c) | bit_range(0, sink - 32 * c); });
+          const uint32_t m = bit_range(first, end) | bit_range(0, sink);
+          seen = __any_sync(0xffffffffu, m != 0u);
+          if (!__all_sync(0xffffffffu, m == 0xffffffffu)) mask_block(p, m);
         }
-        uint32_t p[2][32], g[2][32], ds[32];
-        tmem_ld_32x32b_x32(ts, p[0]);
-        tmem_ld_32x32b_x32(ts + 32, p[1]);
-        tmem_ld_wait();
+        if (seen) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (x >= seen.lo && x < seen.hi) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              float u, v;
-              unpack2(fma2(pack2(p[x][j], p[x][j + 1]), scale2, shift2), u, v);
-              p[x][j] = __float_as_uint(ex2(u));
-              p[x][j + 1] = __float_as_uint(ex2(v));
-            }
+          for (int j = 0; j < 32; j += 2) {
+            float u, v;
+            unpack2(fma2(pack2(p[j], p[j + 1]), scale2, shift2), u, v);
+            p[j] = __float_as_uint(ex2(u));
+            p[j + 1] = __float_as_uint(ex2(v));
           }
+        }
         ok = mbar_wait_warp(dp_full, step & 1, abort_flag, err, kErrDq);
         if (!ok) break;
         tc_fence_after();
-        tmem_ld_32x32b_x32(tmem + lanes + 256u + 64u * half, g[0]);
-        tmem_ld_32x32b_x32(tmem + lanes + 256u + 64u * half + 32, g[1]);
+        tmem_ld_32x32b_x32(tmem + lanes + 256u + 32u * blk, g);
         tmem_ld_wait();
         tc_fence_before();
-        mbar_arrive(dp_empty);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dp_empty);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (x >= seen.lo && x < seen.hi) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              float u, v;
-              unpack2(mul2(pack2(p[x][j], p[x][j + 1]), add2(pack2(g[x][j], g[x][j + 1]), delta2)), u, v);
-              ds[16 * x + j / 2] = op_pack_bf16(u, v);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) ds[16 * x + j] = 0u;
-          }
+        for (int j = 0; j < 32; j += 2) {
+          float u, v;
+          unpack2(mul2(pack2(p[j], p[j + 1]), add2(pack2(g[j], g[j + 1]), delta2)), u, v);
+          ds[j / 2] = seen ? op_pack_bf16(u, v) : 0u;
         }
-        tmem_st_32x32b_x32(ts, ds);
+        tmem_st_32x32b_x16(ts, ds);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(ds_full + 8 * slot);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_full + 8 * slot);
       }
       if (!ok) break;
       if (item + (int)gridDim.x < items) next = dq_item(a, item + gridDim.x, lane);
@@ -235,17 +229,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         dq_ph ^= 1;
         tc_fence_after();
       }
-      store_rows<DP>(tmem + lanes + 384u, a.scale, w.steps == 0,
-                     dq + (((int64_t)w.t.b + row0) * a.heads + w.head) * a.dim, (int64_t)a.heads * a.dim,
-                     w.t.len - row0, a.dim, base + SM::STAGE + warp * 4096, lane, half * (DP / 2), (half + 1) * (DP / 2));
-      if (w.steps) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(do_empty);
+      if (warp < 8) {
+        // half of the columns to each four warps
+        const int half = warp >> 2;
+        store_rows<DP>(tmem + lanes + 384u, a.scale, w.steps == 0,
+                       dq + (((int64_t)w.t.b + row0) * a.heads + w.head) * a.dim, (int64_t)a.heads * a.dim,
+                       w.t.len - row0, a.dim, base + SM::STAGE + warp * 4096, lane, half * (DP / 2),
+                       (half + 1) * (DP / 2));
+        if (w.steps) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(do_empty);
+        }
       }
       tc_fence_before();
     }
-  } else if (warp == 8) {
+  } else if (warp == kTma) {
     Cursor<SM::SLOTS> cur;
     uint32_t loads = 0, raw_phase = 0;
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
@@ -280,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == kMmaA) {
     // S of the next steps, dQ
     Cursor<SM::SLOTS> sc;  // the next S's key tile
     uint32_t q_ph = 0, ds_ph = 0;  // ds_ph: a bit per S slot
@@ -313,9 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ds_ph ^= 1u << slot;
         tc_fence_after();
         if (n > 0 || !sink)
-          mma_ab<DP>(tm + 384u, tm + 128u * (n & 1), 64, qc.data(ring), n > 0);
+          mma_ab<DP, 32>(tm + 384u, tm + 128u * (n & 1), qc.data(ring), n > 0);
         else
-          mma_ab_few<DP>(tm + 384u, tm, 64, qc.data(ring), false, few);
+          mma_ab_few<DP, 32>(tm + 384u, tm, qc.data(ring), false, few);
         umma_commit_warp(qc.empty(ring));
         qc.skip(2);
         if (n + 2 < steps) ok = issue_s(n + 2);
@@ -325,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     umma_commit_warp(drain);
     if (lane == 0) drain_wait(drain, 0);
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == kMmaB) {
     // dP, once the threads have read the one before
     Cursor<SM::SLOTS> pc;  // a key tile, then its value tile
     uint32_t q_ph = 0, step = 0;
@@ -371,17 +370,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc<1>(tmem, 512);
+  if (warp == kMmaA) tmem_dealloc<1>(tmem, 512);
 }
 
 // ---- dK and dV ----
 // Scores are formed transposed, S^T = K Q^T and dP^T = V dO^T, so that P^T and
 // dS^T stand in TMEM as the left operands of dV += P^T dO and dK += dS^T Q.
-// Warps 0-7: a thread to a key and half of a tile's queries; warp 8: TMA;
-// warps 9 and 10: tcgen05.mma, the one dV and then the next step's S^T, the other
-// dK and the next dP^T; warp 11: clears rows of Q and dO that belong to other
-// samples. TMEM: S^T | dP^T | dV | dK; P^T overwrites S^T and dS^T
-// dP^T, each half in the first 32 of its own 64 columns. While the threads form
+// Warps 0-15: a thread to a key and a block of 32 of a tile's queries; warp 16:
+// TMA; warps 17 and 18: tcgen05.mma, the one dV and then the next step's S^T, the
+// other dK and the next dP^T, issued behind them; warp 19: clears rows of Q and
+// dO that belong to other samples. TMEM: S^T | dP^T | dV | dK; P^T overwrites
+// S^T and dS^T dP^T, each block in the first 16 of its own 32 columns. While the threads form
 // P^T of a step the tensor core runs the step before's dK and this one's dP^T;
 // while they form dS^T it runs dV and the next step's S^T. Results leave through
 // the shared memory of V, whose next tile is therefore loaded after the epilogue;
@@ -446,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, bars + SM::SLOTS * 16, SM::TILE};
   const uint32_t own = bars + 3 * SM::SLOTS * 8, k_full = own, k_empty = own + 8, v_full = own + 16,
                  v_empty = own + 24, s_full = own + 32, dp_full = own + 40, p_full = own + 48, ds_full = own + 56,
-                 stat_full = own + 64, done = own + 72, drain = own + 80;
+                 stat_full = own + 64, done = own + 72, drain = own + 80, turn = own + 96;
   float* stats = reinterpret_cast<float*>(smem + SM::STATS);
   if (base & 1023u) {  // the swizzle's phase is that of the address
     if (threadIdx.x == 0) atomicCAS(err, 0, kErrAlign);
@@ -456,11 +455,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     ring.init(2);
     mbar_init(k_full, 1), mbar_init(k_empty, 1), mbar_init(v_full, 1), mbar_init(v_empty, 8);
-    mbar_init(s_full, 1), mbar_init(dp_full, 1), mbar_init(p_full, 256), mbar_init(ds_full, 256);
-    mbar_init(stat_full, 256), mbar_init(done, 2), mbar_init(drain, 1), mbar_init(drain + 8, 1);
+    mbar_init(s_full, 1), mbar_init(dp_full, 1), mbar_init(p_full, kMathWarps), mbar_init(ds_full, kMathWarps);
+    mbar_init(stat_full, kMathWarps), mbar_init(done, 2), mbar_init(drain, 1), mbar_init(drain + 8, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(turn + 8 * i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 9) tmem_alloc<1>(smem_u32(tmem_slot), 512);
+  if (warp == kMmaA) tmem_alloc<1>(smem_u32(tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -474,15 +474,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     a.kv_heads * count_units(a, lane, [](int len, bool) { return (len + kAttnTile - 1) / kAttnTile; });
   bool ok = true;
   // (one instruction for all four warps of a group)
-  if (warp < 8)
+  if (warp < kMathWarps)
     regs_up<kMathRegs>();
   else
     regs_down<kOtherRegs>();
 
-  if (warp < 8) {
-    const int half = warp >> 2, row = threadIdx.x & 127;
+  if (warp < kMathWarps) {
+    const int blk = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + 64u * half, tg = ts + 128u;
+    const uint32_t ts = tmem + lanes + 32u * blk, tg = ts + 128u;
     uint32_t step = 0, done_ph = 0;
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     DkvItem upcoming = dkv_item(a, blockIdx.x, sink_items, lane);
@@ -492,92 +492,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       // threads 0-127 bring nlse2 of a query tile, threads 128-255 ndelta
       auto stat = [&](int head, int tile) {
         const int i = tile * kAttnTile + row;
-        if (i >= w.t.len) return half ? 0.f : -INFINITY;
-        return (half ? a.ndelta : a.nlse2)[(int64_t)head * a.n + w.t.b + i];
+        if (i >= w.t.len) return blk ? 0.f : -INFINITY;
+        return (blk ? a.ndelta : a.nlse2)[(int64_t)head * a.n + w.t.b + i];
       };
       int head = w.kv * group, tile = w.q_lo;  // of the step
       if (steps) {
-        stats[(step & 1) * 256 + threadIdx.x] = stat(head, tile);
-        mbar_arrive(stat_full);
+        if (warp < 8) stats[(step & 1) * 256 + threadIdx.x] = stat(head, tile);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(stat_full);
       }
       for (int n = 0; n < steps && ok; ++n, ++step) {
         const int q0 = tile * kAttnTile;
         if (++tile == w.q_lo + w.nq) tile = w.q_lo, ++head;
-        const float next = n + 1 < steps ? stat(head, tile) : 0.f;
-        const float* st = stats + (step & 1) * 256 + 64 * half;
+        const float next = warp < 8 && n + 1 < steps ? stat(head, tile) : 0.f;
+        const float* st = stats + (step & 1) * 256 + 32 * blk;
         ok = mbar_wait_warp(stat_full, step & 1, abort_flag, err, kErrDkv) &&
              mbar_wait_warp(s_full, step & 1, abort_flag, err, kErrDkv);
         if (!ok) break;
         tc_fence_after();
-        Blocks seen{0, 2, 3u};
-        if (!tile_full(a, q0, w.t.p0)) {
-          // query qh + col sees key j for col >= from and col < to
-          const int qh = q0 + 64 * half, from = j - qh;
-          const int to = j < a.sinks ? kAttnTile : (int)min((int64_t)from + a.window, (int64_t)kAttnTile);
-          // this warp's keys row0 .. row0 + 31: the first is seen by the earliest queries and the last by the latest
-          seen.lo = min(max(row0 - qh, 0) / 32, 2);
-          seen.hi = row0 < a.sinks ? 2 : (int)min((int64_t)2, max((int64_t)0, ((int64_t)row0 + 31 + a.window - 1 - qh + 32) / 32));
-          seen.all = 0;
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            if (row0 + 31 <= qh + 32 * c && (qh + 32 * c + 31 - row0 < a.window || row0 + 31 < a.sinks)) seen.all |= 1u << c;
-          mask_tile(ts, seen, [&](int c) { return bit_range(from - 32 * c, to - 32 * c); });
-        }
-        uint32_t p[2][32], g[2][32], r[32];
-        tmem_ld_32x32b_x32(ts, p[0]);
-        tmem_ld_32x32b_x32(ts + 32, p[1]);
+        uint32_t p[32], g[32], r[16];
+        tmem_ld_32x32b_x32(ts, p);
         tmem_ld_wait();
+        bool seen = true;
+        if (!tile_full(a, q0, w.t.p0)) {
+          // query qb + col sees key j for col >= from and col < to
+          const int qb = q0 + 32 * blk, from = j - qb;
+          const int to = j < a.sinks ? 32 : (int)min((int64_t)from + a.window, (int64_t)32);
+          const uint32_t m = bit_range(from, to);
+          seen = __any_sync(0xffffffffu, m != 0u);
+          if (!__all_sync(0xffffffffu, m == 0xffffffffu)) mask_block(p, m);
+        }
+        if (seen) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (x >= seen.lo && x < seen.hi) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(st + 32 * x + e);
-              float u, v;
-              unpack2(fma2(pack2(p[x][e], p[x][e + 1]), scale2, l.x), u, v);
-              p[x][e] = __float_as_uint(ex2(u));
-              p[x][e + 1] = __float_as_uint(ex2(v));
-              unpack2(fma2(pack2(p[x][e + 2], p[x][e + 3]), scale2, l.y), u, v);
-              p[x][e + 2] = __float_as_uint(ex2(u));
-              p[x][e + 3] = __float_as_uint(ex2(v));
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) p[x][e] = 0u;
+          for (int e = 0; e < 32; e += 4) {
+            const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(st + e);
+            float u, v;
+            unpack2(fma2(pack2(p[e], p[e + 1]), scale2, l.x), u, v);
+            p[e] = __float_as_uint(ex2(u));
+            p[e + 1] = __float_as_uint(ex2(v));
+            unpack2(fma2(pack2(p[e + 2], p[e + 3]), scale2, l.y), u, v);
+            p[e + 2] = __float_as_uint(ex2(u));
+            p[e + 3] = __float_as_uint(ex2(v));
           }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) p[e] = 0u;
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          r[e] = op_pack_bf16(__uint_as_float(p[e >> 4][(2 * e) & 31]), __uint_as_float(p[e >> 4][((2 * e) & 31) + 1]));
-        tmem_st_32x32b_x32(ts, r);
+        for (int e = 0; e < 16; ++e) r[e] = op_pack_bf16(__uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1]));
+        tmem_st_32x32b_x16(ts, r);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(p_full);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
         ok = mbar_wait_warp(dp_full, step & 1, abort_flag, err, kErrDkv);
         if (!ok) break;
         tc_fence_after();
-        tmem_ld_32x32b_x32(tg, g[0]);
-        tmem_ld_32x32b_x32(tg + 32, g[1]);
+        tmem_ld_32x32b_x32(tg, g);
         tmem_ld_wait();
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(st + 128 + 32 * x + e);
-            float u, v;
-            unpack2(mul2(pack2(p[x][e], p[x][e + 1]), add2(pack2(g[x][e], g[x][e + 1]), d.x)), u, v);
-            r[16 * x + e / 2] = op_pack_bf16(u, v);
-            unpack2(mul2(pack2(p[x][e + 2], p[x][e + 3]), add2(pack2(g[x][e + 2], g[x][e + 3]), d.y)), u, v);
-            r[16 * x + e / 2 + 1] = op_pack_bf16(u, v);
-          }
-        tmem_st_32x32b_x32(tg, r);
+        for (int e = 0; e < 32; e += 4) {
+          const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(st + 128 + e);
+          float u, v;
+          unpack2(mul2(pack2(p[e], p[e + 1]), add2(pack2(g[e], g[e + 1]), d.x)), u, v);
+          r[e / 2] = op_pack_bf16(u, v);
+          unpack2(mul2(pack2(p[e + 2], p[e + 3]), add2(pack2(g[e + 2], g[e + 3]), d.y)), u, v);
+          r[e / 2 + 1] = op_pack_bf16(u, v);
+        }
+        tmem_st_32x32b_x16(tg, r);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(ds_full);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_full);
         if (n + 1 < steps) {
-          // every thread has read the buffer's last contents: it arrived after them for this step
-          stats[((step + 1) & 1) * 256 + threadIdx.x] = next;
-          mbar_arrive(stat_full);
+          // every warp has read the buffer's last contents: it arrived after them for this step
+          if (warp < 8) stats[((step + 1) & 1) * 256 + threadIdx.x] = next;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(stat_full);
         }
       }
       if (!ok) break;
@@ -588,6 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         done_ph ^= 1;
         tc_fence_after();
       }
+      if (warp >= 8) continue;
+      const int half = blk;
       // warps 0-3 store dV, warps 4-7 dK; the sink keys' rows go to their partial slot in fp32
       const float f = half ? a.scale : 1.f;
       const uint32_t acc = tmem + lanes + 256u + 128u * half;
@@ -630,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
     }
-  } else if (warp == 8) {
+  } else if (warp == kTma) {
     Cursor<SM::SLOTS> cur;
     uint32_t loads = 0, raw_phase = 0;
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
@@ -667,11 +660,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp < 11) {
+  } else if (warp < kMmaB + 1) {
     // x = 0: S^T of Q, then dV += P^T dO; x = 1: dP^T of dO, then dK += dS^T Q
-    const int x = warp_uniform(warp - 9);
+    const int x = warp_uniform(warp - kMmaA);
     Cursor<SM::SLOTS> cur;  // a step's query tile; its output gradients follow it
-    uint32_t kv_ph = 0, step = 0;
+    uint32_t kv_ph = 0, step = 0, turns = 0;
     const uint32_t ts = warp_uniform(tmem) + 128u * x, to = ts + 256u, kt = base + x * SM::TILE;
     const uint32_t formed = x ? dp_full : s_full, ready = x ? ds_full : p_full;
     DkvItem upcoming = dkv_item(a, blockIdx.x, sink_items, lane);
@@ -685,13 +678,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       // step n issues the second product of step n - 1 and the first of step n
       for (int n = 0; n <= steps && ok; ++n) {
         const Cursor<SM::SLOTS> qc = cur, oc = cur.next();
+        // dK behind the next step's S^T: the threads' next work waits for that
+        if (x == 1 && n < steps) {
+          if (!(ok = mbar_wait_warp(turn + 8 * (turns & 3), turns >> 2 & 1, abort_flag, err, kErrDkv))) break;
+          ++turns;
+        }
         if (n > 0) {
           if (!(ok = mbar_wait_warp(other.full(ring), other.phase, abort_flag, err, kErrDkv) &&
                      mbar_wait_warp(ready, step & 1, abort_flag, err, kErrDkv)))
             break;
           ++step;
           tc_fence_after();
-          mma_ab<DP>(to, ts, 64, other.data(ring), n > 1);
+          mma_ab<DP, 32>(to, ts, other.data(ring), n > 1);
           umma_commit_warp(other.empty(ring));
         }
         if (n == steps) break;
@@ -700,6 +698,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         mma_abt<DP>(ts, kt, c.data(ring));
         umma_commit_warp(formed);
+        if (x == 0) {
+          if (lane == 0) mbar_arrive(turn + 8 * (turns & 3));
+          ++turns;
+        }
         umma_commit_warp(c.empty(ring));
         if (n == steps - 1 && x == 0) umma_commit_warp(k_empty);
         other = x ? qc : oc;
@@ -730,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc<1>(tmem, 512);
+  if (warp == kMmaA) tmem_dealloc<1>(tmem, 512);
 }
 
 // dK and dV of the sink keys: the first tile's own sums, then the chunks'.
