@@ -39,10 +39,9 @@ constexpr int kErrForward = 0x201, kErrAlign = 0x204;
 template <int DP>
 struct FwdSmem {
   static constexpr uint32_t TILE = kAttnTile * DP * 2;
-  static constexpr int SLOTS = DP == 128 ? 4 : 8;
+  static constexpr int SLOTS = DP == 128 ? 4 : 8;  // even: keys in even slots, values in odd ones
   static constexpr uint32_t RING = 2 * TILE;
-  static constexpr uint32_t STAGE = RING + SLOTS * TILE;  // 4 KB a softmax warp, for the results on their way out
-  static constexpr uint32_t BARS = STAGE + 8 * 4096;
+  static constexpr uint32_t BARS = RING + SLOTS * TILE;
   // full[SLOTS], empty[SLOTS], raw[SLOTS], q full, q empty, s full[2], p full[2], o full[2], drain[2], turn[SLOTS / 2]
   static constexpr int NBARS = 3 * SLOTS + 10 + SLOTS / 2;
   static constexpr uint32_t BYTES = BARS + NBARS * 8 + 16;
@@ -150,6 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + 128u * s + lanes, to = tmem + 256u + 128u * s + lanes;
+    const bool wide = rows_wide(out, a.dim);
     uint32_t s_ph = 0, o_ph = 0;
     FwdItem next = fwd_item(a, blockIdx.x, units, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
@@ -247,10 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a query that saw no key: zeros and -infinity
       const float inv = any ? 1.f / l : 0.f;
       const int head = s ? w.head1 : w.head0;
-      store_rows<DP>(to, inv, !any, out + (((int64_t)w.t.b + row0) * a.heads + head) * a.dim, (int64_t)a.heads * a.dim,
-                     w.t.len - row0, a.dim, base + SM::STAGE + warp * 4096, lane);
+      const int64_t t = (int64_t)w.t.b + i;
+      store_row(to, 0, DP, inv, !any, out + (t * a.heads + head) * a.dim, i < w.t.len, a.dim, wide);
       if (i < w.t.len)
-        lse[(int64_t)head * a.n + w.t.b + i] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        lse[(int64_t)head * a.n + t] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
       tc_fence_before();
     }
   } else if (warp == 8) {

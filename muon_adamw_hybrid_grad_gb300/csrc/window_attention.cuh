@@ -332,57 +332,55 @@ __device__ __forceinline__ void mma_ab_few(uint32_t d_tmem, uint32_t a_tmem, uin
     umma_bf16_ts_warp(d_tmem, a_tmem + (ks >> 1) * STEP + (ks & 1) * 8, db + 128u * ks, id, add || ks != 0);
 }
 
-// Rows of a 128-row fp32 accumulator in TMEM, scaled and rounded to bf16, to
-// rows of the output that are `row_stride` elements apart; a warp handles its
-// own 32 lanes, its lane's row being valid where `rows` exceeds the lane. The
-// rows leave through 4 KB of the warp's shared memory, 64 columns at a time, so
-// that a store instruction covers four rows' whole 128-byte lines instead of 16
-// bytes of 32 rows. zero: store zeros and touch neither TMEM nor shared memory.
-template <int DP>
-__device__ __forceinline__ void store_rows(uint32_t taddr, float f, bool zero, __nv_bfloat16* out, int64_t row_stride,
-                                           int rows, int dim, uint32_t stage, int lane, int col0 = 0, int col1 = DP) {
-  const int q = lane & 7, r0 = lane >> 3;
+// Columns c0 .. c1 - 1 (multiples of 32) of this thread's row of an accumulator
+// in TMEM, times f and rounded to bf16, to its row of the output; zero: zeros, TMEM
+// holds nothing. `wide`: rows lie on 32-byte boundaries, and a lane stores whole
+// 32-byte sectors. (Rows gathered through shared memory leave in fewer
+// transactions, but the copy there and back took as long, and the operand whose
+// place it used could be loaded only after it.)
+__device__ __forceinline__ void store_row(uint32_t taddr, int c0, int c1, float f, bool zero, __nv_bfloat16* out, bool mine,
+                                          int dim, bool wide) {
 #pragma unroll 1
-  for (int c0 = col0; c0 < col1; c0 += 64) {
-    const int half = min(col1 - c0, 64);
-    const bool on = 8 * q < half && c0 + 8 * q < dim;
-    __nv_bfloat16* po = out + r0 * row_stride + c0 + 8 * q;
-    if (zero) {
-      for (int i = 0; i < 8; ++i)
-        if (on && 4 * i + r0 < rows) *reinterpret_cast<uint4*>(po + 4 * i * row_stride) = make_uint4(0, 0, 0, 0);
-      continue;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (h * 32 >= half) break;
+  for (int c = c0; c < c1; c += 32) {
+    uint32_t r[16];
+    if (!zero) {
       uint32_t o[32];
-      tmem_ld_32x32b_x32(taddr + c0 + 32 * h, o);
+      tmem_ld_32x32b_x32(taddr + c, o);
       tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t r[4];
+      for (int j = 0; j < 16; ++j) r[j] = op_pack_bf16(__uint_as_float(o[2 * j]) * f, __uint_as_float(o[2 * j + 1]) * f);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          r[e] = op_pack_bf16(__uint_as_float(o[8 * j + 2 * e]) * f, __uint_as_float(o[8 * j + 2 * e + 1]) * f);
-        // 16-byte chunk 4 h + j of this lane's 128-byte row, swizzled by the row
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4)),
-                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-                     : "memory");
-      }
+      for (int j = 0; j < 16; ++j) r[j] = 0u;
     }
-    __syncwarp();
+    if (!mine) continue;
+    if (wide) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = 4 * i + r0;
-      uint4 v;
-      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                   : "r"(stage + row * 128 + ((q ^ (row & 7)) << 4))
-                   : "memory");
-      if (on && row < rows) *reinterpret_cast<uint4*>(po + 4 * i * row_stride) = v;
+      for (int j = 0; j < 16; j += 8)
+        if (c + 2 * j < dim)
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + c + 2 * j), "r"(r[j]),
+                       "r"(r[j + 1]), "r"(r[j + 2]), "r"(r[j + 3]), "r"(r[j + 4]), "r"(r[j + 5]), "r"(r[j + 6]),
+                       "r"(r[j + 7])
+                       : "memory");
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; j += 4)
+        if (c + 2 * j < dim) *reinterpret_cast<uint4*>(out + c + 2 * j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
     }
-    __syncwarp();
   }
+}
+// Rows of `dim` elements from p on are on 32-byte boundaries.
+__device__ __forceinline__ bool rows_wide(const void* p, int dim) {
+  return dim % 16 == 0 && (reinterpret_cast<uintptr_t>(p) & 31) == 0;
+}
+
+// An asynchronous copy of four bytes to shared memory (zero where !on), and the
+// arrival on a barrier when this thread's copies have landed.
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Zeros in the rows of a tile from `rows` on, by a whole warp: tokens there

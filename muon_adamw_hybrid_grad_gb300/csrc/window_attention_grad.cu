@@ -77,19 +77,13 @@ __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant
 // it came from, each block in the first 16 of its own 32 columns. S of the next
 // tile is formed while the threads work on this one's, and dP of the next as
 // soon as this one's has been read.
-//
-// Results leave through the shared memory of dO, whose next tile is therefore
-// loaded after the epilogue; the next Q comes in as soon as the last S has been
-// formed.
 template <int DP>
 struct GradSmem {
   static constexpr uint32_t TILE = kAttnTile * DP * 2;
   static constexpr int SLOTS = DP == 128 ? 5 : 8;
   static constexpr uint32_t RING = 2 * TILE;                   // after Q and dO, or K and V
   static constexpr uint32_t STATS = RING + SLOTS * TILE;       // dkv: [2][nlse2, ndelta][128] of the query tiles
-  static constexpr uint32_t OWN = STATS + 2 * 2 * kAttnTile * 4;
-  static constexpr uint32_t STAGE = DP == 128 ? TILE : OWN;    // 4 KB to each of 8 warps
-  static constexpr uint32_t BARS = DP == 128 ? OWN : OWN + 8 * 4096;
+  static constexpr uint32_t BARS = STATS + 2 * 2 * kAttnTile * 4;
   // full[SLOTS], empty[SLOTS], raw[SLOTS], then each kernel's own
   static constexpr int NBARS = 3 * SLOTS + 16;
   static constexpr uint32_t BYTES = BARS + NBARS * 8 + 16;
@@ -137,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     ring.init(1);
-    mbar_init(q_full, 1), mbar_init(q_empty, 1), mbar_init(do_full, 1), mbar_init(do_empty, 8);
+    mbar_init(q_full, 1), mbar_init(q_empty, 1), mbar_init(do_full, 1), mbar_init(do_empty, 1);
     mbar_init(s_full, 1), mbar_init(s_full + 8, 1), mbar_init(dp_full, 1), mbar_init(dp_empty, kMathWarps);
     mbar_init(ds_full, kMathWarps), mbar_init(ds_full + 8, kMathWarps), mbar_init(dq_full, 1), mbar_init(drain, 1), mbar_init(drain + 8, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -163,10 +157,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t step = 0, s_ph = 0, dq_ph = 0;  // step: over all items; s_ph: a bit per S slot
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
+    const bool wide = rows_wide(dq, a.dim);
     DqItem next = dq_item(a, blockIdx.x, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       const DqItem w = next;
-      const int row0 = w.t.p0 + (row & ~31), i = w.t.p0 + row;
+      const int i = w.t.p0 + row;
       const int64_t t = (int64_t)w.t.b + i;
       const bool mine = i < w.t.len;
       const float nlse2 = mine ? a.nlse2[(int64_t)w.head * a.n + t] : -INFINITY;
@@ -229,19 +224,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         dq_ph ^= 1;
         tc_fence_after();
       }
-      if (warp < 8) {
-        // half of the columns to each four warps
-        const int half = warp >> 2;
-        store_rows<DP>(tmem + lanes + 384u, a.scale, w.steps == 0,
-                       dq + (((int64_t)w.t.b + row0) * a.heads + w.head) * a.dim, (int64_t)a.heads * a.dim,
-                       w.t.len - row0, a.dim, base + SM::STAGE + warp * 4096, lane, half * (DP / 2),
-                       (half + 1) * (DP / 2));
-        if (w.steps) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(do_empty);
-        }
-      }
+      // a quarter of the columns to each four warps (of 64: half to each of the first eight)
+      if (32 * blk < DP)
+        store_row(tmem + lanes + 384u, 32 * blk, 32 * blk + 32, a.scale, w.steps == 0,
+                  dq + (t * a.heads + w.head) * a.dim, mine, a.dim, wide);
       tc_fence_before();
     }
   } else if (warp == kTma) {
@@ -346,6 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_abt<DP>(tm + 256u, base + SM::TILE, pc.data(ring), n == 0 && sink ? few : kAttnTile);
         umma_commit_warp(dp_full);
         umma_commit_warp(pc.empty(ring));
+        if (n == steps - 1) umma_commit_warp(do_empty);
         pc.advance();
       }
     }
@@ -382,9 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // dO that belong to other samples. TMEM: S^T | dP^T | dV | dK; P^T overwrites
 // S^T and dS^T dP^T, each block in the first 16 of its own 32 columns. While the threads form
 // P^T of a step the tensor core runs the step before's dK and this one's dP^T;
-// while they form dS^T it runs dV and the next step's S^T. Results leave through
-// the shared memory of V, whose next tile is therefore loaded after the epilogue;
-// the next K comes in as soon as the last S^T has been formed.
+// while they form dS^T it runs dV and the next step's S^T.
 // First query tile that only the sinks reach in tile 0.
 __device__ __forceinline__ int first_sink_tile(const AttnArgs& a) {
   return a.window == 0 ? 0 : (kAttnTile - 1 + a.window - 1) / kAttnTile + 1;
@@ -454,9 +439,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     ring.init(2);
-    mbar_init(k_full, 1), mbar_init(k_empty, 1), mbar_init(v_full, 1), mbar_init(v_empty, 8);
+    mbar_init(k_full, 1), mbar_init(k_empty, 1), mbar_init(v_full, 1), mbar_init(v_empty, 1);
     mbar_init(s_full, 1), mbar_init(dp_full, 1), mbar_init(p_full, kMathWarps), mbar_init(ds_full, kMathWarps);
-    mbar_init(stat_full, kMathWarps), mbar_init(done, 2), mbar_init(drain, 1), mbar_init(drain + 8, 1);
+    mbar_init(stat_full, kMathWarps * 32), mbar_init(done, 2), mbar_init(drain, 1), mbar_init(drain + 8, 1);
     for (int i = 0; i < 4; ++i) mbar_init(turn + 8 * i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -485,26 +470,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = tmem + lanes + 32u * blk, tg = ts + 128u;
     uint32_t step = 0, done_ph = 0;
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
+    const bool wide = rows_wide(dk, a.dim) && rows_wide(dv, a.dim);
     DkvItem upcoming = dkv_item(a, blockIdx.x, sink_items, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       const DkvItem w = upcoming;
       const int steps = group * w.nq, row0 = w.t.p0 + (row & ~31), j = w.t.p0 + row;
-      // threads 0-127 bring nlse2 of a query tile, threads 128-255 ndelta
-      auto stat = [&](int head, int tile) {
-        const int i = tile * kAttnTile + row;
-        if (i >= w.t.len) return blk ? 0.f : -INFINITY;
-        return (blk ? a.ndelta : a.nlse2)[(int64_t)head * a.n + w.t.b + i];
+      // threads 0-127 bring nlse2 of a query tile, threads 128-255 ndelta. (Rows past the sample's end get zeros:
+      // their rows of Q and dO are zero too, and nothing comes of their weights.)
+      auto bring = [&](uint32_t to_step, int head, int tile) {
+        if (warp < 8) {
+          const int i = tile * kAttnTile + row;
+          const bool on = i < w.t.len;
+          copy4(smem_u32(stats + (to_step & 1) * 256 + threadIdx.x),
+                (warp < 4 ? a.nlse2 : a.ndelta) + (on ? (int64_t)head * a.n + w.t.b + i : 0), on);
+        }
+        // every thread arrives, those without a copy too: a warp that is behind then holds the phase after its own
+        copies_arrive(stat_full);
       };
       int head = w.kv * group, tile = w.q_lo;  // of the step
-      if (steps) {
-        if (warp < 8) stats[(step & 1) * 256 + threadIdx.x] = stat(head, tile);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(stat_full);
-      }
+      if (steps) bring(step, head, tile);
       for (int n = 0; n < steps && ok; ++n, ++step) {
         const int q0 = tile * kAttnTile;
         if (++tile == w.q_lo + w.nq) tile = w.q_lo, ++head;
-        const float next = warp < 8 && n + 1 < steps ? stat(head, tile) : 0.f;
         const float* st = stats + (step & 1) * 256 + 32 * blk;
         ok = mbar_wait_warp(stat_full, step & 1, abort_flag, err, kErrDkv) &&
              mbar_wait_warp(s_full, step & 1, abort_flag, err, kErrDkv);
@@ -548,6 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = mbar_wait_warp(dp_full, step & 1, abort_flag, err, kErrDkv);
         if (!ok) break;
         tc_fence_after();
+        // every warp is through with the step before, whose buffer this is: dP^T was formed after their dS^T
+        if (n + 1 < steps) bring(step + 1, head, tile);
         tmem_ld_32x32b_x32(tg, g);
         tmem_ld_wait();
 #pragma unroll
@@ -564,12 +553,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(ds_full);
-        if (n + 1 < steps) {
-          // every warp has read the buffer's last contents: it arrived after them for this step
-          if (warp < 8) stats[((step + 1) & 1) * 256 + threadIdx.x] = next;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(stat_full);
-        }
       }
       if (!ok) break;
       if (item + (int)gridDim.x < items) upcoming = dkv_item(a, item + gridDim.x, sink_items, lane);
@@ -579,17 +562,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         done_ph ^= 1;
         tc_fence_after();
       }
-      if (warp >= 8) continue;
-      const int half = blk;
-      // warps 0-3 store dV, warps 4-7 dK; the sink keys' rows go to their partial slot in fp32
-      const float f = half ? a.scale : 1.f;
-      const uint32_t acc = tmem + lanes + 256u + 128u * half;
+      // warps 0-7 store dV, warps 8-15 dK, half of the columns to each four; the sink keys' rows go to their partial
+      // slot in fp32 (and here too where this is not for them alone: window_sink_kernel writes them again, in full)
+      const int which = blk >> 1, c0 = (blk & 1) * (DP / 2), c1 = c0 + DP / 2;
+      const float f = which ? a.scale : 1.f;
+      const uint32_t acc = tmem + lanes + 256u + 128u * which;
       const int sinks = w.slot >= 0 ? a.sinks : 0;
       if (row0 < sinks) {
-        float* pp = partial + ((w.slot * a.kv_heads + w.kv) * 2 + half) * (int64_t)a.sinks * a.dim + (int64_t)j * a.dim;
+        float* pp = partial + ((w.slot * a.kv_heads + w.kv) * 2 + which) * (int64_t)a.sinks * a.dim + (int64_t)j * a.dim;
         const bool mine = j < sinks && j < w.t.len && w.slot < partial_slots;
 #pragma unroll 1
-        for (int c = 0; c < DP; c += 32) {
+        for (int c = c0; c < c1; c += 32) {
           uint32_t o[32];
           if (steps) {
             tmem_ld_32x32b_x32(acc + c, o);
@@ -611,18 +594,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!w.sink_only) {
-        // (rows of sink keys among these are written again, in full, by window_sink_kernel)
-        store_rows<DP>(acc, f, steps == 0, (half ? dk : dv) + (((int64_t)w.t.b + row0) * a.kv_heads + w.kv) * a.dim,
-                       (int64_t)a.kv_heads * a.dim, w.t.len - row0, a.dim, base + SM::STAGE + warp * 4096, lane);
-      }
-      if (steps) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_empty);
-      }
+      if (!w.sink_only)
+        store_row(acc, c0, c1, f, steps == 0, (which ? dk : dv) + (((int64_t)w.t.b + j) * a.kv_heads + w.kv) * a.dim,
+                  j < w.t.len, a.dim, wide);
       tc_fence_before();
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // (after a wait that ran out)
   } else if (warp == kTma) {
     Cursor<SM::SLOTS> cur;
     uint32_t loads = 0, raw_phase = 0;
@@ -703,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++turns;
         }
         umma_commit_warp(c.empty(ring));
-        if (n == steps - 1 && x == 0) umma_commit_warp(k_empty);
+        if (n == steps - 1) umma_commit_warp(x ? v_empty : k_empty);
         other = x ? qc : oc;
         cur.skip(2);
       }
@@ -762,14 +739,13 @@ __global__ void __launch_bounds__(256) window_sink_kernel(const __grid_constant_
   if (a.cu) sample_span(a, sample, b, len);
   const int chunks = sink_chunks(a, len, true), rows = min(a.sinks, len);
   const int64_t per = (int64_t)a.sinks * a.dim, slot = (int64_t)a.kv_heads * 2 * per;
-  for (int e = threadIdx.x; e < 2 * rows * a.dim; e += 256) {
+  for (int e = blockIdx.z * 256 + threadIdx.x; e < 2 * rows * a.dim; e += gridDim.z * 256) {
     const int which = e >= rows * a.dim, x = which ? e - rows * a.dim : e;
     const float* p = partial + (kv * 2 + which) * per + x;
     float s = p[sample * slot];
-    for (int c = 0; c < chunks; ++c) {
-      const int64_t at = (int64_t)a.n_seqs + first_chunk + c;
-      if (at < partial_slots) s += p[at * slot];
-    }
+    const int64_t at = (int64_t)a.n_seqs + first_chunk, n = min((int64_t)chunks, partial_slots - at);
+#pragma unroll 8
+    for (int64_t c = 0; c < n; ++c) s += p[(at + c) * slot];
     const int row = x / a.dim;
     (which ? dk : dv)[(((int64_t)b + row) * a.kv_heads + kv) * a.dim + (x - row * a.dim)] = __float2bfloat16_rn(s);
   }
@@ -804,7 +780,8 @@ cudaError_t attn_backward(AttnArgs a, const CUtensorMap& q, const CUtensorMap& k
   e = a.dim > 64 ? run_backward<128>(a, q, k, v, dout, g, err, sms, st)
                  : run_backward<64>(a, q, k, v, dout, g, err, sms, st);
   if (e != cudaSuccess || a.sinks == 0) return e;
-  return op_launch(window_sink_kernel, dim3((unsigned)a.n_seqs, (unsigned)a.kv_heads), dim3(256), 0, st, 1, a,
+  return op_launch(window_sink_kernel, dim3((unsigned)a.n_seqs, (unsigned)a.kv_heads, (unsigned)((2 * a.sinks * a.dim + 255) / 256)),
+                   dim3(256), 0, st, 1, a,
                    static_cast<const float*>(g.partial), g.partial_slots, g.dk, g.dv);
 }
 
