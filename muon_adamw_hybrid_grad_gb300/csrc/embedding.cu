@@ -58,15 +58,24 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const W* __restrict
 }
 
 // ---- gradient of few tokens: one launch ----
-// Block b owns rows b, b + B, b + 2 B, ... (neighbouring ids are of like
+// Blocks b + B y own rows b, b + B, b + 2 B, ... (neighbouring ids are of like
 // frequency in most vocabularies, so consecutive rows would load the first
-// blocks with all the frequent ones). Its warps read all ids, each a contiguous
-// part, and keep the tokens of the block's rows in order; then every row is
-// written once: zeros, or the sum over its tokens by the warps, a warp to 32 VEC
-// columns, eight rows of dout in flight.
+// blocks with all the frequent ones) and the 32 VEC columns of slab y. Their
+// warps read all ids, each a contiguous part, and keep the tokens of the block's
+// rows in order; then every row is written once: zeros, or the sum over its
+// tokens, eight rows of dout in flight. A warp takes a row of up to kFewTokens
+// tokens; the warps share a row of more, each the part of its own ids.
+//
+// Bound by the writes of a dense gradient: 93 us for 16 tokens of 151936 x 2048
+// (bf16, 6.7 TB/s). Against the sorted form, ids drawn by a Zipf law: 6.2 us (22)
+// at 1024 tokens of 1000 x 256, 105 (119) at 1024 of 151936 x 2048, 117 (122) at
+// 4096 of these. Where all tokens have one id its row's block takes longest: 113
+// (117) at 1024, 172 (126) at 4096. Past that the reading of all ids by all blocks
+// costs more than the sort.
 constexpr int kDirectTokens = 4096;
-constexpr int kDirectRows = 4096;  // rows of a block, at most: bits of its presence map
+constexpr int kDirectRows = 4096;  // rows of a block, at most: its counters lie in shared memory
 constexpr int kDirectWarps = kThreads / 32;
+constexpr uint32_t kFewTokens = 16;
 
 struct DirectArgs {
   const void* ids;
@@ -81,15 +90,15 @@ struct DirectArgs {
 template <typename D, typename G, int VEC>
 __global__ void __launch_bounds__(kThreads) embedding_direct_kernel(const __grid_constant__ DirectArgs a,
                                                                     const D* __restrict__ dout, G* __restrict__ grad) {
-  extern __shared__ uint32_t list[];  // [warp][per]: row of the block << 12 | position
-  __shared__ uint32_t present[kDirectRows / 32];
+  extern __shared__ uint32_t list[];  // [warp][per]: row of the block << 12 | position; then a counter per row
   __shared__ int count[kDirectWarps];
   __shared__ float sums[kDirectWarps][32][VEC + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t B = gridDim.x, b = blockIdx.x;
   const int rows = (int)((a.vocab - b + B - 1) / B);
   const int per = ((a.n + kDirectWarps - 1) / kDirectWarps + 31) / 32 * 32;
-  for (int i = threadIdx.x; i < (rows + 31) / 32; i += kThreads) present[i] = 0;
+  uint32_t* tokens = list + kDirectWarps * per;
+  for (int i = threadIdx.x; i < rows; i += kThreads) tokens[i] = 0;
   __syncthreads();
   pdl_launch();
   pdl_wait();
@@ -112,7 +121,7 @@ __global__ void __launch_bounds__(kThreads) embedding_direct_kernel(const __grid
         const uint32_t hits = __ballot_sync(0xffffffffu, hit);
         if (hit) {
           mine[found + __popc(hits & ((1u << lane) - 1))] = r << 12 | (uint32_t)(t0 + 32 * u + lane);
-          atomicOr(present + (r >> 5), 1u << (r & 31));
+          atomicAdd(tokens + r, 1u);
         }
         found += __popc(hits);
       }
@@ -120,19 +129,9 @@ __global__ void __launch_bounds__(kThreads) embedding_direct_kernel(const __grid
     if (lane == 0) count[warp] = found;
   }
   __syncthreads();
-  constexpr int COLS = 32 * VEC;
-  if (!a.accumulate) {
-    float zero[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) zero[i] = 0.f;
-    for (int r = warp; r < rows; r += kDirectWarps) {
-      if (present[r >> 5] >> (r & 31) & 1) continue;
-      G* p = grad + (int64_t)(b + (uint32_t)r * B) * a.gstride;
-      for (int c = lane * VEC; c < a.width; c += COLS) store_vec<VEC>(p + c, zero);
-    }
-  }
+  const int c = (int)(blockIdx.y * 32 + lane) * VEC;
   // s += the rows of the tokens of the block's row r in list q, in order
-  auto add_list = [&](float (&s)[VEC], uint32_t r, int q, int c) {
+  auto add_list = [&](float (&s)[VEC], uint32_t r, int q) {
     for (int e0 = 0; e0 < count[q]; e0 += 32) {
       const uint32_t entry = e0 + lane < count[q] ? list[q * per + e0 + lane] : UINT_MAX;
       uint32_t hits = __ballot_sync(0xffffffffu, (entry >> 12) == r && e0 + lane < count[q]);
@@ -159,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) embedding_direct_kernel(const __grid
       }
     }
   };
-  auto write = [&](uint32_t r, int c, const float (&s)[VEC]) {
+  auto write = [&](uint32_t r, const float (&s)[VEC]) {
     if (c >= a.width) return;
     G* p = grad + (int64_t)(b + r * B) * a.gstride + c;
     float y[VEC];
@@ -173,40 +172,51 @@ __global__ void __launch_bounds__(kThreads) embedding_direct_kernel(const __grid
     }
     store_vec<VEC>(p, y);
   };
-  // A task is 32 VEC columns of a row. With as many tasks as warps each warp
-  // takes its own; with fewer all warps share each, a list to a warp.
-  const int passes = (a.width + COLS - 1) / COLS;
-  int tasks = 0;
-  for (int w = 0; w < (rows + 31) / 32; ++w) tasks += __popc(present[w]);
-  tasks *= passes;
-  const bool share = tasks < kDirectWarps;
-  int task = 0;
-  for (int w = 0; w < (rows + 31) / 32; ++w) {
-    for (uint32_t left = present[w]; left; left &= left - 1) {
-      const uint32_t r = w * 32 + __ffs(left) - 1;
-      for (int pass = 0; pass < passes; ++pass, ++task) {
-        const int c = pass * COLS + lane * VEC;
-        float s[VEC];
+  // rows of no token, whole ones shared out over the slabs, and of few: every eighth row to a warp (the first rows of
+  // a block are those of the most frequent ids)
+  for (int r0 = 0; r0 < rows; r0 += 32 * kDirectWarps) {
+    const int row = r0 + lane * kDirectWarps + warp;
+    const uint32_t mine = row < rows ? tokens[row] : UINT_MAX;
+    if (!a.accumulate) {
+      float zero[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) s[i] = 0.f;
-        if (share) {
-          add_list(s, r, warp, c);
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) sums[warp][lane][i] = s[i];
-          __syncthreads();
-          if (warp == 0) {
-#pragma unroll
-            for (int q = 1; q < kDirectWarps; ++q)
-#pragma unroll
-              for (int i = 0; i < VEC; ++i) s[i] += sums[q][lane][i];
-            write(r, c, s);
-          }
-          __syncthreads();
-        } else if (task % kDirectWarps == warp) {
-          for (int q = 0; q < kDirectWarps; ++q) add_list(s, r, q, c);
-          write(r, c, s);
-        }
+      for (int i = 0; i < VEC; ++i) zero[i] = 0.f;
+      const bool ours = mine == 0u && (row / kDirectWarps) % gridDim.y == blockIdx.y;
+      for (uint32_t left = __ballot_sync(0xffffffffu, ours); left; left &= left - 1) {
+        const uint32_t r = r0 + (__ffs(left) - 1) * kDirectWarps + warp;
+        G* p = grad + (int64_t)(b + r * B) * a.gstride;
+        for (int x = lane * VEC; x < a.width; x += 32 * VEC) store_vec<VEC>(p + x, zero);
       }
+    }
+    for (uint32_t left = __ballot_sync(0xffffffffu, mine >= 1u && mine <= kFewTokens); left; left &= left - 1) {
+      const uint32_t r = r0 + (__ffs(left) - 1) * kDirectWarps + warp;
+      float s[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) s[i] = 0.f;
+      for (int q = 0; q < kDirectWarps; ++q) add_list(s, r, q);
+      write(r, s);
+    }
+  }
+  // rows of many, by all warps
+  for (int r0 = 0; r0 < rows; r0 += 32) {
+    for (uint32_t left = __ballot_sync(0xffffffffu, r0 + lane < rows && tokens[r0 + lane] > kFewTokens); left;
+         left &= left - 1) {
+      const uint32_t r = r0 + __ffs(left) - 1;
+      float s[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) s[i] = 0.f;
+      add_list(s, r, warp);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) sums[warp][lane][i] = s[i];
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int q = 1; q < kDirectWarps; ++q)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) s[i] += sums[q][lane][i];
+        write(r, s);
+      }
+      __syncthreads();
     }
   }
 }
@@ -623,14 +633,20 @@ cudaError_t run_sums(const SumArgs& a, int64_t chunks, const void* dout, void* g
                    dim3((unsigned)((chunks + kJoinChunks - 2) / kJoinChunks), (unsigned)((all + slabs - 1) / slabs)), dim3(kThreads), 0, st, 1, a, static_cast<G*>(grad), slabs);
 }
 
-// Blocks of the one-launch gradient: up to eight an SM.
-int64_t direct_blocks(int64_t vocab, int sms) { return vocab < 8 * sms ? vocab : 8 * (int64_t)sms; }
+// Blocks along x of the one-launch gradient: up to eight an SM over all slabs.
+int64_t direct_blocks(int64_t vocab, int64_t width, int vec, int sms) {
+  const int64_t slabs = (width + 32 * vec - 1) / (32 * vec), most = (8 * (int64_t)sms + slabs - 1) / slabs;
+  return vocab < most ? vocab : most;
+}
 
 template <typename D, typename G, int VEC>
 cudaError_t run_direct(const DirectArgs& a, int64_t blocks, const void* dout, void* grad, cudaStream_t st) {
   const int per = ((a.n + kDirectWarps - 1) / kDirectWarps + 31) / 32 * 32;
-  return op_launch(embedding_direct_kernel<D, G, VEC>, dim3((unsigned)blocks), dim3(kThreads),
-                   (size_t)kDirectWarps * per * 4, st, 1, a, static_cast<const D*>(dout), static_cast<G*>(grad));
+  const int64_t rows = (a.vocab + blocks - 1) / blocks;
+  return op_launch(embedding_direct_kernel<D, G, VEC>,
+                   dim3((unsigned)blocks, (unsigned)((a.width + 32 * VEC - 1) / (32 * VEC))), dim3(kThreads),
+                   (size_t)(kDirectWarps * per + rows) * 4, st, 1, a, static_cast<const D*>(dout),
+                   static_cast<G*>(grad));
 }
 
 // f(dout type, gradient type, vector width) for the call's own.
@@ -714,7 +730,7 @@ ma_status muon_adamw_embedding_backward(const void* dout, int dout_dtype, int64_
   if (e != cudaSuccess) return op_cuda(e, "device query");
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   const bool vec = rows_vec(dout, dout_dtype, dout_stride, width) && rows_vec(grad, grad_dtype, grad_stride, width);
-  const int64_t blocks = direct_blocks(vocab, sms);
+  const int64_t blocks = direct_blocks(vocab, width, vec ? 8 : 1, sms);
   if (n_tokens <= kDirectTokens && (vocab + blocks - 1) / blocks <= kDirectRows) {
     DirectArgs d{};
     d.ids = ids;

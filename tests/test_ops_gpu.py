@@ -526,3 +526,19 @@ def test_window_attention_many_calls(ops, dim):
             same &= (a == b).all()
     assert bool(same)
     ops.check()
+
+
+def test_attention_block_example():
+    """The operators and the optimizer together: the loss of one batch falls."""
+    import importlib.util
+    import os
+
+    from conftest import ROOT
+
+    spec = importlib.util.spec_from_file_location("attention_block", os.path.join(ROOT, "examples", "attention_block.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    losses = example.run(30)
+    assert all(np.isfinite(losses))
+    assert losses[-1] < 0.9 * losses[0]
+    assert example.run(3) == losses[:3]
