@@ -40,7 +40,7 @@ struct AttnGrad {
 cudaError_t attn_backward(AttnArgs a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                           const CUtensorMap& dout, const AttnGrad& g, int* err, int sms, cudaStream_t st);
 
-// Query tiles of a chunk of the gradient for sink keys (see window_dkv_kernel).
+// Query tiles of a chunk of the gradient for sink keys (see dkv_part).
 constexpr int kSinkChunk = 8;
 
 // Upper bound of the tiles of `rows` tokens that any cut into samples gives,

@@ -5,9 +5,9 @@
 //   dS = P (dP - delta),  dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K.
 //
 // window_stats_kernel  lse2 and delta of every query and head.
-// window_dq_kernel     a CTA to 128 queries of a head, walking their key tiles.
-// window_dkv_kernel    a CTA to 128 keys of a key head, walking the query
-//                      tiles of every head that reads it.
+// window_grad_kernel   dkv_part: 128 keys of a key head, walking the query tiles
+//                      of every head that reads it; then dq_part: 128 queries of
+//                      a head, walking their key tiles.
 // window_sink_kernel   joins the partial sums of the sink keys.
 //
 // Seven products instead of the five that one kernel would need, because S and
@@ -84,8 +84,7 @@ struct GradSmem {
   static constexpr uint32_t RING = 2 * TILE;                   // after Q and dO, or K and V
   static constexpr uint32_t STATS = RING + SLOTS * TILE;       // dkv: [2][nlse2, ndelta][128] of the query tiles
   static constexpr uint32_t BARS = STATS + 2 * 2 * kAttnTile * 4;
-  // full[SLOTS], empty[SLOTS], raw[SLOTS], then each kernel's own
-  static constexpr int NBARS = 3 * SLOTS + 16;
+  static constexpr int NBARS = 6 * SLOTS + 29;  // dK/dV's and dQ's
   static constexpr uint32_t BYTES = BARS + NBARS * 8 + 16;
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
@@ -108,58 +107,53 @@ __device__ __forceinline__ DqItem dq_item(const AttnArgs& a, int item, int lane)
   return w;
 }
 
+// The dQ items of a CTA. CTAs that have one dK/dV item less than others (those from
+// `extra` on) take `more` dQ items ahead of the rest, which go round in the
+// opposite order to the dK/dV items.
+struct DqWalk {
+  int cta, ctas, extra, more;
+  __device__ __forceinline__ int at(int i) const {
+    const int light = ctas - extra, first = cta >= extra ? more : 0;
+    return i < first ? cta - extra + i * light : more * light + (ctas - 1 - cta) + (i - first) * ctas;
+  }
+};
+
 template <int DP>
-__global__ void __launch_bounds__(kThreads, 1)
-    window_dq_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tmQ,
-                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                     const __grid_constant__ CUtensorMap tmDO, __nv_bfloat16* __restrict__ dq, int* __restrict__ err) {
+struct DqBarriers {
+  static constexpr int COUNT = 3 * GradSmem<DP>::SLOTS + 13;
+};
+
+template <int DP, bool MATH>
+__device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                        const CUtensorMap& tmV, const CUtensorMap& tmDO,
+                                        __nv_bfloat16* __restrict__ dq, int* __restrict__ err, volatile int* abort_flag,
+                                        uint32_t base, uint32_t bars, uint32_t tmem, const DqWalk& walk, bool set_up) {
   using SM = GradSmem<DP>;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  // two words after the barriers: the TMEM base and the abort flag
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::BARS + SM::NBARS * 8);
-  volatile int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t base = smem_u32(smem), bars = base + SM::BARS;
   Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, bars + SM::SLOTS * 16, SM::TILE};
+  // full[SLOTS], empty[SLOTS], raw[SLOTS], then
   const uint32_t own = bars + 3 * SM::SLOTS * 8, q_full = own, q_empty = own + 8, do_full = own + 16,
                  do_empty = own + 24, s_full = own + 32, dp_full = own + 48, dp_empty = own + 56, ds_full = own + 64,
                  dq_full = own + 80, drain = own + 88;
-  if (base & 1023u) {  // the swizzle's phase is that of the address
-    if (threadIdx.x == 0) atomicCAS(err, 0, kErrAlign);
-    return;
-  }
-  if (threadIdx.x == 0) {
-    *abort_flag = 0;
+  if (set_up) {
     ring.init(1);
     mbar_init(q_full, 1), mbar_init(q_empty, 1), mbar_init(do_full, 1), mbar_init(do_empty, 1);
     mbar_init(s_full, 1), mbar_init(s_full + 8, 1), mbar_init(dp_full, 1), mbar_init(dp_empty, kMathWarps);
     mbar_init(ds_full, kMathWarps), mbar_init(ds_full + 8, kMathWarps), mbar_init(dq_full, 1), mbar_init(drain, 1), mbar_init(drain + 8, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    return;
   }
-  if (warp == kMmaA) tmem_alloc<1>(smem_u32(tmem_slot), 512);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  pdl_launch();
-  pdl_wait();
   const int items = a.heads * count_units(a, lane, [](int len, bool) { return (len + kAttnTile - 1) / kAttnTile; });
   const int few = sink_columns(a);
-  bool ok = true;
-  // (one instruction for all four warps of a group)
-  if (warp < kMathWarps)
-    regs_up<kMathRegs>();
-  else
-    regs_down<kOtherRegs>();
+  bool ok = *abort_flag == 0;
 
-  if (warp < kMathWarps) {
+  if constexpr (MATH) {
     const int blk = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t step = 0, s_ph = 0, dq_ph = 0;  // step: over all items; s_ph: a bit per S slot
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     const bool wide = rows_wide(dq, a.dim);
-    DqItem next = dq_item(a, blockIdx.x, lane);
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+    DqItem next = dq_item(a, walk.at(0), lane);
+    for (int nth = 0; walk.at(nth) < items && ok; ++nth) {
       const DqItem w = next;
       const int i = w.t.p0 + row;
       const int64_t t = (int64_t)w.t.b + i;
@@ -217,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(ds_full + 8 * slot);
       }
       if (!ok) break;
-      if (item + (int)gridDim.x < items) next = dq_item(a, item + gridDim.x, lane);
+      if (walk.at(nth + 1) < items) next = dq_item(a, walk.at(nth + 1), lane);
       if (w.steps) {
         ok = mbar_wait_warp(dq_full, dq_ph, abort_flag, err, kErrDq);
         if (!ok) break;
@@ -233,8 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kTma) {
     Cursor<SM::SLOTS> cur;
     uint32_t loads = 0, raw_phase = 0;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const DqItem w = dq_item(a, item, lane);
+    for (int i = 0; walk.at(i) < items && ok; ++i) {
+      const DqItem w = dq_item(a, walk.at(i), lane);
       if (lane == 0) {
         for (int n = 0; n < w.steps && ok; ++n) {
           const int at = w.tile(n) * kAttnTile;
@@ -270,11 +264,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     Cursor<SM::SLOTS> sc;  // the next S's key tile
     uint32_t q_ph = 0, ds_ph = 0;  // ds_ph: a bit per S slot
     const uint32_t tm = warp_uniform(tmem);
-    DqItem next = dq_item(a, blockIdx.x, lane);
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+    DqItem next = dq_item(a, walk.at(0), lane);
+    for (int i = 0; walk.at(i) < items && ok; ++i) {
       const int steps = warp_uniform(next.steps), sink = warp_uniform((int)next.k.sink);
       if (steps == 0) {
-        if (item + (int)gridDim.x < items) next = dq_item(a, item + gridDim.x, lane);
+        if (walk.at(i + 1) < items) next = dq_item(a, walk.at(i + 1), lane);
         continue;
       }
       Cursor<SM::SLOTS> qc = sc;  // the next dQ's key tile
@@ -289,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       ok = mbar_wait_warp(q_full, q_ph, abort_flag, err, kErrDq) && issue_s(0) && (steps == 1 || issue_s(1));
       q_ph ^= 1;
-      if (item + (int)gridDim.x < items) next = dq_item(a, item + gridDim.x, lane);
+      if (walk.at(i + 1) < items) next = dq_item(a, walk.at(i + 1), lane);
       for (int n = 0; n < steps && ok; ++n) {
         // (a barrier to each slot of S: the threads need nothing of this warp for the step after, so that they
         // may be through with it before this wait, and one barrier's phases would have passed twice)
@@ -315,10 +309,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     Cursor<SM::SLOTS> pc;  // a key tile, then its value tile
     uint32_t q_ph = 0, step = 0;
     const uint32_t tm = warp_uniform(tmem);
-    DqItem next = dq_item(a, blockIdx.x, lane);
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+    DqItem next = dq_item(a, walk.at(0), lane);
+    for (int i = 0; walk.at(i) < items && ok; ++i) {
       const int steps = warp_uniform(next.steps), sink = warp_uniform((int)next.k.sink);
-      if (item + (int)gridDim.x < items) next = dq_item(a, item + gridDim.x, lane);
+      if (walk.at(i + 1) < items) next = dq_item(a, walk.at(i + 1), lane);
       if (steps == 0) continue;
       ok = mbar_wait_warp(do_full, q_ph, abort_flag, err, kErrDq);
       q_ph ^= 1;
@@ -342,8 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     Cursor<SM::SLOTS> cur;
     uint32_t raw_phase = 0;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const DqItem w = dq_item(a, item, lane);
+    for (int i = 0; walk.at(i) < items && ok; ++i) {
+      const DqItem w = dq_item(a, walk.at(i), lane);
       if (w.steps == 0) continue;
       cur.skip(2 * w.steps - 2);
       const int valid = w.t.len - w.tile(w.steps - 1) * kAttnTile;  // only the last tile can be ragged
@@ -354,10 +348,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == kMmaA) tmem_dealloc<1>(tmem, 512);
 }
 
 // ---- dK and dV ----
@@ -414,65 +404,44 @@ __device__ __forceinline__ DkvItem dkv_item(const AttnArgs& a, int item, int sin
 }
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads, 1)
-    window_dkv_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tmQ,
-                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                      const __grid_constant__ CUtensorMap tmDO, __nv_bfloat16* __restrict__ dk,
-                      __nv_bfloat16* __restrict__ dv, float* __restrict__ partial, int64_t partial_slots,
-                      int* __restrict__ err) {
+struct DkvBarriers {
+  static constexpr int COUNT = 3 * GradSmem<DP>::SLOTS + 16;
+};
+
+template <int DP, bool MATH>
+__device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                                         const CUtensorMap& tmV, const CUtensorMap& tmDO,
+                                         __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv,
+                                         float* __restrict__ partial, int64_t partial_slots, int* __restrict__ err,
+                                         volatile int* abort_flag, float* stats, uint32_t base, uint32_t bars,
+                                         uint32_t tmem, int cta, int ctas, int sink_items, int items, bool set_up) {
   using SM = GradSmem<DP>;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  // two words after the barriers: the TMEM base and the abort flag
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::BARS + SM::NBARS * 8);
-  volatile int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t base = smem_u32(smem), bars = base + SM::BARS;
   Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, bars + SM::SLOTS * 16, SM::TILE};
+  // full[SLOTS], empty[SLOTS], raw[SLOTS], then
   const uint32_t own = bars + 3 * SM::SLOTS * 8, k_full = own, k_empty = own + 8, v_full = own + 16,
                  v_empty = own + 24, s_full = own + 32, dp_full = own + 40, p_full = own + 48, ds_full = own + 56,
                  stat_full = own + 64, done = own + 72, drain = own + 80, turn = own + 96;
-  float* stats = reinterpret_cast<float*>(smem + SM::STATS);
-  if (base & 1023u) {  // the swizzle's phase is that of the address
-    if (threadIdx.x == 0) atomicCAS(err, 0, kErrAlign);
-    return;
-  }
-  if (threadIdx.x == 0) {
-    *abort_flag = 0;
+  if (set_up) {
     ring.init(2);
     mbar_init(k_full, 1), mbar_init(k_empty, 1), mbar_init(v_full, 1), mbar_init(v_empty, 1);
     mbar_init(s_full, 1), mbar_init(dp_full, 1), mbar_init(p_full, kMathWarps), mbar_init(ds_full, kMathWarps);
     mbar_init(stat_full, kMathWarps * 32), mbar_init(done, 2), mbar_init(drain, 1), mbar_init(drain + 8, 1);
     for (int i = 0; i < 4; ++i) mbar_init(turn + 8 * i, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    return;
   }
-  if (warp == kMmaA) tmem_alloc<1>(smem_u32(tmem_slot), 512);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  pdl_launch();
-  pdl_wait();
   const int group = a.heads / a.kv_heads;
-  const int sink_items =
-      a.kv_heads * count_units(a, lane, [&](int len, bool live) { return sink_chunks(a, len, live); });
-  const int items = sink_items +
-                    a.kv_heads * count_units(a, lane, [](int len, bool) { return (len + kAttnTile - 1) / kAttnTile; });
   bool ok = true;
-  // (one instruction for all four warps of a group)
-  if (warp < kMathWarps)
-    regs_up<kMathRegs>();
-  else
-    regs_down<kOtherRegs>();
 
-  if (warp < kMathWarps) {
+  if constexpr (MATH) {
     const int blk = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + 32u * blk, tg = ts + 128u;
     uint32_t step = 0, done_ph = 0;
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     const bool wide = rows_wide(dk, a.dim) && rows_wide(dv, a.dim);
-    DkvItem upcoming = dkv_item(a, blockIdx.x, sink_items, lane);
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+    DkvItem upcoming = dkv_item(a, cta, sink_items, lane);
+    for (int item = cta; item < items && ok; item += ctas) {
       const DkvItem w = upcoming;
       const int steps = group * w.nq, row0 = w.t.p0 + (row & ~31), j = w.t.p0 + row;
       // threads 0-127 bring nlse2 of a query tile, threads 128-255 ndelta. (Rows past the sample's end get zeros:
@@ -555,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(ds_full);
       }
       if (!ok) break;
-      if (item + (int)gridDim.x < items) upcoming = dkv_item(a, item + gridDim.x, sink_items, lane);
+      if (item + ctas < items) upcoming = dkv_item(a, item + ctas, sink_items, lane);
       if (steps) {
         ok = mbar_wait_warp(done, done_ph, abort_flag, err, kErrDkv);
         if (!ok) break;
@@ -603,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kTma) {
     Cursor<SM::SLOTS> cur;
     uint32_t loads = 0, raw_phase = 0;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+    for (int item = cta; item < items && ok; item += ctas) {
       const DkvItem w = dkv_item(a, item, sink_items, lane);
       if (lane == 0) {
         const int steps = group * w.nq;
@@ -644,10 +613,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t kv_ph = 0, step = 0, turns = 0;
     const uint32_t ts = warp_uniform(tmem) + 128u * x, to = ts + 256u, kt = base + x * SM::TILE;
     const uint32_t formed = x ? dp_full : s_full, ready = x ? ds_full : p_full;
-    DkvItem upcoming = dkv_item(a, blockIdx.x, sink_items, lane);
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+    DkvItem upcoming = dkv_item(a, cta, sink_items, lane);
+    for (int item = cta; item < items && ok; item += ctas) {
       const int steps = warp_uniform(group * upcoming.nq);
-      if (item + (int)gridDim.x < items) upcoming = dkv_item(a, item + gridDim.x, sink_items, lane);
+      if (item + ctas < items) upcoming = dkv_item(a, item + ctas, sink_items, lane);
       if (steps == 0) continue;
       ok = mbar_wait_warp(x ? v_full : k_full, kv_ph, abort_flag, err, kErrDkv);
       kv_ph ^= 1;
@@ -692,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     Cursor<SM::SLOTS> cur;
     uint32_t raw_phase = 0;
-    for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+    for (int item = cta; item < items && ok; item += ctas) {
       const DkvItem w = dkv_item(a, item, sink_items, lane);
       const int valid = w.t.len - (w.q_lo + w.nq - 1) * kAttnTile;  // of a head's last query tile
       if (w.nq > 0)
@@ -705,6 +674,74 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
     }
+  }
+}
+
+__device__ __forceinline__ void parts_sync() {
+  tc_fence_before();
+  asm volatile("barrier.sync 1, %0;" ::"n"(kThreads) : "memory");
+  tc_fence_after();
+}
+
+// dK and dV, then dQ: one persistent CTA per SM runs its items of the one and then
+// its items of the other, so that no SM waits in between for the slowest. (Two
+// launches took 47 us on six samples of 7 to 1021 tokens and 428 us on 16384 tokens,
+// this one 43 and 426.)
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_grad_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tmQ,
+                       const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const __grid_constant__ CUtensorMap tmDO, __nv_bfloat16* __restrict__ dq,
+                       __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv, float* __restrict__ partial,
+                       int64_t partial_slots, int* __restrict__ err) {
+  using SM = GradSmem<DP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  // two words after the barriers: the TMEM base and the abort flag
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::BARS + SM::NBARS * 8);
+  volatile int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  float* stats = reinterpret_cast<float*>(smem + SM::STATS);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = smem_u32(smem), bars = base + SM::BARS, bars2 = bars + DkvBarriers<DP>::COUNT * 8;
+  if (base & 1023u) {  // the swizzle's phase is that of the address
+    if (threadIdx.x == 0) atomicCAS(err, 0, kErrAlign);
+    return;
+  }
+  const DqWalk none{0, 1, 0, 0};
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    dkv_part<DP, false>(a, tmQ, tmK, tmV, tmDO, dk, dv, partial, partial_slots, err, abort_flag, stats, base, bars, 0, 0, 1, 0, 0,
+                 true);
+    dq_part<DP, false>(a, tmQ, tmK, tmV, tmDO, dq, err, abort_flag, base, bars2, 0, none, true);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaA) tmem_alloc<1>(smem_u32(tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch();
+  pdl_wait();
+  const int cta = blockIdx.x, ctas = gridDim.x, group = a.heads / a.kv_heads;
+  const int sink_items =
+      a.kv_heads * count_units(a, lane, [&](int len, bool live) { return sink_chunks(a, len, live); });
+  const int items = sink_items +
+                    a.kv_heads * count_units(a, lane, [](int len, bool) { return (len + kAttnTile - 1) / kAttnTile; });
+  // a dK/dV item is four products for each head of the group, a dQ item three
+  const DqWalk walk{cta, ctas, items % ctas, max(1, group * 4 / 3)};
+  // (the registers are given by one instruction for all four warps of a group; at the barrier in between every
+  // product and copy of the first part has ended)
+  if (warp < kMathWarps) {
+    regs_up<kMathRegs>();
+    dkv_part<DP, true>(a, tmQ, tmK, tmV, tmDO, dk, dv, partial, partial_slots, err, abort_flag, stats, base, bars, tmem,
+                       cta, ctas, sink_items, items, false);
+    parts_sync();
+    dq_part<DP, true>(a, tmQ, tmK, tmV, tmDO, dq, err, abort_flag, base, bars2, tmem, walk, false);
+  } else {
+    regs_down<kOtherRegs>();
+    dkv_part<DP, false>(a, tmQ, tmK, tmV, tmDO, dk, dv, partial, partial_slots, err, abort_flag, stats, base, bars,
+                        tmem, cta, ctas, sink_items, items, false);
+    parts_sync();
+    dq_part<DP, false>(a, tmQ, tmK, tmV, tmDO, dq, err, abort_flag, base, bars2, tmem, walk, false);
   }
   tc_fence_before();
   __syncthreads();
@@ -754,17 +791,11 @@ __global__ void __launch_bounds__(256) window_sink_kernel(const __grid_constant_
 template <int DP>
 cudaError_t run_backward(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                          const CUtensorMap& dout, const AttnGrad& g, int* err, int sms, cudaStream_t st) {
-  const int64_t tiles = attn_max_tiles(a.n, a.n_seqs, kAttnTile);
-  cudaError_t e = op_smem_limit<window_dq_kernel<DP>>((int)GradSmem<DP>::BYTES);
-  if (e == cudaSuccess) e = op_smem_limit<window_dkv_kernel<DP>>((int)GradSmem<DP>::BYTES);
+  const int64_t tiles = attn_max_tiles(a.n, a.n_seqs, kAttnTile), most = tiles * a.heads;
+  const cudaError_t e = op_smem_limit<window_grad_kernel<DP>>((int)GradSmem<DP>::BYTES);
   if (e != cudaSuccess) return e;
-  int64_t grid = tiles * a.heads;
-  e = op_launch(window_dq_kernel<DP>, dim3((unsigned)(grid < sms ? grid : sms)), dim3(kThreads), GradSmem<DP>::BYTES, st,
-                1, a, q, k, v, dout, g.dq, err);
-  if (e != cudaSuccess) return e;
-  grid = (tiles + g.partial_slots) * a.kv_heads;
-  return op_launch(window_dkv_kernel<DP>, dim3((unsigned)(grid < sms ? grid : sms)), dim3(kThreads),
-                   GradSmem<DP>::BYTES, st, 1, a, q, k, v, dout, g.dk, g.dv, g.partial, g.partial_slots, err);
+  return op_launch(window_grad_kernel<DP>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads),
+                   GradSmem<DP>::BYTES, st, 1, a, q, k, v, dout, g.dq, g.dk, g.dv, g.partial, g.partial_slots, err);
 }
 
 }  // namespace
