@@ -258,6 +258,12 @@ __device__ __forceinline__ uint32_t idesc_bf16(int m, int n, bool b_mn_major) {
   return d;
 }
 
+// Shared memory to a 3-D tensor; elements outside it are not written.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* tm, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tm), "r"(src),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
 // Rank-3 form of tma_load_2d.
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
   asm volatile(

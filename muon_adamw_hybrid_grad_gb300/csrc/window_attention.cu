@@ -21,7 +21,7 @@
 //                   left the tensor core idle half the time (174 us for 16360
 //                   tokens of 16 heads of 128, window 1024);
 //   warp 11         clears the rows of a sample's last value tile that belong to
-//                   other samples.
+//                   other samples, and stores the finished tiles.
 // TMEM: S0 | S1 | O0 | O1, 128 columns each.
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since it
@@ -39,11 +39,12 @@ constexpr int kErrForward = 0x201, kErrAlign = 0x204;
 template <int DP>
 struct FwdSmem {
   static constexpr uint32_t TILE = kAttnTile * DP * 2;
-  static constexpr int SLOTS = DP == 128 ? 4 : 8;  // even: keys in even slots, values in odd ones
+  static constexpr int SLOTS = DP == 128 ? 4 : 8;
   static constexpr uint32_t RING = 2 * TILE;
   static constexpr uint32_t BARS = RING + SLOTS * TILE;
-  // full[SLOTS], empty[SLOTS], raw[SLOTS], q full, q empty, s full[2], p full[2], o full[2], drain[2], turn[SLOTS / 2]
-  static constexpr int NBARS = 3 * SLOTS + 10 + SLOTS / 2;
+  // full[SLOTS], empty[SLOTS], raw[SLOTS], q full, q empty, s full[2], p full[2], o full[2], drain[2], turn[SLOTS / 2],
+  // staged[SLOTS]
+  static constexpr int NBARS = 4 * SLOTS + 10 + SLOTS / 2;
   static constexpr uint32_t BYTES = BARS + NBARS * 8 + 16;
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
@@ -84,6 +85,7 @@ struct FwdItem {
   SampleTile t;
   PairTiles k;
   int head0, head1, kv;
+  bool staged;  // both tiles leave through the ring, two positions after the last values
 };
 
 // Work item: a pair of query tiles. by_head: of two heads, else of one head.
@@ -98,6 +100,7 @@ __device__ __forceinline__ FwdItem fwd_item(const AttnArgs& a, int item, int uni
   w.head0 = by_head ? 2 * u : u;
   w.head1 = by_head ? 2 * u + 1 : u;
   w.kv = w.head0 / (a.heads / a.kv_heads);
+  w.staged = w.k.steps > 0 && w.t.p0 + rows <= w.t.len;
   return w;
 }
 
@@ -105,7 +108,7 @@ template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     window_forward_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                          __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int* __restrict__ err, int units) {
+                          const __grid_constant__ CUtensorMap tmO, __nv_bfloat16* __restrict__ out, float* __restrict__ lse, int* __restrict__ err, int units) {
   using SM = FwdSmem<DP>;
   extern __shared__ __align__(1024) uint8_t smem[];
   // two words after the barriers: the TMEM base and the abort flag
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = smem_u32(smem), bars = base + SM::BARS;
   Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, bars + SM::SLOTS * 16, SM::TILE};
   const uint32_t q_full = bars + 3 * SM::SLOTS * 8, q_empty = q_full + 8, s_full = q_full + 16, p_full = q_full + 32,
-                 o_full = q_full + 48, drain = q_full + 64, turn = q_full + 80;
+                 o_full = q_full + 48, drain = q_full + 64, turn = q_full + 80, staged = turn + 4 * SM::SLOTS;
   if (base & 1023u) {  // the swizzle's phase is that of the address
     if (threadIdx.x == 0) atomicCAS(err, 0, kErrAlign);
     return;
@@ -125,6 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ring.init(2);
     mbar_init(q_full, 1), mbar_init(q_empty, 2), mbar_init(drain, 1), mbar_init(drain + 8, 1);
     for (int i = 0; i < SM::SLOTS / 2; ++i) mbar_init(turn + 8 * i, 1);
+    for (int i = 0; i < SM::SLOTS; ++i) mbar_init(staged + 8 * i, 4);
     for (int s = 0; s < 2; ++s) mbar_init(s_full + 8 * s, 1), mbar_init(p_full + 8 * s, 128), mbar_init(o_full + 8 * s, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -151,6 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = tmem + 128u * s + lanes, to = tmem + 256u + 128u * s + lanes;
     const bool wide = rows_wide(out, a.dim);
     uint32_t s_ph = 0, o_ph = 0;
+    Cursor<SM::SLOTS> cur;
     FwdItem next = fwd_item(a, blockIdx.x, units, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       const FwdItem w = next;
@@ -248,7 +253,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = any ? 1.f / l : 0.f;
       const int head = s ? w.head1 : w.head0;
       const int64_t t = (int64_t)w.t.b + i;
-      store_row(to, 0, DP, inv, !any, out + (t * a.heads + head) * a.dim, i < w.t.len, a.dim, wide);
+      cur.skip(2 * w.k.steps);
+      if (w.staged) {
+        const Cursor<SM::SLOTS> mine = s ? cur.next() : cur;
+        ok = mbar_wait_warp(mine.full(ring), mine.phase, abort_flag, err, kErrForward);
+        if (!ok) break;
+        stage_row(to, 0, DP, inv, !any, mine.data(ring), row);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(staged + 8 * mine.slot);
+        cur.skip(2);
+      } else {
+        store_row(to, 0, DP, inv, !any, out + (t * a.heads + head) * a.dim, i < w.t.len, a.dim, wide);
+      }
       if (i < w.t.len)
         lse[(int64_t)head * a.n + t] = any ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
       tc_fence_before();
@@ -279,6 +295,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        for (int s = 0; w.staged && s < 2 && ok; ++s) {
+          ok = mbar_wait_in(cur.empty(ring), cur.phase ^ 1, abort_flag, err, kErrForward);
+          if (!ok) break;
+          mbar_arrive(cur.full(ring));
+          cur.advance();
+        }
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
     }
@@ -291,14 +313,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 11) {
     // ---- MMA ----
     Cursor<SM::SLOTS> cur;
-    uint32_t q_ph = 0, p_ph = 0;
+    uint32_t q_ph = 0, p_ph = 0, turns = 0;
     const int s = warp_uniform(warp - 9), few = sink_columns(a);
     const uint32_t ts = warp_uniform(tmem) + 128u * s, to = ts + 256u, qt = base + s * SM::TILE;
     const uint32_t sf = s_full + 8 * s, pf = p_full + 8 * s, of = o_full + 8 * s;
     FwdItem next = fwd_item(a, blockIdx.x, units, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       const int steps = warp_uniform(next.k.steps), first = warp_uniform(s ? next.k.a1 : next.k.a0),
-                last = warp_uniform(s ? next.k.b1 : next.k.b0), sink = warp_uniform((int)(s ? next.k.z1 : next.k.z0));
+                last = warp_uniform(s ? next.k.b1 : next.k.b0), sink = warp_uniform((int)(s ? next.k.z1 : next.k.z0)), staged_out = warp_uniform((int)next.staged);
       if (steps == 0 || !(ok = mbar_wait_warp(q_full, q_ph, abort_flag, err, kErrForward))) {
         if (item + (int)gridDim.x < items) next = fwd_item(a, item + gridDim.x, units, lane);
         continue;
@@ -314,8 +336,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // both softmaxes would start when both S are there, and products and softmaxes would alternate instead of
       // overlapping (4000 cycles a step of both tiles instead of 2700).
       for (int n = 0; n <= steps; ++n) {
-        if (n < steps && s == 1 && !(ok = mbar_wait_warp(turn + 4 * cur.slot, cur.phase, abort_flag, err, kErrForward)))
-          break;
+        // (the first tile's warp is never as many turns ahead as there are barriers: the slot of its keys would not
+        // be free)
+        const uint32_t my_turn = turn + 8 * (turns % (SM::SLOTS / 2)), turn_ph = turns / (SM::SLOTS / 2) & 1;
+        if (n < steps && s == 1 && !(ok = mbar_wait_warp(my_turn, turn_ph, abort_flag, err, kErrForward))) break;
         if (n > 0) {
           if (!(ok = mbar_wait_warp(vc.full(ring), vc.phase, abort_flag, err, kErrForward))) break;
           if (pend) {
@@ -340,7 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_abt<DP>(ts, qt, cur.data(ring), whole ? kAttnTile : few);
           umma_commit_warp(sf);
         }
-        if (s == 0 && lane == 0) mbar_arrive(turn + 4 * cur.slot);  // (keys lie in even slots)
+        if (s == 0 && lane == 0) mbar_arrive(my_turn);
+        ++turns;
         umma_commit_warp(cur.empty(ring));
         if (n == steps - 1) umma_commit_warp(q_empty);
         cur.advance();
@@ -348,14 +373,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         cur.advance();
         if (n == 0 && item + (int)gridDim.x < items) next = fwd_item(a, item + gridDim.x, units, lane);
       }
+      if (staged_out) cur.skip(2);
     }
     umma_commit_warp(drain + 8 * s);
     if (lane == 0) drain_wait(drain + 8 * s, 0);
     __syncwarp();
   } else {
-    // ---- rows of other samples ----
+    // ---- rows of other samples, staged tiles ----
     Cursor<SM::SLOTS> cur;
-    uint32_t raw_phase = 0;
+    uint32_t raw_phase = 0, staged_phase = 0;
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       const FwdItem w = fwd_item(a, item, units, lane);
       if (w.k.steps == 0) continue;
@@ -363,6 +389,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int valid = w.t.len - w.k.tile(w.k.steps - 1) * kAttnTile;  // only the last tile can be ragged
       if (valid < kAttnTile) ok = clear_slot<DP>(ring, cur, valid, raw_phase, lane, abort_flag, err, kErrForward);
       cur.advance();
+      for (int s = 0; w.staged && s < 2 && ok; ++s) {
+        ok = store_slot<DP>(ring, cur, staged, staged_phase, &tmO,
+                            w.t.b + w.t.p0 + (s && w.head0 == w.head1 ? kAttnTile : 0), s ? w.head1 : w.head0, 2, lane,
+                            abort_flag, err, kErrForward);
+        cur.advance();
+      }
     }
   }
   tc_fence_before();
@@ -373,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int DP>
 cudaError_t run_forward(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                        __nv_bfloat16* out, float* lse, int* err, int sms, cudaStream_t st) {
+                        const CUtensorMap& o, __nv_bfloat16* out, float* lse, int* err, int sms, cudaStream_t st) {
   const int group = a.heads / a.kv_heads;
   const int units = group % 2 == 0 ? a.heads / 2 : a.heads;
   const int rows = group % 2 == 0 ? kAttnTile : 2 * kAttnTile;
@@ -381,7 +413,7 @@ cudaError_t run_forward(const AttnArgs& a, const CUtensorMap& q, const CUtensorM
   const cudaError_t e = op_smem_limit<window_forward_kernel<DP>>((int)FwdSmem<DP>::BYTES);
   if (e != cudaSuccess) return e;
   return op_launch(window_forward_kernel<DP>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads),
-                   FwdSmem<DP>::BYTES, st, 1, a, q, k, v, out, lse, err, units);
+                   FwdSmem<DP>::BYTES, st, 1, a, q, k, v, o, out, lse, err, units);
 }
 
 // ---- host ----
@@ -435,8 +467,13 @@ AttnArgs args_of(const ma_window_attention* d) {
 }
 
 struct Maps {
-  CUtensorMap q, k, v, dout;
+  CUtensorMap q, k, v, dout, out;
 };
+
+// The operator's own tensors lie without gaps.
+bool dense_map(CUtensorMap* tm, const void* base, const ma_window_attention* d, int heads) {
+  return attn_map(tm, base, d->head_dim, d->n_tokens, heads, (int64_t)heads * d->head_dim, d->head_dim);
+}
 
 bool maps_of(const ma_window_attention* d, Maps* m) {
   return attn_map(&m->q, d->q, d->head_dim, d->n_tokens, d->n_heads, d->q_token_stride, d->q_head_stride) &&
@@ -488,9 +525,9 @@ bool attn_map(CUtensorMap* tm, const void* base, int dim, int64_t tokens, int64_
 }
 
 cudaError_t attn_forward(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                         __nv_bfloat16* out, float* lse, int* err, int sms, cudaStream_t st) {
-  return a.dim > 64 ? run_forward<128>(a, q, k, v, out, lse, err, sms, st)
-                    : run_forward<64>(a, q, k, v, out, lse, err, sms, st);
+                         const CUtensorMap& o, __nv_bfloat16* out, float* lse, int* err, int sms, cudaStream_t st) {
+  return a.dim > 64 ? run_forward<128>(a, q, k, v, o, out, lse, err, sms, st)
+                    : run_forward<64>(a, q, k, v, o, out, lse, err, sms, st);
 }
 
 }  // namespace ma
@@ -511,8 +548,9 @@ ma_status muon_adamw_window_attention(const ma_window_attention* d, void* out, f
     cudaError_t e = op_device(&sms, &err);
     if (e != cudaSuccess) return op_cuda(e, "device query");
     Maps m;
-    if (!maps_of(d, &m)) return op_fail(MA_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor");
-    e = attn_forward(args_of(d), m.q, m.k, m.v, static_cast<__nv_bfloat16*>(out), lse, err, sms,
+    if (!maps_of(d, &m) || !dense_map(&m.out, out, d, d->n_heads))
+      return op_fail(MA_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor");
+    e = attn_forward(args_of(d), m.q, m.k, m.v, m.out, static_cast<__nv_bfloat16*>(out), lse, err, sms,
                      static_cast<cudaStream_t>(cuda_stream));
     if (e != cudaSuccess) return op_cuda(e, "attention launch");
   }
@@ -553,10 +591,13 @@ ma_status muon_adamw_window_attention_backward(const ma_window_attention* d, con
     cudaError_t e = op_device(&sms, &err);
     if (e != cudaSuccess) return op_cuda(e, "device query");
     Maps m;
-    if (!maps_of(d, &m) || !attn_map(&m.dout, dout, d->head_dim, d->n_tokens, d->n_heads, dout_token_stride, dout_head_stride))
+    AttnGrad g{};
+    if (!maps_of(d, &m) ||
+        !attn_map(&m.dout, dout, d->head_dim, d->n_tokens, d->n_heads, dout_token_stride, dout_head_stride) ||
+        !dense_map(&g.tm_dq, dq, d, d->n_heads) || !dense_map(&g.tm_dk, dk, d, d->n_kv_heads) ||
+        !dense_map(&g.tm_dv, dv, d, d->n_kv_heads))
       return op_fail(MA_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor");
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    AttnGrad g{};
     g.dout = static_cast<const __nv_bfloat16*>(dout);
     g.out = static_cast<const __nv_bfloat16*>(out);
     g.do_ts = dout_token_stride;

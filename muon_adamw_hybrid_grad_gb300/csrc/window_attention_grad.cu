@@ -84,7 +84,7 @@ struct GradSmem {
   static constexpr uint32_t RING = 2 * TILE;                   // after Q and dO, or K and V
   static constexpr uint32_t STATS = RING + SLOTS * TILE;       // dkv: [2][nlse2, ndelta][128] of the query tiles
   static constexpr uint32_t BARS = STATS + 2 * 2 * kAttnTile * 4;
-  static constexpr int NBARS = 6 * SLOTS + 29;  // dK/dV's and dQ's
+  static constexpr int NBARS = 8 * SLOTS + 29;  // dK/dV's and dQ's
   static constexpr uint32_t BYTES = BARS + NBARS * 8 + 16;
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
@@ -93,6 +93,7 @@ struct DqItem {
   SampleTile t;
   KeyTiles k;
   int steps, head, kv;
+  bool staged;  // leaves through the ring, in the position after the last values
   __device__ __forceinline__ int tile(int n) const { return k.sink ? (n == 0 ? 0 : k.lo + n - 1) : k.lo + n; }
 };
 __device__ __forceinline__ DqItem dq_item(const AttnArgs& a, int item, int lane) {
@@ -104,6 +105,7 @@ __device__ __forceinline__ DqItem dq_item(const AttnArgs& a, int item, int lane)
   w.t.p0 = w.t.index * kAttnTile;
   w.k = key_tiles(a, w.t.live, w.t.len, w.t.p0);
   w.steps = (w.k.sink ? 1 : 0) + max(0, w.k.hi - w.k.lo + 1);
+  w.staged = w.steps > 0 && w.t.p0 + kAttnTile <= w.t.len;
   return w;
 }
 
@@ -120,23 +122,24 @@ struct DqWalk {
 
 template <int DP>
 struct DqBarriers {
-  static constexpr int COUNT = 3 * GradSmem<DP>::SLOTS + 13;
+  static constexpr int COUNT = 4 * GradSmem<DP>::SLOTS + 13;
 };
 
 template <int DP, bool MATH>
 __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tmQ, const CUtensorMap& tmK,
-                                        const CUtensorMap& tmV, const CUtensorMap& tmDO,
+                                        const CUtensorMap& tmV, const CUtensorMap& tmDO, const CUtensorMap& tmDQ,
                                         __nv_bfloat16* __restrict__ dq, int* __restrict__ err, volatile int* abort_flag,
                                         uint32_t base, uint32_t bars, uint32_t tmem, const DqWalk& walk, bool set_up) {
   using SM = GradSmem<DP>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, bars + SM::SLOTS * 16, SM::TILE};
-  // full[SLOTS], empty[SLOTS], raw[SLOTS], then
-  const uint32_t own = bars + 3 * SM::SLOTS * 8, q_full = own, q_empty = own + 8, do_full = own + 16,
+  // full[SLOTS], empty[SLOTS], raw[SLOTS], staged[SLOTS], then
+  const uint32_t staged = bars + 3 * SM::SLOTS * 8, own = bars + 4 * SM::SLOTS * 8, q_full = own, q_empty = own + 8, do_full = own + 16,
                  do_empty = own + 24, s_full = own + 32, dp_full = own + 48, dp_empty = own + 56, ds_full = own + 64,
                  dq_full = own + 80, drain = own + 88;
   if (set_up) {
     ring.init(1);
+    for (int i = 0; i < SM::SLOTS; ++i) mbar_init(staged + 8 * i, kMathWarps / (DP == 64 ? 2 : 1));
     mbar_init(q_full, 1), mbar_init(q_empty, 1), mbar_init(do_full, 1), mbar_init(do_empty, 1);
     mbar_init(s_full, 1), mbar_init(s_full + 8, 1), mbar_init(dp_full, 1), mbar_init(dp_empty, kMathWarps);
     mbar_init(ds_full, kMathWarps), mbar_init(ds_full + 8, kMathWarps), mbar_init(dq_full, 1), mbar_init(drain, 1), mbar_init(drain + 8, 1);
@@ -150,6 +153,7 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
     const int blk = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t step = 0, s_ph = 0, dq_ph = 0;  // step: over all items; s_ph: a bit per S slot
+    Cursor<SM::SLOTS> cur;
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     const bool wide = rows_wide(dq, a.dim);
     DqItem next = dq_item(a, walk.at(0), lane);
@@ -218,8 +222,18 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
         dq_ph ^= 1;
         tc_fence_after();
       }
+      cur.skip(2 * w.steps);
       // a quarter of the columns to each four warps (of 64: half to each of the first eight)
-      if (32 * blk < DP)
+      if (w.staged) {
+        if (32 * blk < DP) {
+          ok = mbar_wait_warp(cur.full(ring), cur.phase, abort_flag, err, kErrDq);
+          if (!ok) break;
+          stage_row(tmem + lanes + 384u, 32 * blk, 32 * blk + 32, a.scale, false, cur.data(ring), row);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(staged + 8 * cur.slot);
+        }
+        cur.advance();
+      } else if (32 * blk < DP)
         store_row(tmem + lanes + 384u, 32 * blk, 32 * blk + 32, a.scale, w.steps == 0,
                   dq + (t * a.heads + w.head) * a.dim, mine, a.dim, wide);
       tc_fence_before();
@@ -247,6 +261,13 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
           }
         }
         if (w.steps) ++loads;
+        if (w.staged && ok) {
+          ok = mbar_wait_in(cur.empty(ring), cur.phase ^ 1, abort_flag, err, kErrDq);
+          if (ok) {
+            mbar_arrive(cur.full(ring));
+            cur.advance();
+          }
+        }
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
     }
@@ -266,7 +287,8 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
     const uint32_t tm = warp_uniform(tmem);
     DqItem next = dq_item(a, walk.at(0), lane);
     for (int i = 0; walk.at(i) < items && ok; ++i) {
-      const int steps = warp_uniform(next.steps), sink = warp_uniform((int)next.k.sink);
+      const int steps = warp_uniform(next.steps), sink = warp_uniform((int)next.k.sink),
+                out = warp_uniform((int)next.staged);
       if (steps == 0) {
         if (walk.at(i + 1) < items) next = dq_item(a, walk.at(i + 1), lane);
         continue;
@@ -300,6 +322,7 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
         if (n + 2 < steps) ok = issue_s(n + 2);
       }
       if (ok) umma_commit_warp(dq_full);
+      if (out) sc.advance();
     }
     umma_commit_warp(drain);
     if (lane == 0) drain_wait(drain, 0);
@@ -311,7 +334,8 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
     const uint32_t tm = warp_uniform(tmem);
     DqItem next = dq_item(a, walk.at(0), lane);
     for (int i = 0; walk.at(i) < items && ok; ++i) {
-      const int steps = warp_uniform(next.steps), sink = warp_uniform((int)next.k.sink);
+      const int steps = warp_uniform(next.steps), sink = warp_uniform((int)next.k.sink),
+                out = warp_uniform((int)next.staged);
       if (walk.at(i + 1) < items) next = dq_item(a, walk.at(i + 1), lane);
       if (steps == 0) continue;
       ok = mbar_wait_warp(do_full, q_ph, abort_flag, err, kErrDq);
@@ -329,13 +353,14 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
         if (n == steps - 1) umma_commit_warp(do_empty);
         pc.advance();
       }
+      if (out) pc.advance();
     }
     umma_commit_warp(drain + 8);
     if (lane == 0) drain_wait(drain + 8, 0);
     __syncwarp();
   } else {
     Cursor<SM::SLOTS> cur;
-    uint32_t raw_phase = 0;
+    uint32_t raw_phase = 0, staged_phase = 0;
     for (int i = 0; walk.at(i) < items && ok; ++i) {
       const DqItem w = dq_item(a, walk.at(i), lane);
       if (w.steps == 0) continue;
@@ -344,6 +369,11 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
       for (int kv = 0; kv < 2; ++kv) {
         if (valid < kAttnTile && ok)
           ok = clear_slot<DP>(ring, cur, valid, raw_phase, lane, abort_flag, err, kErrDq);
+        cur.advance();
+      }
+      if (w.staged && ok) {
+        ok = store_slot<DP>(ring, cur, staged, staged_phase, &tmDQ, w.t.b + w.t.p0, w.head, 1, lane, abort_flag, err,
+                            kErrDq);
         cur.advance();
       }
     }
@@ -375,6 +405,7 @@ struct DkvItem {
   int kv, q_lo, nq; // query tiles q_lo .. q_lo + nq - 1, for each head of the group
   int64_t slot;     // partial slot of the sink keys, -1: none
   bool sink_only;   // a chunk for the sink keys alone
+  bool staged;      // dV and dK leave through the ring, in the positions after the last step's tiles
 };
 __device__ __forceinline__ DkvItem dkv_item(const AttnArgs& a, int item, int sink_items, int lane) {
   DkvItem w;
@@ -400,30 +431,32 @@ __device__ __forceinline__ DkvItem dkv_item(const AttnArgs& a, int item, int sin
     }
     w.slot = a.sinks > 0 && w.t.index == 0 && w.t.live ? w.t.sample : -1;
   }
+  w.staged = !w.sink_only && w.nq > 0 && w.t.p0 + kAttnTile <= w.t.len;
   return w;
 }
 
 template <int DP>
 struct DkvBarriers {
-  static constexpr int COUNT = 3 * GradSmem<DP>::SLOTS + 16;
+  static constexpr int COUNT = 4 * GradSmem<DP>::SLOTS + 16;
 };
 
 template <int DP, bool MATH>
 __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& tmQ, const CUtensorMap& tmK,
-                                         const CUtensorMap& tmV, const CUtensorMap& tmDO,
-                                         __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv,
+                                         const CUtensorMap& tmV, const CUtensorMap& tmDO, const CUtensorMap& tmDK,
+                                         const CUtensorMap& tmDV, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv,
                                          float* __restrict__ partial, int64_t partial_slots, int* __restrict__ err,
                                          volatile int* abort_flag, float* stats, uint32_t base, uint32_t bars,
                                          uint32_t tmem, int cta, int ctas, int sink_items, int items, bool set_up) {
   using SM = GradSmem<DP>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, bars + SM::SLOTS * 16, SM::TILE};
-  // full[SLOTS], empty[SLOTS], raw[SLOTS], then
-  const uint32_t own = bars + 3 * SM::SLOTS * 8, k_full = own, k_empty = own + 8, v_full = own + 16,
+  // full[SLOTS], empty[SLOTS], raw[SLOTS], staged[SLOTS], then
+  const uint32_t staged = bars + 3 * SM::SLOTS * 8, own = bars + 4 * SM::SLOTS * 8, k_full = own, k_empty = own + 8, v_full = own + 16,
                  v_empty = own + 24, s_full = own + 32, dp_full = own + 40, p_full = own + 48, ds_full = own + 56,
                  stat_full = own + 64, done = own + 72, drain = own + 80, turn = own + 96;
   if (set_up) {
     ring.init(2);
+    for (int i = 0; i < SM::SLOTS; ++i) mbar_init(staged + 8 * i, kMathWarps / 2);
     mbar_init(k_full, 1), mbar_init(k_empty, 1), mbar_init(v_full, 1), mbar_init(v_empty, 1);
     mbar_init(s_full, 1), mbar_init(dp_full, 1), mbar_init(p_full, kMathWarps), mbar_init(ds_full, kMathWarps);
     mbar_init(stat_full, kMathWarps * 32), mbar_init(done, 2), mbar_init(drain, 1), mbar_init(drain + 8, 1);
@@ -438,6 +471,7 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + 32u * blk, tg = ts + 128u;
     uint32_t step = 0, done_ph = 0;
+    Cursor<SM::SLOTS> cur;
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     const bool wide = rows_wide(dk, a.dim) && rows_wide(dv, a.dim);
     DkvItem upcoming = dkv_item(a, cta, sink_items, lane);
@@ -563,7 +597,16 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
           }
         }
       }
-      if (!w.sink_only)
+      cur.skip(2 * steps);
+      if (w.staged) {
+        const Cursor<SM::SLOTS> mine = which ? cur.next() : cur;
+        ok = mbar_wait_warp(mine.full(ring), mine.phase, abort_flag, err, kErrDkv);
+        if (!ok) break;
+        stage_row(acc, c0, c1, f, false, mine.data(ring), row);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(staged + 8 * mine.slot);
+        cur.skip(2);
+      } else if (!w.sink_only)
         store_row(acc, c0, c1, f, steps == 0, (which ? dk : dv) + (((int64_t)w.t.b + j) * a.kv_heads + w.kv) * a.dim,
                   j < w.t.len, a.dim, wide);
       tc_fence_before();
@@ -595,6 +638,12 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
           if (++tile == w.q_lo + w.nq) tile = w.q_lo, ++head;
         }
         if (steps) ++loads;
+        for (int x = 0; w.staged && x < 2 && ok; ++x) {
+          ok = mbar_wait_in(cur.empty(ring), cur.phase ^ 1, abort_flag, err, kErrDkv);
+          if (!ok) break;
+          mbar_arrive(cur.full(ring));
+          cur.advance();
+        }
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
     }
@@ -615,7 +664,7 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
     const uint32_t formed = x ? dp_full : s_full, ready = x ? ds_full : p_full;
     DkvItem upcoming = dkv_item(a, cta, sink_items, lane);
     for (int item = cta; item < items && ok; item += ctas) {
-      const int steps = warp_uniform(group * upcoming.nq);
+      const int steps = warp_uniform(group * upcoming.nq), out = warp_uniform((int)upcoming.staged);
       if (item + ctas < items) upcoming = dkv_item(a, item + ctas, sink_items, lane);
       if (steps == 0) continue;
       ok = mbar_wait_warp(x ? v_full : k_full, kv_ph, abort_flag, err, kErrDkv);
@@ -654,13 +703,14 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
         cur.skip(2);
       }
       if (ok) umma_commit_warp(done);
+      if (out) cur.skip(2);
     }
     umma_commit_warp(drain + 8 * x);
     if (lane == 0) drain_wait(drain + 8 * x, 0);
     __syncwarp();
   } else {
     Cursor<SM::SLOTS> cur;
-    uint32_t raw_phase = 0;
+    uint32_t raw_phase = 0, staged_phase = 0;
     for (int item = cta; item < items && ok; item += ctas) {
       const DkvItem w = dkv_item(a, item, sink_items, lane);
       const int valid = w.t.len - (w.q_lo + w.nq - 1) * kAttnTile;  // of a head's last query tile
@@ -673,6 +723,11 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
             cur.advance();
           }
         }
+      for (int x = 0; w.staged && x < 2 && ok; ++x) {
+        ok = store_slot<DP>(ring, cur, staged, staged_phase, x ? &tmDK : &tmDV, w.t.b + w.t.p0, w.kv, 2, lane, abort_flag,
+                            err, kErrDkv);
+        cur.advance();
+      }
     }
   }
 }
@@ -691,7 +746,9 @@ template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     window_grad_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                       const __grid_constant__ CUtensorMap tmDO, __nv_bfloat16* __restrict__ dq,
+                       const __grid_constant__ CUtensorMap tmDO, const __grid_constant__ CUtensorMap tmDQ,
+                       const __grid_constant__ CUtensorMap tmDK, const __grid_constant__ CUtensorMap tmDV,
+                       __nv_bfloat16* __restrict__ dq,
                        __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv, float* __restrict__ partial,
                        int64_t partial_slots, int* __restrict__ err) {
   using SM = GradSmem<DP>;
@@ -709,9 +766,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const DqWalk none{0, 1, 0, 0};
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    dkv_part<DP, false>(a, tmQ, tmK, tmV, tmDO, dk, dv, partial, partial_slots, err, abort_flag, stats, base, bars, 0, 0, 1, 0, 0,
+    dkv_part<DP, false>(a, tmQ, tmK, tmV, tmDO, tmDK, tmDV, dk, dv, partial, partial_slots, err, abort_flag, stats, base, bars, 0, 0, 1, 0, 0,
                  true);
-    dq_part<DP, false>(a, tmQ, tmK, tmV, tmDO, dq, err, abort_flag, base, bars2, 0, none, true);
+    dq_part<DP, false>(a, tmQ, tmK, tmV, tmDO, tmDQ, dq, err, abort_flag, base, bars2, 0, none, true);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaA) tmem_alloc<1>(smem_u32(tmem_slot), 512);
@@ -732,16 +789,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   // product and copy of the first part has ended)
   if (warp < kMathWarps) {
     regs_up<kMathRegs>();
-    dkv_part<DP, true>(a, tmQ, tmK, tmV, tmDO, dk, dv, partial, partial_slots, err, abort_flag, stats, base, bars, tmem,
+    dkv_part<DP, true>(a, tmQ, tmK, tmV, tmDO, tmDK, tmDV, dk, dv, partial, partial_slots, err, abort_flag, stats, base, bars, tmem,
                        cta, ctas, sink_items, items, false);
     parts_sync();
-    dq_part<DP, true>(a, tmQ, tmK, tmV, tmDO, dq, err, abort_flag, base, bars2, tmem, walk, false);
+    dq_part<DP, true>(a, tmQ, tmK, tmV, tmDO, tmDQ, dq, err, abort_flag, base, bars2, tmem, walk, false);
   } else {
     regs_down<kOtherRegs>();
-    dkv_part<DP, false>(a, tmQ, tmK, tmV, tmDO, dk, dv, partial, partial_slots, err, abort_flag, stats, base, bars,
+    dkv_part<DP, false>(a, tmQ, tmK, tmV, tmDO, tmDK, tmDV, dk, dv, partial, partial_slots, err, abort_flag, stats, base, bars,
                         tmem, cta, ctas, sink_items, items, false);
     parts_sync();
-    dq_part<DP, false>(a, tmQ, tmK, tmV, tmDO, dq, err, abort_flag, base, bars2, tmem, walk, false);
+    dq_part<DP, false>(a, tmQ, tmK, tmV, tmDO, tmDQ, dq, err, abort_flag, base, bars2, tmem, walk, false);
   }
   tc_fence_before();
   __syncthreads();
@@ -795,7 +852,7 @@ cudaError_t run_backward(const AttnArgs& a, const CUtensorMap& q, const CUtensor
   const cudaError_t e = op_smem_limit<window_grad_kernel<DP>>((int)GradSmem<DP>::BYTES);
   if (e != cudaSuccess) return e;
   return op_launch(window_grad_kernel<DP>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads),
-                   GradSmem<DP>::BYTES, st, 1, a, q, k, v, dout, g.dq, g.dk, g.dv, g.partial, g.partial_slots, err);
+                   GradSmem<DP>::BYTES, st, 1, a, q, k, v, dout, g.tm_dq, g.tm_dk, g.tm_dv, g.dq, g.dk, g.dv, g.partial, g.partial_slots, err);
 }
 
 }  // namespace
