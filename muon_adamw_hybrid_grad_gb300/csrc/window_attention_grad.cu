@@ -183,7 +183,7 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
           const int end = min(i - k0 + 1, cols), first = i - k0 - a.window + 1, sink = min(a.sinks - k0, end);
           const uint32_t m = bit_range(first, end) | bit_range(0, sink);
           seen = __any_sync(0xffffffffu, m != 0u);
-          if (!__all_sync(0xffffffffu, m == 0xffffffffu)) mask_block(p, m);
+          if (seen && !__all_sync(0xffffffffu, m == 0xffffffffu)) mask_block(p, m);
         }
         if (seen) {
 #pragma unroll
@@ -510,7 +510,7 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
           const int to = j < a.sinks ? 32 : (int)min((int64_t)from + a.window, (int64_t)32);
           const uint32_t m = bit_range(from, to);
           seen = __any_sync(0xffffffffu, m != 0u);
-          if (!__all_sync(0xffffffffu, m == 0xffffffffu)) mask_block(p, m);
+          if (seen && !__all_sync(0xffffffffu, m == 0xffffffffu)) mask_block(p, m);
         }
         if (seen) {
 #pragma unroll
