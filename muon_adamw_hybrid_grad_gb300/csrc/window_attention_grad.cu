@@ -81,10 +81,14 @@ template <int DP>
 struct GradSmem {
   static constexpr uint32_t TILE = kAttnTile * DP * 2;
   static constexpr int SLOTS = DP == 128 ? 5 : 8;
-  static constexpr uint32_t RING = 2 * TILE;                   // after Q and dO, or K and V
+  // dK/dV: buffers for K and V, and for S^T in TMEM. Heads of up to 64 leave room for two of each: the next item's
+  // operands are there when it begins, and S^T of a step is formed while the threads hold the weights of the one
+  // before.
+  static constexpr int KV = DP == 128 ? 1 : 2, NS = DP == 128 ? 1 : 2;
+  static constexpr uint32_t RING = 2 * KV * TILE;              // after K and V, or Q and dO
   static constexpr uint32_t STATS = RING + SLOTS * TILE;       // dkv: [2][nlse2, ndelta][128] of the query tiles
   static constexpr uint32_t BARS = STATS + 2 * 2 * kAttnTile * 4;
-  static constexpr int NBARS = 8 * SLOTS + 29;  // dK/dV's and dQ's
+  static constexpr int NBARS = 8 * SLOTS + 35;  // dK/dV's and dQ's
   static constexpr uint32_t BYTES = BARS + NBARS * 8 + 16;
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
@@ -137,6 +141,7 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
   const uint32_t staged = bars + 3 * SM::SLOTS * 8, own = bars + 4 * SM::SLOTS * 8, q_full = own, q_empty = own + 8, do_full = own + 16,
                  do_empty = own + 24, s_full = own + 32, dp_full = own + 48, dp_empty = own + 56, ds_full = own + 64,
                  dq_full = own + 80, drain = own + 88;
+  static_assert(DqBarriers<DP>::COUNT == 4 * SM::SLOTS + (88 + 16) / 8, "barriers");
   if (set_up) {
     ring.init(1);
     for (int i = 0; i < SM::SLOTS; ++i) mbar_init(staged + 8 * i, kMathWarps / (DP == 64 ? 2 : 1));
@@ -437,7 +442,7 @@ __device__ __forceinline__ DkvItem dkv_item(const AttnArgs& a, int item, int sin
 
 template <int DP>
 struct DkvBarriers {
-  static constexpr int COUNT = 4 * GradSmem<DP>::SLOTS + 16;
+  static constexpr int COUNT = 4 * GradSmem<DP>::SLOTS + 22;
 };
 
 template <int DP, bool MATH>
@@ -451,14 +456,19 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, bars + SM::SLOTS * 16, SM::TILE};
   // full[SLOTS], empty[SLOTS], raw[SLOTS], staged[SLOTS], then
-  const uint32_t staged = bars + 3 * SM::SLOTS * 8, own = bars + 4 * SM::SLOTS * 8, k_full = own, k_empty = own + 8, v_full = own + 16,
-                 v_empty = own + 24, s_full = own + 32, dp_full = own + 40, p_full = own + 48, ds_full = own + 56,
-                 stat_full = own + 64, done = own + 72, drain = own + 80, turn = own + 96;
+  const uint32_t staged = bars + 3 * SM::SLOTS * 8, own = bars + 4 * SM::SLOTS * 8, k_full = own, k_empty = own + 16,
+                 v_full = own + 32, v_empty = own + 48, s_full = own + 64, p_full = own + 80, dp_full = own + 96,
+                 ds_full = own + 104, stat_full = own + 112, done = own + 120, drain = own + 128, turn = own + 144;
+  static_assert(DkvBarriers<DP>::COUNT == 4 * SM::SLOTS + (144 + 32) / 8, "barriers");
+  constexpr int KV = SM::KV, NS = SM::NS;
   if (set_up) {
     ring.init(2);
     for (int i = 0; i < SM::SLOTS; ++i) mbar_init(staged + 8 * i, kMathWarps / 2);
-    mbar_init(k_full, 1), mbar_init(k_empty, 1), mbar_init(v_full, 1), mbar_init(v_empty, 1);
-    mbar_init(s_full, 1), mbar_init(dp_full, 1), mbar_init(p_full, kMathWarps), mbar_init(ds_full, kMathWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + 8 * i, 1), mbar_init(k_empty + 8 * i, 1), mbar_init(v_full + 8 * i, 1), mbar_init(v_empty + 8 * i, 1);
+      mbar_init(s_full + 8 * i, 1), mbar_init(p_full + 8 * i, kMathWarps);
+    }
+    mbar_init(dp_full, 1), mbar_init(ds_full, kMathWarps);
     mbar_init(stat_full, kMathWarps * 32), mbar_init(done, 2), mbar_init(drain, 1), mbar_init(drain + 8, 1);
     for (int i = 0; i < 4; ++i) mbar_init(turn + 8 * i, 1);
     return;
@@ -469,7 +479,7 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
   if constexpr (MATH) {
     const int blk = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + 32u * blk, tg = ts + 128u;
+    const uint32_t tg = tmem + lanes + 32u * blk + 128u;
     uint32_t step = 0, done_ph = 0;
     Cursor<SM::SLOTS> cur;
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
@@ -496,8 +506,10 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
         const int q0 = tile * kAttnTile;
         if (++tile == w.q_lo + w.nq) tile = w.q_lo, ++head;
         const float* st = stats + (step & 1) * 256 + 32 * blk;
+        // (the second buffer of S^T lies behind dK)
+        const uint32_t slot = step % NS, ts = tg - 128u + 384u * slot;
         ok = mbar_wait_warp(stat_full, step & 1, abort_flag, err, kErrDkv) &&
-             mbar_wait_warp(s_full, step & 1, abort_flag, err, kErrDkv);
+             mbar_wait_warp(s_full + 8 * slot, step / NS & 1, abort_flag, err, kErrDkv);
         if (!ok) break;
         tc_fence_after();
         uint32_t p[32], g[32], r[16];
@@ -534,7 +546,7 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
+        if (lane == 0) mbar_arrive(p_full + 8 * slot);
         ok = mbar_wait_warp(dp_full, step & 1, abort_flag, err, kErrDkv);
         if (!ok) break;
         tc_fence_after();
@@ -569,7 +581,7 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
       // slot in fp32 (and here too where this is not for them alone: window_sink_kernel writes them again, in full)
       const int which = blk >> 1, c0 = (blk & 1) * (DP / 2), c1 = c0 + DP / 2;
       const float f = which ? a.scale : 1.f;
-      const uint32_t acc = tmem + lanes + 256u + 128u * which;
+      const uint32_t acc = tmem + lanes + 256u + DP * which;
       const int sinks = w.slot >= 0 ? a.sinks : 0;
       if (row0 < sinks) {
         float* pp = partial + ((w.slot * a.kv_heads + w.kv) * 2 + which) * (int64_t)a.sinks * a.dim + (int64_t)j * a.dim;
@@ -625,10 +637,11 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
           for (int x = 0; x < 2 && ok; ++x) {
             if (n == 0) {
               // K before the first queries, V before the first output gradients
-              ok = mbar_wait_in(x ? v_empty : k_empty, (loads & 1) ^ 1, abort_flag, err, kErrDkv);
+              const uint32_t b = loads % KV, full = (x ? v_full : k_full) + 8 * b;
+              ok = mbar_wait_in((x ? v_empty : k_empty) + 8 * b, (loads / KV & 1) ^ 1, abort_flag, err, kErrDkv);
               if (!ok) break;
-              mbar_expect_tx(x ? v_full : k_full, SM::TILE);
-              load_tile<DP>(base + x * SM::TILE, x ? &tmV : &tmK, w.t.b + w.t.p0, w.kv, x ? v_full : k_full);
+              mbar_expect_tx(full, SM::TILE);
+              load_tile<DP>(base + (x * KV + b) * SM::TILE, x ? &tmV : &tmK, w.t.b + w.t.p0, w.kv, full);
             }
             ok = mbar_wait_in(cur.empty(ring), cur.phase ^ 1, abort_flag, err, kErrDkv);
             if (!ok) break;
@@ -649,9 +662,9 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
     }
     if (lane == 0) {
       drain_ring(ring, cur, raw_phase);
-      if (loads) {
-        drain_wait(k_full, (loads - 1) & 1);
-        drain_wait(v_full, (loads - 1) & 1);
+      for (uint32_t i = loads > KV ? loads - KV : 0; i < loads; ++i) {
+        drain_wait(k_full + 8 * (i % KV), i / KV & 1);
+        drain_wait(v_full + 8 * (i % KV), i / KV & 1);
       }
     }
     __syncwarp();
@@ -659,48 +672,54 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
     // x = 0: S^T of Q, then dV += P^T dO; x = 1: dP^T of dO, then dK += dS^T Q
     const int x = warp_uniform(warp - kMmaA);
     Cursor<SM::SLOTS> cur;  // a step's query tile; its output gradients follow it
-    uint32_t kv_ph = 0, step = 0, turns = 0;
-    const uint32_t ts = warp_uniform(tmem) + 128u * x, to = ts + 256u, kt = base + x * SM::TILE;
-    const uint32_t formed = x ? dp_full : s_full, ready = x ? ds_full : p_full;
+    uint32_t nth = 0, turns = 0;        // items with steps, steps whose first product has been reached
+    const uint32_t tm = warp_uniform(tmem), to = tm + 256u + (uint32_t)DP * x;
     DkvItem upcoming = dkv_item(a, cta, sink_items, lane);
     for (int item = cta; item < items && ok; item += ctas) {
       const int steps = warp_uniform(group * upcoming.nq), out = warp_uniform((int)upcoming.staged);
       if (item + ctas < items) upcoming = dkv_item(a, item + ctas, sink_items, lane);
       if (steps == 0) continue;
-      ok = mbar_wait_warp(x ? v_full : k_full, kv_ph, abort_flag, err, kErrDkv);
-      kv_ph ^= 1;
+      const uint32_t b = nth % KV, kt = base + (x * KV + b) * SM::TILE;
+      ok = mbar_wait_warp((x ? v_full : k_full) + 8 * b, nth / KV & 1, abort_flag, err, kErrDkv);
+      ++nth;
       Cursor<SM::SLOTS> other;  // the second product's right-hand tile, of the step before
-      // step n issues the second product of step n - 1 and the first of step n
-      for (int n = 0; n <= steps && ok; ++n) {
-        const Cursor<SM::SLOTS> qc = cur, oc = cur.next();
-        // dK behind the next step's S^T: the threads' next work waits for that
-        if (x == 1 && n < steps) {
-          if (!(ok = mbar_wait_warp(turn + 8 * (turns & 3), turns >> 2 & 1, abort_flag, err, kErrDkv))) break;
-          ++turns;
-        }
-        if (n > 0) {
-          if (!(ok = mbar_wait_warp(other.full(ring), other.phase, abort_flag, err, kErrDkv) &&
-                     mbar_wait_warp(ready, step & 1, abort_flag, err, kErrDkv)))
-            break;
-          ++step;
-          tc_fence_after();
-          mma_ab<DP, 32>(to, ts, other.data(ring), n > 1);
-          umma_commit_warp(other.empty(ring));
-        }
-        if (n == steps) break;
-        const Cursor<SM::SLOTS> c = x ? oc : qc;
-        if (!(ok = mbar_wait_warp(c.full(ring), c.phase, abort_flag, err, kErrDkv))) break;
+      // S^T, or dP^T, of step n, which is the `turns`th of all
+      auto first = [&](int n) {
+        const Cursor<SM::SLOTS> c = x ? cur.next() : cur;
+        const uint32_t slot = x ? 0 : turns % NS;
+        if (!mbar_wait_warp(c.full(ring), c.phase, abort_flag, err, kErrDkv)) return false;
         tc_fence_after();
-        mma_abt<DP>(ts, kt, c.data(ring));
-        umma_commit_warp(formed);
-        if (x == 0) {
-          if (lane == 0) mbar_arrive(turn + 8 * (turns & 3));
-          ++turns;
-        }
+        mma_abt<DP>(tm + (x ? 128u : 384u * slot), kt, c.data(ring));
+        umma_commit_warp(x ? dp_full : s_full + 8 * slot);
+        if (x == 0 && lane == 0) mbar_arrive(turn + 8 * (turns & 3));
         umma_commit_warp(c.empty(ring));
-        if (n == steps - 1) umma_commit_warp(x ? v_empty : k_empty);
-        other = x ? qc : oc;
+        if (n == steps - 1) umma_commit_warp((x ? v_empty : k_empty) + 8 * b);
+        return true;
+      };
+      // dV, or dK, of the `at`th step
+      auto second = [&](bool add, uint32_t at) {
+        const uint32_t slot = x ? 0 : at % NS;
+        if (!(mbar_wait_warp(other.full(ring), other.phase, abort_flag, err, kErrDkv) &&
+              mbar_wait_warp(x ? ds_full : p_full + 8 * slot, (x ? at : at / NS) & 1, abort_flag, err, kErrDkv)))
+          return false;
+        tc_fence_after();
+        mma_ab<DP, 32>(to, tm + (x ? 128u : 384u * slot), other.data(ring), add);
+        umma_commit_warp(other.empty(ring));
+        return true;
+      };
+      // step n issues the second product of step n - 1 and the first of step n, S^T ahead of dV where it has a buffer
+      for (int n = 0; n <= steps && ok; ++n) {
+        // dK behind the next step's S^T: the threads' next work waits for that
+        if (x == 1 && n < steps)
+          if (!(ok = mbar_wait_warp(turn + 8 * (turns & 3), turns >> 2 & 1, abort_flag, err, kErrDkv))) break;
+        const bool ahead = NS == 2 && x == 0;
+        if (ahead && n < steps && !(ok = first(n))) break;
+        if (n > 0 && !(ok = second(n > 1, turns - 1))) break;
+        if (n == steps) break;
+        if (!ahead && !(ok = first(n))) break;
+        other = x ? cur : cur.next();
         cur.skip(2);
+        ++turns;
       }
       if (ok) umma_commit_warp(done);
       if (out) cur.skip(2);
@@ -759,6 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* stats = reinterpret_cast<float*>(smem + SM::STATS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem), bars = base + SM::BARS, bars2 = bars + DkvBarriers<DP>::COUNT * 8;
+  static_assert(DkvBarriers<DP>::COUNT + DqBarriers<DP>::COUNT == SM::NBARS, "barriers");
   if (base & 1023u) {  // the swizzle's phase is that of the address
     if (threadIdx.x == 0) atomicCAS(err, 0, kErrAlign);
     return;
