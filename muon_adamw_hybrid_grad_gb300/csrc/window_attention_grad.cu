@@ -39,31 +39,30 @@ __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant
   pdl_launch();
   pdl_wait();
   const int gl = threadIdx.x & 15;
-  const int64_t total = (int64_t)a.n * a.heads, step = (int64_t)gridDim.x * 16;
+  // 16 rows (token, head) a block and step; the row advances without a division
+  const int step = gridDim.x * 16, up_t = step / a.heads, up_h = step - up_t * a.heads;
+  const int64_t first = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  int t = (int)min(first / a.heads, (int64_t)a.n), h = (int)(first - first / a.heads * a.heads);
   // whole warps stay in the loop for the sum across lanes
-  for (int64_t u0 = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 5) * 2; u0 < total; u0 += step) {
-    const int64_t u = u0 + ((threadIdx.x >> 4) & 1);
+  while (__any_sync(0xffffffffu, t < a.n)) {
     float s = 0.f;
-    int64_t t = 0;
-    int h = 0;
-    if (u < total) {
-      t = u / a.heads;
-      h = (int)(u - t * a.heads);
-      if (gl * 8 < a.dim) {
-        float x[8], y[8];
-        load8(dout + t * do_ts + h * do_hs + gl * 8, x);
-        load8(out + u * a.dim + gl * 8, y);
+    if (t < a.n && gl * 8 < a.dim) {
+      float x[8], y[8];
+      load8(dout + t * do_ts + h * do_hs + gl * 8, x);
+      load8(out + ((int64_t)t * a.heads + h) * a.dim + gl * 8, y);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
-      }
+      for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (u < total && gl == 0) {
-      const float l = lse[(int64_t)h * a.n + t];
-      nlse2[(int64_t)h * a.n + t] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
-      ndelta[(int64_t)h * a.n + t] = -s;
+    if (t < a.n && gl == 0) {
+      const int64_t at = (int64_t)h * a.n + t;
+      const float l = lse[at];
+      nlse2[at] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
+      ndelta[at] = -s;
     }
+    t += up_t, h += up_h;
+    if (h >= a.heads) h -= a.heads, ++t;
   }
 }
 
