@@ -566,6 +566,8 @@ typedef struct {
   const void* k;
   const void* v;
   int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+  /* of the gradient call's `out`; both 0: contiguous. The forward call does not read them. */
+  int64_t out_token_stride, out_head_stride;
 } ma_window_attention;
 
 /* out: contiguous [token][head][head_dim] bf16; lse: contiguous
@@ -573,8 +575,8 @@ typedef struct {
  * MA_ERR_CUDA. */
 MA_API ma_status muon_adamw_window_attention(const ma_window_attention* d, void* out, float* lse, void* cuda_stream);
 
-/* Its gradient. dout: [token][head][head_dim] bf16 with strides; out, lse: as
- * the forward call left them; dq, dk, dv: contiguous [token][head][head_dim]
+/* Its gradient. dout, out: [token][head][head_dim] bf16 with strides; out, lse:
+ * the forward call's values; dq, dk, dv: contiguous [token][head][head_dim]
  * bf16 (dk and dv summed over the query heads that share a key head). */
 MA_API ma_status muon_adamw_window_attention_backward_workspace(const ma_window_attention* d, int64_t* bytes);
 MA_API ma_status muon_adamw_window_attention_backward(const ma_window_attention* d, const void* dout,

@@ -163,6 +163,8 @@ class WindowAttention(ctypes.Structure):
         ("k_head_stride", ctypes.c_int64),
         ("v_token_stride", ctypes.c_int64),
         ("v_head_stride", ctypes.c_int64),
+        ("out_token_stride", ctypes.c_int64),
+        ("out_head_stride", ctypes.c_int64),
     ]
 
 

@@ -20,7 +20,10 @@
 // queries first, then the keys; the gradient's incoming rows behind them) and
 // the token's rows of the tables. Two stages a warp and 16 warps an SM keep
 // 100 to 200 KB in flight on every SM, which a warp's registers could not
-// hold.
+// hold. 32749 tokens of 16 + 8 heads of 128 in bf16 take 71 us (5.7 TB/s, 0.84 of
+// the measured copy bandwidth), their gradient 121 us (5.0 TB/s, 0.74: a third
+// stream to read, and warps issue in 64 % of the cycles); loads straight to
+// registers took 153 and 180.
 #include "op_common.cuh"
 #include "tcgen05.cuh"
 
@@ -454,7 +457,8 @@ QkArgs args_of(const ma_qk_norm_rope* d) {
 }
 
 // Heads of a unit: as many as a stage holds, fewer (down to one pass of a
-// warp's lane groups) while there are fewer units than warps on the GPU.
+// warp's lane groups) while there are fewer units than warps on the GPU (50 tokens
+// of 16 + 8 heads: 2.8 us, with whole stages 3.9; 1000 tokens: 3.8 and 4.7).
 void set_units(QkArgs& a, int lph, int esize, bool back, int sms) {
   const int groups = 32 / lph, total = a.heads + a.kv_heads;
   const int most = (kStageBytes - 4 * a.rot) / (a.dim * esize * (back ? 2 : 1));

@@ -345,6 +345,7 @@ void read_attention(Attn& r, PyObject* const* a, PyObject* const* o) {
   d.k_head_stride = r.k.hs;
   d.v_token_stride = r.v.ts;
   d.v_head_stride = r.v.hs;
+  d.out_token_stride = d.out_head_stride = 0;
 }
 
 PyObject* window_attention(PyObject* const* a) {
@@ -363,19 +364,25 @@ PyObject* window_attention_backward(PyObject* const* a) {
   read_attention(x, a + 1, a + 6);
   const Tensor& q = x.q.t;
   const Heads dout = heads_of(tensor(a[0], "dout", q), "dout", true);
-  const Tensor out = packed(tensor(a[4], "out", q)), &lse = tensor(a[5], "lse", q);
-  if (dout.t.sizes() != q.sizes() || out.sizes() != q.sizes() || dout.t.scalar_type() != at::kBFloat16 ||
-      out.scalar_type() != at::kBFloat16)
+  Heads out = heads_of(tensor(a[4], "out", q), "out", true);
+  // rows that do not lie on 16-byte boundaries are copied: what the forward call returned always does
+  if (out.ts % 8 || out.hs % 8 || reinterpret_cast<uintptr_t>(out.t.const_data_ptr()) % 16)
+    out = heads_of(out.t.detach().clone(at::MemoryFormat::Contiguous), "out", true);
+  const Tensor& lse = tensor(a[5], "lse", q);
+  if (dout.t.sizes() != q.sizes() || out.t.sizes() != q.sizes() || dout.t.scalar_type() != at::kBFloat16 ||
+      out.t.scalar_type() != at::kBFloat16)
     refuse(PyExc_ValueError, "dout and out must have the shape and the type of q");
   if (lse.dim() != 2 || lse.size(0) != x.q.h || lse.size(1) != x.q.n || lse.scalar_type() != at::kFloat ||
       !lse.is_contiguous())
     refuse(PyExc_ValueError, "lse must be contiguous fp32 [head, token]");
+  x.d.out_token_stride = out.ts;
+  x.d.out_head_stride = out.hs;
   int64_t bytes = 0;
   check(muon_adamw_window_attention_backward_workspace(&x.d, &bytes));
   Tensor ws = make({bytes}, at::kByte, q), dq = make(q.sizes(), at::kBFloat16, q);
   Tensor dk = make(x.k.t.sizes(), at::kBFloat16, q), dv = make(x.k.t.sizes(), at::kBFloat16, q);
   call(q, [&](void* s) {
-    return muon_adamw_window_attention_backward(&x.d, dout.t.const_data_ptr(), dout.ts, dout.hs, out.const_data_ptr(),
+    return muon_adamw_window_attention_backward(&x.d, dout.t.const_data_ptr(), dout.ts, dout.hs, out.t.const_data_ptr(),
                                                 static_cast<const float*>(lse.const_data_ptr()), dq.mutable_data_ptr(),
                                                 dk.mutable_data_ptr(), dv.mutable_data_ptr(), ws.mutable_data_ptr(),
                                                 bytes, s);

@@ -24,6 +24,20 @@
 //                   other samples, and stores the finished tiles.
 // TMEM: S0 | S1 | O0 | O1, 128 columns each.
 //
+// Finished tiles leave through two positions of the ring and TMA (see stage_row),
+// tiles with rows of other samples from the threads' registers.
+//
+// Bound by the chain of a step: S, its softmax in one thread a row, P V, and S of the
+// next keys, which takes P's place. A step of both tiles takes 3500 cycles, of which
+// the four products fill 2048 and a softmax takes 1950 (maximum 380, exponentials,
+// sum and rounding 1060, TMEM and barriers the rest); it is bound by issue, so that
+// exponentials as polynomials beside the special-function unit cost 12 to 20 %.
+// 16384 tokens of 16 heads of 128 over 8 key heads, all keys visible: 857 us, 1283
+// TFLOP/s (0.68 of the measured bf16 peak). Window 1024 and four sinks: 73 us for
+// 8192 tokens; 139 us for 16360 in packed samples, 800 TFLOP/s counting visible
+// pairs, nine tiles being formed for eight tiles' worth of keys. Up to 61 tokens: 6.3
+// us, the latency of one step and its set-up.
+//
 // O is rescaled only when a row's maximum has grown by more than 2^8 since it
 // was last taken as m: P then stays below 2^8 and sums in fp32 lose nothing.
 #include "window_attention.cuh"
@@ -88,7 +102,9 @@ struct FwdItem {
   bool staged;  // both tiles leave through the ring, two positions after the last values
 };
 
-// Work item: a pair of query tiles. by_head: of two heads, else of one head.
+// Work item: a pair of query tiles. by_head: of two heads, which meet the same keys,
+// else of one head, whose two tiles meet one key tile more (8192 tokens of 16 heads,
+// window 1024: 73 us over 8 key heads, 79 us over 16).
 __device__ __forceinline__ FwdItem fwd_item(const AttnArgs& a, int item, int units, int lane) {
   const bool by_head = units * 2 == a.heads;
   const int rows = by_head ? kAttnTile : 2 * kAttnTile;
@@ -575,7 +591,11 @@ ma_status muon_adamw_window_attention_backward(const ma_window_attention* d, con
   if (st != MA_OK) return st;
   if (d->n_tokens > 0) {
     st = check_rows("dout", dout, d->head_dim, d->n_tokens, d->n_heads, dout_token_stride, dout_head_stride);
-    if (st == MA_OK) st = check_rows("out", out, 0, 1, 1, 0, 0);
+    // (a single token or head has no stride)
+    const bool dense = d->out_token_stride == 0 && d->out_head_stride == 0;
+    const int64_t o_ts = dense ? (int64_t)d->n_heads * d->head_dim : d->out_token_stride;
+    const int64_t o_hs = dense ? d->head_dim : d->out_head_stride;
+    if (st == MA_OK) st = check_rows("out", out, d->head_dim, d->n_tokens, d->n_heads, o_ts, o_hs);
     if (st == MA_OK) st = check_rows("dq", dq, 0, 1, 1, 0, 0);
     if (st == MA_OK) st = check_rows("dk", dk, 0, 1, 1, 0, 0);
     if (st == MA_OK) st = check_rows("dv", dv, 0, 1, 1, 0, 0);
@@ -602,6 +622,8 @@ ma_status muon_adamw_window_attention_backward(const ma_window_attention* d, con
     g.out = static_cast<const __nv_bfloat16*>(out);
     g.do_ts = dout_token_stride;
     g.do_hs = dout_head_stride;
+    g.o_ts = o_ts;
+    g.o_hs = o_hs;
     g.lse = lse;
     g.nlse2 = reinterpret_cast<float*>(ws);
     g.ndelta = reinterpret_cast<float*>(ws + sp.stats);

@@ -14,6 +14,15 @@
 // dP are formed twice: dQ would otherwise have to be added up by atomics in an
 // order that changes from run to run, or stored in fp32 once per key tile.
 //
+// Bound by the tensor cores where samples are long: 16384 tokens of 16 heads of 128
+// over 8 key heads, all keys visible, take 2.5 ms, 1535 TFLOP/s of products formed
+// (0.81 of the measured bf16 peak). With a window of 1024 and four sinks 447 us, of
+// which window_grad_kernel 383 (8192 tokens: 231 us, without sinks 205). There a dK/dV
+// step takes 2950 cycles for 2048 of products, since S^T of the next queries waits
+// for dV, which waits for P^T in its place, a dQ step 2130 for 1536; edge tiles, the
+// sinks' own steps and the ends of items are the rest. Six samples of 7 to 1021 tokens
+// (16 heads of 64, window 256): 58 us, bound by the latency of items of three steps.
+//
 // The sink keys are seen by every query of a sample. Their gradients are cut
 // into chunks of kSinkChunk query tiles, each a work item of its own whose
 // fp32 sums window_sink_kernel adds in a fixed order.
@@ -30,11 +39,13 @@ constexpr int kMathRegs = 104, kOtherRegs = 64;
 constexpr int kErrDq = 0x202, kErrDkv = 0x203, kErrAlign = 0x204;
 
 // ---- lse2 and delta ----
-// A group of 16 lanes to a (token, head), eight elements a lane.
+// A group of 16 lanes to a (token, head), eight elements a lane. Bound by HBM: 134 MB
+// in 25 us (5.4 TB/s) at 16384 tokens of 16 heads of 128. (Four rows of a group in
+// flight took 36 us, with 77 registers; 16 tokens of one head to a block 28.)
 __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant__ AttnArgs a,
                                                            const __nv_bfloat16* __restrict__ dout, int64_t do_ts,
                                                            int64_t do_hs, const __nv_bfloat16* __restrict__ out,
-                                                           const float* __restrict__ lse, float* __restrict__ nlse2,
+                                                           int64_t o_ts, int64_t o_hs, const float* __restrict__ lse, float* __restrict__ nlse2,
                                                            float* __restrict__ ndelta) {
   pdl_launch();
   pdl_wait();
@@ -49,7 +60,7 @@ __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant
     if (t < a.n && gl * 8 < a.dim) {
       float x[8], y[8];
       load8(dout + t * do_ts + h * do_hs + gl * 8, x);
-      load8(out + ((int64_t)t * a.heads + h) * a.dim + gl * 8, y);
+      load8(out + t * o_ts + h * o_hs + gl * 8, y);
 #pragma unroll
       for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
     }
@@ -70,7 +81,7 @@ __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant
 // Warps 0-15: a thread to a query and a block of 32 of a tile's keys (warps 0-3
 // the first block, and so on); warp 16: TMA; warps 17 and 18: tcgen05.mma, the
 // one S and dQ, the other dP; warp 19: clears the key and value rows of other
-// samples. Sixteen warps rather than eight with twice the keys: a step's chain of
+// samples and stores the finished tiles. Sixteen warps rather than eight with twice the keys: a step's chain of
 // waits, TMEM reads and exponentials is what bounds this kernel.
 // TMEM: S of even steps | S of odd steps | dP | dQ. dS (bf16) overwrites the S
 // it came from, each block in the first 16 of its own 32 columns. S of the next
@@ -388,12 +399,15 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
 // Scores are formed transposed, S^T = K Q^T and dP^T = V dO^T, so that P^T and
 // dS^T stand in TMEM as the left operands of dV += P^T dO and dK += dS^T Q.
 // Warps 0-15: a thread to a key and a block of 32 of a tile's queries; warp 16:
-// TMA; warps 17 and 18: tcgen05.mma, the one dV and then the next step's S^T, the
-// other dK and the next dP^T, issued behind them; warp 19: clears rows of Q and
-// dO that belong to other samples. TMEM: S^T | dP^T | dV | dK; P^T overwrites
-// S^T and dS^T dP^T, each block in the first 16 of its own 32 columns. While the threads form
-// P^T of a step the tensor core runs the step before's dK and this one's dP^T;
-// while they form dS^T it runs dV and the next step's S^T.
+// TMA; warps 17 and 18: tcgen05.mma, the one dV and the next step's S^T, the other
+// dK and the next dP^T, issued behind them; warp 19: clears rows of Q and dO that
+// belong to other samples, and stores the finished tiles. TMEM: S^T | dP^T | dV | dK,
+// and for heads of up to 64 a second S^T behind them; P^T overwrites S^T and dS^T
+// dP^T, each block in the first 16 of its own 32 columns. While the threads form P^T
+// of a step the tensor core runs the step before's dK and this one's dP^T; while
+// they form dS^T it runs dV and the next step's S^T (with two buffers S^T is formed a
+// step earlier: 8192 tokens of 16 heads of 64 take 174 us, of 72 229).
+//
 // First query tile that only the sinks reach in tile 0.
 __device__ __forceinline__ int first_sink_tile(const AttnArgs& a) {
   return a.window == 0 ? 0 : (kAttnTile - 1 + a.window - 1) / kAttnTile + 1;
@@ -825,7 +839,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaA) tmem_dealloc<1>(tmem, 512);
 }
 
-// dK and dV of the sink keys: the first tile's own sums, then the chunks'.
+// dK and dV of the sink keys: the first tile's own sums, then the chunks' (9 us for the
+// 15 chunks of 16384 tokens, latency).
 __global__ void __launch_bounds__(256) window_sink_kernel(const __grid_constant__ AttnArgs a,
                                                           const float* __restrict__ partial, int64_t partial_slots,
                                                           __nv_bfloat16* __restrict__ dk,
@@ -880,7 +895,7 @@ cudaError_t attn_backward(AttnArgs a, const CUtensorMap& q, const CUtensorMap& k
                           const CUtensorMap& dout, const AttnGrad& g, int* err, int sms, cudaStream_t st) {
   const int64_t rows = ((int64_t)a.n * a.heads + 15) / 16, most = (int64_t)sms * 8;
   cudaError_t e = op_launch(window_stats_kernel, dim3((unsigned)(rows < most ? rows : most)), dim3(256), 0, st, 1, a,
-                            g.dout, g.do_ts, g.do_hs, g.out, g.lse, g.nlse2, g.ndelta);
+                            g.dout, g.do_ts, g.do_hs, g.out, g.o_ts, g.o_hs, g.lse, g.nlse2, g.ndelta);
   if (e != cudaSuccess) return e;
   a.nlse2 = g.nlse2;
   a.ndelta = g.ndelta;

@@ -131,6 +131,14 @@ def test_window_attention_refuses(mx, kw, status):
             1 << 30, None)
 
 
+@pytest.mark.parametrize("kw,status", [
+    ({"out_token_stride": 132, "out_head_stride": 64}, "ALIGN"), ({"out_token_stride": 256, "out_head_stride": 60}, "ALIGN"),
+    ({"out_token_stride": 256, "out_head_stride": 56}, "SHAPE"), ({"out_token_stride": 56, "out_head_stride": 64}, "SHAPE")])
+def test_window_attention_refuses_output_strides(mx, kw, status):
+    refused(mx, "muon_adamw_window_attention_backward", getattr(mx, "MA_ERR_" + status), attn(mx, **kw), AT, 256, 64, AT,
+            AT, AT, AT, AT, AT, 1 << 30, None)
+
+
 def test_window_attention_refuses_outputs(mx):
     name = "muon_adamw_window_attention"
     refused(mx, name, mx.MA_ERR_ARG, None, AT, AT, None)

@@ -360,6 +360,25 @@ def test_window_attention_strides(ops):
     assert all(torch.equal(x, y) for x, y in zip(gc, gd))
 
 
+def test_window_attention_output_strides(ops):
+    """The saved output may lie in any layout: heads before tokens, a slice, rows off 16-byte boundaries."""
+    import torch
+
+    rng = np.random.default_rng(18)
+    n, h, g, d = 200, 4, 2, 64
+    q, k, v, do = (cuda(signal(rng, n, x, d), "bf16") for x in (h, g, g, h))
+    how = {"window": 70, "sinks": 3, "scale": 0.3}
+    out, lse = ops.window_attention(q, k, v, **how)
+    want = ops.window_attention_backward(do, q, k, v, out, lse, **how)
+    flipped = out.transpose(0, 1).contiguous().transpose(0, 1)
+    part = torch.full((n, h + 3, d + 8), float("nan"), dtype=torch.bfloat16, device="cuda")[:, 1:h + 1, 8:]
+    odd = torch.full((n, h, d + 1), float("nan"), dtype=torch.bfloat16, device="cuda")[:, :, 1:]
+    for other in (flipped, part, odd):
+        other.copy_(out)
+        got = ops.window_attention_backward(do, q, k, v, other, lse, **how)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_window_attention_samples_do_not_mix(ops):
     """Non-finite values in one sample, or behind the last, reach no other."""
     import torch
