@@ -74,10 +74,6 @@ struct PairTiles {
   __device__ __forceinline__ int tile(int n) const { return sink && n == 0 ? 0 : lo + n - sink; }
   __device__ __forceinline__ bool whole(int s, int n) const { return n >= (s ? a1 : a0) && n <= (s ? b1 : b0); }
   __device__ __forceinline__ bool use(int s, int n) const { return whole(s, n) || (n == 0 && (s ? z1 : z0)); }
-  __device__ __forceinline__ int last(int s) const {
-    const int a = s ? a1 : a0, b = s ? b1 : b0;
-    return b >= a ? b : (s ? z1 : z0) ? 0 : -1;
-  }
 };
 __device__ __forceinline__ PairTiles pair_tiles(const AttnArgs& a, const SampleTile& t, int step) {
   PairTiles p;
