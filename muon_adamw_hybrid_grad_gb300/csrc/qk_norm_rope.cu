@@ -458,7 +458,7 @@ QkArgs args_of(const ma_qk_norm_rope* d) {
 
 // Heads of a unit: as many as a stage holds, fewer (down to one pass of a
 // warp's lane groups) while there are fewer units than warps on the GPU (50 tokens
-// of 16 + 8 heads: 2.8 us, with whole stages 3.9; 1000 tokens: 3.8 and 4.7).
+// of 16 + 16 heads of 64: 2.8 us, with whole stages 3.9; 1000 tokens: 3.8 and 4.7).
 void set_units(QkArgs& a, int lph, int esize, bool back, int sms) {
   const int groups = 32 / lph, total = a.heads + a.kv_heads;
   const int most = (kStageBytes - 4 * a.rot) / (a.dim * esize * (back ? 2 : 1));
