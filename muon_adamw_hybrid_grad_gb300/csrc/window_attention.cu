@@ -494,9 +494,9 @@ bool maps_of(const ma_window_attention* d, Maps* m) {
 }
 
 // Workspace of the gradient: lse2 and delta [head][token], then the partial
-// sums of the sink keys, one slot for each sample and each chunk.
+// sums of the sink keys, one slot for each sample and each chunk, then a counter.
 struct GradSpace {
-  int64_t stats, slots, slot_bytes, bytes;
+  int64_t stats, slots, slot_bytes, counter, bytes;
 };
 GradSpace grad_space(const ma_window_attention* d) {
   GradSpace g;
@@ -504,7 +504,8 @@ GradSpace grad_space(const ma_window_attention* d) {
   g.stats = ((int64_t)d->n_heads * d->n_tokens * 4 + 255) / 256 * 256;
   g.slots = d->sinks > 0 ? 2 * seqs + attn_max_tiles(d->n_tokens, seqs, kAttnTile) / kSinkChunk + 1 : 0;
   g.slot_bytes = (int64_t)d->n_kv_heads * 2 * d->sinks * d->head_dim * 4;
-  g.bytes = 2 * g.stats + g.slots * g.slot_bytes + 256;
+  g.counter = 2 * g.stats + g.slots * g.slot_bytes;
+  g.bytes = g.counter + 256;
   return g;
 }
 
@@ -625,6 +626,7 @@ ma_status muon_adamw_window_attention_backward(const ma_window_attention* d, con
     g.ndelta = reinterpret_cast<float*>(ws + sp.stats);
     g.partial = reinterpret_cast<float*>(ws + 2 * sp.stats);
     g.partial_slots = sp.slots;
+    g.counter = reinterpret_cast<int*>(ws + sp.counter);
     g.dq = static_cast<__nv_bfloat16*>(dq);
     g.dk = static_cast<__nv_bfloat16*>(dk);
     g.dv = static_cast<__nv_bfloat16*>(dv);

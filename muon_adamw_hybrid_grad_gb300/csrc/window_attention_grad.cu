@@ -26,6 +26,8 @@
 // The sink keys are seen by every query of a sample. Their gradients are cut
 // into chunks of kSinkChunk query tiles, each a work item of its own whose
 // fp32 sums window_sink_kernel adds in a fixed order.
+#include <limits.h>
+
 #include "window_attention.cuh"
 
 namespace ma {
@@ -46,9 +48,10 @@ __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant
                                                            const __nv_bfloat16* __restrict__ dout, int64_t do_ts,
                                                            int64_t do_hs, const __nv_bfloat16* __restrict__ out,
                                                            int64_t o_ts, int64_t o_hs, const float* __restrict__ lse, float* __restrict__ nlse2,
-                                                           float* __restrict__ ndelta) {
+                                                           float* __restrict__ ndelta, int* __restrict__ counter) {
   pdl_launch();
   pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;  // of the next launch's dQ items
   const int gl = threadIdx.x & 15;
   // 16 rows (token, head) a block and step; the row advances without a division
   const int step = gridDim.x * 16, up_t = step / a.heads, up_h = step - up_t * a.heads;
@@ -98,8 +101,8 @@ struct GradSmem {
   static constexpr uint32_t RING = 2 * KV * TILE;              // after K and V, or Q and dO
   static constexpr uint32_t STATS = RING + SLOTS * TILE;       // dkv: [2][nlse2, ndelta][128] of the query tiles
   static constexpr uint32_t BARS = STATS + 2 * 2 * kAttnTile * 4;
-  static constexpr int NBARS = 8 * SLOTS + 35;  // dK/dV's and dQ's
-  static constexpr uint32_t BYTES = BARS + NBARS * 8 + 16;
+  static constexpr int NBARS = 8 * SLOTS + 43;  // dK/dV's and dQ's
+  static constexpr uint32_t BYTES = BARS + NBARS * 8 + 32;
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
 
@@ -123,27 +126,62 @@ __device__ __forceinline__ DqItem dq_item(const AttnArgs& a, int item, int lane)
   return w;
 }
 
-// The dQ items of a CTA. CTAs that have one dK/dV item less than others (those from
-// `extra` on) take `more` dQ items ahead of the rest, which go round in the
-// opposite order to the dK/dV items.
-struct DqWalk {
-  int cta, ctas, extra, more;
-  __device__ __forceinline__ int at(int i) const {
-    const int light = ctas - extra, first = cta >= extra ? more : 0;
-    return i < first ? cta - extra + i * light : more * light + (ctas - 1 - cta) + (i - first) * ctas;
+__device__ __forceinline__ void parts_sync() {
+  tc_fence_before();
+  asm volatile("barrier.sync 1, %0;" ::"n"(kThreads) : "memory");
+  tc_fence_after();
+}
+
+// dQ items go to the CTAs in the order in which they come for them, so that those
+// whose dK/dV items took longer take fewer. The TMA warp draws an item's number
+// from a counter, one item ahead of its loads, and posts it to the other warps.
+constexpr int kPosts = 4;
+struct DqPosts {
+  uint32_t full, empty, data;  // barriers and numbers, [kPosts] each
+  uint32_t nth;                // the next to be posted or taken
+
+  // By the TMA warp.
+  __device__ __forceinline__ int post(int* counter, int lane, bool& ok, volatile int* abort_flag, int* err) {
+    int item = INT_MAX;
+    if (lane == 0 && ok) {
+      const uint32_t at = nth % kPosts;
+      ok = mbar_wait_in(empty + 8 * at, (nth / kPosts & 1) ^ 1, abort_flag, err, kErrDq);
+      if (ok) {
+        item = atomicAdd(counter, 1);
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(data + 4 * at), "r"(item) : "memory");
+        mbar_arrive(full + 8 * at);
+      }
+    }
+    ++nth;
+    ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+    return __shfl_sync(0xffffffffu, item, 0);
+  }
+  // By each of the other warps, once for each number.
+  __device__ __forceinline__ int take(int lane, bool& ok, volatile int* abort_flag, int* err) {
+    const uint32_t at = nth % kPosts;
+    int item = INT_MAX;
+    ok = ok && mbar_wait_warp(full + 8 * at, nth / kPosts & 1, abort_flag, err, kErrDq);
+    if (ok) {
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(item) : "r"(data + 4 * at) : "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8 * at);
+    }
+    ++nth;
+    return item;
   }
 };
 
 template <int DP>
 struct DqBarriers {
-  static constexpr int COUNT = 4 * GradSmem<DP>::SLOTS + 13;
+  static constexpr int COUNT = 4 * GradSmem<DP>::SLOTS + 13 + 2 * kPosts;
 };
 
 template <int DP, bool MATH>
 __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                                         const CUtensorMap& tmV, const CUtensorMap& tmDO, const CUtensorMap& tmDQ,
                                         __nv_bfloat16* __restrict__ dq, int* __restrict__ err, volatile int* abort_flag,
-                                        uint32_t base, uint32_t bars, uint32_t tmem, const DqWalk& walk, bool set_up) {
+                                        uint32_t base, uint32_t bars, uint32_t tmem, uint32_t numbers, int* counter,
+                                        bool set_up) {
   using SM = GradSmem<DP>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, bars + SM::SLOTS * 16, SM::TILE};
@@ -151,18 +189,26 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
   const uint32_t staged = bars + 3 * SM::SLOTS * 8, own = bars + 4 * SM::SLOTS * 8, q_full = own, q_empty = own + 8, do_full = own + 16,
                  do_empty = own + 24, s_full = own + 32, dp_full = own + 48, dp_empty = own + 56, ds_full = own + 64,
                  dq_full = own + 80, drain = own + 88;
-  static_assert(DqBarriers<DP>::COUNT == 4 * SM::SLOTS + (88 + 16) / 8, "barriers");
+  DqPosts posts{own + 104, own + 104 + 8 * kPosts, numbers, 0};
+  static_assert(DqBarriers<DP>::COUNT == 4 * SM::SLOTS + 104 / 8 + 2 * kPosts, "barriers");
   if (set_up) {
     ring.init(1);
     for (int i = 0; i < SM::SLOTS; ++i) mbar_init(staged + 8 * i, kMathWarps / (DP == 64 ? 2 : 1));
     mbar_init(q_full, 1), mbar_init(q_empty, 1), mbar_init(do_full, 1), mbar_init(do_empty, 1);
     mbar_init(s_full, 1), mbar_init(s_full + 8, 1), mbar_init(dp_full, 1), mbar_init(dp_empty, kMathWarps);
     mbar_init(ds_full, kMathWarps), mbar_init(ds_full + 8, kMathWarps), mbar_init(dq_full, 1), mbar_init(drain, 1), mbar_init(drain + 8, 1);
+    for (int i = 0; i < kPosts; ++i) mbar_init(posts.full + 8 * i, 1), mbar_init(posts.empty + 8 * i, kMathWarps + 3);
     return;
   }
   const int items = a.heads * count_units(a, lane, [](int len, bool) { return (len + kAttnTile - 1) / kAttnTile; });
   const int few = sink_columns(a);
-  bool ok = *abort_flag == 0;
+  bool ok = true;
+  int item = INT_MAX;
+  if (!MATH && warp == kTma) item = posts.post(counter, lane, ok, abort_flag, err);
+  // every product and copy of the first part has ended
+  parts_sync();
+  ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
+  if (MATH || warp != kTma) item = posts.take(lane, ok, abort_flag, err);
 
   if constexpr (MATH) {
     const int blk = warp >> 2, row = threadIdx.x & 127;
@@ -171,8 +217,9 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
     Cursor<SM::SLOTS> cur;
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     const bool wide = rows_wide(dq, a.dim);
-    DqItem next = dq_item(a, walk.at(0), lane);
-    for (int nth = 0; walk.at(nth) < items && ok; ++nth) {
+    DqItem next;
+    if (item < items) next = dq_item(a, item, lane);
+    while (item < items && ok) {
       const DqItem w = next;
       const int i = w.t.p0 + row;
       const int64_t t = (int64_t)w.t.b + i;
@@ -230,7 +277,8 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
         if (lane == 0) mbar_arrive(ds_full + 8 * slot);
       }
       if (!ok) break;
-      if (walk.at(nth + 1) < items) next = dq_item(a, walk.at(nth + 1), lane);
+      item = posts.take(lane, ok, abort_flag, err);
+      if (item < items) next = dq_item(a, item, lane);
       if (w.steps) {
         ok = mbar_wait_warp(dq_full, dq_ph, abort_flag, err, kErrDq);
         if (!ok) break;
@@ -256,8 +304,9 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
   } else if (warp == kTma) {
     Cursor<SM::SLOTS> cur;
     uint32_t loads = 0, raw_phase = 0;
-    for (int i = 0; walk.at(i) < items && ok; ++i) {
-      const DqItem w = dq_item(a, walk.at(i), lane);
+    while (item < items && ok) {
+      const DqItem w = dq_item(a, item, lane);
+      item = posts.post(counter, lane, ok, abort_flag, err);
       if (lane == 0) {
         for (int n = 0; n < w.steps && ok; ++n) {
           const int at = w.tile(n) * kAttnTile;
@@ -300,12 +349,14 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
     Cursor<SM::SLOTS> sc;  // the next S's key tile
     uint32_t q_ph = 0, ds_ph = 0;  // ds_ph: a bit per S slot
     const uint32_t tm = warp_uniform(tmem);
-    DqItem next = dq_item(a, walk.at(0), lane);
-    for (int i = 0; walk.at(i) < items && ok; ++i) {
+    DqItem next;
+    if (item < items) next = dq_item(a, item, lane);
+    while (item < items && ok) {
       const int steps = warp_uniform(next.steps), sink = warp_uniform((int)next.k.sink),
                 out = warp_uniform((int)next.staged);
       if (steps == 0) {
-        if (walk.at(i + 1) < items) next = dq_item(a, walk.at(i + 1), lane);
+        item = posts.take(lane, ok, abort_flag, err);
+        if (item < items) next = dq_item(a, item, lane);
         continue;
       }
       Cursor<SM::SLOTS> qc = sc;  // the next dQ's key tile
@@ -320,7 +371,8 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
       };
       ok = mbar_wait_warp(q_full, q_ph, abort_flag, err, kErrDq) && issue_s(0) && (steps == 1 || issue_s(1));
       q_ph ^= 1;
-      if (walk.at(i + 1) < items) next = dq_item(a, walk.at(i + 1), lane);
+      item = posts.take(lane, ok, abort_flag, err);
+      if (item < items) next = dq_item(a, item, lane);
       for (int n = 0; n < steps && ok; ++n) {
         // (a barrier to each slot of S: the threads need nothing of this warp for the step after, so that they
         // may be through with it before this wait, and one barrier's phases would have passed twice)
@@ -347,13 +399,15 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
     Cursor<SM::SLOTS> pc;  // a key tile, then its value tile
     uint32_t q_ph = 0, step = 0;
     const uint32_t tm = warp_uniform(tmem);
-    DqItem next = dq_item(a, walk.at(0), lane);
-    for (int i = 0; walk.at(i) < items && ok; ++i) {
+    DqItem next;
+    if (item < items) next = dq_item(a, item, lane);
+    while (item < items && ok) {
       const int steps = warp_uniform(next.steps), sink = warp_uniform((int)next.k.sink),
                 out = warp_uniform((int)next.staged);
-      if (walk.at(i + 1) < items) next = dq_item(a, walk.at(i + 1), lane);
+      item = posts.take(lane, ok, abort_flag, err);
+      if (item < items) next = dq_item(a, item, lane);
       if (steps == 0) continue;
-      ok = mbar_wait_warp(do_full, q_ph, abort_flag, err, kErrDq);
+      ok = ok && mbar_wait_warp(do_full, q_ph, abort_flag, err, kErrDq);
       q_ph ^= 1;
       for (int n = 0; n < steps && ok; ++n, ++step) {
         pc.advance();
@@ -376,8 +430,9 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
   } else {
     Cursor<SM::SLOTS> cur;
     uint32_t raw_phase = 0, staged_phase = 0;
-    for (int i = 0; walk.at(i) < items && ok; ++i) {
-      const DqItem w = dq_item(a, walk.at(i), lane);
+    while (item < items && ok) {
+      const DqItem w = dq_item(a, item, lane);
+      item = posts.take(lane, ok, abort_flag, err);
       if (w.steps == 0) continue;
       cur.skip(2 * w.steps - 2);
       const int valid = w.t.len - w.tile(w.steps - 1) * kAttnTile;  // only the last tile can be ragged
@@ -764,12 +819,6 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
   }
 }
 
-__device__ __forceinline__ void parts_sync() {
-  tc_fence_before();
-  asm volatile("barrier.sync 1, %0;" ::"n"(kThreads) : "memory");
-  tc_fence_after();
-}
-
 // dK and dV, then dQ: one persistent CTA per SM runs its items of the one and then
 // its items of the other, so that no SM waits in between for the slowest. (Two
 // launches took 47 us on six samples of 7 to 1021 tokens and 428 us on 16384 tokens,
@@ -782,12 +831,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap tmDK, const __grid_constant__ CUtensorMap tmDV,
                        __nv_bfloat16* __restrict__ dq,
                        __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv, float* __restrict__ partial,
-                       int64_t partial_slots, int* __restrict__ err) {
+                       int64_t partial_slots, int* __restrict__ counter, int* __restrict__ err) {
   using SM = GradSmem<DP>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  // two words after the barriers: the TMEM base and the abort flag
+  // words after the barriers: the TMEM base, the abort flag, the posted numbers
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::BARS + SM::NBARS * 8);
   volatile int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  const uint32_t numbers = smem_u32(tmem_slot + 2);
   float* stats = reinterpret_cast<float*>(smem + SM::STATS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem), bars = base + SM::BARS, bars2 = bars + DkvBarriers<DP>::COUNT * 8;
@@ -796,12 +846,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) atomicCAS(err, 0, kErrAlign);
     return;
   }
-  const DqWalk none{0, 1, 0, 0};
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     dkv_part<DP, false>(a, tmQ, tmK, tmV, tmDO, tmDK, tmDV, dk, dv, partial, partial_slots, err, abort_flag, stats, base, bars, 0, 0, 1, 0, 0,
                  true);
-    dq_part<DP, false>(a, tmQ, tmK, tmV, tmDO, tmDQ, dq, err, abort_flag, base, bars2, 0, none, true);
+    dq_part<DP, false>(a, tmQ, tmK, tmV, tmDO, tmDQ, dq, err, abort_flag, base, bars2, 0, 0, nullptr, true);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaA) tmem_alloc<1>(smem_u32(tmem_slot), 512);
@@ -811,27 +860,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_launch();
   pdl_wait();
-  const int cta = blockIdx.x, ctas = gridDim.x, group = a.heads / a.kv_heads;
+  const int cta = blockIdx.x, ctas = gridDim.x;
   const int sink_items =
       a.kv_heads * count_units(a, lane, [&](int len, bool live) { return sink_chunks(a, len, live); });
   const int items = sink_items +
                     a.kv_heads * count_units(a, lane, [](int len, bool) { return (len + kAttnTile - 1) / kAttnTile; });
-  // a dK/dV item is four products for each head of the group, a dQ item three
-  const DqWalk walk{cta, ctas, items % ctas, max(1, group * 4 / 3)};
-  // (the registers are given by one instruction for all four warps of a group; at the barrier in between every
-  // product and copy of the first part has ended)
+  // (the registers are given by one instruction for all four warps of a group)
   if (warp < kMathWarps) {
     regs_up<kMathRegs>();
     dkv_part<DP, true>(a, tmQ, tmK, tmV, tmDO, tmDK, tmDV, dk, dv, partial, partial_slots, err, abort_flag, stats, base, bars, tmem,
                        cta, ctas, sink_items, items, false);
-    parts_sync();
-    dq_part<DP, true>(a, tmQ, tmK, tmV, tmDO, tmDQ, dq, err, abort_flag, base, bars2, tmem, walk, false);
+    dq_part<DP, true>(a, tmQ, tmK, tmV, tmDO, tmDQ, dq, err, abort_flag, base, bars2, tmem, numbers, counter, false);
   } else {
     regs_down<kOtherRegs>();
     dkv_part<DP, false>(a, tmQ, tmK, tmV, tmDO, tmDK, tmDV, dk, dv, partial, partial_slots, err, abort_flag, stats, base, bars,
                         tmem, cta, ctas, sink_items, items, false);
-    parts_sync();
-    dq_part<DP, false>(a, tmQ, tmK, tmV, tmDO, tmDQ, dq, err, abort_flag, base, bars2, tmem, walk, false);
+    dq_part<DP, false>(a, tmQ, tmK, tmV, tmDO, tmDQ, dq, err, abort_flag, base, bars2, tmem, numbers, counter, false);
   }
   tc_fence_before();
   __syncthreads();
@@ -886,7 +930,7 @@ cudaError_t run_backward(const AttnArgs& a, const CUtensorMap& q, const CUtensor
   const cudaError_t e = op_smem_limit<window_grad_kernel<DP>>((int)GradSmem<DP>::BYTES);
   if (e != cudaSuccess) return e;
   return op_launch(window_grad_kernel<DP>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads),
-                   GradSmem<DP>::BYTES, st, 1, a, q, k, v, dout, g.tm_dq, g.tm_dk, g.tm_dv, g.dq, g.dk, g.dv, g.partial, g.partial_slots, err);
+                   GradSmem<DP>::BYTES, st, 1, a, q, k, v, dout, g.tm_dq, g.tm_dk, g.tm_dv, g.dq, g.dk, g.dv, g.partial, g.partial_slots, g.counter, err);
 }
 
 }  // namespace
@@ -895,7 +939,7 @@ cudaError_t attn_backward(AttnArgs a, const CUtensorMap& q, const CUtensorMap& k
                           const CUtensorMap& dout, const AttnGrad& g, int* err, int sms, cudaStream_t st) {
   const int64_t rows = ((int64_t)a.n * a.heads + 15) / 16, most = (int64_t)sms * 8;
   cudaError_t e = op_launch(window_stats_kernel, dim3((unsigned)(rows < most ? rows : most)), dim3(256), 0, st, 1, a,
-                            g.dout, g.do_ts, g.do_hs, g.out, g.o_ts, g.o_hs, g.lse, g.nlse2, g.ndelta);
+                            g.dout, g.do_ts, g.do_hs, g.out, g.o_ts, g.o_hs, g.lse, g.nlse2, g.ndelta, g.counter);
   if (e != cudaSuccess) return e;
   a.nlse2 = g.nlse2;
   a.ndelta = g.ndelta;
