@@ -494,7 +494,7 @@ bool maps_of(const ma_window_attention* d, Maps* m) {
 }
 
 // Workspace of the gradient: lse2 and delta [head][token], then the partial
-// sums of the sink keys, one slot for each sample and each chunk, then a counter.
+// sums of the sink keys, one slot for each sample and each chunk, then the counters.
 struct GradSpace {
   int64_t stats, slots, slot_bytes, counter, bytes;
 };
@@ -505,7 +505,7 @@ GradSpace grad_space(const ma_window_attention* d) {
   g.slots = d->sinks > 0 ? 2 * seqs + attn_max_tiles(d->n_tokens, seqs, kAttnTile) / kSinkChunk + 1 : 0;
   g.slot_bytes = (int64_t)d->n_kv_heads * 2 * d->sinks * d->head_dim * 4;
   g.counter = 2 * g.stats + g.slots * g.slot_bytes;
-  g.bytes = g.counter + 256;
+  g.bytes = g.counter + (1 + seqs * d->n_kv_heads) * 4 + 256;
   return g;
 }
 

@@ -36,7 +36,7 @@ struct AttnGrad {
   float *nlse2, *ndelta, *partial;
   int64_t partial_slots;
   __nv_bfloat16 *dq, *dk, *dv;
-  int* counter;  // zeroed and drawn from by the launches
+  int* counter;  // 1 + n_seqs kv_heads, zeroed and counted by the launches
   CUtensorMap tm_dq, tm_dk, tm_dv;
 };
 cudaError_t attn_backward(AttnArgs a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,

@@ -8,7 +8,6 @@
 // window_grad_kernel   dkv_part: 128 keys of a key head, walking the query tiles
 //                      of every head that reads it; then dq_part: 128 queries of
 //                      a head, walking their key tiles.
-// window_sink_kernel   joins the partial sums of the sink keys.
 //
 // Seven products instead of the five that one kernel would need, because S and
 // dP are formed twice: dQ would otherwise have to be added up by atomics in an
@@ -24,8 +23,9 @@
 // (16 heads of 64, window 256): 58 us, bound by the latency of items of three steps.
 //
 // The sink keys are seen by every query of a sample. Their gradients are cut
-// into chunks of kSinkChunk query tiles, each a work item of its own whose
-// fp32 sums window_sink_kernel adds in a fixed order.
+// into chunks of kSinkChunk query tiles, each a work item of its own; the CTA that
+// ends the last of a sample's adds their fp32 sums in a fixed order (a launch of its
+// own for that took 9 us at 16384 tokens and 4 at short samples).
 #include <limits.h>
 
 #include "window_attention.cuh"
@@ -51,7 +51,9 @@ __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant
                                                            float* __restrict__ ndelta, int* __restrict__ counter) {
   pdl_launch();
   pdl_wait();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;  // of the next launch's dQ items
+  // the next launch's counters: of dQ items, and of the sink items of each sample and key head
+  const int64_t counters = 1 + (int64_t)a.n_seqs * a.kv_heads;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < counters; i += (int64_t)gridDim.x * 256) counter[i] = 0;
   const int gl = threadIdx.x & 15;
   // 16 rows (token, head) a block and step; the row advances without a division
   const int step = gridDim.x * 16, up_t = step / a.heads, up_h = step - up_t * a.heads;
@@ -101,7 +103,7 @@ struct GradSmem {
   static constexpr uint32_t RING = 2 * KV * TILE;              // after K and V, or Q and dO
   static constexpr uint32_t STATS = RING + SLOTS * TILE;       // dkv: [2][nlse2, ndelta][128] of the query tiles
   static constexpr uint32_t BARS = STATS + 2 * 2 * kAttnTile * 4;
-  static constexpr int NBARS = 8 * SLOTS + 43;  // dK/dV's and dQ's
+  static constexpr int NBARS = 8 * SLOTS + 45;  // dK/dV's and dQ's
   static constexpr uint32_t BYTES = BARS + NBARS * 8 + 32;
   static_assert(BYTES <= 232448, "shared memory per CTA");
 };
@@ -476,7 +478,7 @@ __device__ __forceinline__ int sink_chunks(const AttnArgs& a, int len, bool live
 struct DkvItem {
   SampleTile t;     // the key tile
   int kv, q_lo, nq; // query tiles q_lo .. q_lo + nq - 1, for each head of the group
-  int64_t slot;     // partial slot of the sink keys, -1: none
+  int64_t slot;     // partial slot of the sink keys, -1: none (no other item sees any of them)
   bool sink_only;   // a chunk for the sink keys alone
   bool staged;      // dV and dK leave through the ring, in the positions after the last step's tiles
 };
@@ -502,15 +504,43 @@ __device__ __forceinline__ DkvItem dkv_item(const AttnArgs& a, int item, int sin
       const int hi = (int)min((int64_t)tiles - 1, ((int64_t)w.t.p0 + kAttnTile - 1 + a.window - 1) / kAttnTile);
       w.nq = hi - w.q_lo + 1;
     }
-    w.slot = a.sinks > 0 && w.t.index == 0 && w.t.live ? w.t.sample : -1;
+    w.slot = w.t.index == 0 && sink_chunks(a, w.t.len, w.t.live) > 0 ? w.t.sample : -1;
   }
-  w.staged = !w.sink_only && w.nq > 0 && w.t.p0 + kAttnTile <= w.t.len;
+  w.staged = w.slot < 0 && w.nq > 0 && w.t.p0 + kAttnTile <= w.t.len;
   return w;
+}
+
+// dK and dV of a sample's sink keys, by all threads that hold scores: the first
+// tile's own sums, then the chunks' in their order.
+__device__ __forceinline__ void sum_sinks(const AttnArgs& a, const SampleTile& t, int kv, const float* partial,
+                                          int64_t partial_slots, __nv_bfloat16* __restrict__ dk,
+                                          __nv_bfloat16* __restrict__ dv, int lane) {
+  int before = 0;  // chunks of the samples before this one
+  if (a.cu)
+    for (int i = lane; i < t.sample; i += 32) {
+      int b, len;
+      sample_span(a, i, b, len);
+      before += sink_chunks(a, len, true);
+    }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  const int rows = min(a.sinks, t.len);
+  const int64_t per = (int64_t)a.sinks * a.dim, slot = (int64_t)a.kv_heads * 2 * per, at = (int64_t)a.n_seqs + before;
+  const int64_t n = min((int64_t)sink_chunks(a, t.len, true), partial_slots - at);
+  for (int e = threadIdx.x; e < 2 * rows * a.dim; e += kMathWarps * 32) {
+    const int which = e >= rows * a.dim, x = which ? e - rows * a.dim : e;
+    const float* p = partial + (kv * 2 + which) * per + x;
+    float s = __ldcg(p + t.sample * slot);
+#pragma unroll 8
+    for (int64_t c = 0; c < n; ++c) s += __ldcg(p + (at + c) * slot);
+    const int row = x / a.dim;
+    (which ? dk : dv)[(((int64_t)t.b + row) * a.kv_heads + kv) * a.dim + (x - row * a.dim)] = __float2bfloat16_rn(s);
+  }
 }
 
 template <int DP>
 struct DkvBarriers {
-  static constexpr int COUNT = 4 * GradSmem<DP>::SLOTS + 22;
+  static constexpr int COUNT = 4 * GradSmem<DP>::SLOTS + 24;
 };
 
 template <int DP, bool MATH>
@@ -518,16 +548,17 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
                                          const CUtensorMap& tmV, const CUtensorMap& tmDO, const CUtensorMap& tmDK,
                                          const CUtensorMap& tmDV, __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv,
                                          float* __restrict__ partial, int64_t partial_slots, int* __restrict__ err,
-                                         volatile int* abort_flag, float* stats, uint32_t base, uint32_t bars,
-                                         uint32_t tmem, int cta, int ctas, int sink_items, int items, bool set_up) {
+                                         volatile int* abort_flag, float* stats, int* __restrict__ arrived,
+                                         uint32_t last_word, uint32_t base, uint32_t bars, uint32_t tmem, int cta, int ctas, int sink_items, int items, bool set_up) {
   using SM = GradSmem<DP>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Ring<SM::SLOTS> ring{base + SM::RING, bars, bars + SM::SLOTS * 8, bars + SM::SLOTS * 16, SM::TILE};
   // full[SLOTS], empty[SLOTS], raw[SLOTS], staged[SLOTS], then
   const uint32_t staged = bars + 3 * SM::SLOTS * 8, own = bars + 4 * SM::SLOTS * 8, k_full = own, k_empty = own + 16,
                  v_full = own + 32, v_empty = own + 48, s_full = own + 64, p_full = own + 80, dp_full = own + 96,
-                 ds_full = own + 104, stat_full = own + 112, done = own + 120, drain = own + 128, turn = own + 144;
-  static_assert(DkvBarriers<DP>::COUNT == 4 * SM::SLOTS + (144 + 32) / 8, "barriers");
+                 ds_full = own + 104, stat_full = own + 112, done = own + 120, drain = own + 128, turn = own + 144,
+                 summed = own + 176, told = own + 184;
+  static_assert(DkvBarriers<DP>::COUNT == 4 * SM::SLOTS + (184 + 8) / 8, "barriers");
   constexpr int KV = SM::KV, NS = SM::NS;
   if (set_up) {
     ring.init(2);
@@ -536,24 +567,27 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
       mbar_init(k_full + 8 * i, 1), mbar_init(k_empty + 8 * i, 1), mbar_init(v_full + 8 * i, 1), mbar_init(v_empty + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1), mbar_init(p_full + 8 * i, kMathWarps);
     }
-    mbar_init(dp_full, 1), mbar_init(ds_full, kMathWarps);
+    mbar_init(dp_full, 1), mbar_init(ds_full, kMathWarps), mbar_init(summed, kMathWarps), mbar_init(told, 1);
     mbar_init(stat_full, kMathWarps * 32), mbar_init(done, 2), mbar_init(drain, 1), mbar_init(drain + 8, 1);
     for (int i = 0; i < 4; ++i) mbar_init(turn + 8 * i, 1);
     return;
   }
   const int group = a.heads / a.kv_heads;
   bool ok = true;
+  // The first items, the sinks' among them, go to the CTAs in turn, the others the other way round: the CTAs that
+  // begin with a long one are the last to get one more.
+  auto at = [&](int i) { return i == 0 ? cta : i * ctas + ctas - 1 - cta; };
 
   if constexpr (MATH) {
     const int blk = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tg = tmem + lanes + 32u * blk + 128u;
-    uint32_t step = 0, done_ph = 0;
+    uint32_t step = 0, done_ph = 0, slot_ph = 0;
     Cursor<SM::SLOTS> cur;
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     const bool wide = rows_wide(dk, a.dim) && rows_wide(dv, a.dim);
     DkvItem upcoming = dkv_item(a, cta, sink_items, lane);
-    for (int item = cta; item < items && ok; item += ctas) {
+    for (int i = 0, item = cta; item < items && ok; item = at(++i)) {
       const DkvItem w = upcoming;
       const int steps = group * w.nq, row0 = w.t.p0 + (row & ~31), j = w.t.p0 + row;
       // threads 0-127 bring nlse2 of a query tile, threads 128-255 ndelta. (Rows past the sample's end get zeros:
@@ -638,7 +672,7 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
         if (lane == 0) mbar_arrive(ds_full);
       }
       if (!ok) break;
-      if (item + ctas < items) upcoming = dkv_item(a, item + ctas, sink_items, lane);
+      if (at(i + 1) < items) upcoming = dkv_item(a, at(i + 1), sink_items, lane);
       if (steps) {
         ok = mbar_wait_warp(done, done_ph, abort_flag, err, kErrDkv);
         if (!ok) break;
@@ -646,7 +680,7 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
         tc_fence_after();
       }
       // warps 0-7 store dV, warps 8-15 dK, half of the columns to each four; the sink keys' rows go to their partial
-      // slot in fp32 (and here too where this is not for them alone: window_sink_kernel writes them again, in full)
+      // slot in fp32
       const int which = blk >> 1, c0 = (blk & 1) * (DP / 2), c1 = c0 + DP / 2;
       const float f = which ? a.scale : 1.f;
       const uint32_t acc = tmem + lanes + 256u + DP * which;
@@ -688,14 +722,38 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
         cur.skip(2);
       } else if (!w.sink_only)
         store_row(acc, c0, c1, f, steps == 0, (which ? dk : dv) + (((int64_t)w.t.b + j) * a.kv_heads + w.kv) * a.dim,
-                  j < w.t.len, a.dim, wide);
+                  j < w.t.len && j >= sinks, a.dim, wide);
+      if (w.slot >= 0) {
+        // the last of a sample's items to come here adds up its sink keys' rows
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(summed);
+        if (warp == 0) {
+          ok = mbar_wait_warp(summed, slot_ph, abort_flag, err, kErrDkv);
+          if (ok && lane == 0) {
+            const int all = 1 + sink_chunks(a, w.t.len, true);
+            const int before = atomicAdd(arrived + (int64_t)w.t.sample * a.kv_heads + w.kv, 1);
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(last_word), "r"((int)(before + 1 == all)) : "memory");
+            mbar_arrive(told);
+          }
+        }
+        ok = ok && mbar_wait_warp(told, slot_ph, abort_flag, err, kErrDkv);
+        if (!ok) break;
+        slot_ph ^= 1;
+        int last;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(last) : "r"(last_word) : "memory");
+        if (last) {
+          __threadfence();
+          sum_sinks(a, w.t, w.kv, partial, partial_slots, dk, dv, lane);
+        }
+      }
       tc_fence_before();
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // (after a wait that ran out)
   } else if (warp == kTma) {
     Cursor<SM::SLOTS> cur;
     uint32_t loads = 0, raw_phase = 0;
-    for (int item = cta; item < items && ok; item += ctas) {
+    for (int i = 0, item = cta; item < items && ok; item = at(++i)) {
       const DkvItem w = dkv_item(a, item, sink_items, lane);
       if (lane == 0) {
         const int steps = group * w.nq;
@@ -743,9 +801,9 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
     uint32_t nth = 0, turns = 0;        // items with steps, steps whose first product has been reached
     const uint32_t tm = warp_uniform(tmem), to = tm + 256u + (uint32_t)DP * x;
     DkvItem upcoming = dkv_item(a, cta, sink_items, lane);
-    for (int item = cta; item < items && ok; item += ctas) {
+    for (int i = 0, item = cta; item < items && ok; item = at(++i)) {
       const int steps = warp_uniform(group * upcoming.nq), out = warp_uniform((int)upcoming.staged);
-      if (item + ctas < items) upcoming = dkv_item(a, item + ctas, sink_items, lane);
+      if (at(i + 1) < items) upcoming = dkv_item(a, at(i + 1), sink_items, lane);
       if (steps == 0) continue;
       const uint32_t b = nth % KV, kt = base + (x * KV + b) * SM::TILE;
       ok = mbar_wait_warp((x ? v_full : k_full) + 8 * b, nth / KV & 1, abort_flag, err, kErrDkv);
@@ -798,7 +856,7 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
   } else {
     Cursor<SM::SLOTS> cur;
     uint32_t raw_phase = 0, staged_phase = 0;
-    for (int item = cta; item < items && ok; item += ctas) {
+    for (int i = 0, item = cta; item < items && ok; item = at(++i)) {
       const DkvItem w = dkv_item(a, item, sink_items, lane);
       const int valid = w.t.len - (w.q_lo + w.nq - 1) * kAttnTile;  // of a head's last query tile
       if (w.nq > 0)
@@ -848,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    dkv_part<DP, false>(a, tmQ, tmK, tmV, tmDO, tmDK, tmDV, dk, dv, partial, partial_slots, err, abort_flag, stats, base, bars, 0, 0, 1, 0, 0,
+    dkv_part<DP, false>(a, tmQ, tmK, tmV, tmDO, tmDK, tmDV, dk, dv, partial, partial_slots, err, abort_flag, stats, nullptr, 0, base, bars, 0, 0, 1, 0, 0,
                  true);
     dq_part<DP, false>(a, tmQ, tmK, tmV, tmDO, tmDQ, dq, err, abort_flag, base, bars2, 0, 0, nullptr, true);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -868,12 +926,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (the registers are given by one instruction for all four warps of a group)
   if (warp < kMathWarps) {
     regs_up<kMathRegs>();
-    dkv_part<DP, true>(a, tmQ, tmK, tmV, tmDO, tmDK, tmDV, dk, dv, partial, partial_slots, err, abort_flag, stats, base, bars, tmem,
+    dkv_part<DP, true>(a, tmQ, tmK, tmV, tmDO, tmDK, tmDV, dk, dv, partial, partial_slots, err, abort_flag, stats, counter + 1, numbers + 4 * kPosts, base, bars, tmem,
                        cta, ctas, sink_items, items, false);
     dq_part<DP, true>(a, tmQ, tmK, tmV, tmDO, tmDQ, dq, err, abort_flag, base, bars2, tmem, numbers, counter, false);
   } else {
     regs_down<kOtherRegs>();
-    dkv_part<DP, false>(a, tmQ, tmK, tmV, tmDO, tmDK, tmDV, dk, dv, partial, partial_slots, err, abort_flag, stats, base, bars,
+    dkv_part<DP, false>(a, tmQ, tmK, tmV, tmDO, tmDK, tmDV, dk, dv, partial, partial_slots, err, abort_flag, stats, counter + 1, numbers + 4 * kPosts, base, bars,
                         tmem, cta, ctas, sink_items, items, false);
     dq_part<DP, false>(a, tmQ, tmK, tmV, tmDO, tmDQ, dq, err, abort_flag, base, bars2, tmem, numbers, counter, false);
   }
@@ -881,46 +939,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaA) tmem_dealloc<1>(tmem, 512);
-}
-
-// dK and dV of the sink keys: the first tile's own sums, then the chunks' (9 us for the
-// 15 chunks of 16384 tokens, latency).
-__global__ void __launch_bounds__(256) window_sink_kernel(const __grid_constant__ AttnArgs a,
-                                                          const float* __restrict__ partial, int64_t partial_slots,
-                                                          __nv_bfloat16* __restrict__ dk,
-                                                          __nv_bfloat16* __restrict__ dv) {
-  __shared__ int first_chunk;
-  pdl_launch();
-  pdl_wait();
-  const int sample = blockIdx.x, kv = blockIdx.y;
-  if (threadIdx.x < 32) {
-    // chunks of the samples before this one
-    int sum = 0;
-    if (a.cu)
-      for (int i = threadIdx.x; i < sample; i += 32) {
-        int b, len;
-        sample_span(a, i, b, len);
-        sum += sink_chunks(a, len, true);
-      }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (threadIdx.x == 0) first_chunk = sum;
-  }
-  __syncthreads();
-  int b = 0, len = a.n;
-  if (a.cu) sample_span(a, sample, b, len);
-  const int chunks = sink_chunks(a, len, true), rows = min(a.sinks, len);
-  const int64_t per = (int64_t)a.sinks * a.dim, slot = (int64_t)a.kv_heads * 2 * per;
-  for (int e = blockIdx.z * 256 + threadIdx.x; e < 2 * rows * a.dim; e += gridDim.z * 256) {
-    const int which = e >= rows * a.dim, x = which ? e - rows * a.dim : e;
-    const float* p = partial + (kv * 2 + which) * per + x;
-    float s = p[sample * slot];
-    const int64_t at = (int64_t)a.n_seqs + first_chunk, n = min((int64_t)chunks, partial_slots - at);
-#pragma unroll 8
-    for (int64_t c = 0; c < n; ++c) s += p[(at + c) * slot];
-    const int row = x / a.dim;
-    (which ? dk : dv)[(((int64_t)b + row) * a.kv_heads + kv) * a.dim + (x - row * a.dim)] = __float2bfloat16_rn(s);
-  }
 }
 
 template <int DP>
@@ -943,12 +961,8 @@ cudaError_t attn_backward(AttnArgs a, const CUtensorMap& q, const CUtensorMap& k
   if (e != cudaSuccess) return e;
   a.nlse2 = g.nlse2;
   a.ndelta = g.ndelta;
-  e = a.dim > 64 ? run_backward<128>(a, q, k, v, dout, g, err, sms, st)
-                 : run_backward<64>(a, q, k, v, dout, g, err, sms, st);
-  if (e != cudaSuccess || a.sinks == 0) return e;
-  return op_launch(window_sink_kernel, dim3((unsigned)a.n_seqs, (unsigned)a.kv_heads, (unsigned)((2 * a.sinks * a.dim + 255) / 256)),
-                   dim3(256), 0, st, 1, a,
-                   static_cast<const float*>(g.partial), g.partial_slots, g.dk, g.dv);
+  return a.dim > 64 ? run_backward<128>(a, q, k, v, dout, g, err, sms, st)
+                    : run_backward<64>(a, q, k, v, dout, g, err, sms, st);
 }
 
 }  // namespace ma
