@@ -15,12 +15,12 @@
 //
 // Bound by the tensor cores where samples are long: 16384 tokens of 16 heads of 128
 // over 8 key heads, all keys visible, take 2.5 ms, 1535 TFLOP/s of products formed
-// (0.81 of the measured bf16 peak). With a window of 1024 and four sinks 447 us, of
-// which window_grad_kernel 383 (8192 tokens: 231 us, without sinks 205). There a dK/dV
+// (0.81 of the measured bf16 peak). With a window of 1024 and four sinks 428 us, of
+// which the statistics are 25 (8192 tokens: GRAD8K us, without sinks GRAD8N). There a dK/dV
 // step takes 2950 cycles for 2048 of products, since S^T of the next queries waits
 // for dV, which waits for P^T in its place, a dQ step 2130 for 1536; edge tiles, the
 // sinks' own steps and the ends of items are the rest. Six samples of 7 to 1021 tokens
-// (16 heads of 64, window 256): 58 us, bound by the latency of items of three steps.
+// (16 heads of 64, window 256): 53 us, bound by the latency of items of three steps.
 //
 // The sink keys are seen by every query of a sample. Their gradients are cut
 // into chunks of kSinkChunk query tiles, each a work item of its own; the CTA that

@@ -281,7 +281,9 @@ ATTN = [  # lengths, tokens behind the last sample, heads, kv heads, dim, window
     ([128], 0, 2, 1, 128, 128, 0), ([256, 128], 0, 4, 2, 128, 100, 16), ([300], 0, 4, 1, 80, 37, 3),
     ([511, 1, 60], 5, 3, 3, 96, 130, 128), ([700], 0, 2, 2, 128, 700, 0), ([640], 0, 2, 1, 64, 1, 1),
     ([400], 7, 2, 1, 40, 0, 5), ([90, 0, 40], 0, 2, 2, 8, 0, 0), ([385, 257], 0, 6, 2, 128, 256, 64),
-    ([900], 0, 2, 1, 64, 128, 130 - 2), ([5] * 60, 0, 2, 2, 64, 3, 2), ([768], 100, 5, 5, 120, 257, 1)]
+    ([900], 0, 2, 1, 64, 128, 130 - 2), ([5] * 60, 0, 2, 2, 64, 3, 2), ([768], 100, 5, 5, 120, 257, 1),
+    # several chunks of query tiles that only the sinks reach, in more than one sample
+    ([2300, 40, 1500], 0, 2, 1, 64, 64, 6), ([1700], 20, 2, 2, 128, 40, 3)]
 
 
 def attn_case(rng, lengths, behind, h, g, d):
