@@ -32,8 +32,8 @@
 // the four products fill 2048 and a softmax takes 1950 (maximum 380, exponentials,
 // sum and rounding 1060, TMEM and barriers the rest); it is bound by issue, so that
 // exponentials as polynomials beside the special-function unit cost 12 to 20 %.
-// 16384 tokens of 16 heads of 128 over 8 key heads, all keys visible: 857 us, 1283
-// TFLOP/s (0.68 of the measured bf16 peak). Window 1024 and four sinks: 73 us for
+// 16384 tokens of 16 heads of 128 over 8 key heads, all keys visible: 775 us, 1419
+// TFLOP/s (0.75 of the measured bf16 peak). Window 1024 and four sinks: 73 us for
 // 8192 tokens; 139 us for 16360 in packed samples, 800 TFLOP/s counting visible
 // pairs, nine tiles being formed for eight tiles' worth of keys. 50 tokens of 16 heads
 // of 64: 6.3 us, the latency of one step and its set-up.
@@ -101,7 +101,17 @@ struct FwdItem {
 // Work item: a pair of query tiles. by_head: of two heads, which meet the same keys,
 // else of one head, whose two tiles meet one key tile more (8192 tokens of 16 heads,
 // window 1024: 73 us over 8 key heads, 79 us over 16).
-__device__ __forceinline__ FwdItem fwd_item(const AttnArgs& a, int item, int units, int lane) {
+//
+// FRO: the last tiles come first, which meet the most keys, and the CTAs take them to
+// and fro: every second round of items (the last one may be short) goes round the
+// other way.
+template <bool FRO>
+__device__ __forceinline__ FwdItem fwd_item(const AttnArgs& a, int nth, int items, int units, int lane) {
+  int item = nth;
+  if constexpr (FRO) {
+    const int ctas = gridDim.x, turn = nth / ctas, at = nth - turn * ctas, round = min(ctas, items - turn * ctas);
+    item = items - 1 - (turn * ctas + (turn & 1 ? round - 1 - at : at));
+  }
   const bool by_head = units * 2 == a.heads;
   const int rows = by_head ? kAttnTile : 2 * kAttnTile;
   const int tile = item / units, u = item - tile * units;
@@ -116,7 +126,7 @@ __device__ __forceinline__ FwdItem fwd_item(const AttnArgs& a, int item, int uni
   return w;
 }
 
-template <int DP>
+template <int DP, bool FRO>
 __global__ void __launch_bounds__(kThreads, 1)
     window_forward_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tmQ,
                           const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -168,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool wide = rows_wide(out, a.dim);
     uint32_t s_ph = 0, o_ph = 0;
     Cursor<SM::SLOTS> cur;
-    FwdItem next = fwd_item(a, blockIdx.x, units, lane);
+    FwdItem next = fwd_item<FRO>(a, blockIdx.x, items, units, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       const FwdItem w = next;
       const int p0 = w.t.p0 + (w.head0 == w.head1 ? s * kAttnTile : 0), i = p0 + row, row0 = p0 + (row & ~31);
@@ -254,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(p_full + 8 * s);
       }
       if (!ok) break;
-      if (item + (int)gridDim.x < items) next = fwd_item(a, item + gridDim.x, units, lane);
+      if (item + (int)gridDim.x < items) next = fwd_item<FRO>(a, item + gridDim.x, items, units, lane);
       if (any) {
         ok = mbar_wait_warp(o_full + 8 * s, o_ph, abort_flag, err, kErrForward);
         if (!ok) break;
@@ -286,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Cursor<SM::SLOTS> cur;
     uint32_t loads = 0, raw_phase = 0;
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const FwdItem w = fwd_item(a, item, units, lane);
+      const FwdItem w = fwd_item<FRO>(a, item, items, units, lane);
       if (lane == 0) {
         for (int n = 0; n < w.k.steps && ok; ++n) {
           const int at = w.k.tile(n) * kAttnTile;
@@ -329,12 +339,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s = warp_uniform(warp - 9), few = sink_columns(a);
     const uint32_t ts = warp_uniform(tmem) + 128u * s, to = ts + 256u, qt = base + s * SM::TILE;
     const uint32_t sf = s_full + 8 * s, pf = p_full + 8 * s, of = o_full + 8 * s;
-    FwdItem next = fwd_item(a, blockIdx.x, units, lane);
+    FwdItem next = fwd_item<FRO>(a, blockIdx.x, items, units, lane);
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
       const int steps = warp_uniform(next.k.steps), first = warp_uniform(s ? next.k.a1 : next.k.a0),
                 last = warp_uniform(s ? next.k.b1 : next.k.b0), sink = warp_uniform((int)(s ? next.k.z1 : next.k.z0)), staged_out = warp_uniform((int)next.staged);
       if (steps == 0 || !(ok = mbar_wait_warp(q_full, q_ph, abort_flag, err, kErrForward))) {
-        if (item + (int)gridDim.x < items) next = fwd_item(a, item + gridDim.x, units, lane);
+        if (item + (int)gridDim.x < items) next = fwd_item<FRO>(a, item + gridDim.x, items, units, lane);
         continue;
       }
       q_ph ^= 1;
@@ -383,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         cur.advance();
         vc = cur;
         cur.advance();
-        if (n == 0 && item + (int)gridDim.x < items) next = fwd_item(a, item + gridDim.x, units, lane);
+        if (n == 0 && item + (int)gridDim.x < items) next = fwd_item<FRO>(a, item + gridDim.x, items, units, lane);
       }
       if (staged_out) cur.skip(2);
     }
@@ -395,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Cursor<SM::SLOTS> cur;
     uint32_t raw_phase = 0, staged_phase = 0;
     for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
-      const FwdItem w = fwd_item(a, item, units, lane);
+      const FwdItem w = fwd_item<FRO>(a, item, items, units, lane);
       if (w.k.steps == 0) continue;
       cur.skip(2 * w.k.steps - 1);
       const int valid = w.t.len - w.k.tile(w.k.steps - 1) * kAttnTile;  // only the last tile can be ragged
@@ -415,16 +425,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) tmem_dealloc<1>(tmem, 512);
 }
 
-template <int DP>
+template <int DP, bool FRO>
 cudaError_t run_forward(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                         const CUtensorMap& o, __nv_bfloat16* out, float* lse, int* err, int sms, cudaStream_t st) {
   const int group = a.heads / a.kv_heads;
   const int units = group % 2 == 0 ? a.heads / 2 : a.heads;
   const int rows = group % 2 == 0 ? kAttnTile : 2 * kAttnTile;
   const int64_t most = attn_max_tiles(a.n, a.cu ? a.n_seqs : 1, rows) * units;
-  const cudaError_t e = op_smem_limit<window_forward_kernel<DP>>((int)FwdSmem<DP>::BYTES);
+  const cudaError_t e = op_smem_limit<window_forward_kernel<DP, FRO>>((int)FwdSmem<DP>::BYTES);
   if (e != cudaSuccess) return e;
-  return op_launch(window_forward_kernel<DP>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads),
+  return op_launch(window_forward_kernel<DP, FRO>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads),
                    FwdSmem<DP>::BYTES, st, 1, a, q, k, v, o, out, lse, err, units);
 }
 
@@ -539,8 +549,16 @@ bool attn_map(CUtensorMap* tm, const void* base, int dim, int64_t tokens, int64_
 
 cudaError_t attn_forward(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                          const CUtensorMap& o, __nv_bfloat16* out, float* lse, int* err, int sms, cudaStream_t st) {
-  return a.dim > 64 ? run_forward<128>(a, q, k, v, o, out, lse, err, sms, st)
-                    : run_forward<64>(a, q, k, v, o, out, lse, err, sms, st);
+  // Items that differ go longest first, to and fro: where the window is more than an eighth of all tokens (all keys of
+  // 16384 visible: 772 us, in plain order 865; of 8192 211 and 249). Below they are alike, and in plain order only the
+  // last keys of a tile have not been read before (window 1024 of 16384: 134 us, the other way 138; 16360 tokens in
+  // eight samples 136 and 143).
+  const bool fro = (int64_t)a.window * 8 > a.n;
+  if (a.dim > 64)
+    return fro ? run_forward<128, true>(a, q, k, v, o, out, lse, err, sms, st)
+               : run_forward<128, false>(a, q, k, v, o, out, lse, err, sms, st);
+  return fro ? run_forward<64, true>(a, q, k, v, o, out, lse, err, sms, st)
+             : run_forward<64, false>(a, q, k, v, o, out, lse, err, sms, st);
 }
 
 }  // namespace ma

@@ -14,13 +14,14 @@
 // order that changes from run to run, or stored in fp32 once per key tile.
 //
 // Bound by the tensor cores where samples are long: 16384 tokens of 16 heads of 128
-// over 8 key heads, all keys visible, take 2.5 ms, 1535 TFLOP/s of products formed
-// (0.81 of the measured bf16 peak). With a window of 1024 and four sinks 428 us, of
-// which the statistics are 25 (8192 tokens: GRAD8K us, without sinks GRAD8N). There a dK/dV
+// over 8 key heads, all keys visible, take 2.3 ms, 1659 TFLOP/s of products formed
+// (0.88 of the measured bf16 peak). With a window of 1024 and four sinks 440 us, of
+// which the statistics are 25 (8192 tokens over 16 key heads: 222 us, without sinks
+// 204). There a dK/dV
 // step takes 2950 cycles for 2048 of products, since S^T of the next queries waits
 // for dV, which waits for P^T in its place, a dQ step 2130 for 1536; edge tiles, the
 // sinks' own steps and the ends of items are the rest. Six samples of 7 to 1021 tokens
-// (16 heads of 64, window 256): 53 us, bound by the latency of items of three steps.
+// (16 heads of 64, window 256): 52 us, bound by the latency of items of three steps.
 //
 // The sink keys are seen by every query of a sample. Their gradients are cut
 // into chunks of kSinkChunk query tiles, each a work item of its own; the CTA that
@@ -135,7 +136,9 @@ __device__ __forceinline__ void parts_sync() {
 }
 
 // dQ items go to the CTAs in the order in which they come for them, so that those
-// whose dK/dV items took longer take fewer. The TMA warp draws an item's number
+// whose dK/dV items took longer take fewer (static shares: 6 % longer on short
+// samples, 1 % at 16384 tokens; all keys of 8192 visible 700 us, drawn 618, and drawn
+// with the last tiles first 590). The TMA warp draws an item's number
 // from a counter, one item ahead of its loads, and posts it to the other warps.
 constexpr int kPosts = 4;
 struct DqPosts {
@@ -204,6 +207,8 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
   }
   const int items = a.heads * count_units(a, lane, [](int len, bool) { return (len + kAttnTile - 1) / kAttnTile; });
   const int few = sink_columns(a);
+  // the last tiles first: where the window lets them, they meet the most keys
+  auto nth_item = [&](int n) { return dq_item(a, items - 1 - n, lane); };
   bool ok = true;
   int item = INT_MAX;
   if (!MATH && warp == kTma) item = posts.post(counter, lane, ok, abort_flag, err);
@@ -220,7 +225,7 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     const bool wide = rows_wide(dq, a.dim);
     DqItem next;
-    if (item < items) next = dq_item(a, item, lane);
+    if (item < items) next = nth_item(item);
     while (item < items && ok) {
       const DqItem w = next;
       const int i = w.t.p0 + row;
@@ -280,7 +285,7 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
       }
       if (!ok) break;
       item = posts.take(lane, ok, abort_flag, err);
-      if (item < items) next = dq_item(a, item, lane);
+      if (item < items) next = nth_item(item);
       if (w.steps) {
         ok = mbar_wait_warp(dq_full, dq_ph, abort_flag, err, kErrDq);
         if (!ok) break;
@@ -307,7 +312,7 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
     Cursor<SM::SLOTS> cur;
     uint32_t loads = 0, raw_phase = 0;
     while (item < items && ok) {
-      const DqItem w = dq_item(a, item, lane);
+      const DqItem w = nth_item(item);
       item = posts.post(counter, lane, ok, abort_flag, err);
       if (lane == 0) {
         for (int n = 0; n < w.steps && ok; ++n) {
@@ -352,13 +357,13 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
     uint32_t q_ph = 0, ds_ph = 0;  // ds_ph: a bit per S slot
     const uint32_t tm = warp_uniform(tmem);
     DqItem next;
-    if (item < items) next = dq_item(a, item, lane);
+    if (item < items) next = nth_item(item);
     while (item < items && ok) {
       const int steps = warp_uniform(next.steps), sink = warp_uniform((int)next.k.sink),
                 out = warp_uniform((int)next.staged);
       if (steps == 0) {
         item = posts.take(lane, ok, abort_flag, err);
-        if (item < items) next = dq_item(a, item, lane);
+        if (item < items) next = nth_item(item);
         continue;
       }
       Cursor<SM::SLOTS> qc = sc;  // the next dQ's key tile
@@ -374,7 +379,7 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
       ok = mbar_wait_warp(q_full, q_ph, abort_flag, err, kErrDq) && issue_s(0) && (steps == 1 || issue_s(1));
       q_ph ^= 1;
       item = posts.take(lane, ok, abort_flag, err);
-      if (item < items) next = dq_item(a, item, lane);
+      if (item < items) next = nth_item(item);
       for (int n = 0; n < steps && ok; ++n) {
         // (a barrier to each slot of S: the threads need nothing of this warp for the step after, so that they
         // may be through with it before this wait, and one barrier's phases would have passed twice)
@@ -402,12 +407,12 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
     uint32_t q_ph = 0, step = 0;
     const uint32_t tm = warp_uniform(tmem);
     DqItem next;
-    if (item < items) next = dq_item(a, item, lane);
+    if (item < items) next = nth_item(item);
     while (item < items && ok) {
       const int steps = warp_uniform(next.steps), sink = warp_uniform((int)next.k.sink),
                 out = warp_uniform((int)next.staged);
       item = posts.take(lane, ok, abort_flag, err);
-      if (item < items) next = dq_item(a, item, lane);
+      if (item < items) next = nth_item(item);
       if (steps == 0) continue;
       ok = ok && mbar_wait_warp(do_full, q_ph, abort_flag, err, kErrDq);
       q_ph ^= 1;
@@ -433,7 +438,7 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
     Cursor<SM::SLOTS> cur;
     uint32_t raw_phase = 0, staged_phase = 0;
     while (item < items && ok) {
-      const DqItem w = dq_item(a, item, lane);
+      const DqItem w = nth_item(item);
       item = posts.take(lane, ok, abort_flag, err);
       if (w.steps == 0) continue;
       cur.skip(2 * w.steps - 2);
@@ -463,7 +468,7 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
 // dP^T, each block in the first 16 of its own 32 columns. While the threads form P^T
 // of a step the tensor core runs the step before's dK and this one's dP^T; while
 // they form dS^T it runs dV and the next step's S^T (with two buffers S^T is formed a
-// step earlier: 8192 tokens of 16 heads of 64 take 174 us, of 72 229).
+// step earlier: 8192 tokens of 16 heads of 64 take 162 us, of 72 208).
 //
 // First query tile that only the sinks reach in tile 0.
 __device__ __forceinline__ int first_sink_tile(const AttnArgs& a) {
@@ -878,9 +883,7 @@ __device__ __forceinline__ void dkv_part(const AttnArgs& a, const CUtensorMap& t
 }
 
 // dK and dV, then dQ: one persistent CTA per SM runs its items of the one and then
-// its items of the other, so that no SM waits in between for the slowest. (Two
-// launches took 47 us on six samples of 7 to 1021 tokens and 428 us on 16384 tokens,
-// this one 43 and 426.)
+// its items of the other, so that no SM waits in between for the slowest.
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     window_grad_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tmQ,

@@ -529,6 +529,30 @@ def test_wrappers_refuse(ops):
     ops.check()
 
 
+@pytest.mark.parametrize("n,h,g,d,window,sinks", [
+    (3890, 16, 8, 64, None, 0), (3890, 16, 8, 64, 300, 5), (2600, 16, 8, 128, 900, 3), (5000, 12, 12, 64, None, 2),
+    (1300, 40, 20, 64, None, 1)])
+def test_window_attention_many_items(ops, n, h, g, d, window, sinks):
+    """More items than CTAs, in whole and part rounds: each key head's results are those of a call of its own."""
+    import torch
+
+    rng = np.random.default_rng(n + h)
+    q, k, v, do = (cuda(signal(rng, n, x, d), "bf16") for x in (h, g, g, h))
+    how = {"window": window, "sinks": sinks}
+    out, lse = ops.window_attention(q, k, v, **how)
+    grads = ops.window_attention_backward(do, q, k, v, out, lse, **how)
+    assert all(bool(x.isfinite().all()) for x in (out, lse, *grads))
+    per = h // g
+    for i in range(g):
+        hs, ks = slice(per * i, per * (i + 1)), slice(i, i + 1)
+        o1, l1 = ops.window_attention(q[:, hs], k[:, ks], v[:, ks], **how)
+        assert torch.equal(o1, out[:, hs]) and torch.equal(l1, lse[hs])
+        one = ops.window_attention_backward(do[:, hs], q[:, hs], k[:, ks], v[:, ks], o1, l1, **how)
+        for a, b in zip(one, (grads[0][:, hs], grads[1][:, ks], grads[2][:, ks])):
+            assert torch.equal(a, b)
+    ops.check()
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 def test_window_attention_many_calls(ops, dim):
     """A packed batch again and again: no bounded wait runs out, and every call gives the same bits."""
