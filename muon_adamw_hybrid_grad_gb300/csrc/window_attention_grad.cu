@@ -17,11 +17,11 @@
 // over 8 key heads, all keys visible, take 2.3 ms, 1659 TFLOP/s of products formed
 // (0.88 of the measured bf16 peak). With a window of 1024 and four sinks 440 us, of
 // which the statistics are 25 (8192 tokens over 16 key heads: 222 us, without sinks
-// 204). There a dK/dV
-// step takes 2950 cycles for 2048 of products, since S^T of the next queries waits
-// for dV, which waits for P^T in its place, a dQ step 2130 for 1536; edge tiles, the
-// sinks' own steps and the ends of items are the rest. Six samples of 7 to 1021 tokens
-// (16 heads of 64, window 256): 52 us, bound by the latency of items of three steps.
+// 204). There a dK/dV step takes 2950 cycles for 2048 of products, since S^T of the
+// next queries waits for dV, which waits for P^T in its place, a dQ step 2130 for 1536;
+// edge tiles, the sinks' own steps and the ends of items are the rest. Six samples of 7
+// to 1021 tokens (16 heads of 64, window 256): 52 us, bound by the latency of items of
+// three steps.
 //
 // The sink keys are seen by every query of a sample. Their gradients are cut
 // into chunks of kSinkChunk query tiles, each a work item of its own; the CTA that
@@ -87,8 +87,8 @@ __global__ void __launch_bounds__(256) window_stats_kernel(const __grid_constant
 // Warps 0-15: a thread to a query and a block of 32 of a tile's keys (warps 0-3
 // the first block, and so on); warp 16: TMA; warps 17 and 18: tcgen05.mma, the
 // one S and dQ, the other dP; warp 19: clears the key and value rows of other
-// samples and stores the finished tiles. Sixteen warps rather than eight with twice the keys: a step's chain of
-// waits, TMEM reads and exponentials is what bounds this kernel.
+// samples and stores the finished tiles. Sixteen warps rather than eight with twice
+// the keys: a step's chain of waits, TMEM reads and exponentials is what bounds this.
 // TMEM: S of even steps | S of odd steps | dP | dQ. dS (bf16) overwrites the S
 // it came from, each block in the first 16 of its own 32 columns. S of the next
 // tile is formed while the threads work on this one's, and dP of the next as
