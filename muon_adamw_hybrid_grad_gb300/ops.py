@@ -125,14 +125,16 @@ class _QkNormRope(torch.autograd.Function):
 class _WindowAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, cu_seqlens, window, sinks, scale):
-        ctx.how = {"window": window, "sinks": sinks, "scale": scale, "cu_seqlens": cu_seqlens}
-        out, lse = window_attention(q, k, v, **ctx.how)
-        ctx.save_for_backward(q, k, v, out, lse)
+        ctx.how = {"window": window, "sinks": sinks, "scale": scale}
+        out, lse = window_attention(q, k, v, cu_seqlens=cu_seqlens, **ctx.how)
+        # the bounds too: autograd then refuses a gradient behind a write to them
+        ctx.save_for_backward(q, k, v, out, lse, cu_seqlens)
         return out
 
     @staticmethod
     def backward(ctx, dout):
-        return (*window_attention_backward(dout, *ctx.saved_tensors, **ctx.how), None, None, None, None)
+        *saved, cu_seqlens = ctx.saved_tensors
+        return (*window_attention_backward(dout, *saved, cu_seqlens=cu_seqlens, **ctx.how), None, None, None, None)
 
 
 def embedding_autograd(weight, ids, *, scale: float = 1.0, dtype: Optional[torch.dtype] = None):

@@ -1,0 +1,108 @@
+"""The operators' autograd forms and what autograd is told of them.
+
+What needs no kernel runs on the CPU, with plain stand-ins for the calls into
+the library; the rest runs on the GPU.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def ops():
+    from muon_adamw_hybrid_grad_gb300 import build
+
+    build.build()
+    from muon_adamw_hybrid_grad_gb300 import ops as m
+
+    return m
+
+
+def sample_of(bounds, n):
+    return torch.searchsorted(bounds.long(), torch.arange(n), right=True)
+
+
+@pytest.fixture
+def plain_attention(ops, monkeypatch):
+    """Attention of one query head in plain CPU operations, in place of the library's calls."""
+
+    def weights(q, k, window, sinks, scale, cu_seqlens):
+        n = q.shape[0]
+        i, j = torch.arange(n)[:, None], torch.arange(n)[None]
+        cu = torch.tensor([0, n]) if cu_seqlens is None else cu_seqlens
+        s = sample_of(cu, n)
+        first = cu.long()[s - 1]
+        see = (s[:, None] == s[None]) & (j <= i) & ((i - j < window) | (j - first[None] < sinks))
+        return torch.softmax((scale * q[:, 0] @ k[:, 0].T).masked_fill(~see, -np.inf), -1)
+
+    def forward(q, k, v, *, window, sinks=0, scale=None, cu_seqlens=None):
+        p = weights(q, k, window, sinks, scale, cu_seqlens)
+        return (p @ v[:, 0])[:, None], torch.zeros(1, q.shape[0])
+
+    def backward(dout, q, k, v, out, lse, *, window, sinks=0, scale=None, cu_seqlens=None):
+        p = weights(q, k, window, sinks, scale, cu_seqlens)
+        dp = dout[:, 0] @ v[:, 0].T
+        ds = scale * p * (dp - (p * dp).sum(1, keepdim=True))
+        return tuple(x[:, None] for x in (ds @ k[:, 0], ds.T @ q[:, 0], p.T @ dout[:, 0]))
+
+    monkeypatch.setattr(ops, "window_attention", forward)
+    monkeypatch.setattr(ops, "window_attention_backward", backward)
+    return weights
+
+
+def leaves(n, d, seed):
+    gen = torch.Generator().manual_seed(seed)
+    return [torch.randn(n, 1, d, generator=gen, dtype=torch.float64).requires_grad_() for _ in range(3)]
+
+
+# ---- the samples' bounds ----
+
+def test_attention_gradient_of_bounds_written_again_raises(ops, plain_attention):
+    """One buffer of bounds, filled anew for each batch: a backward pass behind that must not take the new ones."""
+    q, k, v = leaves(12, 4, 0)
+    bounds = torch.tensor([0, 5, 12], dtype=torch.int32)
+    out = ops.window_attention_autograd(q, k, v, window=3, scale=0.5, cu_seqlens=bounds)
+    bounds.copy_(torch.tensor([0, 9, 12], dtype=torch.int32))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+
+
+@pytest.mark.parametrize("cu", [None, [0, 5, 12]])
+def test_attention_form_takes_the_bounds_to_its_gradient(ops, plain_attention, cu):
+    q, k, v = leaves(12, 4, 1)
+    bounds = None if cu is None else torch.tensor(cu, dtype=torch.int32)
+    how = {"window": 3, "sinks": 1, "scale": 0.5, "cu_seqlens": bounds}
+    d = torch.randn(12, 1, 4, generator=torch.Generator().manual_seed(2), dtype=torch.float64)
+    got = torch.autograd.grad(ops.window_attention_autograd(q, k, v, **how), (q, k, v), d)
+    want = torch.autograd.grad((plain_attention(q, k, *how.values()) @ v[:, 0])[:, None], (q, k, v), d)
+    # sums of at most 12 terms of size 10 in fp64
+    assert all((a - b).abs().max() < 1e-12 for a, b in zip(got, want))
+
+
+def packed_case(lengths, h, g, d, seed=0):
+    rng = np.random.default_rng(seed)
+    n = sum(lengths)
+    q, k, v, do = (torch.tensor(rng.normal(size=(n, x, d)), dtype=torch.bfloat16, device="cuda") for x in (h, g, g, h))
+    return q, k, v, do, torch.tensor(np.cumsum([0] + lengths), dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.gpu
+def test_autograd_of_packed_attention(ops):
+    """Two micro-batches in flight, each with its own bounds; then bounds that are written again."""
+    lengths = ([70, 1, 129], [200])
+    cases = [packed_case(x, 4, 2, 64, i) for i, x in enumerate(lengths)]
+    forms = []
+    for q, k, v, do, cu in cases:
+        x = [t.clone().requires_grad_() for t in (q, k, v)]
+        forms.append((x, ops.window_attention_autograd(*x, window=40, sinks=2, cu_seqlens=cu)))
+    for (q, k, v, do, cu), (x, out) in zip(cases, forms):
+        out.backward(do)
+        o, lse = ops.window_attention(q, k, v, window=40, sinks=2, cu_seqlens=cu)
+        want = ops.window_attention_backward(do, q, k, v, o, lse, window=40, sinks=2, cu_seqlens=cu)
+        assert torch.equal(out, o) and all(torch.equal(a.grad, b) for a, b in zip(x, want))
+    q, k, v, do, cu = cases[0]
+    out = ops.window_attention_autograd(q.requires_grad_(), k, v, window=40, cu_seqlens=cu)
+    cu[1] = 7
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.backward(do)
