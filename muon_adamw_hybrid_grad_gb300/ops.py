@@ -13,6 +13,7 @@ MuonAdamWError with the library's status.
 """
 from __future__ import annotations
 
+import functools
 import importlib.machinery
 import importlib.util
 import os
@@ -95,6 +96,36 @@ def check() -> None:
 
 # ---- forms for autograd ----
 
+class _FirstOrder(torch.autograd.Function):
+    """The gradients, unchanged, as a function of what they were formed from: differentiating them raises. Left
+    without a graph they would count as constants."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(x.view_as(x) for x in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the operators have no second derivative")
+
+
+def _first_order(backward):
+    """For the backward functions below, whose kernels record no graph of their own."""
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        with torch.no_grad():
+            outputs = backward(ctx, *grads)
+        if not torch.is_grad_enabled():  # no create_graph
+            return outputs
+        formed_from = [x for x in (*grads, *ctx.saved_tensors) if x is not None and x.requires_grad]
+        if not formed_from:
+            return outputs
+        some = [x for x in outputs if x is not None]
+        some = iter(_FirstOrder.apply(len(some), *some, *formed_from))
+        return tuple(None if x is None else next(some) for x in outputs)
+    return run
+
+
 class _Embedding(torch.autograd.Function):
     @staticmethod
     def forward(ctx, weight, ids, scale, dtype):
@@ -103,6 +134,7 @@ class _Embedding(torch.autograd.Function):
         return embedding(weight, ids, scale=scale, dtype=dtype)
 
     @staticmethod
+    @_first_order
     def backward(ctx, dout):
         (ids,) = ctx.saved_tensors
         shape, dtype, dev = ctx.like
@@ -118,6 +150,7 @@ class _QkNormRope(torch.autograd.Function):
         return qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, **ctx.how)
 
     @staticmethod
+    @_first_order
     def backward(ctx, dq_out, dk_out):
         return (*qk_norm_rope_backward(dq_out, dk_out, *ctx.saved_tensors, **ctx.how), None, None, None, None, None)
 
@@ -132,6 +165,7 @@ class _WindowAttention(torch.autograd.Function):
         return out
 
     @staticmethod
+    @_first_order
     def backward(ctx, dout):
         *saved, cu_seqlens = ctx.saved_tensors
         return (*window_attention_backward(dout, *saved, cu_seqlens=cu_seqlens, **ctx.how), None, None, None, None)

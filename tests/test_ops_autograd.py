@@ -106,3 +106,53 @@ def test_autograd_of_packed_attention(ops):
     cu[1] = 7
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         out.backward(do)
+
+
+# ---- second derivatives ----
+
+NO_SECOND = "no second derivative"
+
+
+def test_attention_refuses_a_second_derivative(ops, plain_attention):
+    """A penalty on the gradient would otherwise go missing from the loss without a word."""
+    q, k, v = leaves(9, 4, 3)
+    out = ops.window_attention_autograd(q, k, v, window=4, scale=0.5)
+    (g,) = torch.autograd.grad(out.sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError, match=NO_SECOND):
+        (out.sum() + g.square().sum()).backward()
+
+
+def test_norm_refuses_a_second_derivative(ops, monkeypatch):
+    monkeypatch.setattr(ops, "qk_norm_rope", lambda q, k, qw, kw, *rest, **how: (q * q * qw, k * k * kw))
+    monkeypatch.setattr(ops, "qk_norm_rope_backward", lambda dq, dk, q, k, qw, kw, *rest, **how: (
+        2 * dq * q * qw, 2 * dk * k * kw, (dq * q * q).sum((0, 1)), (dk * k * k).sum((0, 1))))
+    q, k, w = (torch.ones(s, dtype=torch.float64).requires_grad_() for s in ((3, 2, 4), (3, 1, 4), (4,)))
+    t, pos = torch.ones(3, 2), torch.zeros(3, dtype=torch.int64)
+    qo, ko = ops.qk_norm_rope_autograd(q, k, w, w, t, t, pos)
+    (g,) = torch.autograd.grad(qo.sum() + ko.sum(), w, create_graph=True)
+    with pytest.raises(RuntimeError, match=NO_SECOND):
+        (qo.sum() + g.square().sum()).backward()
+
+
+def test_embedding_refuses_a_second_derivative(ops, monkeypatch):
+    """Its gradient is linear in what comes in: only a gradient of that one goes on."""
+    monkeypatch.setattr(ops, "embedding", lambda w, ids, *, scale, dtype: scale * w[ids])
+    monkeypatch.setattr(ops, "embedding_backward",
+                        lambda dout, ids, grad, *, scale: grad.zero_().index_add_(0, ids, scale * dout))
+    w, ids = torch.ones(5, 4, dtype=torch.float64).requires_grad_(), torch.tensor([1, 3, 1])
+    out = ops.embedding_autograd(w, ids, scale=2.0)
+    (g,) = torch.autograd.grad(out.square().sum(), w, create_graph=True)
+    with pytest.raises(RuntimeError, match=NO_SECOND):
+        (out.sum() + g.square().sum()).backward()
+    (g,) = torch.autograd.grad(ops.embedding_autograd(w, ids, scale=2.0).sum(), w, create_graph=True)
+    assert not g.requires_grad
+
+
+def test_a_graph_of_the_gradient_that_nothing_differentiates(ops, plain_attention):
+    """create_graph alone is no error, and gives the same first derivatives."""
+    q, k, v = leaves(9, 4, 4)
+    out = ops.window_attention_autograd(q, k, v, window=4, scale=0.5)
+    held = torch.autograd.grad(out.square().sum(), (q, k, v), create_graph=True)
+    out = ops.window_attention_autograd(q, k, v, window=4, scale=0.5)
+    plain = torch.autograd.grad(out.square().sum(), (q, k, v))
+    assert all(torch.equal(a, b) for a, b in zip(held, plain))
