@@ -206,6 +206,17 @@ Heads heads_of(const Tensor& t, const char* name, bool apart) {
   return r;
 }
 
+// The same with every row on a 16-byte boundary, by a copy where one is not. For
+// gradients and saved outputs: autograd chooses their layout (a slice of a wider
+// row, say), and a caller of a backward pass can do nothing about it.
+Heads aligned_heads(const Tensor& t, const char* name, bool apart) {
+  Heads r = heads_of(t, name, apart);
+  const int64_t e = (int64_t)r.t.element_size();
+  if (r.ts * e % 16 || r.hs * e % 16 || reinterpret_cast<uintptr_t>(r.t.const_data_ptr()) % 16)
+    r = heads_of(r.t.detach().clone(at::MemoryFormat::Contiguous), name, apart);
+  return r;
+}
+
 struct Qk {
   Heads q, k;
   Tensor keep[5];
@@ -274,8 +285,8 @@ PyObject* qk_norm_rope_backward(PyObject* const* a) {
   read_qk(x, a + 2);
   const Tensor& q = x.q.t;
   const at::ScalarType type = q.scalar_type();
-  const Heads dqo = heads_of(tensor(a[0], "dq_out", q), "dq_out", false);
-  const Heads dko = heads_of(tensor(a[1], "dk_out", q), "dk_out", false);
+  const Heads dqo = aligned_heads(tensor(a[0], "dq_out", q), "dq_out", false);
+  const Heads dko = aligned_heads(tensor(a[1], "dk_out", q), "dk_out", false);
   if (dqo.t.sizes() != q.sizes() || dko.t.sizes() != x.k.t.sizes() || dqo.t.scalar_type() != type ||
       dko.t.scalar_type() != type)
     refuse(PyExc_ValueError, "dq_out and dk_out must have the shapes and the type of q and k");
@@ -363,11 +374,8 @@ PyObject* window_attention_backward(PyObject* const* a) {
   Attn x;
   read_attention(x, a + 1, a + 6);
   const Tensor& q = x.q.t;
-  const Heads dout = heads_of(tensor(a[0], "dout", q), "dout", true);
-  Heads out = heads_of(tensor(a[4], "out", q), "out", true);
-  // rows that do not lie on 16-byte boundaries are copied: what the forward call returned always does
-  if (out.ts % 8 || out.hs % 8 || reinterpret_cast<uintptr_t>(out.t.const_data_ptr()) % 16)
-    out = heads_of(out.t.detach().clone(at::MemoryFormat::Contiguous), "out", true);
+  const Heads dout = aligned_heads(tensor(a[0], "dout", q), "dout", true);
+  const Heads out = aligned_heads(tensor(a[4], "out", q), "out", true);
   const Tensor& lse = tensor(a[5], "lse", q);
   if (dout.t.sizes() != q.sizes() || out.t.sizes() != q.sizes() || dout.t.scalar_type() != at::kBFloat16 ||
       out.t.scalar_type() != at::kBFloat16)

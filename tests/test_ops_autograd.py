@@ -156,3 +156,49 @@ def test_a_graph_of_the_gradient_that_nothing_differentiates(ops, plain_attentio
     out = ops.window_attention_autograd(q, k, v, window=4, scale=0.5)
     plain = torch.autograd.grad(out.square().sum(), (q, k, v))
     assert all(torch.equal(a, b) for a, b in zip(held, plain))
+
+
+# ---- gradients in layouts that autograd chose ----
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("first", [False, True])
+@pytest.mark.parametrize("d", [64, 72])
+def test_attention_gradient_of_a_slice_off_16_bytes(ops, first, d):
+    """The output joined with a column: its gradient comes back as a slice whose rows miss 16-byte boundaries."""
+    h, g = 4, 2
+    q, k, v, do, cu = packed_case([130, 57], h, g, d)
+    how = {"window": 50, "sinks": 2, "cu_seqlens": cu}
+    x = [t.clone().requires_grad_() for t in (q, k, v)]
+    out = ops.window_attention_autograd(*x, **how)
+    gate = torch.ones(len(do), 1, dtype=torch.bfloat16, device="cuda")
+    parts = [out.flatten(1), gate] if first else [gate, out.flatten(1)]
+    wide = torch.full((len(do), h * d + 1), 3.0, dtype=torch.bfloat16, device="cuda")
+    (wide[:, :-1] if first else wide[:, 1:]).copy_(do.flatten(1))
+    torch.cat(parts, 1).backward(wide)
+    o, lse = ops.window_attention(q, k, v, **how)
+    want = ops.window_attention_backward(do, q, k, v, o, lse, **how)
+    assert all(torch.equal(a.grad, b) for a, b in zip(x, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("first", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norm_gradient_of_a_slice_off_16_bytes(ops, first, dtype):
+    n, h, g, d = 37, 4, 2, 64
+    rng = np.random.default_rng(1)
+    t = lambda *s: torch.tensor(rng.normal(size=s), dtype=dtype, device="cuda")  # noqa: E731
+    q, k, dq, dk = t(n, h, d), t(n, g, d), t(n, h, d), t(n, g, d)
+    qw, kw = (1 + 0.1 * t(d).float() for _ in range(2))
+    cos, sin = t(8, 16).float(), t(8, 16).float()
+    pos = torch.arange(n, device="cuda") % 8
+    x = [y.clone().requires_grad_() for y in (q, k, qw, kw)]
+    outs = ops.qk_norm_rope_autograd(*x, cos, sin, pos)
+    gate = torch.ones(n, 1, dtype=dtype, device="cuda")
+    joined, wides = [], []
+    for y, dy in zip(outs, (dq, dk)):
+        joined.append(torch.cat([y.flatten(1), gate] if first else [gate, y.flatten(1)], 1))
+        wides.append(torch.full_like(joined[-1], 3.0))
+        (wides[-1][:, :-1] if first else wides[-1][:, 1:]).copy_(dy.flatten(1))
+    torch.autograd.backward(joined, wides)
+    want = ops.qk_norm_rope_backward(dq, dk, q, k, qw, kw, cos, sin, pos)
+    assert all(torch.equal(a.grad, b) for a, b in zip(x, want))
