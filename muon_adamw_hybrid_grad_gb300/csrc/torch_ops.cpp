@@ -182,6 +182,8 @@ PyObject* embedding_backward(PyObject* const* a) {
                                          grad.mutable_data_ptr(), gdt, g.stride, g.vocab, g.width, acc,
                                          ws.mutable_data_ptr(), bytes, s);
   });
+  // as any write in place: a graph that saved the tensor is to notice (inference tensors count no versions)
+  if (!grad.is_inference()) grad.unsafeGetTensorImpl()->bump_version();
   return Py_NewRef(a[2]);
 }
 

@@ -202,3 +202,28 @@ def test_norm_gradient_of_a_slice_off_16_bytes(ops, first, dtype):
     torch.autograd.backward(joined, wides)
     want = ops.qk_norm_rope_backward(dq, dk, q, k, qw, kw, cos, sin, pos)
     assert all(torch.equal(a.grad, b) for a, b in zip(x, want))
+
+
+# ---- the gradient buffer's version ----
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [40, 5000])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embedding_gradient_tells_autograd_of_its_write(ops, n, accumulate):
+    """A graph that saved the buffer before the call must not go on with what the call has put there."""
+    ids = torch.arange(n, device="cuda") % 30
+    grad = torch.ones(30, 16, device="cuda")
+    x = torch.ones(30, 16, device="cuda", requires_grad=True)
+    y = (x * grad).sum()
+    before = grad._version
+    ops.embedding_backward(torch.ones(n, 16, device="cuda"), ids, grad, accumulate=accumulate)
+    assert grad._version > before
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    before = grad._version
+    with pytest.raises(ValueError):
+        ops.embedding_backward(torch.ones(n, 8, device="cuda"), ids, grad)
+    assert grad._version == before  # a refused call has written nothing
+    with torch.inference_mode():
+        held = torch.ones(30, 16, device="cuda")
+    ops.embedding_backward(torch.ones(n, 16, device="cuda"), ids, held)  # an inference tensor has no version
