@@ -29,7 +29,8 @@ def _load():
     load_library()  # raises LibraryNotBuilt where nothing has been built
     path = _build.torch_ops_path()
     if not os.path.exists(path):
-        raise LibraryNotBuilt(f"{path} is missing: build it with muon_adamw_hybrid_grad_gb300.build.build()")
+        raise LibraryNotBuilt(f"{path} is missing: build it with muon_adamw_hybrid_grad_gb300.build.build()\n"
+                              f"{_build.torch_ops_problem()}".rstrip())
     loader = importlib.machinery.ExtensionFileLoader("_torch_ops", path)
     module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_torch_ops", path, loader=loader))
     loader.exec_module(module)
