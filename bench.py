@@ -55,13 +55,13 @@ STREAM_KINDS = ("grad_norm", "momentum", "adamw")
 # DRAM bytes per ns_tc_kernel launch (dram__bytes_read.sum + dram__bytes_write.sum) from one ncu
 # capture of a 3-layer case of the full_vla expert (expert:2048:8192:3:fp32_mixed: the same matrix
 # shapes and policy; the ns_tc_kernel summary in profiles/): the 15 launches of one step (5 X X^T,
-# 5 A A, 4 B X, 1 last) averaged, 726.1 MB, and scaled to the 24-layer expert by the matrices
+# 5 A A, 4 B X, 1 last) averaged, 726.8 MB, and scaled to the 24-layer expert by the matrices
 # processed (x 8: each launch reads its operands and writes its output once per matrix). It describes
 # only the kernel sources it was measured on: any change to them makes it null until it is measured
 # again.
-NS_TRAFFIC = {"sources_sha256": "bae68366bf9cb926aa40cb7ba7bd0546a19d20cf6a1af3d5352a60e3588fc515",
-              "bytes_per_launch": 5808463189, "workload": "full_vla"}
-NS_SOURCES = ("ns_tc.cu", "ns_epilogue.cuh", "internal.h")
+NS_TRAFFIC = {"sources_sha256": "c34db5b11c2aef8970d5f337d7d4b8388aac5fca851ef5406dea33b4c83ff6ac",
+              "bytes_per_launch": 5814285926, "workload": "full_vla"}
+NS_SOURCES = ("ns_tc.cu", "ns_epilogue.cuh", "internal.h", "tcgen05.cuh")
 
 
 def ns_traffic_per_launch(workload: str):

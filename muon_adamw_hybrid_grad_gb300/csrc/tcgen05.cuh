@@ -1,6 +1,6 @@
 // Inline PTX of the tensor-core kernels (sm_103a): mbarriers with bounded
 // waits, TMA copies, tcgen05 products, TMEM, and the descriptors they take.
-// Shared by ns_tc.cu and window_attention.cu.
+// Shared by ns_tc.cu, the attention kernels and qk_norm_rope.cu (waits and copies).
 #pragma once
 
 #include <cuda.h>
