@@ -16,6 +16,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <cstdint>
 #include <optional>
 
 #include "muon_adamw.h"
@@ -83,8 +84,11 @@ double real(PyObject* o) {
   return v;
 }
 
+// A number past 64 bits counts as the largest, or the smallest, of them.
 int64_t integer(PyObject* o) {
-  const long long v = PyLong_AsLongLong(o);
+  int over = 0;
+  const long long v = PyLong_AsLongLongAndOverflow(o, &over);
+  if (over) return over > 0 ? INT64_MAX : INT64_MIN;
   if (v == -1 && PyErr_Occurred()) throw Refused();
   return v;
 }

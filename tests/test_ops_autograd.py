@@ -227,3 +227,19 @@ def test_embedding_gradient_tells_autograd_of_its_write(ops, n, accumulate):
     with torch.inference_mode():
         held = torch.ones(30, 16, device="cuda")
     ops.embedding_backward(torch.ones(n, 16, device="cuda"), ids, held)  # an inference tensor has no version
+
+
+# ---- numbers past 64 bits ----
+
+@pytest.mark.gpu
+def test_window_past_64_bits_is_every_earlier_token(ops):
+    """And a count of sinks past them is refused like any other that is too large."""
+    from muon_adamw_hybrid_grad_gb300 import MuonAdamWError
+
+    q, k, v, do, cu = packed_case([90, 40], 2, 1, 64)
+    want = ops.window_attention(q, k, v, window=None, cu_seqlens=cu)
+    got = ops.window_attention(q, k, v, window=10 ** 30, cu_seqlens=cu)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for how in ({"window": -10 ** 30}, {"window": 1, "sinks": 10 ** 30}, {"window": 1, "sinks": -10 ** 30}):
+        with pytest.raises(MuonAdamWError):
+            ops.window_attention(q, k, v, **how)
