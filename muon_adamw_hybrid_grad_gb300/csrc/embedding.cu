@@ -229,9 +229,12 @@ __global__ void __launch_bounds__(kThreads) embedding_direct_kernel(const __grid
 // radix sort over the cluster's CTAs, digit totals exchanged through
 // distributed shared memory); every other CTA meanwhile fills the gradient
 // with zeros, which hides the sort behind the writes of a large vocabulary: 105 us
-// for 151936 x 2048 in bf16 (5.9 TB/s), the sort of 32749 ids among them. The sums
+// for 151936 x 2048 in bf16 (5.9 TB/s, where the one-launch form writes the same
+// zeros at 6.7; why has not been found), the sort of 32749 ids among them. The sums
 // then take 35 us and the joins 16. (Zeros shared out over all three launches, so
-// that the sums read beside them: 153 to 158 us in all, as against 156.)
+// that the sums read beside them: 153 to 158 us in all, as against 156.) With
+// accumulate there are no zeros and the sort stands alone: 89 us at 32749 tokens,
+// 33 at 4097; the one-launch form 36 at 4096, 20 at 777.
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortCluster = 8;

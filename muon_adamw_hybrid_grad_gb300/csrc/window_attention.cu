@@ -22,7 +22,8 @@
 //                   tokens of 16 heads of 128, window 1024);
 //   warp 11         clears the rows of a sample's last value tile that belong to
 //                   other samples, and stores the finished tiles.
-// TMEM: S0 | S1 | O0 | O1, 128 columns each.
+// TMEM: S0 | S1 | O0 | O1, 128 columns each (heads of up to 64 leave half of each O
+// idle).
 //
 // Finished tiles leave through two positions of the ring and TMA (see stage_row),
 // tiles with rows of other samples from the threads' registers.
@@ -32,11 +33,15 @@
 // the four products fill 2048 and a softmax takes 1950 (maximum 380, exponentials,
 // sum and rounding 1060, TMEM and barriers the rest); it is bound by issue, so that
 // exponentials as polynomials beside the special-function unit cost 12 to 20 %.
-// 16384 tokens of 16 heads of 128 over 8 key heads, all keys visible: 775 us, 1419
-// TFLOP/s (0.75 of the measured bf16 peak). Window 1024 and four sinks: 73 us for
+// 16384 tokens of 16 heads of 128 over 8 key heads, all keys visible: 772 us, 1425
+// TFLOP/s (0.76 of the measured bf16 peak). Window 1024 and four sinks: 73 us for
 // 8192 tokens; 139 us for 16360 in packed samples, 800 TFLOP/s counting visible
 // pairs, nine tiles being formed for eight tiles' worth of keys. 50 tokens of 16 heads
 // of 64: 6.3 us, the latency of one step and its set-up.
+//
+// Heads of other widths run at the next of 64 and 128, the columns past their own
+// zero: 8192 tokens of 16 heads over 8 with window 1024 and four sinks take 65 us of
+// 32 or 64, 72 to 74 of 72, 80, 96 or 128.
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since it
 // was last taken as m: P then stays below 2^8 and sums in fp32 lose nothing.
@@ -550,9 +555,11 @@ bool attn_map(CUtensorMap* tm, const void* base, int dim, int64_t tokens, int64_
 cudaError_t attn_forward(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                          const CUtensorMap& o, __nv_bfloat16* out, float* lse, int* err, int sms, cudaStream_t st) {
   // Items that differ go longest first, to and fro: where the window is more than an eighth of all tokens (all keys of
-  // 16384 visible: 772 us, in plain order 865; of 8192 211 and 249). Below they are alike, and in plain order only the
+  // 16384 visible: 772 us, in plain order 865; of 8192 208 and 249). Below they are alike, and in plain order only the
   // last keys of a tile have not been read before (window 1024 of 16384: 134 us, the other way 138; 16360 tokens in
-  // eight samples 136 and 143).
+  // eight samples 136 and 143). The samples' own lengths, which set how much the items differ, are not known here.
+  // Beside the bound little hangs on it: windows of 2047 in plain order and 2049 to and fro take 223 and 219 us of one
+  // sample of 16384 tokens, 145 and 147 of eight of 2048.
   const bool fro = (int64_t)a.window * 8 > a.n;
   if (a.dim > 64)
     return fro ? run_forward<128, true>(a, q, k, v, o, out, lse, err, sms, st)

@@ -21,7 +21,12 @@
 // next queries waits for dV, which waits for P^T in its place, a dQ step 2130 for 1536;
 // edge tiles, the sinks' own steps and the ends of items are the rest. Six samples of 7
 // to 1021 tokens (16 heads of 64, window 256): 52 us, bound by the latency of items of
-// three steps.
+// three steps: a CTA has about 16 steps in all, of some 5000 cycles each for 1000 of
+// products, since the ends of its items do not overlap (dq_part has one buffer each
+// for Q and dO and one accumulator, for heads of up to 64 too).
+//
+// Heads of other widths run at the next of 64 and 128: 8192 tokens of 16 heads over 8,
+// window 1024, four sinks, take 158 us of 32, 163 of 64, 201 to 210 of 72 to 128.
 //
 // The sink keys are seen by every query of a sample. Their gradients are cut
 // into chunks of kSinkChunk query tiles, each a work item of its own; the CTA that
@@ -468,7 +473,8 @@ __device__ __forceinline__ void dq_part(const AttnArgs& a, const CUtensorMap& tm
 // dP^T, each block in the first 16 of its own 32 columns. While the threads form P^T
 // of a step the tensor core runs the step before's dK and this one's dP^T; while
 // they form dS^T it runs dV and the next step's S^T (with two buffers S^T is formed a
-// step earlier: 8192 tokens of 16 heads of 64 take 162 us, of 72 208).
+// step earlier: 8192 tokens of 16 heads of 64 over 8, window 1024, four sinks, take
+// 163 us, of 72 209).
 //
 // First query tile that only the sinks reach in tile 0.
 __device__ __forceinline__ int first_sink_tile(const AttnArgs& a) {

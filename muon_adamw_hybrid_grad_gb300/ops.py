@@ -8,7 +8,12 @@ stream, on which the work is queued; nothing here waits for the GPU.
 
 ``embedding``, ``qk_norm_rope`` and ``window_attention`` each have a
 ``_backward`` function, and an ``_autograd`` form that torch's autograd
-differentiates with it. Refused arguments raise TypeError or ValueError, or
+differentiates with it, once: a second derivative raises. The plain forms
+record no graph, whatever their arguments require: a result that a loss is to
+reach the parameters through comes from an ``_autograd`` form. Queries, keys,
+values, weights and tables start every row on a 16-byte boundary and are
+refused otherwise (MA_ERR_ALIGN); gradients and saved outputs may lie in any
+layout, at the price of a copy where the kernels cannot read it. Refused arguments raise TypeError or ValueError, or
 MuonAdamWError with the library's status.
 """
 from __future__ import annotations
@@ -43,6 +48,7 @@ _ext = _load()
 
 def embedding(weight, ids, *, scale: float = 1.0, dtype: Optional[torch.dtype] = None):
     """scale * weight[ids], a row of zeros where an id is outside the vocabulary.
+    Records no graph, as no plain form does.
 
     weight: [vocab, width] fp32 or bf16, rows may be strided; ids: any shape,
     int32 or int64; dtype: the result's (the weight's by default)."""
@@ -60,7 +66,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, *, eps: float = 
     """RMS norm of every head of q and k, then the rotation by the token's
     position. q, k: [token, head, head_dim] fp32 or bf16 (e.g. slices of one
     projection's output); weights and the tables [position, rotated pairs]
-    fp32; positions int32 or int64. Returns contiguous (q_out, k_out)."""
+    fp32; positions int32 or int64. Returns contiguous (q_out, k_out), which
+    carry no graph."""
     return _ext.qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, neighbours)
 
 
@@ -78,7 +85,7 @@ def window_attention(q, k, v, *, window: Optional[int], sinks: int = 0, scale: O
     `sinks` keys. q: [token, head, head_dim] bf16; k, v: [token, kv head,
     head_dim]; cu_seqlens: int32 bounds of the samples on the GPU (None: one
     sample); scale: 1 / sqrt(head_dim) by default. Returns (out, lse): out like
-    q, lse [head, token] fp32."""
+    q, lse [head, token] fp32; they carry no graph."""
     return _ext.window_attention(q, k, v, window, sinks, scale, cu_seqlens)
 
 
