@@ -584,6 +584,140 @@ MA_API ma_status muon_adamw_window_attention_backward(const ma_window_attention*
                                                       const void* out, const float* lse, void* dq, void* dk, void* dv,
                                                       void* workspace, int64_t workspace_bytes, void* cuda_stream);
 
+/* Dropout whose mask is never stored. out[i] = x[i] / (1 - p) where element i
+ * is kept, 0 where it is dropped (whatever x[i] holds), and p is first rounded
+ * to a multiple of 2^-16. The gradient is the same call on the output's
+ * gradient, with the same p, rng and site.
+ * Element i is kept where its 16 random bits are at least p 2^16. They come
+ * from Philox4x32-10 with the key `seed` (low word first) and the counter
+ * (i / 8, site, low and high word of `step`); of the four result words w,
+ * element i of a group of eight has the low half of w[i / 2] for even i, the
+ * high half for odd i.
+ *   x, out  n contiguous elements of dtype MA_DT_F32 or MA_DT_BF16, n in [0, 2^35];
+ *   rng     device, two int64 values: seed and step. They are read when the
+ *           work runs, so that a captured call takes the step of each replay;
+ *   site    which of a step's calls this is, >= 0.
+ * Errors: MA_ERR_ARG, MA_ERR_SHAPE, MA_ERR_DTYPE, MA_ERR_ALIGN, MA_ERR_CUDA. */
+#define MA_DROPOUT_MAX_ELEMENTS (1ll << 35)
+MA_API ma_status muon_adamw_dropout(const void* x, int dtype, int64_t n, double p, const int64_t* rng, int32_t site,
+                                    void* out, void* cuda_stream);
+
+/* The residual's addition with RMS norm, over rows of `width` elements:
+ *   r = residual + dropout(x),   y = weight * r / sqrt(mean(r^2) + eps),
+ * with the dropout of muon_adamw_dropout over the n_tokens * width elements
+ * (p 0: none, rng is not read).
+ *   dtype         of x, y and their gradients;
+ *   stream_dtype  of residual, res and their gradients: dtype, or MA_DT_F32;
+ *   width         1 .. 32768;
+ *   residual      NULL: r is dropout(x) alone;
+ *   weight        fp32, `width` values.
+ * The norm is of r before r is rounded for the stream. Rows of inputs may be
+ * strided, outputs are contiguous. 16-byte accesses are used where width is a
+ * multiple of 8 and all rows start on 16-byte boundaries, single elements
+ * otherwise. */
+typedef struct {
+  int64_t n_tokens, width;
+  int32_t dtype, stream_dtype;
+  double eps, p;
+  const int64_t* rng;
+  int32_t site, reserved;
+} ma_residual_norm;
+
+/* res (NULL allowed): r in the stream's type. scales NULL: y in `dtype`.
+ * Otherwise y is e4m3, one byte an element, and scales[t] = max |y[t]| / 448:
+ * y[t] stands for scales[t] times the stored values (a row of zeros has scale
+ * 0). Errors: MA_ERR_ARG, MA_ERR_SHAPE, MA_ERR_DTYPE, MA_ERR_ALIGN, MA_ERR_CUDA. */
+MA_API ma_status muon_adamw_residual_norm(const ma_residual_norm* d, const void* x, int64_t x_stride,
+                                          const void* residual, int64_t residual_stride, const float* weight, void* y,
+                                          float* scales, void* res, void* cuda_stream);
+
+/* Its gradient, from the gradients of y (dy) and of res (dres, NULL for none)
+ * and from res as the forward call stored it: dresidual, dx = dropout(dresidual)
+ * and dweight (fp32, summed over the rows). dx may be NULL where it is
+ * dresidual: no dropout and one type. */
+MA_API ma_status muon_adamw_residual_norm_backward_workspace(const ma_residual_norm* d, int64_t* bytes);
+MA_API ma_status muon_adamw_residual_norm_backward(const ma_residual_norm* d, const void* dy, int64_t dy_stride,
+                                                   const void* dres, int64_t dres_stride, const void* res,
+                                                   int64_t res_stride, const float* weight, void* dx, void* dresidual,
+                                                   float* dweight, void* workspace, int64_t workspace_bytes,
+                                                   void* cuda_stream);
+
+/* Products grouped by expert: out[t] = weight[e] x[t] for the tokens t of
+ * expert e, offsets[e] to offsets[e + 1] - 1.
+ *   n_experts  1 .. 1024; inner (x's width) and outer (out's) multiples of 8 in
+ *              [8, 2^20]; n_tokens in [0, 2^30]; all tensors bf16, sums fp32;
+ *   offsets    device, n_experts + 1 int32 values, ascending from 0 and at most
+ *              n_tokens. Whatever they hold, no access leaves the tensors:
+ *              the first counts as 0, each other one as at least the one before
+ *              it and at most n_tokens;
+ *   x          rows of `inner` elements, x_stride apart;
+ *   weight     [expert][outer][inner], rows weight_row_stride and matrices
+ *              weight_expert_stride apart.
+ * Bases are 16-byte aligned and strides multiples of 8 elements. Tokens behind
+ * the last expert's get rows of zeros. A token's result depends on no other
+ * token and on no other expert. */
+typedef struct {
+  int64_t n_tokens;
+  int32_t n_experts, inner, outer, reserved;
+  const int32_t* offsets;
+  const void* x;
+  int64_t x_stride;
+  const void* weight;
+  int64_t weight_row_stride, weight_expert_stride;
+} ma_expert_matmul;
+
+/* out: contiguous [token][outer] bf16. Errors: MA_ERR_ARG, MA_ERR_SHAPE,
+ * MA_ERR_DTYPE, MA_ERR_ALIGN, MA_ERR_CUDA. */
+MA_API ma_status muon_adamw_expert_matmul(const ma_expert_matmul* d, void* out, void* cuda_stream);
+
+/* Its gradients. dout: rows of `outer` elements, dout_stride apart.
+ *   dx       contiguous [token][inner] bf16: weight[e]^T dout[t]; rows of zeros
+ *            behind the last expert's tokens; NULL: not formed;
+ *   dweight  contiguous [expert][outer][inner], MA_DT_BF16 or MA_DT_F32: the sum
+ *            over the expert's tokens of dout[t] x[t]^T, zero for an expert
+ *            without tokens; NULL: not formed. accumulate = 1: added to what it
+ *            holds. */
+MA_API ma_status muon_adamw_expert_matmul_backward(const ma_expert_matmul* d, const void* dout, int64_t dout_stride,
+                                                   void* dx, void* dweight, int grad_dtype, int accumulate,
+                                                   void* cuda_stream);
+
+/* Log probabilities of given tokens. With z = scale * logits[t]:
+ *   lse = log(sum_v exp(z_v)),  logprobs = z_ids - lse,
+ *   entropy = lse - sum_v p_v z_v,  p_v = exp(z_v - lse),
+ * and the `top` largest logits with their log probabilities, in descending
+ * order, the lowest index first among equal ones.
+ *   vocab    1 .. 2^20; n_tokens in [0, 2^30]; rows of dtype MA_DT_F32 or
+ *            MA_DT_BF16, `stride` apart, 16-byte accesses wherever a row allows;
+ *   ids      int32 (id_bytes 4) or int64 (id_bytes 8); a token outside [0, vocab)
+ *            has log probability 0 and no gradient from it;
+ *   scale    positive (an inverse temperature);
+ *   top      0 .. 32, at most vocab.
+ * A logit of -infinity has probability 0 and adds nothing. A row without any
+ * other has lse -infinity, log probabilities -infinity (0 for a token outside),
+ * entropy 0 and no gradient. Rows that hold a NaN or +infinity have results
+ * that are NaN, and indices in range. */
+typedef struct {
+  int64_t n_tokens, vocab, stride;
+  int32_t dtype, id_bytes;
+  double scale;
+  const void* logits;
+  const void* ids;
+} ma_token_logprobs;
+
+/* logprobs, entropy, lse: n_tokens fp32 values; top_logprobs [token][top] fp32
+ * and top_ids [token][top] int64, not read with top = 0. Errors: MA_ERR_ARG,
+ * MA_ERR_SHAPE, MA_ERR_DTYPE, MA_ERR_ALIGN, MA_ERR_CUDA. */
+MA_API ma_status muon_adamw_token_logprobs(const ma_token_logprobs* d, int32_t top, float* logprobs, float* entropy,
+                                           float* lse, float* top_logprobs, int64_t* top_ids, void* cuda_stream);
+
+/* Gradient of sum_t dlogprobs[t] logprobs[t] + dentropy[t] entropy[t] with
+ * respect to the logits (either may be NULL for none), from the forward call's
+ * inputs and its entropy and lse: dlogits, rows dlogits_stride apart, in the
+ * logits' type. */
+MA_API ma_status muon_adamw_token_logprobs_backward(const ma_token_logprobs* d, const float* dlogprobs,
+                                                    const float* dentropy, const float* entropy, const float* lse,
+                                                    void* dlogits, int64_t dlogits_stride, void* cuda_stream);
+
 /* Wait for cuda_stream and read the operators' error word.
  * MA_ERR_DEVICE_CHECK if a bounded in-kernel wait of an earlier call on this
  * device ran out (the word is then cleared); MA_ERR_CUDA. */

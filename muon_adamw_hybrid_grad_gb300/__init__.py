@@ -141,6 +141,52 @@ class QkNormRope(ctypes.Structure):
     ]
 
 
+class ResidualNorm(ctypes.Structure):
+    """ma_residual_norm: the residual's addition with RMS norm."""
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64),
+        ("width", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("stream_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_double),
+        ("p", ctypes.c_double),
+        ("rng", ctypes.c_void_p),
+        ("site", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class ExpertMatmul(ctypes.Structure):
+    """ma_expert_matmul: products grouped by expert."""
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64),
+        ("n_experts", ctypes.c_int32),
+        ("inner", ctypes.c_int32),
+        ("outer", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("offsets", ctypes.c_void_p),
+        ("x", ctypes.c_void_p),
+        ("x_stride", ctypes.c_int64),
+        ("weight", ctypes.c_void_p),
+        ("weight_row_stride", ctypes.c_int64),
+        ("weight_expert_stride", ctypes.c_int64),
+    ]
+
+
+class TokenLogprobs(ctypes.Structure):
+    """ma_token_logprobs: log probabilities of given tokens."""
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64),
+        ("vocab", ctypes.c_int64),
+        ("stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("id_bytes", ctypes.c_int32),
+        ("scale", ctypes.c_double),
+        ("logits", ctypes.c_void_p),
+        ("ids", ctypes.c_void_p),
+    ]
+
+
 class WindowAttention(ctypes.Structure):
     """ma_window_attention: causal attention with a window and sinks."""
     _fields_ = [
@@ -243,6 +289,22 @@ _SIGNATURES = {
     "muon_adamw_window_attention_backward": (ctypes.c_int, [ctypes.POINTER(WindowAttention), _P, ctypes.c_int64,
                                                             ctypes.c_int64, _P, _P, _P, _P, _P, _P, ctypes.c_int64,
                                                             _P]),
+    "muon_adamw_dropout": (ctypes.c_int, [_P, ctypes.c_int, ctypes.c_int64, ctypes.c_double, _P, ctypes.c_int32, _P,
+                                          _P]),
+    "muon_adamw_residual_norm": (ctypes.c_int, [ctypes.POINTER(ResidualNorm), _P, ctypes.c_int64, _P, ctypes.c_int64,
+                                                _P, _P, _P, _P, _P]),
+    "muon_adamw_residual_norm_backward_workspace": (ctypes.c_int, [ctypes.POINTER(ResidualNorm),
+                                                                   ctypes.POINTER(ctypes.c_int64)]),
+    "muon_adamw_residual_norm_backward": (ctypes.c_int, [ctypes.POINTER(ResidualNorm), _P, ctypes.c_int64, _P,
+                                                         ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _P, _P, _P,
+                                                         ctypes.c_int64, _P]),
+    "muon_adamw_expert_matmul": (ctypes.c_int, [ctypes.POINTER(ExpertMatmul), _P, _P]),
+    "muon_adamw_expert_matmul_backward": (ctypes.c_int, [ctypes.POINTER(ExpertMatmul), _P, ctypes.c_int64, _P, _P,
+                                                         ctypes.c_int, ctypes.c_int, _P]),
+    "muon_adamw_token_logprobs": (ctypes.c_int, [ctypes.POINTER(TokenLogprobs), ctypes.c_int32, _P, _P, _P, _P, _P,
+                                                 _P]),
+    "muon_adamw_token_logprobs_backward": (ctypes.c_int, [ctypes.POINTER(TokenLogprobs), _P, _P, _P, _P, _P,
+                                                          ctypes.c_int64, _P]),
     "muon_adamw_operators_check": (ctypes.c_int, [_P]),
     "muon_adamw_last_error": (ctypes.c_char_p, []),
     "muon_adamw_version": (ctypes.c_char_p, []),

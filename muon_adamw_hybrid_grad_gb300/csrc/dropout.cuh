@@ -1,0 +1,63 @@
+// Which elements dropout keeps, recomputed wherever it is asked for.
+//
+// Sixteen bits for each element from Philox4x32-10 (Salmon, Moraes, Dror and
+// Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011): the key is the
+// 64-bit seed, the counter the element's group of eight, the call's site and
+// the 64-bit step. A call of the generator gives a group's 128 bits: word i / 2
+// of the result has element i in its low half where i is even. An element is
+// kept where its bits are at least `threshold`, p in units of 2^-16. Sixteen
+// bits instead of 32 halve the integer work, which would otherwise take as long
+// as the memory does.
+#pragma once
+
+#include <stdint.h>
+
+namespace ma {
+
+struct DropArgs {
+  const int64_t* rng;  // seed, step
+  uint32_t site, threshold;
+  float factor;  // 1 / (1 - p), 0 where nothing is kept
+};
+
+namespace {
+
+struct DropKey {
+  uint32_t k0, k1, site, step0, step1, threshold;
+  float factor;
+};
+
+__device__ __forceinline__ DropKey drop_key(const DropArgs& a) {
+  const uint64_t seed = (uint64_t)__ldg(a.rng), step = (uint64_t)__ldg(a.rng + 1);
+  return {(uint32_t)seed, (uint32_t)(seed >> 32), a.site,  (uint32_t)step,
+          (uint32_t)(step >> 32), a.threshold, a.factor};
+}
+
+__device__ __forceinline__ uint4 philox(uint4 c, uint32_t k0, uint32_t k1) {
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t a = (uint64_t)c.x * 0xD2511F53u, b = (uint64_t)c.z * 0xCD9E8D57u;
+    c = make_uint4((uint32_t)(b >> 32) ^ c.y ^ k0, (uint32_t)b, (uint32_t)(a >> 32) ^ c.w ^ k1, (uint32_t)a);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return c;
+}
+
+// The eight elements of group `group`. Dropped ones become 0 whatever they hold.
+__device__ __forceinline__ void drop8(const DropKey& k, uint32_t group, float (&x)[8]) {
+  const uint4 r = philox(make_uint4(group, k.site, k.step0, k.step1), k.k0, k.k1);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = (w[i] & 0xFFFFu) >= k.threshold ? x[2 * i] * k.factor : 0.f;
+    x[2 * i + 1] = (w[i] >> 16) >= k.threshold ? x[2 * i + 1] * k.factor : 0.f;
+  }
+}
+
+}  // namespace
+
+// Of a probability and where the generator stands; false if p is outside [0, 1].
+bool drop_args(double p, const int64_t* rng, int32_t site, DropArgs* out);
+
+}  // namespace ma

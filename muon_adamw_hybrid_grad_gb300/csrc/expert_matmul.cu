@@ -1,0 +1,714 @@
+// Products grouped by expert on the 5th-generation tensor cores (sm_103a).
+//
+//   forward   out[t]  = W_e x[t]              D[outer, token] = W[outer, inner]  x^T
+//   input     dx[t]   = W_e^T dout[t]         D[inner, token] = W^T[inner, outer] dout^T
+//   weights   dW_e    = sum_t dout[t] x[t]^T  D[outer, inner] = dout^T x
+//
+// In the first two the tokens are the products' N side and the weights their M
+// side: N goes in steps of 32, so that an expert's last tokens, or its only few,
+// cost what they are, where the M side would round them up to 256. Weights are
+// read as they lie (K-major forward, MN-major for dx), nothing is transposed in
+// memory. The third sums over an expert's tokens: its last block of 64 reaches
+// into the next expert, and a warp of its own clears those rows before the
+// product, so that whatever they hold meets no product.
+//
+// Persistent pairs of CTAs (a cluster of two) run tcgen05.mma.cta_group::2 with
+// M = 256, N <= 256: each CTA loads its own 128 rows of the left operand and its
+// half of the right one, 32 KB a block of 64, which is what the L2 delivers to
+// an SM in the 512 cycles of the block's products; with a CTA for itself it
+// would be 48 KB.
+//   warp 0     TMA loads into a ring of six stages (five with fp32 gradients)
+//   warp 1     products, issued by the even CTA; two accumulators of 256 columns
+//   warps 2-9  results from TMEM: rounded, transposed where tokens are columns,
+//              out through shared memory and TMA; tiles with other experts'
+//              tokens by plain stores of the rows that are theirs
+//   warp 10    clears the rows behind an expert's tokens (third product)
+// Which unit belongs to whom follows from the offsets, which only the device
+// knows: every CTA adds them up for itself first.
+//
+// Every wait is bounded; where one runs out the error word is set, copies and
+// products in flight end, and TMEM is freed.
+#include <math.h>
+
+#include <algorithm>
+
+#include "op_common.cuh"
+#include "tcgen05.cuh"
+
+namespace ma {
+namespace {
+
+constexpr int kTile = 256;       // M of a pair, and the most N
+constexpr int kHalf = kTile / 2;
+constexpr int kBlock = 64;       // of the contraction
+constexpr int kSmallBox = 16;    // rows of the copies of a token tile below 256
+constexpr int kOperand = kHalf * kBlock * 2;  // 16 KB: a CTA's part of one operand in a stage
+constexpr int kStage = 2 * kOperand;
+constexpr int kPanel = kBlock * 64 * 2;  // MN-major: 64 columns of a block's 64 rows
+constexpr int kWarps = 11;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStoreWarps = 8;
+constexpr int kMaxExperts = 1024;
+constexpr int kRaster = 8;  // token (or inner) tiles that walk together along the features
+constexpr uint32_t kTmemColumns = 512;
+
+enum Mode { kForward, kInput, kWeights };
+
+// error codes of the waits that ran out
+constexpr int kErrLoad = 0x501, kErrProduct = 0x502, kErrStore = 0x503, kErrClear = 0x504;
+
+struct ExpertArgs {
+  CUtensorMap a, b, b_small, out;
+  const int32_t* offsets;
+  int tokens, experts;
+  int m, n, k;  // forward: outer, -, inner; input: inner, -, outer; weights: outer, inner, -
+  void* dst;
+  int accumulate;
+  int* err;
+};
+
+template <bool F32>
+struct Layout {
+  static constexpr int kStages = F32 ? 5 : 6;
+  static constexpr int kBlockBytes = 32 * 32 * (F32 ? 4 : 2);
+  static constexpr int kStore = kStages * kStage;
+  static constexpr int kTable = kStore + kStoreWarps * kBlockBytes;
+  static constexpr int kBars = kTable + (2 * kMaxExperts + 8) * 4;
+  // full, empty, tail, fixed [stage]; accumulator full, free [2]; drain
+  static constexpr int kNumBars = 4 * kStages + 5;
+  static constexpr int kBytes = 1024 + kBars + kNumBars * 8 + 16;
+  static_assert(kBytes <= 232448, "shared memory of a CTA");
+};
+
+__device__ __forceinline__ void umma_pair_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The products issued so far have ended: one arrival in each CTA of the pair.
+__device__ __forceinline__ void commit_pair_warp(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}\n" ::"r"(bar),
+      "r"(mapa_shared(bar, 1))
+      : "memory");
+}
+__device__ __forceinline__ void commit_own_warp(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar)
+      : "memory");
+}
+// A wait whose outcome is the whole warp's, on a barrier at which the other CTA arrives too.
+__device__ __forceinline__ bool mbar_wait_warp_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                                       int* err, int code) {
+  if (__all_sync(0xffffffffu, mbar_try_wait<true>(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait_loop<true>(bar, parity, abort_flag, err, code));
+}
+// A copy into this CTA that counts on barrier `bar` of the pair's even CTA.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* tm, int x, int y, int z,
+                                                 uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// What a pair works on: rows m0 to m0 + 255 of D and `n` of its columns.
+struct Unit {
+  int expert, m0, n0, n;
+  int at, count;  // the unit's tokens
+  int blocks;     // of the contraction; 0: zeros
+};
+
+struct Table {
+  const int* bound;  // expert e's tokens are bound[e] to bound[e + 1]; e = experts: those behind the last
+  const int* first;  // its units (weights: unused)
+  int units;
+};
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Units come in ascending order, so the expert is looked for from the last one on.
+template <int MODE>
+__device__ __forceinline__ Unit unit_at(const ExpertArgs& a, const Table& tab, int pos, int& expert) {
+  Unit u;
+  const int mt = ceil_div(a.m, kTile);
+  if constexpr (MODE == kWeights) {
+    const int nt = ceil_div(a.n, kTile), local = pos % (mt * nt);
+    u.expert = pos / (mt * nt);
+    const int group = local / (kRaster * mt), width = min(kRaster, nt - group * kRaster);
+    const int r = local - group * kRaster * mt;
+    u.m0 = r / width * kTile;
+    u.n0 = (group * kRaster + r % width) * kTile;
+    u.n = a.n - u.n0 > kHalf ? kTile : kHalf;
+    u.at = tab.bound[u.expert];
+    u.count = tab.bound[u.expert + 1] - u.at;
+    u.blocks = ceil_div(u.count, kBlock);
+  } else {
+    while (pos >= tab.first[expert + 1]) ++expert;
+    const int begin = tab.bound[expert], count = tab.bound[expert + 1] - begin;
+    const int tt = ceil_div(count, kTile), local = pos - tab.first[expert];
+    const int group = local / (kRaster * mt), width = min(kRaster, tt - group * kRaster);
+    const int r = local - group * kRaster * mt;
+    // token tiles of one size; the last is never empty, since count > 256 (tt - 1)
+    const int per = (ceil_div(count, tt) + 31) & ~31, tile = group * kRaster + r % width;
+    u.expert = expert;
+    u.m0 = r / width * kTile;
+    u.n0 = 0;
+    u.at = begin + tile * per;
+    u.count = min(per, count - tile * per);
+    u.n = (u.count + 31) & ~31;
+    u.blocks = expert < a.experts ? ceil_div(a.k, kBlock) : 0;
+  }
+  return u;
+}
+
+// Bytes that land in a CTA for one block.
+template <int MODE>
+__device__ __forceinline__ uint32_t stage_bytes(const Unit& u) {
+  return (uint32_t)(kOperand + (MODE == kWeights ? u.n / 2 / 64 * kPanel : u.n / 2 * kBlock * 2));
+}
+
+template <int MODE, typename LOAD>
+__device__ __forceinline__ void load_block(const ExpertArgs& a, const Unit& u, int block, uint32_t stage, uint32_t rank,
+                                           LOAD load) {
+  const int k0 = block * kBlock, m0 = u.m0 + (int)rank * kHalf;
+  const uint32_t sb = stage + kOperand;
+  if constexpr (MODE == kForward) {
+    load(stage, &a.a, k0, m0, u.expert);
+  } else {
+    for (int p = 0; p < kHalf / 64; ++p)
+      load(stage + p * kPanel, &a.a, m0 + p * 64, MODE == kInput ? k0 : u.at + k0, MODE == kInput ? u.expert : 0);
+  }
+  if constexpr (MODE == kWeights) {
+    const int n0 = u.n0 + (int)rank * (u.n / 2);
+    for (int p = 0; p < u.n / 2 / 64; ++p) load(sb + p * kPanel, &a.b, n0 + p * 64, u.at + k0, 0);
+  } else {
+    const int t0 = u.at + (int)rank * (u.n / 2);
+    if (u.n == kTile) {
+      load(sb, &a.b, k0, t0, 0);
+    } else {
+      for (int p = 0; p < u.n / 2; p += kSmallBox) load(sb + p * kBlock * 2, &a.b_small, k0, t0 + p, 0);
+    }
+  }
+}
+
+// 32 rows of D by 32 columns, D's rows the lanes: tokens are columns, so the
+// block leaves transposed, a row of 32 features for each token.
+__device__ __forceinline__ void store_tokens(const ExpertArgs& a, const Unit& u, int row0, int c0,
+                                             const uint32_t (&r)[32], uint8_t* tile, int lane) {
+  if (lane == 0) bulk_wait_read_all();  // the last block's store has read the tile
+  __syncwarp();
+  // rows of 64 bytes, 16-byte chunk q of row t at q ^ (t / 2 % 4): lanes 2 k and 2 k + 1 swap, the even one writes
+  // the pair's even tokens, the odd one its odd ones
+  uint8_t* const to = tile + (lane & 1) * 64 + ((lane >> 1) & 3) * 4;
+  const uint32_t sel = (lane & 1) ? 0x3276u : 0x5410u;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const uint32_t mine = op_pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+    *reinterpret_cast<uint32_t*>(to + 2 * j * 64 + (((lane >> 3) ^ (j & 3)) << 4)) = __byte_perm(mine, other, sel);
+  }
+  if (c0 + 32 <= u.count) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(&a.out, smem_u32(tile), row0, u.at + c0);
+      bulk_commit();
+    }
+    return;
+  }
+  __syncwarp();
+  const int q = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = i * 8 + (lane >> 2);
+    if (c0 + t < u.count && row0 + q * 8 < a.m)
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dst) + (int64_t)(u.at + c0 + t) * a.m + row0 + q * 8) =
+          *reinterpret_cast<const uint4*>(tile + t * 64 + ((q ^ ((t >> 1) & 3)) << 4));
+  }
+  __syncwarp();
+}
+
+// 32 rows of an expert's gradient by 32 columns, a row to a lane.
+template <bool F32>
+__device__ __forceinline__ void store_weights(const ExpertArgs& a, const Unit& u, int row0, int col0,
+                                              const uint32_t (&r)[32], uint8_t* tile, int lane) {
+  float v[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
+  if (a.accumulate && row0 + lane < a.m) {
+    const int64_t at = ((int64_t)u.expert * a.m + row0 + lane) * a.n + col0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (col0 + q * 8 >= a.n) break;
+      float old[8];
+      if constexpr (F32)
+        load8(static_cast<const float*>(a.dst) + at + q * 8, old);
+      else
+        load8(static_cast<const __nv_bfloat16*>(a.dst) + at + q * 8, old);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[q * 8 + e] += old[e];
+    }
+  }
+  if (lane == 0) bulk_wait_read_all();
+  __syncwarp();
+  if constexpr (F32) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      *reinterpret_cast<float4*>(tile + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+          make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<uint4*>(tile + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+          make_uint4(op_pack_bf16(v[8 * q], v[8 * q + 1]), op_pack_bf16(v[8 * q + 2], v[8 * q + 3]),
+                     op_pack_bf16(v[8 * q + 4], v[8 * q + 5]), op_pack_bf16(v[8 * q + 6], v[8 * q + 7]));
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_3d(&a.out, smem_u32(tile), col0, row0, u.expert);
+    bulk_commit();
+  }
+}
+
+template <int MODE, bool F32>
+__global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid_constant__ ExpertArgs a) {
+  using L = Layout<F32>;
+  constexpr int S = L::kStages;
+  extern __shared__ uint8_t raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  int* const bound = reinterpret_cast<int*>(smem + L::kTable);
+  int* const first = bound + kMaxExperts + 4;
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(bars + L::kNumBars);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * S, tail = empty + 8 * S, fixed = tail + 8 * S;
+  const uint32_t acc_full = fixed + 8 * S, acc_free = acc_full + 16, drain = acc_free + 16;
+  const uint32_t rank = cluster_ctarank();
+  const int step = gridDim.x / 2, pos0 = blockIdx.x / 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, 1);
+      mbar_init(tail + 8 * s, 1);
+      mbar_init(fixed + 8 * s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(acc_full + 8 * i, 1);
+      mbar_init(acc_free + 8 * i, 2 * kStoreWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) tmem_alloc<2>(smem_u32(tmem_slot), kTmemColumns);
+  pdl_wait();
+  pdl_launch();
+  if (warp == 0) {
+    // the experts' bounds, kept in order and in range whatever the offsets hold, and their units
+    int before = 0, units = 0;
+    const int mt = ceil_div(a.m, kTile);
+    if (lane == 0) bound[0] = first[0] = 0;
+    for (int e0 = 0; e0 <= a.experts; e0 += 32) {
+      const int e = e0 + lane;  // bound[e + 1]; the last one is where the tokens end
+      int b = e < a.experts ? min(max(a.offsets[e + 1], 0), a.tokens) : a.tokens;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, b, d);
+        if (lane >= d) b = max(b, o);
+      }
+      b = max(b, before);
+      int begin = __shfl_up_sync(0xffffffffu, b, 1);
+      if (lane == 0) begin = before;
+      before = __shfl_sync(0xffffffffu, b, 31);
+      int n = ceil_div(b - begin, kTile) * mt;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, n, d);
+        if (lane >= d) n += o;
+      }
+      n += units;
+      units = __shfl_sync(0xffffffffu, n, 31);
+      if (e <= a.experts) {
+        bound[e + 1] = b;
+        first[e + 1] = n;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the other CTA's barriers are there before a copy or a commit reaches them
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Table tab{bound, first,
+                  MODE == kWeights ? a.experts * ceil_div(a.m, kTile) * ceil_div(a.n, kTile) : first[a.experts + 1]};
+  int expert = 0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- loads ----
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int pos = pos0; pos < tab.units && ok; pos += step) {
+        const Unit u = unit_at<MODE>(a, tab, pos, expert);
+        const uint32_t bytes = stage_bytes<MODE>(u);
+        for (int b = 0; b < u.blocks; ++b) {
+          if (!mbar_wait(empty + 8 * stage, phase ^ 1u, abort_flag, a.err, kErrLoad)) {
+            ok = false;
+            break;
+          }
+          const uint32_t at = smem_u32(smem) + (uint32_t)(stage * kStage), bar = full + 8 * stage;
+          if (MODE == kWeights && b == u.blocks - 1 && u.count % kBlock != 0) {
+            // rows of the next expert in it: lands on a barrier of this CTA's, and is cleared before it is full
+            mbar_expect_tx(tail + 8 * stage, bytes);
+            load_block<MODE>(a, u, b, at, rank, [&](uint32_t dst, const CUtensorMap* tm, int x, int y, int z) {
+              tma_load_3d(dst, tm, x, y, z, tail + 8 * stage);
+            });
+          } else if (rank == 0) {
+            mbar_expect_tx(bar, 2 * bytes);
+            load_block<MODE>(a, u, b, at, rank, [&](uint32_t dst, const CUtensorMap* tm, int x, int y, int z) {
+              tma_load_3d(dst, tm, x, y, z, bar);
+            });
+          } else {
+            load_block<MODE>(a, u, b, at, rank, [&](uint32_t dst, const CUtensorMap* tm, int x, int y, int z) {
+              tma_load_3d_pair(dst, tm, x, y, z, mapa_shared(bar, 0));
+            });
+          }
+          ++issued;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // copies in flight land before the CTA leaves: those of the odd CTA count on the even one's barriers
+      if (rank == 0) {
+        for (int i = 0; i < min(issued, S); ++i) {
+          if (--stage < 0) {
+            stage = S - 1;
+            phase ^= 1u;
+          }
+          drain_wait(full + 8 * stage, phase);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      // ---- products ----
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      const uint32_t s0 = smem_u32(smem);
+      // MN-major: panels of 64 columns, sixteen rows of the contraction 2 KB further
+      const uint64_t a0 = MODE == kForward ? sdesc(s0, 16, 1024) : sdesc(s0, kPanel, 1024);
+      const uint64_t b0 = MODE == kWeights ? sdesc(s0 + kOperand, kPanel, 1024) : sdesc(s0 + kOperand, 16, 1024);
+      constexpr uint32_t kStepA = MODE == kForward ? 2 : 128, kStepB = MODE == kWeights ? 128 : 2;
+      for (int pos = pos0; pos < tab.units && ok; pos += step) {
+        const Unit u = unit_at<MODE>(a, tab, pos, expert);
+        if (u.blocks == 0) continue;
+        const uint32_t idesc = idesc_bf16(kTile, u.n, MODE == kWeights) | (MODE == kForward ? 0u : 1u << 15);
+        if (!mbar_wait_warp_cluster(acc_free + 8 * acc, acc_phase ^ 1u, abort_flag, a.err, kErrProduct)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(acc * kTile);
+        for (int b = 0; b < u.blocks; ++b) {
+          if (!mbar_wait_warp_cluster(full + 8 * stage, phase, abort_flag, a.err, kErrProduct)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t off = (uint32_t)stage * (uint32_t)(kStage >> 4);
+          const int left = MODE == kWeights ? u.count - b * kBlock : kBlock;
+#pragma unroll
+          for (int i = 0; i < kBlock / 16; ++i)
+            if (i * 16 < left)
+              umma_pair_warp(d, a0 + off + kStepA * i, b0 + off + kStepB * i, idesc, (b | i) != 0 ? 1u : 0u);
+          commit_pair_warp(empty + 8 * stage);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        commit_pair_warp(acc_full + 8 * acc);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      commit_own_warp(drain);  // products in flight end before TMEM is freed
+      drain_wait(drain, 0);
+      __syncwarp();
+    }
+  } else if (warp < 2 + kStoreWarps) {
+    // ---- results ----
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* const tile = smem + L::kStore + (warp - 2) * L::kBlockBytes;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int pos = pos0; pos < tab.units; pos += step) {
+      const Unit u = unit_at<MODE>(a, tab, pos, expert);
+      const int row0 = u.m0 + (int)rank * kHalf + quarter * 32;
+      if (u.blocks > 0) {
+        const bool got = mbar_wait(acc_full + 8 * acc, acc_phase, abort_flag, a.err, kErrStore);
+        if (!__all_sync(0xffffffffu, got)) break;
+        tc_fence_after();
+      }
+      const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kTile);
+      const int columns = MODE == kWeights ? min(u.n, a.n - u.n0) : u.count;
+      if (row0 < a.m && !(MODE == kWeights && u.blocks == 0 && a.accumulate)) {
+        for (int c0 = 32 * half; c0 < columns; c0 += 64) {
+          uint32_t r[32];
+          if (u.blocks > 0) {
+            tmem_ld_32x32b_x32(t0 + (uint32_t)c0, r);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = 0;
+          }
+          if constexpr (MODE == kWeights)
+            store_weights<F32>(a, u, row0, u.n0 + c0, r, tile, lane);
+          else
+            store_tokens(a, u, row0, c0, r, tile, lane);
+        }
+      }
+      if (u.blocks > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(acc_free + 8 * acc, 0));
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_read_all();  // the stores have read shared memory
+    __syncwarp();
+  } else if (MODE == kWeights) {
+    // ---- rows behind an expert's tokens ----
+    int issued = 0;
+    uint32_t tail_phase = 0, fixed_phase = 0;  // a bit a stage
+    for (int pos = pos0; pos < tab.units; pos += step) {
+      const Unit u = unit_at<MODE>(a, tab, pos, expert);
+      issued += u.blocks;
+      const int left = u.count % kBlock;
+      if (left == 0) continue;
+      const int stage = (issued - 1) % S;
+      if (!mbar_wait_warp(tail + 8 * stage, (tail_phase >> stage) & 1u, abort_flag, a.err, kErrClear)) break;
+      tail_phase ^= 1u << stage;
+      const int end = (left + 15) & ~15;  // products go in steps of 16
+      uint8_t* const at = smem + stage * kStage;
+      const int panels = kHalf / 64 + u.n / 2 / 64;  // the left operand's, then the right one's
+      for (int p = 0; p < panels; ++p)
+        for (int i = left * 8 + lane; i < end * 8; i += 32)
+          *reinterpret_cast<uint4*>(at + p * kPanel + i * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (rank != 0) {
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(fixed + 8 * stage, 0));
+        continue;
+      }
+      if (!mbar_wait_warp_cluster(fixed + 8 * stage, (fixed_phase >> stage) & 1u, abort_flag, a.err, kErrClear)) break;
+      fixed_phase ^= 1u << stage;
+      fence_proxy_async_smem();
+      if (lane == 0) mbar_arrive(full + 8 * stage);
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither leaves while the other may reach its shared memory or TMEM
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc<2>(tmem, kTmemColumns);
+}
+
+// ---- host ----
+
+// A row-major tensor [z][y][x] of 16-byte aligned rows.
+bool map3(CUtensorMap* tm, const void* base, bool f32, int64_t x, int64_t y, int64_t z, int64_t sy, int64_t sz,
+          int box_x, int box_y, CUtensorMapSwizzle swizzle) {
+  const int64_t e = f32 ? 4 : 2;
+  // the stride of a single row or matrix is never used, but has to be a legal one
+  if (y <= 1) sy = x;
+  if (z <= 1) sz = y * sy;
+  const cuuint64_t dims[3] = {(cuuint64_t)x, (cuuint64_t)y, (cuuint64_t)z};
+  const cuuint64_t strides[2] = {(cuuint64_t)(sy * e), (cuuint64_t)(sz * e)};
+  const cuuint32_t box[3] = {(cuuint32_t)box_x, (cuuint32_t)box_y, 1}, step[3] = {1, 1, 1};
+  return op_tensor_map(tm, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims,
+                       strides, box, step, swizzle);
+}
+
+bool map2(CUtensorMap* tm, const void* base, int64_t x, int64_t y, int box_x, int box_y, CUtensorMapSwizzle swizzle) {
+  const cuuint64_t dims[2] = {(cuuint64_t)x, (cuuint64_t)y}, strides[1] = {(cuuint64_t)(x * 2)};
+  const cuuint32_t box[2] = {(cuuint32_t)box_x, (cuuint32_t)box_y}, step[2] = {1, 1};
+  return op_tensor_map(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, step, swizzle);
+}
+
+template <int MODE, bool F32>
+cudaError_t launch(ExpertArgs& a, int sms, int64_t most_units, cudaStream_t st) {
+  using L = Layout<F32>;
+  cudaError_t e = op_smem_limit<expert_matmul_kernel<MODE, F32>>(L::kBytes);
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(sms / 2, most_units));
+  return op_launch(expert_matmul_kernel<MODE, F32>, dim3((unsigned)(2 * pairs)), dim3(kThreads), L::kBytes, st, 2, a);
+}
+
+ma_status check(const ma_expert_matmul* d, bool weight) {
+  if (!d) return op_fail(MA_ERR_ARG, "the description must not be NULL");
+  if (d->n_experts < 1 || d->n_experts > kMaxExperts)
+    return op_fail(MA_ERR_SHAPE, "%d experts: outside [1, %d]", d->n_experts, kMaxExperts);
+  if (d->inner < 8 || d->inner > 1 << 20 || d->inner % 8 || d->outer < 8 || d->outer > 1 << 20 || d->outer % 8)
+    return op_fail(MA_ERR_SHAPE, "inner %d or outer %d is no multiple of 8 in [8, 2^20]", d->inner, d->outer);
+  if (d->n_tokens < 0 || d->n_tokens > 1ll << 30)
+    return op_fail(MA_ERR_SHAPE, "%lld tokens: outside [0, 2^30]", (long long)d->n_tokens);
+  const int64_t wide = (std::max(d->inner, d->outer) + kTile - 1) / kTile;
+  const int64_t narrow = (std::min(d->inner, d->outer) + kTile - 1) / kTile;
+  if ((d->n_tokens / kTile + d->n_experts + 1) * wide > INT32_MAX / 2 || d->n_experts * wide * narrow > INT32_MAX / 2)
+    return op_fail(MA_ERR_SHAPE, "%lld tokens and %d experts of %d x %d are too many for a call",
+                   (long long)d->n_tokens, d->n_experts, d->outer, d->inner);
+  if (!d->offsets) return op_fail(MA_ERR_ARG, "offsets must not be NULL");
+  if (!op_aligned(d->offsets, 4)) return op_fail(MA_ERR_ALIGN, "offsets is not aligned to 4 bytes");
+  if (d->n_tokens > 0 && weight) {
+    if (!d->weight) return op_fail(MA_ERR_ARG, "weight must not be NULL");
+    if (d->weight_row_stride < d->inner ||
+        (d->n_experts > 1 && d->weight_expert_stride < (d->outer - 1) * d->weight_row_stride + d->inner))
+      return op_fail(MA_ERR_SHAPE, "the weights' rows or matrices overlap");
+    if (!op_aligned(d->weight, 16) || d->weight_row_stride % 8 || (d->n_experts > 1 && d->weight_expert_stride % 8))
+      return op_fail(MA_ERR_ALIGN, "the weights' rows do not start on 16-byte boundaries");
+    if (d->weight_row_stride > 1ll << 38 || d->weight_expert_stride > 1ll << 38)
+      return op_fail(MA_ERR_SHAPE, "a stride of the weights is above 2^38");
+  }
+  return MA_OK;
+}
+
+ma_status check_rows(const char* name, const void* p, int64_t n, int64_t width, int64_t stride) {
+  if (!p) return op_fail(MA_ERR_ARG, "%s must not be NULL", name);
+  if (n > 1 && (stride < width || stride > 1ll << 38))
+    return op_fail(MA_ERR_SHAPE, "%s has rows %lld apart: below the width, or above 2^38", name, (long long)stride);
+  if (!op_aligned(p, 16) || (n > 1 && stride % 8))
+    return op_fail(MA_ERR_ALIGN, "%s does not have its rows on 16-byte boundaries", name);
+  return MA_OK;
+}
+
+ma_status refused_map() { return op_fail(MA_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor"); }
+
+ExpertArgs args_of(const ma_expert_matmul* d, int m, int n, int k, int* err) {
+  ExpertArgs a{};
+  a.offsets = d->offsets;
+  a.tokens = (int)d->n_tokens;
+  a.experts = d->n_experts;
+  a.m = m;
+  a.n = n;
+  a.k = k;
+  a.err = err;
+  return a;
+}
+
+constexpr CUtensorMapSwizzle kWide = CU_TENSOR_MAP_SWIZZLE_128B, kNarrow = CU_TENSOR_MAP_SWIZZLE_64B;
+
+// Units of a product whose columns are tokens, at most.
+int64_t token_units(const ExpertArgs& a) {
+  return ((int64_t)a.tokens / kTile + std::min(a.experts + 1, a.tokens)) * ((a.m + kTile - 1) / kTile);
+}
+
+}  // namespace
+}  // namespace ma
+
+using namespace ma;
+
+extern "C" {
+
+ma_status muon_adamw_expert_matmul(const ma_expert_matmul* d, void* out, void* cuda_stream) {
+  ma_status st = check(d, true);
+  if (st != MA_OK) return st;
+  if (d->n_tokens > 0) {
+    st = check_rows("x", d->x, d->n_tokens, d->inner, d->x_stride);
+    if (st == MA_OK) st = check_rows("out", out, d->n_tokens, d->outer, d->outer);
+    if (st != MA_OK) return st;
+    int sms = 0, *err = nullptr;
+    cudaError_t e = op_device(&sms, &err);
+    if (e != cudaSuccess) return op_cuda(e, "device query");
+    ExpertArgs a = args_of(d, d->outer, 0, d->inner, err);
+    a.dst = out;
+    if (!map3(&a.a, d->weight, false, d->inner, d->outer, d->n_experts, d->weight_row_stride, d->weight_expert_stride,
+              kBlock, kHalf, kWide) ||
+        !map3(&a.b, d->x, false, d->inner, d->n_tokens, 1, d->x_stride, 0, kBlock, kHalf, kWide) ||
+        !map3(&a.b_small, d->x, false, d->inner, d->n_tokens, 1, d->x_stride, 0, kBlock, kSmallBox, kWide) ||
+        !map2(&a.out, out, d->outer, d->n_tokens, 32, 32, kNarrow))
+      return refused_map();
+    e = launch<kForward, false>(a, sms, token_units(a), static_cast<cudaStream_t>(cuda_stream));
+    if (e != cudaSuccess) return op_cuda(e, "expert product launch");
+  }
+  clear_last_error();
+  return MA_OK;
+}
+
+ma_status muon_adamw_expert_matmul_backward(const ma_expert_matmul* d, const void* dout, int64_t dout_stride,
+                                            void* dx, void* dweight, int grad_dtype, int accumulate,
+                                            void* cuda_stream) {
+  ma_status st = check(d, dx != nullptr);
+  if (st != MA_OK) return st;
+  if (!op_dtype_ok(grad_dtype))
+    return op_fail(MA_ERR_DTYPE, "grad_dtype %d is neither MA_DT_F32 nor MA_DT_BF16", grad_dtype);
+  if (accumulate != 0 && accumulate != 1) return op_fail(MA_ERR_ARG, "accumulate %d is neither 0 nor 1", accumulate);
+  if (d->n_tokens > 0) {
+    st = check_rows("dout", dout, d->n_tokens, d->outer, dout_stride);
+    if (st == MA_OK && dweight) st = check_rows("x", d->x, d->n_tokens, d->inner, d->x_stride);
+    if (st == MA_OK && dx) st = check_rows("dx", dx, d->n_tokens, d->inner, d->inner);
+    if (st != MA_OK) return st;
+  }
+  if (dweight && !op_aligned(dweight, 16)) return op_fail(MA_ERR_ALIGN, "dweight is not aligned to 16 bytes");
+  int sms = 0, *err = nullptr;
+  cudaError_t e = op_device(&sms, &err);
+  if (e != cudaSuccess) return op_cuda(e, "device query");
+  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (dx && d->n_tokens > 0) {
+    ExpertArgs a = args_of(d, d->inner, 0, d->outer, err);
+    a.dst = dx;
+    if (!map3(&a.a, d->weight, false, d->inner, d->outer, d->n_experts, d->weight_row_stride, d->weight_expert_stride,
+              64, kBlock, kWide) ||
+        !map3(&a.b, dout, false, d->outer, d->n_tokens, 1, dout_stride, 0, kBlock, kHalf, kWide) ||
+        !map3(&a.b_small, dout, false, d->outer, d->n_tokens, 1, dout_stride, 0, kBlock, kSmallBox, kWide) ||
+        !map2(&a.out, dx, d->inner, d->n_tokens, 32, 32, kNarrow))
+      return refused_map();
+    e = launch<kInput, false>(a, sms, token_units(a), s);
+    if (e != cudaSuccess) return op_cuda(e, "expert input gradient launch");
+  }
+  const bool f32 = grad_dtype == MA_DT_F32;
+  if (dweight && d->n_tokens == 0 && !accumulate) {
+    e = cudaMemsetAsync(dweight, 0, (size_t)d->n_experts * d->outer * d->inner * op_dtype_size(grad_dtype), s);
+    if (e != cudaSuccess) return op_cuda(e, "expert weight gradient");
+  } else if (dweight && d->n_tokens > 0) {
+    ExpertArgs a = args_of(d, d->outer, d->inner, 0, err);
+    a.dst = dweight;
+    a.accumulate = accumulate;
+    if (!map3(&a.a, dout, false, d->outer, d->n_tokens, 1, dout_stride, 0, 64, kBlock, kWide) ||
+        !map3(&a.b, d->x, false, d->inner, d->n_tokens, 1, d->x_stride, 0, 64, kBlock, kWide) ||
+        !map3(&a.out, dweight, f32, d->inner, d->outer, d->n_experts, d->inner, (int64_t)d->outer * d->inner, 32, 32,
+              f32 ? kWide : kNarrow))
+      return refused_map();
+    const int64_t units =
+        (int64_t)d->n_experts * ((a.m + kTile - 1) / kTile) * ((a.n + kTile - 1) / kTile);
+    e = f32 ? launch<kWeights, true>(a, sms, units, s) : launch<kWeights, false>(a, sms, units, s);
+    if (e != cudaSuccess) return op_cuda(e, "expert weight gradient launch");
+  }
+  clear_last_error();
+  return MA_OK;
+}
+
+}  // extern "C"

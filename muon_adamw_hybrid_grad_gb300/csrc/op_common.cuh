@@ -1,8 +1,10 @@
 // Shared by the operators beside the optimizer step (embedding.cu,
-// qk_norm_rope.cu, window_attention.cu): error reporting at the C boundary
+// qk_norm_rope.cu, window_attention.cu, dropout.cu, residual_norm.cu,
+// expert_matmul.cu, token_logprobs.cu): error reporting at the C boundary
 // and 8-element vector access to fp32 and bf16 rows.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdarg.h>
@@ -38,6 +40,12 @@ inline bool op_aligned(const void* p, int64_t bytes) { return reinterpret_cast<u
 // the first error code of a bounded wait that ran out (operators.cu; looked up
 // once per device).
 cudaError_t op_device(int* sms, int** err);
+
+// cuTensorMapEncodeTiled without interleaving, its elements outside read as
+// zero; false if the driver refuses the tensor.
+bool op_tensor_map(CUtensorMap* tm, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+                   const cuuint64_t* strides, const cuuint32_t* box, const cuuint32_t* step,
+                   CUtensorMapSwizzle swizzle);
 
 // Raise a kernel's dynamic shared memory limit, once per device.
 constexpr int kOpMaxDevices = 64;

@@ -1,0 +1,128 @@
+// Rows of the residual stream in registers: shared by the forward pass and the gradient.
+//
+// T threads share a row and hold V vectors of eight elements each: vector j of
+// thread t is columns (j T + t) 8 onwards, so that a warp's accesses are whole
+// lines. VEC: the width is a multiple of 8 and all rows start on 16-byte
+// boundaries; otherwise elements are accessed one by one.
+#pragma once
+
+#include <utility>
+
+#include "dropout.cuh"
+#include "op_common.cuh"
+
+namespace ma {
+
+constexpr int kNormMaxWidth = 32768;  // 512 threads of eight vectors
+
+struct NormArgs {
+  int64_t n;
+  int w;
+  float eps;
+  DropArgs drop;  // threshold 0: none
+  const float* weight;
+  const void *x, *residual;  // forward; residual may be NULL
+  int64_t xs, rs;
+  void* y;
+  float* scales;  // forward, 8 bits
+  void* res;      // forward: output, may be NULL
+  const void *dy, *dres, *r;  // gradient; dres may be NULL
+  int64_t dys, dress, ress;
+  void *dx, *dr;  // dx may be NULL
+  float *partial, *dweight;
+};
+
+cudaError_t residual_norm_forward(const NormArgs& a, int dtype, int stream_dtype, bool vec, cudaStream_t st);
+cudaError_t residual_norm_backward(const NormArgs& a, int dtype, int stream_dtype, bool vec, cudaStream_t st);
+int64_t residual_norm_backward_space(int64_t n, int w);  // bytes of partial sums
+
+namespace {
+
+template <typename T, bool VEC>
+struct RowVec {
+  RawVec<T, 8> raw;
+  __device__ __forceinline__ void load(const T* row, int col, int w) {
+    if (col < w) raw.load(row + col);
+  }
+  __device__ __forceinline__ void get(int col, int w, float (&v)[8]) const {
+    if (col < w) {
+      raw.get(v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    }
+  }
+};
+template <typename T>
+struct RowVec<T, false> {
+  T v8[8];
+  __device__ __forceinline__ void load(const T* row, int col, int w) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (col + e < w) v8[e] = row[col + e];
+  }
+  __device__ __forceinline__ void get(int col, int w, float (&v)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = col + e < w ? load1(&v8[e]) : 0.f;
+  }
+};
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_row(T* row, int col, int w, const float (&v)[8]) {
+  if constexpr (VEC) {
+    if (col < w) store8(row + col, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (col + e < w) store1(row + col + e, v[e]);
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void load_weight(const float* weight, int col, int w, float (&v)[8]) {
+  if constexpr (VEC) {
+    if (col < w) {
+      load8(weight + col, v);
+      return;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = col + e < w ? weight[col + e] : 0.f;
+}
+
+// drop8 of the elements from `at` on. VEC: `at` is a multiple of 8.
+template <bool VEC>
+__device__ __forceinline__ void drop8_at(const DropKey& k, int64_t at, float (&x)[8]) {
+  const uint32_t group = (uint32_t)(at >> 3);
+  if (VEC || (at & 7) == 0) {
+    drop8(k, group, x);
+    return;
+  }
+  // the end of one group and the beginning of the next
+  const uint4 a = philox(make_uint4(group, k.site, k.step0, k.step1), k.k0, k.k1);
+  const uint4 b = philox(make_uint4(group + 1, k.site, k.step0, k.step1), k.k0, k.k1);
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  const int s = (int)(at & 7);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i == s + e) bits = w[i / 2] >> (16 * (i & 1)) & 0xFFFFu;
+    x[e] = bits >= k.threshold ? x[e] * k.factor : 0.f;
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+
+}  // namespace
+}  // namespace ma

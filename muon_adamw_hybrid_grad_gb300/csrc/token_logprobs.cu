@@ -1,0 +1,670 @@
+// Log probabilities of given tokens with entropy and top alternatives, and their gradient.
+//
+// Forward, one pass over a row: each thread keeps its own running maximum m, the
+// sum s of 2^a and the sum u of a 2^a, a = (x - m) scale log2(e), over groups of
+// 32 elements, and joins them at the end:
+//   lse = m scale + ln s,  entropy = ln s - ln(2) u / s.
+// Sums are kept relative to the maximum, so that neither entropy nor a log
+// probability is a difference of large numbers.
+//
+// The alternatives cost the pass next to nothing: a group's maximum, which the
+// softmax needs anyway, is kept in shared memory. The k-th largest of the
+// threads' maxima is at most the k-th largest element, since k threads have an
+// element that reaches it. So only groups whose maximum reaches it are read
+// again, some 25 of thousands, and their few candidates ranked by comparison.
+//
+// A row of the large vocabulary has a block; where rows are few, a cluster of up
+// to eight blocks shares one and joins through distributed shared memory.
+// Bound by HBM for many rows, by latency for few.
+//
+// Gradient: an element-wise pass, bound by HBM (one row in, one out).
+#include <math.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "op_common.cuh"
+#include "tcgen05.cuh"
+
+namespace ma {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVecs = 4;  // vectors of eight elements in a group
+constexpr int kStep = kThreads * kVecs;  // vectors of a block's pass
+constexpr int kMaxTop = 32;
+constexpr int kListed = 1024;  // candidates above the threshold, and as many that equal it
+constexpr int kMaxVocab = 1 << 20;
+constexpr int kMaxParts = 8;
+constexpr int kMaxGroupBytes = (kMaxVocab / (kStep * 8) + 1) * kThreads * 4;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct LogprobArgs {
+  const void* logits;
+  const void* ids;
+  int64_t n, stride, out_stride;
+  int vocab, id_bytes, top, parts;
+  float scale;
+  float *logprobs, *entropy, *lse, *top_logprobs;
+  int64_t* top_ids;
+  const float *dlogprobs, *dentropy, *entropy_in, *lse_in;
+  void* dlogits;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Two floats as one operand.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ void fill(RawVec<__nv_bfloat16, 8>& r) {
+  r.v = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);  // -infinity
+}
+__device__ __forceinline__ void fill(RawVec<float, 8>& r) {
+  r.a = r.b = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+}
+
+// The largest of a group's elements, NaN if there is one.
+__device__ __forceinline__ float group_max(const RawVec<__nv_bfloat16, 8> (&r)[kVecs]) {
+  __nv_bfloat162 m[4];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const uint32_t w[4] = {r[i].v.x, r[i].v.y, r[i].v.z, r[i].v.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[q]);
+      m[q] = i == 0 ? x : __hmax2_nan(m[q], x);
+    }
+  }
+  m[0] = __hmax2_nan(__hmax2_nan(m[0], m[1]), __hmax2_nan(m[2], m[3]));
+  return max_nan(__low2float(m[0]), __high2float(m[0]));
+}
+__device__ __forceinline__ float group_max(const RawVec<float, 8> (&r)[kVecs]) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i)
+    m = max_nan(m, max_nan(max_nan(max_nan(r[i].a.x, r[i].a.y), max_nan(r[i].a.z, r[i].a.w)),
+                           max_nan(max_nan(r[i].b.x, r[i].b.y), max_nan(r[i].b.z, r[i].b.w))));
+  return m;
+}
+
+// Softmax sums relative to their maximum m; m -infinity: nothing so far.
+struct Sums {
+  float m, s, u;
+};
+// The same sums relative to `m`, which is at least x.m.
+__device__ __forceinline__ Sums rebase(const Sums& x, float m, float c) {
+  if (x.m == -INFINITY) return {m, 0.f, 0.f};
+  const float d = (x.m - m) * c, f = ex2(d);
+  // where nothing is left the difference may be infinite
+  return {m, f * x.s, f == 0.f ? f * x.u : f * fmaf(d, x.s, x.u)};
+}
+__device__ __forceinline__ Sums join(const Sums& x, const Sums& y, float c) {
+  const float m = max_nan(x.m, y.m);
+  const Sums a = rebase(x, m, c), b = rebase(y, m, c);
+  return {m, a.s + b.s, a.u + b.u};
+}
+
+// An element's place in the order of the alternatives: by value, the lowest
+// index first among equal ones. NaN counts as -infinity.
+__device__ __forceinline__ uint32_t rank_bits(float x) {
+  x = x != x ? -INFINITY : x + 0.f;  // one zero
+  const uint32_t b = __float_as_uint(x);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t rank_key(float x, uint32_t index) {
+  return (uint64_t)rank_bits(x) << 32 | (0xFFFFFFFFu - index);
+}
+__device__ __forceinline__ float key_value(uint64_t key) {
+  const uint32_t b = (uint32_t)(key >> 32);
+  return __uint_as_float(b & 0x80000000u ? b & 0x7FFFFFFFu : ~b);
+}
+__device__ __forceinline__ uint32_t key_index(uint64_t key) { return 0xFFFFFFFFu - (uint32_t)key; }
+
+__device__ __forceinline__ int64_t token_id(const LogprobArgs& a, int64_t row) {
+  return a.id_bytes == 8 ? __ldg(static_cast<const long long*>(a.ids) + row)
+                         : (int64_t)__ldg(static_cast<const int*>(a.ids) + row);
+}
+
+__device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// A row as its elements up to the first 16-byte boundary, vectors of eight, and the rest.
+template <typename T>
+struct Row {
+  const T* p;
+  int head, vecs, tail;
+  __device__ __forceinline__ Row(const T* row, int vocab) : p(row) {
+    const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15);
+    head = min(off ? (16 - off) / (int)sizeof(T) : 0, vocab);
+    vecs = (vocab - head) / 8;
+    tail = vocab - head - vecs * 8;
+  }
+  __device__ __forceinline__ int index(int vec) const { return head + vec * 8; }
+  // the edge element of thread t, -1 for none
+  __device__ __forceinline__ int edge(int t) const {
+    return t < head ? t : t >= 32 && t - 32 < tail ? head + vecs * 8 + t - 32 : -1;
+  }
+};
+
+struct TopShared {
+  float best[kThreads];
+  uint64_t list[2 * kListed];  // above the threshold, then equal to it
+  uint64_t chosen[kMaxTop];
+  uint64_t warp_best[kThreads / 32];
+  int warp_count[kThreads / 32];
+  float threshold;
+  int above, equal;
+};
+
+// The block's `top` first elements of vectors [v0, v1), and of the row's edges
+// with `edges`, into sh.chosen in their order; 0 where there are fewer.
+template <typename T>
+__device__ void choose_top(const Row<T>& row, int v0, int v1, bool edges, int top, float best, const float* groups,
+                           TopShared& sh) {
+  const int t = threadIdx.x;
+  sh.best[t] = best;
+  if (t < kMaxTop) sh.chosen[t] = 0;
+  if (t == 0) sh.above = sh.equal = 0;
+  __syncthreads();
+  int rank = 0;
+#pragma unroll 16
+  for (int i = 0; i < kThreads; ++i) {
+    const float b = sh.best[i];
+    rank += b > best || (b == best && i < t);
+  }
+  if (rank == top - 1) sh.threshold = best;
+  __syncthreads();
+  const float limit = sh.threshold;
+  const uint32_t limit_bits = rank_bits(limit);
+  auto offer = [&](float x, int index) {
+    const uint64_t key = rank_key(x, (uint32_t)index);
+    const uint32_t bits = (uint32_t)(key >> 32);
+    if (bits > limit_bits) {
+      const int at = atomicAdd(&sh.above, 1);
+      if (at < kListed) sh.list[at] = key;
+    } else if (bits == limit_bits) {
+      const int at = atomicAdd(&sh.equal, 1);
+      if (at < kListed) sh.list[kListed + at] = key;
+    }
+  };
+  // every element of this thread whose group reaches the threshold
+  auto each = [&](auto&& f) {
+    int g = t;
+    for (int v = v0; v < v1; v += kStep, g += kThreads) {
+      const float m = groups[g];
+      if (m < limit) continue;
+      for (int j = 0; j < kVecs; ++j) {
+        const int vec = v + j * kThreads + t;
+        if (vec >= v1) break;
+        float x[8];
+        load8(row.p + row.index(vec), x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f(x[e], row.index(vec) + e);
+      }
+    }
+    if (edges && row.edge(t) >= 0) f(load1(row.p + row.edge(t)), row.edge(t));
+  };
+  each(offer);
+  __syncthreads();
+  int above = sh.above, equal = sh.equal;
+  if (above > kListed) {
+    // a few threads hold more large elements than the list takes: one element a pass
+    uint64_t before = ~0ull;
+    for (int r = 0; r < top; ++r) {
+      uint64_t mine = 0;
+      each([&](float x, int index) {
+        const uint64_t key = rank_key(x, (uint32_t)index);
+        if (key < before && key > mine) mine = key;
+      });
+      for (int d = 16; d > 0; d >>= 1) mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, d));
+      if ((t & 31) == 0) sh.warp_best[t >> 5] = mine;
+      __syncthreads();
+      before = 0;
+#pragma unroll
+      for (int i = 0; i < kThreads / 32; ++i) before = max(before, (uint64_t)sh.warp_best[i]);
+      if (t == 0) sh.chosen[r] = before;
+      __syncthreads();
+    }
+    return;
+  }
+  if (equal > kListed) {
+    // ties without end, as in a masked row: the first ones in the order of their indices. The vectors hold enough
+    // of them, so that the edge behind them, whose indices are the largest, is not needed.
+    int found = 0;
+    if (edges) {
+      if (t < 32) {
+        const bool tie = t < row.head && rank_bits(load1(row.p + t)) == limit_bits;
+        const uint32_t votes = __ballot_sync(0xffffffffu, tie);
+        if (tie) sh.list[kListed + __popc(votes & ((1u << t) - 1))] = rank_key(limit, (uint32_t)t);
+        if (t == 0) sh.warp_count[0] = __popc(votes);
+      }
+      __syncthreads();
+      found = sh.warp_count[0];
+      __syncthreads();
+    }
+    for (int v = v0; v < v1 && found < top; v += kThreads) {
+      uint32_t ties = 0;
+      if (v + t < v1) {
+        float x[8];
+        load8(row.p + row.index(v + t), x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ties |= (uint32_t)(rank_bits(x[e]) == limit_bits) << e;
+      }
+      const int mine = __popc(ties);
+      int upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, upto, d);
+        if ((t & 31) >= d) upto += o;
+      }
+      if ((t & 31) == 31) sh.warp_count[t >> 5] = upto;
+      __syncthreads();
+      int place = found + upto - mine, total = 0;
+#pragma unroll
+      for (int i = 0; i < kThreads / 32; ++i) {
+        const int c = sh.warp_count[i];
+        if (i < (t >> 5)) place += c;
+        total += c;
+      }
+      for (; ties; ties &= ties - 1, ++place)
+        if (place < top) sh.list[kListed + place] = rank_key(limit, (uint32_t)(row.index(v + t) + __ffs(ties) - 1));
+      found += total;
+      __syncthreads();
+    }
+    equal = min(found, top);
+  }
+  for (int i = t; i < above + equal; i += kThreads) {
+    const uint64_t key = sh.list[i < above ? i : kListed + i - above];
+    int r = 0;
+    for (int k = 0; k < above; ++k) r += sh.list[k] > key;
+    for (int k = 0; k < equal; ++k) r += sh.list[kListed + k] > key;
+    if (r < top) sh.chosen[r] = key;
+  }
+  __syncthreads();
+}
+
+// A thread's running sums, in pairs.
+struct Running {
+  float m;
+  uint64_t s, u;
+  __device__ __forceinline__ void raise(float gm, float c) {
+    const float f = m == -INFINITY ? 0.f : ex2((m - gm) * c);
+    const float d = f == 0.f ? 0.f : (m - gm) * c;
+    u = mul2(pack2(f, f), fma2(pack2(d, d), s, u));
+    s = mul2(pack2(f, f), s);
+    m = gm;
+  }
+  __device__ __forceinline__ void add(float x, float y, float c) {
+    const uint64_t a = mul2(add2(pack2(x, y), pack2(-m, -m)), pack2(c, c));
+    float p, q;
+    unpack2(a, p, q);
+    // -infinity would meet a zero
+    p = max_nan(p, -1e30f);
+    q = max_nan(q, -1e30f);
+    const uint64_t e = pack2(ex2(p), ex2(q));
+    s = add2(s, e);
+    u = fma2(e, pack2(p, q), u);
+  }
+  __device__ __forceinline__ Sums sums() const {
+    float s0, s1, u0, u1;
+    unpack2(s, s0, s1);
+    unpack2(u, u0, u1);
+    return {m, s0 + s1, u0 + u1};
+  }
+};
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
+  extern __shared__ float groups[];  // TOP: the maximum of every thread's groups
+  __shared__ Sums warp_sums[kThreads / 32];
+  __shared__ Sums part_sums;
+  __shared__ TopShared sh;
+  const int t = threadIdx.x;
+  const int64_t at = blockIdx.x / a.parts;
+  const int part = (int)(blockIdx.x - at * a.parts);
+  pdl_wait();
+  pdl_launch();
+  const Row<T> row(static_cast<const T*>(a.logits) + at * a.stride, a.vocab);
+  const int share = (row.vecs + a.parts * kStep - 1) / (a.parts * kStep) * kStep;
+  const int v0 = min(part * share, row.vecs), v1 = min(v0 + share, row.vecs);
+  const bool edges = part == 0;
+  const float c = a.scale * kLog2e;
+
+  // the given token's logit, by the thread that needs it
+  int64_t id = -1;
+  float given = 0.f;
+  if (edges && t == 0) {
+    id = token_id(a, at);
+    if (id >= 0 && id < a.vocab) given = load1(row.p + id);
+  }
+  Running run{-INFINITY, 0, 0};
+  float best = -INFINITY;
+  RawVec<T, 8> next[kVecs];
+  auto fetch = [&](int v) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const int vec = v + j * kThreads + t;
+      if (vec < v1)
+        next[j].load(row.p + row.index(vec));
+      else
+        fill(next[j]);
+    }
+  };
+  if (v0 < v1) fetch(v0);
+  int g = t;
+  for (int v = v0; v < v1; v += kStep, g += kThreads) {
+    RawVec<T, 8> cur[kVecs];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) cur[j] = next[j];
+    if (v + kStep < v1) fetch(v + kStep);
+    const float gm = group_max(cur);
+    if (TOP) {
+      groups[g] = gm;
+      best = fmaxf(best, gm);
+    }
+    if (!(gm <= run.m)) run.raise(gm, c);
+    if (run.m == -INFINITY) continue;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      float x[8];
+      cur[j].get(x);
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) run.add(x[e], x[e + 1], c);
+    }
+  }
+  if (edges && row.edge(t) >= 0) {
+    const float x = load1(row.p + row.edge(t));
+    best = fmaxf(best, x);
+    if (!(x <= run.m)) run.raise(x, c);
+    if (run.m != -INFINITY) run.add(x, -INFINITY, c);
+  }
+  Sums all = run.sums();
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1)
+    all = join(all, {__shfl_xor_sync(0xffffffffu, all.m, d), __shfl_xor_sync(0xffffffffu, all.s, d),
+                     __shfl_xor_sync(0xffffffffu, all.u, d)}, c);
+  if ((t & 31) == 0) warp_sums[t >> 5] = all;
+  __syncthreads();
+  all = warp_sums[0];
+#pragma unroll
+  for (int i = 1; i < kThreads / 32; ++i) all = join(all, warp_sums[i], c);
+  if constexpr (TOP) choose_top(row, v0, v1, edges, a.top, best, groups, sh);
+
+  if (a.parts > 1) {
+    // the cluster's first block reads the others' results
+    if (t == 0) part_sums = all;
+    cluster_sync();
+    if (part == 0) {
+      const uint32_t theirs = smem_u32(&part_sums);
+      for (int i = 1; i < a.parts; ++i) {
+        const uint32_t p = mapa_shared(theirs, i);
+        all = join(all, {ld_cluster_f32(p), ld_cluster_f32(p + 4), ld_cluster_f32(p + 8)}, c);
+      }
+      if constexpr (TOP) {
+        const uint32_t lists = smem_u32(sh.chosen);
+        const int i = t / kMaxTop;  // one key a thread
+        sh.list[t] = i < a.parts && t % kMaxTop < a.top ? ld_cluster_u64(mapa_shared(lists, i) + 8 * (t % kMaxTop)) : 0;
+      }
+    }
+    cluster_sync();
+    if (part != 0) return;
+    if constexpr (TOP) {
+      const uint64_t key = sh.list[t];
+      int r = 0;
+#pragma unroll 16
+      for (int i = 0; i < kThreads; ++i) r += sh.list[i] > key;
+      if (key != 0 && r < a.top) sh.chosen[r] = key;
+      __syncthreads();
+    }
+  }
+  const bool empty = all.m == -INFINITY;
+  const float log_s = logf(all.s);
+  if (t == 0) {
+    const bool inside = id >= 0 && id < a.vocab;
+    a.logprobs[at] = !inside ? 0.f : empty ? -INFINITY : (given - all.m) * a.scale - log_s;
+    a.entropy[at] = empty ? 0.f : log_s - kLn2 * (all.u / all.s);
+    a.lse[at] = empty ? -INFINITY : fmaf(all.m, a.scale, log_s);
+  }
+  if constexpr (TOP) {
+    if (t < a.top) {
+      const uint64_t key = sh.chosen[t];
+      a.top_logprobs[at * a.top + t] = empty ? -INFINITY : (key_value(key) - all.m) * a.scale - log_s;
+      a.top_ids[at * a.top + t] = (int64_t)key_index(key);
+    }
+  }
+}
+
+// ---- gradient ----
+// d_v = scale (dlogprob (1[v = id] - p_v) - dentropy p_v (log p_v + entropy))
+
+struct GradRow {
+  float shift, c, base, slope, given;  // d = 2^a (base + slope a) [+ given], a = (x - shift) c
+  int64_t id;
+  bool empty;
+};
+
+__device__ __forceinline__ GradRow grad_row(const LogprobArgs& a, int64_t at) {
+  GradRow g;
+  const float lse = __ldg(a.lse_in + at), h = a.dentropy ? __ldg(a.dentropy + at) : 0.f;
+  g.id = token_id(a, at);
+  const float l = a.dlogprobs && g.id >= 0 && g.id < a.vocab ? __ldg(a.dlogprobs + at) : 0.f;
+  g.shift = lse / a.scale;
+  g.c = a.scale * kLog2e;
+  g.given = a.scale * l;
+  g.base = -a.scale * (h == 0.f ? l : fmaf(h, __ldg(a.entropy_in + at), l));
+  g.slope = -a.scale * h * kLn2;
+  g.empty = lse == -INFINITY;
+  return g;
+}
+
+__device__ __forceinline__ float grad_of(const GradRow& g, float x) {
+  const float a = max_nan((x - g.shift) * g.c, -1e30f);
+  return g.empty ? 0.f : ex2(a) * fmaf(g.slope, a, g.base);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) token_logprobs_grad_kernel(const __grid_constant__ LogprobArgs a) {
+  const int t = threadIdx.x;
+  const int64_t at = blockIdx.x / a.parts;
+  const int part = (int)(blockIdx.x - at * a.parts);
+  pdl_wait();
+  pdl_launch();
+  const Row<T> row(static_cast<const T*>(a.logits) + at * a.stride, a.vocab);
+  T* const out = static_cast<T*>(a.dlogits) + at * a.out_stride;
+  auto single = [&](const GradRow& g, int i) {
+    store1(out + i, grad_of(g, load1(row.p + i)) + (i == g.id && !g.empty ? g.given : 0.f));
+  };
+  if (((reinterpret_cast<uintptr_t>(row.p) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0) {
+    // rows that lie differently: no boundary is both's
+    const GradRow g = grad_row(a, at);
+    const int end = min(a.vocab, (part + 1) * kStep * 8);
+    for (int i = part * kStep * 8 + t; i < end; i += kThreads) single(g, i);
+    return;
+  }
+  const int v0 = part * kStep;
+  RawVec<T, 8> raw[kVecs];
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    const int vec = v0 + j * kThreads + t;
+    if (vec < row.vecs) raw[j].load(row.p + row.index(vec));
+  }
+  const GradRow g = grad_row(a, at);
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    const int vec = v0 + j * kThreads + t;
+    if (vec >= row.vecs) break;
+    const int i = row.index(vec);
+    float x[8];
+    raw[j].get(x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = grad_of(g, x[e]);
+    if (g.id >= i && g.id < i + 8 && !g.empty) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (i + e == g.id) x[e] += g.given;
+    }
+    store8(out + i, x);
+  }
+  if (part == 0 && row.edge(t) >= 0) single(g, row.edge(t));
+}
+
+ma_status check(const ma_token_logprobs* d) {
+  if (!d) return op_fail(MA_ERR_ARG, "the description must not be NULL");
+  if (!op_dtype_ok(d->dtype)) return op_fail(MA_ERR_DTYPE, "dtype %d is neither MA_DT_F32 nor MA_DT_BF16", d->dtype);
+  if (d->id_bytes != 4 && d->id_bytes != 8) return op_fail(MA_ERR_ARG, "id_bytes %d is neither 4 nor 8", d->id_bytes);
+  if (d->n_tokens < 0 || d->n_tokens > (1ll << 30) || d->vocab < 1 || d->vocab > kMaxVocab)
+    return op_fail(MA_ERR_SHAPE, "%lld tokens of %lld logits: outside [0, 2^30] or [1, 2^20]", (long long)d->n_tokens,
+                   (long long)d->vocab);
+  // the gradient's blocks of 8192 logits, and a cluster's, are numbered in 31 bits
+  const int64_t parts = std::max<int64_t>((d->vocab + kStep * 8 - 1) / (kStep * 8), 1);
+  if (d->n_tokens * parts > INT32_MAX)
+    return op_fail(MA_ERR_SHAPE, "%lld tokens of %lld logits are too many for a call", (long long)d->n_tokens,
+                   (long long)d->vocab);
+  if (!(d->scale > 0.0) || !std::isfinite(d->scale) || !((float)d->scale > 0.f) || !std::isfinite((float)d->scale))
+    return op_fail(MA_ERR_ARG, "scale = %g is not positive and finite in fp32", d->scale);
+  if (d->n_tokens == 0) return MA_OK;
+  if (!d->logits || !d->ids) return op_fail(MA_ERR_ARG, "logits and ids must not be NULL");
+  if (!op_aligned(d->logits, op_dtype_size(d->dtype)) || !op_aligned(d->ids, d->id_bytes))
+    return op_fail(MA_ERR_ALIGN, "logits or ids is not aligned to its elements");
+  if (d->n_tokens > 1 && d->stride < d->vocab)
+    return op_fail(MA_ERR_SHAPE, "logits has rows %lld apart, below the vocabulary", (long long)d->stride);
+  return MA_OK;
+}
+
+LogprobArgs args_of(const ma_token_logprobs* d) {
+  LogprobArgs a{};
+  a.logits = d->logits;
+  a.ids = d->ids;
+  a.n = d->n_tokens;
+  a.stride = d->stride;
+  a.vocab = (int)d->vocab;
+  a.id_bytes = d->id_bytes;
+  a.scale = (float)d->scale;
+  return a;
+}
+
+template <typename T, bool TOP>
+cudaError_t forward(LogprobArgs& a, cudaStream_t st) {
+  int sms = 0, *err = nullptr;
+  cudaError_t e = op_device(&sms, &err);
+  if (e != cudaSuccess) return e;
+  a.parts = 1;
+  const int64_t steps = (a.vocab / 8 + kStep - 1) / kStep;
+  while (a.parts < kMaxParts && a.n * a.parts < sms && steps >= 2 * a.parts) a.parts *= 2;
+  const int64_t per = (steps + a.parts - 1) / a.parts;
+  if (TOP) {
+    e = op_smem_limit<token_logprobs_kernel<T, TOP>>(kMaxGroupBytes);
+    if (e != cudaSuccess) return e;
+  }
+  return op_launch(token_logprobs_kernel<T, TOP>, dim3((unsigned)(a.n * a.parts)), dim3(kThreads),
+                   TOP ? (size_t)std::max<int64_t>(per, 1) * kThreads * 4 : 0, st, a.parts, a);
+}
+
+}  // namespace
+}  // namespace ma
+
+using namespace ma;
+
+extern "C" {
+
+ma_status muon_adamw_token_logprobs(const ma_token_logprobs* d, int32_t top, float* logprobs, float* entropy,
+                                    float* lse, float* top_logprobs, int64_t* top_ids, void* cuda_stream) {
+  const ma_status st = check(d);
+  if (st != MA_OK) return st;
+  if (top < 0 || top > kMaxTop || top > d->vocab)
+    return op_fail(MA_ERR_ARG, "top = %d outside [0, %d], or above the vocabulary", top, kMaxTop);
+  if (d->n_tokens > 0) {
+    if (!logprobs || !entropy || !lse || (top > 0 && (!top_logprobs || !top_ids)))
+      return op_fail(MA_ERR_ARG, "the results must not be NULL");
+    if (!op_aligned(logprobs, 4) || !op_aligned(entropy, 4) || !op_aligned(lse, 4) ||
+        (top > 0 && (!op_aligned(top_logprobs, 4) || !op_aligned(top_ids, 8))))
+      return op_fail(MA_ERR_ALIGN, "a result is not aligned to its elements");
+    LogprobArgs a = args_of(d);
+    a.top = top;
+    a.logprobs = logprobs;
+    a.entropy = entropy;
+    a.lse = lse;
+    a.top_logprobs = top_logprobs;
+    a.top_ids = top_ids;
+    const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    const cudaError_t e = d->dtype == MA_DT_BF16
+                              ? (top ? forward<__nv_bfloat16, true>(a, s) : forward<__nv_bfloat16, false>(a, s))
+                              : (top ? forward<float, true>(a, s) : forward<float, false>(a, s));
+    if (e != cudaSuccess) return op_cuda(e, "log probabilities launch");
+  }
+  clear_last_error();
+  return MA_OK;
+}
+
+ma_status muon_adamw_token_logprobs_backward(const ma_token_logprobs* d, const float* dlogprobs,
+                                             const float* dentropy, const float* entropy, const float* lse,
+                                             void* dlogits, int64_t dlogits_stride, void* cuda_stream) {
+  const ma_status st = check(d);
+  if (st != MA_OK) return st;
+  if (d->n_tokens > 0) {
+    if (!lse || !dlogits || (dentropy && !entropy))
+      return op_fail(MA_ERR_ARG, "lse, dlogits and, with dentropy, entropy must not be NULL");
+    if (!op_aligned(dlogprobs, 4) || !op_aligned(dentropy, 4) || !op_aligned(entropy, 4) || !op_aligned(lse, 4) ||
+        !op_aligned(dlogits, op_dtype_size(d->dtype)))
+      return op_fail(MA_ERR_ALIGN, "a tensor is not aligned to its elements");
+    if (d->n_tokens > 1 && dlogits_stride < d->vocab)
+      return op_fail(MA_ERR_SHAPE, "dlogits has rows %lld apart, below the vocabulary", (long long)dlogits_stride);
+    LogprobArgs a = args_of(d);
+    a.dlogprobs = dlogprobs;
+    a.dentropy = dentropy;
+    a.entropy_in = entropy;
+    a.lse_in = lse;
+    a.dlogits = dlogits;
+    a.out_stride = dlogits_stride;
+    a.parts = std::max((a.vocab + kStep * 8 - 1) / (kStep * 8), 1);
+    const dim3 grid((unsigned)(a.n * a.parts));
+    const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    const cudaError_t e = d->dtype == MA_DT_BF16
+                              ? op_launch(token_logprobs_grad_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, s, 1, a)
+                              : op_launch(token_logprobs_grad_kernel<float>, grid, dim3(kThreads), 0, s, 1, a);
+    if (e != cudaSuccess) return op_cuda(e, "log probabilities gradient launch");
+  }
+  clear_last_error();
+  return MA_OK;
+}
+
+}  // extern "C"

@@ -405,6 +405,300 @@ PyObject* window_attention_backward(PyObject* const* a) {
                        THPVariable_Wrap(std::move(dv)));
 }
 
+// ---- rows: dropout, residual and norm, log probabilities ----
+
+// [..., width] as rows: 2-D tensors may have strided rows, others are copied where they are not contiguous.
+struct Rows2 {
+  Tensor t;
+  int64_t n, w, stride;
+};
+Rows2 rows_of(const Tensor& t, const char* name) {
+  if (t.dim() < 1) refuse(PyExc_ValueError, "%s must have at least one dimension", name);
+  Rows2 r{t, 1, t.size(-1), t.size(-1)};
+  for (int64_t i = 0; i + 1 < t.dim(); ++i) r.n *= t.size(i);
+  if (t.is_contiguous()) return r;
+  if (t.dim() == 2 && (r.w <= 1 || t.stride(1) == 1) && (r.n <= 1 || t.stride(0) >= r.w)) {
+    if (r.n > 1) r.stride = t.stride(0);
+    return r;
+  }
+  r.t = packed(t);
+  return r;
+}
+
+int32_t small(int64_t v) { return (int32_t)(v > INT32_MAX ? INT32_MAX : v < INT32_MIN ? INT32_MIN : v); }
+
+// seed and step; null where None
+const int64_t* rng_of(PyObject* o, const Tensor& like) {
+  if (o == Py_None) return nullptr;
+  const Tensor& r = tensor(o, "rng", like);
+  if (r.scalar_type() != at::kLong || r.dim() != 1 || r.size(0) != 2 || !r.is_contiguous())
+    refuse(PyExc_ValueError, "rng must be 2 contiguous int64 values: seed and step");
+  return static_cast<const int64_t*>(r.const_data_ptr());
+}
+
+// a: x, p, rng, site
+PyObject* dropout(PyObject* const* a) {
+  const Tensor& given = tensor(a[0], "x");
+  need_cuda(given);
+  const Tensor x = packed(given);
+  const int dt = dtype_of(x, "x");
+  const double p = real(a[1]);
+  if (a[2] == Py_None) refuse(PyExc_ValueError, "rng must be 2 contiguous int64 values: seed and step");
+  const int64_t* rng = rng_of(a[2], x);
+  const int32_t site = small(integer(a[3]));
+  Tensor out = make(x.sizes(), x.scalar_type(), x);
+  // an empty tensor has no address
+  const void* in = x.numel() ? x.const_data_ptr() : rng;
+  void* to = x.numel() ? out.mutable_data_ptr() : const_cast<int64_t*>(rng);
+  call(x, [&](void* s) { return muon_adamw_dropout(in, dt, x.numel(), p, rng, site, to, s); });
+  return THPVariable_Wrap(std::move(out));
+}
+
+struct Norm {
+  Tensor weight;
+  bool drops;
+  ma_residual_norm d;
+};
+
+// o: weight, eps, p, rng, site
+void read_norm(Norm& r, const Rows2& x, int dtype, int stream_dtype, PyObject* const* o) {
+  r.weight = tensor(o[0], "weight", x.t);
+  if (r.weight.scalar_type() != at::kFloat || r.weight.dim() != 1 || r.weight.size(0) != x.w ||
+      !r.weight.is_contiguous())
+    refuse(PyExc_ValueError, "weight must be %lld contiguous fp32 values", (long long)x.w);
+  ma_residual_norm& d = r.d;
+  d.n_tokens = x.n;
+  d.width = x.w;
+  d.dtype = dtype;
+  d.stream_dtype = stream_dtype;
+  d.eps = real(o[1]);
+  d.p = real(o[2]);
+  d.rng = rng_of(o[3], x.t);
+  d.site = small(integer(o[4]));
+  d.reserved = 0;
+  r.drops = !(d.p < 0.5 / 65536);
+}
+
+// a: x, residual or None, weight, eps, p, rng or None, site, eight_bit
+PyObject* residual_norm(PyObject* const* a) {
+  const Tensor& given = tensor(a[0], "x");
+  need_cuda(given);
+  const Rows2 x = rows_of(given, "x");
+  const int dt = dtype_of(given, "x");
+  Rows2 res{};
+  int st = dt;
+  if (a[1] != Py_None) {
+    const Tensor& t = tensor(a[1], "residual", given);
+    if (t.sizes() != given.sizes()) refuse(PyExc_ValueError, "residual does not have the shape of x");
+    res = rows_of(t, "residual");
+    st = dtype_of(t, "residual");
+  }
+  Norm m;
+  read_norm(m, x, dt, st, a + 2);
+  const bool eight = truth(a[7]), stored = a[1] != Py_None || m.drops;
+  Tensor y = make(given.sizes(), eight ? at::kFloat8_e4m3fn : given.scalar_type(), given);
+  Tensor scales, r;
+  if (eight) scales = make(given.sizes().slice(0, given.dim() - 1), at::kFloat, given);
+  if (stored) r = make(given.sizes(), st == MA_DT_F32 ? at::kFloat : at::kBFloat16, given);
+  call(given, [&](void* s) {
+    return muon_adamw_residual_norm(&m.d, x.t.const_data_ptr(), x.stride,
+                                    res.t.defined() ? res.t.const_data_ptr() : nullptr, res.stride,
+                                    static_cast<const float*>(m.weight.const_data_ptr()), y.mutable_data_ptr(),
+                                    eight ? static_cast<float*>(scales.mutable_data_ptr()) : nullptr,
+                                    stored ? r.mutable_data_ptr() : nullptr, s);
+  });
+  // without a residual and without dropout the stream is x itself
+  PyObject* stream = stored ? THPVariable_Wrap(std::move(r)) : Py_NewRef(a[0]);
+  if (eight)
+    return Py_BuildValue("NNN", THPVariable_Wrap(std::move(y)), THPVariable_Wrap(std::move(scales)), stream);
+  return Py_BuildValue("NN", THPVariable_Wrap(std::move(y)), stream);
+}
+
+// a: dy, dres or None, res, weight, eps, p, rng or None, site
+PyObject* residual_norm_backward(PyObject* const* a) {
+  const Tensor& given = tensor(a[2], "res");
+  need_cuda(given);
+  const Rows2 res = rows_of(given, "res");
+  const int st = dtype_of(given, "res");
+  const Tensor& gy = tensor(a[0], "dy", given);
+  const int dt = dtype_of(gy, "dy");
+  if (gy.sizes() != given.sizes()) refuse(PyExc_ValueError, "dy does not have the shape of res");
+  const Rows2 dy = rows_of(gy, "dy");
+  Rows2 dres{};
+  if (a[1] != Py_None) {
+    const Tensor& t = tensor(a[1], "dres", given);
+    if (t.sizes() != given.sizes() || t.scalar_type() != given.scalar_type())
+      refuse(PyExc_ValueError, "dres must have the shape and the type of res");
+    dres = rows_of(t, "dres");
+  }
+  Norm m;
+  read_norm(m, res, dt, st, a + 3);
+  int64_t bytes = 0;
+  check(muon_adamw_residual_norm_backward_workspace(&m.d, &bytes));
+  const bool apart = m.drops || dt != st;
+  Tensor ws = make({bytes}, at::kByte, given), dr = make(given.sizes(), given.scalar_type(), given);
+  Tensor dx, dw = make({res.w}, at::kFloat, given);
+  if (apart) dx = make(given.sizes(), gy.scalar_type(), given);
+  call(given, [&](void* s) {
+    return muon_adamw_residual_norm_backward(
+        &m.d, dy.t.const_data_ptr(), dy.stride, dres.t.defined() ? dres.t.const_data_ptr() : nullptr, dres.stride,
+        res.t.const_data_ptr(), res.stride, static_cast<const float*>(m.weight.const_data_ptr()),
+        apart ? dx.mutable_data_ptr() : nullptr, dr.mutable_data_ptr(), static_cast<float*>(dw.mutable_data_ptr()),
+        ws.mutable_data_ptr(), bytes, s);
+  });
+  PyObject* stream = THPVariable_Wrap(std::move(dr));
+  PyObject* branch = apart ? THPVariable_Wrap(std::move(dx)) : Py_NewRef(stream);
+  return Py_BuildValue("NNN", branch, stream, THPVariable_Wrap(std::move(dw)));
+}
+
+struct Logits {
+  Rows2 logits;
+  Tensor ids;
+  ma_token_logprobs d;
+};
+
+void read_logits(Logits& r, PyObject* logits, PyObject* ids, PyObject* scale) {
+  const Tensor& z = tensor(logits, "logits");
+  need_cuda(z);
+  r.logits = rows_of(z, "logits");
+  r.ids = packed(tensor(ids, "ids", z));
+  if (r.ids.sizes() != z.sizes().slice(0, z.dim() - 1))
+    refuse(PyExc_ValueError, "ids does not have the shape of logits without its last dimension");
+  r.d.n_tokens = r.logits.n;
+  r.d.vocab = r.logits.w;
+  r.d.stride = r.logits.stride;
+  r.d.dtype = dtype_of(z, "logits");
+  r.d.id_bytes = int_bytes(r.ids, "ids");
+  r.d.scale = real(scale);
+  r.d.logits = r.logits.t.const_data_ptr();
+  r.d.ids = r.ids.const_data_ptr();
+}
+
+// a: logits, ids, scale, top
+PyObject* token_logprobs(PyObject* const* a) {
+  Logits x;
+  read_logits(x, a[0], a[1], a[2]);
+  const int32_t top = small(integer(a[3]));
+  const Tensor& like = x.logits.t;
+  Tensor lp = make(x.ids.sizes(), at::kFloat, like), h = make(x.ids.sizes(), at::kFloat, like);
+  Tensor lse = make(x.ids.sizes(), at::kFloat, like);
+  c10::SmallVector<int64_t, 5> size(x.ids.sizes().begin(), x.ids.sizes().end());
+  size.push_back(top < 0 || top > 32 ? 0 : top);  // refused below
+  Tensor tl = make(size, at::kFloat, like), ti = make(size, at::kLong, like);
+  call(like, [&](void* s) {
+    return muon_adamw_token_logprobs(&x.d, top, static_cast<float*>(lp.mutable_data_ptr()),
+                                     static_cast<float*>(h.mutable_data_ptr()),
+                                     static_cast<float*>(lse.mutable_data_ptr()),
+                                     static_cast<float*>(tl.mutable_data_ptr()),
+                                     static_cast<int64_t*>(ti.mutable_data_ptr()), s);
+  });
+  return Py_BuildValue("NNNNN", THPVariable_Wrap(std::move(lp)), THPVariable_Wrap(std::move(h)),
+                       THPVariable_Wrap(std::move(lse)), THPVariable_Wrap(std::move(tl)),
+                       THPVariable_Wrap(std::move(ti)));
+}
+
+// a: dlogprobs or None, dentropy or None, logits, ids, entropy, lse, scale
+PyObject* token_logprobs_backward(PyObject* const* a) {
+  Logits x;
+  read_logits(x, a[2], a[3], a[6]);
+  const Tensor& like = x.logits.t;
+  static const char* const names[4] = {"dlogprobs", "dentropy", "entropy", "lse"};
+  PyObject* const given[4] = {a[0], a[1], a[4], a[5]};
+  Tensor keep[4];
+  const float* at[4] = {};
+  for (int i = 0; i < 4; ++i) {
+    if (i < 2 && given[i] == Py_None) continue;
+    keep[i] = packed(tensor(given[i], names[i], like));
+    if (keep[i].scalar_type() != at::kFloat || keep[i].sizes() != x.ids.sizes())
+      refuse(PyExc_ValueError, "%s must be fp32 of the shape of ids", names[i]);
+    at[i] = static_cast<const float*>(keep[i].const_data_ptr());
+  }
+  Tensor out = make(like.sizes(), like.scalar_type(), like);
+  call(like, [&](void* s) {
+    return muon_adamw_token_logprobs_backward(&x.d, at[0], at[1], at[2], at[3], out.mutable_data_ptr(), x.logits.w, s);
+  });
+  return THPVariable_Wrap(std::move(out));
+}
+
+// ---- products grouped by expert ----
+
+struct Expert {
+  Tensor x, weight, offsets;
+  ma_expert_matmul d;
+};
+
+// a: x, weight, offsets
+void read_expert(Expert& r, PyObject* const* a) {
+  r.x = tensor(a[0], "x");
+  need_cuda(r.x);
+  r.weight = tensor(a[1], "weight", r.x);
+  r.offsets = tensor(a[2], "offsets", r.x);
+  const Tensor &x = r.x, &w = r.weight;
+  if (x.dim() != 2 || w.dim() != 3 || w.size(2) != x.size(1))
+    refuse(PyExc_ValueError, "x must be [token, inner] and weight [expert, outer, inner]");
+  if (x.scalar_type() != at::kBFloat16 || w.scalar_type() != at::kBFloat16)
+    refuse(PyExc_TypeError, "x and weight must be bf16");
+  if ((x.size(1) > 1 && x.stride(1) != 1) || (w.size(2) > 1 && w.stride(2) != 1))
+    refuse(PyExc_ValueError, "x and weight must have consecutive elements in a row");
+  if (r.offsets.scalar_type() != at::kInt || r.offsets.dim() != 1 || r.offsets.size(0) != w.size(0) + 1 ||
+      !r.offsets.is_contiguous())
+    refuse(PyExc_ValueError, "offsets must be %lld contiguous int32 values", (long long)w.size(0) + 1);
+  ma_expert_matmul& d = r.d;
+  d.n_tokens = x.size(0);
+  d.n_experts = small(w.size(0));
+  d.inner = small(x.size(1));
+  d.outer = small(w.size(1));
+  d.reserved = 0;
+  d.offsets = static_cast<const int32_t*>(r.offsets.const_data_ptr());
+  d.x = x.const_data_ptr();
+  d.x_stride = x.size(0) > 1 ? x.stride(0) : x.size(1);
+  d.weight = w.const_data_ptr();
+  d.weight_row_stride = w.size(1) > 1 ? w.stride(1) : w.size(2);
+  d.weight_expert_stride = w.size(0) > 1 ? w.stride(0) : w.size(1) * w.size(2);
+}
+
+PyObject* expert_matmul(PyObject* const* a) {
+  Expert x;
+  read_expert(x, a);
+  Tensor out = make({x.x.size(0), x.weight.size(1)}, at::kBFloat16, x.x);
+  call(x.x, [&](void* s) { return muon_adamw_expert_matmul(&x.d, out.mutable_data_ptr(), s); });
+  return THPVariable_Wrap(std::move(out));
+}
+
+// a: dout, x, weight, offsets, grad or None, accumulate, input_grad
+PyObject* expert_matmul_backward(PyObject* const* a) {
+  Expert x;
+  read_expert(x, a + 1);
+  const Tensor& given = tensor(a[0], "dout", x.x);
+  if (given.dim() != 2 || given.size(0) != x.x.size(0) || given.size(1) != x.weight.size(1) ||
+      given.scalar_type() != at::kBFloat16)
+    refuse(PyExc_ValueError, "dout must be bf16 [token, outer]");
+  Rows2 dout = rows_of(given, "dout");
+  // gradients come in layouts of autograd's choice
+  if (dout.stride % 8 || reinterpret_cast<uintptr_t>(dout.t.const_data_ptr()) % 16) {
+    dout.t = given.detach().clone(at::MemoryFormat::Contiguous);
+    dout.stride = dout.w;
+  }
+  const bool acc = truth(a[5]), input = truth(a[6]);
+  Tensor grad, dx;
+  int gdt = MA_DT_BF16;
+  if (a[4] != Py_None) {
+    grad = tensor(a[4], "grad", x.x);
+    gdt = dtype_of(grad, "grad");
+    if (grad.sizes() != x.weight.sizes() || !grad.is_contiguous())
+      refuse(PyExc_ValueError, "grad must be contiguous, of the weight's shape");
+  }
+  if (input) dx = make(x.x.sizes(), at::kBFloat16, x.x);
+  call(x.x, [&](void* s) {
+    return muon_adamw_expert_matmul_backward(&x.d, dout.t.const_data_ptr(), dout.stride,
+                                             input ? dx.mutable_data_ptr() : nullptr,
+                                             grad.defined() ? grad.mutable_data_ptr() : nullptr, gdt, acc, s);
+  });
+  // as any write in place: a graph that saved the tensor is to notice
+  if (grad.defined() && !grad.is_inference()) grad.unsafeGetTensorImpl()->bump_version();
+  return Py_BuildValue("NO", input ? THPVariable_Wrap(std::move(dx)) : Py_NewRef(Py_None), a[4]);
+}
+
 // ---- module ----
 
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
@@ -443,6 +737,16 @@ PyMethodDef g_methods[] = {
     {"window_attention", method<window_attention, 7>(), METH_FASTCALL, "q, k, v, window, sinks, scale, cu_seqlens"},
     {"window_attention_backward", method<window_attention_backward, 10>(), METH_FASTCALL,
      "dout, q, k, v, out, lse, window, sinks, scale, cu_seqlens"},
+    {"dropout", method<dropout, 4>(), METH_FASTCALL, "x, p, rng, site"},
+    {"residual_norm", method<residual_norm, 8>(), METH_FASTCALL, "x, residual, weight, eps, p, rng, site, eight_bit"},
+    {"residual_norm_backward", method<residual_norm_backward, 8>(), METH_FASTCALL,
+     "dy, dres, res, weight, eps, p, rng, site"},
+    {"expert_matmul", method<expert_matmul, 3>(), METH_FASTCALL, "x, weight, offsets"},
+    {"expert_matmul_backward", method<expert_matmul_backward, 7>(), METH_FASTCALL,
+     "dout, x, weight, offsets, grad, accumulate, input_grad"},
+    {"token_logprobs", method<token_logprobs, 4>(), METH_FASTCALL, "logits, ids, scale, top"},
+    {"token_logprobs_backward", method<token_logprobs_backward, 7>(), METH_FASTCALL,
+     "dlogprobs, dentropy, logits, ids, entropy, lse, scale"},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_ops", "The operators over torch tensors.", -1, g_methods,
