@@ -609,9 +609,11 @@ MA_API ma_status muon_adamw_dropout(const void* x, int dtype, int64_t n, double 
  *   dtype         of x, y and their gradients;
  *   stream_dtype  of residual, res and their gradients: dtype, or MA_DT_F32;
  *   width         1 .. 32768;
+ *   eps           a positive normal number in fp32;
  *   residual      NULL: r is dropout(x) alone;
  *   weight        fp32, `width` values.
- * The norm is of r before r is rounded for the stream. Rows of inputs may be
+ * The norm is of r before r is rounded for the stream; its sum of squares is
+ * fp32 (a row whose squares add up to more than 3.4e38 gets y = 0). Rows of inputs may be
  * strided, outputs are contiguous. 16-byte accesses are used where width is a
  * multiple of 8 and all rows start on 16-byte boundaries, single elements
  * otherwise. */

@@ -10,6 +10,7 @@
 // own, which needs no barrier, and a warp's loads are all in flight at once.
 #include <cuda_fp8.h>
 
+#include <cfloat>
 #include <cmath>
 
 #include "residual_norm.cuh"
@@ -156,7 +157,9 @@ ma_status check(const ma_residual_norm* d, const float* weight) {
   if (d->n_tokens < 0 || d->n_tokens > (1ll << 30) || d->width < 1 || d->width > kNormMaxWidth)
     return op_fail(MA_ERR_SHAPE, "%lld tokens of %lld elements: outside [0, 2^30] or [1, %d]", (long long)d->n_tokens,
                    (long long)d->width, kNormMaxWidth);
-  if (!(d->eps >= 0.0) || !std::isfinite(d->eps)) return op_fail(MA_ERR_ARG, "eps = %g", d->eps);
+  // squares below the smallest normal number may be lost: eps, which is at least that, outweighs them
+  if (!((float)d->eps >= FLT_MIN) || !std::isfinite((float)d->eps))
+    return op_fail(MA_ERR_ARG, "eps = %g is no positive normal number in fp32", d->eps);
   DropArgs drop;
   if (!drop_args(d->p, d->rng, d->site, &drop)) return op_fail(MA_ERR_ARG, "p = %g outside [0, 1]", d->p);
   if (drop.threshold) {

@@ -638,7 +638,7 @@ void read_expert(Expert& r, PyObject* const* a) {
     refuse(PyExc_ValueError, "x must be [token, inner] and weight [expert, outer, inner]");
   if (x.scalar_type() != at::kBFloat16 || w.scalar_type() != at::kBFloat16)
     refuse(PyExc_TypeError, "x and weight must be bf16");
-  if ((x.size(1) > 1 && x.stride(1) != 1) || (w.size(2) > 1 && w.stride(2) != 1))
+  if ((x.numel() > 0 && x.size(1) > 1 && x.stride(1) != 1) || (w.numel() > 0 && w.size(2) > 1 && w.stride(2) != 1))
     refuse(PyExc_ValueError, "x and weight must have consecutive elements in a row");
   if (r.offsets.scalar_type() != at::kInt || r.offsets.dim() != 1 || r.offsets.size(0) != w.size(0) + 1 ||
       !r.offsets.is_contiguous())
