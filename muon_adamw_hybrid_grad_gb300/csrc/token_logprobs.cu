@@ -185,14 +185,16 @@ struct Row {
   }
 };
 
+constexpr int kHits = 512;  // groups that reach the threshold
+
 struct TopShared {
   float best[kThreads];
+  uint32_t hits[kHits];
   uint64_t list[2 * kListed];  // above the threshold, then equal to it
   uint64_t chosen[kMaxTop];
   uint64_t warp_best[kThreads / 32];
   int warp_count[kThreads / 32];
-  float threshold;
-  int above, equal;
+  int hit, above, equal;
 };
 
 // The block's `top` first elements of vectors [v0, v1), and of the row's edges
@@ -200,50 +202,73 @@ struct TopShared {
 template <typename T>
 __device__ void choose_top(const Row<T>& row, int v0, int v1, bool edges, int top, float best, const float* groups,
                            TopShared& sh) {
-  const int t = threadIdx.x;
+  const int t = threadIdx.x, lane = t & 31;
   sh.best[t] = best;
   if (t < kMaxTop) sh.chosen[t] = 0;
-  if (t == 0) sh.above = sh.equal = 0;
+  if (t == 0) sh.hit = sh.above = sh.equal = 0;
   __syncthreads();
+  // the threshold: the top-th largest of 32 maxima, each of the threads of one lane. It is met by as many elements
+  // as are wanted; with fewer lanes that hold any it is -infinity, and everything is a candidate
+  float mine = sh.best[lane];
+#pragma unroll
+  for (int i = 1; i < kThreads / 32; ++i) mine = fmaxf(mine, sh.best[i * 32 + lane]);
   int rank = 0;
-#pragma unroll 16
-  for (int i = 0; i < kThreads; ++i) {
-    const float b = sh.best[i];
-    rank += b > best || (b == best && i < t);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float b = __shfl_sync(0xffffffffu, mine, i);
+    rank += b > mine || (b == mine && i < lane);
   }
-  if (rank == top - 1) sh.threshold = best;
-  __syncthreads();
-  const float limit = sh.threshold;
+  const float limit = __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, rank == top - 1)) - 1);
   const uint32_t limit_bits = rank_bits(limit);
+  const bool everything = limit == -INFINITY;
   auto offer = [&](float x, int index) {
+    if (!(x >= limit) && !everything) return;
     const uint64_t key = rank_key(x, (uint32_t)index);
-    const uint32_t bits = (uint32_t)(key >> 32);
-    if (bits > limit_bits) {
+    if ((uint32_t)(key >> 32) > limit_bits) {
       const int at = atomicAdd(&sh.above, 1);
       if (at < kListed) sh.list[at] = key;
-    } else if (bits == limit_bits) {
+    } else {
       const int at = atomicAdd(&sh.equal, 1);
       if (at < kListed) sh.list[kListed + at] = key;
     }
+  };
+  auto of_vector = [&](int vec, auto&& f) {
+    float x[8];
+    load8(row.p + row.index(vec), x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f(x[e], row.index(vec) + e);
   };
   // every element of this thread whose group reaches the threshold
   auto each = [&](auto&& f) {
     int g = t;
     for (int v = v0; v < v1; v += kStep, g += kThreads) {
-      const float m = groups[g];
-      if (m < limit) continue;
-      for (int j = 0; j < kVecs; ++j) {
-        const int vec = v + j * kThreads + t;
-        if (vec >= v1) break;
-        float x[8];
-        load8(row.p + row.index(vec), x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f(x[e], row.index(vec) + e);
-      }
+      if (groups[g] < limit) continue;
+      for (int j = 0; j < kVecs; ++j)
+        if (v + j * kThreads + t < v1) of_vector(v + j * kThreads + t, f);
     }
     if (edges && row.edge(t) >= 0) f(load1(row.p + row.edge(t)), row.edge(t));
   };
-  each(offer);
+  // the groups that reach it, and then their vectors shared out over all threads
+  if (best >= limit) {
+    int g = t;
+    for (int v = v0; v < v1; v += kStep, g += kThreads)
+      if (!(groups[g] < limit)) {
+        const int at = atomicAdd(&sh.hit, 1);
+        if (at < kHits) sh.hits[at] = (uint32_t)g;
+      }
+  }
+  __syncthreads();
+  const int hit = sh.hit;
+  if (hit > kHits) {
+    each(offer);
+  } else {
+    for (int i = t; i < hit * kVecs; i += kThreads) {
+      const int g = (int)sh.hits[i / kVecs];
+      const int vec = v0 + g / kThreads * kStep + i % kVecs * kThreads + g % kThreads;
+      if (vec < v1) of_vector(vec, offer);
+    }
+    if (edges && row.edge(t) >= 0) offer(load1(row.p + row.edge(t)), row.edge(t));
+  }
   __syncthreads();
   int above = sh.above, equal = sh.equal;
   if (above > kListed) {
@@ -441,18 +466,19 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
       }
       if constexpr (TOP) {
         const uint32_t lists = smem_u32(sh.chosen);
-        const int i = t / kMaxTop;  // one key a thread
-        sh.list[t] = i < a.parts && t % kMaxTop < a.top ? ld_cluster_u64(mapa_shared(lists, i) + 8 * (t % kMaxTop)) : 0;
+        if (t < a.parts * a.top) sh.list[t] = ld_cluster_u64(mapa_shared(lists, t / a.top) + 8 * (t % a.top));
       }
     }
     cluster_sync();
     if (part != 0) return;
     if constexpr (TOP) {
-      const uint64_t key = sh.list[t];
-      int r = 0;
-#pragma unroll 16
-      for (int i = 0; i < kThreads; ++i) r += sh.list[i] > key;
-      if (key != 0 && r < a.top) sh.chosen[r] = key;
+      if (t < a.parts * a.top) {
+        const uint64_t key = sh.list[t];
+        int r = 0;
+#pragma unroll 8
+        for (int i = 0; i < a.parts * a.top; ++i) r += sh.list[i] > key;
+        if (key != 0 && r < a.top) sh.chosen[r] = key;
+      }
       __syncthreads();
     }
   }
