@@ -23,14 +23,15 @@ struct DropArgs {
 namespace {
 
 struct DropKey {
-  uint32_t k0, k1, site, step0, step1, threshold;
+  uint32_t k0, k1, site, step0, step1;
+  uint32_t threshold2;  // the threshold in both halves
   float factor;
 };
 
 __device__ __forceinline__ DropKey drop_key(const DropArgs& a) {
   const uint64_t seed = (uint64_t)__ldg(a.rng), step = (uint64_t)__ldg(a.rng + 1);
-  return {(uint32_t)seed, (uint32_t)(seed >> 32), a.site,  (uint32_t)step,
-          (uint32_t)(step >> 32), a.threshold, a.factor};
+  return {(uint32_t)seed, (uint32_t)(seed >> 32), a.site, (uint32_t)step, (uint32_t)(step >> 32), a.threshold * 0x10001u,
+          a.factor};
 }
 
 __device__ __forceinline__ uint4 philox(uint4 c, uint32_t k0, uint32_t k1) {
@@ -44,15 +45,26 @@ __device__ __forceinline__ uint4 philox(uint4 c, uint32_t k0, uint32_t k1) {
   return c;
 }
 
-// The eight elements of group `group`. Dropped ones become 0 whatever they hold.
-__device__ __forceinline__ void drop8(const DropKey& k, uint32_t group, float (&x)[8]) {
-  const uint4 r = philox(make_uint4(group, k.site, k.step0, k.step1), k.k0, k.k1);
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// Eight elements by their bits, four words of them. Dropped ones become 0 whatever they hold.
+__device__ __forceinline__ void drop8_by(const DropKey& k, const uint32_t (&w)[4], float (&x)[8]) {
+  if (k.factor == 0.f) {  // p = 1, whose threshold no 16 bits reach
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = (w[i] & 0xFFFFu) >= k.threshold ? x[2 * i] * k.factor : 0.f;
-    x[2 * i + 1] = (w[i] >> 16) >= k.threshold ? x[2 * i + 1] * k.factor : 0.f;
+    bool low, high;  // both halves compared by one instruction
+    __vibmax_u16x2(w[i], k.threshold2, &high, &low);
+    x[2 * i] = low ? x[2 * i] * k.factor : 0.f;
+    x[2 * i + 1] = high ? x[2 * i + 1] * k.factor : 0.f;
   }
+}
+
+// The eight elements of group `group`.
+__device__ __forceinline__ void drop8(const DropKey& k, uint32_t group, float (&x)[8]) {
+  const uint4 r = philox(make_uint4(group, k.site, k.step0, k.step1), k.k0, k.k1);
+  drop8_by(k, {r.x, r.y, r.z, r.w}, x);
 }
 
 }  // namespace

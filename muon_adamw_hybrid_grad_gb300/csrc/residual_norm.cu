@@ -6,8 +6,8 @@
 // and the norm is of r in fp32, before r is rounded for the stream. With 8 bits
 // a second reduction finds the row's largest |y|.
 //
-// Bound by HBM: two rows in, two out. Rows of up to 2048 elements are a warp's
-// own, which needs no barrier, and a warp's loads are all in flight at once.
+// Bound by HBM: two rows in, two out. Rows of up to 1024 elements are a warp's
+// own, which needs no barrier, and a thread's loads are all in flight at once.
 #include <cuda_fp8.h>
 
 #include <cfloat>
@@ -22,7 +22,7 @@ constexpr int kMinThreads = 128;
 
 template <int T>
 struct RowThreads {
-  static constexpr int kBlock = T < kMinThreads ? kMinThreads : T;
+  static constexpr int kBlock = T == 32 ? kMinThreads : T;
   static constexpr int kRows = kBlock / T;
   static_assert(T == 32 || kRows == 1, "several warps share a row: one row to a block");
 };
@@ -137,12 +137,16 @@ cudaError_t forward(const NormArgs& a, bool vec, cudaStream_t st) {
     if (units <= 128 * 8) return launch<TX, TS, 128, 8, false>(a, st);
     return launch<TX, TS, 512, 8, false>(a, st);
   }
+  // Two to four vectors a thread: enough loads in flight, and warps enough to hide the generator. 64M elements of bf16
+  // without and with dropout: width 2048 with (threads, vectors) = (32, 8) 79 and 102 us, (128, 2) 78 and 87, (256, 1)
+  // 77 and 94; 1024 with (32, 4) 78 and 79, (64, 2) 77 and 85; 8192 with (128, 8) 86, (256, 4) 81 and 96, (512, 2) 94
+  // and 110; 16384 with (256, 8) 111 and 162, (512, 4) 102 and 140, (1024, 2) 105 and 134.
   if (units <= 32) return launch<TX, TS, 32, 1, true>(a, st);
   if (units <= 64) return launch<TX, TS, 32, 2, true>(a, st);
   if (units <= 128) return launch<TX, TS, 32, 4, true>(a, st);
-  if (units <= 256) return launch<TX, TS, 32, 8, true>(a, st);
+  if (units <= 256) return launch<TX, TS, 128, 2, true>(a, st);
   if (units <= 512) return launch<TX, TS, 128, 4, true>(a, st);
-  if (units <= 1024) return launch<TX, TS, 128, 8, true>(a, st);
+  if (units <= 1024) return launch<TX, TS, 256, 4, true>(a, st);
   if (units <= 2048) return launch<TX, TS, 512, 4, true>(a, st);
   return launch<TX, TS, 512, 8, true>(a, st);
 }

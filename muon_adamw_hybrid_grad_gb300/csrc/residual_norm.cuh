@@ -98,19 +98,23 @@ __device__ __forceinline__ void drop8_at(const DropKey& k, int64_t at, float (&x
     drop8(k, group, x);
     return;
   }
-  // the end of one group and the beginning of the next
+  // the end of one group and the beginning of the next, the same shift for a whole row
   const uint4 a = philox(make_uint4(group, k.site, k.step0, k.step1), k.k0, k.k1);
   const uint4 b = philox(make_uint4(group + 1, k.site, k.step0, k.step1), k.k0, k.k1);
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  const int s = (int)(at & 7);
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (at & 4) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    uint32_t bits = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i == s + e) bits = w[i / 2] >> (16 * (i & 1)) & 0xFFFFu;
-    x[e] = bits >= k.threshold ? x[e] * k.factor : 0.f;
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
   }
+  if (at & 2) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  if (at & 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  }
+  drop8_by(k, {w[0], w[1], w[2], w[3]}, x);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {

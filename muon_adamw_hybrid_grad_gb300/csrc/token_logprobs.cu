@@ -29,11 +29,13 @@
 namespace ma {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kVecs = 4;  // vectors of eight elements in a group
 constexpr int kStep = kThreads * kVecs;  // vectors of a block's pass
+constexpr int kGradThreads = 256;
+constexpr int kGradStep = kGradThreads * kVecs;
 constexpr int kMaxTop = 32;
-constexpr int kListed = 1024;  // candidates above the threshold, and as many that equal it
+constexpr int kListed = 512;  // candidates above the threshold, and as many that equal it
 constexpr int kMaxVocab = 1 << 20;
 constexpr int kMaxParts = 8;
 constexpr int kMaxGroupBytes = (kMaxVocab / (kStep * 8) + 1) * kThreads * 4;
@@ -200,7 +202,7 @@ struct TopShared {
 // The block's `top` first elements of vectors [v0, v1), and of the row's edges
 // with `edges`, into sh.chosen in their order; 0 where there are fewer.
 template <typename T>
-__device__ void choose_top(const Row<T>& row, int v0, int v1, bool edges, int top, float best, const float* groups,
+__device__ void choose_top(const Row<T>& row, int v0, int v1, bool edges, int top, float best, const T* groups,
                            TopShared& sh) {
   const int t = threadIdx.x, lane = t & 31;
   sh.best[t] = best;
@@ -242,7 +244,7 @@ __device__ void choose_top(const Row<T>& row, int v0, int v1, bool edges, int to
   auto each = [&](auto&& f) {
     int g = t;
     for (int v = v0; v < v1; v += kStep, g += kThreads) {
-      if (groups[g] < limit) continue;
+      if (load1(groups + g) < limit) continue;
       for (int j = 0; j < kVecs; ++j)
         if (v + j * kThreads + t < v1) of_vector(v + j * kThreads + t, f);
     }
@@ -252,7 +254,7 @@ __device__ void choose_top(const Row<T>& row, int v0, int v1, bool edges, int to
   if (best >= limit) {
     int g = t;
     for (int v = v0; v < v1; v += kStep, g += kThreads)
-      if (!(groups[g] < limit)) {
+      if (!(load1(groups + g) < limit)) {
         const int at = atomicAdd(&sh.hit, 1);
         if (at < kHits) sh.hits[at] = (uint32_t)g;
       }
@@ -379,7 +381,8 @@ struct Running {
 
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
-  extern __shared__ float groups[];  // TOP: the maximum of every thread's groups
+  extern __shared__ uint8_t shared[];
+  T* const groups = reinterpret_cast<T*>(shared);  // TOP: the maximum of every thread's groups
   __shared__ Sums warp_sums[kThreads / 32];
   __shared__ Sums part_sums;
   __shared__ TopShared sh;
@@ -423,7 +426,7 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
     if (v + kStep < v1) fetch(v + kStep);
     const float gm = group_max(cur);
     if (TOP) {
-      groups[g] = gm;
+      store1(groups + g, gm);  // as it was read: nothing is rounded
       best = fmaxf(best, gm);
     }
     if (!(gm <= run.m)) run.raise(gm, c);
@@ -466,14 +469,15 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
       }
       if constexpr (TOP) {
         const uint32_t lists = smem_u32(sh.chosen);
-        if (t < a.parts * a.top) sh.list[t] = ld_cluster_u64(mapa_shared(lists, t / a.top) + 8 * (t % a.top));
+        for (int i = t; i < a.parts * a.top; i += kThreads)
+          sh.list[i] = ld_cluster_u64(mapa_shared(lists, i / a.top) + 8 * (i % a.top));
       }
     }
     cluster_sync();
     if (part != 0) return;
     if constexpr (TOP) {
-      if (t < a.parts * a.top) {
-        const uint64_t key = sh.list[t];
+      for (int k = t; k < a.parts * a.top; k += kThreads) {
+        const uint64_t key = sh.list[k];
         int r = 0;
 #pragma unroll 8
         for (int i = 0; i < a.parts * a.top; ++i) r += sh.list[i] > key;
@@ -528,7 +532,7 @@ __device__ __forceinline__ float grad_of(const GradRow& g, float x) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) token_logprobs_grad_kernel(const __grid_constant__ LogprobArgs a) {
+__global__ void __launch_bounds__(kGradThreads) token_logprobs_grad_kernel(const __grid_constant__ LogprobArgs a) {
   const int t = threadIdx.x;
   const int64_t at = blockIdx.x / a.parts;
   const int part = (int)(blockIdx.x - at * a.parts);
@@ -542,21 +546,21 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_grad_kernel(const __g
   if (((reinterpret_cast<uintptr_t>(row.p) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0) {
     // rows that lie differently: no boundary is both's
     const GradRow g = grad_row(a, at);
-    const int end = min(a.vocab, (part + 1) * kStep * 8);
-    for (int i = part * kStep * 8 + t; i < end; i += kThreads) single(g, i);
+    const int end = min(a.vocab, (part + 1) * kGradStep * 8);
+    for (int i = part * kGradStep * 8 + t; i < end; i += kGradThreads) single(g, i);
     return;
   }
-  const int v0 = part * kStep;
+  const int v0 = part * kGradStep;
   RawVec<T, 8> raw[kVecs];
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
-    const int vec = v0 + j * kThreads + t;
+    const int vec = v0 + j * kGradThreads + t;
     if (vec < row.vecs) raw[j].load(row.p + row.index(vec));
   }
   const GradRow g = grad_row(a, at);
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
-    const int vec = v0 + j * kThreads + t;
+    const int vec = v0 + j * kGradThreads + t;
     if (vec >= row.vecs) break;
     const int i = row.index(vec);
     float x[8];
@@ -581,7 +585,7 @@ ma_status check(const ma_token_logprobs* d) {
     return op_fail(MA_ERR_SHAPE, "%lld tokens of %lld logits: outside [0, 2^30] or [1, 2^20]", (long long)d->n_tokens,
                    (long long)d->vocab);
   // the gradient's blocks of 8192 logits, and a cluster's, are numbered in 31 bits
-  const int64_t parts = std::max<int64_t>((d->vocab + kStep * 8 - 1) / (kStep * 8), 1);
+  const int64_t parts = std::max<int64_t>((d->vocab + kGradStep * 8 - 1) / (kGradStep * 8), 1);
   if (d->n_tokens * parts > INT32_MAX)
     return op_fail(MA_ERR_SHAPE, "%lld tokens of %lld logits are too many for a call", (long long)d->n_tokens,
                    (long long)d->vocab);
@@ -615,14 +619,17 @@ cudaError_t forward(LogprobArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   a.parts = 1;
   const int64_t steps = (a.vocab / 8 + kStep - 1) / kStep;
-  while (a.parts < kMaxParts && a.n * a.parts < sms && steps >= 2 * a.parts) a.parts *= 2;
+  // A cluster to a row where blocks would be few; the larger the clusters, the slower they are dispatched. Times with
+  // 1, 2, 4, 8 blocks a row of 151936 (no alternatives): 1 row 13.9, 8.9, 6.5, 5.1 us; 64 rows 14.1, 9.0, 7.4, 7.6;
+  // 150 rows 14.1, 10.6, 17.1, 13.6; 300 rows 22.2, 17.5, 21.5, 23.4; 900 rows 62, 58, 56, 64.
+  for (int k = 4; a.parts < kMaxParts && 2 * a.parts * a.n <= (int64_t)k * sms && steps >= 2 * a.parts; --k) a.parts *= 2;
   const int64_t per = (steps + a.parts - 1) / a.parts;
   if (TOP) {
     e = op_smem_limit<token_logprobs_kernel<T, TOP>>(kMaxGroupBytes);
     if (e != cudaSuccess) return e;
   }
   return op_launch(token_logprobs_kernel<T, TOP>, dim3((unsigned)(a.n * a.parts)), dim3(kThreads),
-                   TOP ? (size_t)std::max<int64_t>(per, 1) * kThreads * 4 : 0, st, a.parts, a);
+                   TOP ? (size_t)std::max<int64_t>(per, 1) * kThreads * sizeof(T) : 0, st, a.parts, a);
 }
 
 }  // namespace
@@ -681,12 +688,12 @@ ma_status muon_adamw_token_logprobs_backward(const ma_token_logprobs* d, const f
     a.lse_in = lse;
     a.dlogits = dlogits;
     a.out_stride = dlogits_stride;
-    a.parts = std::max((a.vocab + kStep * 8 - 1) / (kStep * 8), 1);
+    a.parts = std::max((a.vocab + kGradStep * 8 - 1) / (kGradStep * 8), 1);
     const dim3 grid((unsigned)(a.n * a.parts));
     const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     const cudaError_t e = d->dtype == MA_DT_BF16
-                              ? op_launch(token_logprobs_grad_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, s, 1, a)
-                              : op_launch(token_logprobs_grad_kernel<float>, grid, dim3(kThreads), 0, s, 1, a);
+                              ? op_launch(token_logprobs_grad_kernel<__nv_bfloat16>, grid, dim3(kGradThreads), 0, s, 1, a)
+                              : op_launch(token_logprobs_grad_kernel<float>, grid, dim3(kGradThreads), 0, s, 1, a);
     if (e != cudaSuccess) return op_cuda(e, "log probabilities gradient launch");
   }
   clear_last_error();
