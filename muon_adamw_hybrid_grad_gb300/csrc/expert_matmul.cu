@@ -80,6 +80,32 @@ struct Layout {
   static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
+// Everything below is issued by a converged warp, and the instructions elect the
+// thread: addresses stay warp-uniform, as the instructions take them. From a
+// branch of one lane a block's two copies took 360 cycles to issue, and bound
+// small tiles.
+
+// The four steps of a block, KA and KB further in the operands' descriptors each.
+template <int KA, int KB>
+__device__ __forceinline__ void umma_block_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  static_assert(kBlock == 64, "four steps of 16");
+  asm volatile(
+      "{\n\t.reg .pred p, q, t;\n\t"
+      ".reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "add.s64 a1, %1, %5;\n\tadd.s64 a2, %1, %6;\n\tadd.s64 a3, %1, %7;\n\t"
+      "add.s64 b1, %2, %8;\n\tadd.s64 b2, %2, %9;\n\tadd.s64 b3, %2, %10;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, t;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, t;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, t;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "n"(KA), "n"(2 * KA), "n"(3 * KA), "n"(KB), "n"(2 * KB),
+      "n"(3 * KB)
+      : "memory");
+}
 __device__ __forceinline__ void umma_pair_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                uint32_t accumulate) {
   asm volatile(
@@ -91,13 +117,13 @@ __device__ __forceinline__ void umma_pair_warp(uint32_t d_tmem, uint64_t adesc, 
       : "memory");
 }
 // The products issued so far have ended: one arrival in each CTA of the pair.
-__device__ __forceinline__ void commit_pair_warp(uint32_t bar) {
+__device__ __forceinline__ void commit_pair_warp(uint32_t bar, uint32_t odd_bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
       "elect.sync _|q, 0xffffffff;\n\t"
       "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t"
       "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}\n" ::"r"(bar),
-      "r"(mapa_shared(bar, 1))
+      "r"(odd_bar)
       : "memory");
 }
 __device__ __forceinline__ void commit_own_warp(uint32_t bar) {
@@ -113,12 +139,30 @@ __device__ __forceinline__ bool mbar_wait_warp_cluster(uint32_t bar, uint32_t pa
   if (__all_sync(0xffffffffu, mbar_try_wait<true>(bar, parity))) return true;
   return __all_sync(0xffffffffu, mbar_wait_loop<true>(bar, parity, abort_flag, err, code));
 }
-// A copy into this CTA that counts on barrier `bar` of the pair's even CTA.
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* tm, int x, int y, int z,
-                                                 uint32_t bar) {
+__device__ __forceinline__ void expect_warp(uint32_t bar, uint32_t bytes) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}\n" ::"r"(bar),
+      "r"(bytes)
+      : "memory");
+}
+__device__ __forceinline__ void load_warp(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];\n\t}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// A copy into this CTA that counts on barrier `bar` of the pair's even CTA, a cluster address.
+__device__ __forceinline__ void load_pair_warp(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %4}], [%5];\n\t}\n" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
@@ -360,61 +404,59 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
   int expert = 0;
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---- loads ----
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int pos = pos0; pos < tab.units && ok; pos += step) {
-        const Unit u = unit_at<MODE>(a, tab, pos, expert);
-        const uint32_t bytes = stage_bytes<MODE>(u);
-        for (int b = 0; b < u.blocks; ++b) {
-          if (!mbar_wait(empty + 8 * stage, phase ^ 1u, abort_flag, a.err, kErrLoad)) {
-            ok = false;
-            break;
-          }
-          const uint32_t at = smem_u32(smem) + (uint32_t)(stage * kStage), bar = full + 8 * stage;
-          if (MODE == kWeights && b == u.blocks - 1 && u.count % kBlock != 0) {
-            // rows of the next expert in it: lands on a barrier of this CTA's, and is cleared before it is full
-            mbar_expect_tx(tail + 8 * stage, bytes);
-            load_block<MODE>(a, u, b, at, rank, [&](uint32_t dst, const CUtensorMap* tm, int x, int y, int z) {
-              tma_load_3d(dst, tm, x, y, z, tail + 8 * stage);
-            });
-          } else if (rank == 0) {
-            mbar_expect_tx(bar, 2 * bytes);
-            load_block<MODE>(a, u, b, at, rank, [&](uint32_t dst, const CUtensorMap* tm, int x, int y, int z) {
-              tma_load_3d(dst, tm, x, y, z, bar);
-            });
-          } else {
-            load_block<MODE>(a, u, b, at, rank, [&](uint32_t dst, const CUtensorMap* tm, int x, int y, int z) {
-              tma_load_3d_pair(dst, tm, x, y, z, mapa_shared(bar, 0));
-            });
-          }
-          ++issued;
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
-          }
+    // ---- loads ----
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    const uint32_t s0 = smem_u32(smem), full_pair = mapa_shared(full, 0);
+    for (int pos = pos0; pos < tab.units && ok; pos += step) {
+      const Unit u = unit_at<MODE>(a, tab, pos, expert);
+      const uint32_t bytes = stage_bytes<MODE>(u);
+      for (int b = 0; b < u.blocks; ++b) {
+        if (!mbar_wait_warp(empty + 8 * stage, phase ^ 1u, abort_flag, a.err, kErrLoad)) {
+          ok = false;
+          break;
         }
-      }
-      // copies in flight land before the CTA leaves: those of the odd CTA count on the even one's barriers
-      if (rank == 0) {
-        for (int i = 0; i < min(issued, S); ++i) {
-          if (--stage < 0) {
-            stage = S - 1;
-            phase ^= 1u;
-          }
-          drain_wait(full + 8 * stage, phase);
+        const uint32_t at = s0 + (uint32_t)(stage * kStage);
+        if (MODE == kWeights && b == u.blocks - 1 && u.count % kBlock != 0) {
+          // rows of the next expert in it: lands on a barrier of this CTA's, and is cleared before it is full
+          const uint32_t bar = tail + 8 * stage;
+          expect_warp(bar, bytes);
+          load_block<MODE>(a, u, b, at, rank, [&](uint32_t dst, const CUtensorMap* tm, int x, int y, int z) {
+            load_warp(dst, tm, x, y, z, bar);
+          });
+        } else {
+          if (rank == 0) expect_warp(full + 8 * stage, 2 * bytes);
+          const uint32_t bar = full_pair + 8 * stage;
+          load_block<MODE>(a, u, b, at, rank, [&](uint32_t dst, const CUtensorMap* tm, int x, int y, int z) {
+            load_pair_warp(dst, tm, x, y, z, bar);
+          });
+        }
+        ++issued;
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
     }
+    // copies in flight land before the CTA leaves: those of the odd CTA count on the even one's barriers
+    if (rank == 0) {
+      for (int i = 0; i < min(issued, S); ++i) {
+        if (--stage < 0) {
+          stage = S - 1;
+          phase ^= 1u;
+        }
+        drain_wait(full + 8 * stage, phase);
+      }
+    }
+    __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {
       // ---- products ----
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      const uint32_t s0 = smem_u32(smem);
+      const uint32_t s0 = smem_u32(smem), empty_odd = mapa_shared(empty, 1);
       // MN-major: panels of 64 columns, sixteen rows of the contraction 2 KB further
       const uint64_t a0 = MODE == kForward ? sdesc(s0, 16, 1024) : sdesc(s0, kPanel, 1024);
       const uint64_t b0 = MODE == kWeights ? sdesc(s0 + kOperand, kPanel, 1024) : sdesc(s0 + kOperand, 16, 1024);
@@ -434,18 +476,21 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
           tc_fence_after();
           const uint32_t off = (uint32_t)stage * (uint32_t)(kStage >> 4);
           const int left = MODE == kWeights ? u.count - b * kBlock : kBlock;
-#pragma unroll
-          for (int i = 0; i < kBlock / 16; ++i)
-            if (i * 16 < left)
-              umma_pair_warp(d, a0 + off + kStepA * i, b0 + off + kStepB * i, idesc, (b | i) != 0 ? 1u : 0u);
-          commit_pair_warp(empty + 8 * stage);
+          const uint64_t ad = a0 + off, bd = b0 + off;
+          if (MODE != kWeights || left > kBlock - 16) {
+            umma_block_warp<kStepA, kStepB>(d, ad, bd, idesc, b != 0 ? 1u : 0u);
+          } else {
+            for (int i = 0; i * 16 < left; ++i)
+              umma_pair_warp(d, ad + kStepA * i, bd + kStepB * i, idesc, (b | i) != 0 ? 1u : 0u);
+          }
+          commit_pair_warp(empty + 8 * stage, empty_odd + 8 * stage);
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        commit_pair_warp(acc_full + 8 * acc);
+        commit_pair_warp(acc_full + 8 * acc, mapa_shared(acc_full + 8 * acc, 1));
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
