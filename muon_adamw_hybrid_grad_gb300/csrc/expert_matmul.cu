@@ -17,7 +17,8 @@
 // half of the right one, 32 KB a block of 64, which is what the L2 delivers to
 // an SM in the 512 cycles of the block's products; with a CTA for itself it
 // would be 48 KB.
-//   warp 0     TMA loads into a ring of six stages (five with fp32 gradients)
+//   warps 0, 11  TMA loads of the left and of the right operand into a ring of
+//              six stages (five with fp32 gradients)
 //   warp 1     products, issued by the even CTA; two accumulators of 256 columns
 //   warps 2-9  results from TMEM: rounded, transposed where tokens are columns,
 //              out through shared memory and TMA; tiles with other experts'
@@ -41,11 +42,11 @@ namespace {
 constexpr int kTile = 256;       // M of a pair, and the most N
 constexpr int kHalf = kTile / 2;
 constexpr int kBlock = 64;       // of the contraction
-constexpr int kSmallBox = 16;    // rows of the copies of a token tile below 256
+constexpr int kMidBox = 64, kSmallBox = 16;  // rows of the copies of smaller token tiles
 constexpr int kOperand = kHalf * kBlock * 2;  // 16 KB: a CTA's part of one operand in a stage
 constexpr int kStage = 2 * kOperand;
 constexpr int kPanel = kBlock * 64 * 2;  // MN-major: 64 columns of a block's 64 rows
-constexpr int kWarps = 11;
+constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStoreWarps = 8;
 constexpr int kMaxExperts = 1024;
@@ -58,7 +59,7 @@ enum Mode { kForward, kInput, kWeights };
 constexpr int kErrLoad = 0x501, kErrProduct = 0x502, kErrStore = 0x503, kErrClear = 0x504;
 
 struct ExpertArgs {
-  CUtensorMap a, b, b_small, out;
+  CUtensorMap a, b, b_mid, b_small, out;
   const int32_t* offsets;
   int tokens, experts;
   int m, n, k;  // forward: outer, -, inner; input: inner, -, outer; weights: outer, inner, -
@@ -217,32 +218,46 @@ __device__ __forceinline__ Unit unit_at(const ExpertArgs& a, const Table& tab, i
   return u;
 }
 
+// Rows of a token tile's copies into a CTA: its half of the tile, or more where one copy beats several.
+__device__ __forceinline__ int token_rows(const Unit& u) {
+  const int half = u.n / 2;
+  return half <= 2 * kSmallBox ? half : half <= kMidBox ? kMidBox : kHalf;
+}
+
 // Bytes that land in a CTA for one block.
 template <int MODE>
 __device__ __forceinline__ uint32_t stage_bytes(const Unit& u) {
-  return (uint32_t)(kOperand + (MODE == kWeights ? u.n / 2 / 64 * kPanel : u.n / 2 * kBlock * 2));
+  return (uint32_t)(kOperand + (MODE == kWeights ? u.n / 2 / 64 * kPanel : token_rows(u) * kBlock * 2));
 }
 
 template <int MODE, typename LOAD>
-__device__ __forceinline__ void load_block(const ExpertArgs& a, const Unit& u, int block, uint32_t stage, uint32_t rank,
-                                           LOAD load) {
+__device__ __forceinline__ void load_left(const ExpertArgs& a, const Unit& u, int block, uint32_t stage, uint32_t rank,
+                                          LOAD load) {
   const int k0 = block * kBlock, m0 = u.m0 + (int)rank * kHalf;
-  const uint32_t sb = stage + kOperand;
   if constexpr (MODE == kForward) {
     load(stage, &a.a, k0, m0, u.expert);
   } else {
     for (int p = 0; p < kHalf / 64; ++p)
       load(stage + p * kPanel, &a.a, m0 + p * 64, MODE == kInput ? k0 : u.at + k0, MODE == kInput ? u.expert : 0);
   }
+}
+
+template <int MODE, typename LOAD>
+__device__ __forceinline__ void load_right(const ExpertArgs& a, const Unit& u, int block, uint32_t stage, uint32_t rank,
+                                           LOAD load) {
+  const int k0 = block * kBlock;
+  const uint32_t sb = stage + kOperand;
   if constexpr (MODE == kWeights) {
     const int n0 = u.n0 + (int)rank * (u.n / 2);
-    for (int p = 0; p < u.n / 2 / 64; ++p) load(sb + p * kPanel, &a.b, n0 + p * 64, u.at + k0, 0);
+    load(sb, &a.b, n0, u.at + k0, 0);
+    if (u.n == kTile) load(sb + kPanel, &a.b, n0 + 64, u.at + k0, 0);
   } else {
-    const int t0 = u.at + (int)rank * (u.n / 2);
-    if (u.n == kTile) {
-      load(sb, &a.b, k0, t0, 0);
+    const int t0 = u.at + (int)rank * (u.n / 2), rows = token_rows(u);
+    if (rows > 2 * kSmallBox) {
+      load(sb, rows == kHalf ? &a.b : &a.b_mid, k0, t0, 0);
     } else {
-      for (int p = 0; p < u.n / 2; p += kSmallBox) load(sb + p * kBlock * 2, &a.b_small, k0, t0 + p, 0);
+      load(sb, &a.b_small, k0, t0, 0);
+      if (rows > kSmallBox) load(sb + kSmallBox * kBlock * 2, &a.b_small, k0, t0 + kSmallBox, 0);
     }
   }
 }
@@ -403,8 +418,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
                   MODE == kWeights ? a.experts * ceil_div(a.m, kTile) * ceil_div(a.n, kTile) : first[a.experts + 1]};
   int expert = 0;
 
-  if (warp == 0) {
-    // ---- loads ----
+  if (warp == 0 || warp == kWarps - 1) {
+    // ---- loads, a warp for each operand: issuing a copy takes some 100 cycles ----
+    const bool left = warp == 0;
     int stage = 0, issued = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -421,16 +437,24 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
         if (MODE == kWeights && b == u.blocks - 1 && u.count % kBlock != 0) {
           // rows of the next expert in it: lands on a barrier of this CTA's, and is cleared before it is full
           const uint32_t bar = tail + 8 * stage;
-          expect_warp(bar, bytes);
-          load_block<MODE>(a, u, b, at, rank, [&](uint32_t dst, const CUtensorMap* tm, int x, int y, int z) {
-            load_warp(dst, tm, x, y, z, bar);
-          });
+          auto load = [&](uint32_t dst, const CUtensorMap* tm, int x, int y, int z) { load_warp(dst, tm, x, y, z, bar); };
+          if (left) {
+            expect_warp(bar, bytes);
+            load_left<MODE>(a, u, b, at, rank, load);
+          } else {
+            load_right<MODE>(a, u, b, at, rank, load);
+          }
         } else {
-          if (rank == 0) expect_warp(full + 8 * stage, 2 * bytes);
           const uint32_t bar = full_pair + 8 * stage;
-          load_block<MODE>(a, u, b, at, rank, [&](uint32_t dst, const CUtensorMap* tm, int x, int y, int z) {
+          auto load = [&](uint32_t dst, const CUtensorMap* tm, int x, int y, int z) {
             load_pair_warp(dst, tm, x, y, z, bar);
-          });
+          };
+          if (left) {
+            if (rank == 0) expect_warp(full + 8 * stage, 2 * bytes);
+            load_left<MODE>(a, u, b, at, rank, load);
+          } else {
+            load_right<MODE>(a, u, b, at, rank, load);
+          }
         }
         ++issued;
         if (++stage == S) {
@@ -440,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
       }
     }
     // copies in flight land before the CTA leaves: those of the odd CTA count on the even one's barriers
-    if (rank == 0) {
+    if (left && rank == 0) {
       for (int i = 0; i < min(issued, S); ++i) {
         if (--stage < 0) {
           stage = S - 1;
@@ -693,6 +717,7 @@ ma_status muon_adamw_expert_matmul(const ma_expert_matmul* d, void* out, void* c
     if (!map3(&a.a, d->weight, false, d->inner, d->outer, d->n_experts, d->weight_row_stride, d->weight_expert_stride,
               kBlock, kHalf, kWide) ||
         !map3(&a.b, d->x, false, d->inner, d->n_tokens, 1, d->x_stride, 0, kBlock, kHalf, kWide) ||
+        !map3(&a.b_mid, d->x, false, d->inner, d->n_tokens, 1, d->x_stride, 0, kBlock, kMidBox, kWide) ||
         !map3(&a.b_small, d->x, false, d->inner, d->n_tokens, 1, d->x_stride, 0, kBlock, kSmallBox, kWide) ||
         !map2(&a.out, out, d->outer, d->n_tokens, 32, 32, kNarrow))
       return refused_map();
@@ -728,6 +753,7 @@ ma_status muon_adamw_expert_matmul_backward(const ma_expert_matmul* d, const voi
     if (!map3(&a.a, d->weight, false, d->inner, d->outer, d->n_experts, d->weight_row_stride, d->weight_expert_stride,
               64, kBlock, kWide) ||
         !map3(&a.b, dout, false, d->outer, d->n_tokens, 1, dout_stride, 0, kBlock, kHalf, kWide) ||
+        !map3(&a.b_mid, dout, false, d->outer, d->n_tokens, 1, dout_stride, 0, kBlock, kMidBox, kWide) ||
         !map3(&a.b_small, dout, false, d->outer, d->n_tokens, 1, dout_stride, 0, kBlock, kSmallBox, kWide) ||
         !map2(&a.out, dx, d->inner, d->n_tokens, 32, 32, kNarrow))
       return refused_map();
