@@ -18,11 +18,11 @@
 // an SM in the 512 cycles of the block's products; with a CTA for itself it
 // would be 48 KB.
 //   warps 0, 11  TMA loads of the left and of the right operand into a ring of
-//              six stages (five with fp32 gradients)
+//              six stages
 //   warp 1     products, issued by the even CTA; two accumulators of 256 columns
-//   warps 2-9  results from TMEM: rounded, transposed where tokens are columns,
-//              out through shared memory and TMA; tiles with other experts'
-//              tokens by plain stores of the rows that are theirs
+//   warps 2-9  results from TMEM: transposed where tokens are columns, out
+//              through shared memory and TMA; tiles with other experts' tokens
+//              by plain stores of the rows that are theirs
 //   warp 10    clears the rows behind an expert's tokens (third product)
 // Which unit belongs to whom follows from the offsets, which only the device
 // knows: every CTA adds them up for itself first.
@@ -49,14 +49,14 @@ constexpr int kPanel = kBlock * 64 * 2;  // MN-major: 64 columns of a block's 64
 constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStoreWarps = 8;
-constexpr int kMaxExperts = 1024;
+constexpr int kMaxExperts = 512;
 constexpr int kRaster = 8;  // token (or inner) tiles that walk together along the features
 constexpr uint32_t kTmemColumns = 512;
 
 enum Mode { kForward, kInput, kWeights };
 
 // error codes of the waits that ran out
-constexpr int kErrLoad = 0x501, kErrProduct = 0x502, kErrStore = 0x503, kErrClear = 0x504;
+constexpr int kErrLoad = 0x501, kErrProduct = 0x502, kErrStore = 0x503, kErrClear = 0x504, kErrAlign = 0x505;
 
 struct ExpertArgs {
   CUtensorMap a, b, b_mid, b_small, out;
@@ -68,16 +68,20 @@ struct ExpertArgs {
   int* err;
 };
 
-template <bool F32>
+template <int MODE>
 struct Layout {
-  static constexpr int kStages = F32 ? 5 : 6;
-  static constexpr int kBlockBytes = 32 * 32 * (F32 ? 4 : 2);
+  static constexpr int kStages = 6;
+  // results on their way out, 32 rows of 64 bytes; the weights' gradients, which can be many for few products, have two
+  // a warp, so that one is written while the other is read
+  static constexpr int kTileBytes = 2048, kTiles = MODE == kWeights ? 2 : 1;
   static constexpr int kStore = kStages * kStage;
-  static constexpr int kTable = kStore + kStoreWarps * kBlockBytes;
-  static constexpr int kBars = kTable + (2 * kMaxExperts + 8) * 4;
+  static constexpr int kTable = kStore + kStoreWarps * kTiles * kTileBytes;
+  static constexpr int kTableInts = kMaxExperts + 2;
+  static constexpr int kBars = kTable + (MODE == kWeights ? 1 : 2) * (kTableInts + 2) / 2 * 2 * 4;
   // full, empty, tail, fixed [stage]; accumulator full, free [2]; drain
   static constexpr int kNumBars = 4 * kStages + 5;
-  static constexpr int kBytes = 1024 + kBars + kNumBars * 8 + 16;
+  static constexpr int kBytes = kBars + kNumBars * 8 + 16;
+  static_assert(kBars % 8 == 0, "barriers");
   static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
@@ -166,6 +170,12 @@ __device__ __forceinline__ void load_pair_warp(uint32_t dst, const CUtensorMap* 
       "[%1, {%2, %3, %4}], [%5];\n\t}\n" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
+}
+
+// Until at most the last bulk store of this thread still reads shared memory.
+__device__ __forceinline__ void bulk_wait_read_but_one() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+__device__ __forceinline__ uint32_t pack(uint32_t lo, uint32_t hi) {
+  return op_pack_bf16(__uint_as_float(lo), __uint_as_float(hi));
 }
 
 // What a pair works on: rows m0 to m0 + 255 of D and `n` of its columns.
@@ -274,7 +284,7 @@ __device__ __forceinline__ void store_tokens(const ExpertArgs& a, const Unit& u,
   const uint32_t sel = (lane & 1) ? 0x3276u : 0x5410u;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    const uint32_t mine = op_pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+    const uint32_t mine = pack(r[2 * j], r[2 * j + 1]);
     const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
     *reinterpret_cast<uint32_t*>(to + 2 * j * 64 + (((lane >> 3) ^ (j & 3)) << 4)) = __byte_perm(mine, other, sel);
   }
@@ -299,57 +309,64 @@ __device__ __forceinline__ void store_tokens(const ExpertArgs& a, const Unit& u,
   __syncwarp();
 }
 
-// 32 rows of an expert's gradient by 32 columns, a row to a lane.
+// What an expert's gradient holds so far in a lane's 32 columns of a block, as it lies in memory.
+template <bool F32>
+struct Before {
+  uint4 v[F32 ? 8 : 4];
+  __device__ __forceinline__ void load(const ExpertArgs& a, const Unit& u, int row, int col) {
+    const uint4* const p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.dst) +
+                                                          (((int64_t)u.expert * a.m + row) * a.n + col) * (F32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < (F32 ? 8 : 4); ++i)
+      if (row < a.m && col + i * (F32 ? 4 : 8) < a.n) v[i] = p[i];
+  }
+  __device__ __forceinline__ float get(int e) const {
+    const uint4 x = v[e / (F32 ? 4 : 8)];
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if constexpr (F32) return __uint_as_float(w[e % 4]);
+    return __uint_as_float(e & 1 ? w[e / 2 % 4] & 0xFFFF0000u : w[e / 2 % 4] << 16);
+  }
+};
+
+// 32 rows of an expert's gradient by 32 columns, a row to a lane. `turn`: the tile that is next.
 template <bool F32>
 __device__ __forceinline__ void store_weights(const ExpertArgs& a, const Unit& u, int row0, int col0,
-                                              const uint32_t (&r)[32], uint8_t* tile, int lane) {
-  float v[32];
+                                              const uint32_t (&r)[32], uint8_t* tiles, int& turn, int lane) {
 #pragma unroll
-  for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
-  if (a.accumulate && row0 + lane < a.m) {
-    const int64_t at = ((int64_t)u.expert * a.m + row0 + lane) * a.n + col0;
+  for (int h = 0; h < (F32 ? 2 : 1); ++h, turn ^= 1) {
+    uint8_t* const tile = tiles + turn * 2048;
+    if (lane == 0) bulk_wait_read_but_one();  // this tile's last store has read it
+    __syncwarp();
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      if (col0 + q * 8 >= a.n) break;
-      float old[8];
+      uint4 v;
       if constexpr (F32)
-        load8(static_cast<const float*>(a.dst) + at + q * 8, old);
+        v = make_uint4(r[16 * h + 4 * q], r[16 * h + 4 * q + 1], r[16 * h + 4 * q + 2], r[16 * h + 4 * q + 3]);
       else
-        load8(static_cast<const __nv_bfloat16*>(a.dst) + at + q * 8, old);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[q * 8 + e] += old[e];
+        v = make_uint4(pack(r[8 * q], r[8 * q + 1]), pack(r[8 * q + 2], r[8 * q + 3]), pack(r[8 * q + 4], r[8 * q + 5]),
+                       pack(r[8 * q + 6], r[8 * q + 7]));
+      *reinterpret_cast<uint4*>(tile + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) = v;
     }
-  }
-  if (lane == 0) bulk_wait_read_all();
-  __syncwarp();
-  if constexpr (F32) {
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      *reinterpret_cast<float4*>(tile + lane * 128 + ((q ^ (lane & 7)) << 4)) =
-          make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<uint4*>(tile + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
-          make_uint4(op_pack_bf16(v[8 * q], v[8 * q + 1]), op_pack_bf16(v[8 * q + 2], v[8 * q + 3]),
-                     op_pack_bf16(v[8 * q + 4], v[8 * q + 5]), op_pack_bf16(v[8 * q + 6], v[8 * q + 7]));
-  }
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    tma_store_3d(&a.out, smem_u32(tile), col0, row0, u.expert);
-    bulk_commit();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && col0 + 16 * h < a.n) {
+      tma_store_3d(&a.out, smem_u32(tile), col0 + 16 * h, row0, u.expert);
+      bulk_commit();
+    }
   }
 }
 
 template <int MODE, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid_constant__ ExpertArgs a) {
-  using L = Layout<F32>;
+  using L = Layout<MODE>;
   constexpr int S = L::kStages;
-  extern __shared__ uint8_t raw[];
-  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023) {  // the operands' swizzle counts on it; in both CTAs alike
+    if (threadIdx.x == 0) atomicCAS(a.err, 0, kErrAlign);
+    return;
+  }
   int* const bound = reinterpret_cast<int*>(smem + L::kTable);
-  int* const first = bound + kMaxExperts + 4;
+  int* const first = bound + L::kTableInts;  // not for the weights' gradients
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(bars + L::kNumBars);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -382,7 +399,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
     // the experts' bounds, kept in order and in range whatever the offsets hold, and their units
     int before = 0, units = 0;
     const int mt = ceil_div(a.m, kTile);
-    if (lane == 0) bound[0] = first[0] = 0;
+    if (lane == 0) {
+      bound[0] = 0;
+      if (MODE != kWeights) first[0] = 0;
+    }
     for (int e0 = 0; e0 <= a.experts; e0 += 32) {
       const int e = e0 + lane;  // bound[e + 1]; the last one is where the tokens end
       int b = e < a.experts ? min(max(a.offsets[e + 1], 0), a.tokens) : a.tokens;
@@ -405,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
       units = __shfl_sync(0xffffffffu, n, 31);
       if (e <= a.experts) {
         bound[e + 1] = b;
-        first[e + 1] = n;
+        if (MODE != kWeights) first[e + 1] = n;
       }
     }
   }
@@ -527,12 +547,15 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
   } else if (warp < 2 + kStoreWarps) {
     // ---- results ----
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* const tile = smem + L::kStore + (warp - 2) * L::kBlockBytes;
-    int acc = 0;
+    uint8_t* const tile = smem + L::kStore + (warp - 2) * L::kTiles * L::kTileBytes;
+    int acc = 0, turn = 0;
     uint32_t acc_phase = 0;
     for (int pos = pos0; pos < tab.units; pos += step) {
       const Unit u = unit_at<MODE>(a, tab, pos, expert);
       const int row0 = u.m0 + (int)rank * kHalf + quarter * 32;
+      Before<F32> next;
+      const bool adds = MODE == kWeights && a.accumulate != 0;
+      if (adds && u.blocks > 0) next.load(a, u, row0 + lane, u.n0 + 32 * half);
       if (u.blocks > 0) {
         const bool got = mbar_wait(acc_full + 8 * acc, acc_phase, abort_flag, a.err, kErrStore);
         if (!__all_sync(0xffffffffu, got)) break;
@@ -540,8 +563,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
       }
       const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kTile);
       const int columns = MODE == kWeights ? min(u.n, a.n - u.n0) : u.count;
-      if (row0 < a.m && !(MODE == kWeights && u.blocks == 0 && a.accumulate)) {
+      if (row0 < a.m && !(adds && u.blocks == 0)) {
         for (int c0 = 32 * half; c0 < columns; c0 += 64) {
+          const Before<F32> before = next;
+          if (adds && c0 + 64 < columns) next.load(a, u, row0 + lane, u.n0 + c0 + 64);
           uint32_t r[32];
           if (u.blocks > 0) {
             tmem_ld_32x32b_x32(t0 + (uint32_t)c0, r);
@@ -550,10 +575,15 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
 #pragma unroll
             for (int e = 0; e < 32; ++e) r[e] = 0;
           }
-          if constexpr (MODE == kWeights)
-            store_weights<F32>(a, u, row0, u.n0 + c0, r, tile, lane);
-          else
+          if constexpr (MODE == kWeights) {
+            if (adds) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) + before.get(e));
+            }
+            store_weights<F32>(a, u, row0, u.n0 + c0, r, tile, turn, lane);
+          } else {
             store_tokens(a, u, row0, c0, r, tile, lane);
+          }
         }
       }
       if (u.blocks > 0) {
@@ -630,7 +660,7 @@ bool map2(CUtensorMap* tm, const void* base, int64_t x, int64_t y, int box_x, in
 
 template <int MODE, bool F32>
 cudaError_t launch(ExpertArgs& a, int sms, int64_t most_units, cudaStream_t st) {
-  using L = Layout<F32>;
+  using L = Layout<MODE>;
   cudaError_t e = op_smem_limit<expert_matmul_kernel<MODE, F32>>(L::kBytes);
   if (e != cudaSuccess) return e;
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(sms / 2, most_units));
@@ -770,8 +800,8 @@ ma_status muon_adamw_expert_matmul_backward(const ma_expert_matmul* d, const voi
     a.accumulate = accumulate;
     if (!map3(&a.a, dout, false, d->outer, d->n_tokens, 1, dout_stride, 0, 64, kBlock, kWide) ||
         !map3(&a.b, d->x, false, d->inner, d->n_tokens, 1, d->x_stride, 0, 64, kBlock, kWide) ||
-        !map3(&a.out, dweight, f32, d->inner, d->outer, d->n_experts, d->inner, (int64_t)d->outer * d->inner, 32, 32,
-              f32 ? kWide : kNarrow))
+        !map3(&a.out, dweight, f32, d->inner, d->outer, d->n_experts, d->inner, (int64_t)d->outer * d->inner, f32 ? 16 : 32,
+              32, kNarrow))
       return refused_map();
     const int64_t units =
         (int64_t)d->n_experts * ((a.m + kTile - 1) / kTile) * ((a.n + kTile - 1) / kTile);
