@@ -24,47 +24,56 @@ namespace {
 
 struct DropKey {
   uint32_t k0, k1, site, step0, step1;
-  uint32_t threshold2;  // the threshold in both halves
+  uint32_t threshold_up;  // the threshold in the upper half
   float factor;
 };
 
 __device__ __forceinline__ DropKey drop_key(const DropArgs& a) {
   const uint64_t seed = (uint64_t)__ldg(a.rng), step = (uint64_t)__ldg(a.rng + 1);
-  return {(uint32_t)seed, (uint32_t)(seed >> 32), a.site, (uint32_t)step, (uint32_t)(step >> 32), a.threshold * 0x10001u,
+  return {(uint32_t)seed, (uint32_t)(seed >> 32), a.site, (uint32_t)step, (uint32_t)(step >> 32), a.threshold << 16,
           a.factor};
 }
 
-__device__ __forceinline__ uint4 philox(uint4 c, uint32_t k0, uint32_t k1) {
+// Ten rounds over N counters in step, which form each round's keys once.
+template <int N>
+__device__ __forceinline__ void philox(uint4 (&c)[N], uint32_t k0, uint32_t k1) {
 #pragma unroll
   for (int i = 0; i < 10; ++i) {
-    const uint64_t a = (uint64_t)c.x * 0xD2511F53u, b = (uint64_t)c.z * 0xCD9E8D57u;
-    c = make_uint4((uint32_t)(b >> 32) ^ c.y ^ k0, (uint32_t)b, (uint32_t)(a >> 32) ^ c.w ^ k1, (uint32_t)a);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const uint64_t a = (uint64_t)c[j].x * 0xD2511F53u, b = (uint64_t)c[j].z * 0xCD9E8D57u;
+      c[j] = make_uint4((uint32_t)(b >> 32) ^ c[j].y ^ k0, (uint32_t)b, (uint32_t)(a >> 32) ^ c[j].w ^ k1, (uint32_t)a);
+    }
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
   }
-  return c;
 }
 
 // Eight elements by their bits, four words of them. Dropped ones become 0 whatever they hold.
-__device__ __forceinline__ void drop8_by(const DropKey& k, const uint32_t (&w)[4], float (&x)[8]) {
+__device__ __forceinline__ void drop8_by(const DropKey& k, const uint4& bits, float (&x)[8]) {
   if (k.factor == 0.f) {  // p = 1, whose threshold no 16 bits reach
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = 0.f;
     return;
   }
+  const uint32_t w[4] = {bits.x, bits.y, bits.z, bits.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    bool low, high;  // both halves compared by one instruction
-    __vibmax_u16x2(w[i], k.threshold2, &high, &low);
-    x[2 * i] = low ? x[2 * i] * k.factor : 0.f;
-    x[2 * i + 1] = high ? x[2 * i + 1] * k.factor : 0.f;
+    // the threshold lies in the upper half: the high element compares as it is, the low one moved up
+    x[2 * i] = w[i] << 16 >= k.threshold_up ? x[2 * i] * k.factor : 0.f;
+    x[2 * i + 1] = w[i] >= k.threshold_up ? x[2 * i + 1] * k.factor : 0.f;
   }
 }
 
-// The eight elements of group `group`.
-__device__ __forceinline__ void drop8(const DropKey& k, uint32_t group, float (&x)[8]) {
-  const uint4 r = philox(make_uint4(group, k.site, k.step0, k.step1), k.k0, k.k1);
-  drop8_by(k, {r.x, r.y, r.z, r.w}, x);
+// The eight elements of each of N groups, `stride` apart from `group` on.
+template <int N>
+__device__ __forceinline__ void drop8(const DropKey& k, uint32_t group, uint32_t stride, float (&x)[N][8]) {
+  uint4 c[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) c[j] = make_uint4(group + j * stride, k.site, k.step0, k.step1);
+  philox(c, k.k0, k.k1);
+#pragma unroll
+  for (int j = 0; j < N; ++j) drop8_by(k, c[j], x[j]);
 }
 
 }  // namespace

@@ -62,12 +62,7 @@ __global__ void __launch_bounds__(RowThreads<T>::kBlock) residual_norm_kernel(co
   float r[V][8];
 #pragma unroll
   for (int j = 0; j < V; ++j) rx[j].get((j * T + t) * 8, a.w, r[j]);
-  if (a.drop.threshold) {
-    const DropKey key = drop_key(a.drop);
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if ((j * T + t) * 8 < a.w) drop8_at<VEC>(key, row * a.w + (j * T + t) * 8, r[j]);
-  }
+  if (a.drop.threshold) drop_row<VEC, T>(drop_key(a.drop), row * a.w, t, r);
   float ss = 0.f;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -138,12 +133,12 @@ cudaError_t forward(const NormArgs& a, bool vec, cudaStream_t st) {
     return launch<TX, TS, 512, 8, false>(a, st);
   }
   // Two to four vectors a thread: enough loads in flight, and warps enough to hide the generator. 64M elements of bf16
-  // without and with dropout: width 2048 with (threads, vectors) = (32, 8) 79 and 102 us, (128, 2) 78 and 87, (256, 1)
-  // 77 and 94; 1024 with (32, 4) 78 and 79, (64, 2) 77 and 85; 8192 with (128, 8) 86, (256, 4) 81 and 96, (512, 2) 94
-  // and 110; 16384 with (256, 8) 111 and 162, (512, 4) 102 and 140, (1024, 2) 105 and 134.
+  // without and with dropout: width 1024 with (threads, vectors) = (32, 4) 78 and 85 us, (64, 2) 77 and 83; 2048 with
+  // (32, 8) 79 and 102, (128, 2) 77 and 84, (256, 1) 77 and 94; 8192 with (128, 8) 86, (256, 4) 85 and 100, (512, 2) 95
+  // and 98; 16384 with (256, 8) 111 and 162, (512, 4) 104 and 111, (1024, 2) 105 and 134.
   if (units <= 32) return launch<TX, TS, 32, 1, true>(a, st);
   if (units <= 64) return launch<TX, TS, 32, 2, true>(a, st);
-  if (units <= 128) return launch<TX, TS, 32, 4, true>(a, st);
+  if (units <= 128) return launch<TX, TS, 64, 2, true>(a, st);
   if (units <= 256) return launch<TX, TS, 128, 2, true>(a, st);
   if (units <= 512) return launch<TX, TS, 128, 4, true>(a, st);
   if (units <= 1024) return launch<TX, TS, 256, 4, true>(a, st);

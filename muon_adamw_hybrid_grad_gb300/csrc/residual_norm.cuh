@@ -90,18 +90,18 @@ __device__ __forceinline__ void load_weight(const float* weight, int col, int w,
   for (int e = 0; e < 8; ++e) v[e] = col + e < w ? weight[col + e] : 0.f;
 }
 
-// drop8 of the elements from `at` on. VEC: `at` is a multiple of 8.
+// Dropout of the eight elements from number `at` on. VEC: a multiple of 8.
 template <bool VEC>
 __device__ __forceinline__ void drop8_at(const DropKey& k, int64_t at, float (&x)[8]) {
   const uint32_t group = (uint32_t)(at >> 3);
   if (VEC || (at & 7) == 0) {
-    drop8(k, group, x);
+    drop8<1>(k, group, 0, *reinterpret_cast<float(*)[1][8]>(&x));
     return;
   }
   // the end of one group and the beginning of the next, the same shift for a whole row
-  const uint4 a = philox(make_uint4(group, k.site, k.step0, k.step1), k.k0, k.k1);
-  const uint4 b = philox(make_uint4(group + 1, k.site, k.step0, k.step1), k.k0, k.k1);
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint4 c[2] = {make_uint4(group, k.site, k.step0, k.step1), make_uint4(group + 1, k.site, k.step0, k.step1)};
+  philox(c, k.k0, k.k1);
+  uint32_t w[8] = {c[0].x, c[0].y, c[0].z, c[0].w, c[1].x, c[1].y, c[1].z, c[1].w};
   if (at & 4) {
 #pragma unroll
     for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
@@ -114,7 +114,23 @@ __device__ __forceinline__ void drop8_at(const DropKey& k, int64_t at, float (&x
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
   }
-  drop8_by(k, {w[0], w[1], w[2], w[3]}, x);
+  drop8_by(k, make_uint4(w[0], w[1], w[2], w[3]), x);
+}
+
+// Of a thread's V vectors in the row whose first element is number `row0`.
+template <bool VEC, int T, int V>
+__device__ __forceinline__ void drop_row(const DropKey& k, int64_t row0, int t, float (&x)[V][8]) {
+  if constexpr (VEC) {
+    // in step where the registers allow it: 32765 rows of 2048 84 us, one by one 88; 16381 of 4096 86 and 91; eight
+    // vectors, or four of wide rows, lose more by fewer warps
+    constexpr int N = V == 2 || (V == 4 && T == 128) ? 2 : 1;
+#pragma unroll
+    for (int j = 0; j < V; j += N)
+      drop8<N>(k, (uint32_t)(row0 >> 3) + (uint32_t)(j * T + t), T, *reinterpret_cast<float(*)[N][8]>(&x[j]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) drop8_at<false>(k, row0 + (j * T + t) * 8, x[j]);
+  }
 }
 
 __device__ __forceinline__ float warp_sum(float v) {

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(RowGroups<T>::kBlock) residual_norm_grad_kerne
       }
       store_row<VEC>(static_cast<TS*>(a.dr) + row * a.w, col, a.w, d);
       if (a.dx) {
-        if (a.drop.threshold && col < a.w) drop8_at<VEC>(key, row * a.w + col, d);
+        if (a.drop.threshold) drop8_at<VEC>(key, row * a.w + col, d);
         store_row<VEC>(static_cast<TX*>(a.dx) + row * a.w, col, a.w, d);
       }
     }
@@ -290,21 +290,24 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     const float rstd = rsqrtf(ss0 / (float)a.w + a.eps);
     const float c = gr0 / (float)a.w * rstd * rstd * rstd;
     const uint64_t rstd2 = pack2(rstd, rstd), c2 = pack2(-c, -c);
+    float v[V][8];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int col = (j * T + t) * 8;
-      float v[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint64_t g = mul2(rstd2, dy[j][i]);
         dw[j][i] = fma2(g, r[j][i], dw[j][i]);
-        unpack2(add2(d[j][i], fma2(g, w[j][i], mul2(c2, r[j][i]))), v[2 * i], v[2 * i + 1]);
+        unpack2(add2(d[j][i], fma2(g, w[j][i], mul2(c2, r[j][i]))), v[j][2 * i], v[j][2 * i + 1]);
       }
-      if (col >= a.w) continue;
-      store8(static_cast<TS*>(a.dr) + row * a.w + col, v);
-      if (a.dx) {
-        if (a.drop.threshold) drop8(key, (uint32_t)((row * a.w + col) >> 3), v);
-        store8(static_cast<TX*>(a.dx) + row * a.w + col, v);
+      if (col < a.w) store8(static_cast<TS*>(a.dr) + row * a.w + col, v[j]);
+    }
+    if (a.dx) {
+      if (a.drop.threshold) drop_row<true, T>(key, row * a.w, t, v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int col = (j * T + t) * 8;
+        if (col < a.w) store8(static_cast<TX*>(a.dx) + row * a.w + col, v[j]);
       }
     }
   }
