@@ -226,14 +226,19 @@ __device__ void choose_top(const Row<T>& row, int v0, int v1, bool edges, int to
     }
     if (edges && row.edge(t) >= 0) f(load1(row.p + row.edge(t)), row.edge(t));
   };
-  // the groups that reach it, and then their vectors shared out over all threads
+  // the groups that reach it, looked at 32 at a time, and then their vectors shared out over all threads
   if (best >= limit) {
-    int g = t;
-    for (int v = v0; v < v1; v += kStep, g += kThreads)
-      if (!(load1(groups + g) < limit)) {
+    const int all = (v1 - v0 + kStep - 1) / kStep;
+    for (int i0 = 0; i0 < all; i0 += 32) {
+      uint32_t reach = 0;
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i)
+        if (i0 + i < all) reach |= (uint32_t)!(load1(groups + (i0 + i) * kThreads + t) < limit) << i;
+      for (; reach; reach &= reach - 1) {
         const int at = atomicAdd(&sh.hit, 1);
-        if (at < kHits) sh.hits[at] = (uint32_t)g;
+        if (at < kHits) sh.hits[at] = (uint32_t)((i0 + __ffs(reach) - 1) * kThreads + t);
       }
+    }
   }
   __syncthreads();
   const int hit = sh.hit;
@@ -318,7 +323,9 @@ __device__ void choose_top(const Row<T>& row, int v0, int v1, bool edges, int to
   for (int i = t; i < above + equal; i += kThreads) {
     const uint64_t key = sh.list[i < above ? i : kListed + i - above];
     int r = 0;
+#pragma unroll 8
     for (int k = 0; k < above; ++k) r += sh.list[k] > key;
+#pragma unroll 8
     for (int k = 0; k < equal; ++k) r += sh.list[kListed + k] > key;
     if (r < top) sh.chosen[r] = key;
   }
@@ -421,16 +428,29 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
     if (!(x <= run.m)) run.raise(x, c);
     if (run.m != -INFINITY) run.add(x, -INFINITY, c);
   }
+  // the warp's sums relative to its maximum, then the block's
   Sums all = run.sums();
+  float m = all.m;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1)
-    all = join(all, {__shfl_xor_sync(0xffffffffu, all.m, d), __shfl_xor_sync(0xffffffffu, all.s, d),
-                     __shfl_xor_sync(0xffffffffu, all.u, d)}, c);
+  for (int d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+  all = rebase(all, m, c);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    all.s += __shfl_xor_sync(0xffffffffu, all.s, d);
+    all.u += __shfl_xor_sync(0xffffffffu, all.u, d);
+  }
   if ((t & 31) == 0) warp_sums[t >> 5] = all;
   __syncthreads();
-  all = warp_sums[0];
+  m = warp_sums[0].m;
 #pragma unroll
-  for (int i = 1; i < kThreads / 32; ++i) all = join(all, warp_sums[i], c);
+  for (int i = 1; i < kThreads / 32; ++i) m = max_nan(m, warp_sums[i].m);
+  all = {m, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) {
+    const Sums w = rebase(warp_sums[i], m, c);
+    all.s += w.s;
+    all.u += w.u;
+  }
   if constexpr (TOP) choose_top(row, v0, v1, edges, a.top, best, groups, sh);
 
   if (a.parts > 1) {
@@ -449,8 +469,13 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
           sh.list[i] = ld_cluster_u64(mapa_shared(lists, i / a.top) + 8 * (i % a.top));
       }
     }
-    cluster_sync();
-    if (part != 0) return;
+    // the others may leave once this block has read
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (part != 0) {
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      return;
+    }
+    __syncthreads();
     if constexpr (TOP) {
       for (int k = t; k < a.parts * a.top; k += kThreads) {
         const uint64_t key = sh.list[k];
@@ -477,6 +502,7 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
       a.top_ids[at * a.top + t] = (int64_t)key_index(key);
     }
   }
+  if (a.parts > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ---- gradient ----
