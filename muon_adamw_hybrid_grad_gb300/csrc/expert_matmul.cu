@@ -53,31 +53,32 @@ constexpr int kMaxExperts = 512;
 constexpr int kRaster = 8;  // token (or inner) tiles that walk together along the features
 constexpr uint32_t kTmemColumns = 512;
 
-enum Mode { kForward, kInput, kWeights };
-
 // error codes of the waits that ran out
 constexpr int kErrLoad = 0x501, kErrProduct = 0x502, kErrStore = 0x503, kErrClear = 0x504, kErrAlign = 0x505;
 
 struct ExpertArgs {
+  // the product whose columns are tokens: out, or dx
   CUtensorMap a, b, b_mid, b_small, out;
+  int m, k;  // rows of D; the contraction, 0: no such product
+  void* dst;
+  // the weights' gradients
+  CUtensorMap wa, wb, wout;
+  int wm, wn;  // rows (0: no such product) and columns
+  void* grad;
+  int accumulate;
+  int rounds;  // units of these that take as long as one of dx
   const int32_t* offsets;
   int tokens, experts;
-  int m, n, k;  // forward: outer, -, inner; input: inner, -, outer; weights: outer, inner, -
-  void* dst;
-  int accumulate;
   int* err;
 };
 
-template <int MODE>
 struct Layout {
   static constexpr int kStages = 6;
-  // results on their way out, 32 rows of 64 bytes; the weights' gradients, which can be many for few products, have two
-  // a warp, so that one is written while the other is read
-  static constexpr int kTileBytes = 2048, kTiles = MODE == kWeights ? 2 : 1;
+  // results on their way out, 32 rows of 64 bytes, two a warp: one is written while the other is read
+  static constexpr int kTileBytes = 2048, kTiles = 2;
   static constexpr int kStore = kStages * kStage;
   static constexpr int kTable = kStore + kStoreWarps * kTiles * kTileBytes;
-  static constexpr int kTableInts = kMaxExperts + 2;
-  static constexpr int kBars = kTable + (MODE == kWeights ? 1 : 2) * (kTableInts + 2) / 2 * 2 * 4;
+  static constexpr int kBars = kTable + (kMaxExperts + 4) * 4;
   // full, empty, tail, fixed [stage]; accumulator full, free [2]; drain
   static constexpr int kNumBars = 4 * kStages + 5;
   static constexpr int kBytes = kBars + kNumBars * 8 + 16;
@@ -180,50 +181,88 @@ __device__ __forceinline__ uint32_t pack(uint32_t lo, uint32_t hi) {
 
 // What a pair works on: rows m0 to m0 + 255 of D and `n` of its columns.
 struct Unit {
+  bool weights;  // of the weights' gradients
   int expert, m0, n0, n;
   int at, count;  // the unit's tokens
   int blocks;     // of the contraction; 0: zeros
 };
+template <bool BACK>
+__device__ __forceinline__ bool is_weights(const Unit& u) {
+  return BACK && u.weights;
+}
 
-struct Table {
-  const int* bound;  // expert e's tokens are bound[e] to bound[e + 1]; e = experts: those behind the last
-  const int* first;  // its units (weights: unused)
-  int units;
+// Expert e's tokens are bound[e] to bound[e + 1]; e = experts: those behind the last. `tokens` units of the product
+// over tokens come first, in ascending order, so that each warp looks for a unit's expert from its last one on.
+struct Units {
+  const int* bound;
+  int tokens, all;
+  int expert, first;  // `first`: that expert's first unit
 };
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// Units come in ascending order, so the expert is looked for from the last one on.
-template <int MODE>
-__device__ __forceinline__ Unit unit_at(const ExpertArgs& a, const Table& tab, int pos, int& expert) {
+// Which units a pair takes, one of `pairs`: in turn; but the pairs with one unit of the product over tokens more than
+// the others leave the first `early` units of the weights' gradients to those.
+template <bool BACK>
+struct Deal {
+  int pair, pairs, tokens, weights, extra, early;
+  __device__ __forceinline__ Deal(const ExpertArgs& a, const Units& all, int pair_, int pairs_)
+      : pair(pair_), pairs(pairs_), tokens(all.tokens), weights(all.all - all.tokens) {
+    extra = !BACK ? 0 : tokens < pairs ? tokens : tokens % pairs;
+    early = extra ? (int)min((int64_t)a.rounds * (pairs - extra), (int64_t)weights) : 0;
+  }
+  __device__ __forceinline__ int begin() const { return !BACK || pair < tokens ? pair : weights_from(); }
+  __device__ __forceinline__ int after(int pos) const {
+    if (!BACK) return pos + pairs;
+    if (pos < tokens) return pos + pairs < tokens ? pos + pairs : weights_from();
+    int i = pos - tokens;
+    if (i < early) {
+      i += pairs - extra;
+      return tokens + (i < early ? i : early + pair);
+    }
+    return pos + pairs;
+  }
+  __device__ __forceinline__ int weights_from() const {
+    return tokens + (pair >= extra && pair - extra < early ? pair - extra : early + pair);
+  }
+};
+
+template <bool BACK>
+__device__ __forceinline__ Unit unit_at(const ExpertArgs& a, Units& all, int pos) {
   Unit u;
-  const int mt = ceil_div(a.m, kTile);
-  if constexpr (MODE == kWeights) {
-    const int nt = ceil_div(a.n, kTile), local = pos % (mt * nt);
-    u.expert = pos / (mt * nt);
+  u.weights = pos >= all.tokens;
+  if (is_weights<BACK>(u)) {
+    const int mt = ceil_div(a.wm, kTile), nt = ceil_div(a.wn, kTile), local = (pos - all.tokens) % (mt * nt);
+    u.expert = (pos - all.tokens) / (mt * nt);
     const int group = local / (kRaster * mt), width = min(kRaster, nt - group * kRaster);
     const int r = local - group * kRaster * mt;
     u.m0 = r / width * kTile;
     u.n0 = (group * kRaster + r % width) * kTile;
-    u.n = a.n - u.n0 > kHalf ? kTile : kHalf;
-    u.at = tab.bound[u.expert];
-    u.count = tab.bound[u.expert + 1] - u.at;
+    u.n = a.wn - u.n0 > kHalf ? kTile : kHalf;
+    u.at = all.bound[u.expert];
+    u.count = all.bound[u.expert + 1] - u.at;
     u.blocks = ceil_div(u.count, kBlock);
   } else {
-    while (pos >= tab.first[expert + 1]) ++expert;
-    const int begin = tab.bound[expert], count = tab.bound[expert + 1] - begin;
-    const int tt = ceil_div(count, kTile), local = pos - tab.first[expert];
+    const int mt = ceil_div(a.m, kTile);
+    int begin, count, tt;
+    for (;; ++all.expert, all.first += tt * mt) {
+      begin = all.bound[all.expert];
+      count = all.bound[all.expert + 1] - begin;
+      tt = ceil_div(count, kTile);
+      if (pos < all.first + tt * mt) break;
+    }
+    const int local = pos - all.first;
     const int group = local / (kRaster * mt), width = min(kRaster, tt - group * kRaster);
     const int r = local - group * kRaster * mt;
     // token tiles of one size; the last is never empty, since count > 256 (tt - 1)
     const int per = (ceil_div(count, tt) + 31) & ~31, tile = group * kRaster + r % width;
-    u.expert = expert;
+    u.expert = all.expert;
     u.m0 = r / width * kTile;
     u.n0 = 0;
     u.at = begin + tile * per;
     u.count = min(per, count - tile * per);
     u.n = (u.count + 31) & ~31;
-    u.blocks = expert < a.experts ? ceil_div(a.k, kBlock) : 0;
+    u.blocks = u.expert < a.experts ? ceil_div(a.k, kBlock) : 0;
   }
   return u;
 }
@@ -235,32 +274,33 @@ __device__ __forceinline__ int token_rows(const Unit& u) {
 }
 
 // Bytes that land in a CTA for one block.
-template <int MODE>
+template <bool BACK>
 __device__ __forceinline__ uint32_t stage_bytes(const Unit& u) {
-  return (uint32_t)(kOperand + (MODE == kWeights ? u.n / 2 / 64 * kPanel : token_rows(u) * kBlock * 2));
+  return (uint32_t)(kOperand + (is_weights<BACK>(u) ? u.n / 2 / 64 * kPanel : token_rows(u) * kBlock * 2));
 }
 
-template <int MODE, typename LOAD>
+template <bool BACK, typename LOAD>
 __device__ __forceinline__ void load_left(const ExpertArgs& a, const Unit& u, int block, uint32_t stage, uint32_t rank,
                                           LOAD load) {
   const int k0 = block * kBlock, m0 = u.m0 + (int)rank * kHalf;
-  if constexpr (MODE == kForward) {
+  if constexpr (!BACK) {
     load(stage, &a.a, k0, m0, u.expert);
   } else {
-    for (int p = 0; p < kHalf / 64; ++p)
-      load(stage + p * kPanel, &a.a, m0 + p * 64, MODE == kInput ? k0 : u.at + k0, MODE == kInput ? u.expert : 0);
+    const CUtensorMap* const map = u.weights ? &a.wa : &a.a;
+    const int y = u.weights ? u.at + k0 : k0, z = u.weights ? 0 : u.expert;
+    for (int p = 0; p < kHalf / 64; ++p) load(stage + p * kPanel, map, m0 + p * 64, y, z);
   }
 }
 
-template <int MODE, typename LOAD>
+template <bool BACK, typename LOAD>
 __device__ __forceinline__ void load_right(const ExpertArgs& a, const Unit& u, int block, uint32_t stage, uint32_t rank,
                                            LOAD load) {
   const int k0 = block * kBlock;
   const uint32_t sb = stage + kOperand;
-  if constexpr (MODE == kWeights) {
+  if (is_weights<BACK>(u)) {
     const int n0 = u.n0 + (int)rank * (u.n / 2);
-    load(sb, &a.b, n0, u.at + k0, 0);
-    if (u.n == kTile) load(sb + kPanel, &a.b, n0 + 64, u.at + k0, 0);
+    load(sb, &a.wb, n0, u.at + k0, 0);
+    if (u.n == kTile) load(sb + kPanel, &a.wb, n0 + 64, u.at + k0, 0);
   } else {
     const int t0 = u.at + (int)rank * (u.n / 2), rows = token_rows(u);
     if (rows > 2 * kSmallBox) {
@@ -275,8 +315,10 @@ __device__ __forceinline__ void load_right(const ExpertArgs& a, const Unit& u, i
 // 32 rows of D by 32 columns, D's rows the lanes: tokens are columns, so the
 // block leaves transposed, a row of 32 features for each token.
 __device__ __forceinline__ void store_tokens(const ExpertArgs& a, const Unit& u, int row0, int c0,
-                                             const uint32_t (&r)[32], uint8_t* tile, int lane) {
-  if (lane == 0) bulk_wait_read_all();  // the last block's store has read the tile
+                                             const uint32_t (&r)[32], uint8_t* tiles, int& turn, int lane) {
+  uint8_t* const tile = tiles + turn * Layout::kTileBytes;
+  turn ^= 1;
+  if (lane == 0) bulk_wait_read_but_one();  // this tile's last store has read it
   __syncwarp();
   // rows of 64 bytes, 16-byte chunk q of row t at q ^ (t / 2 % 4): lanes 2 k and 2 k + 1 swap, the even one writes
   // the pair's even tokens, the odd one its odd ones
@@ -307,6 +349,7 @@ __device__ __forceinline__ void store_tokens(const ExpertArgs& a, const Unit& u,
           *reinterpret_cast<const uint4*>(tile + t * 64 + ((q ^ ((t >> 1) & 3)) << 4));
   }
   __syncwarp();
+  if (lane == 0) bulk_commit();  // an empty group, so that the tiles' turns and the groups stay in step
 }
 
 // What an expert's gradient holds so far in a lane's 32 columns of a block, as it lies in memory.
@@ -314,11 +357,11 @@ template <bool F32>
 struct Before {
   uint4 v[F32 ? 8 : 4];
   __device__ __forceinline__ void load(const ExpertArgs& a, const Unit& u, int row, int col) {
-    const uint4* const p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.dst) +
-                                                          (((int64_t)u.expert * a.m + row) * a.n + col) * (F32 ? 4 : 2));
+    const uint4* const p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.grad) +
+                                                          (((int64_t)u.expert * a.wm + row) * a.wn + col) * (F32 ? 4 : 2));
 #pragma unroll
     for (int i = 0; i < (F32 ? 8 : 4); ++i)
-      if (row < a.m && col + i * (F32 ? 4 : 8) < a.n) v[i] = p[i];
+      if (row < a.wm && col + i * (F32 ? 4 : 8) < a.wn) v[i] = p[i];
   }
   __device__ __forceinline__ float get(int e) const {
     const uint4 x = v[e / (F32 ? 4 : 8)];
@@ -334,7 +377,7 @@ __device__ __forceinline__ void store_weights(const ExpertArgs& a, const Unit& u
                                               const uint32_t (&r)[32], uint8_t* tiles, int& turn, int lane) {
 #pragma unroll
   for (int h = 0; h < (F32 ? 2 : 1); ++h, turn ^= 1) {
-    uint8_t* const tile = tiles + turn * 2048;
+    uint8_t* const tile = tiles + turn * Layout::kTileBytes;
     if (lane == 0) bulk_wait_read_but_one();  // this tile's last store has read it
     __syncwarp();
 #pragma unroll
@@ -349,16 +392,17 @@ __device__ __forceinline__ void store_weights(const ExpertArgs& a, const Unit& u
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0 && col0 + 16 * h < a.n) {
-      tma_store_3d(&a.out, smem_u32(tile), col0 + 16 * h, row0, u.expert);
+    if (lane == 0) {
+      if (col0 + 16 * h < a.wn) tma_store_3d(&a.wout, smem_u32(tile), col0 + 16 * h, row0, u.expert);
       bulk_commit();
     }
   }
 }
 
-template <int MODE, bool F32>
+// BACK: dx and the weights' gradients in one launch, the units of both dealt out as they come.
+template <bool BACK, bool F32>
 __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid_constant__ ExpertArgs a) {
-  using L = Layout<MODE>;
+  using L = Layout;
   constexpr int S = L::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023) {  // the operands' swizzle counts on it; in both CTAs alike
@@ -366,7 +410,6 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
     return;
   }
   int* const bound = reinterpret_cast<int*>(smem + L::kTable);
-  int* const first = bound + L::kTableInts;  // not for the weights' gradients
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(bars + L::kNumBars);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -374,7 +417,6 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
   const uint32_t full = smem_u32(bars), empty = full + 8 * S, tail = empty + 8 * S, fixed = tail + 8 * S;
   const uint32_t acc_full = fixed + 8 * S, acc_free = acc_full + 16, drain = acc_free + 16;
   const uint32_t rank = cluster_ctarank();
-  const int step = gridDim.x / 2, pos0 = blockIdx.x / 2;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -399,10 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
     // the experts' bounds, kept in order and in range whatever the offsets hold, and their units
     int before = 0, units = 0;
     const int mt = ceil_div(a.m, kTile);
-    if (lane == 0) {
-      bound[0] = 0;
-      if (MODE != kWeights) first[0] = 0;
-    }
+    if (lane == 0) bound[0] = 0;
     for (int e0 = 0; e0 <= a.experts; e0 += 32) {
       const int e = e0 + lane;  // bound[e + 1]; the last one is where the tokens end
       int b = e < a.experts ? min(max(a.offsets[e + 1], 0), a.tokens) : a.tokens;
@@ -415,28 +454,21 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
       int begin = __shfl_up_sync(0xffffffffu, b, 1);
       if (lane == 0) begin = before;
       before = __shfl_sync(0xffffffffu, b, 31);
-      int n = ceil_div(b - begin, kTile) * mt;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, n, d);
-        if (lane >= d) n += o;
-      }
-      n += units;
-      units = __shfl_sync(0xffffffffu, n, 31);
-      if (e <= a.experts) {
-        bound[e + 1] = b;
-        if (MODE != kWeights) first[e + 1] = n;
-      }
+      units += ceil_div(b - begin, kTile) * mt;
+      if (e <= a.experts) bound[e + 1] = b;
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) units += __shfl_xor_sync(0xffffffffu, units, d);
+    if (lane == 0) bound[kMaxExperts + 3] = a.k > 0 ? units : 0;
   }
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // the other CTA's barriers are there before a copy or a commit reaches them
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const Table tab{bound, first,
-                  MODE == kWeights ? a.experts * ceil_div(a.m, kTile) * ceil_div(a.n, kTile) : first[a.experts + 1]};
-  int expert = 0;
+  Units tab{bound, bound[kMaxExperts + 3], 0, 0, 0};
+  tab.all = tab.tokens + (BACK ? a.experts * ceil_div(a.wm, kTile) * ceil_div(a.wn, kTile) : 0);
+  const Deal<BACK> deal(a, tab, blockIdx.x / 2, gridDim.x / 2);
 
   if (warp == 0 || warp == kWarps - 1) {
     // ---- loads, a warp for each operand: issuing a copy takes some 100 cycles ----
@@ -445,24 +477,24 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
     uint32_t phase = 0;
     bool ok = true;
     const uint32_t s0 = smem_u32(smem), full_pair = mapa_shared(full, 0);
-    for (int pos = pos0; pos < tab.units && ok; pos += step) {
-      const Unit u = unit_at<MODE>(a, tab, pos, expert);
-      const uint32_t bytes = stage_bytes<MODE>(u);
+    for (int pos = deal.begin(); pos < tab.all && ok; pos = deal.after(pos)) {
+      const Unit u = unit_at<BACK>(a, tab, pos);
+      const uint32_t bytes = stage_bytes<BACK>(u);
       for (int b = 0; b < u.blocks; ++b) {
         if (!mbar_wait_warp(empty + 8 * stage, phase ^ 1u, abort_flag, a.err, kErrLoad)) {
           ok = false;
           break;
         }
         const uint32_t at = s0 + (uint32_t)(stage * kStage);
-        if (MODE == kWeights && b == u.blocks - 1 && u.count % kBlock != 0) {
+        if (is_weights<BACK>(u) && b == u.blocks - 1 && u.count % kBlock != 0) {
           // rows of the next expert in it: lands on a barrier of this CTA's, and is cleared before it is full
           const uint32_t bar = tail + 8 * stage;
           auto load = [&](uint32_t dst, const CUtensorMap* tm, int x, int y, int z) { load_warp(dst, tm, x, y, z, bar); };
           if (left) {
             expect_warp(bar, bytes);
-            load_left<MODE>(a, u, b, at, rank, load);
+            load_left<BACK>(a, u, b, at, rank, load);
           } else {
-            load_right<MODE>(a, u, b, at, rank, load);
+            load_right<BACK>(a, u, b, at, rank, load);
           }
         } else {
           const uint32_t bar = full_pair + 8 * stage;
@@ -471,9 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
           };
           if (left) {
             if (rank == 0) expect_warp(full + 8 * stage, 2 * bytes);
-            load_left<MODE>(a, u, b, at, rank, load);
+            load_left<BACK>(a, u, b, at, rank, load);
           } else {
-            load_right<MODE>(a, u, b, at, rank, load);
+            load_right<BACK>(a, u, b, at, rank, load);
           }
         }
         ++issued;
@@ -502,13 +534,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
       bool ok = true;
       const uint32_t s0 = smem_u32(smem), empty_odd = mapa_shared(empty, 1);
       // MN-major: panels of 64 columns, sixteen rows of the contraction 2 KB further
-      const uint64_t a0 = MODE == kForward ? sdesc(s0, 16, 1024) : sdesc(s0, kPanel, 1024);
-      const uint64_t b0 = MODE == kWeights ? sdesc(s0 + kOperand, kPanel, 1024) : sdesc(s0 + kOperand, 16, 1024);
-      constexpr uint32_t kStepA = MODE == kForward ? 2 : 128, kStepB = MODE == kWeights ? 128 : 2;
-      for (int pos = pos0; pos < tab.units && ok; pos += step) {
-        const Unit u = unit_at<MODE>(a, tab, pos, expert);
+      constexpr int kStepA = BACK ? 128 : 2;
+      const uint64_t a0 = BACK ? sdesc(s0, kPanel, 1024) : sdesc(s0, 16, 1024);
+      const uint64_t b_k = sdesc(s0 + kOperand, 16, 1024), b_mn = sdesc(s0 + kOperand, kPanel, 1024);
+      for (int pos = deal.begin(); pos < tab.all && ok; pos = deal.after(pos)) {
+        const Unit u = unit_at<BACK>(a, tab, pos);
         if (u.blocks == 0) continue;
-        const uint32_t idesc = idesc_bf16(kTile, u.n, MODE == kWeights) | (MODE == kForward ? 0u : 1u << 15);
+        const bool weights = is_weights<BACK>(u);
+        const uint32_t idesc = idesc_bf16(kTile, u.n, weights) | (BACK ? 1u << 15 : 0u);
         if (!mbar_wait_warp_cluster(acc_free + 8 * acc, acc_phase ^ 1u, abort_flag, a.err, kErrProduct)) break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(acc * kTile);
@@ -519,13 +552,17 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
           }
           tc_fence_after();
           const uint32_t off = (uint32_t)stage * (uint32_t)(kStage >> 4);
-          const int left = MODE == kWeights ? u.count - b * kBlock : kBlock;
-          const uint64_t ad = a0 + off, bd = b0 + off;
-          if (MODE != kWeights || left > kBlock - 16) {
-            umma_block_warp<kStepA, kStepB>(d, ad, bd, idesc, b != 0 ? 1u : 0u);
+          const uint64_t ad = a0 + off;
+          if (!weights) {
+            umma_block_warp<kStepA, 2>(d, ad, b_k + off, idesc, b != 0 ? 1u : 0u);
           } else {
-            for (int i = 0; i * 16 < left; ++i)
-              umma_pair_warp(d, ad + kStepA * i, bd + kStepB * i, idesc, (b | i) != 0 ? 1u : 0u);
+            const int left = u.count - b * kBlock;
+            if (left > kBlock - 16) {
+              umma_block_warp<kStepA, 128>(d, ad, b_mn + off, idesc, b != 0 ? 1u : 0u);
+            } else {
+              for (int i = 0; i * 16 < left; ++i)
+                umma_pair_warp(d, ad + kStepA * i, b_mn + off + 128 * i, idesc, (b | i) != 0 ? 1u : 0u);
+            }
           }
           commit_pair_warp(empty + 8 * stage, empty_odd + 8 * stage);
           if (++stage == S) {
@@ -547,14 +584,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
   } else if (warp < 2 + kStoreWarps) {
     // ---- results ----
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* const tile = smem + L::kStore + (warp - 2) * L::kTiles * L::kTileBytes;
+    uint8_t* const tiles = smem + L::kStore + (warp - 2) * L::kTiles * L::kTileBytes;
     int acc = 0, turn = 0;
     uint32_t acc_phase = 0;
-    for (int pos = pos0; pos < tab.units; pos += step) {
-      const Unit u = unit_at<MODE>(a, tab, pos, expert);
+    for (int pos = deal.begin(); pos < tab.all; pos = deal.after(pos)) {
+      const Unit u = unit_at<BACK>(a, tab, pos);
+      const bool weights = is_weights<BACK>(u), adds = weights && a.accumulate != 0;
       const int row0 = u.m0 + (int)rank * kHalf + quarter * 32;
       Before<F32> next;
-      const bool adds = MODE == kWeights && a.accumulate != 0;
       if (adds && u.blocks > 0) next.load(a, u, row0 + lane, u.n0 + 32 * half);
       if (u.blocks > 0) {
         const bool got = mbar_wait(acc_full + 8 * acc, acc_phase, abort_flag, a.err, kErrStore);
@@ -562,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
         tc_fence_after();
       }
       const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kTile);
-      const int columns = MODE == kWeights ? min(u.n, a.n - u.n0) : u.count;
-      if (row0 < a.m && !(adds && u.blocks == 0)) {
+      const int columns = weights ? min(u.n, a.wn - u.n0) : u.count;
+      if (row0 < (weights ? a.wm : a.m) && !(adds && u.blocks == 0)) {
         for (int c0 = 32 * half; c0 < columns; c0 += 64) {
           const Before<F32> before = next;
           if (adds && c0 + 64 < columns) next.load(a, u, row0 + lane, u.n0 + c0 + 64);
@@ -575,14 +612,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
 #pragma unroll
             for (int e = 0; e < 32; ++e) r[e] = 0;
           }
-          if constexpr (MODE == kWeights) {
+          if (weights) {
             if (adds) {
 #pragma unroll
               for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) + before.get(e));
             }
-            store_weights<F32>(a, u, row0, u.n0 + c0, r, tile, turn, lane);
+            store_weights<F32>(a, u, row0, u.n0 + c0, r, tiles, turn, lane);
           } else {
-            store_tokens(a, u, row0, c0, r, tile, lane);
+            store_tokens(a, u, row0, c0, r, tiles, turn, lane);
           }
         }
       }
@@ -598,15 +635,15 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
     }
     if (lane == 0) bulk_wait_read_all();  // the stores have read shared memory
     __syncwarp();
-  } else if (MODE == kWeights) {
+  } else if (BACK) {
     // ---- rows behind an expert's tokens ----
     int issued = 0;
     uint32_t tail_phase = 0, fixed_phase = 0;  // a bit a stage
-    for (int pos = pos0; pos < tab.units; pos += step) {
-      const Unit u = unit_at<MODE>(a, tab, pos, expert);
+    for (int pos = deal.begin(); pos < tab.all; pos = deal.after(pos)) {
+      const Unit u = unit_at<BACK>(a, tab, pos);
       issued += u.blocks;
       const int left = u.count % kBlock;
-      if (left == 0) continue;
+      if (!u.weights || left == 0) continue;
       const int stage = (issued - 1) % S;
       if (!mbar_wait_warp(tail + 8 * stage, (tail_phase >> stage) & 1u, abort_flag, a.err, kErrClear)) break;
       tail_phase ^= 1u << stage;
@@ -658,13 +695,13 @@ bool map2(CUtensorMap* tm, const void* base, int64_t x, int64_t y, int box_x, in
   return op_tensor_map(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, step, swizzle);
 }
 
-template <int MODE, bool F32>
+template <bool BACK, bool F32>
 cudaError_t launch(ExpertArgs& a, int sms, int64_t most_units, cudaStream_t st) {
-  using L = Layout<MODE>;
-  cudaError_t e = op_smem_limit<expert_matmul_kernel<MODE, F32>>(L::kBytes);
+  using L = Layout;
+  cudaError_t e = op_smem_limit<expert_matmul_kernel<BACK, F32>>(L::kBytes);
   if (e != cudaSuccess) return e;
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(sms / 2, most_units));
-  return op_launch(expert_matmul_kernel<MODE, F32>, dim3((unsigned)(2 * pairs)), dim3(kThreads), L::kBytes, st, 2, a);
+  return op_launch(expert_matmul_kernel<BACK, F32>, dim3((unsigned)(2 * pairs)), dim3(kThreads), L::kBytes, st, 2, a);
 }
 
 ma_status check(const ma_expert_matmul* d, bool weight) {
@@ -684,13 +721,13 @@ ma_status check(const ma_expert_matmul* d, bool weight) {
   if (!op_aligned(d->offsets, 4)) return op_fail(MA_ERR_ALIGN, "offsets is not aligned to 4 bytes");
   if (d->n_tokens > 0 && weight) {
     if (!d->weight) return op_fail(MA_ERR_ARG, "weight must not be NULL");
+    if (d->weight_row_stride > 1ll << 38 || d->weight_expert_stride > 1ll << 38)
+      return op_fail(MA_ERR_SHAPE, "a stride of the weights is above 2^38");
     if (d->weight_row_stride < d->inner ||
         (d->n_experts > 1 && d->weight_expert_stride < (d->outer - 1) * d->weight_row_stride + d->inner))
       return op_fail(MA_ERR_SHAPE, "the weights' rows or matrices overlap");
     if (!op_aligned(d->weight, 16) || d->weight_row_stride % 8 || (d->n_experts > 1 && d->weight_expert_stride % 8))
       return op_fail(MA_ERR_ALIGN, "the weights' rows do not start on 16-byte boundaries");
-    if (d->weight_row_stride > 1ll << 38 || d->weight_expert_stride > 1ll << 38)
-      return op_fail(MA_ERR_SHAPE, "a stride of the weights is above 2^38");
   }
   return MA_OK;
 }
@@ -706,14 +743,11 @@ ma_status check_rows(const char* name, const void* p, int64_t n, int64_t width, 
 
 ma_status refused_map() { return op_fail(MA_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor"); }
 
-ExpertArgs args_of(const ma_expert_matmul* d, int m, int n, int k, int* err) {
+ExpertArgs args_of(const ma_expert_matmul* d, int* err) {
   ExpertArgs a{};
   a.offsets = d->offsets;
   a.tokens = (int)d->n_tokens;
   a.experts = d->n_experts;
-  a.m = m;
-  a.n = n;
-  a.k = k;
   a.err = err;
   return a;
 }
@@ -742,7 +776,9 @@ ma_status muon_adamw_expert_matmul(const ma_expert_matmul* d, void* out, void* c
     int sms = 0, *err = nullptr;
     cudaError_t e = op_device(&sms, &err);
     if (e != cudaSuccess) return op_cuda(e, "device query");
-    ExpertArgs a = args_of(d, d->outer, 0, d->inner, err);
+    ExpertArgs a = args_of(d, err);
+    a.m = d->outer;
+    a.k = d->inner;
     a.dst = out;
     if (!map3(&a.a, d->weight, false, d->inner, d->outer, d->n_experts, d->weight_row_stride, d->weight_expert_stride,
               kBlock, kHalf, kWide) ||
@@ -751,7 +787,7 @@ ma_status muon_adamw_expert_matmul(const ma_expert_matmul* d, void* out, void* c
         !map3(&a.b_small, d->x, false, d->inner, d->n_tokens, 1, d->x_stride, 0, kBlock, kSmallBox, kWide) ||
         !map2(&a.out, out, d->outer, d->n_tokens, 32, 32, kNarrow))
       return refused_map();
-    e = launch<kForward, false>(a, sms, token_units(a), static_cast<cudaStream_t>(cuda_stream));
+    e = launch<false, false>(a, sms, token_units(a), static_cast<cudaStream_t>(cuda_stream));
     if (e != cudaSuccess) return op_cuda(e, "expert product launch");
   }
   clear_last_error();
@@ -777,36 +813,44 @@ ma_status muon_adamw_expert_matmul_backward(const ma_expert_matmul* d, const voi
   cudaError_t e = op_device(&sms, &err);
   if (e != cudaSuccess) return op_cuda(e, "device query");
   const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  if (dx && d->n_tokens > 0) {
-    ExpertArgs a = args_of(d, d->inner, 0, d->outer, err);
-    a.dst = dx;
-    if (!map3(&a.a, d->weight, false, d->inner, d->outer, d->n_experts, d->weight_row_stride, d->weight_expert_stride,
-              64, kBlock, kWide) ||
-        !map3(&a.b, dout, false, d->outer, d->n_tokens, 1, dout_stride, 0, kBlock, kHalf, kWide) ||
-        !map3(&a.b_mid, dout, false, d->outer, d->n_tokens, 1, dout_stride, 0, kBlock, kMidBox, kWide) ||
-        !map3(&a.b_small, dout, false, d->outer, d->n_tokens, 1, dout_stride, 0, kBlock, kSmallBox, kWide) ||
-        !map2(&a.out, dx, d->inner, d->n_tokens, 32, 32, kNarrow))
-      return refused_map();
-    e = launch<kInput, false>(a, sms, token_units(a), s);
-    if (e != cudaSuccess) return op_cuda(e, "expert input gradient launch");
-  }
   const bool f32 = grad_dtype == MA_DT_F32;
-  if (dweight && d->n_tokens == 0 && !accumulate) {
-    e = cudaMemsetAsync(dweight, 0, (size_t)d->n_experts * d->outer * d->inner * op_dtype_size(grad_dtype), s);
-    if (e != cudaSuccess) return op_cuda(e, "expert weight gradient");
-  } else if (dweight && d->n_tokens > 0) {
-    ExpertArgs a = args_of(d, d->outer, d->inner, 0, err);
-    a.dst = dweight;
-    a.accumulate = accumulate;
-    if (!map3(&a.a, dout, false, d->outer, d->n_tokens, 1, dout_stride, 0, 64, kBlock, kWide) ||
-        !map3(&a.b, d->x, false, d->inner, d->n_tokens, 1, d->x_stride, 0, 64, kBlock, kWide) ||
-        !map3(&a.out, dweight, f32, d->inner, d->outer, d->n_experts, d->inner, (int64_t)d->outer * d->inner, f32 ? 16 : 32,
-              32, kNarrow))
-      return refused_map();
-    const int64_t units =
-        (int64_t)d->n_experts * ((a.m + kTile - 1) / kTile) * ((a.n + kTile - 1) / kTile);
-    e = f32 ? launch<kWeights, true>(a, sms, units, s) : launch<kWeights, false>(a, sms, units, s);
-    if (e != cudaSuccess) return op_cuda(e, "expert weight gradient launch");
+  if (d->n_tokens == 0) {
+    if (dweight && !accumulate) {
+      e = cudaMemsetAsync(dweight, 0, (size_t)d->n_experts * d->outer * d->inner * op_dtype_size(grad_dtype), s);
+      if (e != cudaSuccess) return op_cuda(e, "expert weight gradient");
+    }
+  } else if (dx || dweight) {
+    ExpertArgs a = args_of(d, err);
+    int64_t units = 0;
+    if (dx) {
+      a.m = d->inner;
+      a.k = d->outer;
+      a.dst = dx;
+      if (!map3(&a.a, d->weight, false, d->inner, d->outer, d->n_experts, d->weight_row_stride,
+                d->weight_expert_stride, 64, kBlock, kWide) ||
+          !map3(&a.b, dout, false, d->outer, d->n_tokens, 1, dout_stride, 0, kBlock, kHalf, kWide) ||
+          !map3(&a.b_mid, dout, false, d->outer, d->n_tokens, 1, dout_stride, 0, kBlock, kMidBox, kWide) ||
+          !map3(&a.b_small, dout, false, d->outer, d->n_tokens, 1, dout_stride, 0, kBlock, kSmallBox, kWide) ||
+          !map2(&a.out, dx, d->inner, d->n_tokens, 32, 32, kNarrow))
+        return refused_map();
+      units += token_units(a);
+    }
+    if (dweight) {
+      a.wm = d->outer;
+      a.wn = d->inner;
+      a.grad = dweight;
+      a.accumulate = accumulate;
+      if (!map3(&a.wa, dout, false, d->outer, d->n_tokens, 1, dout_stride, 0, 64, kBlock, kWide) ||
+          !map3(&a.wb, d->x, false, d->inner, d->n_tokens, 1, d->x_stride, 0, 64, kBlock, kWide) ||
+          !map3(&a.wout, dweight, f32, d->inner, d->outer, d->n_experts, d->inner, (int64_t)d->outer * d->inner,
+                f32 ? 16 : 32, 32, kNarrow))
+        return refused_map();
+      units += (int64_t)d->n_experts * ((a.wm + kTile - 1) / kTile) * ((a.wn + kTile - 1) / kTile);
+    }
+    // a unit of dx has its contraction's blocks, one of the weights its expert's tokens' or, for few, the time of nine
+    a.rounds = (d->outer + kBlock - 1) / kBlock / (int)std::max<int64_t>(d->n_tokens / d->n_experts / kBlock, 9);
+    e = f32 ? launch<true, true>(a, sms, units, s) : launch<true, false>(a, sms, units, s);
+    if (e != cudaSuccess) return op_cuda(e, "expert gradient launch");
   }
   clear_last_error();
   return MA_OK;
