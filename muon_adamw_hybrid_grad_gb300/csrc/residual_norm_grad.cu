@@ -395,6 +395,12 @@ cudaError_t launch_ring(const NormArgs& a, cudaStream_t st) {
   const int stages = ring_stages<TX, TS>(a, kGroups);
   const int row = a.w * (int)(sizeof(TX) + sizeof(TS) * (a.dres ? 2 : 1));
   const int smem = std::max(stages * kGroups * row, kRingThreads * V * 32);  // the rows, then the shares of dw
+  if (a.n <= 2 * kGroups && op_aligned(a.dweight, 8)) {
+    // two rows a group at most: one block, whose partial row is the whole sum
+    NormArgs one = a;
+    one.partial = a.dweight;
+    return op_launch(kernel, dim3(1), dim3(kRingThreads), smem, st, 1, one, stages, err);
+  }
   const int blocks = (int)std::min<int64_t>(sms, (a.n + kGroups - 1) / kGroups);
   e = op_launch(kernel, dim3(blocks), dim3(kRingThreads), smem, st, 1, a, stages, err);
   return e == cudaSuccess ? join(a, blocks, st) : e;
