@@ -251,6 +251,25 @@ def test_residual_norm_shapes(ops):
                        ops.residual_norm_backward(shared.contiguous(), None, r, w)[1])
 
 
+def test_residual_norm_past_2_31_elements(ops):
+    n, width = 1_050_007, 2056
+    x, res = (torch.empty(n, width, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    x.normal_(generator=gen)
+    res.normal_(generator=gen)
+    w, how = cuda(np.linspace(0.5, 1.5, width)), {"eps": 1e-5, "p": 0.5, "rng": rng_of(SEED, STEP), "site": 2}
+    y, r = ops.residual_norm(x, res, w, **how)
+    dx, dr, _ = ops.residual_norm_backward(x, res, r, w, **how)
+    for rows in (slice(0, 2), slice(n - 3, n)):
+        f = factors((rows.stop - rows.start) * width, 0.5, 2, first=rows.start * width).reshape(-1, width)
+        wy, wr, by, br = O.residual_norm(host(x[rows]), host(res[rows]), host(w), 1e-5, f)
+        within(y[rows], wy, by)
+        within(r[rows], wr, br)
+        (wx, wd, _), (bx, bd, _) = O.residual_norm_backward(host(x[rows]), host(res[rows]), host(r[rows]), host(w), 1e-5, f)
+        within(dx[rows], wx, bx)
+        within(dr[rows], wd, bd)
+
+
 # ---- log probabilities ----
 
 def logit_rows(rng, n, v):
@@ -540,6 +559,24 @@ def test_expert_matmul_of_many_units(ops, lengths, inner, outer):
             bound = (k + 16) * O.U32 * mag
             assert bool(((got.double() - want).abs() <= bound + UNIT[got.dtype] * (want.abs() + bound)).all())
     ops.check()
+
+
+def test_expert_matmul_past_2_31_elements(ops):
+    lengths, inner, outer = (1, 263001, 7), 16, 8200
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    t, off = sum(lengths) + 5, offsets_of(lengths)
+    x = torch.randn(t, inner, generator=gen, device="cuda").bfloat16()
+    w = torch.randn(3, outer, inner, generator=gen, device="cuda").bfloat16()
+    out = ops.expert_matmul(x, w, off)
+    for rows in (slice(0, 40), slice(263001 // 2, 263001 // 2 + 40), slice(t - 40, t)):
+        local = [min(max(int(o) - rows.start, 0), 40) for o in off]
+        want, mag = O.expert_matmul(host(x[rows]), host(w), local)
+        within(out[rows], want, (inner + 16) * O.U32 * mag)
+    dx, _ = ops.expert_matmul_backward(out, x, w, off, None)
+    rows = slice(t - 40, t)
+    (want, _), (mag, _) = O.expert_matmul_backward(host(out[rows]), host(x[rows]), host(w),
+                                                   [min(max(int(o) - rows.start, 0), 40) for o in off])
+    within(dx[rows], want, (outer + 16) * O.U32 * mag)
 
 
 # ---- refusals, streams, graphs, autograd ----
