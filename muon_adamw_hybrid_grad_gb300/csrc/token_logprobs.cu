@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
 // d_v = scale (dlogprob (1[v = id] - p_v) - dentropy p_v (log p_v + entropy))
 
 struct GradRow {
-  float shift, c, base, slope, given;  // d = 2^a (base + slope a) [+ given], a = (x - shift) c
+  float shift, rest, c, base, slope, given;  // d = 2^a (base + slope a) [+ given], a = (x - shift - rest) c
   int64_t id;
   bool empty;
 };
@@ -519,7 +519,9 @@ __device__ __forceinline__ GradRow grad_row(const LogprobArgs& a, int64_t at) {
   const float lse = __ldg(a.lse_in + at), h = a.dentropy ? __ldg(a.dentropy + at) : 0.f;
   g.id = token_id(a, at);
   const float l = a.dlogprobs && g.id >= 0 && g.id < a.vocab ? __ldg(a.dlogprobs + at) : 0.f;
+  // lse / scale in two parts: its rounding would scale the whole row
   g.shift = lse / a.scale;
+  g.rest = fmaf(-g.shift, a.scale, lse) / a.scale;
   g.c = a.scale * kLog2e;
   g.given = a.scale * l;
   g.base = -a.scale * (h == 0.f ? l : fmaf(h, __ldg(a.entropy_in + at), l));
@@ -529,7 +531,7 @@ __device__ __forceinline__ GradRow grad_row(const LogprobArgs& a, int64_t at) {
 }
 
 __device__ __forceinline__ float grad_of(const GradRow& g, float x) {
-  const float a = max_nan((x - g.shift) * g.c, -1e30f);
+  const float a = max_nan((x - g.shift - g.rest) * g.c, -1e30f);
   return g.empty ? 0.f : ex2(a) * fmaf(g.slope, a, g.base);
 }
 
