@@ -445,11 +445,12 @@ MA_API ma_status muon_adamw_grad_norm_noalloc(const void* const* grads, const in
 
 /* ---- Operators of the training step ----
  * The article's optimizer takes gradients that a model's training step has
- * produced; it has no counterpart to these calls. They are three operators of
- * that step, each with its gradient: the embedding lookup, the norm and
- * rotation of queries and keys, and causal attention with a sliding window
- * and sink tokens. Their gradients come out in the layouts and types that
- * muon_adamw_register_param takes.
+ * produced; it has no counterpart to these calls. They are operators of that
+ * step, each with its gradient: the embedding lookup, the norm and rotation of
+ * queries and keys, causal attention with a sliding window and sink tokens,
+ * dropout, the residual's addition with RMS norm, products grouped by expert,
+ * and the log probabilities of given tokens. Their gradients come out in the
+ * layouts and types that muon_adamw_register_param takes.
  *
  * Conventions: no handle; work is queued on cuda_stream (a cudaStream_t of the
  * current device, NULL = legacy default stream) and the call does not wait for

@@ -6,7 +6,8 @@ kernels of ``lib/libmuon_adamw_gb300.so`` behind the C ABI declared in
 ``MuonAdamW`` class is a convenience wrapper that takes torch tensors and
 passes their device pointers and the current CUDA stream. The operators of
 the training step (embedding, query/key norm and rotation, sliding-window
-attention) have their wrappers over torch tensors in the module ``ops``.
+attention, dropout, residual norm, expert products, token log probabilities)
+have their wrappers over torch tensors in the module ``ops``.
 
 There is no fallback: if the shared library has not been built, every call
 raises ``LibraryNotBuilt`` (run ``muon_adamw_hybrid_grad_gb300.build.build()``).
