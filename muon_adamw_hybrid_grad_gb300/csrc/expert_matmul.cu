@@ -56,14 +56,22 @@ constexpr uint32_t kTmemColumns = 512;
 // error codes of the waits that ran out
 constexpr int kErrLoad = 0x501, kErrProduct = 0x502, kErrStore = 0x503, kErrClear = 0x504, kErrAlign = 0x505;
 
+// Division of numbers below 2^31 by a divisor that the host knows: every warp takes every unit apart, and a division
+// takes longer than the products of a small one.
+struct Divisor {
+  uint32_t d, mul, shift;  // mul 0: a power of two
+};
+
 struct ExpertArgs {
   // the product whose columns are tokens: out, or dx
   CUtensorMap a, b, b_mid, b_small, out;
   int m, k;  // rows of D; the contraction, 0: no such product
+  Divisor band;  // units of kRaster token tiles
   void* dst;
   // the weights' gradients
   CUtensorMap wa, wb, wout;
   int wm, wn;  // rows (0: no such product) and columns
+  Divisor wunits, wband;  // units of an expert; of kRaster column tiles
   void* grad;
   int accumulate;
   int rounds;  // units of these that take as long as one of dx
@@ -138,6 +146,11 @@ __device__ __forceinline__ void commit_own_warp(uint32_t bar) {
       "elect.sync _|q, 0xffffffff;\n\t"
       "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar)
       : "memory");
+}
+// An arrival at a barrier of either CTA of threads that have read TMEM (behind tc_fence_before). Nothing else is
+// handed over, so that it need not wait for their writes to be visible in the cluster: that took 2500 cycles a unit.
+__device__ __forceinline__ void arrive_either(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 // A wait whose outcome is the whole warp's, on a barrier at which the other CTA arrives too.
 __device__ __forceinline__ bool mbar_wait_warp_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag,
@@ -227,17 +240,26 @@ struct Deal {
   }
 };
 
+__device__ __forceinline__ int divide(int n, const Divisor& d) {
+  return d.mul ? (int)(__umulhi((uint32_t)n, d.mul) >> d.shift) : n >> d.shift;
+}
+// Of r below 2^18 by at most kRaster.
+__device__ __forceinline__ int divide_small(int r, int by) {
+  return by == kRaster ? r / kRaster : __float2int_rz(__fdividef((float)r + 0.5f, (float)by));
+}
+
 template <bool BACK>
 __device__ __forceinline__ Unit unit_at(const ExpertArgs& a, Units& all, int pos) {
   Unit u;
   u.weights = pos >= all.tokens;
   if (is_weights<BACK>(u)) {
-    const int mt = ceil_div(a.wm, kTile), nt = ceil_div(a.wn, kTile), local = (pos - all.tokens) % (mt * nt);
-    u.expert = (pos - all.tokens) / (mt * nt);
-    const int group = local / (kRaster * mt), width = min(kRaster, nt - group * kRaster);
-    const int r = local - group * kRaster * mt;
-    u.m0 = r / width * kTile;
-    u.n0 = (group * kRaster + r % width) * kTile;
+    const int nt = ceil_div(a.wn, kTile);
+    u.expert = divide(pos - all.tokens, a.wunits);
+    const int local = pos - all.tokens - u.expert * (int)a.wunits.d;
+    const int group = divide(local, a.wband), width = min(kRaster, nt - group * kRaster);
+    const int r = local - group * (int)a.wband.d, row = divide_small(r, width);
+    u.m0 = row * kTile;
+    u.n0 = (group * kRaster + r - row * width) * kTile;
     u.n = a.wn - u.n0 > kHalf ? kTile : kHalf;
     u.at = all.bound[u.expert];
     u.count = all.bound[u.expert + 1] - u.at;
@@ -252,12 +274,12 @@ __device__ __forceinline__ Unit unit_at(const ExpertArgs& a, Units& all, int pos
       if (pos < all.first + tt * mt) break;
     }
     const int local = pos - all.first;
-    const int group = local / (kRaster * mt), width = min(kRaster, tt - group * kRaster);
-    const int r = local - group * kRaster * mt;
+    const int group = divide(local, a.band), width = min(kRaster, tt - group * kRaster);
+    const int r = local - group * (int)a.band.d, row = divide_small(r, width);
     // token tiles of one size; the last is never empty, since count > 256 (tt - 1)
-    const int per = (ceil_div(count, tt) + 31) & ~31, tile = group * kRaster + r % width;
+    const int per = ((tt == 1 ? count : ceil_div(count, tt)) + 31) & ~31, tile = group * kRaster + r - row * width;
     u.expert = all.expert;
-    u.m0 = r / width * kTile;
+    u.m0 = row * kTile;
     u.n0 = 0;
     u.at = begin + tile * per;
     u.count = min(per, count - tile * per);
@@ -626,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
       if (u.blocks > 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(acc_free + 8 * acc, 0));
+        if (lane == 0) arrive_either(mapa_shared(acc_free + 8 * acc, 0));
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
@@ -743,6 +765,14 @@ ma_status check_rows(const char* name, const void* p, int64_t n, int64_t width, 
 
 ma_status refused_map() { return op_fail(MA_ERR_CUDA, "cuTensorMapEncodeTiled refused a tensor"); }
 
+Divisor divisor(int64_t d) {
+  uint32_t s = 0;
+  while ((2ll << s) <= d) ++s;  // 2^s <= d < 2^(s + 1)
+  if ((1ll << s) == d) return {(uint32_t)d, 0, s};
+  // with e = mul d - 2^(32 + s) <= d: n e < 2^31 2^(s + 1), so that the quotient's fraction is not carried over
+  return {(uint32_t)d, (uint32_t)((1ull << (32 + s)) / (uint64_t)d + 1), s};
+}
+
 ExpertArgs args_of(const ma_expert_matmul* d, int* err) {
   ExpertArgs a{};
   a.offsets = d->offsets;
@@ -779,6 +809,7 @@ ma_status muon_adamw_expert_matmul(const ma_expert_matmul* d, void* out, void* c
     ExpertArgs a = args_of(d, err);
     a.m = d->outer;
     a.k = d->inner;
+    a.band = divisor(kRaster * ((a.m + kTile - 1) / kTile));
     a.dst = out;
     if (!map3(&a.a, d->weight, false, d->inner, d->outer, d->n_experts, d->weight_row_stride, d->weight_expert_stride,
               kBlock, kHalf, kWide) ||
@@ -825,6 +856,7 @@ ma_status muon_adamw_expert_matmul_backward(const ma_expert_matmul* d, const voi
     if (dx) {
       a.m = d->inner;
       a.k = d->outer;
+      a.band = divisor(kRaster * ((a.m + kTile - 1) / kTile));
       a.dst = dx;
       if (!map3(&a.a, d->weight, false, d->inner, d->outer, d->n_experts, d->weight_row_stride,
                 d->weight_expert_stride, 64, kBlock, kWide) ||
@@ -838,6 +870,9 @@ ma_status muon_adamw_expert_matmul_backward(const ma_expert_matmul* d, const voi
     if (dweight) {
       a.wm = d->outer;
       a.wn = d->inner;
+      const int64_t mt = (a.wm + kTile - 1) / kTile, nt = (a.wn + kTile - 1) / kTile;
+      a.wunits = divisor(mt * nt);
+      a.wband = divisor(mt * kRaster);
       a.grad = dweight;
       a.accumulate = accumulate;
       if (!map3(&a.wa, dout, false, d->outer, d->n_tokens, 1, dout_stride, 0, 64, kBlock, kWide) ||
@@ -845,7 +880,7 @@ ma_status muon_adamw_expert_matmul_backward(const ma_expert_matmul* d, const voi
           !map3(&a.wout, dweight, f32, d->inner, d->outer, d->n_experts, d->inner, (int64_t)d->outer * d->inner,
                 f32 ? 16 : 32, 32, kNarrow))
         return refused_map();
-      units += (int64_t)d->n_experts * ((a.wm + kTile - 1) / kTile) * ((a.wn + kTile - 1) / kTile);
+      units += d->n_experts * mt * nt;
     }
     // a unit of dx has its contraction's blocks, one of the weights its expert's tokens' or, for few, the time of nine
     a.rounds = (d->outer + kBlock - 1) / kBlock / (int)std::max<int64_t>(d->n_tokens / d->n_experts / kBlock, 9);
