@@ -130,14 +130,14 @@ __device__ __forceinline__ void umma_pair_warp(uint32_t d_tmem, uint64_t adesc, 
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// The products issued so far have ended: one arrival in each CTA of the pair.
-__device__ __forceinline__ void commit_pair_warp(uint32_t bar, uint32_t odd_bar) {
+// The products issued so far have ended: one arrival on the barrier at this offset in each CTA of the pair.
+__device__ __forceinline__ void commit_pair_warp(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
       "elect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t"
-      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}\n" ::"r"(bar),
-      "r"(odd_bar)
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(
+          bar),
+      "h"((uint16_t)3)
       : "memory");
 }
 __device__ __forceinline__ void commit_own_warp(uint32_t bar) {
@@ -186,8 +186,34 @@ __device__ __forceinline__ void load_pair_warp(uint32_t dst, const CUtensorMap* 
       : "memory");
 }
 
-// Until at most the last bulk store of this thread still reads shared memory.
-__device__ __forceinline__ void bulk_wait_read_but_one() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
+// Stores out of shared memory, a group each, and the wait until at most the last one still reads it.
+__device__ __forceinline__ void store_2d_warp(const CUtensorMap* tm, uint32_t src, int x, int y) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t"
+      "@q cp.async.bulk.commit_group;\n\t}\n" ::"l"(reinterpret_cast<uint64_t>(tm)),
+      "r"(src), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void store_3d_warp(const CUtensorMap* tm, uint32_t src, int x, int y, int z) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];\n\t"
+      "@q cp.async.bulk.commit_group;\n\t}\n" ::"l"(reinterpret_cast<uint64_t>(tm)),
+      "r"(src), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void stores_read_warp() {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q cp.async.bulk.wait_group.read %0;\n\t}\n" ::"n"(LEFT)
+      : "memory");
+  __syncwarp();
+}
 __device__ __forceinline__ uint32_t pack(uint32_t lo, uint32_t hi) {
   return op_pack_bf16(__uint_as_float(lo), __uint_as_float(hi));
 }
@@ -340,8 +366,7 @@ __device__ __forceinline__ void store_tokens(const ExpertArgs& a, const Unit& u,
                                              const uint32_t (&r)[32], uint8_t* tiles, int& turn, int lane) {
   uint8_t* const tile = tiles + turn * Layout::kTileBytes;
   turn ^= 1;
-  if (lane == 0) bulk_wait_read_but_one();  // this tile's last store has read it
-  __syncwarp();
+  stores_read_warp<1>();  // this tile's last store has read it
   // rows of 64 bytes, 16-byte chunk q of row t at q ^ (t / 2 % 4): lanes 2 k and 2 k + 1 swap, the even one writes
   // the pair's even tokens, the odd one its odd ones
   uint8_t* const to = tile + (lane & 1) * 64 + ((lane >> 1) & 3) * 4;
@@ -355,10 +380,7 @@ __device__ __forceinline__ void store_tokens(const ExpertArgs& a, const Unit& u,
   if (c0 + 32 <= u.count) {
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) {
-      tma_store_2d(&a.out, smem_u32(tile), row0, u.at + c0);
-      bulk_commit();
-    }
+    store_2d_warp(&a.out, smem_u32(tile), row0, u.at + c0);
     return;
   }
   __syncwarp();
@@ -371,7 +393,8 @@ __device__ __forceinline__ void store_tokens(const ExpertArgs& a, const Unit& u,
           *reinterpret_cast<const uint4*>(tile + t * 64 + ((q ^ ((t >> 1) & 3)) << 4));
   }
   __syncwarp();
-  if (lane == 0) bulk_commit();  // an empty group, so that the tiles' turns and the groups stay in step
+  // an empty group, so that the tiles' turns and the groups stay in step
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t@q cp.async.bulk.commit_group;\n\t}\n" ::: "memory");
 }
 
 // What an expert's gradient holds so far in a lane's 32 columns of a block, as it lies in memory.
@@ -400,8 +423,7 @@ __device__ __forceinline__ void store_weights(const ExpertArgs& a, const Unit& u
 #pragma unroll
   for (int h = 0; h < (F32 ? 2 : 1); ++h, turn ^= 1) {
     uint8_t* const tile = tiles + turn * Layout::kTileBytes;
-    if (lane == 0) bulk_wait_read_but_one();  // this tile's last store has read it
-    __syncwarp();
+    stores_read_warp<1>();  // this tile's last store has read it
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       uint4 v;
@@ -414,10 +436,8 @@ __device__ __forceinline__ void store_weights(const ExpertArgs& a, const Unit& u
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) {
-      if (col0 + 16 * h < a.wn) tma_store_3d(&a.wout, smem_u32(tile), col0 + 16 * h, row0, u.expert);
-      bulk_commit();
-    }
+    // (the second half of 32 fp32 columns may lie outside: nothing of it is written)
+    store_3d_warp(&a.wout, smem_u32(tile), col0 + 16 * h, row0, u.expert);
   }
 }
 
@@ -554,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
-      const uint32_t s0 = smem_u32(smem), empty_odd = mapa_shared(empty, 1);
+      const uint32_t s0 = smem_u32(smem);
       // MN-major: panels of 64 columns, sixteen rows of the contraction 2 KB further
       constexpr int kStepA = BACK ? 128 : 2;
       const uint64_t a0 = BACK ? sdesc(s0, kPanel, 1024) : sdesc(s0, 16, 1024);
@@ -586,14 +606,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
                 umma_pair_warp(d, ad + kStepA * i, b_mn + off + 128 * i, idesc, (b | i) != 0 ? 1u : 0u);
             }
           }
-          commit_pair_warp(empty + 8 * stage, empty_odd + 8 * stage);
+          commit_pair_warp(empty + 8 * stage);
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        commit_pair_warp(acc_full + 8 * acc, mapa_shared(acc_full + 8 * acc, 1));
+        commit_pair_warp(acc_full + 8 * acc);
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
@@ -655,8 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
         }
       }
     }
-    if (lane == 0) bulk_wait_read_all();  // the stores have read shared memory
-    __syncwarp();
+    stores_read_warp<0>();  // the stores have read shared memory
   } else if (BACK) {
     // ---- rows behind an expert's tokens ----
     int issued = 0;
