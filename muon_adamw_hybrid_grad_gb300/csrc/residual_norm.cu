@@ -54,19 +54,19 @@ __global__ void __launch_bounds__(RowThreads<T>::kBlock) residual_norm_kernel(co
   RowVec<TX, VEC> rx[V];
   RowVec<TS, VEC> rr[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) rx[j].load(x, (j * T + t) * 8, a.w);
+  for (int j = 0; j < V; ++j) rx[j].load(x, col_of<VEC, T>(j, t), a.w);
   if (res) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) rr[j].load(res, (j * T + t) * 8, a.w);
+    for (int j = 0; j < V; ++j) rr[j].load(res, col_of<VEC, T>(j, t), a.w);
   }
   float r[V][8];
 #pragma unroll
-  for (int j = 0; j < V; ++j) rx[j].get((j * T + t) * 8, a.w, r[j]);
+  for (int j = 0; j < V; ++j) rx[j].get(col_of<VEC, T>(j, t), a.w, r[j]);
   if (a.drop.threshold) drop_row<VEC, T>(drop_key(a.drop), row * a.w, t, r);
   float ss = 0.f;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int col = (j * T + t) * 8;
+    const int col = col_of<VEC, T>(j, t);
     if (res) {
       float s[8];
       rr[j].get(col, a.w, s);
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(RowThreads<T>::kBlock) residual_norm_kernel(co
   float top = 0.f;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int col = (j * T + t) * 8;
+    const int col = col_of<VEC, T>(j, t);
     float w[8];
     load_weight<VEC>(a.weight, col, a.w, w);
 #pragma unroll
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(RowThreads<T>::kBlock) residual_norm_kernel(co
   uint8_t* const q = static_cast<uint8_t*>(a.y) + row * a.w;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int col = (j * T + t) * 8;
+    const int col = col_of<VEC, T>(j, t);
     uint32_t p[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(RowThreads<T>::kBlock) residual_norm_kernel(co
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (col + e < a.w) q[col + e] = (uint8_t)(p[e / 2] >> (8 * (e & 1)));
+        if (col + 32 * e < a.w) q[col + 32 * e] = (uint8_t)(p[e / 2] >> (8 * (e & 1)));
     }
   }
 }
@@ -128,8 +128,12 @@ template <typename TX, typename TS>
 cudaError_t forward(const NormArgs& a, bool vec, cudaStream_t st) {
   const int units = (a.w + 7) / 8;
   if (!vec) {
-    if (units <= 32 * 8) return launch<TX, TS, 32, 8, false>(a, st);
-    if (units <= 128 * 8) return launch<TX, TS, 128, 8, false>(a, st);
+    if (units <= 32) return launch<TX, TS, 32, 1, false>(a, st);
+    if (units <= 128) return launch<TX, TS, 64, 2, false>(a, st);
+    if (units <= 256) return launch<TX, TS, 128, 2, false>(a, st);
+    if (units <= 384) return launch<TX, TS, 192, 2, false>(a, st);
+    if (units <= 512) return launch<TX, TS, 128, 4, false>(a, st);
+    if (units <= 1024) return launch<TX, TS, 256, 4, false>(a, st);
     return launch<TX, TS, 512, 8, false>(a, st);
   }
   // Two to four vectors a thread: enough loads in flight, and warps enough to hide the generator. 64M elements of bf16
@@ -140,6 +144,7 @@ cudaError_t forward(const NormArgs& a, bool vec, cudaStream_t st) {
   if (units <= 64) return launch<TX, TS, 32, 2, true>(a, st);
   if (units <= 128) return launch<TX, TS, 64, 2, true>(a, st);
   if (units <= 256) return launch<TX, TS, 128, 2, true>(a, st);
+  if (units <= 384) return launch<TX, TS, 192, 2, true>(a, st);
   if (units <= 512) return launch<TX, TS, 128, 4, true>(a, st);
   if (units <= 1024) return launch<TX, TS, 256, 4, true>(a, st);
   if (units <= 2048) return launch<TX, TS, 512, 4, true>(a, st);

@@ -50,13 +50,13 @@ struct GradRow {
     const TX* const py = static_cast<const TX*>(a.dy) + row * a.dys;
     const TS* const pr = static_cast<const TS*>(a.r) + row * a.ress;
 #pragma unroll
-    for (int j = 0; j < V; ++j) dy[j].load(py, (j * T + t) * 8, a.w);
+    for (int j = 0; j < V; ++j) dy[j].load(py, col_of<VEC, T>(j, t), a.w);
 #pragma unroll
-    for (int j = 0; j < V; ++j) r[j].load(pr, (j * T + t) * 8, a.w);
+    for (int j = 0; j < V; ++j) r[j].load(pr, col_of<VEC, T>(j, t), a.w);
     if (a.dres) {
       const TS* const pd = static_cast<const TS*>(a.dres) + row * a.dress;
 #pragma unroll
-      for (int j = 0; j < V; ++j) dres[j].load(pd, (j * T + t) * 8, a.w);
+      for (int j = 0; j < V; ++j) dres[j].load(pd, col_of<VEC, T>(j, t), a.w);
     }
   }
 };
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(RowGroups<T>::kBlock) residual_norm_grad_kerne
     float ss = 0.f, gr = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int col = (j * T + t) * 8;
+      const int col = col_of<VEC, T>(j, t);
       float dy[8], r[8], w[8];
       cur.dy[j].get(col, a.w, dy);
       cur.r[j].get(col, a.w, r);
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(RowGroups<T>::kBlock) residual_norm_grad_kerne
     const float c = gr / (float)a.w * rstd * rstd * rstd;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int col = (j * T + t) * 8;
+      const int col = col_of<VEC, T>(j, t);
       float dy[8], r[8], w[8], d[8];
       cur.dy[j].get(col, a.w, dy);
       cur.r[j].get(col, a.w, r);
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(RowGroups<T>::kBlock) residual_norm_grad_kerne
       }
       store_row<VEC>(static_cast<TS*>(a.dr) + row * a.w, col, a.w, d);
       if (a.dx) {
-        if (a.drop.threshold) drop8_at<VEC>(key, row * a.w + col, d);
+        if (a.drop.threshold) drop_vector<VEC, T>(key, row * a.w, j, t, d);
         store_row<VEC>(static_cast<TX*>(a.dx) + row * a.w, col, a.w, d);
       }
     }
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(RowGroups<T>::kBlock) residual_norm_grad_kerne
   }
   float* const out = a.partial + (int64_t)blockIdx.x * a.w;
 #pragma unroll
-  for (int j = 0; j < V; ++j) store_row<VEC>(out, (j * T + t) * 8, a.w, dw[j]);
+  for (int j = 0; j < V; ++j) store_row<VEC>(out, col_of<VEC, T>(j, t), a.w, dw[j]);
 }
 
 // ---- rows through a ring of shared memory ----
@@ -411,8 +411,11 @@ cudaError_t backward(const NormArgs& a, bool vec, cudaStream_t st) {
   const int units = (a.w + 7) / 8;
   if (a.n == 0) return join(a, 0, st);
   if (!vec) {
+    if (units <= 32) return launch<TX, TS, 32, 1, false>(a, st);
     if (units <= 128) return launch<TX, TS, 64, 2, false>(a, st);
-    if (units <= 1024) return launch<TX, TS, 256, 4, false>(a, st);
+    if (units <= 256) return launch<TX, TS, 128, 2, false>(a, st);
+    if (units <= 512) return launch<TX, TS, 256, 2, false>(a, st);
+    if (units <= 1024) return launch<TX, TS, 512, 2, false>(a, st);
     return launch<TX, TS, 512, 8, false>(a, st);
   }
   if (units <= 32) return launch_ring<TX, TS, 32, 1>(a, st);
