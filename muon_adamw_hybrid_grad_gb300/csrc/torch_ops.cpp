@@ -427,6 +427,12 @@ Rows2 rows_of(const Tensor& t, const char* name) {
 
 int32_t small(int64_t v) { return (int32_t)(v > INT32_MAX ? INT32_MAX : v < INT32_MIN ? INT32_MIN : v); }
 
+// Past 31 bits: no other call's number, but -1, which is refused.
+int32_t site_of(PyObject* o) {
+  const int64_t v = integer(o);
+  return v < 0 || v > INT32_MAX ? -1 : (int32_t)v;
+}
+
 // seed and step; null where None
 const int64_t* rng_of(PyObject* o, const Tensor& like) {
   if (o == Py_None) return nullptr;
@@ -445,7 +451,7 @@ PyObject* dropout(PyObject* const* a) {
   const double p = real(a[1]);
   if (a[2] == Py_None) refuse(PyExc_ValueError, "rng must be 2 contiguous int64 values: seed and step");
   const int64_t* rng = rng_of(a[2], x);
-  const int32_t site = small(integer(a[3]));
+  const int32_t site = site_of(a[3]);
   Tensor out = make(x.sizes(), x.scalar_type(), x);
   // an empty tensor has no address
   const void* in = x.numel() ? x.const_data_ptr() : rng;
@@ -474,7 +480,7 @@ void read_norm(Norm& r, const Rows2& x, int dtype, int stream_dtype, PyObject* c
   d.eps = real(o[1]);
   d.p = real(o[2]);
   d.rng = rng_of(o[3], x.t);
-  d.site = small(integer(o[4]));
+  d.site = site_of(o[4]);
   d.reserved = 0;
   r.drops = !(d.p < 0.5 / 65536);
 }

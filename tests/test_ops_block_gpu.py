@@ -591,6 +591,8 @@ def test_refusals(ops):
         (TypeError, lambda: ops.dropout(x.half(), 0.1, rng)), (MuonAdamWError, lambda: ops.dropout(x, 1.5, rng)),
         (ValueError, lambda: ops.dropout(x, 0.1, None)), (ValueError, lambda: ops.dropout(x, 0.1, rng.int())),
         (ValueError, lambda: ops.dropout(x, 0.1, rng.cpu())), (MuonAdamWError, lambda: ops.dropout(x, 0.1, rng, site=-1)),
+        (MuonAdamWError, lambda: ops.dropout(x, 0.1, rng, site=2 ** 31)),
+        (MuonAdamWError, lambda: ops.residual_norm(x, x, w, p=0.1, rng=rng, site=2 ** 32)),
         (ValueError, lambda: ops.residual_norm(x, x[:2], w)), (ValueError, lambda: ops.residual_norm(x, x, w[:8])),
         (ValueError, lambda: ops.residual_norm(x, x, w.bfloat16())), (MuonAdamWError, lambda: ops.residual_norm(x, x, w, p=0.1)),
         (MuonAdamWError, lambda: ops.residual_norm(x.float(), x, w)),
