@@ -648,7 +648,7 @@ MA_API ma_status muon_adamw_residual_norm_backward(const ma_residual_norm* d, co
 /* Products grouped by expert: out[t] = weight[e] x[t] for the tokens t of
  * expert e, offsets[e] to offsets[e + 1] - 1.
  *   n_experts  1 .. 512; inner (x's width) and outer (out's) multiples of 8 in
- *              [8, 2^20]; n_tokens in [0, 2^30]; all tensors bf16, sums fp32 as
+ *              [8, 2^20]; n_tokens in [0, 2^28]; all tensors bf16, sums fp32 as
  *              the tensor cores form them (toward zero: an fp32 gradient of the
  *              weights is off by about 1e-9 of itself for each token);
  *   offsets    device, n_experts + 1 int32 values, ascending from 0 and at most

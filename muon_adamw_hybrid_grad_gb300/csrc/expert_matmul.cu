@@ -722,7 +722,7 @@ bool map3(CUtensorMap* tm, const void* base, bool f32, int64_t x, int64_t y, int
   const int64_t e = f32 ? 4 : 2;
   // the stride of a single row or matrix is never used, but has to be a legal one
   if (y <= 1) sy = x;
-  if (z <= 1) sz = y * sy;
+  if (z <= 1) sz = sy;
   const cuuint64_t dims[3] = {(cuuint64_t)x, (cuuint64_t)y, (cuuint64_t)z};
   const cuuint64_t strides[2] = {(cuuint64_t)(sy * e), (cuuint64_t)(sz * e)};
   const cuuint32_t box[3] = {(cuuint32_t)box_x, (cuuint32_t)box_y, 1}, step[3] = {1, 1, 1};
@@ -751,8 +751,9 @@ ma_status check(const ma_expert_matmul* d, bool weight) {
     return op_fail(MA_ERR_SHAPE, "%d experts: outside [1, %d]", d->n_experts, kMaxExperts);
   if (d->inner < 8 || d->inner > 1 << 20 || d->inner % 8 || d->outer < 8 || d->outer > 1 << 20 || d->outer % 8)
     return op_fail(MA_ERR_SHAPE, "inner %d or outer %d is no multiple of 8 in [8, 2^20]", d->inner, d->outer);
-  if (d->n_tokens < 0 || d->n_tokens > 1ll << 30)
-    return op_fail(MA_ERR_SHAPE, "%lld tokens: outside [0, 2^30]", (long long)d->n_tokens);
+  // (a gradient's sum over all of them, four million blocks of 0.3 us, ends within the waits' two seconds)
+  if (d->n_tokens < 0 || d->n_tokens > 1ll << 28)
+    return op_fail(MA_ERR_SHAPE, "%lld tokens: outside [0, 2^28]", (long long)d->n_tokens);
   const int64_t wide = (std::max(d->inner, d->outer) + kTile - 1) / kTile;
   const int64_t narrow = (std::min(d->inner, d->outer) + kTile - 1) / kTile;
   if ((d->n_tokens / kTile + d->n_experts + 1) * wide > INT32_MAX / 2 || d->n_experts * wide * narrow > INT32_MAX / 2)

@@ -180,11 +180,11 @@ def expert(mx, **kw):
 @pytest.mark.parametrize("kw,status", [
     ({"n_experts": 0}, "SHAPE"), ({"n_experts": 513}, "SHAPE"), ({"inner": 12}, "SHAPE"), ({"inner": 0}, "SHAPE"),
     ({"outer": 20}, "SHAPE"), ({"outer": 2 ** 21}, "SHAPE"), ({"n_tokens": -1}, "SHAPE"),
-    ({"n_tokens": 2 ** 30 + 1}, "SHAPE"), ({"offsets": None}, "ARG"), ({"offsets": AT + 2}, "ALIGN"),
+    ({"n_tokens": 2 ** 28 + 1}, "SHAPE"), ({"offsets": None}, "ARG"), ({"offsets": AT + 2}, "ALIGN"),
     ({"weight": None}, "ARG"), ({"weight": AT + 8}, "ALIGN"), ({"weight_row_stride": 8}, "SHAPE"),
     ({"weight_row_stride": 20, "weight_expert_stride": 480}, "ALIGN"), ({"weight_expert_stride": 100}, "SHAPE"),
     ({"weight_expert_stride": 388}, "ALIGN"), ({"x": None}, "ARG"), ({"x": AT + 2}, "ALIGN"), ({"x_stride": 8}, "SHAPE"),
-    ({"x_stride": 20}, "ALIGN"), ({"n_tokens": 2 ** 30, "outer": 2 ** 20, "weight_expert_stride": 2 ** 25}, "SHAPE")])
+    ({"x_stride": 20}, "ALIGN"), ({"n_tokens": 2 ** 28, "outer": 2 ** 20, "weight_expert_stride": 2 ** 25}, "SHAPE")])
 def test_expert_matmul_refuses(mx, kw, status):
     refused(mx, "muon_adamw_expert_matmul", status, expert(mx, **kw), AT, None)
     refused(mx, "muon_adamw_expert_matmul_backward", status, expert(mx, **kw), AT, kw.get("outer", 24), AT, AT, 0, 0, None)
