@@ -336,7 +336,9 @@ __device__ void choose_top(const Row<T>& row, int v0, int v1, bool edges, int to
 struct Running {
   float m;
   uint64_t s, u;
+  // gm is above m, or one of them is NaN, which stays
   __device__ __forceinline__ void raise(float gm, float c) {
+    gm = max_nan(gm, m);
     const float f = m == -INFINITY ? 0.f : ex2((m - gm) * c);
     const float d = f == 0.f ? 0.f : (m - gm) * c;
     u = mul2(pack2(f, f), fma2(pack2(d, d), s, u));

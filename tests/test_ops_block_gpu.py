@@ -397,6 +397,21 @@ def test_token_logprobs_rows_of_nan_and_infinity(ops, v, n):
     assert bool(((got[4] >= 0) & (got[4] < v)).all()) and got[0][0].isnan()
 
 
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("n", [1, 700])
+def test_token_logprobs_of_nan_before_masked_tokens(ops, dt, n):
+    """A NaN whose thread sees nothing but masked logits after it."""
+    z = torch.full((n, 30000), -float("inf"), device="cuda", dtype=DTYPES[dt])
+    ids = torch.zeros(n, device="cuda", dtype=torch.int64)
+    z[:, 0] = 1.0
+    for column in (8, 1000, 29999):
+        z[0, column] = float("nan")
+        assert all(x[0].isnan().all() for x in ops.token_logprobs(z, ids, top=3)[:4])
+        assert all(x[0].isnan() for x in ops.token_logprobs(z, ids)[:3])
+        z[0, column] = -float("inf")
+    assert not any(x.any() for x in ops.token_logprobs(z, ids)[:2])
+
+
 def test_token_logprobs_past_2_31_elements(ops):
     n, v = 14200, 151936
     z = torch.empty(n, v, device="cuda", dtype=torch.bfloat16)
