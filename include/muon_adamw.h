@@ -695,7 +695,7 @@ MA_API ma_status muon_adamw_expert_matmul_backward(const ma_expert_matmul* d, co
  *            MA_DT_BF16, `stride` apart, 16-byte accesses wherever a row allows;
  *   ids      int32 (id_bytes 4) or int64 (id_bytes 8); a token outside [0, vocab)
  *            has log probability 0 and no gradient from it;
- *   scale    positive (an inverse temperature);
+ *   scale    an inverse temperature, 1e-30 .. 1e30;
  *   top      0 .. 32, at most vocab.
  * A logit of -infinity has probability 0 and adds nothing. A row without any
  * other has lse -infinity, log probabilities -infinity (0 for a token outside),

@@ -516,7 +516,36 @@ struct GradRow {
   bool empty;
 };
 
-__device__ __forceinline__ GradRow grad_row(const LogprobArgs& a, int64_t at) {
+// Up to this magnitude lse's rounding changes a probability by 2^-14 of itself at most. Far above it ln s would be lost,
+// as in a row of the type's lowest value alone, or lse be infinite: there the sums are formed once more.
+constexpr float kLseMax = 2048.f;
+
+// The row's maximum and the logarithm of its sum, by the whole block.
+template <typename T>
+__device__ __noinline__ float2 row_sums(const T* p, int vocab, float c) {
+  __shared__ float shared[2][kGradThreads / 32];
+  const int t = threadIdx.x;
+  float m = -INFINITY, s = 0.f;
+  for (int i = t; i < vocab; i += kGradThreads) m = max_nan(m, load1(p + i));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+  if ((t & 31) == 0) shared[0][t >> 5] = m;
+  __syncthreads();
+  m = shared[0][0];
+  for (int i = 1; i < kGradThreads / 32; ++i) m = max_nan(m, shared[0][i]);
+  if (m == -INFINITY) return make_float2(m, 0.f);
+  for (int i = t; i < vocab; i += kGradThreads) s += ex2((load1(p + i) - m) * c);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  if ((t & 31) == 0) shared[1][t >> 5] = s;
+  __syncthreads();
+  s = shared[1][0];
+  for (int i = 1; i < kGradThreads / 32; ++i) s += shared[1][i];
+  return make_float2(m, logf(s));
+}
+
+template <typename T>
+__device__ __forceinline__ GradRow grad_row(const LogprobArgs& a, int64_t at, const T* row) {
   GradRow g;
   const float lse = __ldg(a.lse_in + at), h = a.dentropy ? __ldg(a.dentropy + at) : 0.f;
   g.id = token_id(a, at);
@@ -529,11 +558,17 @@ __device__ __forceinline__ GradRow grad_row(const LogprobArgs& a, int64_t at) {
   g.base = -a.scale * (h == 0.f ? l : fmaf(h, __ldg(a.entropy_in + at), l));
   g.slope = -a.scale * h * kLn2;
   g.empty = lse == -INFINITY;
+  if (fabsf(lse) > kLseMax) {
+    const float2 sums = row_sums(row, a.vocab, g.c);
+    g.shift = sums.x;
+    g.rest = sums.y / a.scale;
+    g.empty = sums.x == -INFINITY;
+  }
   return g;
 }
 
 __device__ __forceinline__ float grad_of(const GradRow& g, float x) {
-  const float a = max_nan((x - g.shift - g.rest) * g.c, -1e30f);
+  const float a = max_nan((x - g.shift - g.rest) * g.c, -1000.f);  // where 2^a is 0, and a times the slope no infinity
   return g.empty ? 0.f : ex2(a) * fmaf(g.slope, a, g.base);
 }
 
@@ -551,7 +586,7 @@ __global__ void __launch_bounds__(kGradThreads) token_logprobs_grad_kernel(const
   };
   if (((reinterpret_cast<uintptr_t>(row.p) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0) {
     // rows that lie differently: no boundary is both's
-    const GradRow g = grad_row(a, at);
+    const GradRow g = grad_row(a, at, row.p);
     const int end = min(a.vocab, (part + 1) * kGradStep * 8);
     for (int i = part * kGradStep * 8 + t; i < end; i += kGradThreads) single(g, i);
     return;
@@ -563,7 +598,7 @@ __global__ void __launch_bounds__(kGradThreads) token_logprobs_grad_kernel(const
     const int vec = v0 + j * kGradThreads + t;
     if (vec < row.vecs) raw[j].load(row.p + row.index(vec));
   }
-  const GradRow g = grad_row(a, at);
+  const GradRow g = grad_row(a, at, row.p);
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
     const int vec = v0 + j * kGradThreads + t;
@@ -595,8 +630,8 @@ ma_status check(const ma_token_logprobs* d) {
   if (d->n_tokens * parts > INT32_MAX)
     return op_fail(MA_ERR_SHAPE, "%lld tokens of %lld logits are too many for a call", (long long)d->n_tokens,
                    (long long)d->vocab);
-  if (!(d->scale > 0.0) || !std::isfinite(d->scale) || !((float)d->scale > 0.f) || !std::isfinite((float)d->scale))
-    return op_fail(MA_ERR_ARG, "scale = %g is not positive and finite in fp32", d->scale);
+  if (!(d->scale >= 1e-30 && d->scale <= 1e30))  // its products and quotients stay normal fp32 numbers
+    return op_fail(MA_ERR_ARG, "scale = %g outside [1e-30, 1e30]", d->scale);
   if (d->n_tokens == 0) return MA_OK;
   if (!d->logits || !d->ids) return op_fail(MA_ERR_ARG, "logits and ids must not be NULL");
   if (!op_aligned(d->logits, op_dtype_size(d->dtype)) || !op_aligned(d->ids, d->id_bytes))

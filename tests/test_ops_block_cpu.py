@@ -212,7 +212,7 @@ def logits(mx, **kw):
     ({"dtype": 2}, "DTYPE"), ({"id_bytes": 2}, "ARG"), ({"n_tokens": -1}, "SHAPE"), ({"vocab": 0}, "SHAPE"),
     ({"vocab": 2 ** 20 + 1, "stride": 2 ** 21}, "SHAPE"), ({"n_tokens": 2 ** 30, "vocab": 2 ** 20, "stride": 2 ** 20}, "SHAPE"),
     ({"stride": 29}, "SHAPE"), ({"scale": 0.0}, "ARG"), ({"scale": -1.0}, "ARG"), ({"scale": math.nan}, "ARG"),
-    ({"scale": 1e39}, "ARG"), ({"scale": 1e-60}, "ARG"), ({"logits": None}, "ARG"), ({"ids": None}, "ARG"),
+    ({"scale": 1e39}, "ARG"), ({"scale": 1e-60}, "ARG"), ({"scale": 1e-31}, "ARG"), ({"scale": 1e31}, "ARG"), ({"logits": None}, "ARG"), ({"ids": None}, "ARG"),
     ({"logits": AT + 1}, "ALIGN"), ({"ids": AT + 4}, "ALIGN")])
 def test_token_logprobs_refuses(mx, kw, status):
     refused(mx, "muon_adamw_token_logprobs", status, logits(mx, **kw), 2, AT, AT, AT, AT, AT, None)

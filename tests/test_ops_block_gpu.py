@@ -368,6 +368,41 @@ def test_token_logprobs_masked_rows_and_ties(ops, v, dt, n):
     assert not ops.token_logprobs_backward(0 * one, 0 * one, z, ids, got[1], got[2]).any()
 
 
+@pytest.mark.parametrize("v", [50, 9000, 70001])
+@pytest.mark.parametrize("dt", ["fp32", "bf16"])
+@pytest.mark.parametrize("scale", [0.7, 1.0, 3.0])
+def test_token_logprobs_gradient_of_rows_of_large_values(ops, v, dt, scale):
+    """Rows whose lse is too large to hold ln(sum), or is infinite: the gradient is the formula's, of z less its maximum."""
+    rng = np.random.default_rng(v)
+    lowest = float(torch.finfo(DTYPES[dt]).min)
+    z = np.full((7, v), lowest)
+    z[1, 5:] = -np.inf
+    z[2] = 5000 + rng.normal(size=v)
+    z[3] = np.where(rng.random(v) < 0.5, lowest, -4000 + 4 * rng.normal(size=v))
+    z[4] = -lowest * np.where(rng.random(v) < 0.5, 1, 0.5)
+    z[5] = -np.inf
+    z[6] = rng.normal(size=v)
+    z = cuda(z, dt)
+    ids = torch.tensor([0, 3, 7, v - 1, 9, 1, 2], device="cuda")
+    _, entropy, lse, _, _ = ops.token_logprobs(z, ids, scale=scale)
+    one = torch.ones(7, device="cuda")
+    for l, h in ((one, 0 * one), (0 * one, one), (-one, 0.5 * one)):
+        d = ops.token_logprobs_backward(l, h, z, ids, entropy, lse, scale=scale)
+        zr, at = host(z), ids.cpu().numpy()
+        top = zr.max(-1, keepdims=True)
+        zr = np.where(zr == -np.inf, -np.inf, zr - np.where(top == -np.inf, 0, top))
+        (_, _, sums, _, _), _ = O.token_logprobs(zr, at, scale, 1)
+        want, bound = O.token_logprobs_backward(host(l), host(h), zr, at, host(entropy), sums, scale)
+        # ln s and its sum of v / 256 terms a thread; row 6 has its own lse, of magnitude below 2^4
+        extra = (v / 256 + 16 + 2 ** 4) * O.U32 + 2 * O.EX2
+        a = np.where(zr == -np.inf, 0, zr * scale - np.where(sums == -np.inf, 0, sums)[:, None])
+        p = np.where(zr == -np.inf, 0, np.exp(a)) * (sums != -np.inf)[:, None]
+        mag = scale * p * (1 + np.abs(a) + host(entropy)[:, None] + 1)
+        within(d, want, bound + extra * mag)
+    assert not ops.token_logprobs_backward(0 * one, 0 * one, z, ids, entropy, lse, scale=scale).any()
+    assert ops.token_logprobs_backward(one, 1e12 * one, z, ids, entropy, lse, scale=scale).isfinite().all()
+
+
 @pytest.mark.parametrize("n", [1, 200])
 def test_token_logprobs_large_values_in_few_threads(ops, n):
     """More large logits in one thread's share than its list takes: columns 2048 apart, eight at a time."""
