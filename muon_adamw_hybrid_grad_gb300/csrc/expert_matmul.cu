@@ -28,7 +28,9 @@
 // knows: every CTA adds them up for itself first.
 //
 // Every wait is bounded; where one runs out the error word is set, copies and
-// products in flight end, and TMEM is freed.
+// products in flight end, and TMEM is freed. A wait spans a few blocks, but
+// for warp 10's: the units before the next one with rows to clear, any number of
+// them, go by meanwhile. Its limit counts from the last progress of the loads.
 #include <math.h>
 
 #include <algorithm>
@@ -157,6 +159,34 @@ __device__ __forceinline__ bool mbar_wait_warp_cluster(uint32_t bar, uint32_t pa
                                                        int* err, int code) {
   if (__all_sync(0xffffffffu, mbar_try_wait<true>(bar, parity))) return true;
   return __all_sync(0xffffffffu, mbar_wait_loop<true>(bar, parity, abort_flag, err, code));
+}
+// A wait during which the CTA may have any amount of work: it runs out once `progress`, a word of shared memory, has
+// stood still for the limit.
+__device__ __forceinline__ bool mbar_wait_warp_while(uint32_t bar, uint32_t parity, volatile int* progress,
+                                                     volatile int* abort_flag, int* err, int code) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  bool ok = false;
+  int seen = *progress;
+  uint64_t since = global_timer();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) {
+      ok = true;
+      break;
+    }
+    if ((it & 63u) != 0) continue;
+    if (*abort_flag) break;
+    const int at = *progress;
+    const uint64_t now = global_timer();
+    if (at != seen) {
+      seen = at;
+      since = now;
+    } else if (now - since > kWaitLimitNs) {
+      *abort_flag = 1;
+      atomicCAS(err, 0, code);
+      break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ void expect_warp(uint32_t bar, uint32_t bytes) {
   asm volatile(
@@ -455,6 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(bars + L::kNumBars);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* const progress = abort_flag + 1;  // blocks that warp 0 has loaded, every 64
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t full = smem_u32(bars), empty = full + 8 * S, tail = empty + 8 * S, fixed = tail + 8 * S;
   const uint32_t acc_full = fixed + 8 * S, acc_free = acc_full + 16, drain = acc_free + 16;
@@ -472,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
       mbar_init(acc_free + 8 * i, 2 * kStoreWarps);
     }
     mbar_init(drain, 1);
-    *abort_flag = 0;
+    *abort_flag = *progress = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
@@ -523,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
       const Unit u = unit_at<BACK>(a, tab, pos);
       const uint32_t bytes = stage_bytes<BACK>(u);
       for (int b = 0; b < u.blocks; ++b) {
+        if (BACK && left && (b & 63) == 0 && lane == 0) *progress = issued + 1;
         if (!mbar_wait_warp(empty + 8 * stage, phase ^ 1u, abort_flag, a.err, kErrLoad)) {
           ok = false;
           break;
@@ -686,7 +718,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
       const int left = u.count % kBlock;
       if (!u.weights || left == 0) continue;
       const int stage = (issued - 1) % S;
-      if (!mbar_wait_warp(tail + 8 * stage, (tail_phase >> stage) & 1u, abort_flag, a.err, kErrClear)) break;
+      if (!mbar_wait_warp_while(tail + 8 * stage, (tail_phase >> stage) & 1u, progress, abort_flag, a.err, kErrClear))
+        break;
       tail_phase ^= 1u << stage;
       const int end = (left + 15) & ~15;  // products go in steps of 16
       uint8_t* const at = smem + stage * kStage;
