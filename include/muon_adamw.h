@@ -648,9 +648,11 @@ MA_API ma_status muon_adamw_residual_norm_backward(const ma_residual_norm* d, co
 /* Products grouped by expert: out[t] = weight[e] x[t] for the tokens t of
  * expert e, offsets[e] to offsets[e + 1] - 1.
  *   n_experts  1 .. 512; inner (x's width) and outer (out's) multiples of 8 in
- *              [8, 2^20]; n_tokens in [0, 2^28]; all tensors bf16, sums fp32 as
- *              the tensor cores form them (toward zero: an fp32 gradient of the
- *              weights is off by about 1e-9 of itself for each token);
+ *              [8, 2^20]; n_tokens in [0, 2^28]; all tensors bf16. Sums are fp32,
+ *              over runs of 8192 terms (2048 in an fp32 gradient of the weights)
+ *              as the tensor cores form them, toward zero; the runs' sums are
+ *              added to nearest. An fp32 gradient is off by some 2e-6 of itself,
+ *              6e-6 where all terms have one sign, for any number of tokens;
  *   offsets    device, n_experts + 1 int32 values, ascending from 0 and at most
  *              n_tokens. Whatever they hold, no access leaves the tensors:
  *              the first counts as 0, each other one as at least the one before

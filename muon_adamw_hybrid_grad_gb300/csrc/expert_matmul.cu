@@ -19,7 +19,8 @@
 // would be 48 KB.
 //   warps 0, 11  TMA loads of the left and of the right operand into a ring of
 //              six stages
-//   warp 1     products, issued by the even CTA; two accumulators of 256 columns
+//   warp 1     products, issued by the even CTA; two accumulators of 256 columns, in turn, or one and the sum of its
+//              runs (kRun)
 //   warps 2-9  results from TMEM: transposed where tokens are columns, out
 //              through shared memory and TMA; tiles with other experts' tokens
 //              by plain stores of the rows that are theirs
@@ -52,6 +53,12 @@ constexpr int kWarps = 12;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStoreWarps = 8;
 constexpr int kMaxExperts = 512;
+// Blocks that one accumulator adds up. The tensor cores cut off toward zero what a sum cannot hold, so that a long
+// one loses in proportion to its length (4096 tokens 4.4e-6, a million 1.2e-3; of terms of one sign 1.4e-5 and 6.8e-3).
+// Longer sums are those of runs of this many blocks, which the warps that store add up in the other accumulator, to
+// nearest. For results in bf16 8192 terms, 3.5e-5 of themselves at most; for fp32 2048: 2.1e-6, with 4096 4.4e-6 and
+// with 1024 1.0e-6, at 5, 1 and 12 % more time (8192 tokens, 2048 -> 2048; 44.4 us in one run).
+constexpr int kRun = 128, kRunF32 = 32;  // kRunF32: of an fp32 gradient of the weights
 constexpr int kRaster = 8;  // token (or inner) tiles that walk together along the features
 constexpr uint32_t kTmemColumns = 512;
 
@@ -351,6 +358,11 @@ __device__ __forceinline__ int token_rows(const Unit& u) {
   return half <= 2 * kSmallBox ? half : half <= kMidBox ? kMidBox : kHalf;
 }
 
+template <bool BACK, bool F32>
+__device__ __forceinline__ int run_of(const Unit& u) {
+  return F32 && is_weights<BACK>(u) ? kRunF32 : kRun;
+}
+
 // Bytes that land in a CTA for one block.
 template <bool BACK>
 __device__ __forceinline__ uint32_t stage_bytes(const Unit& u) {
@@ -469,6 +481,22 @@ __device__ __forceinline__ void store_weights(const ExpertArgs& a, const Unit& u
     // (the second half of 32 fp32 columns may lie outside: nothing of it is written)
     store_3d_warp(&a.wout, smem_u32(tile), col0 + 16 * h, row0, u.expert);
   }
+}
+
+// A run's sum with that of the runs before it, to `to`: every second 32 columns of this warp's rows in TMEM.
+__device__ __forceinline__ void add_run(uint32_t run, uint32_t before, uint32_t to, int c0, int columns, bool first) {
+  for (; c0 < columns; c0 += 64) {
+    uint32_t r[32], s[32];
+    tmem_ld_32x32b_x32(run + (uint32_t)c0, r);
+    if (!first) tmem_ld_32x32b_x32(before + (uint32_t)c0, s);
+    tmem_ld_wait();
+    if (!first) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) + __uint_as_float(s[e]));
+    }
+    tmem_st_32x32b_x32(to + (uint32_t)c0, r);
+  }
+  tmem_st_wait();
 }
 
 // BACK: dx and the weights' gradients in one launch, the units of both dealt out as they come.
@@ -604,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
     if (rank == 0) {
       // ---- products ----
       int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
+      uint32_t phase = 0, acc_phase = 0;  // acc_phase: a bit an accumulator
       bool ok = true;
       const uint32_t s0 = smem_u32(smem);
       // MN-major: panels of 64 columns, sixteen rows of the contraction 2 KB further
@@ -616,40 +644,44 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
         if (u.blocks == 0) continue;
         const bool weights = is_weights<BACK>(u);
         const uint32_t idesc = idesc_bf16(kTile, u.n, weights) | (BACK ? 1u << 15 : 0u);
-        if (!mbar_wait_warp_cluster(acc_free + 8 * acc, acc_phase ^ 1u, abort_flag, a.err, kErrProduct)) break;
-        tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(acc * kTile);
-        for (int b = 0; b < u.blocks; ++b) {
-          if (!mbar_wait_warp_cluster(full + 8 * stage, phase, abort_flag, a.err, kErrProduct)) {
-            ok = false;
-            break;
-          }
+        const int run = run_of<BACK, F32>(u);
+        for (int b0 = 0; b0 < u.blocks; b0 += run) {
+          ok = mbar_wait_warp_cluster(acc_free + 8 * acc, (acc_phase >> acc & 1u) ^ 1u, abort_flag, a.err, kErrProduct);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t off = (uint32_t)stage * (uint32_t)(kStage >> 4);
-          const uint64_t ad = a0 + off;
-          if (!weights) {
-            umma_block_warp<kStepA, 2>(d, ad, b_k + off, idesc, b != 0 ? 1u : 0u);
-          } else {
-            const int left = u.count - b * kBlock;
-            if (left > kBlock - 16) {
-              umma_block_warp<kStepA, 128>(d, ad, b_mn + off, idesc, b != 0 ? 1u : 0u);
+          const int end = min(b0 + run, u.blocks);
+          for (int b = b0; b < end; ++b) {
+            if (!mbar_wait_warp_cluster(full + 8 * stage, phase, abort_flag, a.err, kErrProduct)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t off = (uint32_t)stage * (uint32_t)(kStage >> 4);
+            const uint64_t ad = a0 + off;
+            if (!weights) {
+              umma_block_warp<kStepA, 2>(d, ad, b_k + off, idesc, b != b0 ? 1u : 0u);
             } else {
-              for (int i = 0; i * 16 < left; ++i)
-                umma_pair_warp(d, ad + kStepA * i, b_mn + off + 128 * i, idesc, (b | i) != 0 ? 1u : 0u);
+              const int left = u.count - b * kBlock;
+              if (left > kBlock - 16) {
+                umma_block_warp<kStepA, 128>(d, ad, b_mn + off, idesc, b != b0 ? 1u : 0u);
+              } else {
+                for (int i = 0; i * 16 < left; ++i)
+                  umma_pair_warp(d, ad + kStepA * i, b_mn + off + 128 * i, idesc, ((b - b0) | i) != 0 ? 1u : 0u);
+              }
+            }
+            commit_pair_warp(empty + 8 * stage);
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1u;
             }
           }
-          commit_pair_warp(empty + 8 * stage);
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (!ok) break;
+          commit_pair_warp(acc_full + 8 * acc);
+          acc_phase ^= 1u << acc;
         }
-        if (!ok) break;
-        commit_pair_warp(acc_full + 8 * acc);
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
-        }
+        // the sum of several runs is in the other accumulator, until its tile has left and this one is free
+        if (u.blocks <= run) acc ^= 1;
       }
       commit_own_warp(drain);  // products in flight end before TMEM is freed
       drain_wait(drain, 0);
@@ -665,16 +697,29 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
       const Unit u = unit_at<BACK>(a, tab, pos);
       const bool weights = is_weights<BACK>(u), adds = weights && a.accumulate != 0;
       const int row0 = u.m0 + (int)rank * kHalf + quarter * 32;
+      const int columns = weights ? min(u.n, a.wn - u.n0) : u.count, run = run_of<BACK, F32>(u);
+      const bool inside = row0 < (weights ? a.wm : a.m);
+      const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+      const uint32_t t0 = lanes + (uint32_t)(acc * kTile), sum0 = lanes + (uint32_t)((acc ^ 1) * kTile);
       Before<F32> next;
       if (adds && u.blocks > 0) next.load(a, u, row0 + lane, u.n0 + 32 * half);
-      if (u.blocks > 0) {
-        const bool got = mbar_wait(acc_full + 8 * acc, acc_phase, abort_flag, a.err, kErrStore);
-        if (!__all_sync(0xffffffffu, got)) break;
+      bool ok = true;
+      for (int b = run; u.blocks > 0; b += run) {
+        const bool got = mbar_wait(acc_full + 8 * acc, acc_phase >> acc & 1u, abort_flag, a.err, kErrStore);
+        ok = __all_sync(0xffffffffu, got);
+        if (!ok) break;
         tc_fence_after();
+        const bool last = b >= u.blocks;
+        // the sum so far lies in the other accumulator, whose last tile this warp has read, and in the end in this one
+        if (__builtin_expect(inside && u.blocks > run, 0)) add_run(t0, sum0, last ? t0 : sum0, 32 * half, columns, b == run);
+        if (last) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_either(mapa_shared(acc_free + 8 * acc, 0));
+        acc_phase ^= 1u << acc;
       }
-      const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * kTile);
-      const int columns = weights ? min(u.n, a.wn - u.n0) : u.count;
-      if (row0 < (weights ? a.wm : a.m) && !(adds && u.blocks == 0)) {
+      if (!ok) break;
+      if (inside && !(adds && u.blocks == 0)) {
         for (int c0 = 32 * half; c0 < columns; c0 += 64) {
           const Before<F32> before = next;
           if (adds && c0 + 64 < columns) next.load(a, u, row0 + lane, u.n0 + c0 + 64);
@@ -701,10 +746,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_matmul_kernel(const __grid
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_either(mapa_shared(acc_free + 8 * acc, 0));
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
-        }
+        acc_phase ^= 1u << acc;
+        if (u.blocks <= run) acc ^= 1;
       }
     }
     stores_read_warp<0>();  // the stores have read shared memory
@@ -784,7 +827,7 @@ ma_status check(const ma_expert_matmul* d, bool weight) {
     return op_fail(MA_ERR_SHAPE, "%d experts: outside [1, %d]", d->n_experts, kMaxExperts);
   if (d->inner < 8 || d->inner > 1 << 20 || d->inner % 8 || d->outer < 8 || d->outer > 1 << 20 || d->outer % 8)
     return op_fail(MA_ERR_SHAPE, "inner %d or outer %d is no multiple of 8 in [8, 2^20]", d->inner, d->outer);
-  // (a gradient's sum over all of them, four million blocks of 0.3 us, ends within the waits' two seconds)
+  // (rows and a CTA's blocks are counted in 31 bits)
   if (d->n_tokens < 0 || d->n_tokens > 1ll << 28)
     return op_fail(MA_ERR_SHAPE, "%lld tokens: outside [0, 2^28]", (long long)d->n_tokens);
   const int64_t wide = (std::max(d->inner, d->outer) + kTile - 1) / kTile;

@@ -75,3 +75,64 @@ def test_expert_gradients_longer_than_a_wait(ops, short_waits):
     grad = torch.empty_like(w)
     again, _ = ops.expert_matmul_backward(dout, x, w, offsets, grad)
     assert torch.equal(dx, again) and torch.equal(dw, grad)
+
+
+# Of one step of 16 terms, relative to the sum so far: it and the terms are cut off toward zero where they are added,
+# the sum by less than its last bit, each term by less than a quarter of that (two bits further): 1 + 16 / 4 bits of
+# 2^-23 at the most. (Of positive terms a million times smaller than their sum 2.4 are lost on average.)
+STEP = 5 * 2.0 ** -23
+
+
+@pytest.mark.parametrize("tokens", [2048, 4096, 65536, 1 << 20, (1 << 20) + 77])
+@pytest.mark.parametrize("sign", ["both", "one"])
+def test_fp32_weight_gradients_of_many_tokens(ops, tokens, sign):
+    """The error does not grow with the tokens: an accumulator takes runs of 2048, 128 steps. The sum so far is on
+    average half of the whole for terms of one sign, and 2/3 for those of both (it grows as a square root). The runs'
+    sums are added to nearest: 512 additions, each off by 2^-24 of at most the whole, in both directions."""
+    x, dout = normal(tokens, 64), normal(tokens, 128, seed=1)
+    if sign == "one":
+        x.abs_(), dout.abs_()
+    w, offsets = normal(1, 128, 64, seed=2), torch.tensor([0, tokens], device="cuda", dtype=torch.int32)
+    want = dout.double().T @ x.double()
+    bound = 128 * STEP * 2 / 3 + 512 ** 0.5 * 2.0 ** -24
+    before = normal(1, 128, 64, seed=3, dtype=torch.float32)
+    for held in (None, before):
+        grad = torch.empty_like(before) if held is None else held.clone()
+        ops.expert_matmul_backward(dout, x, w, offsets, grad, accumulate=held is not None, input_grad=False)
+        total = want if held is None else want + held[0].double()
+        assert float((grad[0].double() - total).norm()) <= bound * float(want.norm()) + 2.0 ** -24 * float(total.norm())
+
+
+@pytest.mark.parametrize("length,tokens", [(8192, 40), (8200, 300), (65536, 40), (1 << 20, 8)])
+def test_long_contractions_of_expert_products(ops, length, tokens):
+    """out and dx of terms of one sign, whose sums an accumulator cuts off in one direction. Runs of 8192, 512 steps,
+    keep that below 1.6e-4; the result's own rounding is half a step of bf16, up to 3.9e-3."""
+    x, w = normal(tokens, length).abs_(), normal(1, 16, length, seed=1).abs_()
+    offsets = torch.tensor([0, tokens], device="cuda", dtype=torch.int32)
+    want = x.double() @ w[0].double().T
+    bound = torch.exp2(torch.floor(torch.log2(want)) - 8) + 512 * STEP / 2 * want
+    assert ((ops.expert_matmul(x, w, offsets).double() - want).abs() <= bound).all()
+    dx, _ = ops.expert_matmul_backward(x, x[:, :16], w.transpose(1, 2).contiguous(), offsets, None)
+    assert ((dx.double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("lengths,inner,outer", [((2049, 0, 4096, 31, 8193), 72, 520), ((20000, 64, 3), 264, 136)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_expert_gradients_of_several_runs(ops, lengths, inner, outer, dtype):
+    """Units of one run between units of several: each result is that of its expert alone, bit by bit."""
+    t = sum(lengths)
+    x, dout, w = normal(t, inner), normal(t, outer, seed=1), normal(len(lengths), outer, inner, seed=2)
+    bounds = [sum(lengths[:i]) for i in range(len(lengths) + 1)]
+    offsets = torch.tensor(bounds, device="cuda", dtype=torch.int32)
+    grad = torch.empty(w.shape, device="cuda", dtype=dtype)
+    dx, _ = ops.expert_matmul_backward(dout, x, w, offsets, grad)
+    for e, (a, b) in enumerate(zip(bounds, bounds[1:])):
+        one = torch.tensor([0, b - a], device="cuda", dtype=torch.int32)
+        alone = torch.empty_like(grad[e:e + 1])
+        dx_e, _ = ops.expert_matmul_backward(dout[a:b], x[a:b], w[e:e + 1], one, alone)
+        assert torch.equal(grad[e], alone[0]) and torch.equal(dx[a:b], dx_e)
+        exact = dout[a:b].double().T @ x[a:b].double()
+        unit = 2.0 ** -8 if dtype is torch.bfloat16 else 2.0 ** -24
+        run = 128 if dtype is torch.float32 else 512
+        size = dout[a:b].double().abs().T @ x[a:b].double().abs()
+        assert ((grad[e].double() - exact).abs() <= unit * exact.abs() + (run * STEP + 2.0 ** -20) * size).all()
