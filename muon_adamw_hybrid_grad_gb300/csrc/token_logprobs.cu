@@ -364,6 +364,34 @@ struct Running {
   }
 };
 
+// The sums of a block of THREADS: of each warp relative to its maximum, then of the block.
+template <int THREADS>
+__device__ __forceinline__ Sums block_sums(const Running& run, float c, Sums (&warps)[THREADS / 32]) {
+  Sums all = run.sums();
+  float m = all.m;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+  all = rebase(all, m, c);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    all.s += __shfl_xor_sync(0xffffffffu, all.s, d);
+    all.u += __shfl_xor_sync(0xffffffffu, all.u, d);
+  }
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = all;
+  __syncthreads();
+  m = warps[0].m;
+#pragma unroll
+  for (int i = 1; i < THREADS / 32; ++i) m = max_nan(m, warps[i].m);
+  all = {m, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < THREADS / 32; ++i) {
+    const Sums w = rebase(warps[i], m, c);
+    all.s += w.s;
+    all.u += w.u;
+  }
+  return all;
+}
+
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_constant__ LogprobArgs a) {
   extern __shared__ uint8_t shared[];
@@ -430,29 +458,7 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
     if (!(x <= run.m)) run.raise(x, c);
     if (run.m != -INFINITY) run.add(x, -INFINITY, c);
   }
-  // the warp's sums relative to its maximum, then the block's
-  Sums all = run.sums();
-  float m = all.m;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-  all = rebase(all, m, c);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    all.s += __shfl_xor_sync(0xffffffffu, all.s, d);
-    all.u += __shfl_xor_sync(0xffffffffu, all.u, d);
-  }
-  if ((t & 31) == 0) warp_sums[t >> 5] = all;
-  __syncthreads();
-  m = warp_sums[0].m;
-#pragma unroll
-  for (int i = 1; i < kThreads / 32; ++i) m = max_nan(m, warp_sums[i].m);
-  all = {m, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) {
-    const Sums w = rebase(warp_sums[i], m, c);
-    all.s += w.s;
-    all.u += w.u;
-  }
+  Sums all = block_sums<kThreads>(run, c, warp_sums);
   if constexpr (TOP) choose_top(row, v0, v1, edges, a.top, best, groups, sh);
 
   if (a.parts > 1) {
@@ -517,37 +523,42 @@ struct GradRow {
 };
 
 // Up to this magnitude lse's rounding changes a probability by 2^-14 of itself at most. Far above it ln s would be lost,
-// as in a row of the type's lowest value alone, or lse be infinite: there the sums are formed once more.
+// as in a row of the type's lowest value alone, or lse be infinite: there each block forms the row's sums once more.
 constexpr float kLseMax = 2048.f;
 
 // The row's maximum and the logarithm of its sum, by the whole block.
 template <typename T>
-__device__ __noinline__ float2 row_sums(const T* p, int vocab, float c) {
-  __shared__ float shared[2][kGradThreads / 32];
+__device__ __forceinline__ float2 row_sums(const Row<T> row, float c) {
+  __shared__ Sums warps[kGradThreads / 32];
   const int t = threadIdx.x;
-  float m = -INFINITY, s = 0.f;
-  for (int i = t; i < vocab; i += kGradThreads) m = max_nan(m, load1(p + i));
+  Running run{-INFINITY, 0, 0};
+  RawVec<T, 8> next;
+  if (t < row.vecs) next.load(row.p + row.index(t));
+#pragma unroll 1
+  for (int v = t; v < row.vecs; v += kGradThreads) {
+    float x[8];
+    next.get(x);
+    if (v + kGradThreads < row.vecs) next.load(row.p + row.index(v + kGradThreads));
+    float m = x[0];
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-  if ((t & 31) == 0) shared[0][t >> 5] = m;
-  __syncthreads();
-  m = shared[0][0];
-  for (int i = 1; i < kGradThreads / 32; ++i) m = max_nan(m, shared[0][i]);
-  if (m == -INFINITY) return make_float2(m, 0.f);
-  for (int i = t; i < vocab; i += kGradThreads) s += ex2((load1(p + i) - m) * c);
+    for (int e = 1; e < 8; ++e) m = max_nan(m, x[e]);
+    if (!(m <= run.m)) run.raise(m, c);
+    if (run.m == -INFINITY) continue;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-  if ((t & 31) == 0) shared[1][t >> 5] = s;
-  __syncthreads();
-  s = shared[1][0];
-  for (int i = 1; i < kGradThreads / 32; ++i) s += shared[1][i];
-  return make_float2(m, logf(s));
+    for (int e = 0; e < 8; e += 2) run.add(x[e], x[e + 1], c);
+  }
+  if (row.edge(t) >= 0) {
+    const float x = load1(row.p + row.edge(t));
+    if (!(x <= run.m)) run.raise(x, c);
+    if (run.m != -INFINITY) run.add(x, -INFINITY, c);
+  }
+  const Sums all = block_sums<kGradThreads>(run, c, warps);
+  return make_float2(all.m, all.m == -INFINITY ? 0.f : logf(all.s));
 }
 
-template <typename T>
-__device__ __forceinline__ GradRow grad_row(const LogprobArgs& a, int64_t at, const T* row) {
+__device__ __forceinline__ GradRow grad_row(const LogprobArgs& a, int64_t at, float lse) {
   GradRow g;
-  const float lse = __ldg(a.lse_in + at), h = a.dentropy ? __ldg(a.dentropy + at) : 0.f;
+  const float h = a.dentropy ? __ldg(a.dentropy + at) : 0.f;
   g.id = token_id(a, at);
   const float l = a.dlogprobs && g.id >= 0 && g.id < a.vocab ? __ldg(a.dlogprobs + at) : 0.f;
   // lse / scale in two parts: its rounding would scale the whole row
@@ -557,19 +568,44 @@ __device__ __forceinline__ GradRow grad_row(const LogprobArgs& a, int64_t at, co
   g.given = a.scale * l;
   g.base = -a.scale * (h == 0.f ? l : fmaf(h, __ldg(a.entropy_in + at), l));
   g.slope = -a.scale * h * kLn2;
-  g.empty = lse == -INFINITY;
-  if (fabsf(lse) > kLseMax) {
-    const float2 sums = row_sums(row, a.vocab, g.c);
-    g.shift = sums.x;
-    g.rest = sums.y / a.scale;
-    g.empty = sums.x == -INFINITY;
-  }
+  g.empty = false;  // which it may be above kLseMax only
   return g;
 }
 
 __device__ __forceinline__ float grad_of(const GradRow& g, float x) {
   const float a = max_nan((x - g.shift - g.rest) * g.c, -1000.f);  // where 2^a is 0, and a times the slope no infinity
   return g.empty ? 0.f : ex2(a) * fmaf(g.slope, a, g.base);
+}
+
+template <typename T>
+__device__ __forceinline__ void grad_single(const GradRow& g, const T* row, T* out, int i) {
+  store1(out + i, grad_of(g, load1(row + i)) + (i == g.id && !g.empty ? g.given : 0.f));
+}
+
+// A block's part of a row whose lse is above kLseMax, element by element. It is called behind the usual rows' path and
+// keeps nothing across row_sums, so that it costs those neither registers nor a branch that waits for lse.
+template <typename T>
+__device__ __noinline__ void grad_large(const LogprobArgs& a, int64_t at, int part, T* out) {
+  const T* const p = static_cast<const T*>(a.logits) + at * a.stride;
+  const float lse = __ldg(a.lse_in + at);
+  GradRow g = grad_row(a, at, lse);
+  const int begin = part * kGradStep * 8 + threadIdx.x, end = min(a.vocab, (part + 1) * kGradStep * 8);
+  // No sums for a row that no gradient reaches. Nor, where lse is -infinity, for a part of masked logits without the
+  // given token, or in which that has no gradient: whatever the row's other logits are.
+  bool look = g.given != 0.f || g.base != 0.f || g.slope != 0.f || lse == INFINITY;
+  if (look && lse == -INFINITY) {
+    bool any = false;
+    for (int i = begin; i < end; i += kGradThreads) any |= load1(p + i) > -INFINITY || (i == g.id && g.given != 0.f);
+    look = __syncthreads_or(any);
+  }
+  g.empty = !look;
+  if (look) {
+    const float2 sums = row_sums(Row<T>(p, a.vocab), g.c);
+    g.shift = sums.x;
+    g.rest = sums.y / a.scale;
+    g.empty = sums.x == -INFINITY;
+  }
+  for (int i = begin; i < end; i += kGradThreads) grad_single(g, p, out, i);
 }
 
 template <typename T>
@@ -581,41 +617,45 @@ __global__ void __launch_bounds__(kGradThreads) token_logprobs_grad_kernel(const
   pdl_launch();
   const Row<T> row(static_cast<const T*>(a.logits) + at * a.stride, a.vocab);
   T* const out = static_cast<T*>(a.dlogits) + at * a.out_stride;
-  auto single = [&](const GradRow& g, int i) {
-    store1(out + i, grad_of(g, load1(row.p + i)) + (i == g.id && !g.empty ? g.given : 0.f));
-  };
+  bool large;
   if (((reinterpret_cast<uintptr_t>(row.p) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0) {
     // rows that lie differently: no boundary is both's
-    const GradRow g = grad_row(a, at, row.p);
-    const int end = min(a.vocab, (part + 1) * kGradStep * 8);
-    for (int i = part * kGradStep * 8 + t; i < end; i += kGradThreads) single(g, i);
-    return;
-  }
-  const int v0 = part * kGradStep;
-  RawVec<T, 8> raw[kVecs];
+    const float lse = __ldg(a.lse_in + at);
+    const GradRow g = grad_row(a, at, lse);
+    large = fabsf(lse) > kLseMax;
+    const int end = large ? 0 : min(a.vocab, (part + 1) * kGradStep * 8);
+    for (int i = part * kGradStep * 8 + t; i < end; i += kGradThreads) grad_single(g, row.p, out, i);
+  } else {
+    const int v0 = part * kGradStep;
+    RawVec<T, 8> raw[kVecs];
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
-    const int vec = v0 + j * kGradThreads + t;
-    if (vec < row.vecs) raw[j].load(row.p + row.index(vec));
-  }
-  const GradRow g = grad_row(a, at, row.p);
-#pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
-    const int vec = v0 + j * kGradThreads + t;
-    if (vec >= row.vecs) break;
-    const int i = row.index(vec);
-    float x[8];
-    raw[j].get(x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = grad_of(g, x[e]);
-    if (g.id >= i && g.id < i + 8 && !g.empty) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (i + e == g.id) x[e] += g.given;
+    for (int j = 0; j < kVecs; ++j) {
+      const int vec = v0 + j * kGradThreads + t;
+      if (vec < row.vecs) raw[j].load(row.p + row.index(vec));
     }
-    store8(out + i, x);
+    const float lse = __ldg(a.lse_in + at);
+    const GradRow g = grad_row(a, at, lse);
+    large = fabsf(lse) > kLseMax;
+    const int vecs = large ? 0 : row.vecs;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const int vec = v0 + j * kGradThreads + t;
+      if (vec >= vecs) break;
+      const int i = row.index(vec);
+      float x[8];
+      raw[j].get(x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = grad_of(g, x[e]);
+      if (g.id >= i && g.id < i + 8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (i + e == g.id) x[e] += g.given;
+      }
+      store8(out + i, x);
+    }
+    if (part == 0 && row.edge(t) >= 0 && !large) grad_single(g, row.p, out, row.edge(t));
   }
-  if (part == 0 && row.edge(t) >= 0) single(g, row.edge(t));
+  if (large) grad_large(a, at, part, out);
 }
 
 ma_status check(const ma_token_logprobs* d) {
