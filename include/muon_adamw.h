@@ -720,7 +720,9 @@ MA_API ma_status muon_adamw_token_logprobs(const ma_token_logprobs* d, int32_t t
 /* Gradient of sum_t dlogprobs[t] logprobs[t] + dentropy[t] entropy[t] with
  * respect to the logits (either may be NULL for none), from the forward call's
  * inputs and its entropy and lse: dlogits, rows dlogits_stride apart, in the
- * logits' type. */
+ * logits' type. lse's own rounding scales a row's probabilities by up to 2^-19
+ * for fp32 logits (|lse| up to 64) and 2^-14 for bf16 ones (up to 2048); rows
+ * above have their sums formed again, which takes several times as long. */
 MA_API ma_status muon_adamw_token_logprobs_backward(const ma_token_logprobs* d, const float* dlogprobs,
                                                     const float* dentropy, const float* entropy, const float* lse,
                                                     void* dlogits, int64_t dlogits_stride, void* cuda_stream);

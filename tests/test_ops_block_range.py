@@ -5,7 +5,10 @@ import os
 import shutil
 import subprocess
 
+import numpy as np
 import pytest
+
+from oracle import operators as O
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -21,6 +24,10 @@ def ops():
     yield m
     m.check()
     torch.cuda.empty_cache()
+
+
+def host(x):
+    return x.detach().double().cpu().numpy()
 
 
 def normal(*shape, seed=0, dtype=torch.bfloat16):
@@ -137,6 +144,39 @@ def test_expert_gradients_of_several_runs(ops, lengths, inner, outer, dtype):
         size = dout[a:b].double().abs().T @ x[a:b].double().abs()
         assert ((grad[e].double() - exact).abs() <= unit * exact.abs() + (run * STEP + 2.0 ** -20) * size).all()
 # ---- log probabilities ----
+
+@pytest.mark.parametrize("v", [60, 1003, 40001])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("at", [0.0, 50.0, 500.0, 2000.0, -700.0])
+@pytest.mark.parametrize("scale", [1.0, 0.7])
+def test_token_logprobs_gradient_of_the_logits_alone(ops, v, dtype, at, scale):
+    """The gradient is that of the logits, wherever their maximum lies: a stored lse adds no more than half a step of
+    fp32 below kLseMax, 2^-19 for fp32 logits and 2^-14 for bf16 ones. The rest is the arithmetic of z less its
+    maximum, and ln s, whose sum has v / 512 terms a thread, its joins and its new maxima."""
+    n = 40
+    z = (at + 3 * normal(n, v, dtype=torch.float32)).to(dtype)
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    ids = torch.randint(-1, v, (n,), generator=gen, device="cuda")
+    l, h = normal(n, seed=5, dtype=torch.float32), normal(n, seed=6, dtype=torch.float32)
+    _, entropy, lse, _, _ = ops.token_logprobs(z, ids, scale=scale)
+    zr = host(z)
+    zr = zr - zr.max(-1, keepdims=True)
+    at_ = ids.cpu().numpy()
+    (_, exact_h, exact_lse, _, _), (_, bound_h, _, _) = O.token_logprobs(zr, at_, scale, 1)
+    logs = (v / 512 + 64) * O.U32 + (v / 8192 + 16) * 2 * O.EX2
+    unit = 2.0 ** -8 if dtype is torch.bfloat16 else 2.0 ** -24
+    for dl, dh in ((l, None), (None, h), (l, h)):
+        d = host(ops.token_logprobs_backward(dl, dh, z, ids, entropy, lse, scale=scale))
+        dl, dh = (np.zeros(n) if x is None else host(x) for x in (dl, dh))
+        want, bound = O.token_logprobs_backward(dl, dh, zr, at_, exact_h, exact_lse, scale)
+        p = np.exp(zr * scale - exact_lse[:, None])
+        a, hh = np.abs(zr * scale - exact_lse[:, None]), np.abs(dh)[:, None]
+        # a relative error of p, and an absolute one of log p and of the entropy
+        off = (2.0 ** -14 if dtype is torch.bfloat16 else 2.0 ** -19) + logs
+        inside = np.where((at_ >= 0) & (at_ < v), np.abs(dl), 0)[:, None]
+        bound = bound + scale * p * (off * (inside + hh * (a + exact_h[:, None] + 1)) + hh * bound_h[:, None])
+        assert (np.abs(d - want) <= bound + unit * (np.abs(want) + bound) + 1e-30).all()
+
 
 def test_token_logprobs_gradient_of_masked_rows_takes_no_longer(ops):
     """A quarter of the rows without any token, or without a gradient at values whose lse is not used, beside usual
