@@ -1,7 +1,10 @@
 // Gradient of the residual's addition with RMS norm.
 //
-//   g = dy w,  c = mean(g r) rstd^3,  dr = dres + rstd g - c r,
-//   dx = drop(dr),  dw = sum over rows of dy r rstd
+//   g = dy w,  n = r rstd,  dr = dres + rstd (g - n mean(g n)),
+//   dx = drop(dr),  dw = sum over rows of dy n
+//
+// The sum over the row is of g r, and c = mean(g r) rstd^2 is taken times n: with
+// rstd^3 times r it would leave fp32's range for rows of 1e-13 or 1e13 and beyond.
 //
 // One pass over dy, dres and r: both of a row's sums are formed together, so it
 // waits once for its threads. Bound by HBM (three rows in, two out). Blocks are
@@ -118,7 +121,7 @@ __global__ void __launch_bounds__(RowGroups<T>::kBlock) residual_norm_grad_kerne
       }
     }
     const float rstd = rsqrtf(ss / (float)a.w + a.eps);
-    const float c = gr / (float)a.w * rstd * rstd * rstd;
+    const float c = gr / (float)a.w * rstd * rstd;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int col = col_of<VEC, T>(j, t);
@@ -134,8 +137,9 @@ __global__ void __launch_bounds__(RowGroups<T>::kBlock) residual_norm_grad_kerne
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        d[e] += fmaf(rstd * dy[e], w[e], -c * r[e]);
-        dw[j][e] = fmaf(dy[e], r[e] * rstd, dw[j][e]);
+        const float n = r[e] * rstd;
+        d[e] = fmaf(-c, n, fmaf(rstd * dy[e], w[e], d[e]));
+        dw[j][e] = fmaf(dy[e], n, dw[j][e]);
       }
       store_row<VEC>(static_cast<TS*>(a.dr) + row * a.w, col, a.w, d);
       if (a.dx) {
@@ -288,7 +292,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
       phase ^= 1u;
     }
     const float rstd = rsqrtf(ss0 / (float)a.w + a.eps);
-    const float c = gr0 / (float)a.w * rstd * rstd * rstd;
+    const float c = gr0 / (float)a.w * rstd * rstd;
     const uint64_t rstd2 = pack2(rstd, rstd), c2 = pack2(-c, -c);
     float v[V][8];
 #pragma unroll
@@ -296,9 +300,9 @@ __global__ void __launch_bounds__(kRingThreads, 1)
       const int col = (j * T + t) * 8;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint64_t g = mul2(rstd2, dy[j][i]);
-        dw[j][i] = fma2(g, r[j][i], dw[j][i]);
-        unpack2(add2(d[j][i], fma2(g, w[j][i], mul2(c2, r[j][i]))), v[j][2 * i], v[j][2 * i + 1]);
+        const uint64_t n = mul2(rstd2, r[j][i]), g = mul2(rstd2, dy[j][i]);
+        dw[j][i] = fma2(dy[j][i], n, dw[j][i]);
+        unpack2(fma2(c2, n, fma2(g, w[j][i], d[j][i])), v[j][2 * i], v[j][2 * i + 1]);
       }
       if (col < a.w) store8(static_cast<TS*>(a.dr) + row * a.w + col, v[j]);
     }

@@ -35,6 +35,24 @@ def normal(*shape, seed=0, dtype=torch.bfloat16):
     return torch.empty(*shape, device="cuda", dtype=dtype).normal_(generator=gen)
 
 
+# ---- residual and norm ----
+
+@pytest.mark.parametrize("width", [64, 1001, 2048, 2050, 16384])
+@pytest.mark.parametrize("size,eps,of_dy", [(1e17, 1e-6, 1e-6), (1e17, 1e-6, 1e-10), (1e15, 1e-6, 1e-12),
+                                            (1e-19, 2e-38, 100.0), (3e-20, 1.2e-38, 1e15), (1e-17, 1e-34, 1e16)])
+def test_residual_norm_gradient_of_large_and_small_rows(ops, width, size, eps, of_dy):
+    """Rows far from 1 whose squares still have a sum in fp32, or are outweighed by eps: the formula's intermediate
+    values stay in range, and the bounds are those of usual rows."""
+    r = size * normal(13, width, dtype=torch.float32)
+    dy = of_dy * normal(13, width, seed=1, dtype=torch.float32)
+    w = 1 + 0.2 * normal(width, seed=2, dtype=torch.float32)
+    dx, dr, dw = (host(x) for x in ops.residual_norm_backward(dy, None, r, w, eps=eps))
+    one = np.ones((13, width))
+    want, bound = O.residual_norm_backward(host(dy), 0 * one, host(r), host(w), float(np.float32(eps)), one)
+    for x, y, b in zip((dx, dr, dw), want, bound):
+        assert np.isfinite(x).all() and (np.abs(x - y) <= b + 2.0 ** -24 * (np.abs(y) + b)).all()
+
+
 # ---- products grouped by expert ----
 
 WAIT_LIMIT = "kWaitLimitNs = 2000000000ull"
