@@ -29,9 +29,10 @@
 // knows: every CTA adds them up for itself first.
 //
 // Every wait is bounded; where one runs out the error word is set, copies and
-// products in flight end, and TMEM is freed. A wait spans a few blocks, but
-// for warp 10's: the units before the next one with rows to clear, any number of
-// them, go by meanwhile. Its limit counts from the last progress of the loads.
+// products in flight end, and TMEM is freed. A wait spans a run's
+// blocks at most, but for warp 10's: the units before the next one with rows to
+// clear, any number of them, go by meanwhile. Its limit counts from the last
+// progress of the loads.
 #include <math.h>
 
 #include <algorithm>

@@ -1,6 +1,7 @@
 // Inline PTX of the tensor-core kernels (sm_103a): mbarriers with bounded
 // waits, TMA copies, tcgen05 products, TMEM, and the descriptors they take.
-// Shared by ns_tc.cu, the attention kernels and qk_norm_rope.cu (waits and copies).
+// Used by ns_tc.cu, the attention kernels and expert_matmul.cu; qk_norm_rope.cu and residual_norm_grad.cu take
+// the waits and copies, token_logprobs.cu the addresses in a cluster.
 #pragma once
 
 #include <cuda.h>

@@ -8,10 +8,11 @@
 // probability is a difference of large numbers.
 //
 // The alternatives cost the pass next to nothing: a group's maximum, which the
-// softmax needs anyway, is kept in shared memory. The k-th largest of the
-// threads' maxima is at most the k-th largest element, since k threads have an
-// element that reaches it. So only groups whose maximum reaches it are read
-// again, some 25 of thousands, and their few candidates ranked by comparison.
+// softmax needs anyway, is kept in shared memory. The threshold is the k-th
+// largest of 32 maxima, each over the threads of one lane of every warp: it is at
+// most the k-th largest element, since k lanes have an element that reaches it. So
+// only groups whose maximum reaches it are read again, some 25 of thousands, and
+// their few candidates ranked by comparison.
 //
 // A row of the large vocabulary has a block; where rows are few, a cluster of up
 // to eight blocks shares one and joins through distributed shared memory.

@@ -12,10 +12,12 @@ stream, on which the work is queued; nothing here waits for the GPU.
 differentiates with it, once: a second derivative raises. The plain forms
 record no graph, whatever their arguments require: a result that a loss is to
 reach the parameters through comes from an ``_autograd`` form. Queries, keys,
-values, experts' inputs, weights and tables start every row on a 16-byte boundary and are
-refused otherwise (MA_ERR_ALIGN); the rows of the residual stream and of logits may start anywhere; gradients and saved outputs may lie in any
-layout, at the price of a copy where the kernels cannot read it. Refused arguments raise TypeError or ValueError, or
-MuonAdamWError with the library's status.
+values, experts' inputs, weights and tables start every row on a 16-byte
+boundary and are refused otherwise (MA_ERR_ALIGN); the rows of the residual
+stream and of logits may start anywhere; gradients and saved outputs may lie in
+any layout, at the price of a copy where the kernels cannot read it. Refused
+arguments raise TypeError or ValueError, or MuonAdamWError with the library's
+status.
 """
 from __future__ import annotations
 
