@@ -161,6 +161,34 @@ def test_expert_gradients_of_several_runs(ops, lengths, inner, outer, dtype):
         run = 128 if dtype is torch.float32 else 512
         size = dout[a:b].double().abs().T @ x[a:b].double().abs()
         assert ((grad[e].double() - exact).abs() <= unit * exact.abs() + (run * STEP + 2.0 ** -20) * size).all()
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_several_runs_in_several_units_of_a_pair(ops, dtype, accumulate):
+    """270 units of the weights and some 350 of dx over 76 pairs, of one to five runs each in any order: the two
+    accumulators change their parts between units. dx has 8200 terms, two runs."""
+    lengths, inner, outer = (2049, 100, 4096, 0, 31, 8193, 640, 2048), 1032, 8200
+    t = sum(lengths)
+    x, w = normal(t, inner), 0.02 * normal(len(lengths), outer, inner, seed=2)
+    dout = 0.1 * normal(t, outer, seed=1)
+    bounds = [sum(lengths[:i]) for i in range(len(lengths) + 1)]
+    offsets = torch.tensor(bounds, device="cuda", dtype=torch.int32)
+    held = normal(*w.shape, seed=3).to(dtype)
+    grad = held.clone() if accumulate else torch.empty(w.shape, device="cuda", dtype=dtype)
+    dx, _ = ops.expert_matmul_backward(dout, x, w, offsets, grad, accumulate=accumulate)
+    unit, run = (2.0 ** -8, 512) if dtype is torch.bfloat16 else (2.0 ** -24, 128)
+    for e, (a, b) in enumerate(zip(bounds, bounds[1:])):
+        if a == b:
+            assert torch.equal(grad[e], held[e]) if accumulate else not grad[e].any()
+            continue
+        d, xe, we = dout[a:b].double(), x[a:b].double(), w[e].double()
+        want = d.T @ xe + (held[e].double() if accumulate else 0)
+        # (every step is off by STEP at most, of a sum so far that is no larger than its terms' magnitudes)
+        size = d.abs().T @ xe.abs()
+        assert ((grad[e].double() - want).abs() <= unit * want.abs() + (run * STEP + 2.0 ** -20) * size).all()
+        want, size = d @ we, d.abs() @ we.abs()
+        assert ((dx[a:b].double() - want).abs() <= 2.0 ** -8 * want.abs() + (512 * STEP + 2.0 ** -20) * size).all()
+
+
 # ---- log probabilities ----
 
 @pytest.mark.parametrize("v", [60, 1003, 40001])
