@@ -1,8 +1,10 @@
 // Log probabilities of given tokens with entropy and top alternatives, and their gradient.
 //
 // Forward, one pass over a row: each thread keeps its own running maximum m, the
-// sum s of 2^a and the sum u of a 2^a, a = (x - m) scale log2(e), over groups of
-// 32 elements, and joins them at the end:
+// sum s of 2^a and the sum u of a 2^a, a = (x - m) scale log2(e). It adds those
+// of a group of 32 elements at a time (one by one, what lies below a step of s was
+// lost: 1.3e-6 of every log probability of 4093 rows of 151936, now 6e-8), and
+// the threads' are joined at the end:
 //   lse = m scale + ln s,  entropy = ln s - ln(2) u / s.
 // Sums are kept relative to the maximum, so that neither entropy nor a log
 // probability is a difference of large numbers.
@@ -74,10 +76,11 @@ __device__ __forceinline__ void fill(RawVec<float, 8>& r) {
 }
 
 // The largest of a group's elements, NaN if there is one.
-__device__ __forceinline__ float group_max(const RawVec<__nv_bfloat16, 8> (&r)[kVecs]) {
+template <int N>
+__device__ __forceinline__ float group_max(const RawVec<__nv_bfloat16, 8> (&r)[N]) {
   __nv_bfloat162 m[4];
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
+  for (int i = 0; i < N; ++i) {
     const uint32_t w[4] = {r[i].v.x, r[i].v.y, r[i].v.z, r[i].v.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -88,10 +91,11 @@ __device__ __forceinline__ float group_max(const RawVec<__nv_bfloat16, 8> (&r)[k
   m[0] = __hmax2_nan(__hmax2_nan(m[0], m[1]), __hmax2_nan(m[2], m[3]));
   return max_nan(__low2float(m[0]), __high2float(m[0]));
 }
-__device__ __forceinline__ float group_max(const RawVec<float, 8> (&r)[kVecs]) {
+template <int N>
+__device__ __forceinline__ float group_max(const RawVec<float, 8> (&r)[N]) {
   float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i)
+  for (int i = 0; i < N; ++i)
     m = max_nan(m, max_nan(max_nan(max_nan(r[i].a.x, r[i].a.y), max_nan(r[i].a.z, r[i].a.w)),
                            max_nan(max_nan(r[i].b.x, r[i].b.y), max_nan(r[i].b.z, r[i].b.w))));
   return m;
@@ -357,6 +361,20 @@ struct Running {
     s = add2(s, e);
     u = fma2(e, pack2(p, q), u);
   }
+  // A group's vectors: their own sums first, so that a long row's are not added to one by one.
+  template <typename T, int N>
+  __device__ __forceinline__ void add_group(const RawVec<T, 8> (&raw)[N], float c) {
+    Running group{m, 0, 0};
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      float x[8];
+      raw[j].get(x);
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) group.add(x[e], x[e + 1], c);
+    }
+    s = add2(s, group.s);
+    u = add2(u, group.u);
+  }
   __device__ __forceinline__ Sums sums() const {
     float s0, s1, u0, u1;
     unpack2(s, s0, s1);
@@ -444,14 +462,7 @@ __global__ void __launch_bounds__(kThreads) token_logprobs_kernel(const __grid_c
       best = fmaxf(best, gm);
     }
     if (!(gm <= run.m)) run.raise(gm, c);
-    if (run.m == -INFINITY) continue;
-#pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      float x[8];
-      cur[j].get(x);
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) run.add(x[e], x[e + 1], c);
-    }
+    if (run.m != -INFINITY) run.add_group(cur, c);
   }
   if (edges && row.edge(t) >= 0) {
     const float x = load1(row.p + row.edge(t));
@@ -526,7 +537,7 @@ struct GradRow {
 // Above this magnitude of lse its rounding, half a step of fp32, would change a row's probabilities by more than 2^-14
 // of themselves for bf16 logits, whose gradient is rounded to 2^-9, and 2^-19 for fp32. Far above it ln s would be lost,
 // as in a row of the type's lowest value alone, or lse be infinite. There each block forms the row's sums once more:
-// 4093 bf16 rows of 151936 3.4 ms, usual ones 0.37; 2046 fp32 rows 2.1 and 0.36; 8000 fp32 rows of 8000 113 and 79 us.
+// 4093 bf16 rows of 151936 3.8 ms, usual ones 0.37; 2046 fp32 rows 2.1 and 0.36; 8000 fp32 rows of 8000 113 and 79 us.
 template <typename T>
 constexpr float kLseMax = sizeof(T) == 2 ? 2048.f : 64.f;
 
@@ -540,16 +551,11 @@ __device__ __forceinline__ float2 row_sums(const Row<T> row, float c) {
   if (t < row.vecs) next.load(row.p + row.index(t));
 #pragma unroll 1
   for (int v = t; v < row.vecs; v += kGradThreads) {
-    float x[8];
-    next.get(x);
+    const RawVec<T, 8> cur[1] = {next};
     if (v + kGradThreads < row.vecs) next.load(row.p + row.index(v + kGradThreads));
-    float m = x[0];
-#pragma unroll
-    for (int e = 1; e < 8; ++e) m = max_nan(m, x[e]);
+    const float m = group_max(cur);
     if (!(m <= run.m)) run.raise(m, c);
-    if (run.m == -INFINITY) continue;
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) run.add(x[e], x[e + 1], c);
+    if (run.m != -INFINITY) run.add_group(cur, c);
   }
   if (row.edge(t) >= 0) {
     const float x = load1(row.p + row.edge(t));
@@ -612,8 +618,10 @@ __device__ __noinline__ void grad_large(const LogprobArgs& a, int64_t at, int pa
   for (int i = begin; i < end; i += kGradThreads) grad_single(g, p, out, i);
 }
 
+// (fp32 for four blocks an SM, which it would have anyway: with other registers 81 us in place of 79 for 8000 rows of 8000)
 template <typename T>
-__global__ void __launch_bounds__(kGradThreads) token_logprobs_grad_kernel(const __grid_constant__ LogprobArgs a) {
+__global__ void __launch_bounds__(kGradThreads, sizeof(T) == 2 ? 0 : 4)
+    token_logprobs_grad_kernel(const __grid_constant__ LogprobArgs a) {
   const int t = threadIdx.x;
   const int64_t at = blockIdx.x / a.parts;
   const int part = (int)(blockIdx.x - at * a.parts);

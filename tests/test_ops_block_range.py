@@ -224,6 +224,31 @@ def test_token_logprobs_gradient_of_the_logits_alone(ops, v, dtype, at, scale):
         assert (np.abs(d - want) <= bound + unit * (np.abs(want) + bound) + 1e-30).all()
 
 
+@pytest.mark.parametrize("v", [40001, 151936, 1 << 20])
+def test_token_logprobs_of_many_unlikely_tokens(ops, v):
+    """A few likely tokens and a long tail, whose terms lie below one of the running sum: the errors of many rows have
+    no common direction but the power of two's (2^-22 of each term) and that of the rounded scale * log2(e), 2^-24 of
+    each exponent. The others are roundings to nearest: a group's 16 additions, the sum's, one for each group, and the
+    results' own, each uniform within 2^-24 of a value below 1 + |log p|."""
+    n, scale = 600, 1.25
+    z = 2 * normal(n, v)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    ids = torch.randint(0, v, (n,), generator=gen, device="cuda")
+    z[torch.arange(n, device="cuda"), ids] = (12 + 2 * normal(n, seed=2)).to(z.dtype)
+    logprobs, entropy, lse, _, _ = ops.token_logprobs(z, ids, scale=scale)
+    error, width, exponent = [], [], []
+    for rows in torch.arange(n, device="cuda").split(50):
+        a = z[rows].double() * scale
+        want = torch.log_softmax(a, -1)
+        given = want[torch.arange(len(rows)), ids[rows]]
+        error.append(logprobs[rows].double() - given)
+        width.append((16 + v / 4096 + 16 + (1 + given.abs()) ** 2) ** 0.5 * 2.0 ** -24 / 3 ** 0.5)
+        exponent.append((want.exp() * (a.amax(-1, keepdim=True) - a)).sum(-1))
+    error, width, exponent = torch.cat(error), torch.cat(width), torch.cat(exponent)
+    common = 2.0 ** -22 + 2.0 ** -24 * float(exponent.mean())
+    assert abs(float(error.mean())) <= common + 4 * float(width.square().mean()) ** 0.5 / n ** 0.5
+
+
 def test_token_logprobs_gradient_of_masked_rows_takes_no_longer(ops):
     """A quarter of the rows without any token, or without a gradient at values whose lse is not used, beside usual
     rows: the batch moves the same bytes, and takes less than twice as long (times of one GPU in one process)."""
