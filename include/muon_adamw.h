@@ -662,7 +662,7 @@ MA_API ma_status muon_adamw_residual_norm_backward(const ma_residual_norm* d, co
  *              weight_expert_stride apart.
  * Bases are 16-byte aligned and strides multiples of 8 elements. Tokens behind
  * the last expert's get rows of zeros. A token's result depends on no other
- * token and on no other expert. */
+ * token and on no other expert. Results must not overlap what is read. */
 typedef struct {
   int64_t n_tokens;
   int32_t n_experts, inner, outer, reserved;
@@ -722,7 +722,9 @@ MA_API ma_status muon_adamw_token_logprobs(const ma_token_logprobs* d, int32_t t
  * inputs and its entropy and lse: dlogits, rows dlogits_stride apart, in the
  * logits' type. lse's own rounding scales a row's probabilities by up to 2^-19
  * for fp32 logits (|lse| up to 64) and 2^-14 for bf16 ones (up to 2048); rows
- * above have their sums formed again, which takes several times as long. */
+ * above have their sums formed again, which takes several times as long.
+ * dlogits must not overlap the logits, but may be the logits themselves where
+ * vocab is at most 8192. */
 MA_API ma_status muon_adamw_token_logprobs_backward(const ma_token_logprobs* d, const float* dlogprobs,
                                                     const float* dentropy, const float* entropy, const float* lse,
                                                     void* dlogits, int64_t dlogits_stride, void* cuda_stream);

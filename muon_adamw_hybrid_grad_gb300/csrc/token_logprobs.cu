@@ -784,6 +784,9 @@ ma_status muon_adamw_token_logprobs_backward(const ma_token_logprobs* d, const f
     a.dlogits = dlogits;
     a.out_stride = dlogits_stride;
     a.parts = std::max((a.vocab + kGradStep * 8 - 1) / (kGradStep * 8), 1);
+    // each of a row's blocks may read all of it while the others write (above kLseMax)
+    if (dlogits == d->logits && a.parts > 1)
+      return op_fail(MA_ERR_ARG, "dlogits are the logits, with more than %d of them in a row", kGradStep * 8);
     const dim3 grid((unsigned)(a.n * a.parts));
     const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     const cudaError_t e = d->dtype == MA_DT_BF16
